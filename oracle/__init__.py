@@ -11,7 +11,8 @@ only) or from the tests themselves.
 front of the verification.  ``sampler_filter`` holds the top-k / top-p filters applied to p and q
 before verification (llmstudio.ru section 38); ``penalties`` the repetition,
 frequency and presence penalties ahead of them, with the sampler state of
-each row following the speculative branch (sections 38-39).  ``draft_gate`` is the
+each row following the speculative branch (sections 38-39).  ``lm_head_q4`` is the LM head on weights in 4 bits,
+``beam`` beam search's selection and the reordering of its states.  ``draft_gate`` is the
 draft-length gate that produces the ragged ``cu_k``
 (PocketLLM docs/dspark.md, the draft-length gate section).
 
@@ -64,6 +65,16 @@ from .lm_head import (  # noqa: F401
     lm_head_logits,
     accept_lm_head,
     verify_greedy_lm_head,
+)
+from .lm_head_q4 import (  # noqa: F401
+    q4_weights,
+    q4_logits,
+    q4_abs_sums,
+)
+from .beam import (  # noqa: F401
+    BeamResult,
+    beam_select,
+    beam_reorder,
 )
 from .penalties import (  # noqa: F401
     penalize_value,

@@ -21,21 +21,27 @@ from ._lib import (  # noqa: F401
     load as load_library,
 )
 from .api import (  # noqa: F401
+    BeamCandidates,
     GateResult,
     LMHeadResult,
+    Q4Projection,
     SVError,
     VerifyResult,
     accept,
     accept_from_logits,
     apply_penalties,
+    beam_reorder,
+    beam_select,
+    beam_select_workspace,
     gate_draft_lengths,
     gate_update,
     lm_head_logits,
     lm_head_verify,
     lm_head_verify_static,
     lm_head_workspace,
+    q4_quantize,
     sampler_floors,
     verify_greedy,
 )
 from ._build import build  # noqa: F401
-from .decoder import SpeculativeDecoder  # noqa: F401,E402
+from .decoder import BeamDecoder, SpeculativeDecoder  # noqa: F401,E402

@@ -1,4 +1,4 @@
-"""ctypes declarations of the C ABI in include/sv.h and include/sv_gate.h (loads lib/libsv.so)."""
+"""ctypes declarations of the C ABI in include/*.h (loads lib/libsv.so)."""
 
 import ctypes
 import os
@@ -6,7 +6,8 @@ import re
 
 from ._build import LIB_PATH, PKG_DIR
 
-HEADERS = [os.path.join(os.path.dirname(PKG_DIR), "include", h) for h in ("sv.h", "sv_gate.h", "sv_filter.h", "sv_lm_head.h", "sv_penalties.h")]
+HEADERS = [os.path.join(os.path.dirname(PKG_DIR), "include", h) for h in ("sv.h", "sv_gate.h", "sv_filter.h", "sv_lm_head.h", "sv_penalties.h",
+                                                                                   "sv_beam.h", "sv_lm_head_q4.h")]
 
 SV_F32, SV_BF16, SV_F16 = 0, 1, 2
 SV_OK, SV_ERR_ARG, SV_ERR_CUDA, SV_ERR_UNSUPPORTED = 0, 1, 2, 3
@@ -29,6 +30,19 @@ class GateParams(ctypes.Structure):
                 ("verify_base_ms", ctypes.c_double), ("verify_slope_ms", ctypes.c_double),
                 ("plain_ms", ctypes.c_double), ("margin_threshold", ctypes.c_float),
                 ("min_draft", ctypes.c_int32)]
+
+
+class BeamState(ctypes.Structure):
+    """sv_beam_state (include/sv_beam.h)."""
+    _fields_ = [("data", ctypes.c_void_p), ("seq_stride", ctypes.c_int64), ("beam_stride", ctypes.c_int64),
+                ("seg_stride", ctypes.c_int64), ("token_bytes", ctypes.c_int64), ("segs", ctypes.c_int32),
+                ("tokens", ctypes.c_int32), ("timed", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class Q4Proj(ctypes.Structure):
+    """sv_q4_proj (include/sv_lm_head_q4.h)."""
+    _fields_ = [("packed", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("zeros", ctypes.c_void_p),
+                ("scale_dtype", ctypes.c_int32), ("group", ctypes.c_int32)]
 
 
 SIGNATURES = {
@@ -59,6 +73,14 @@ SIGNATURES = {
                                         _vp, _vp, _vp, _u32, _vp]),
     "sv_apply_penalties": (_i32, [_vp, _vp, _i32, _i64, _vp, _vp, _i32, _vp, _vp, _i32, _i32, _i32, _i32,
                                   _vp, _vp, _vp, _vp, _vp]),
+    "sv_beam_select_workspace_size": (ctypes.c_size_t, [_i32, _i32, _i32, _i32]),
+    # logits, dtype, stride, scores, finished, eos, B, W, V, n, scores, parents, tokens, status, workspace, stream
+    "sv_beam_select": (_i32, [_vp, _i32, _i64, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp,
+                              _vp, ctypes.c_size_t, _vp]),
+    "sv_beam_reorder": (_i32, [ctypes.POINTER(BeamState), _i32, _vp, _vp, _i32, _i32, _vp, _vp]),
+    "sv_lm_head_q4_logits": (_i32, [_vp, _i32, ctypes.POINTER(Q4Proj), _i32, _i32, _i32, _vp, _i64, _vp, _vp]),
+    "sv_lm_head_q4_verify": (_i32, [_vp, _vp, _i32, ctypes.POINTER(Q4Proj), _i32, _vp, _vp, _vp, _vp, _i32, _i32,
+                                    _i32, _i32, _vp, _vp, _vp, _vp, ctypes.c_size_t, _u32, _vp]),
     "sv_status_string": (ctypes.c_char_p, [_i32]),
     "sv_last_error": (ctypes.c_char_p, []),
     "sv_version": (_i32, []),
@@ -70,7 +92,7 @@ _lib = None
 def header_symbols():
     """Function names declared in the headers under include/."""
     text = "".join(open(h).read() for h in HEADERS)
-    return sorted(set(re.findall(r"\b(sv_[a-z_]+)\s*\(", text)))
+    return sorted(set(re.findall(r"\b(sv_[a-z0-9_]+)\s*\(", text)))
 
 
 def load():

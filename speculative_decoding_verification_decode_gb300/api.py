@@ -10,7 +10,7 @@ results back, which is how an end-to-end caller with host buffers uses it.
 from __future__ import annotations
 
 import ctypes
-from typing import NamedTuple, Optional
+from typing import NamedTuple, Optional, Sequence, Union
 
 import torch
 
@@ -321,19 +321,114 @@ def gate_update(confidence: torch.Tensor, n_submitted: torch.Tensor, n_accepted:
 # ---------------------------------------------------------------- LM head in front of verification
 
 def _bf16_rows(x: torch.Tensor, m: "_Marshal") -> torch.Tensor:
+    if not isinstance(x, torch.Tensor):
+        raise ValueError("states and projection must be bfloat16 tensors (this call takes no 4-bit projection)")
     x = m.dev(x)
     if x.dtype != torch.bfloat16:
         raise ValueError("states and projection must be bfloat16")
     return x.reshape(-1, x.shape[-1]).contiguous()
 
 
-def lm_head_logits(states: torch.Tensor, proj: torch.Tensor, out: Optional[torch.Tensor] = None,
+class Q4Projection(NamedTuple):
+    """A vocabulary projection in 4 bits (include/sv_lm_head_q4.h):
+    ``W[v, k] = scales[v, k // group] * (q[v, k] - zeros[v, k // group])``.
+    ``lm_head_logits`` and ``lm_head_verify`` take it in place of the bf16
+    matrix; ``q4_quantize`` makes one from such a matrix."""
+    packed: torch.Tensor  # uint8 [V, d / 2]: q[2j] in the low four bits of byte j, q[2j + 1] in the high four
+    scales: torch.Tensor  # f32 / bf16 / f16 [V, ceil(d / group)]
+    zeros: Optional[torch.Tensor] = None  # uint8 [V, ceil(d / group)] in 0..15; None: 8 everywhere
+    group: int = 128  # weights per scale: 32, 64 or 128
+
+
+def q4_quantize(weight: torch.Tensor, group: int = 128, zeros: bool = False,
+                scale_dtype: torch.dtype = torch.bfloat16) -> Q4Projection:
+    """A ``[V, d]`` matrix in 4 bits, each weight rounded to the nearest step
+    of its group.  Without ``zeros`` the steps are -8..7 times the scale, the
+    largest magnitude at 7; with them 0..15 from the group's smallest to its
+    largest value (0 always among them).  Done once, where the weights are
+    laid out; any device."""
+    if weight.dim() != 2 or group not in (32, 64, 128):
+        raise ValueError("weight must be [V, d], group 32, 64 or 128")
+    if weight.shape[1] % 32:
+        raise ValueError("d must be a multiple of 32")
+    if scale_dtype not in _DTYPES:
+        raise ValueError("scale_dtype must be float32, bfloat16 or float16")
+    V, d = weight.shape
+    G = -(-d // group)
+    w = torch.nn.functional.pad(weight.float(), (0, G * group - d)).view(V, G, group)
+    if zeros:
+        lo, hi = w.amin(2).clamp(max=0), w.amax(2).clamp(min=0)
+        scale = ((hi - lo) / 15).to(scale_dtype)
+        step = torch.where(scale > 0, scale.float(), 1.0)
+        z = (-lo / step).round().clamp(0, 15)
+    else:
+        scale = (w.abs().amax(2) / 7).to(scale_dtype)
+        step = torch.where(scale > 0, scale.float(), 1.0)
+        z = torch.full_like(step, 8.0)
+    q = ((w / step[..., None]).round() + z[..., None]).clamp(0, 15).to(torch.uint8).view(V, G * group)[:, :d]
+    packed = q[:, 0::2] | (q[:, 1::2] << 4)
+    return Q4Projection(packed.contiguous(), scale, z.to(torch.uint8) if zeros else None, group)
+
+
+class _Head:
+    """A bf16 or a 4-bit projection checked against the states' width: the
+    calls below are the same for both but for the entry point and the
+    arguments that describe the projection."""
+
+    def __init__(self, proj: Union[torch.Tensor, "Q4Projection"], m: "_Marshal"):
+        self.lib = _lib.load()
+        self.q4 = isinstance(proj, Q4Projection)
+        if not self.q4:
+            self.w = _bf16_rows(proj, m)
+            self.V, self.d = self.w.shape
+            return
+        if proj.packed.dim() != 2 or proj.packed.dtype != torch.uint8:
+            raise ValueError("packed must be uint8 [V, d / 2]")
+        self.V, self.d = proj.packed.shape[0], 2 * proj.packed.shape[1]
+        if proj.group not in (32, 64, 128):
+            raise ValueError("group must be 32, 64 or 128")
+        shape = (self.V, -(-self.d // proj.group))
+        if proj.scales.dtype not in _DTYPES or tuple(proj.scales.shape) != shape:
+            raise ValueError(f"scales must be f32, bf16 or f16 {list(shape)}")
+        if proj.zeros is not None and (proj.zeros.dtype != torch.uint8 or tuple(proj.zeros.shape) != shape):
+            raise ValueError(f"zeros must be uint8 {list(shape)}")
+        self.keep = tuple(None if t is None else m.dev(t).contiguous() for t in proj[:3])
+        self.arg = ctypes.byref(_lib.Q4Proj(*(_p(t) for t in self.keep), _DTYPES[proj.scales.dtype], proj.group))
+
+    def states(self, x: torch.Tensor, m: "_Marshal") -> torch.Tensor:
+        if not self.q4:
+            x = _bf16_rows(x, m)
+        else:
+            x = m.dev(x)
+            if x.dtype not in (torch.bfloat16, torch.float16):
+                raise ValueError("states must be bfloat16 or float16")
+            x = x.reshape(-1, x.shape[-1]).contiguous()
+        if x.numel() and x.shape[1] != self.d:
+            raise ValueError("states and projection must have the same last dimension")
+        return x
+
+
+def lm_head_logits(states: torch.Tensor, proj: Union[torch.Tensor, Q4Projection], out: Optional[torch.Tensor] = None,
                    err: Optional[torch.Tensor] = None) -> torch.Tensor:
     """``states [rows, d] . proj[V, d]^T`` in fp32 on the tensor cores
-    (include/sv_lm_head.h).  ``out``: optional f32 ``[rows, >= V]`` device
-    tensor with unit stride along V; ``err``: optional int32 ``[1]`` device
-    word that receives bit 0 if a device wait gave up."""
+    (include/sv_lm_head.h).  ``proj``: bf16 ``[V, d]``, or a ``Q4Projection``
+    (include/sv_lm_head_q4.h; the states may then be f16 too).  ``out``:
+    optional f32 ``[rows, >= V]`` device tensor with unit stride along V;
+    ``err``: optional int32 ``[1]`` device word that receives bit 0 if a
+    device wait gave up."""
     m = _Marshal(states)
+    if isinstance(proj, Q4Projection):
+        head = _Head(proj, m)
+        h = head.states(states, m)
+        if out is None:
+            out = torch.empty(h.shape[0], (head.V + 3) // 4 * 4, dtype=torch.float32, device=m.device)[:, :head.V]
+        elif (out.device != m.device or out.dtype != torch.float32 or out.dim() != 2 or out.shape[0] < h.shape[0]
+              or out.shape[1] < head.V or out.stride(1) != 1):
+            raise ValueError("out must be f32 [rows, >= V] on the states' device with unit stride along V")
+        with torch.cuda.device(m.device):
+            _check(head.lib.sv_lm_head_q4_logits(_p(h), _DTYPES[h.dtype], head.arg, h.shape[0], head.V, head.d,
+                                                 _p(out), out.stride(0), _p(err), m.stream()))
+        return out.cpu() if m.host else out
     h = _bf16_rows(states, m)
     w = _bf16_rows(proj, m)
     if h.shape[1] != w.shape[1]:
@@ -362,7 +457,8 @@ def lm_head_workspace(batch: int, sum_k: int, vocab: int, device=None) -> torch.
     return torch.empty(n, dtype=torch.uint8, device=device or torch.device("cuda", torch.cuda.current_device()))
 
 
-def lm_head_verify(target_states: torch.Tensor, draft_states: torch.Tensor, proj: torch.Tensor,
+def lm_head_verify(target_states: torch.Tensor, draft_states: torch.Tensor,
+                   proj: Union[torch.Tensor, Q4Projection],
                    temperature: torch.Tensor, draft_tokens: torch.Tensor, uniforms: torch.Tensor,
                    cu_k: Optional[torch.Tensor] = None, k: Optional[int] = None, flags: int = 0,
                    workspace: Optional[torch.Tensor] = None) -> LMHeadResult:
@@ -372,26 +468,28 @@ def lm_head_verify(target_states: torch.Tensor, draft_states: torch.Tensor, proj
     Returns the verification results and, for device inputs, the fp32 logits
     it read (views of the workspace, valid until it is reused)."""
     m = _Marshal(target_states)
-    ht = _bf16_rows(target_states, m)
-    hd = _bf16_rows(draft_states, m)
-    w = _bf16_rows(proj, m)
+    head = _Head(proj, m)
+    ht = head.states(target_states, m)
+    hd = head.states(draft_states, m)
+    if hd.dtype != ht.dtype:
+        raise ValueError("target and draft states must have the same dtype")
     tok = m.dev(draft_tokens.reshape(-1), torch.int32)
     u = m.dev(uniforms.reshape(-1), torch.float32)
     T = m.dev(temperature.reshape(-1), torch.float32)
     cu = m.dev(cu_k, torch.int32)
     B, K, sum_k = _layout(ht.shape[0], tok, cu, k)
-    V, d = w.shape
-    if ht.shape[1] != d or (hd.numel() and hd.shape[1] != d):
-        raise ValueError("states and projection must have the same last dimension")
-    lib = _lib.load()
+    V, d, lib = head.V, head.d, head.lib
     need = int(lib.sv_lm_head_workspace_size(B, sum_k, V))
     if workspace is None or workspace.numel() * workspace.element_size() < need:
         workspace = lm_head_workspace(B, sum_k, V, m.device)
     n, nxt, st = m.outputs(B)
     with torch.cuda.device(m.device):
-        _check(lib.sv_lm_head_verify(_p(ht), _p(hd), _p(w), d, _p(T), _p(tok), _p(u), _p(cu), B, K, sum_k, V,
-                                     _p(n), _p(nxt), _p(st), _p(workspace),
-                                     workspace.numel() * workspace.element_size(), flags, m.stream()))
+        tail = (d, _p(T), _p(tok), _p(u), _p(cu), B, K, sum_k, V, _p(n), _p(nxt), _p(st), _p(workspace),
+                workspace.numel() * workspace.element_size(), flags, m.stream())
+        if head.q4:
+            _check(lib.sv_lm_head_q4_verify(_p(ht), _p(hd), _DTYPES[ht.dtype], head.arg, *tail))
+        else:
+            _check(lib.sv_lm_head_verify(_p(ht), _p(hd), _p(head.w), *tail))
     res = m.finish(VerifyResult(n, nxt, st))
     lt = ld = None
     if not m.host:
@@ -461,4 +559,146 @@ def apply_penalties(target_logits: torch.Tensor, draft_logits: torch.Tensor, dra
         _check(lib.sv_apply_penalties(_p(tg), _p(dr), _DTYPES[tg.dtype], tg.stride(0), _p(ho), _p(ht),
                                       0 if ht is None else ht.numel(), _p(tok), _p(cu), B, K, sum_k, tg.shape[1],
                                       _p(r), _p(fr), _p(pr), _p(st), m.stream()))
+    return st
+
+
+# ---------------------------------------------------------------- beam search
+
+class BeamCandidates(NamedTuple):
+    scores: torch.Tensor  # f32 [B, n]: accumulated log-probabilities, best first; -inf where there is none
+    parents: torch.Tensor  # int32 [B, n]: the beam each candidate extends; -1 where there is none
+    tokens: torch.Tensor  # int32 [B, n]; -1 where there is none
+    status: torch.Tensor  # int32 [B]; SEQ_BAD_VALUE or 0
+
+
+def beam_select_workspace(batch: int, beams: int, vocab: int, n: int, device=None) -> torch.Tensor:
+    """A workspace for sv_beam_select of this size (uninitialised bytes)."""
+    size = int(_lib.load().sv_beam_select_workspace_size(batch, beams, vocab, n))
+    return torch.empty(size, dtype=torch.uint8, device=device or torch.device("cuda", torch.cuda.current_device()))
+
+
+def beam_select(logits: torch.Tensor, scores: torch.Tensor, n: Optional[int] = None,
+                finished: Optional[torch.Tensor] = None, eos: int = -1,
+                workspace: Optional[torch.Tensor] = None) -> BeamCandidates:
+    """The ``n`` best continuations (default: as many as beams) of every
+    sequence's beams (include/sv_beam.h): ``logits [B, W, V]`` (or the
+    ``[B * W, V]`` rows) in f32 / bf16 / f16, ``scores [B, W]`` the beams'
+    accumulated log-probabilities (-inf: a dead beam); a candidate's score is
+    its beam's plus the token's log-softmax; equal ones go by the lower beam,
+    then the lower token.  ``finished [B, W]``: beams that have ended offer
+    only ``(eos, their score)``.  ``workspace``: optional bytes of
+    ``beam_select_workspace``; calls that overlap on the GPU must not share
+    one."""
+    if scores.dim() != 2:
+        raise ValueError("scores must be [B, W]")
+    B, W = scores.shape
+    m = _Marshal(logits)
+    rows = _rows(m.dev(logits))
+    if rows.dtype not in _DTYPES:
+        raise ValueError("logits must be float32, bfloat16 or float16")
+    if rows.shape[0] != B * W:
+        raise ValueError(f"logits must hold one row for each of the {B} x {W} scores (got {rows.shape[0]})")
+    if finished is not None:
+        if finished.shape != scores.shape:
+            raise ValueError("finished must have the shape of scores")
+        finished = m.dev(finished if finished.dtype == torch.bool else finished != 0).contiguous().view(torch.uint8)
+    c = m.dev(scores, torch.float32).contiguous()
+    V, n = rows.shape[1], W if n is None else int(n)
+    lib = _lib.load()
+    need = int(lib.sv_beam_select_workspace_size(B, W, V, n))
+    if workspace is None or workspace.numel() * workspace.element_size() < need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=m.device)
+    shape = (B, max(n, 0))
+    out = torch.empty(shape, dtype=torch.float32, device=m.device)
+    par = torch.empty(shape, dtype=torch.int32, device=m.device)
+    tok = torch.empty(shape, dtype=torch.int32, device=m.device)
+    st = torch.empty(B, dtype=torch.int32, device=m.device)
+    with torch.cuda.device(m.device):
+        _check(lib.sv_beam_select(_p(rows), _DTYPES[rows.dtype], rows.stride(0) if B * W > 1 else max(rows.stride(0), V),
+                                  _p(c), _p(finished), int(eos), B, W, V, n, _p(out), _p(par), _p(tok), _p(st),
+                                  _p(workspace), workspace.numel() * workspace.element_size(), m.stream()))
+    res = BeamCandidates(out, par, tok, st)
+    return BeamCandidates(*(x.to("cpu") for x in res)) if m.host else res
+
+
+def _flat_stride(t: torch.Tensor, lo: int, hi: int, what: str):
+    """Extent and stride (elements) of dimensions lo..hi-1 taken as one."""
+    size, stride = 1, None
+    for d in range(hi - 1, lo - 1, -1):
+        if t.shape[d] == 1:
+            continue
+        if stride is None:
+            size, stride = t.shape[d], t.stride(d)
+        elif t.stride(d) == size * stride:
+            size *= t.shape[d]
+        else:
+            raise ValueError(f"{what} are not addressable in place with one stride")
+    return size, 0 if stride is None else stride
+
+
+def _beam_state(t: torch.Tensor, time_dim: Optional[int]) -> "_lib.BeamState":
+    e = t.element_size()
+    if time_dim is None:
+        span, k = 1, t.dim()  # the run of memory at the end of the shape, then segments of it
+        while k > 2 and (t.shape[k - 1] == 1 or t.stride(k - 1) == span):
+            span *= t.shape[k - 1]
+            k -= 1
+        if k == t.dim() and k > 2:
+            raise ValueError("a state's last dimension must have unit stride (moved in place)")
+        segs, seg = _flat_stride(t, 2, k, "a state's dimensions after [B, W]")
+        return _lib.BeamState(t.data_ptr(), t.stride(0) * e, t.stride(1) * e, seg * e, span * e, segs, 1, 0, 0)
+    segs, seg = _flat_stride(t, 2, time_dim, "a state's dimensions between the beams and the time")
+    span, stride = _flat_stride(t, time_dim + 1, t.dim(), "a state's dimensions after the time")
+    if (span > 1 and stride != 1) or (t.shape[time_dim] > 1 and t.stride(time_dim) != span):
+        raise ValueError("a state's tokens must be contiguous: unit stride after the time, one after another along it")
+    return _lib.BeamState(t.data_ptr(), t.stride(0) * e, t.stride(1) * e, seg * e, span * e, segs,
+                          t.shape[time_dim], 1, 0)
+
+
+def beam_reorder(states: Union[torch.Tensor, Sequence[torch.Tensor]], parents: torch.Tensor,
+                 lengths: Optional[torch.Tensor] = None,
+                 time_dim: Union[None, int, Sequence[Optional[int]]] = None) -> torch.Tensor:
+    """Moves beam states to their new slots, in place (include/sv_beam.h):
+    slot ``w`` of sequence ``b`` receives what slot ``parents[b, w]`` held
+    before the call; a negative parent leaves its slot as it is.  ``states``:
+    one CUDA tensor ``[B, W, ...]`` or several, of any types; none may share
+    memory with another.  ``lengths [B]`` with ``time_dim`` (one dimension for
+    all states, or one per state, None for a state without time): only the
+    first ``lengths[b]`` positions along it are in use and move.  Returns the
+    per-sequence status (int32 ``[B]``)."""
+    states = [states] if isinstance(states, torch.Tensor) else list(states)
+    dims = list(time_dim) if isinstance(time_dim, (list, tuple)) else [time_dim] * len(states)
+    if not states or len(dims) != len(states):
+        raise ValueError("at least one state is needed, and one time_dim for all or for each")
+    if parents.dim() != 2:
+        raise ValueError("parents must be [B, W]")
+    B, W = parents.shape
+    dev = states[0].device
+    if dev.type != "cuda":
+        raise ValueError("the states must be CUDA tensors (modified in place)")
+    if len({t.data_ptr() for t in states if t.numel()}) < sum(1 for t in states if t.numel()):
+        raise ValueError("a state is listed twice")
+    descs = (_lib.BeamState * len(states))()
+    for i, (t, td) in enumerate(zip(states, dims)):
+        if t.device != dev or t.dim() < 2 or tuple(t.shape[:2]) != (B, W):
+            raise ValueError(f"state {i} must be a CUDA tensor [{B}, {W}, ...] on {dev}")
+        if t.requires_grad and torch.is_grad_enabled():
+            raise ValueError(f"state {i} requires a gradient: it is modified in place")
+        if td is not None:
+            td = td + t.dim() if td < 0 else td
+            if not 2 <= td < t.dim():
+                raise ValueError(f"time_dim of state {i} must be a dimension after the beams")
+            if lengths is None:
+                raise ValueError("time_dim needs lengths")
+        if any(n > 1 and s == 0 for n, s in zip(t.shape, t.stride())):
+            raise ValueError(f"state {i} is a broadcast view (modified in place)")
+        descs[i] = _beam_state(t, td)
+    if lengths is not None and lengths.numel() != B:
+        raise ValueError("lengths must be [B]")
+    p = parents.to(device=dev, dtype=torch.int32).contiguous()
+    ln = None if lengths is None else lengths.reshape(-1).to(device=dev, dtype=torch.int32).contiguous()
+    st = torch.empty(B, dtype=torch.int32, device=dev)
+    with torch.cuda.device(dev):
+        _check(_lib.load().sv_beam_reorder(descs, len(states), _p(p), _p(ln), B, W, _p(st),
+                                           torch.cuda.current_stream(dev).cuda_stream))
     return st

@@ -1,0 +1,233 @@
+// Reordering of beam states in place (include/sv_beam.h).
+//
+// A slot's new contents are another slot's old ones, and one parent may go to
+// several slots while its own slot is overwritten.  A thread therefore owns a
+// column: the same bytes of every beam of one sequence.  It loads the column
+// of every moving slot's parent into registers, then stores; nobody else
+// touches those bytes, so the permutation with repetitions needs no second
+// buffer, no order among the slots and no barrier.  A slot that keeps its
+// parent costs nothing.
+#include <cuda_runtime.h>
+
+#include "../../include/sv_beam.h"
+#include "sv_host.h"
+
+namespace svb {
+
+constexpr int kThreads = 256;
+constexpr int kStates = 48;    // per launch: their descriptions are kernel parameters
+constexpr int kColBytes = 65536;  // bytes of one segment that a CTA takes (of every beam)
+
+struct State {
+  char* data;
+  long long seq, beam, seg;  // strides, bytes
+  long long token_bytes;
+  int segs, tokens, timed;
+  int unit;    // bytes of one access: divides every address, stride and extent
+  int chunks;  // CTAs per segment
+  unsigned first;  // first CTA of this state
+};
+
+struct Params {
+  State s[kStates];
+  const int* parents;
+  const int* lengths;
+  unsigned* status;  // NULL: another launch writes it
+  int n, B, W, min_tokens, status_ctas;
+};
+
+// Columns lo + tid, lo + tid + kThreads, ... < hi of one segment, M moves at
+// most, N columns at a time per thread: N x M accesses in flight.
+template <typename U, int M, int N>
+__device__ __forceinline__ void move_columns(char* base, const long long* src, const long long* dst, int m,
+                                             long long lo, long long hi) {
+  for (long long c = lo + threadIdx.x; c < hi; c += N * kThreads) {
+    U v[N][M];
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int j = 0; j < M; ++j)
+        if (j < m && c + i * kThreads < hi)
+          v[i][j] = *reinterpret_cast<const U*>(base + src[j] + (c + i * kThreads) * sizeof(U));
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int j = 0; j < M; ++j)
+        if (j < m && c + i * kThreads < hi)
+          *reinterpret_cast<U*>(base + dst[j] + (c + i * kThreads) * sizeof(U)) = v[i][j];
+  }
+}
+
+// 64 registers of data per thread whatever the number of moves; more moves
+// than fit at this access width take a narrower one.
+template <typename U>
+__device__ __forceinline__ void move_all(char* base, const long long* src, const long long* dst, int m, long long lo,
+                                         long long hi) {
+  if (m <= 2)
+    move_columns<U, 2, 8>(base, src, dst, m, lo, hi);
+  else if (m <= 4)
+    move_columns<U, 4, 4>(base, src, dst, m, lo, hi);
+  else if (m <= 8)
+    move_columns<U, 8, 2>(base, src, dst, m, lo, hi);
+  else if (m <= 16)
+    move_columns<U, 16, 1>(base, src, dst, m, lo, hi);
+  else if constexpr (sizeof(U) == 16)
+    m <= 32 ? move_columns<uint2, 32, 1>(base, src, dst, m, 2 * lo, 2 * hi)
+            : move_columns<unsigned, 64, 1>(base, src, dst, m, 4 * lo, 4 * hi);
+  else if constexpr (sizeof(U) == 8)
+    m <= 32 ? move_columns<uint2, 32, 1>(base, src, dst, m, lo, hi)
+            : move_columns<unsigned, 64, 1>(base, src, dst, m, 2 * lo, 2 * hi);
+  else
+    move_columns<U, 64, 1>(base, src, dst, m, lo, hi);
+}
+
+__device__ __forceinline__ bool sequence_ok(const Params& P, int b) {
+  for (int w = 0; w < P.W; ++w)
+    if (P.parents[b * P.W + w] >= P.W) return false;
+  if (P.lengths) {
+    const int len = P.lengths[b];
+    if (len < 0 || len > P.min_tokens) return false;
+  }
+  return true;
+}
+
+__global__ void __launch_bounds__(kThreads) reorder_kernel(const __grid_constant__ Params P) {
+  __shared__ long long src[SV_BEAM_MAX_BEAMS], dst[SV_BEAM_MAX_BEAMS];
+  __shared__ int s_moves;
+  unsigned cta = blockIdx.x;
+  if (cta < static_cast<unsigned>(P.status_ctas)) {
+    const int b = static_cast<int>(cta) * kThreads + static_cast<int>(threadIdx.x);
+    if (b < P.B) P.status[b] = sequence_ok(P, b) ? 0u : SV_SEQ_BAD_LAYOUT;
+    return;
+  }
+  cta -= static_cast<unsigned>(P.status_ctas);
+  int k = 0;
+  while (k + 1 < P.n && cta >= P.s[k + 1].first) ++k;
+  const State& S = P.s[k];
+  cta -= S.first;
+  const int chunk = static_cast<int>(cta % static_cast<unsigned>(S.chunks));
+  cta /= static_cast<unsigned>(S.chunks);
+  const int seg = static_cast<int>(cta % static_cast<unsigned>(S.segs));
+  const int b = static_cast<int>(cta / static_cast<unsigned>(S.segs));
+
+  const int len = S.timed ? P.lengths[b] : S.tokens;
+  const long long per = kColBytes / S.unit;
+  const long long lo = chunk * per;
+  long long hi = static_cast<long long>(len) * S.token_bytes / S.unit;
+  if (hi > lo + per) hi = lo + per;
+  if (lo >= hi) return;  // also a negative length
+  // the sequence's moves, by the first warp
+  if (threadIdx.x < 32) {
+    int moves = 0;
+    bool ok = !P.lengths || (P.lengths[b] >= 0 && P.lengths[b] <= P.min_tokens);
+    for (int w0 = 0; w0 < P.W; w0 += 32) {
+      const int w = w0 + static_cast<int>(threadIdx.x);
+      const int p = w < P.W ? P.parents[b * P.W + w] : -1;
+      const bool moving = p >= 0 && p != w;
+      ok = ok && !__any_sync(0xFFFFFFFFu, p >= P.W);
+      const unsigned mask = __ballot_sync(0xFFFFFFFFu, moving);
+      if (moving) {
+        const int at = moves + __popc(mask & ((1u << threadIdx.x) - 1u));
+        src[at] = p * S.beam;
+        dst[at] = w * S.beam;
+      }
+      moves += __popc(mask);
+    }
+    if (threadIdx.x == 0) s_moves = ok ? moves : 0;
+  }
+  __syncthreads();
+  const int m = s_moves;
+  if (m == 0) return;
+  char* base = S.data + b * S.seq + seg * S.seg;
+  switch (S.unit) {
+    case 16: move_all<uint4>(base, src, dst, m, lo, hi); break;
+    case 8: move_all<uint2>(base, src, dst, m, lo, hi); break;
+    case 4: move_all<unsigned>(base, src, dst, m, lo, hi); break;
+    case 2: move_all<unsigned short>(base, src, dst, m, lo, hi); break;
+    default: move_all<unsigned char>(base, src, dst, m, lo, hi); break;
+  }
+}
+
+}  // namespace svb
+
+extern "C" sv_status sv_beam_reorder(const sv_beam_state* states, int32_t n_states, const int32_t* parents,
+                                     const int32_t* lengths, int32_t batch, int32_t beams, uint32_t* status,
+                                     void* stream) {
+  svh::clear_error();
+  if (batch < 0) return svh::fail(SV_ERR_ARG, "batch (%d) must be >= 0", batch);
+  if (beams < 1 || beams > SV_BEAM_MAX_BEAMS)
+    return svh::fail(SV_ERR_ARG, "beams (%d) must be in [1, %d]", beams, SV_BEAM_MAX_BEAMS);
+  if (n_states < 1 || !states) return svh::fail(SV_ERR_ARG, "at least one state is needed");
+  if (static_cast<long long>(batch) * beams > 0x7FFFFFFFLL) return svh::fail(SV_ERR_ARG, "batch * beams too large");
+  int min_tokens = 0x7FFFFFFF;
+  long long all_ctas = batch;
+  for (int i = 0; i < n_states; ++i) {
+    const sv_beam_state& s = states[i];
+    if (s.segs < 0 || s.tokens < 0 || s.token_bytes < 0)
+      return svh::fail(SV_ERR_ARG, "state %d: a size is negative", i);
+    if (s.seq_stride < 0 || s.beam_stride < 0 || s.seg_stride < 0)
+      return svh::fail(SV_ERR_ARG, "state %d: a stride is negative", i);
+    if (s.token_bytes > 0 && s.tokens > (1LL << 46) / s.token_bytes)
+      return svh::fail(SV_ERR_ARG, "state %d: a segment is too large", i);
+    const long long bytes = s.tokens * s.token_bytes;
+    if (batch > 0 && s.segs > 0 && bytes > 0) {
+      if (!s.data) return svh::fail(SV_ERR_ARG, "state %d: data is NULL", i);
+      if ((s.segs > 1 && s.seg_stride < bytes) || (beams > 1 && s.beam_stride < bytes))
+        return svh::fail(SV_ERR_ARG, "state %d: a stride is shorter than a segment", i);
+    }
+    const long long chunks = (bytes + svb::kColBytes - 1) / svb::kColBytes;
+    all_ctas += chunks > 0x7FFFFFFFLL ? 0x7FFFFFFFLL : chunks * s.segs;
+    if (all_ctas > 0x7FFFFFFFLL || (batch > 0 && all_ctas > 0x7FFFFFFFLL / batch))
+      return svh::fail(SV_ERR_UNSUPPORTED, "the states are too large for one call");
+    if (s.timed) {
+      if (!lengths) return svh::fail(SV_ERR_ARG, "state %d is timed: lengths is NULL", i);
+      if (s.tokens < min_tokens) min_tokens = s.tokens;
+    }
+  }
+  if (batch == 0) return SV_OK;
+  if (!parents || !status) return svh::fail(SV_ERR_ARG, "parents or status is NULL");
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  for (int at = 0; at < n_states; at += svb::kStates) {
+    svb::Params p;
+    p.parents = parents;
+    p.lengths = lengths;
+    p.status = at == 0 ? status : nullptr;
+    p.B = batch;
+    p.W = beams;
+    p.min_tokens = min_tokens;
+    p.status_ctas = at == 0 ? (batch + svb::kThreads - 1) / svb::kThreads : 0;
+    p.n = 0;
+    long long ctas = 0;
+    for (int i = at; i < n_states && i < at + svb::kStates; ++i) {
+      const sv_beam_state& s = states[i];
+      const long long bytes = s.tokens * s.token_bytes;
+      if (s.segs == 0 || bytes == 0) continue;
+      svb::State& q = p.s[p.n++];
+      q.data = static_cast<char*>(s.data);
+      q.seq = s.seq_stride;
+      q.beam = s.beam_stride;
+      q.seg = s.seg_stride;
+      q.token_bytes = s.token_bytes;
+      q.segs = s.segs;
+      q.tokens = s.tokens;
+      q.timed = s.timed != 0;
+      // the widest access that every address and extent allows
+      // (a timed state may end after any token, another one only at its end)
+      unsigned long long any = reinterpret_cast<uintptr_t>(s.data) | 16u |
+                               static_cast<unsigned long long>(q.timed ? s.token_bytes : bytes);
+      if (batch > 1) any |= static_cast<unsigned long long>(s.seq_stride);
+      if (beams > 1) any |= static_cast<unsigned long long>(s.beam_stride);
+      if (s.segs > 1) any |= static_cast<unsigned long long>(s.seg_stride);
+      q.unit = static_cast<int>(any & (~any + 1));
+      q.chunks = static_cast<int>((bytes + svb::kColBytes - 1) / svb::kColBytes);
+      q.first = static_cast<unsigned>(ctas);
+      ctas += static_cast<long long>(q.chunks) * s.segs * batch;
+    }
+    const long long grid = ctas + p.status_ctas;
+    if (grid == 0) continue;
+    svb::reorder_kernel<<<static_cast<unsigned>(grid), svb::kThreads, 0, st>>>(p);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return svh::fail(SV_ERR_CUDA, "kernel launch: %s", cudaGetErrorString(e));
+  }
+  return SV_OK;
+}

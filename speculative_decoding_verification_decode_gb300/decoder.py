@@ -149,3 +149,81 @@ class SpeculativeDecoder:
             else:
                 self.round()
         return self.tokens, self.lengths
+
+
+class BeamDecoder:
+    """Device-resident beam search: every step scores the beams
+    (``step_fn``), selects the best continuations, moves the beams' states to
+    their parents' new slots and appends the tokens, with no host
+    synchronisation, so a step can be captured once as a CUDA graph and
+    replayed (beam_select and beam_reorder, include/sv_beam.h).
+
+    ``step_fn(tokens, lengths) -> [B, W, V]``: logits of the next token after
+    the first ``lengths[b]`` tokens of each beam; deterministic and
+    graph-capturable.  What it keeps per beam (caches, recurrent states) is
+    given in ``states`` and moves with the beams."""
+
+    def __init__(self, step_fn: Callable, tokens: torch.Tensor, lengths: torch.Tensor, eos: int = -1,
+                 states=(), time_dims=()):
+        """``tokens`` [B, W, max_len] int32 with the prompt in every beam,
+        ``lengths`` [B] int32; ``eos`` ends a beam (negative: no token does);
+        ``states`` / ``time_dims`` as ``beam_reorder`` takes them (one
+        ``time_dims`` entry per state)."""
+        if tokens.dim() != 3 or tokens.dtype != torch.int32 or lengths.dtype != torch.int32:
+            raise ValueError("tokens must be [B, W, max_len] int32 and lengths [B] int32")
+        if len(states) != len(time_dims):
+            raise ValueError("one entry of time_dims per state")
+        self.step_fn, self.tokens, self.lengths, self.eos = step_fn, tokens, lengths, int(eos)
+        self.B, self.W, self.max_len = tokens.shape
+        self.states, self.time_dims = [tokens, *states], [2, *time_dims]
+        dev = tokens.device
+        # every beam starts as the prompt: only the first may extend it, or all beams would stay alike
+        self.scores = torch.full((self.B, self.W), float("-inf"), device=dev)
+        self.scores[:, 0] = 0.0
+        self.finished = torch.zeros(self.B, self.W, dtype=torch.bool, device=dev)
+        self.rows = torch.arange(self.B, device=dev)
+        self.graph = None
+
+    def step(self):
+        """One token for every beam; returns the selection."""
+        logits = self.step_fn(self.tokens, self.lengths)
+        sel = api.beam_select(logits, self.scores, finished=self.finished if self.eos >= 0 else None, eos=self.eos)
+        api.beam_reorder(self.states, sel.parents, self.lengths, self.time_dims)
+        at = self.lengths.long().clamp(max=self.max_len - 1)
+        self.tokens[self.rows, :, at] = sel.tokens.clamp(min=0)
+        if self.eos >= 0:  # a finished beam's one candidate is eos again, so the token tells
+            self.finished.copy_(sel.tokens == self.eos)
+        self.scores.copy_(sel.scores)
+        self.lengths.add_(1).clamp_(max=self.max_len)
+        return sel
+
+    def capture(self):
+        """Capture one step as a CUDA graph (after a warm-up step on a saved
+        copy of the state, restored before the capture)."""
+        kept = [*self.states, self.lengths, self.scores, self.finished]
+        saved = [t.clone() for t in kept]
+        s = torch.cuda.Stream(self.tokens.device)
+        s.wait_stream(torch.cuda.current_stream(self.tokens.device))
+        with torch.cuda.stream(s):
+            self.step()
+        torch.cuda.current_stream(self.tokens.device).wait_stream(s)
+        for t, o in zip(kept, saved):
+            t.copy_(o)
+        torch.cuda.synchronize(self.tokens.device)
+        self.graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(self.graph, stream=s, capture_error_mode="relaxed"):
+            self.step()
+        torch.cuda.synchronize(self.tokens.device)
+        return self.graph
+
+    def run(self, steps: int, graph: bool = True):
+        """``steps`` steps, replaying the captured graph when ``graph``;
+        returns (tokens, lengths, scores), beams best first."""
+        if graph and self.graph is None:
+            self.capture()
+        for _ in range(steps):
+            if graph:
+                self.graph.replay()
+            else:
+                self.step()
+        return self.tokens, self.lengths, self.scores
