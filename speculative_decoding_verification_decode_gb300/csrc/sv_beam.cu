@@ -1,28 +1,51 @@
 // Beam search's selection over beams and vocabulary (include/sv_beam.h).
 //
-// First form: one CTA per row takes the row's maximum and sum of exponentials
-// in 64 bits; then one CTA per sequence takes the n candidates one after
-// another, each the best that comes after the one before it in the order
-// (score descending, beam W + token ascending).
+// The n best of W x V scores c_w + l_wv - lse_w need every logit once for the
+// logarithms of the sums, and nearly none of them a second time.  Two kernels:
+//
+// 1 rows_kernel, over (row, slice): a streaming pass that leaves, per slice,
+//   the maximum M and s = sum 2^(l k - ceil(M k)) (k = log2 e in f32; the
+//   subtrahend is an integer, so partial sums are joined by exact powers of
+//   two), and per group of 64 16-byte vectors its maximum.
+// 2 pick_kernel, one CTA per sequence: the logarithms; tau, a lower bound of
+//   the n-th best of the groups' maxima in score terms (bisection over values
+//   in registers, ended as soon as between n and 2n of them lie above): n
+//   candidates lie at or above tau, so only groups whose maximum reaches it
+//   are read again, about n of them, and of those the logits that reach it
+//   are ranked.
+//
+// Order.  Scores of one beam are ordered by its logits, exactly.  Between
+// beams the logarithms' f32 errors count, so pairs of different beams that lie
+// closer than their bound (eps each) send their rows through precise_lse: the sum in 64-bit fixed point from terms good to 2^-37, equal
+// for rows that are permutations of one another, whatever the order.  All
+// scores are then compared as doubles.
+//
+// eps, relative error of a row's sum (hence absolute error of its log), in
+// units of 2^-24: an exponent's rounding, 1 per unit of its size, which is
+// H - H_min <= 17 bits on average under the row's own weights (17 ln 2 = 12);
+// k's representation, at most 3 for entropies up to 12 nats after dividing by
+// the same k; the exponential, 8 (2^-21); the additions on a term's way, 3 in
+// its vector, 3 to its batch, 8 batches of a warp, 5 + 3 + 6 in warp, CTA and
+// row; the logarithm of a value in [1, 2), 2.  Together 53, taken as 64 (and
+// one more for each doubling of the vocabulary beyond 2^17 and each 32 slices).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include "../../include/sv_beam.h"
 #include "sv_host.h"
+#include "sv_ptx.cuh"
 
 namespace svs {
 
-constexpr int kThreads = 512;
-
-template <typename T>
-__device__ __forceinline__ float to_f32(T x);
-template <>
-__device__ __forceinline__ float to_f32(float x) { return x; }
-template <>
-__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
-template <>
-__device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
+constexpr int kRowThreads = 256, kRowWarps = kRowThreads / 32;
+constexpr int kPickThreads = 512, kPickWarps = kPickThreads / 32;
+constexpr int kGroupVecs = 64;   // 16-byte vectors per group: two per lane of a warp
+constexpr int kCap = 4096;       // candidate entries a CTA holds (power of two)
+constexpr int kGroupList = 1024; // groups read again before the ordered pass takes over
+constexpr int kPerThread = 16;   // maxima per thread in the bisection
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLarge = 1048576.f;  // |M| above this: the row's sum is taken precisely (l k - c would lose bits)
 
 struct Params {
   const void* logits;
@@ -30,7 +53,12 @@ struct Params {
   const float* scores;
   const unsigned char* finished;
   int eos, B, W, V, n;
-  double* lse;  // [B W]: -inf: no candidates; NaN: bad value
+  int groups;  // per row
+  int slices;  // CTAs per row
+  int per_slice;  // groups per slice
+  double eps;     // bound of a fast logarithm's error
+  float2* part;   // [B W][slices]: (M, s); M NaN: bad value
+  float* gmax;    // [B W][groups]
   float* out_s;
   int* out_p;
   int* out_t;
@@ -38,120 +66,714 @@ struct Params {
 };
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) row_kernel(Params P) {
-  const long long r = blockIdx.x;
-  __shared__ double red[kThreads];
-  const float c = P.scores[r];
-  if ((P.finished && P.finished[r]) || c == -INFINITY) return;
-  const T* row = static_cast<const T*>(P.logits) + r * P.stride;
-  float m = -INFINITY;
-  bool bad = false;
-  for (int v = threadIdx.x; v < P.V; v += kThreads) {
-    const float x = to_f32(row[v]);
-    bad |= isnan(x) || x == INFINITY;
-    m = fmaxf(m, x);
+struct Elem;
+template <>
+struct Elem<float> {
+  static constexpr int E = 4;
+  static __device__ float f32(float x) { return x; }
+  static __device__ void unpack(uint4 v, float (&x)[4]) {
+    x[0] = __uint_as_float(v.x);
+    x[1] = __uint_as_float(v.y);
+    x[2] = __uint_as_float(v.z);
+    x[3] = __uint_as_float(v.w);
   }
-  red[threadIdx.x] = bad ? static_cast<double>(NAN) : static_cast<double>(m);
-  __syncthreads();
-  for (int h = kThreads / 2; h > 0; h /= 2) {
-    if (threadIdx.x < h) {
-      const double a = red[threadIdx.x], b = red[threadIdx.x + h];
-      red[threadIdx.x] = isnan(a) ? a : isnan(b) ? b : fmax(a, b);
-    }
-    __syncthreads();
+  // the maximum of a vector, NaN if it holds one
+  static __device__ float max_of(uint4 v) {
+    return svk::fmax_nan(svk::fmax_nan(__uint_as_float(v.x), __uint_as_float(v.y)),
+                         svk::fmax_nan(__uint_as_float(v.z), __uint_as_float(v.w)));
   }
-  const double mx = red[0];
-  __syncthreads();
-  if (isnan(mx) || mx == -INFINITY) {
-    if (threadIdx.x == 0) P.lse[r] = mx;
-    return;
+  static __device__ float max_of(uint4 a, uint4 b) { return svk::fmax_nan(max_of(a), max_of(b)); }
+  static __device__ uint4 neg_inf() { return make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u); }
+};
+template <>
+struct Elem<__nv_bfloat16> {
+  static constexpr int E = 8;
+  static __device__ float f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+  static __device__ void two(unsigned w, float& a, float& b) {
+    a = __uint_as_float(w << 16);
+    b = __uint_as_float(w & 0xFFFF0000u);
   }
-  // the sum in units of 2^-60, exact whatever the order: rows that are
-  // permutations of one another get equal sums, so their candidates tie
-  unsigned long long hi = 0, lo = 0;
-  for (int v = threadIdx.x; v < P.V; v += kThreads) {
-    const auto q = static_cast<unsigned long long>(exp(static_cast<double>(to_f32(row[v])) - mx) * 1152921504606846976.0);
-    hi += q >> 32;
-    lo += q & 0xFFFFFFFFu;
+  static __device__ void unpack(uint4 v, float (&x)[8]) {
+    two(v.x, x[0], x[1]);
+    two(v.y, x[2], x[3]);
+    two(v.z, x[4], x[5]);
+    two(v.w, x[6], x[7]);
   }
-  __shared__ unsigned long long ih[kThreads], il[kThreads];
-  ih[threadIdx.x] = hi;
-  il[threadIdx.x] = lo;
-  __syncthreads();
-  for (int h = kThreads / 2; h > 0; h /= 2) {
-    if (threadIdx.x < h) {
-      ih[threadIdx.x] += ih[threadIdx.x + h];
-      il[threadIdx.x] += il[threadIdx.x + h];
-    }
-    __syncthreads();
+  static __device__ unsigned pack_max(uint4 v) {
+    return svk::bf16x2_max_nan(svk::bf16x2_max_nan(v.x, v.y), svk::bf16x2_max_nan(v.z, v.w));
   }
-  if (threadIdx.x == 0) {
-    const double total = static_cast<double>(ih[0] + (il[0] >> 32)) + static_cast<double>(il[0] & 0xFFFFFFFFu) * 0x1p-32;
-    P.lse[r] = mx + log(total * 0x1p-28);
+  static __device__ float max_of(uint4 a, uint4 b) {
+    float x, y;
+    two(svk::bf16x2_max_nan(pack_max(a), pack_max(b)), x, y);
+    return svk::fmax_nan(x, y);
   }
+  static __device__ uint4 neg_inf() { return make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u); }
+};
+template <>
+struct Elem<__half> {
+  static constexpr int E = 8;
+  static __device__ float f32(__half x) { return __half2float(x); }
+  static __device__ void two(unsigned w, float& a, float& b) {
+    const float2 f = __half22float2(*reinterpret_cast<__half2*>(&w));
+    a = f.x;
+    b = f.y;
+  }
+  static __device__ void unpack(uint4 v, float (&x)[8]) {
+    two(v.x, x[0], x[1]);
+    two(v.y, x[2], x[3]);
+    two(v.z, x[4], x[5]);
+    two(v.w, x[6], x[7]);
+  }
+  static __device__ unsigned pack_max(uint4 v) {
+    return svk::f16x2_max_nan(svk::f16x2_max_nan(v.x, v.y), svk::f16x2_max_nan(v.z, v.w));
+  }
+  static __device__ float max_of(uint4 a, uint4 b) {
+    float x, y;
+    two(svk::f16x2_max_nan(pack_max(a), pack_max(b)), x, y);
+    return svk::fmax_nan(x, y);
+  }
+  static __device__ uint4 neg_inf() { return make_uint4(0xFC00FC00u, 0xFC00FC00u, 0xFC00FC00u, 0xFC00FC00u); }
+};
+
+// A row as aligned 16-byte vectors: vector i holds elements i E - head ..,
+// those outside [0, V) read as -inf and never touched in memory.
+template <typename T>
+struct Row {
+  static constexpr int E = Elem<T>::E;
+  const T* p;
+  int head;  // elements of vector 0 before the row
+  int V;
+  __device__ Row(const T* row, int vocab)
+      : p(row), head(static_cast<int>((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(T))), V(vocab) {}
+  __device__ long long first(long long vec) const { return vec * E - head; }
+  __device__ bool inside(long long v0, long long v1) const { return first(v0) >= 0 && first(v1) + E <= V; }
+  __device__ uint4 whole(long long vec) const { return __ldg(reinterpret_cast<const uint4*>(p + first(vec))); }
+  __device__ uint4 load(long long vec) const {
+    const long long e = first(vec);
+    if (e >= 0 && e + E <= V) return whole(vec);
+    uint4 v = Elem<T>::neg_inf();
+    T* x = reinterpret_cast<T*>(&v);
+#pragma unroll
+    for (int i = 0; i < E; ++i)
+      if (e + i >= 0 && e + i < V) x[i] = p[e + i];
+    return v;
+  }
+};
+
+__device__ __forceinline__ float warp_max_nan(float x) {
+#pragma unroll
+  for (int o = 16; o > 0; o /= 2) x = svk::fmax_nan(x, __shfl_xor_sync(0xFFFFFFFFu, x, o));
+  return x;
+}
+
+// Sum of one vector's terms 2^(x k - c), a tree.
+template <int E>
+__device__ __forceinline__ float terms(const float (&x)[E], float c) {
+  float e[E];
+#pragma unroll
+  for (int i = 0; i < E; ++i) e[i] = svk::ex2_ftz(fmaf(x[i], kLog2e, -c));
+#pragma unroll
+  for (int h = E / 2; h > 0; h /= 2)
+#pragma unroll
+    for (int i = 0; i < h; ++i) e[i] += e[i + h];
+  return e[0];
+}
+
+// The integer that the exponents of a sum with maximum M are taken below.
+__device__ __forceinline__ float base_of(float M) { return ceilf(M * kLog2e); }
+
+// Joins (M, s) and (M2, s2): the scale factors are powers of two.
+__device__ __forceinline__ void join(float& M, float& s, float M2, float s2) {
+  const float m = svk::fmax_nan(M, M2);
+  if (m == M2 && M == M2) {
+    s += s2;
+  } else if (m > -INFINITY && m < INFINITY) {
+    const float c = base_of(m);
+    s = (M > -INFINITY ? s * svk::ex2_ftz(base_of(M) - c) : 0.f) + (M2 > -INFINITY ? s2 * svk::ex2_ftz(base_of(M2) - c) : 0.f);
+  }
+  M = m;
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) pick_kernel(Params P) {
-  const int b = blockIdx.x;
-  __shared__ double rs[kThreads];
-  __shared__ int ri[kThreads];
-  bool bad = false;
-  for (int w = 0; w < P.W; ++w) {
-    const float c = P.scores[b * P.W + w];
-    bad |= isnan(c) || c == INFINITY;
-    if (!(P.finished && P.finished[b * P.W + w]) && c != -INFINITY) bad |= isnan(P.lse[b * P.W + w]);
-  }
-  double last = INFINITY;
-  int last_i = -1;
-  for (int k = 0; k < P.n; ++k) {
-    double best = -INFINITY;
-    int bi = 0x7FFFFFFF;
-    auto offer = [&](double s, int i) {
-      if (s > -INFINITY && (s < last || (s == last && i > last_i)) && (s > best || (s == best && i < bi))) {
-        best = s;
-        bi = i;
-      }
-    };
-    for (int w = 0; !bad && w < P.W; ++w) {
-      const long long r = static_cast<long long>(b) * P.W + w;
-      const float c = P.scores[r];
-      if (c == -INFINITY) continue;
-      if (P.finished && P.finished[r]) {
-        offer(c, w * P.V + P.eos);
-        continue;
-      }
-      const double lse = P.lse[r];
-      if (lse == -INFINITY) continue;
-      const T* row = static_cast<const T*>(P.logits) + r * P.stride;
-      for (int v = threadIdx.x; v < P.V; v += kThreads)
-        offer(static_cast<double>(c) + (static_cast<double>(to_f32(row[v])) - lse), w * P.V + v);
+__global__ void __launch_bounds__(kRowThreads) rows_kernel(const Params P) {
+  constexpr int E = Elem<T>::E;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const long long r = blockIdx.x / static_cast<unsigned>(P.slices);
+  const int slice = static_cast<int>(blockIdx.x % static_cast<unsigned>(P.slices));
+  if ((P.finished && P.finished[r]) || P.scores[r] == -INFINITY) return;
+  const Row<T> row(static_cast<const T*>(P.logits) + r * P.stride, P.V);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int g_end = min(P.groups, (slice + 1) * P.per_slice);
+  float* gmax = P.gmax + r * P.groups;
+  float M = -INFINITY, s = 0.f;
+  for (int g = slice * P.per_slice + 2 * warp; g < g_end; g += 2 * kRowWarps) {
+    const long long v0 = static_cast<long long>(g) * kGroupVecs + lane;
+    uint4 q[4];
+    if (row.inside(v0 - lane, v0 - lane + 2 * kGroupVecs - 1)) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) q[i] = row.whole(v0 + 32 * i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) q[i] = row.load(v0 + 32 * i);
     }
-    rs[threadIdx.x] = best;
-    ri[threadIdx.x] = bi;
+    const float ma = warp_max_nan(Elem<T>::max_of(q[0], q[1])), mb = warp_max_nan(Elem<T>::max_of(q[2], q[3]));
+    if (lane == 0) {
+      gmax[g] = ma;
+      if (g + 1 < P.groups) gmax[g + 1] = mb;
+    }
+    const float m = svk::fmax_nan(M, svk::fmax_nan(ma, mb));
+    if (m > -INFINITY && m < INFINITY) {
+      const float c = base_of(m);
+      if (M > -INFINITY && M < m) s *= svk::ex2_ftz(base_of(M) - c);
+      float t[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float x[E];
+        Elem<T>::unpack(q[i], x);
+        t[i] = terms(x, c);
+      }
+      s += (t[0] + t[1]) + (t[2] + t[3]);
+    }
+    M = m;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o /= 2) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+  __shared__ float2 part[kRowWarps];
+  if (lane == 0) part[warp] = make_float2(M, s);
+  __syncthreads();
+  if (warp == 0) {
+    float2 a = lane < kRowWarps ? part[lane] : make_float2(-INFINITY, 0.f);
+#pragma unroll
+    for (int o = kRowWarps / 2; o > 0; o /= 2) {
+      const float M2 = __shfl_xor_sync(0xFFFFFFFFu, a.x, o), s2 = __shfl_xor_sync(0xFFFFFFFFu, a.y, o);
+      join(a.x, a.y, M2, s2);
+    }
+    if (lane == 0) P.part[r * P.slices + slice] = a;
+  }
+}
+
+// ---------------------------------------------------------------- the second kernel
+
+struct Shared {
+  double lse[SV_BEAM_MAX_BEAMS];
+  double cum[SV_BEAM_MAX_BEAMS];
+  float M[SV_BEAM_MAX_BEAMS];
+  float add[SV_BEAM_MAX_BEAMS];  // f32 score = logit + add; -inf: no candidates
+  unsigned char ended[SV_BEAM_MAX_BEAMS], precise[SV_BEAM_MAX_BEAMS], again[SV_BEAM_MAX_BEAMS];
+  unsigned long long table[33];  // 2^(j / 32), j = -16..16, units of 2^-61
+  unsigned long long sum_hi[kPickWarps], sum_lo[kPickWarps];
+  int cnt[2][kPickWarps];
+  int bad, n_groups, n_entries, redo, next;
+  int order[SV_BEAM_MAX_CANDIDATES];
+  int2 group[kGroupList];  // (row, group)
+  unsigned long long key[kCap];  // ordered bits of the score
+  int index[kCap];               // w V + v
+  float logit[kCap];
+};
+
+__device__ __forceinline__ unsigned f32_key(float x) {
+  const unsigned b = __float_as_uint(x);
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float key_f32(unsigned k) {
+  return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
+}
+__device__ __forceinline__ unsigned long long f64_key(double x) {
+  const unsigned long long b = __double_as_longlong(x);
+  return b >> 63 ? ~b : b | 0x8000000000000000ull;
+}
+__device__ __forceinline__ double key_f64(unsigned long long k) {
+  return __longlong_as_double(k >> 63 ? k & 0x7FFFFFFFFFFFFFFFull : ~k);
+}
+
+// Sum over the CTA; `turn` alternates the slots, so one barrier is enough.
+__device__ __forceinline__ int block_sum(Shared& sm, int x, int& turn) {
+  x = __reduce_add_sync(0xFFFFFFFFu, x);
+  if (threadIdx.x % 32 == 0) sm.cnt[turn][threadIdx.x / 32] = x;
+  __syncthreads();
+  int t = 0;
+#pragma unroll
+  for (int w = 0; w < kPickWarps; ++w) t += sm.cnt[turn][w];
+  turn ^= 1;
+  return t;
+}
+
+// e^(x - M) in units of 2^-60, within 2^-37 of it: x - M exactly as a sum of
+// two floats; times log2 e likewise; the fraction as j / 32 + g; 2^(j/32)
+// from the table, 2^g - 1 by the first terms of its series (g ln 2 <= 0.011,
+// the fifth power's term is the last above 2^-40).
+__device__ __forceinline__ unsigned long long precise_term(float x, float M, const unsigned long long* table) {
+  constexpr double kL = 1.4426950408889634, kN = 0.6931471805599453;
+  constexpr float L1 = static_cast<float>(kL), L2 = static_cast<float>(kL - static_cast<double>(L1));
+  constexpr float N1 = static_cast<float>(kN), N2 = static_cast<float>(kN - static_cast<double>(N1));
+  const float y = __fsub_rn(x, M);
+  if (!(y > -45.f)) return 0;  // below 2^-64; -inf
+  const float bb = __fsub_rn(y, x);
+  const float yl = __fadd_rn(__fsub_rn(x, __fsub_rn(y, bb)), __fsub_rn(-M, bb));
+  const float t = __fmul_rn(y, L1);
+  const float tl = fmaf(yl, L1, fmaf(y, L2, fmaf(y, L1, -t)));
+  const float n = rintf(t), f = __fsub_rn(t, n), j = rintf(f * 32.f), g = fmaf(j, -0.03125f, f);
+  const float z = __fmul_rn(g, N1);
+  const float zl = fmaf(tl, N1, fmaf(g, N2, fmaf(g, N1, -z)));
+  const float a = z + zl;
+  const float w = fmaf(a * a, fmaf(a, fmaf(a, fmaf(a, 1.f / 120.f, 1.f / 24.f), 1.f / 6.f), 0.5f), zl);
+  const long long Z = __float2ll_rn(z * 1125899906842624.f) + __float2ll_rn(w * 1125899906842624.f);  // units of 2^-50
+  const long long e = static_cast<long long>(table[static_cast<int>(j) + 16]);
+  const int shift = 1 - static_cast<int>(n);
+  return shift < 64 ? static_cast<unsigned long long>(e + __mul64hi(e, Z * 16384)) >> shift : 0ull;
+}
+
+// The row's logarithm to better than 2^-36, by the whole CTA.
+template <typename T>
+__device__ __noinline__ void precise_lse(Shared& sm, const Params& P, int b, int w) {
+  constexpr int E = Elem<T>::E;
+  const Row<T> row(static_cast<const T*>(P.logits) + (static_cast<long long>(b) * P.W + w) * P.stride, P.V);
+  if (threadIdx.x < 33)
+    sm.table[threadIdx.x] = static_cast<unsigned long long>(exp2((static_cast<int>(threadIdx.x) - 16) / 32.0) * 0x1p61);
+  __syncthreads();
+  const float M = sm.M[w];
+  unsigned long long hi = 0, lo = 0;
+  const long long vecs = (static_cast<long long>(row.head) + P.V + E - 1) / E;
+  for (long long v = threadIdx.x; v < vecs; v += kPickThreads) {
+    float x[E];
+    Elem<T>::unpack(row.load(v), x);
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const unsigned long long q = precise_term(x[i], M, sm.table);
+      hi += q >> 32;
+      lo += q & 0xFFFFFFFFu;
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o /= 2) {
+    hi += __shfl_xor_sync(0xFFFFFFFFu, hi, o);
+    lo += __shfl_xor_sync(0xFFFFFFFFu, lo, o);
+  }
+  if (threadIdx.x % 32 == 0) {
+    sm.sum_hi[threadIdx.x / 32] = hi;
+    sm.sum_lo[threadIdx.x / 32] = lo;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    hi = lo = 0;
+    for (int i = 0; i < kPickWarps; ++i) {
+      hi += sm.sum_hi[i];
+      lo += sm.sum_lo[i];
+    }
+    const double total = static_cast<double>(hi + (lo >> 32)) + static_cast<double>(lo & 0xFFFFFFFFu) * 0x1p-32;
+    sm.lse[w] = static_cast<double>(M) + log(total * 0x1p-28);
+    sm.precise[w] = 1;
+    sm.again[w] = 0;
+  }
+  __syncthreads();
+}
+
+__device__ __forceinline__ double score_of(const Shared& sm, int w, float l) {
+  return sm.ended[w] ? sm.cum[w] : sm.cum[w] + (static_cast<double>(l) - sm.lse[w]);
+}
+
+__device__ __forceinline__ bool before(unsigned long long ka, int ia, unsigned long long kb, int ib) {
+  return ka > kb || (ka == kb && ia < ib);
+}
+
+// order[0..min(L, most) - 1]: the entries' places, best first.
+__device__ __forceinline__ void sort_entries(Shared& sm, int L, int most) {
+  if (L <= kPickThreads) {  // by counting
+    const int i = threadIdx.x;
+    if (i < L) {
+      const unsigned long long k = sm.key[i];
+      const int x = sm.index[i];
+      int rank = 0;
+      for (int j = 0; j < L; ++j) rank += before(sm.key[j], sm.index[j], k, x);
+      if (rank < most) sm.order[rank] = i;
+    }
     __syncthreads();
-    for (int h = kThreads / 2; h > 0; h /= 2) {
-      if (threadIdx.x < h) {
-        const double s = rs[threadIdx.x + h];
-        const int i = ri[threadIdx.x + h];
-        if (s > rs[threadIdx.x] || (s == rs[threadIdx.x] && i < ri[threadIdx.x])) {
-          rs[threadIdx.x] = s;
-          ri[threadIdx.x] = i;
+    return;
+  }
+  int size = kPickThreads;
+  while (size < L) size *= 2;
+  for (int i = L + threadIdx.x; i < size; i += kPickThreads) {
+    sm.key[i] = 0;
+    sm.index[i] = 0x7FFFFFFF;
+  }
+  __syncthreads();
+  for (int k = 2; k <= size; k *= 2)
+    for (int h = k / 2; h > 0; h /= 2) {
+      for (int t = threadIdx.x; t < size / 2; t += kPickThreads) {
+        const int i = (t / h) * 2 * h + t % h, j = i + h;
+        const bool up = (i & k) == 0;  // best first
+        if (before(sm.key[j], sm.index[j], sm.key[i], sm.index[i]) == up) {
+          const unsigned long long kk = sm.key[i];
+          const int ii = sm.index[i];
+          const float ll = sm.logit[i];
+          sm.key[i] = sm.key[j];
+          sm.index[i] = sm.index[j];
+          sm.logit[i] = sm.logit[j];
+          sm.key[j] = kk;
+          sm.index[j] = ii;
+          sm.logit[j] = ll;
         }
       }
       __syncthreads();
     }
-    last = rs[0];
-    last_i = ri[0];
-    if (threadIdx.x == 0) {
-      const bool none = last == -INFINITY;
-      P.out_s[b * P.n + k] = static_cast<float>(last);
-      P.out_p[b * P.n + k] = none ? -1 : last_i / P.V;
-      P.out_t[b * P.n + k] = none ? -1 : last_i % P.V;
+  for (int i = threadIdx.x; i < most && i < L; i += kPickThreads) sm.order[i] = i;
+  __syncthreads();
+}
+
+// Appends this lane's entry if `take`; the whole warp calls it.
+__device__ __forceinline__ void append(Shared& sm, bool take, int index, float logit) {
+  const unsigned mask = __ballot_sync(0xFFFFFFFFu, take);
+  if (!mask) return;
+  int at = 0;
+  if (threadIdx.x % 32 == 0) at = atomicAdd(&sm.n_entries, __popc(mask));
+  at = __shfl_sync(0xFFFFFFFFu, at, 0) + __popc(mask & ((1u << (threadIdx.x % 32)) - 1u));
+  if (take && at < kCap) {
+    sm.index[at] = index;
+    sm.logit[at] = logit;
+  }
+}
+
+// f32 scores of logit l of row w may be off the exact ones by this much.
+__device__ __forceinline__ float margin(double eps, float add_max, float tau) {
+  return static_cast<float>(eps) + (add_max + fabsf(tau)) * 0x1p-22f;
+}
+
+// More candidates than the lists hold (many equal logits, rows in ascending
+// order): a pass over the tiles of the rows in index order that keeps the n
+// best so far.  Later equals lose their ties, so a full list only admits
+// strictly better entries.
+template <typename T>
+__device__ __noinline__ int ordered_pass(Shared& sm, const Params& P, int b, float thr) {
+  constexpr int E = Elem<T>::E, kTileVecs = 256;  // 4 groups; at most 2048 entries
+  constexpr int kTileGroups = kTileVecs / kGroupVecs;
+  const int tiles = (P.groups + kTileGroups - 1) / kTileGroups;
+  const long long all = static_cast<long long>(tiles) * P.W;
+  int have = 0;                  // entries kept
+  unsigned long long worst = 0;  // key of the n-th best once n are kept
+  if (threadIdx.x == 0) sm.n_entries = 0;
+  __syncthreads();
+  for (long long t0 = 0; t0 < all;) {
+    // the first tile at or after t0 that may hold better entries
+    if (threadIdx.x == 0) sm.next = kPickThreads;
+    __syncthreads();
+    const long long mine = t0 + threadIdx.x;
+    bool may = false;
+    if (mine < all) {
+      const int w = static_cast<int>(mine / tiles), tile = static_cast<int>(mine % tiles);
+      if (sm.ended[w]) {
+        may = tile == 0 && (have < P.n || f64_key(sm.cum[w]) > worst);
+      } else if (sm.add[w] > -INFINITY) {
+        const float* gm = P.gmax + (static_cast<long long>(b) * P.W + w) * P.groups;
+        float m = -INFINITY;
+        for (int g = tile * kTileGroups; g < min(P.groups, (tile + 1) * kTileGroups); ++g) m = fmaxf(m, gm[g]);
+        may = m > -INFINITY && m + sm.add[w] >= thr && (have < P.n || f64_key(score_of(sm, w, m)) > worst);
+      }
+    }
+    if (may) atomicMin(&sm.next, static_cast<int>(threadIdx.x));
+    __syncthreads();
+    const int found = sm.next;
+    __syncthreads();
+    if (found == kPickThreads) {
+      t0 += kPickThreads;
+      continue;
+    }
+    t0 += found;
+    const int w = static_cast<int>(t0 / tiles), tile = static_cast<int>(t0 % tiles);
+    ++t0;
+    if (sm.ended[w]) {
+      if (threadIdx.x < 32) append(sm, threadIdx.x == 0, w * P.V + P.eos, 0.f);
+    } else {
+      const Row<T> row(static_cast<const T*>(P.logits) + (static_cast<long long>(b) * P.W + w) * P.stride, P.V);
+      if (threadIdx.x < kTileVecs) {
+        const long long v = static_cast<long long>(tile) * kTileVecs + threadIdx.x;
+        float x[E];
+        Elem<T>::unpack(row.load(v), x);
+#pragma unroll
+        for (int i = 0; i < E; ++i)
+          append(sm, x[i] > -INFINITY && (have < P.n || f64_key(score_of(sm, w, x[i])) > worst),
+                 w * P.V + static_cast<int>(row.first(v) + i), x[i]);
+      }
     }
     __syncthreads();
+    const int L = sm.n_entries;
+    __syncthreads();
+    if (L == have) continue;
+    for (int i = have + threadIdx.x; i < L; i += kPickThreads) sm.key[i] = f64_key(score_of(sm, sm.index[i] / P.V, sm.logit[i]));
+    __syncthreads();
+    if (L >= P.n) {  // keep the n best, in order, at the front
+      sort_entries(sm, L, P.n);
+      unsigned long long k = 0;
+      int x = 0;
+      float l = 0.f;
+      if (threadIdx.x < P.n) {
+        const int i = sm.order[threadIdx.x];
+        k = sm.key[i];
+        x = sm.index[i];
+        l = sm.logit[i];
+      }
+      __syncthreads();
+      if (threadIdx.x < P.n) {
+        sm.key[threadIdx.x] = k;
+        sm.index[threadIdx.x] = x;
+        sm.logit[threadIdx.x] = l;
+      }
+      if (threadIdx.x == 0) sm.n_entries = P.n;
+      __syncthreads();
+      worst = sm.key[P.n - 1];
+      have = P.n;
+    } else {
+      have = L;
+    }
   }
-  if (threadIdx.x == 0) P.st[b] = bad ? SV_SEQ_BAD_VALUE : 0u;
+  return have;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kPickThreads) pick_kernel(const Params P) {
+  constexpr int E = Elem<T>::E;
+  extern __shared__ __align__(16) unsigned char raw[];
+  Shared& sm = *reinterpret_cast<Shared*>(raw);
+  const int b = blockIdx.x, tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const long long r0 = static_cast<long long>(b) * P.W;
+  if (tid < P.W) {
+    const float c = P.scores[r0 + tid];
+    sm.cum[tid] = c;
+    sm.ended[tid] = P.finished && P.finished[r0 + tid] && c > -INFINITY;
+    sm.precise[tid] = sm.again[tid] = 0;
+  }
+  if (tid == 0) sm.bad = sm.n_groups = sm.n_entries = sm.redo = 0;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  __syncthreads();
+
+  // the rows' logarithms
+  for (int w = warp; w < P.W; w += kPickWarps) {
+    const double c = sm.cum[w];
+    const bool live = !sm.ended[w] && !(P.finished && P.finished[r0 + w]) && c != -INFINITY;
+    float M = -INFINITY, s = 0.f;
+    if (live)
+      for (int i = lane; i < P.slices; i += 32) {
+        const float2 a = P.part[(r0 + w) * P.slices + i];
+        join(M, s, a.x, a.y);
+      }
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) {
+      const float M2 = __shfl_xor_sync(0xFFFFFFFFu, M, o), s2 = __shfl_xor_sync(0xFFFFFFFFu, s, o);
+      join(M, s, M2, s2);
+    }
+    if (lane == 0) {
+      if (isnan(c) || c == INFINITY || isnan(M) || M == INFINITY) sm.bad = 1;
+      sm.M[w] = M;
+      // log2 s = exponent + log2 of the significand
+      const int e = static_cast<int>(__float_as_uint(s) >> 23) - 127;
+      const float f = __uint_as_float((__float_as_uint(s) & 0x7FFFFFu) | 0x3F800000u);
+      sm.lse[w] = M > -INFINITY ? (static_cast<double>(base_of(M)) + e + static_cast<double>(log2f(f))) / static_cast<double>(kLog2e)
+                                : -INFINITY;
+      sm.again[w] = fabsf(M) > kLarge && M > -INFINITY;
+    }
+  }
+  __syncthreads();
+  if (sm.bad) {
+    for (int k = tid; k < P.n; k += kPickThreads) {
+      P.out_s[static_cast<long long>(b) * P.n + k] = -INFINITY;
+      P.out_p[static_cast<long long>(b) * P.n + k] = -1;
+      P.out_t[static_cast<long long>(b) * P.n + k] = -1;
+    }
+    if (tid == 0) P.st[b] = SV_SEQ_BAD_VALUE;
+    return;
+  }
+  for (int w = 0; w < P.W; ++w)
+    if (sm.again[w]) precise_lse<T>(sm, P, b, w);
+  if (tid < P.W) sm.add[tid] = !sm.ended[tid] && sm.M[tid] > -INFINITY ? static_cast<float>(sm.cum[tid] - sm.lse[tid]) : -INFINITY;
+  __syncthreads();
+  float add_max = 0.f;
+  for (int w = 0; w < P.W; ++w)
+    if (sm.add[w] > -INFINITY) add_max = fmaxf(add_max, fabsf(sm.add[w]));
+
+  // tau: units are runs of q groups of a row, at most kPerThread per thread
+  int q = 1;
+  while (static_cast<long long>((P.groups + q - 1) / q) * P.W > kPerThread * kPickThreads) ++q;
+  const int units = (P.groups + q - 1) / q, total = units * P.W;
+  unsigned key[kPerThread];
+  unsigned top = 0, low = 0xFFFFFFFFu;
+  const unsigned none = f32_key(-INFINITY);
+  int finite = 0;
+#pragma unroll
+  for (int i = 0; i < kPerThread; ++i) {
+    const int u = tid + i * kPickThreads;
+    key[i] = none;
+    if (u < total) {
+      const int w = u / units, u0 = u % units;
+      float x = -INFINITY;
+      if (sm.ended[w]) {
+        if (u0 == 0) x = static_cast<float>(sm.cum[w]);
+      } else if (sm.add[w] > -INFINITY) {
+        for (int g = u0 * q; g < min(P.groups, u0 * q + q); ++g) x = fmaxf(x, P.gmax[(r0 + w) * P.groups + g]);
+        x += sm.add[w];
+      }
+      key[i] = f32_key(x);
+    }
+    if (key[i] > none) {
+      ++finite;
+      top = max(top, key[i]);
+      low = min(low, key[i]);
+    }
+  }
+  top = __reduce_max_sync(0xFFFFFFFFu, top);
+  low = __reduce_min_sync(0xFFFFFFFFu, low);
+  if (lane == 0) {
+    sm.sum_hi[warp] = top;
+    sm.sum_lo[warp] = low;
+  }
+  int turn = 0;
+  const int all = block_sum(sm, finite, turn);
+  float thr = -INFINITY, tau = 0.f;
+  if (all >= P.n) {
+    for (int w = 0; w < kPickWarps; ++w) {
+      top = max(top, static_cast<unsigned>(sm.sum_hi[w]));
+      low = min(low, static_cast<unsigned>(sm.sum_lo[w]));
+    }
+    unsigned lo = low, hi = top + 1;  // at least n keys >= lo, fewer than n >= hi
+    int above = all;
+    while (hi - lo > 1 && above > 2 * P.n) {
+      const unsigned mid = lo + (hi - lo) / 2;
+      int c = 0;
+#pragma unroll
+      for (int i = 0; i < kPerThread; ++i) c += key[i] >= mid;
+      c = block_sum(sm, c, turn);
+      if (c >= P.n) {
+        lo = mid;
+        above = c;
+      } else {
+        hi = mid;
+      }
+    }
+    tau = key_f32(lo);
+    thr = tau - 2.f * margin(P.eps, add_max, tau);
+  }
+
+  // the groups that reach it, then their logits that do
+#pragma unroll
+  for (int i = 0; i < kPerThread; ++i) {
+    const float x = key_f32(key[i]);
+    if (key[i] > none && x >= thr) {
+      const int u = tid + i * kPickThreads, w = u / units, u0 = u % units;
+      if (sm.ended[w]) {
+        const int at = atomicAdd(&sm.n_entries, 1);
+        if (at < kCap) {
+          sm.index[at] = w * P.V + P.eos;
+          sm.logit[at] = 0.f;
+        }
+      } else {
+        for (int g = u0 * q; g < min(P.groups, u0 * q + q); ++g)
+          if (q == 1 || P.gmax[(r0 + w) * P.groups + g] + sm.add[w] >= thr) {
+            const int at = atomicAdd(&sm.n_groups, 1);
+            if (at < kGroupList) sm.group[at] = make_int2(w, g);
+          }
+      }
+    }
+  }
+  __syncthreads();
+  const int n_groups = sm.n_groups;
+  if (n_groups <= kGroupList) {
+    for (int j = warp; j < n_groups; j += kPickWarps) {
+      const int2 wg = sm.group[j];
+      const Row<T> row(static_cast<const T*>(P.logits) + (r0 + wg.x) * P.stride, P.V);
+      const long long v = static_cast<long long>(wg.y) * kGroupVecs + lane;
+      const uint4 qa = row.load(v), qb = row.load(v + 32);
+      const float add = sm.add[wg.x];
+      float x[E];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        Elem<T>::unpack(h ? qb : qa, x);
+#pragma unroll
+        for (int i = 0; i < E; ++i)
+          append(sm, x[i] > -INFINITY && x[i] + add >= thr, wg.x * P.V + static_cast<int>(row.first(v + 32 * h) + i), x[i]);
+      }
+    }
+  }
+  __syncthreads();
+  int L = sm.n_entries;
+  const bool overflow = L > kCap || n_groups > kGroupList;
+  if (overflow) {
+    // every row that may hold candidates, precisely; then the ordered pass
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i)
+      if (key[i] > none && key_f32(key[i]) >= thr) sm.again[(tid + i * kPickThreads) / units] = 1;
+    __syncthreads();
+    for (int w = 0; w < P.W; ++w)
+      if (sm.again[w] && !sm.ended[w] && !sm.precise[w]) precise_lse<T>(sm, P, b, w);
+    L = ordered_pass<T>(sm, P, b, thr);
+    for (int i = tid; i < L; i += kPickThreads) sm.key[i] = f64_key(score_of(sm, sm.index[i] / P.V, sm.logit[i]));
+    __syncthreads();
+    sort_entries(sm, L, P.n);
+  } else {
+    for (int i = tid; i < L; i += kPickThreads) sm.key[i] = f64_key(score_of(sm, sm.index[i] / P.V, sm.logit[i]));
+    __syncthreads();
+    sort_entries(sm, L, P.n);
+    // pairs of different beams that the logarithms' errors could swap: neighbours
+    // among the n best, and whatever lies as near to the last of them
+    auto flag = [&](int wi, int wj) {
+      if (!sm.precise[wi] && !sm.ended[wi]) sm.again[wi] = sm.redo = 1;
+      if (!sm.precise[wj] && !sm.ended[wj]) sm.again[wj] = sm.redo = 1;
+    };
+    if (tid + 1 < P.n && tid + 1 < L) {
+      const int i = sm.order[tid], j = sm.order[tid + 1], wi = sm.index[i] / P.V, wj = sm.index[j] / P.V;
+      if (wi != wj && key_f64(sm.key[i]) - key_f64(sm.key[j]) <= 2.0 * P.eps) flag(wi, wj);
+    }
+    if (L > P.n) {
+      const int last = sm.order[P.n - 1], wl = sm.index[last] / P.V;
+      const unsigned long long k_hi = f64_key(key_f64(sm.key[last]) + 2.0 * P.eps),
+                               k_lo = f64_key(key_f64(sm.key[last]) - 2.0 * P.eps);
+      for (int i = tid; i < L; i += kPickThreads)
+        if (sm.key[i] >= k_lo && sm.key[i] <= k_hi && sm.index[i] / P.V != wl) flag(sm.index[i] / P.V, wl);
+    }
+    __syncthreads();
+    if (sm.redo) {
+      for (int w = 0; w < P.W; ++w)
+        if (sm.again[w]) precise_lse<T>(sm, P, b, w);
+      for (int i = tid; i < L; i += kPickThreads) sm.key[i] = f64_key(score_of(sm, sm.index[i] / P.V, sm.logit[i]));
+      __syncthreads();
+      sort_entries(sm, L, P.n);
+    }
+  }
+  for (int k = tid; k < P.n; k += kPickThreads) {
+    float s = -INFINITY;
+    int p = -1, t = -1;
+    if (k < L) {
+      const int i = sm.order[k];
+      s = static_cast<float>(key_f64(sm.key[i]));
+      p = sm.index[i] / P.V;
+      t = sm.index[i] % P.V;
+    }
+    const long long o = static_cast<long long>(b) * P.n + k;
+    P.out_s[o] = s;
+    P.out_p[o] = p;
+    P.out_t[o] = t;
+  }
+  if (tid == 0) P.st[b] = 0u;
+}
+
+// Sizes of a call: groups of a row at the worst alignment, slices, workspace.
+struct Plan {
+  int groups, per_slice, slices;
+  size_t part_bytes, bytes;
+};
+
+Plan plan_of(int batch, int beams, int vocab, int elem) {
+  Plan p;
+  const long long E = 16 / elem;
+  const long long vecs = (vocab + 2 * (E - 1)) / E;  // ceil((E - 1 + vocab) / E)
+  p.groups = static_cast<int>((vecs + kGroupVecs - 1) / kGroupVecs);
+  const long long rows = static_cast<long long>(batch) * beams;
+  // groups per CTA: as many as leave four waves of five CTAs per SM, between
+  // two per warp (one load round) and sixteen
+  int per = 2 * kRowWarps;
+  while (per < 16 * kRowWarps && rows * ((p.groups + per - 1) / per) > 152 * 5 * 4) per *= 2;
+  p.per_slice = per;
+  p.slices = (p.groups + per - 1) / per;
+  p.part_bytes = (static_cast<size_t>(rows) * p.slices * sizeof(float2) + 15) / 16 * 16;
+  p.bytes = p.part_bytes + (static_cast<size_t>(rows) * p.groups * sizeof(float) + 15) / 16 * 16;
+  return p;
 }
 
 }  // namespace svs
@@ -160,7 +782,8 @@ extern "C" {
 
 size_t sv_beam_select_workspace_size(int32_t batch, int32_t beams, int32_t vocab, int32_t n) {
   if (batch < 0 || beams < 1 || beams > SV_BEAM_MAX_BEAMS || vocab < 1 || n < 1 || n > SV_BEAM_MAX_CANDIDATES) return 0;
-  return (static_cast<size_t>(batch) * beams * sizeof(double) + 15) / 16 * 16;
+  const svs::Plan a = svs::plan_of(batch, beams, vocab, 4), b = svs::plan_of(batch, beams, vocab, 2);
+  return a.bytes > b.bytes ? a.bytes : b.bytes;  // any dtype
 }
 
 sv_status sv_beam_select(const void* logits, sv_dtype dtype, int64_t row_stride, const float* scores,
@@ -193,20 +816,66 @@ sv_status sv_beam_select(const void* logits, sv_dtype dtype, int64_t row_stride,
     return svh::fail(SV_ERR_ARG, "workspace_bytes (%zu) < the %zu bytes sv_beam_select_workspace_size() asks for",
                      workspace_bytes, need);
   if (reinterpret_cast<uintptr_t>(workspace) % 16) return svh::fail(SV_ERR_ARG, "workspace must be 16-byte aligned");
-  svs::Params p{logits, row_stride, scores, finished, eos, batch, beams, vocab, n, static_cast<double*>(workspace),
-                out_scores, out_parents, out_tokens, status};
+  const svs::Plan plan = svs::plan_of(batch, beams, vocab, static_cast<int>(elem));
+  const long long ctas = static_cast<long long>(batch) * beams * plan.slices;
+  if (ctas > 0x7FFFFFFFLL) return svh::fail(SV_ERR_UNSUPPORTED, "batch * beams * vocab too large for one launch");
+  svs::Params p;
+  p.logits = logits;
+  p.stride = row_stride;
+  p.scores = scores;
+  p.finished = finished;
+  p.eos = eos;
+  p.B = batch;
+  p.W = beams;
+  p.V = vocab;
+  p.n = n;
+  p.groups = plan.groups;
+  p.slices = plan.slices;
+  p.per_slice = plan.per_slice;
+  int units = 64 + plan.slices / 32;
+  for (long long v = 131072; v < vocab; v *= 2) ++units;
+  p.eps = units / 16777216.0;
+  p.part = static_cast<float2*>(workspace);
+  p.gmax = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + plan.part_bytes);
+  p.out_s = out_scores;
+  p.out_p = out_parents;
+  p.out_t = out_tokens;
+  p.st = status;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  // the shared-memory opt-in, once per (device, element type)
+  static bool attr_set[64][3] = {};
   auto go = [&](void (*rows)(svs::Params), void (*pick)(svs::Params)) -> sv_status {
-    rows<<<static_cast<unsigned>(batch * beams), svs::kThreads, 0, st>>>(p);
-    pick<<<static_cast<unsigned>(batch), svs::kThreads, 0, st>>>(p);
-    const cudaError_t e = cudaGetLastError();
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 0;
+    if (!attr_set[dev][dtype]) {
+      const cudaError_t e = cudaFuncSetAttribute(pick, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 static_cast<int>(sizeof(svs::Shared)));
+      if (e != cudaSuccess) return svh::fail(SV_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+      attr_set[dev][dtype] = true;
+    }
+    rows<<<static_cast<unsigned>(ctas), svs::kRowThreads, 0, st>>>(p);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return svh::fail(SV_ERR_CUDA, "kernel launch: %s", cudaGetErrorString(e));
+    // the second kernel is set up while the first one's last CTAs run; it
+    // waits for them before it reads anything they wrote
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at = {};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(batch));
+    cfg.blockDim = dim3(svs::kPickThreads);
+    cfg.dynamicSmemBytes = sizeof(svs::Shared);
+    cfg.stream = st;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, pick, p);
     if (e != cudaSuccess) return svh::fail(SV_ERR_CUDA, "kernel launch: %s", cudaGetErrorString(e));
     return SV_OK;
   };
   switch (dtype) {
-    case SV_F32: return go(svs::row_kernel<float>, svs::pick_kernel<float>);
-    case SV_BF16: return go(svs::row_kernel<__nv_bfloat16>, svs::pick_kernel<__nv_bfloat16>);
-    default: return go(svs::row_kernel<__half>, svs::pick_kernel<__half>);
+    case SV_F32: return go(svs::rows_kernel<float>, svs::pick_kernel<float>);
+    case SV_BF16: return go(svs::rows_kernel<__nv_bfloat16>, svs::pick_kernel<__nv_bfloat16>);
+    default: return go(svs::rows_kernel<__half>, svs::pick_kernel<__half>);
   }
 }
 
