@@ -43,7 +43,8 @@ constexpr int kPickThreads = 512, kPickWarps = kPickThreads / 32;
 constexpr int kGroupVecs = 64;   // 16-byte vectors per group: two per lane of a warp
 constexpr int kCap = 4096;       // candidate entries a CTA holds (power of two)
 constexpr int kGroupList = 1024; // groups read again before the ordered pass takes over
-constexpr int kPerThread = 16;   // maxima per thread in the bisection
+constexpr int kUnits = 8192;     // maxima in the bisection
+constexpr int kAhead = 8;        // of a row's maxima, loads per lane in flight
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLarge = 1048576.f;  // |M| above this: the row's sum is taken precisely (l k - c would lose bits)
 
@@ -195,7 +196,7 @@ __device__ __forceinline__ void join(float& M, float& s, float M2, float s2) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kRowThreads) rows_kernel(const Params P) {
+__global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant__ Params P) {
   constexpr int E = Elem<T>::E;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const long long r = blockIdx.x / static_cast<unsigned>(P.slices);
@@ -263,12 +264,17 @@ struct Shared {
   unsigned long long table[33];  // 2^(j / 32), j = -16..16, units of 2^-61
   unsigned long long sum_hi[kPickWarps], sum_lo[kPickWarps];
   int cnt[2][kPickWarps];
-  int bad, n_groups, n_entries, redo, next;
+  int n_groups, n_entries, redo, next;
   int order[SV_BEAM_MAX_CANDIDATES];
+  int rank[kPickThreads];
+  union {
+    unsigned unit[kUnits];         // ordered bits of the units' best f32 scores (until the groups are listed)
+    unsigned long long key[kCap];  // ordered bits of the entries' scores
+  };
   int2 group[kGroupList];  // (row, group)
-  unsigned long long key[kCap];  // ordered bits of the score
-  int index[kCap];               // w V + v
+  int index[kCap];         // w V + v
   float logit[kCap];
+  unsigned char row[kCap];  // w
 };
 
 __device__ __forceinline__ unsigned f32_key(float x) {
@@ -378,15 +384,22 @@ __device__ __forceinline__ bool before(unsigned long long ka, int ia, unsigned l
 
 // order[0..min(L, most) - 1]: the entries' places, best first.
 __device__ __forceinline__ void sort_entries(Shared& sm, int L, int most) {
-  if (L <= kPickThreads) {  // by counting
-    const int i = threadIdx.x;
+  if (L <= kPickThreads) {  // by counting, each entry's rivals split over several threads
+    int lanes = 32;
+    while (lanes < L) lanes *= 2;
+    const int i = threadIdx.x & (lanes - 1), parts = kPickThreads / lanes, part = threadIdx.x / lanes;
+    sm.rank[threadIdx.x] = 0;
+    __syncthreads();
     if (i < L) {
       const unsigned long long k = sm.key[i];
       const int x = sm.index[i];
       int rank = 0;
-      for (int j = 0; j < L; ++j) rank += before(sm.key[j], sm.index[j], k, x);
-      if (rank < most) sm.order[rank] = i;
+#pragma unroll 2
+      for (int j = part; j < L; j += parts) rank += before(sm.key[j], sm.index[j], k, x);
+      if (rank) atomicAdd(&sm.rank[i], rank);
     }
+    __syncthreads();
+    if (threadIdx.x < L && sm.rank[threadIdx.x] < most) sm.order[sm.rank[threadIdx.x]] = threadIdx.x;
     __syncthreads();
     return;
   }
@@ -400,18 +413,21 @@ __device__ __forceinline__ void sort_entries(Shared& sm, int L, int most) {
   for (int k = 2; k <= size; k *= 2)
     for (int h = k / 2; h > 0; h /= 2) {
       for (int t = threadIdx.x; t < size / 2; t += kPickThreads) {
-        const int i = (t / h) * 2 * h + t % h, j = i + h;
+        const int i = (t & ~(h - 1)) * 2 + (t & (h - 1)), j = i + h;
         const bool up = (i & k) == 0;  // best first
         if (before(sm.key[j], sm.index[j], sm.key[i], sm.index[i]) == up) {
           const unsigned long long kk = sm.key[i];
           const int ii = sm.index[i];
           const float ll = sm.logit[i];
+          const unsigned char rr = sm.row[i];
           sm.key[i] = sm.key[j];
           sm.index[i] = sm.index[j];
           sm.logit[i] = sm.logit[j];
+          sm.row[i] = sm.row[j];
           sm.key[j] = kk;
           sm.index[j] = ii;
           sm.logit[j] = ll;
+          sm.row[j] = rr;
         }
       }
       __syncthreads();
@@ -420,17 +436,19 @@ __device__ __forceinline__ void sort_entries(Shared& sm, int L, int most) {
   __syncthreads();
 }
 
-// Appends this lane's entry if `take`; the whole warp calls it.
-__device__ __forceinline__ void append(Shared& sm, bool take, int index, float logit) {
-  const unsigned mask = __ballot_sync(0xFFFFFFFFu, take);
-  if (!mask) return;
-  int at = 0;
-  if (threadIdx.x % 32 == 0) at = atomicAdd(&sm.n_entries, __popc(mask));
-  at = __shfl_sync(0xFFFFFFFFu, at, 0) + __popc(mask & ((1u << (threadIdx.x % 32)) - 1u));
-  if (take && at < kCap) {
-    sm.index[at] = index;
+// Appends an entry; counts it even where the list is full.
+__device__ __forceinline__ void append(Shared& sm, int V, int w, int token, float logit) {
+  const int at = atomicAdd(&sm.n_entries, 1);
+  if (at < kCap) {
+    sm.index[at] = w * V + token;
+    sm.row[at] = static_cast<unsigned char>(w);
     sm.logit[at] = logit;
   }
+}
+
+__device__ __forceinline__ void score_entries(Shared& sm, int from, int L) {
+  for (int i = from + threadIdx.x; i < L; i += kPickThreads) sm.key[i] = f64_key(score_of(sm, sm.row[i], sm.logit[i]));
+  __syncthreads();
 }
 
 // f32 scores of logit l of row w may be off the exact ones by this much.
@@ -481,41 +499,41 @@ __device__ __noinline__ int ordered_pass(Shared& sm, const Params& P, int b, flo
     const int w = static_cast<int>(t0 / tiles), tile = static_cast<int>(t0 % tiles);
     ++t0;
     if (sm.ended[w]) {
-      if (threadIdx.x < 32) append(sm, threadIdx.x == 0, w * P.V + P.eos, 0.f);
-    } else {
+      if (threadIdx.x == 0) append(sm, P.V, w, P.eos, 0.f);
+    } else if (threadIdx.x < kTileVecs) {
       const Row<T> row(static_cast<const T*>(P.logits) + (static_cast<long long>(b) * P.W + w) * P.stride, P.V);
-      if (threadIdx.x < kTileVecs) {
-        const long long v = static_cast<long long>(tile) * kTileVecs + threadIdx.x;
-        float x[E];
-        Elem<T>::unpack(row.load(v), x);
+      const long long v = static_cast<long long>(tile) * kTileVecs + threadIdx.x;
+      float x[E];
+      Elem<T>::unpack(row.load(v), x);
 #pragma unroll
-        for (int i = 0; i < E; ++i)
-          append(sm, x[i] > -INFINITY && (have < P.n || f64_key(score_of(sm, w, x[i])) > worst),
-                 w * P.V + static_cast<int>(row.first(v) + i), x[i]);
-      }
+      for (int i = 0; i < E; ++i)
+        if (x[i] > -INFINITY && (have < P.n || f64_key(score_of(sm, w, x[i])) > worst))
+          append(sm, P.V, w, static_cast<int>(row.first(v) + i), x[i]);
     }
     __syncthreads();
     const int L = sm.n_entries;
     __syncthreads();
     if (L == have) continue;
-    for (int i = have + threadIdx.x; i < L; i += kPickThreads) sm.key[i] = f64_key(score_of(sm, sm.index[i] / P.V, sm.logit[i]));
-    __syncthreads();
+    score_entries(sm, have, L);
     if (L >= P.n) {  // keep the n best, in order, at the front
       sort_entries(sm, L, P.n);
       unsigned long long k = 0;
       int x = 0;
       float l = 0.f;
+      unsigned char w_of = 0;
       if (threadIdx.x < P.n) {
         const int i = sm.order[threadIdx.x];
         k = sm.key[i];
         x = sm.index[i];
         l = sm.logit[i];
+        w_of = sm.row[i];
       }
       __syncthreads();
       if (threadIdx.x < P.n) {
         sm.key[threadIdx.x] = k;
         sm.index[threadIdx.x] = x;
         sm.logit[threadIdx.x] = l;
+        sm.row[threadIdx.x] = w_of;
       }
       if (threadIdx.x == 0) sm.n_entries = P.n;
       __syncthreads();
@@ -528,51 +546,89 @@ __device__ __noinline__ int ordered_pass(Shared& sm, const Params& P, int b, flo
   return have;
 }
 
+// The kernel runs once through code that is new to its SM, on a handful of
+// values: what it takes is barriers, trips to L2 and instruction fetches.  So
+// a warp takes a row's maxima and sums together, in one round of loads; loops
+// stay rolled; and nothing divides.
 template <typename T>
-__global__ void __launch_bounds__(kPickThreads) pick_kernel(const Params P) {
+__global__ void __launch_bounds__(kPickThreads) pick_kernel(const __grid_constant__ Params P) {
   constexpr int E = Elem<T>::E;
   extern __shared__ __align__(16) unsigned char raw[];
   Shared& sm = *reinterpret_cast<Shared*>(raw);
   const int b = blockIdx.x, tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const long long r0 = static_cast<long long>(b) * P.W;
-  if (tid < P.W) {
-    const float c = P.scores[r0 + tid];
-    sm.cum[tid] = c;
-    sm.ended[tid] = P.finished && P.finished[r0 + tid] && c > -INFINITY;
-    sm.precise[tid] = sm.again[tid] = 0;
-  }
-  if (tid == 0) sm.bad = sm.n_groups = sm.n_entries = sm.redo = 0;
+  if (tid == 0) sm.n_groups = sm.n_entries = sm.redo = 0;
+  int q = 1;  // a unit of the bisection: q groups of a row
+  while (static_cast<long long>((P.groups + q - 1) / q) * P.W > kUnits) ++q;
+  const int units = q == 1 ? P.groups : (P.groups + q - 1) / q, total = units * P.W;
+  const unsigned none = f32_key(-INFINITY);
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  __syncthreads();
 
-  // the rows' logarithms
+  // the rows' logarithms, and the units' best scores
+  unsigned top = 0, low = 0xFFFFFFFFu;
+  int finite = 0;
+  bool bad = false, large = false;
+  float add_max = 0.f;
+  auto put = [&](int at, float x) {
+    const unsigned k = f32_key(x);
+    sm.unit[at] = k;
+    if (k > none) {
+      ++finite;
+      top = max(top, k);
+      low = min(low, k);
+    }
+  };
+  auto unit_max = [&](int w, int u) {
+    float x = -INFINITY;
+    for (int g = u * q; g < min(P.groups, u * q + q); ++g) x = fmaxf(x, P.gmax[(r0 + w) * P.groups + g]);
+    return x;
+  };
+#pragma unroll 1
   for (int w = warp; w < P.W; w += kPickWarps) {
-    const double c = sm.cum[w];
-    const bool live = !sm.ended[w] && !(P.finished && P.finished[r0 + w]) && c != -INFINITY;
-    float M = -INFINITY, s = 0.f;
+    const float c = P.scores[r0 + w];
+    const bool fin = P.finished && P.finished[r0 + w], live = !fin && c != -INFINITY, ended = fin && c > -INFINITY;
+    float M = -INFINITY, s = 0.f, m[kAhead];
+    const int ahead = q == 1 ? min(units, 32 * kAhead) : 0;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) m[i] = live && lane + 32 * i < ahead ? P.gmax[(r0 + w) * P.groups + lane + 32 * i] : -INFINITY;
     if (live)
       for (int i = lane; i < P.slices; i += 32) {
         const float2 a = P.part[(r0 + w) * P.slices + i];
         join(M, s, a.x, a.y);
       }
-#pragma unroll
+#pragma unroll 1
     for (int o = 16; o > 0; o /= 2) {
       const float M2 = __shfl_xor_sync(0xFFFFFFFFu, M, o), s2 = __shfl_xor_sync(0xFFFFFFFFu, s, o);
       join(M, s, M2, s2);
     }
+    float add = -INFINITY;
     if (lane == 0) {
-      if (isnan(c) || c == INFINITY || isnan(M) || M == INFINITY) sm.bad = 1;
-      sm.M[w] = M;
       // log2 s = exponent + log2 of the significand
       const int e = static_cast<int>(__float_as_uint(s) >> 23) - 127;
       const float f = __uint_as_float((__float_as_uint(s) & 0x7FFFFFu) | 0x3F800000u);
-      sm.lse[w] = M > -INFINITY ? (static_cast<double>(base_of(M)) + e + static_cast<double>(log2f(f))) / static_cast<double>(kLog2e)
-                                : -INFINITY;
-      sm.again[w] = fabsf(M) > kLarge && M > -INFINITY;
+      constexpr double kBack = 1.0 / static_cast<double>(kLog2e);
+      const double lse = (static_cast<double>(base_of(M) + static_cast<float>(e)) + static_cast<double>(log2f(f))) * kBack;
+      sm.cum[w] = c;
+      sm.lse[w] = lse;
+      sm.M[w] = M;
+      if (M > -INFINITY) add = static_cast<float>(static_cast<double>(c) - lse);
+      sm.add[w] = add;
+      sm.ended[w] = ended;
+      sm.precise[w] = 0;
+      sm.again[w] = M > -INFINITY && fabsf(M) > kLarge;
     }
+    bad |= isnan(c) || c == INFINITY || isnan(M) || M == INFINITY;
+    large |= M > -INFINITY && fabsf(M) > kLarge;
+    add = __shfl_sync(0xFFFFFFFFu, add, 0);
+    if (add > -INFINITY) add_max = fmaxf(add_max, fabsf(add));
+    if (ended && lane == 0) m[0] = c;
+    const float plus = ended ? 0.f : add;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (lane + 32 * i < ahead) put(w * units + lane + 32 * i, m[i] + plus);
+    for (int u = ahead + lane; u < units; u += 32) put(w * units + u, ended ? (u == 0 ? c : -INFINITY) : live ? unit_max(w, u) + plus : -INFINITY);
   }
-  __syncthreads();
-  if (sm.bad) {
+  if (__syncthreads_or(bad)) {
     for (int k = tid; k < P.n; k += kPickThreads) {
       P.out_s[static_cast<long long>(b) * P.n + k] = -INFINITY;
       P.out_p[static_cast<long long>(b) * P.n + k] = -1;
@@ -581,64 +637,50 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const Params P) {
     if (tid == 0) P.st[b] = SV_SEQ_BAD_VALUE;
     return;
   }
-  for (int w = 0; w < P.W; ++w)
-    if (sm.again[w]) precise_lse<T>(sm, P, b, w);
-  if (tid < P.W) sm.add[tid] = !sm.ended[tid] && sm.M[tid] > -INFINITY ? static_cast<float>(sm.cum[tid] - sm.lse[tid]) : -INFINITY;
-  __syncthreads();
-  float add_max = 0.f;
-  for (int w = 0; w < P.W; ++w)
-    if (sm.add[w] > -INFINITY) add_max = fmaxf(add_max, fabsf(sm.add[w]));
-
-  // tau: units are runs of q groups of a row, at most kPerThread per thread
-  int q = 1;
-  while (static_cast<long long>((P.groups + q - 1) / q) * P.W > kPerThread * kPickThreads) ++q;
-  const int units = (P.groups + q - 1) / q, total = units * P.W;
-  unsigned key[kPerThread];
-  unsigned top = 0, low = 0xFFFFFFFFu;
-  const unsigned none = f32_key(-INFINITY);
-  int finite = 0;
-#pragma unroll
-  for (int i = 0; i < kPerThread; ++i) {
-    const int u = tid + i * kPickThreads;
-    key[i] = none;
-    if (u < total) {
-      const int w = u / units, u0 = u % units;
-      float x = -INFINITY;
-      if (sm.ended[w]) {
-        if (u0 == 0) x = static_cast<float>(sm.cum[w]);
-      } else if (sm.add[w] > -INFINITY) {
-        for (int g = u0 * q; g < min(P.groups, u0 * q + q); ++g) x = fmaxf(x, P.gmax[(r0 + w) * P.groups + g]);
-        x += sm.add[w];
+  if (__syncthreads_or(large)) {  // rows whose fast sum says nothing: precisely, and their scores again
+    add_max = 0.f;
+    top = 0;
+    low = 0xFFFFFFFFu;
+    finite = 0;
+    for (int w = 0; w < P.W; ++w) {
+      if (sm.again[w]) {
+        precise_lse<T>(sm, P, b, w);
+        if (tid == 0) sm.add[w] = static_cast<float>(sm.cum[w] - sm.lse[w]);
+        __syncthreads();
       }
-      key[i] = f32_key(x);
-    }
-    if (key[i] > none) {
-      ++finite;
-      top = max(top, key[i]);
-      low = min(low, key[i]);
+      if (sm.add[w] > -INFINITY) add_max = fmaxf(add_max, fabsf(sm.add[w]));
+      for (int u = tid; u < units; u += kPickThreads)
+        put(w * units + u, sm.ended[w] ? (u == 0 ? static_cast<float>(sm.cum[w]) : -INFINITY)
+                                       : sm.add[w] > -INFINITY ? unit_max(w, u) + sm.add[w] : -INFINITY);
     }
   }
+
+  // tau: at least n units reach it, and hardly more than 2 n
   top = __reduce_max_sync(0xFFFFFFFFu, top);
   low = __reduce_min_sync(0xFFFFFFFFu, low);
+  add_max = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(add_max)));
   if (lane == 0) {
-    sm.sum_hi[warp] = top;
+    sm.sum_hi[warp] = static_cast<unsigned long long>(__float_as_uint(add_max)) << 32 | top;
     sm.sum_lo[warp] = low;
   }
   int turn = 0;
   const int all = block_sum(sm, finite, turn);
-  float thr = -INFINITY, tau = 0.f;
+#pragma unroll 1
+  for (int w = 0; w < kPickWarps; ++w) {
+    top = max(top, static_cast<unsigned>(sm.sum_hi[w]));
+    low = min(low, static_cast<unsigned>(sm.sum_lo[w]));
+    add_max = fmaxf(add_max, __uint_as_float(static_cast<unsigned>(sm.sum_hi[w] >> 32)));
+  }
+  float thr = -INFINITY;
   if (all >= P.n) {
-    for (int w = 0; w < kPickWarps; ++w) {
-      top = max(top, static_cast<unsigned>(sm.sum_hi[w]));
-      low = min(low, static_cast<unsigned>(sm.sum_lo[w]));
-    }
-    unsigned lo = low, hi = top + 1;  // at least n keys >= lo, fewer than n >= hi
+    unsigned lo = low, hi = top + 1;  // at least n units >= lo, fewer than n >= hi
     int above = all;
+#pragma unroll 1
     while (hi - lo > 1 && above > 2 * P.n) {
       const unsigned mid = lo + (hi - lo) / 2;
       int c = 0;
-#pragma unroll
-      for (int i = 0; i < kPerThread; ++i) c += key[i] >= mid;
+#pragma unroll 4
+      for (int i = tid; i < total; i += kPickThreads) c += sm.unit[i] >= mid;
       c = block_sum(sm, c, turn);
       if (c >= P.n) {
         lo = mid;
@@ -647,68 +689,58 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const Params P) {
         hi = mid;
       }
     }
-    tau = key_f32(lo);
+    const float tau = key_f32(lo);
     thr = tau - 2.f * margin(P.eps, add_max, tau);
   }
 
   // the groups that reach it, then their logits that do
-#pragma unroll
-  for (int i = 0; i < kPerThread; ++i) {
-    const float x = key_f32(key[i]);
-    if (key[i] > none && x >= thr) {
-      const int u = tid + i * kPickThreads, w = u / units, u0 = u % units;
+  const unsigned thr_key = max(f32_key(thr), none + 1);
+#pragma unroll 1
+  for (int i = tid; i < total; i += kPickThreads)
+    if (sm.unit[i] >= thr_key) {
+      const int w = i / units, u = i - w * units;
       if (sm.ended[w]) {
-        const int at = atomicAdd(&sm.n_entries, 1);
-        if (at < kCap) {
-          sm.index[at] = w * P.V + P.eos;
-          sm.logit[at] = 0.f;
-        }
+        append(sm, P.V, w, P.eos, 0.f);
       } else {
-        for (int g = u0 * q; g < min(P.groups, u0 * q + q); ++g)
+#pragma unroll 1
+        for (int g = u * q; g < min(P.groups, u * q + q); ++g)
           if (q == 1 || P.gmax[(r0 + w) * P.groups + g] + sm.add[w] >= thr) {
             const int at = atomicAdd(&sm.n_groups, 1);
             if (at < kGroupList) sm.group[at] = make_int2(w, g);
           }
       }
     }
-  }
   __syncthreads();
   const int n_groups = sm.n_groups;
   if (n_groups <= kGroupList) {
-    for (int j = warp; j < n_groups; j += kPickWarps) {
-      const int2 wg = sm.group[j];
+#pragma unroll 1
+    for (int j = 2 * warp; j < 2 * n_groups; j += j & 1 ? 2 * kPickWarps - 1 : 1) {  // half a group at a time
+      const int2 wg = sm.group[j / 2];
       const Row<T> row(static_cast<const T*>(P.logits) + (r0 + wg.x) * P.stride, P.V);
-      const long long v = static_cast<long long>(wg.y) * kGroupVecs + lane;
-      const uint4 qa = row.load(v), qb = row.load(v + 32);
+      const long long v = static_cast<long long>(wg.y) * kGroupVecs + 32 * (j & 1) + lane;
       const float add = sm.add[wg.x];
       float x[E];
+      Elem<T>::unpack(row.load(v), x);
+      const int e = static_cast<int>(row.first(v));
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        Elem<T>::unpack(h ? qb : qa, x);
-#pragma unroll
-        for (int i = 0; i < E; ++i)
-          append(sm, x[i] > -INFINITY && x[i] + add >= thr, wg.x * P.V + static_cast<int>(row.first(v + 32 * h) + i), x[i]);
-      }
+      for (int i = 0; i < E; ++i)
+        if (x[i] > -INFINITY && x[i] + add >= thr) append(sm, P.V, wg.x, e + i, x[i]);
     }
   }
   __syncthreads();
   int L = sm.n_entries;
-  const bool overflow = L > kCap || n_groups > kGroupList;
-  if (overflow) {
+  if (L > kCap || n_groups > kGroupList) {
     // every row that may hold candidates, precisely; then the ordered pass
-#pragma unroll
-    for (int i = 0; i < kPerThread; ++i)
-      if (key[i] > none && key_f32(key[i]) >= thr) sm.again[(tid + i * kPickThreads) / units] = 1;
+    for (int i = tid; i < total; i += kPickThreads)
+      if (sm.unit[i] >= thr_key) sm.again[i / units] = 1;
     __syncthreads();
     for (int w = 0; w < P.W; ++w)
       if (sm.again[w] && !sm.ended[w] && !sm.precise[w]) precise_lse<T>(sm, P, b, w);
     L = ordered_pass<T>(sm, P, b, thr);
-    for (int i = tid; i < L; i += kPickThreads) sm.key[i] = f64_key(score_of(sm, sm.index[i] / P.V, sm.logit[i]));
-    __syncthreads();
+    score_entries(sm, 0, L);
     sort_entries(sm, L, P.n);
   } else {
-    for (int i = tid; i < L; i += kPickThreads) sm.key[i] = f64_key(score_of(sm, sm.index[i] / P.V, sm.logit[i]));
-    __syncthreads();
+    score_entries(sm, 0, L);
     sort_entries(sm, L, P.n);
     // pairs of different beams that the logarithms' errors could swap: neighbours
     // among the n best, and whatever lies as near to the last of them
@@ -717,35 +749,35 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const Params P) {
       if (!sm.precise[wj] && !sm.ended[wj]) sm.again[wj] = sm.redo = 1;
     };
     if (tid + 1 < P.n && tid + 1 < L) {
-      const int i = sm.order[tid], j = sm.order[tid + 1], wi = sm.index[i] / P.V, wj = sm.index[j] / P.V;
+      const int i = sm.order[tid], j = sm.order[tid + 1], wi = sm.row[i], wj = sm.row[j];
       if (wi != wj && key_f64(sm.key[i]) - key_f64(sm.key[j]) <= 2.0 * P.eps) flag(wi, wj);
     }
     if (L > P.n) {
-      const int last = sm.order[P.n - 1], wl = sm.index[last] / P.V;
+      const int last = sm.order[P.n - 1], wl = sm.row[last];
       const unsigned long long k_hi = f64_key(key_f64(sm.key[last]) + 2.0 * P.eps),
                                k_lo = f64_key(key_f64(sm.key[last]) - 2.0 * P.eps);
+#pragma unroll 1
       for (int i = tid; i < L; i += kPickThreads)
-        if (sm.key[i] >= k_lo && sm.key[i] <= k_hi && sm.index[i] / P.V != wl) flag(sm.index[i] / P.V, wl);
+        if (sm.key[i] >= k_lo && sm.key[i] <= k_hi && sm.row[i] != wl) flag(sm.row[i], wl);
     }
     __syncthreads();
     if (sm.redo) {
       for (int w = 0; w < P.W; ++w)
         if (sm.again[w]) precise_lse<T>(sm, P, b, w);
-      for (int i = tid; i < L; i += kPickThreads) sm.key[i] = f64_key(score_of(sm, sm.index[i] / P.V, sm.logit[i]));
-      __syncthreads();
+      score_entries(sm, 0, L);
       sort_entries(sm, L, P.n);
     }
   }
-  for (int k = tid; k < P.n; k += kPickThreads) {
+  if (tid < P.n) {
     float s = -INFINITY;
     int p = -1, t = -1;
-    if (k < L) {
-      const int i = sm.order[k];
+    if (tid < L) {
+      const int i = sm.order[tid];
       s = static_cast<float>(key_f64(sm.key[i]));
-      p = sm.index[i] / P.V;
-      t = sm.index[i] % P.V;
+      p = sm.row[i];
+      t = sm.index[i] - p * P.V;
     }
-    const long long o = static_cast<long long>(b) * P.n + k;
+    const long long o = static_cast<long long>(b) * P.n + tid;
     P.out_s[o] = s;
     P.out_p[o] = p;
     P.out_t[o] = t;
