@@ -96,6 +96,24 @@ def ctypes_ptr(v):
     return None if v is None else int(v)
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _launch(dev: torch.device, fn, *args):
+    """``fn(*args, stream)`` on ``dev``'s current stream, the device made
+    current only where it is not (host time counts in the calls of a few
+    microseconds that this serves)."""
+    i = dev.index
+    if i == torch.cuda.current_device():
+        rc = fn(*args, _raw_stream(i))
+    else:
+        with torch.cuda.device(i):
+            rc = fn(*args, _raw_stream(i))
+    if rc != _lib.SV_OK:
+        _check(rc)
+
+
 def _p(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
@@ -420,14 +438,16 @@ def lm_head_logits(states: torch.Tensor, proj: Union[torch.Tensor, Q4Projection]
     if isinstance(proj, Q4Projection):
         head = _Head(proj, m)
         h = head.states(states, m)
+        rows, V = h.shape[0], head.V
         if out is None:
-            out = torch.empty(h.shape[0], (head.V + 3) // 4 * 4, dtype=torch.float32, device=m.device)[:, :head.V]
-        elif (out.device != m.device or out.dtype != torch.float32 or out.dim() != 2 or out.shape[0] < h.shape[0]
-              or out.shape[1] < head.V or out.stride(1) != 1):
+            out = torch.empty((rows, (V + 3) // 4 * 4), dtype=torch.float32, device=m.device)
+            if V % 4:  # rows start on 16-byte boundaries
+                out = out[:, :V]
+        elif (out.device != m.device or out.dtype != torch.float32 or out.dim() != 2 or out.shape[0] < rows
+              or out.shape[1] < V or out.stride(1) != 1):
             raise ValueError("out must be f32 [rows, >= V] on the states' device with unit stride along V")
-        with torch.cuda.device(m.device):
-            _check(head.lib.sv_lm_head_q4_logits(_p(h), _DTYPES[h.dtype], head.arg, h.shape[0], head.V, head.d,
-                                                 _p(out), out.stride(0), _p(err), m.stream()))
+        _launch(m.device, head.lib.sv_lm_head_q4_logits, h.data_ptr(), _DTYPES[h.dtype], head.arg, rows, V, head.d,
+                out.data_ptr(), max(out.stride(0), V), _p(err))
         return out.cpu() if m.host else out
     h = _bf16_rows(states, m)
     w = _bf16_rows(proj, m)
@@ -593,32 +613,36 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, n: Optional[int] = N
         raise ValueError("scores must be [B, W]")
     B, W = scores.shape
     m = _Marshal(logits)
+    dev = m.device
     rows = _rows(m.dev(logits))
-    if rows.dtype not in _DTYPES:
+    dtype = _DTYPES.get(rows.dtype)
+    if dtype is None:
         raise ValueError("logits must be float32, bfloat16 or float16")
-    if rows.shape[0] != B * W:
-        raise ValueError(f"logits must hold one row for each of the {B} x {W} scores (got {rows.shape[0]})")
+    R, V = rows.shape
+    if R != B * W:
+        raise ValueError(f"logits must hold one row for each of the {B} x {W} scores (got {R})")
     if finished is not None:
         if finished.shape != scores.shape:
             raise ValueError("finished must have the shape of scores")
-        finished = m.dev(finished if finished.dtype == torch.bool else finished != 0).contiguous().view(torch.uint8)
+        finished = m.dev(finished if finished.dtype == torch.bool else finished != 0).contiguous()
     c = m.dev(scores, torch.float32).contiguous()
-    V, n = rows.shape[1], W if n is None else int(n)
+    n = W if n is None else int(n)
     lib = _lib.load()
-    need = int(lib.sv_beam_select_workspace_size(B, W, V, n))
-    if workspace is None or workspace.numel() * workspace.element_size() < need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=m.device)
+    need = lib.sv_beam_select_workspace_size(B, W, V, n)
+    have = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    if have < need:
+        workspace, have = torch.empty(need, dtype=torch.uint8, device=dev), need
     shape = (B, max(n, 0))
-    out = torch.empty(shape, dtype=torch.float32, device=m.device)
-    par = torch.empty(shape, dtype=torch.int32, device=m.device)
-    tok = torch.empty(shape, dtype=torch.int32, device=m.device)
-    st = torch.empty(B, dtype=torch.int32, device=m.device)
-    with torch.cuda.device(m.device):
-        _check(lib.sv_beam_select(_p(rows), _DTYPES[rows.dtype], rows.stride(0) if B * W > 1 else max(rows.stride(0), V),
-                                  _p(c), _p(finished), int(eos), B, W, V, n, _p(out), _p(par), _p(tok), _p(st),
-                                  _p(workspace), workspace.numel() * workspace.element_size(), m.stream()))
-    res = BeamCandidates(out, par, tok, st)
-    return BeamCandidates(*(x.to("cpu") for x in res)) if m.host else res
+    out = torch.empty(shape, dtype=torch.float32, device=dev)
+    par = torch.empty(shape, dtype=torch.int32, device=dev)
+    tok = torch.empty(shape, dtype=torch.int32, device=dev)
+    st = torch.empty(B, dtype=torch.int32, device=dev)
+    _launch(dev, lib.sv_beam_select, rows.data_ptr(), dtype, max(rows.stride(0), V) if R < 2 else rows.stride(0),
+            c.data_ptr(), _p(finished), int(eos), B, W, V, n, out.data_ptr(), par.data_ptr(), tok.data_ptr(),
+            st.data_ptr(), _p(workspace), have)
+    if m.host:
+        return BeamCandidates(out.cpu(), par.cpu(), tok.cpu(), st.cpu())
+    return BeamCandidates(out, par, tok, st)
 
 
 def _flat_stride(t: torch.Tensor, lo: int, hi: int, what: str):
@@ -636,7 +660,11 @@ def _flat_stride(t: torch.Tensor, lo: int, hi: int, what: str):
     return size, 0 if stride is None else stride
 
 
-def _beam_state(t: torch.Tensor, time_dim: Optional[int]) -> "_lib.BeamState":
+def _beam_layout(t: torch.Tensor, time_dim: Optional[int]) -> tuple:
+    """The words of sv_beam_state after its pointer: four strides and sizes in
+    bytes, then (segs, tokens) and (timed, 0) as pairs of 32 bits."""
+    if any(n > 1 and s == 0 for n, s in zip(t.shape, t.stride())):
+        raise ValueError("a state is a broadcast view (modified in place)")
     e = t.element_size()
     if time_dim is None:
         span, k = 1, t.dim()  # the run of memory at the end of the shape, then segments of it
@@ -646,13 +674,12 @@ def _beam_state(t: torch.Tensor, time_dim: Optional[int]) -> "_lib.BeamState":
         if k == t.dim() and k > 2:
             raise ValueError("a state's last dimension must have unit stride (moved in place)")
         segs, seg = _flat_stride(t, 2, k, "a state's dimensions after [B, W]")
-        return _lib.BeamState(t.data_ptr(), t.stride(0) * e, t.stride(1) * e, seg * e, span * e, segs, 1, 0, 0)
+        return (t.stride(0) * e, t.stride(1) * e, seg * e, span * e, segs | 1 << 32, 0)
     segs, seg = _flat_stride(t, 2, time_dim, "a state's dimensions between the beams and the time")
     span, stride = _flat_stride(t, time_dim + 1, t.dim(), "a state's dimensions after the time")
     if (span > 1 and stride != 1) or (t.shape[time_dim] > 1 and t.stride(time_dim) != span):
         raise ValueError("a state's tokens must be contiguous: unit stride after the time, one after another along it")
-    return _lib.BeamState(t.data_ptr(), t.stride(0) * e, t.stride(1) * e, seg * e, span * e, segs,
-                          t.shape[time_dim], 1, 0)
+    return (t.stride(0) * e, t.stride(1) * e, seg * e, span * e, segs | t.shape[time_dim] << 32, 1)
 
 
 def beam_reorder(states: Union[torch.Tensor, Sequence[torch.Tensor]], parents: torch.Tensor,
@@ -676,29 +703,34 @@ def beam_reorder(states: Union[torch.Tensor, Sequence[torch.Tensor]], parents: t
     dev = states[0].device
     if dev.type != "cuda":
         raise ValueError("the states must be CUDA tensors (modified in place)")
-    if len({t.data_ptr() for t in states if t.numel()}) < sum(1 for t in states if t.numel()):
-        raise ValueError("a state is listed twice")
-    descs = (_lib.BeamState * len(states))()
-    for i, (t, td) in enumerate(zip(states, dims)):
-        if t.device != dev or t.dim() < 2 or tuple(t.shape[:2]) != (B, W):
-            raise ValueError(f"state {i} must be a CUDA tensor [{B}, {W}, ...] on {dev}")
+    words, layouts, seen = [], {}, set()
+    for t, td in zip(states, dims):
+        key = (t.shape, t.stride(), t.dtype, t.device, td)
+        layout = layouts.get(key)
+        if layout is None:  # a layer's states are alike: their layout is worked out once
+            if t.device != dev or t.dim() < 2 or t.shape[0] != B or t.shape[1] != W:
+                raise ValueError(f"a state must be a CUDA tensor [{B}, {W}, ...] on {dev} (got {list(t.shape)} on {t.device})")
+            d = td
+            if d is not None:
+                d = d + t.dim() if d < 0 else d
+                if not 2 <= d < t.dim():
+                    raise ValueError("time_dim must be a dimension after the beams")
+                if lengths is None:
+                    raise ValueError("time_dim needs lengths")
+            layout = layouts[key] = _beam_layout(t, d)
         if t.requires_grad and torch.is_grad_enabled():
-            raise ValueError(f"state {i} requires a gradient: it is modified in place")
-        if td is not None:
-            td = td + t.dim() if td < 0 else td
-            if not 2 <= td < t.dim():
-                raise ValueError(f"time_dim of state {i} must be a dimension after the beams")
-            if lengths is None:
-                raise ValueError("time_dim needs lengths")
-        if any(n > 1 and s == 0 for n, s in zip(t.shape, t.stride())):
-            raise ValueError(f"state {i} is a broadcast view (modified in place)")
-        descs[i] = _beam_state(t, td)
+            raise ValueError("a state requires a gradient: it is modified in place")
+        p = t.data_ptr()
+        if p in seen and p:
+            raise ValueError("a state is listed twice")
+        seen.add(p)
+        words.append(p)
+        words.extend(layout)
     if lengths is not None and lengths.numel() != B:
         raise ValueError("lengths must be [B]")
-    p = parents.to(device=dev, dtype=torch.int32).contiguous()
+    par = parents.to(device=dev, dtype=torch.int32).contiguous()
     ln = None if lengths is None else lengths.reshape(-1).to(device=dev, dtype=torch.int32).contiguous()
     st = torch.empty(B, dtype=torch.int32, device=dev)
-    with torch.cuda.device(dev):
-        _check(_lib.load().sv_beam_reorder(descs, len(states), _p(p), _p(ln), B, W, _p(st),
-                                           torch.cuda.current_stream(dev).cuda_stream))
+    descs = ctypes.cast((ctypes.c_int64 * len(words))(*words), ctypes.POINTER(_lib.BeamState))
+    _launch(dev, _lib.load().sv_beam_reorder, descs, len(states), par.data_ptr(), _p(ln), B, W, st.data_ptr())
     return st

@@ -162,7 +162,13 @@ def test_binding_refusals():
 
 def test_state_descriptions():
     """Strides of the layouts a cache may have, and those that cannot move in place."""
-    from speculative_decoding_verification_decode_gb300.api import _beam_state
+    from speculative_decoding_verification_decode_gb300.api import _beam_layout
+
+    def _beam_state(t, td):
+        words = (t.data_ptr(), *_beam_layout(t, td))
+        return ctypes.cast((ctypes.c_int64 * 7)(*words), ctypes.POINTER(_lib.BeamState))[0]
+
+    assert ctypes.sizeof(_lib.BeamState) == 56
     t = torch.zeros(2, 3, 4, 10, 16, dtype=torch.bfloat16)  # heads before time
     d = _beam_state(t, 3)
     assert (d.segs, d.tokens, d.token_bytes, d.seg_stride, d.beam_stride, d.timed) == (4, 10, 32, 320, 1280, 1)
@@ -176,6 +182,8 @@ def test_state_descriptions():
     assert (d.segs, d.token_bytes, d.seg_stride) == (40, 10, 32)
     d = _beam_state(torch.zeros(2, 3, dtype=torch.int32), None)  # one value per beam
     assert (d.segs, d.tokens, d.token_bytes) == (1, 1, 4)
+    with pytest.raises(ValueError, match="broadcast"):
+        _beam_state(t[:, :1].expand(2, 3, 4, 10, 16), None)
     for bad, td in ((t.transpose(3, 4), 4), (t[..., ::2], None), (t[:, :, ::1, :, ::2], 3), (t[:, :, :, :7], 2)):
         with pytest.raises(ValueError):
             _beam_state(bad, td)
