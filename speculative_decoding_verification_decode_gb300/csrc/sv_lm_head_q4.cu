@@ -1,494 +1,12 @@
-// The LM head with a projection in 4 bits (include/sv_lm_head_q4.h).
-//
-// Logits = H W^T with W[v][k] = s[v][k / g] (q[v][k] - z[v][k / g]).
-//
-// The projection's bytes bound the product up to some tens of rows: every
-// weight is read once for up to 64 rows of states, and what has to be kept
-// up with that stream is turning 4-bit codes into operands.  So:
-//   - the weights are the A operand (128 vocabulary rows of an MMA), the
-//     states the B operand (N rows).  A thread owns a vocabulary row: it takes
-//     the row's codes from shared memory (TMA, 128-byte swizzle), makes the
-//     integers q - z in 16 bits (exact), and stores them as its lane of tensor
-//     memory, from where the MMA reads them: no round trip through shared
-//     memory.
-//   - one MMA chain per group; its f32 result, N columns of the thread's lane,
-//     is read back and added to the thread's N f32 sums times the group's
-//     scale.  No weight is rounded, and a scale is one register.
-//   - operands and results go through a ring of buffers in tensor memory, so
-//     the tensor cores work on some groups while the warps turn the next and
-//     add the last.  A warp passes its turn with a single arrival: by then it
-//     has read the result that the MMA will overwrite.
-//   - two warpgroups share the rows: each turns half of a group's codes and
-//     keeps half of the N sums, so an SM has sixteen warps to hide the steps'
-//     latencies with.  Turning is 1.1 ALU operations per weight, 0.8 of the
-//     memory's rate on this machine, and nothing else may wait in its way:
-//     scales come by cp.async from a warp of their own.
-// A CTA has H halves of 128 rows (8 warps each), H scale warps, a producer
-// and an MMA warp.  Its tiles have R <= 128 H rows, R chosen so that the
-// vocabulary divides evenly over the CTAs (the MMA's idle rows cost nothing).
-//
-// Every wait is bounded; one that gives up sets bit 0 of *err.
-#include <cuda.h>
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-#include <cuda_runtime.h>
-#include <cudaTypedefs.h>
-
-#include <cstdint>
-
+// Host side of the LM head on a projection in 4 bits
+// (include/sv_lm_head_q4.h); the kernel is in sv_lm_head_q4.cuh.
 #include "../../include/sv_lm_head.h"
-#include "../../include/sv_lm_head_q4.h"
-#include "sv_host.h"
-#include "sv_ptx.cuh"
+#include "sv_lm_head_q4.cuh"
 
 namespace svq {
 
-using svk::mbar_arrive_expect_tx;
-using svk::mbar_arrive_local;
-using svk::mbar_init;
-using svk::smem_u32;
-
-constexpr int kStageK = 256;    // weights of a row per ring stage: 128 bytes
-constexpr int kMaxStages = 6;
-constexpr int kHalfCols = 256;  // tensor-memory columns of a half: `ring` operands of group / 2 columns and results of N
-constexpr int kMaxRing = 4;
-
-struct Args {
-  const void* scales;
-  const unsigned char* zeros;
-  float* out0;
-  float* out1;
-  unsigned* err;
-  long long ld;
-  int scale_dtype, group, G;  // G scales per row
-  int rows0, rows1, split;    // virtual rows: rows0 from 0, rows1 from `split` (a multiple of 8)
-  int blocks;                 // row blocks of N
-  int V, d, R, tiles, nk, stages;
-  int ring;                   // operand / result buffers
-  int s_words, z_words;       // 32-bit words of a row's scales and zeros in a stage (odd: no bank conflicts)
-};
-
-struct __align__(8) Bars {
-  uint64_t full[kMaxStages];   // producer and scale warps -> all: the stage landed
-  uint64_t empty[kMaxStages];  // warps (codes read) and MMA (states read) -> producer
-  uint64_t a_full[2][kMaxRing];  // [half][buffer] warps -> MMA: operand written, result buffer free
-  uint64_t d_full[2][kMaxRing];  // MMA -> warps: result ready, operand buffer free
-  uint64_t done;               // every MMA has completed
-  uint32_t tmem;
-  volatile int abort;
-};
-
-__device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
-  d |= static_cast<uint64_t>(1u) << 16;
-  d |= static_cast<uint64_t>(1024u >> 4) << 32;
-  d |= static_cast<uint64_t>(1u) << 46;
-  d |= static_cast<uint64_t>(2u) << 61;
-  return d;
-}
-
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-      "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
-      : "memory");
-}
-
-// D (tensor memory) (+)= A (tensor memory) x B (shared memory), K = 16.
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
-      "r"(a), "l"(bdesc), "r"(idesc), "r"(acc)
-      : "memory");
-}
-
-__device__ __forceinline__ void mma_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-               : "memory");
-}
-
-// Consecutive columns of this thread's lane.
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-      "%15, %16};" ::"r"(taddr),
-      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-      : "memory");
-}
-
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(v[0]),
-               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-               : "memory");
-}
-
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* v) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
-               : "r"(taddr));
-}
-
-__device__ __forceinline__ void give_up(Bars& bars, unsigned* err) {
-  bars.abort = 1;
-  if (err) atomicOr(err, 1u);
-}
-
-// A bounded wait that also gives up once another role has.
-__device__ __forceinline__ bool wait_or_abort(Bars& bars, uint64_t* bar, uint32_t parity, unsigned* err) {
-  for (uint32_t i = 0; i < svk::kWaitPolls; ++i) {
-    if (svk::mbar_try_wait(bar, parity)) return true;
-    if (bars.abort) return false;
-  }
-  give_up(bars, err);
-  return false;
-}
-
-// Two codes as 16-bit integers in a word: base + code, where base is a power
-// of two whose unit in the last place is 1, then minus (base + zero), exact.
-template <typename T>
-struct Code;
-template <>
-struct Code<__nv_bfloat16> {
-  static constexpr uint32_t kBase = 0x43004300u;  // 128
-  static __device__ uint32_t sub(uint32_t a, uint32_t z) {
-    const __nv_bfloat162 r = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&z));
-    return *reinterpret_cast<const uint32_t*>(&r);
-  }
-};
-template <>
-struct Code<__half> {
-  static constexpr uint32_t kBase = 0x64006400u;  // 1024
-  static __device__ uint32_t sub(uint32_t a, uint32_t z) {
-    const __half2 r = __hsub2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&z));
-    return *reinterpret_cast<const uint32_t*>(&r);
-  }
-};
-
-// Eight codes of a word to four words of two, in order.
-template <typename T>
-__device__ __forceinline__ void turn(uint32_t w, uint32_t z, uint32_t* a) {
-  const uint32_t odd = w >> 4;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint32_t both = __byte_perm(w, odd, j | j << 4 | (4 + j) << 8 | (4 + j) << 12);
-    a[j] = Code<T>::sub((both & 0x000F000Fu) | Code<T>::kBase, z);
-  }
-}
-
-// One 32-bit word to shared memory; its arrival is counted by the barrier that
-// cp_async_arrive names.
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
-
-template <typename T, int N, int H>
-__global__ void __launch_bounds__(288 * H + 64, H == 1 ? 2 : 1)
-    q4_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap h0,
-              const __grid_constant__ CUtensorMap h1, const __grid_constant__ Args g) {
-  constexpr int kWarps = 8 * H;  // that turn codes
-  constexpr int kHelp = H;       // that fetch scales
-  constexpr bool kBf16 = Code<T>::kBase == 0x43004300u;
-  // instruction descriptor: D f32, A and B bf16 / f16, both K-major, N / 8, M / 16
-  constexpr uint32_t kIdesc = (1u << 4) | (kBf16 ? (1u << 7) | (1u << 10) : 0u) | ((uint32_t(N) >> 3) << 17) |
-                              ((128u >> 4) << 24);
-  extern __shared__ __align__(1024) unsigned char smem_raw[];
-  unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                                         ~static_cast<uintptr_t>(1023));
-  const int w_bytes = g.R * 128, stage_bytes = w_bytes + N * kStageK * 2;
-  uint32_t* sbuf = reinterpret_cast<uint32_t*>(smem + g.stages * stage_bytes);  // [stage][128 H][s_words]
-  uint32_t* zbuf = sbuf + g.stages * 128 * H * g.s_words;                       // [stage][128 H][z_words]
-  Bars& bars = *reinterpret_cast<Bars*>(zbuf + g.stages * 128 * H * g.z_words);
-  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < g.stages; ++s) {
-      mbar_init(&bars.full[s], 1 + 32 * kHelp);
-      mbar_init(&bars.empty[s], kWarps + 1);
-    }
-    for (int h = 0; h < 2; ++h)
-      for (int i = 0; i < kMaxRing; ++i) {
-        mbar_init(&bars.a_full[h][i], 8);
-        mbar_init(&bars.d_full[h][i], 1);
-      }
-    mbar_init(&bars.done, 1);
-    bars.abort = 0;
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-  }
-  if (warp == kWarps + kHelp + 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&bars.tmem)),
-                 "r"(H * kHalfCols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-  }
-  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-  __syncthreads();
-  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-  const uint32_t tmem = bars.tmem;
-  const int steps = (g.d + g.group - 1) / g.group;  // groups of a row
-  const int per_stage = kStageK / g.group;
-  const int a_cols = g.group / 2, d_at = g.ring * a_cols;  // a half's columns: operands, then results
-
-  if (warp == kWarps + kHelp) {
-    // ---- producer: one thread
-    if (lane == 0) {
-      int gk = 0, s = 0, use = 0;  // stages issued, slot, times round
-      for (int t = blockIdx.x; t < g.tiles && !bars.abort; t += gridDim.x)
-        for (int blk = 0; blk < g.blocks && !bars.abort; ++blk)
-          for (int ks = 0; ks < g.nk; ++ks, ++gk) {
-            if (use > 0 && !wait_or_abort(bars, &bars.empty[s], (use - 1) & 1, g.err)) break;
-            const uint32_t dst = smem_u32(smem + s * stage_bytes);
-            mbar_arrive_expect_tx(&bars.full[s], stage_bytes);
-            tma_load_2d(dst, &wmap, ks * 128, t * g.R, &bars.full[s]);
-            for (int r = 0; r < N; r += 8) {  // 8 rows of one of the two row sets
-              const int v = blk * N + r;
-              const bool second = v >= g.split;
-              for (int c = 0; c < kStageK / 64; ++c)
-                tma_load_2d(dst + w_bytes + c * N * 128 + r * 128, second ? &h1 : &h0, ks * kStageK + c * 64,
-                            second ? v - g.split : v, &bars.full[s]);
-            }
-            if (++s == g.stages) {
-              s = 0;
-              ++use;
-            }
-          }
-      // no copy may still be writing shared memory at exit; once a role has
-      // given up, a stage may lack the scale warps' arrivals for good
-      for (int k = gk - g.stages > 0 ? gk - g.stages : 0; k < gk; ++k)
-        if (!svk::mbar_wait_bounded(&bars.full[k % g.stages], (k / g.stages) & 1)) give_up(bars, g.err);
-    }
-  } else if (warp >= kWarps && warp < kWarps + kHelp) {
-    // ---- scales (and zeros) of 128 rows, as the 32-bit words that hold them:
-    // lanes take neighbouring words of a row
-    const int base_row = (warp - kWarps) * 128;
-    const int elem = g.scale_dtype == SV_F32 ? 4 : 2;
-    const int sw = 31 - __clz(per_stage);            // log2 of the words looked at per row: per_stage covers both types
-    const int zw = per_stage == 8 ? 2 : 1;
-    int s = 0, use = 0;
-    bool ok = true;
-    for (int t = blockIdx.x; ok && t < g.tiles; t += gridDim.x) {
-      const int v0 = t * g.R + base_row;
-      const int rows = min(min(128, g.R - base_row), g.V - v0);
-      for (int blk = 0; ok && blk < g.blocks; ++blk)
-        for (int ks = 0; ok && ks < g.nk; ++ks) {
-          if (use > 0) ok = __all_sync(0xFFFFFFFFu, wait_or_abort(bars, &bars.empty[s], (use - 1) & 1, g.err));
-          if (!ok) break;
-          const int j0 = ks * per_stage, n = min(per_stage, g.G - j0);
-          uint32_t* sd = sbuf + (s * 128 * H + base_row) * g.s_words;
-          for (int e = lane; e < rows << sw; e += 32) {
-            const int r = e >> sw, k = e & ((1 << sw) - 1);
-            const uintptr_t at = reinterpret_cast<uintptr_t>(g.scales) + (static_cast<long long>(v0 + r) * g.G + j0) * elem;
-            const uintptr_t word = (at & ~static_cast<uintptr_t>(3)) + 4 * k;
-            if (word < at + n * elem) cp_async4(smem_u32(sd + r * g.s_words + k), reinterpret_cast<const void*>(word));
-          }
-          if (g.zeros) {
-            uint32_t* zd = zbuf + (s * 128 * H + base_row) * g.z_words;
-            for (int e = lane; e < rows << zw; e += 32) {
-              const int r = e >> zw, k = e & ((1 << zw) - 1);
-              const uintptr_t at = reinterpret_cast<uintptr_t>(g.zeros) + static_cast<long long>(v0 + r) * g.G + j0;
-              const uintptr_t word = (at & ~static_cast<uintptr_t>(3)) + 4 * k;
-              if (word < at + n) cp_async4(smem_u32(zd + r * g.z_words + k), reinterpret_cast<const void*>(word));
-            }
-          }
-          cp_async_arrive(&bars.full[s]);
-          if (++s == g.stages) {
-            s = 0;
-            ++use;
-          }
-        }
-    }
-    asm volatile("cp.async.wait_all;" ::: "memory");
-  } else if (warp == kWarps + kHelp + 1) {
-    // ---- MMA: one thread issues
-    if (lane == 0) {
-      int s = 0, use = 0, buf = 0, turn_no = 0;
-      bool ok = true;
-      for (int t = blockIdx.x; ok && t < g.tiles; t += gridDim.x)
-        for (int blk = 0; ok && blk < g.blocks; ++blk)
-          for (int ks = 0; ok && ks < g.nk; ++ks) {
-            ok = wait_or_abort(bars, &bars.full[s], use & 1, g.err);
-            const uint32_t b0 = smem_u32(smem + s * stage_bytes) + w_bytes;
-            for (int i = 0; ok && i < per_stage && ks * per_stage + i < steps; ++i) {
-              for (int h = 0; h < H; ++h) {
-                ok = wait_or_abort(bars, &bars.a_full[h][buf], turn_no & 1, g.err);
-                if (!ok) break;
-                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                const uint32_t a = tmem + h * kHalfCols + buf * a_cols, dd = tmem + h * kHalfCols + d_at + buf * N;
-                for (int kk = 0; kk < g.group / 16; ++kk) {
-                  const int k = i * g.group + kk * 16;
-                  mma_ts(dd, a + kk * 8, desc_sw128(b0 + (k / 64) * N * 128 + (k % 64) * 2), kIdesc, kk ? 1u : 0u);
-                }
-                mma_commit(&bars.d_full[h][buf]);
-              }
-              if (++buf == g.ring) {
-                buf = 0;
-                ++turn_no;
-              }
-            }
-            if (ok) mma_commit(&bars.empty[s]);
-            if (++s == g.stages) {
-              s = 0;
-              ++use;
-            }
-          }
-      mma_commit(&bars.done);
-      if (!svk::mbar_wait_bounded(&bars.done, 0)) give_up(bars, g.err);
-    }
-  } else {
-    // ---- a thread per vocabulary row and warpgroup
-    const int half = warp / 8, wg = warp / 4 % 2;
-    const int in_tile = half * 128 + warp % 4 * 32 + lane;
-    const int row = min(in_tile, g.R - 1);  // rows past the tile repeat its last one, unused
-    const uint32_t ta = tmem + half * kHalfCols + (static_cast<uint32_t>(warp % 4 * 32) << 16) + wg * (a_cols / 2);
-    const uint32_t td = tmem + half * kHalfCols + (static_cast<uint32_t>(warp % 4 * 32) << 16) + d_at + wg * (N / 2);
-    const int lag = g.ring - 1;  // results are added this many groups later
-    int s = 0, use = 0, buf = 0, turn_no = 0;
-    bool ok = true;
-    for (int t = blockIdx.x; ok && t < g.tiles; t += gridDim.x) {
-      const long long v = static_cast<long long>(t) * g.R + in_tile;
-      // where the row's scales and zeros begin in their first words
-      const long long first = (static_cast<long long>(t) * g.R + row) * g.G;
-      const int s_off = g.scale_dtype == SV_F32 ? 0 : static_cast<int>((reinterpret_cast<uintptr_t>(g.scales) / 2 + first) & 1);
-      const int z_off = static_cast<int>((reinterpret_cast<uintptr_t>(g.zeros) + first) & 3);
-      for (int blk = 0; ok && blk < g.blocks; ++blk) {
-        float acc[N / 2];
-#pragma unroll
-        for (int n = 0; n < N / 2; ++n) acc[n] = 0.f;
-        float sc[kMaxRing - 1] = {};  // scales of the groups whose results are still to be added, newest first
-        int pending = 0, rbuf = buf, rturn = turn_no;
-        auto add_oldest = [&]() {
-          const float scale = pending == 1 ? sc[0] : pending == 2 ? sc[1] : sc[2];
-          if (!__all_sync(0xFFFFFFFFu, wait_or_abort(bars, &bars.d_full[half][rbuf], rturn & 1, g.err))) return false;
-          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-          uint32_t d[N / 2];
-#pragma unroll
-          for (int n = 0; n < N / 2; n += 8) tmem_ld8(td + rbuf * N + n, d + n);
-          asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-          for (int n = 0; n < N / 2; ++n) acc[n] = fmaf(scale, __uint_as_float(d[n]), acc[n]);
-          --pending;
-          if (++rbuf == g.ring) {
-            rbuf = 0;
-            ++rturn;
-          }
-          return true;
-        };
-        for (int ks = 0; ok && ks < g.nk; ++ks) {
-          ok = __all_sync(0xFFFFFFFFu, wait_or_abort(bars, &bars.full[s], use & 1, g.err));
-          const unsigned char* codes = smem + s * stage_bytes + row * 128;
-          const uint32_t* srow = sbuf + (s * 128 * H + row) * g.s_words;
-          const unsigned char* zrow = reinterpret_cast<const unsigned char*>(zbuf + (s * 128 * H + row) * g.z_words) +
-                                      ((z_off + ks * per_stage) & 3);
-          for (int i = 0; ok && i < per_stage && ks * per_stage + i < steps; ++i) {
-            const uint32_t z0 = g.zeros ? zrow[i] & 15u : 8u;
-            const uint32_t z = (z0 | z0 << 16) + Code<T>::kBase;
-            const uint32_t dst = ta + buf * a_cols;
-            if (a_cols == 64) {
-#pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                const uint4 q = *reinterpret_cast<const uint4*>(codes + (((4 * i + 2 * wg + c) ^ (row & 7)) << 4));
-                uint32_t a[16];
-                turn<T>(q.x, z, a);
-                turn<T>(q.y, z, a + 4);
-                turn<T>(q.z, z, a + 8);
-                turn<T>(q.w, z, a + 12);
-                tmem_st16(dst + c * 16, a);
-              }
-            } else if (a_cols == 32) {
-              const uint4 q = *reinterpret_cast<const uint4*>(codes + (((2 * i + wg) ^ (row & 7)) << 4));
-              uint32_t a[16];
-              turn<T>(q.x, z, a);
-              turn<T>(q.y, z, a + 4);
-              turn<T>(q.z, z, a + 8);
-              turn<T>(q.w, z, a + 12);
-              tmem_st16(dst, a);
-            } else {
-              const uint2 q = *reinterpret_cast<const uint2*>(codes + ((i ^ (row & 7)) << 4) + wg * 8);
-              uint32_t a[8];
-              turn<T>(q.x, z, a);
-              turn<T>(q.y, z, a + 4);
-              tmem_st8(dst, a);
-            }
-            float scale;
-            if (g.scale_dtype == SV_F32)
-              scale = __uint_as_float(srow[i]);
-            else if (g.scale_dtype == SV_BF16)
-              scale = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(srow)[s_off + i]);
-            else
-              scale = __half2float(reinterpret_cast<const __half*>(srow)[s_off + i]);
-            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-            asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-            __syncwarp();
-            if (lane == 0) {
-              mbar_arrive_local(&bars.a_full[half][buf]);
-              if (i + 1 == per_stage || ks * per_stage + i + 1 == steps) mbar_arrive_local(&bars.empty[s]);
-            }
-            if (++buf == g.ring) {
-              buf = 0;
-              ++turn_no;
-            }
-            if (pending == lag) ok = add_oldest();
-            sc[2] = sc[1];
-            sc[1] = sc[0];
-            sc[0] = scale;
-            ++pending;
-          }
-          if (++s == g.stages) {
-            s = 0;
-            ++use;
-          }
-        }
-        while (ok && pending > 0) ok = add_oldest();
-        if (ok && in_tile < g.R && v < g.V) {
-#pragma unroll
-          for (int n = 0; n < N / 2; ++n) {
-            const int r = blk * N + wg * (N / 2) + n;
-            float* out = r >= g.split ? (r - g.split < g.rows1 ? g.out1 + (r - g.split) * g.ld : nullptr)
-                                      : (r < g.rows0 ? g.out0 + r * g.ld : nullptr);
-            if (out) out[v] = acc[n];
-          }
-        }
-      }
-    }
-  }
-  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-  __syncthreads();
-  if (warp == kWarps + kHelp + 1) {
-    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(H * kHalfCols) : "memory");
-  }
-}
-
-PFN_cuTensorMapEncodeTiled_v12000 encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  if (!fn) {
-    cudaDriverEntryPointQueryResult q;
-    void* p = nullptr;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  }
-  return fn;
-}
-
-// A row-major matrix in boxes of 128 bytes x box_rows, 128-byte swizzle;
-// what lies outside reads 0.
-bool encode(CUtensorMap* map, CUtensorMapDataType type, int elem, const void* base, long long rows, long long cols,
-            int box_rows) {
-  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * elem};
-  const cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / elem), static_cast<cuuint32_t>(box_rows)};
-  const cuuint32_t es[2] = {1, 1};
-  return encoder()(map, type, 2, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
+sv_status start_bf16(const Args& g, int n, const sv_q4_proj* proj, const void* s0, const void* s1, cudaStream_t st);
+sv_status start_f16(const Args& g, int n, const sv_q4_proj* proj, const void* s0, const void* s1, cudaStream_t st);
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -514,63 +32,6 @@ sv_status check_pointers(const sv_q4_proj* p) {
   return SV_OK;
 }
 
-// Rows of states per block, CTAs per SM and ring of an instantiation.
-template <typename T, int N, int H>
-sv_status start(Args g, const sv_q4_proj* proj, const void* s0, const void* s1, cudaStream_t stream) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 0;
-  static int sms[64] = {0};
-  if (!sms[dev]) {
-    int n = 0;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 148;
-    sms[dev] = n;
-  }
-  constexpr int kCtas = H == 1 ? 2 : 1;
-  constexpr int kBudget = (H == 1 ? 113 : 227) * 1024;  // shared memory per CTA
-  constexpr int kFixed = 1024 + static_cast<int>(sizeof(Bars));
-  g.ring = kHalfCols / (g.group / 2 + N);
-  if (g.ring > kMaxRing) g.ring = kMaxRing;
-  const int per_stage = kStageK / g.group;
-  g.s_words = per_stage + 1;
-  g.z_words = g.zeros ? 3 : 0;
-  // tile rows: as few rounds as 128 H rows per CTA allow, then rows spread evenly
-  const long long slots = static_cast<long long>(sms[dev]) * kCtas;
-  const long long rounds = (g.V + slots * 128 * H - 1) / (slots * 128 * H);
-  g.R = static_cast<int>(((g.V + slots * rounds - 1) / (slots * rounds) + 7) / 8 * 8);
-  g.tiles = (g.V + g.R - 1) / g.R;
-  const int stage_bytes = g.R * 128 + N * kStageK * 2 + 128 * H * 4 * (g.s_words + g.z_words);
-  g.stages = (kBudget - kFixed) / stage_bytes;
-  if (g.stages > kMaxStages) g.stages = kMaxStages;
-  g.nk = (g.d + kStageK - 1) / kStageK;
-  CUtensorMap mw, m0, m1;
-  const CUtensorMapDataType type =
-      Code<T>::kBase == 0x43004300u ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-  if (!encode(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, proj->packed, g.V, g.d / 2, g.R) ||
-      !encode(&m0, type, 2, g.rows0 ? s0 : s1, g.rows0 ? g.rows0 : g.rows1, g.d, 8) ||
-      !encode(&m1, type, 2, g.rows1 ? s1 : s0, g.rows1 ? g.rows1 : g.rows0, g.d, 8))
-    return svh::fail(SV_ERR_ARG, "tensor map encoding failed (alignment or size)");
-  const int smem = kFixed + g.stages * stage_bytes;
-  static bool attr_set[64] = {false};
-  if (!attr_set[dev]) {
-    const cudaError_t e = cudaFuncSetAttribute(q4_kernel<T, N, H>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBudget);
-    if (e != cudaSuccess) return svh::fail(SV_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
-    attr_set[dev] = true;
-  }
-  const unsigned grid = static_cast<unsigned>(g.tiles < slots ? g.tiles : slots);
-  q4_kernel<T, N, H><<<grid, 288 * H + 64, smem, stream>>>(mw, m0, m1, g);
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return svh::fail(SV_ERR_CUDA, "kernel launch: %s", cudaGetErrorString(e));
-  return SV_OK;
-}
-
-template <typename T>
-sv_status start_rows(const Args& g, int n, const sv_q4_proj* proj, const void* s0, const void* s1, cudaStream_t st) {
-  if (n <= 16) return start<T, 16, 1>(g, proj, s0, s1, st);
-  if (n <= 32) return start<T, 32, 2>(g, proj, s0, s1, st);
-  if (n <= 48) return start<T, 48, 2>(g, proj, s0, s1, st);
-  return start<T, 64, 2>(g, proj, s0, s1, st);
-}
-
 // rows0 rows of s0 into out0 and rows1 rows of s1 into out1, in one launch:
 // the two sets follow one another as rows of one product, the second from a
 // multiple of 8.
@@ -581,7 +42,6 @@ sv_status launch(const void* s0, int rows0, const void* s1, int rows1, sv_dtype 
   g.scales = proj->scales;
   g.zeros = proj->zeros;
   g.scale_dtype = proj->scale_dtype;
-  g.group = proj->group;
   g.G = (dim + proj->group - 1) / proj->group;
   g.out0 = out0;
   g.out1 = out1;
@@ -598,8 +58,7 @@ sv_status launch(const void* s0, int rows0, const void* s1, int rows1, sv_dtype 
   g.blocks = static_cast<int>((all + 63) / 64);
   const int n = static_cast<int>(((all + g.blocks - 1) / g.blocks + 15) / 16 * 16);
   g.blocks = static_cast<int>((all + n - 1) / n);
-  return dtype == SV_BF16 ? start_rows<__nv_bfloat16>(g, n, proj, s0, s1, stream)
-                          : start_rows<__half>(g, n, proj, s0, s1, stream);
+  return dtype == SV_BF16 ? start_bf16(g, n, proj, s0, s1, stream) : start_f16(g, n, proj, s0, s1, stream);
 }
 
 }  // namespace svq
