@@ -497,36 +497,44 @@ inline PFN_cuTensorMapEncodeTiled_v12000 encoder() {
   return fn;
 }
 
-// A row-major matrix in boxes of 128 bytes x box_rows, 128-byte swizzle;
-// what lies outside reads 0.
-inline bool encode(CUtensorMap* map, CUtensorMapDataType type, int elem, const void* base, long long rows, long long cols,
-            int box_rows) {
+// A row-major matrix in boxes of `width` (64 or 128) bytes x box_rows, swizzled
+// over that width; what lies outside reads 0.
+inline bool encode(CUtensorMap* map, CUtensorMapDataType type, int elem, const void* base, long long rows,
+                   long long cols, int box_rows, int width = 128) {
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
   const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * elem};
-  const cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / elem), static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(width / elem), static_cast<cuuint32_t>(box_rows)};
   const cuuint32_t es[2] = {1, 1};
   return encoder()(map, type, 2, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   width == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// SMs of the current device, which it also names.
+inline int sm_count(int* dev_out) {
+  static int sms[64] = {0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 0;
+  if (!sms[dev]) {
+    int n = 0;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 148;
+    sms[dev] = n;
+  }
+  *dev_out = dev;
+  return sms[dev];
 }
 
 // Rows of states per block, CTAs per SM and ring of an instantiation.
 template <typename T, int N, int G, int H>
 sv_status start(Args g, const sv_q4_proj* proj, const void* s0, const void* s1, cudaStream_t stream) {
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 0;
-  static int sms[64] = {0};
-  if (!sms[dev]) {
-    int n = 0;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 148;
-    sms[dev] = n;
-  }
+  const int sms = sm_count(&dev);
   constexpr int kCtas = H == 1 ? 2 : 1;
   constexpr int kBudget = (H == 1 ? 113 : 227) * 1024;  // shared memory per CTA
   constexpr int kFixed = 1024 + static_cast<int>(sizeof(Bars));
   constexpr int kWords = per_stage_of(G) + 1;
   // tile rows: as few rounds as 128 H rows per CTA allow, then rows spread evenly
-  const long long slots = static_cast<long long>(sms[dev]) * kCtas;
+  const long long slots = static_cast<long long>(sms) * kCtas;
   const long long rounds = (g.V + slots * 128 * H - 1) / (slots * 128 * H);
   g.R = static_cast<int>(((g.V + slots * rounds - 1) / (slots * rounds) + 7) / 8 * 8);
   g.tiles = (g.V + g.R - 1) / g.R;

@@ -77,6 +77,7 @@ def check(h, p, **kw):
     (1, 1, 32, 32), (1, 5, 64, 64), (3, 300, 96, 32), (7, 1000, 160, 128), (8, 257, 256, 64), (9, 255, 512, 128),
     (16, 2048, 1024, 32), (17, 1025, 2080, 128), (33, 700, 288, 64), (64, 512, 544, 32), (65, 300, 128, 128),
     (130, 900, 1056, 128), (11, 32000, 4096, 128), (1, 50257, 2080, 64), (5, 3000, 16384, 128),
+    (16, 700, 8192, 32), (14, 5000, 10016, 64), (16, 40000, 8192, 128), (12, 39000, 1024, 32), (2, 160000, 64, 32),
 ])
 def test_logits_shapes(dtype, rows, V, d, group):
     h, p = make(rows + V + d, rows, V, d, group, dtype, "f16" if dtype == "f16" else "bf16", zeros=rows % 2 == 0)
