@@ -1,16 +1,11 @@
-// The 4-bit LM head's kernels for bf16 states (a translation unit of its own:
-// they compile in parallel).
+// The 4-bit LM head's tensor-memory kernels for bf16 states (a translation unit
+// of its own: they compile in parallel).
 #include "sv_lm_head_q4.cuh"
-#include "sv_lm_head_q4_few.cuh"
 
 namespace svq {
 
 sv_status start_bf16(const Args& g, int n, const sv_q4_proj* proj, const void* s0, const void* s1, cudaStream_t st) {
   return start_group<__nv_bfloat16>(g, n, proj, s0, s1, st);
-}
-
-sv_status start_few_bf16(const Args& g, const sv_q4_proj* proj, const void* s0, const void* s1, cudaStream_t st) {
-  return start_few_any<__nv_bfloat16>(g, proj, s0, s1, st);
 }
 
 }  // namespace svq

@@ -10,17 +10,26 @@
 // the memory delivers 45 weights per clock and SM, so it is fast enough up to
 // here and not beyond.
 //
-//   - W rows are the MMA's 16 rows; a warp has 32 of them (two m tiles) and
-//     one 64-column half of every 128-column stage, sixteen warps in all.
-//   - Eight codes of a word make the pairs (0,4) (1,5) (2,6) (3,7) with one
-//     mask each; the states are laid out in that order once, as operands, in
-//     shared memory, where all of them stay.
+//   - W rows are the MMA's 16 rows; a warp has 32 of them (two m tiles) of
+//     every other 128-column stage, sixteen warps in all.
+//   - Eight codes of a word make the pairs (0,4) (1,5) (2,6) (3,7).  In f16
+//     that is nine instructions: a code at the bottom of a half word is
+//     1024 + q under a fixed exponent, one four bits up 1024 + 16 q, and one
+//     subtraction or multiply-add gives q - z exactly.  (bf16, with three
+//     mantissa bits less, needs eleven.)  So bf16 states become f16 under a
+//     power of two per row, which takes the row's largest to 2^14: exact for
+//     whatever is above 2^-28 of it, within 2^-39 of it below, far under the
+//     f32 sums' roundings; the logits take the power back.
+//   - The states lie in shared memory as operands in the pairs' order, all of
+//     them, for the kernel's life.
 //   - The sums of a group are f32 accumulators of their own, added to the
-//     row's with the group's scale: no weight is rounded.
-//   - Codes come by TMA, scales by cp.async from a warp of their own, in one
-//     ring of stages.
-//   - The two halves' sums are joined through shared memory at the tile's end,
-//     in a fixed order.
+//     row's with the group's scale: no weight is rounded.  A lane's codes of a
+//     stage are those of whole groups (32, 16 or 8 in a row for groups of 128,
+//     64, 32), so an MMA never mixes two.
+//   - Codes come by TMA, scales by cp.async from two warps of their own, in
+//     one ring of stages.
+//   - The two stage parities' sums are joined through shared memory at the
+//     tile's end, in a fixed order.
 // Every mbarrier wait is bounded; one that gives up sets bit 0 of *err, and
 // the warps then run through their remaining barriers without computing.
 #pragma once
@@ -30,8 +39,9 @@ namespace svq {
 
 constexpr int kFewK = 128;       // columns per stage: 64 bytes of a row
 constexpr int kFewTile = 256;    // rows per tile at most
-constexpr int kFewWarps = 16;    // that compute: 8 row groups x 2 halves of a stage
-constexpr int kFewThreads = 32 * (kFewWarps + 2);
+constexpr int kFewWarps = 16;    // that compute: 8 row groups x 2 stage parities
+constexpr int kFewHelp = 2;      // that fetch scales
+constexpr int kFewThreads = 32 * (kFewWarps + kFewHelp + 1);
 constexpr int kFewStages = 8;    // at most
 constexpr int kFewBudget = 227 * 1024;
 
@@ -59,88 +69,103 @@ __device__ __forceinline__ void bar_arrive() {
   asm volatile("bar.arrive %0, %1;" ::"n"(ID), "n"(32 * kFewWarps) : "memory");
 }
 
-// A word's eight codes as the pairs (0,4) (1,5) (2,6) (3,7) of integers minus
-// the zero.  In f16 a code four bits up is 16 times itself above 1024, which
-// the subtraction's multiplier takes back (exact), so half the shifts go.
-__device__ __forceinline__ void pairs_of(uint32_t w, uint32_t z, uint32_t (&p)[4], __nv_bfloat16) {
-  using C = Code<__nv_bfloat16>;
-  p[0] = C::sub((w & 0x000F000Fu) | C::kBase, z);
-  p[1] = C::sub((w >> 4 & 0x000F000Fu) | C::kBase, z);
-  p[2] = C::sub((w >> 8 & 0x000F000Fu) | C::kBase, z);
-  p[3] = C::sub((w >> 12 & 0x000F000Fu) | C::kBase, z);
-}
-__device__ __forceinline__ void pairs_of(uint32_t w, uint32_t z, uint32_t (&p)[4], __half) {
+// A word's eight codes as the pairs (0,4) (1,5) (2,6) (3,7) of q - zero in
+// f16, with z = 1024 + zero and z16 = -(64 + zero), twice each.
+__device__ __forceinline__ void pairs_of(uint32_t w, uint32_t z, uint32_t z16, uint32_t (&p)[4]) {
   using C = Code<__half>;
-  const __half2 sixteenth = __float2half2_rn(0.0625f), down = __float2half2_rn(960.f);  // 1024 - 64
-  const __half2 z16 = __hsub2(down, *reinterpret_cast<__half2*>(&z));                   // -(64 + zero)
   auto high = [&](uint32_t x) {
     uint32_t y = (x & 0x00F000F0u) | C::kBase;
-    const __half2 r = __hfma2(*reinterpret_cast<__half2*>(&y), sixteenth, z16);
+    const __half2 r = __hfma2(*reinterpret_cast<__half2*>(&y), __float2half2_rn(0.0625f), *reinterpret_cast<__half2*>(&z16));
     return *reinterpret_cast<const uint32_t*>(&r);
   };
+  const uint32_t x = w >> 8;
   p[0] = C::sub((w & 0x000F000Fu) | C::kBase, z);
   p[1] = high(w);
-  const uint32_t x = w >> 8;
   p[2] = C::sub((x & 0x000F000Fu) | C::kBase, z);
   p[3] = high(x);
 }
 
-template <typename T>
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
-  if constexpr (Code<T>::kBase == 0x43004300u)
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-  else
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// The same from zero.
+__device__ __forceinline__ void mma16816_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 struct FewArgs {
   Args g;
   const uint4* s0;
   const uint4* s1;
-  int group;
+  int bf16;  // the states' type
 };
 
-// Words of a row's scales (zeros) looked at per stage of `n` groups, and the
-// odd stride they lie at.
+// The odd stride at which a row's scales (zeros) of a stage of n groups lie, in words.
 __host__ __device__ constexpr int few_stride(int n) { return n == 1 ? 1 : n + 1; }
 __host__ __device__ constexpr int few_zstride(int n) { return n == 1 ? 1 : 3; }
 
-// NT tiles of 8 states; SMALL: groups of 32 (two to a warp's half stage).
-template <typename T, int NT, bool SMALL>
+// Words `from + 4 k` of every row of a tile to shared memory: word k of row r
+// for the lanes' (r, k), the next rows 32 / kWords on.  The rows of a lane lie
+// 8 apart or more, so their places within a word are alike.
+template <int kWords>
+__device__ __forceinline__ void fetch_words(uintptr_t from, long long row_bytes, int bytes, uint32_t* to, int stride,
+                                            int rows, int lane, int first) {
+  constexpr int kRows = 32 / kWords;  // per load
+  const int k = lane % kWords;
+  int r = first * kRows + lane / kWords;
+  const uintptr_t at = from + r * row_bytes;
+  uintptr_t word = (at & ~static_cast<uintptr_t>(3)) + 4 * k;
+  if (word >= at + bytes) return;
+  uint32_t dst = smem_u32(to + r * stride + k);
+#pragma unroll 4
+  for (; r < rows; r += kFewHelp * kRows) {
+    cp_async4(dst, reinterpret_cast<const void*>(word));
+    word += kFewHelp * kRows * row_bytes;
+    dst += kFewHelp * kRows * stride * 4;
+  }
+}
+
+// NT tiles of 8 states, groups of G, scales of type S (an sv_dtype).
+template <int NT, int G, int S>
 __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_constant__ CUtensorMap wmap,
                                                              const __grid_constant__ FewArgs f) {
+  constexpr int kPer = kFewK / G;       // groups per stage
+  constexpr int kLen = G / 32;          // words of a lane in a group
+  constexpr int kElem = S == SV_F32 ? 4 : 2;
+  constexpr int kStride = few_stride(kPer);
   const Args& g = f.g;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                          ~static_cast<uintptr_t>(1023));
-  const int stage_bytes = g.R * 64, rows = g.rows0 + g.rows1, per_stage = kFewK / f.group;
-  const int sstride = few_stride(per_stage), zstride = g.zeros ? few_zstride(per_stage) : 0;
-  unsigned char* frag = smem + g.stages * stage_bytes;                             // [32-column block][row][4 x 16 bytes]
-  float* red = reinterpret_cast<float*>(frag + g.nk * 4 * rows * 64);              // [row warp][8 NT][32]
-  uint32_t* sbuf = reinterpret_cast<uint32_t*>(red + kFewWarps / 2 * 8 * NT * 32);  // [stage][tile row][sstride]
-  uint32_t* zbuf = sbuf + g.stages * kFewTile * sstride;
+  const int stage_bytes = g.R * 64, rows = g.rows0 + g.rows1;
+  const int zstride = g.zeros ? few_zstride(kPer) : 0;
+  unsigned char* frag = smem + g.stages * stage_bytes;                              // [stage][operand 0..3][row][4 x 16 bytes]
+  float* red = reinterpret_cast<float*>(frag + g.nk * 4 * rows * 64);               // [row warp][8 NT][32]
+  uint32_t* sbuf = reinterpret_cast<uint32_t*>(red + kFewWarps / 2 * 8 * NT * 32);  // [slot][tile row][kStride]
+  uint32_t* zbuf = sbuf + g.stages * kFewTile * kStride;
   FewBars& bars = *reinterpret_cast<FewBars*>(zbuf + g.stages * kFewTile * zstride);
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < g.stages; ++s) {
-      mbar_init(&bars.full[s], 1 + 32);
-      mbar_init(&bars.empty[s], kFewWarps);
+      mbar_init(&bars.full[s], 1 + 32 * kFewHelp);
+      mbar_init(&bars.empty[s], kFewWarps / 2);
     }
     bars.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   __syncthreads();
 
-  if (warp == kFewWarps) {
+  if (warp == kFewWarps + kFewHelp) {
     // ---- codes: one thread
     if (lane == 0) {
       int s = 0, use = 0, issued = 0;
@@ -165,10 +190,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
     }
     return;
   }
-  if (warp == kFewWarps + 1) {
+  if (warp >= kFewWarps) {
     // ---- scales and zeros, as the 32-bit words that hold them
-    const int elem = g.scale_dtype == SV_F32 ? 4 : 2;
-    const int sw = per_stage == 4 ? 2 : per_stage == 2 ? 1 : 0, zw = per_stage == 1 ? 0 : 1;
     int s = 0, use = 0;
     bool ok = true;
     for (int t = blockIdx.x; ok && t < g.tiles; t += gridDim.x) {
@@ -177,25 +200,13 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
       for (int ks = 0; ok && ks < g.nk; ++ks) {
         if (use > 0) ok = __all_sync(0xFFFFFFFFu, few_wait(bars, &bars.empty[s], (use - 1) & 1, g.err));
         if (!ok) break;
-        const int j0 = ks * per_stage, n = min(per_stage, g.G - j0);
-        uint32_t* sd = sbuf + s * kFewTile * sstride;
-#pragma unroll 4
-        for (int e = lane; e < n_rows << sw; e += 32) {
-          const int r = e >> sw, k = e & ((1 << sw) - 1);
-          const uintptr_t at = reinterpret_cast<uintptr_t>(g.scales) + ((v0 + r) * g.G + j0) * elem;
-          const uintptr_t word = (at & ~static_cast<uintptr_t>(3)) + 4 * k;
-          if (word < at + n * elem) cp_async4(smem_u32(sd + r * sstride + k), reinterpret_cast<const void*>(word));
-        }
-        if (g.zeros) {
-          uint32_t* zd = zbuf + s * kFewTile * zstride;
-#pragma unroll 4
-          for (int e = lane; e < n_rows << zw; e += 32) {
-            const int r = e >> zw, k = e & ((1 << zw) - 1);
-            const uintptr_t at = reinterpret_cast<uintptr_t>(g.zeros) + (v0 + r) * g.G + j0;
-            const uintptr_t word = (at & ~static_cast<uintptr_t>(3)) + 4 * k;
-            if (word < at + n) cp_async4(smem_u32(zd + r * zstride + k), reinterpret_cast<const void*>(word));
-          }
-        }
+        const int n = min(kPer, g.G - ks * kPer);
+        fetch_words<kPer>(reinterpret_cast<uintptr_t>(g.scales) + (v0 * g.G + ks * kPer) * kElem,
+                          static_cast<long long>(g.G) * kElem, n * kElem, sbuf + s * kFewTile * kStride, kStride, n_rows,
+                          lane, warp - kFewWarps);
+        if (g.zeros)
+          fetch_words<kPer == 1 ? 1 : 2>(reinterpret_cast<uintptr_t>(g.zeros) + v0 * g.G + ks * kPer, g.G, n,
+                                         zbuf + s * kFewTile * zstride, zstride, n_rows, lane, warp - kFewWarps);
         cp_async_arrive(&bars.full[s]);
         if (++s == g.stages) {
           s = 0;
@@ -207,31 +218,74 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
     return;
   }
 
-  // ---- the states as operands: block q, row n, quarter t holds columns
-  // 32 q + 8 t .. + 7 as the pairs above; columns past dim are 0
-  for (int e = threadIdx.x; e < rows * g.nk * 16; e += 32 * kFewWarps) {
-    const int n = e / (g.nk * 16), j = e - n * (g.nk * 16);
-    uint4 x = make_uint4(0, 0, 0, 0);
-    if (j < g.d / 8)
-      x = __ldg((n < g.rows0 ? f.s0 + static_cast<long long>(n) * (g.d / 8) : f.s1 + static_cast<long long>(n - g.rows0) * (g.d / 8)) + j);
-    uint4 y;
-    y.x = __byte_perm(x.x, x.z, 0x5410);
-    y.y = __byte_perm(x.x, x.z, 0x7632);
-    y.z = __byte_perm(x.y, x.w, 0x5410);
-    y.w = __byte_perm(x.y, x.w, 0x7632);
-    *reinterpret_cast<uint4*>(frag + ((j / 4) * rows + n) * 64 + j % 4 * 16) = y;
+  // ---- the states as operands; columns past dim are 0.  A warp has a row.
+  if (warp < rows) {
+    const uint4* src = warp < g.rows0 ? f.s0 + static_cast<long long>(warp) * (g.d / 8)
+                                      : f.s1 + static_cast<long long>(warp - g.rows0) * (g.d / 8);
+    const int chunks = g.d / 8;
+    int shift = 0;  // bf16: the power of two that takes the largest finite state to 2^14
+    if (f.bf16) {
+      uint32_t top = 0;
+      for (int j = lane; j < chunks; j += 32) {
+        const uint4 x = __ldg(src + j);
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t lo = w[i] & 0x7FFFu, hi = w[i] >> 16 & 0x7FFFu;
+          if (lo < 0x7F80u) top = max(top, lo);
+          if (hi < 0x7F80u) top = max(top, hi);
+        }
+      }
+      top = __reduce_max_sync(0xFFFFFFFFu, top);
+      if (top) shift = 14 - ilogbf(__uint_as_float(top << 16));
+    }
+    if (lane == 0) red[warp] = static_cast<float>(shift);  // until the first tile ends
+    for (int j = lane; j < g.nk * 16; j += 32) {
+      uint4 x = make_uint4(0, 0, 0, 0);
+      if (j < chunks) x = __ldg(src + j);
+      if (f.bf16) {
+        uint32_t* w = &x.x;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const __half2 h = __floats2half2_rn(scalbnf(__uint_as_float(w[i] << 16), shift), scalbnf(__uint_as_float(w[i] & 0xFFFF0000u), shift));
+          w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+      }
+      uint4 y;
+      y.x = __byte_perm(x.x, x.z, 0x5410);
+      y.y = __byte_perm(x.x, x.z, 0x7632);
+      y.z = __byte_perm(x.y, x.w, 0x5410);
+      y.w = __byte_perm(x.y, x.w, 0x7632);
+      // which lane quarter multiplies these 8 columns, and as its how manieth word
+      const int c = j % 16, q = G == 128 ? c / 4 : G == 64 ? c % 8 / 2 : c % 4,
+                i = G == 128 ? c % 4 : G == 64 ? c / 8 * 2 + c % 2 : c / 4;
+      *reinterpret_cast<uint4*>(frag + (((j / 16) * 4 + i) * rows + warp) * 64 + q * 16) = y;
+    }
   }
   bar_sync<1>();
 
   const int rw = warp % 8, kh = warp / 8, gq = lane / 4, t4 = lane % 4;
   const bool active = rw * 32 < g.R;
-  const int code0 = (rw * 32 + gq) * 64 + t4 * 4, swz = gq >> 1 & 3;
-  int s = 0, use = 0;
-  bool ok = true, first_tile = true;
-  for (int t = blockIdx.x; t < g.tiles; t += gridDim.x) {
+  int back[NT][2];  // the rows' powers of two, to take back
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int r = n * 8 + 2 * t4 + e;
+      back[n][e] = r < rows ? -static_cast<int>(red[r]) : 0;
+    }
+  bar_sync<1>();
+  const int swz = gq >> 1 & 3;
+  const unsigned char* my_codes = smem + (rw * 32 + gq) * 64;
+  const unsigned char* my_frag[NT];  // columns of an MMA past the last row repeat it, unused
+#pragma unroll
+  for (int n = 0; n < NT; ++n) my_frag[n] = frag + min(n * 8 + gq, rows - 1) * 64 + t4 * 16;
+  bool ok = true;
+  int tile_no = 0;
+  for (int t = blockIdx.x; t < g.tiles; t += gridDim.x, ++tile_no) {
     const long long v0 = static_cast<long long>(t) * g.R + rw * 32;
     // place of a row's first scale in its word; the rows of a lane lie 8 apart, so it is theirs all
-    const int s_par = g.scale_dtype == SV_F32 ? 0 : static_cast<int>((reinterpret_cast<uintptr_t>(g.scales) / 2 + (v0 + gq) * g.G) & 1);
+    const int s_par = S == SV_F32 ? 0 : static_cast<int>((reinterpret_cast<uintptr_t>(g.scales) / 2 + (v0 + gq) * g.G) & 1);
     const int z_par = static_cast<int>((reinterpret_cast<uintptr_t>(g.zeros) + (v0 + gq) * g.G) & 3);
     float acc[2][NT][4];
 #pragma unroll
@@ -240,89 +294,99 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.f;
-    for (int ks = 0; ks < g.nk; ++ks) {
-      ok = __all_sync(0xFFFFFFFFu, ok && few_wait(bars, &bars.full[s], use & 1, g.err));
+    const long long count = static_cast<long long>(tile_no) * g.nk + kh;
+    int s = static_cast<int>(count % g.stages), use = static_cast<int>(count / g.stages & 1);
+    for (int ks = kh; ks < g.nk; ks += 2) {
+      ok = __all_sync(0xFFFFFFFFu, ok && few_wait(bars, &bars.full[s], use, g.err));
       if (ok && active) {
-        const unsigned char* codes = smem + s * stage_bytes + code0;
-        uint32_t w[2][2][2];  // [m tile][row half][32-column block]
+        const unsigned char* codes = my_codes + s * stage_bytes;
+        const uint32_t* srow = sbuf + (s * kFewTile + rw * 32 + gq) * kStride;
+        const unsigned char* zrow = reinterpret_cast<const unsigned char*>(zbuf + (s * kFewTile + rw * 32 + gq) * zstride) + (z_par + ks * kPer & 3);
+        const int s_at = s_par + ks * kPer & 1;
+        const int n_groups = min(kPer, g.G - ks * kPer);
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int j = 0; j < kPer; ++j) {
+          if (j >= n_groups) break;
+          uint32_t w[2][2][kLen];  // [m tile][row half][word]
 #pragma unroll
           for (int m = 0; m < 2; ++m)
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-              w[m][h][i] = *reinterpret_cast<const uint32_t*>(codes + (m * 16 + h * 8) * 64 + (((2 * kh + i) ^ swz) << 4));
-        const int j0 = ks * per_stage;
-        const uint32_t* srow = sbuf + (s * kFewTile + rw * 32 + gq) * sstride;
-        const unsigned char* zrow = reinterpret_cast<const unsigned char*>(zbuf + (s * kFewTile + rw * 32 + gq) * zstride) + (z_par + j0 & 3);
-        const int s_at = s_par + j0 & 1;
-        float part[2][NT][4];
-        float scale[2][2];
-        uint32_t z[2][2];
+            for (int h = 0; h < 2; ++h) {
+              const unsigned char* p = codes + (m * 16 + h * 8) * 64;
+              if constexpr (G == 128) {
+                const uint4 q = *reinterpret_cast<const uint4*>(p + ((t4 ^ swz) << 4));
+                w[m][h][0] = q.x, w[m][h][1] = q.y, w[m][h][2] = q.z, w[m][h][3] = q.w;
+              } else if constexpr (G == 64) {
+                const uint2 q = *reinterpret_cast<const uint2*>(p + (((2 * j + t4 / 2) ^ swz) << 4) + t4 % 2 * 8);
+                w[m][h][0] = q.x, w[m][h][1] = q.y;
+              } else {
+                w[m][h][0] = *reinterpret_cast<const uint32_t*>(p + ((j ^ swz) << 4) + t4 * 4);
+              }
+            }
+          float scale[2][2];
+          uint32_t z[2][2], z16[2][2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          if (i == 0 || SMALL) {
-            const int j = SMALL ? 2 * kh + i : f.group == 64 ? kh : 0;  // the group within the stage
-            const bool in = j0 + j < g.G;
+          for (int m = 0; m < 2; ++m)
 #pragma unroll
-            for (int m = 0; m < 2; ++m)
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t* p = srow + (m * 16 + h * 8) * kStride;
+              if constexpr (S == SV_F32)
+                scale[m][h] = __uint_as_float(p[j]);
+              else if constexpr (S == SV_BF16)
+                scale[m][h] = __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const unsigned short*>(p)[s_at + j]) << 16);
+              else
+                scale[m][h] = __half2float(reinterpret_cast<const __half*>(p)[s_at + j]);
+              z[m][h] = 0x64086408u;    // 1024 + 8
+              z16[m][h] = 0xD480D480u;  // -(64 + 8)
+              if (g.zeros) {
+                const uint32_t zero = zrow[(m * 16 + h * 8) * zstride * 4 + j] & 15u;
+                z[m][h] = (zero | zero << 16) + Code<__half>::kBase;
+                z16[m][h] = 0xD400D400u + ((zero | zero << 16) << 4);  // -64 has 1/16 as its last bit
+              }
+            }
+          float part[2][NT][4];
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const uint32_t* p = srow + (m * 16 + h * 8) * sstride;
-                float x;
-                if (g.scale_dtype == SV_F32)
-                  x = __uint_as_float(p[j]);
-                else if (g.scale_dtype == SV_BF16)
-                  x = __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const unsigned short*>(p)[s_at + j]) << 16);
+          for (int i = 0; i < kLen; ++i) {
+            uint4 b[NT];
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+              b[n] = *reinterpret_cast<const uint4*>(my_frag[n] + (ks * 4 + j * kLen + i) * rows * 64);
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+              uint32_t lo[4], hi[4];
+              pairs_of(w[m][0][i], z[m][0], z16[m][0], lo);
+              pairs_of(w[m][1][i], z[m][1], z16[m][1], hi);
+#pragma unroll
+              for (int n = 0; n < NT; ++n) {
+                if (i == 0)
+                  mma16816_first(part[m][n], lo[0], hi[0], lo[1], hi[1], b[n].x, b[n].y);
                 else
-                  x = __half2float(reinterpret_cast<const __half*>(p)[s_at + j]);
-                scale[m][h] = in ? x : 0.f;  // past the row's last group the codes are padding
-                const uint32_t zero = g.zeros ? zrow[(m * 16 + h * 8) * zstride * 4 + j] & 15u : 8u;
-                z[m][h] = (zero | zero << 16) + Code<T>::kBase;
+                  mma16816(part[m][n], lo[0], hi[0], lo[1], hi[1], b[n].x, b[n].y);
               }
 #pragma unroll
-            for (int m = 0; m < 2; ++m)
-#pragma unroll
-              for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) part[m][n][e] = 0.f;
+              for (int n = 0; n < NT; ++n) mma16816(part[m][n], lo[2], hi[2], lo[3], hi[3], b[n].z, b[n].w);
+            }
           }
-          uint4 b[NT];
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
-            b[n] = n * 8 + gq < rows ? *reinterpret_cast<const uint4*>(frag + (((ks * 4 + kh * 2 + i) * rows + n * 8 + gq) * 4 + t4) * 16)
-                                     : make_uint4(0, 0, 0, 0);
+          for (int m = 0; m < 2; ++m)
 #pragma unroll
-          for (int m = 0; m < 2; ++m) {
-            uint32_t lo[4], hi[4];
-            pairs_of(w[m][0][i], z[m][0], lo, T());
-            pairs_of(w[m][1][i], z[m][1], hi, T());
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int n = 0; n < NT; ++n) mma16816<T>(part[m][n], lo[0], hi[0], lo[1], hi[1], b[n].x, b[n].y);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) mma16816<T>(part[m][n], lo[2], hi[2], lo[3], hi[3], b[n].z, b[n].w);
-          }
-          if (i == 1 || SMALL) {
-#pragma unroll
-            for (int m = 0; m < 2; ++m)
-#pragma unroll
-              for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[m][n][e] = fmaf(scale[m][e / 2], part[m][n][e], acc[m][n][e]);
-          }
+              for (int e = 0; e < 4; ++e) acc[m][n][e] = fmaf(scale[m][e / 2], part[m][n][e], acc[m][n][e]);
         }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive_local(&bars.empty[s]);
-      if (++s == g.stages) {
-        s = 0;
-        ++use;
+      s += 2;
+      if (s >= g.stages) {
+        s -= g.stages;
+        use ^= 1;
       }
     }
-    // join the halves; the first one's warps write the logits
+    // join the parities; the first one's warps write the logits
     float* mine = red + rw * 8 * NT * 32 + lane;
     if (kh == 1) {
-      if (!first_tile) bar_sync<3>();  // the last tile's sums have been read
+      if (tile_no) bar_sync<3>();  // the last tile's sums have been read
 #pragma unroll
       for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -353,13 +417,12 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
             for (int m = 0; m < 2; ++m)
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                const int in = rw * 32 + m * 16 + h * 8 + gq;
-                if (in < g.R && v0 + m * 16 + h * 8 + gq < g.V) out[v0 + m * 16 + h * 8 + gq] = acc[m][n][2 * h + e];
+                const long long v = v0 + m * 16 + h * 8 + gq;
+                if (v < g.V) out[v] = scalbnf(acc[m][n][2 * h + e], back[n][e]);
               }
           }
       }
     }
-    first_tile = false;
   }
 }
 
@@ -367,13 +430,13 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
 inline int few_smem(const Args& g, int group, int stages, int nt) {
   const int per = kFewK / group;
   return 1024 + stages * (g.R * 64 + kFewTile * 4 * (few_stride(per) + (g.zeros ? few_zstride(per) : 0))) +
-         g.nk * 4 * (g.rows0 + g.rows1) * 64 + kFewWarps / 2 * 8 * nt * 32 * 4 + 8 + static_cast<int>(sizeof(FewBars));
+         g.nk * 4 * (g.rows0 + g.rows1) * 64 + kFewWarps / 2 * 8 * nt * 32 * 4 + static_cast<int>(sizeof(FewBars));
 }
 
 // Launches the call here if its states fit beside a ring of four stages
 // (SV_ERR_UNSUPPORTED otherwise, with nothing enqueued).
-template <typename T, int NT, bool SMALL>
-sv_status start_few(Args g, const sv_q4_proj* proj, const void* s0, const void* s1, cudaStream_t stream) {
+template <int NT, int G, int S>
+sv_status start_few(Args g, bool bf16, const sv_q4_proj* proj, const void* s0, const void* s1, cudaStream_t stream) {
   int dev = 0;
   const int sms = sm_count(&dev);
   // tile rows: as few rounds as tiles of 256 allow, then spread evenly, in warps' 32 rows
@@ -382,32 +445,31 @@ sv_status start_few(Args g, const sv_q4_proj* proj, const void* s0, const void* 
   g.tiles = (g.V + g.R - 1) / g.R;
   g.nk = (g.d + kFewK - 1) / kFewK;
   g.stages = kFewStages;
-  while (g.stages >= 4 && few_smem(g, proj->group, g.stages, NT) > kFewBudget) --g.stages;
+  while (g.stages >= 4 && few_smem(g, G, g.stages, NT) > kFewBudget) --g.stages;
   if (g.stages < 4) return SV_ERR_UNSUPPORTED;
   CUtensorMap mw;
   if (!encode(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, proj->packed, g.V, g.d / 2, g.R, 64))
     return svh::fail(SV_ERR_ARG, "tensor map encoding failed (alignment or size)");
   static bool attr_set[64] = {false};
   if (!attr_set[dev]) {
-    const cudaError_t e = cudaFuncSetAttribute(few_kernel<T, NT, SMALL>, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewBudget);
+    const cudaError_t e = cudaFuncSetAttribute(few_kernel<NT, G, S>, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewBudget);
     if (e != cudaSuccess) return svh::fail(SV_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
     attr_set[dev] = true;
   }
-  FewArgs f{g, static_cast<const uint4*>(s0), static_cast<const uint4*>(s1), proj->group};
-  few_kernel<T, NT, SMALL><<<static_cast<unsigned>(g.tiles < sms ? g.tiles : sms), kFewThreads,
-                             few_smem(g, proj->group, g.stages, NT), stream>>>(mw, f);
+  FewArgs f{g, static_cast<const uint4*>(s0), static_cast<const uint4*>(s1), bf16};
+  few_kernel<NT, G, S><<<static_cast<unsigned>(g.tiles < sms ? g.tiles : sms), kFewThreads,
+                         few_smem(g, G, g.stages, NT), stream>>>(mw, f);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return svh::fail(SV_ERR_CUDA, "kernel launch: %s", cudaGetErrorString(e));
   return SV_OK;
 }
 
-template <typename T>
-sv_status start_few_any(const Args& g, const sv_q4_proj* proj, const void* s0, const void* s1, cudaStream_t st) {
-  const int rows = g.rows0 + g.rows1;
-  if (rows > 16) return SV_ERR_UNSUPPORTED;
-  if (proj->group == 32)
-    return rows <= 8 ? start_few<T, 1, true>(g, proj, s0, s1, st) : start_few<T, 2, true>(g, proj, s0, s1, st);
-  return rows <= 8 ? start_few<T, 1, false>(g, proj, s0, s1, st) : start_few<T, 2, false>(g, proj, s0, s1, st);
+template <int S>
+sv_status start_few_scale(const Args& g, bool bf16, const sv_q4_proj* proj, const void* s0, const void* s1, cudaStream_t st) {
+  const bool one = g.rows0 + g.rows1 <= 8;
+  if (proj->group == 32) return one ? start_few<1, 32, S>(g, bf16, proj, s0, s1, st) : start_few<2, 32, S>(g, bf16, proj, s0, s1, st);
+  if (proj->group == 64) return one ? start_few<1, 64, S>(g, bf16, proj, s0, s1, st) : start_few<2, 64, S>(g, bf16, proj, s0, s1, st);
+  return one ? start_few<1, 128, S>(g, bf16, proj, s0, s1, st) : start_few<2, 128, S>(g, bf16, proj, s0, s1, st);
 }
 
 }  // namespace svq
