@@ -180,6 +180,38 @@ __device__ __forceinline__ void turn(uint32_t w, uint32_t z, uint32_t* a) {
   }
 }
 
+// Shared memory by 32-bit address (a pointer that went through an integer, as
+// aligned ones do, loads by the generic path).
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+// A 16-bit scale's value.
+__device__ __forceinline__ float scale16(uint32_t v, int dtype) {
+  return dtype == SV_BF16 ? __uint_as_float(v << 16) : __half2float(__ushort_as_half(static_cast<unsigned short>(v)));
+}
+
 // One 32-bit word to shared memory; its arrival is counted by the barrier that
 // cp_async_arrive names.
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
@@ -392,34 +424,28 @@ __global__ void __launch_bounds__(288 * H + 64, H == 1 ? 2 : 1)
         };
         for (int ks = 0; ok && ks < g.nk; ++ks) {
           ok = __all_sync(0xFFFFFFFFu, wait_or_abort(bars, &bars.full[s], use & 1, g.err));
-          const unsigned char* codes = smem + s * stage_bytes + row * 128;
-          const uint32_t* srow = sbuf + (s * 128 * H + row) * kSWords;
-          const unsigned char* zrow = reinterpret_cast<const unsigned char*>(zbuf + (s * 128 * H + row) * z_words) +
-                                      ((z_off + ks * per_stage) & 3);
+          const uint32_t codes = smem_u32(smem) + s * stage_bytes + row * 128;
+          const uint32_t srow = smem_u32(sbuf) + (s * 128 * H + row) * kSWords * 4;
+          const uint32_t zrow = smem_u32(zbuf) + (s * 128 * H + row) * z_words * 4 + ((z_off + ks * per_stage) & 3);
           const int n = min(per_stage, g.G - ks * per_stage);
           float scales[per_stage];
           if (g.scale_dtype == SV_F32) {
 #pragma unroll
-            for (int i = 0; i < per_stage; ++i) scales[i] = __uint_as_float(srow[i]);
+            for (int i = 0; i < per_stage; ++i) scales[i] = __uint_as_float(lds32(srow + i * 4));
           } else {
-            uint32_t w[per_stage];
 #pragma unroll
-            for (int i = 0; i < per_stage; ++i) w[i] = reinterpret_cast<const unsigned short*>(srow)[s_off + i];
-#pragma unroll
-            for (int i = 0; i < per_stage; ++i)
-              scales[i] = g.scale_dtype == SV_BF16 ? __uint_as_float(w[i] << 16)
-                                                   : __half2float(__ushort_as_half(static_cast<unsigned short>(w[i])));
+            for (int i = 0; i < per_stage; ++i) scales[i] = scale16(lds16(srow + (s_off + i) * 2), g.scale_dtype);
           }
 #pragma unroll
           for (int i = 0; i < per_stage; ++i) {
             if (!ok || i >= n) break;
-            const uint32_t z0 = g.zeros ? zrow[i] & 15u : 8u;
+            const uint32_t z0 = g.zeros ? lds8(zrow + i) & 15u : 8u;
             const uint32_t z = (z0 | z0 << 16) + Code<T>::kBase;
             const uint32_t dst = ta + buf * a_cols;
             if constexpr (a_cols == 64) {
 #pragma unroll
               for (int c = 0; c < 2; ++c) {
-                const uint4 q = *reinterpret_cast<const uint4*>(codes + (((4 * i + 2 * wg + c) ^ (row & 7)) << 4));
+                const uint4 q = lds128(codes + (((4 * i + 2 * wg + c) ^ (row & 7)) << 4));
                 uint32_t a[16];
                 turn<T>(q.x, z, a);
                 turn<T>(q.y, z, a + 4);
@@ -428,7 +454,7 @@ __global__ void __launch_bounds__(288 * H + 64, H == 1 ? 2 : 1)
                 tmem_st16(dst + c * 16, a);
               }
             } else if constexpr (a_cols == 32) {
-              const uint4 q = *reinterpret_cast<const uint4*>(codes + (((2 * i + wg) ^ (row & 7)) << 4));
+              const uint4 q = lds128(codes + (((2 * i + wg) ^ (row & 7)) << 4));
               uint32_t a[16];
               turn<T>(q.x, z, a);
               turn<T>(q.y, z, a + 4);
@@ -436,7 +462,7 @@ __global__ void __launch_bounds__(288 * H + 64, H == 1 ? 2 : 1)
               turn<T>(q.w, z, a + 12);
               tmem_st16(dst, a);
             } else {
-              const uint2 q = *reinterpret_cast<const uint2*>(codes + ((i ^ (row & 7)) << 4) + wg * 8);
+              const uint2 q = lds64(codes + ((i ^ (row & 7)) << 4) + wg * 8);
               uint32_t a[8];
               turn<T>(q.x, z, a);
               turn<T>(q.y, z, a + 4);

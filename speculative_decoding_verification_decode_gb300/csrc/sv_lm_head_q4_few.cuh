@@ -87,7 +87,7 @@ __device__ __forceinline__ void pairs_of(uint32_t w, uint32_t z, uint32_t z16, u
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -96,7 +96,7 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
 // The same from zero.
 __device__ __forceinline__ void mma16816_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                                uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%10, %10, %10, %10};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
@@ -135,25 +135,25 @@ __device__ __forceinline__ void fetch_words(uintptr_t from, long long row_bytes,
   }
 }
 
-// NT tiles of 8 states, groups of G, scales of type S (an sv_dtype).
-template <int NT, int G, int S>
+// NT tiles of 8 states, groups of G, Z: zeros are given.
+template <int NT, int G, bool Z>
 __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_constant__ CUtensorMap wmap,
                                                              const __grid_constant__ FewArgs f) {
   constexpr int kPer = kFewK / G;       // groups per stage
   constexpr int kLen = G / 32;          // words of a lane in a group
-  constexpr int kElem = S == SV_F32 ? 4 : 2;
   constexpr int kStride = few_stride(kPer);
   const Args& g = f.g;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                          ~static_cast<uintptr_t>(1023));
   const int stage_bytes = g.R * 64, rows = g.rows0 + g.rows1;
-  const int zstride = g.zeros ? few_zstride(kPer) : 0;
+  constexpr int kZStride = Z ? few_zstride(kPer) : 0;
+  const int elem = g.scale_dtype == SV_F32 ? 4 : 2;
   unsigned char* frag = smem + g.stages * stage_bytes;                              // [stage][operand 0..3][row][4 x 16 bytes]
   float* red = reinterpret_cast<float*>(frag + g.nk * 4 * rows * 64);               // [row warp][8 NT][32]
   uint32_t* sbuf = reinterpret_cast<uint32_t*>(red + kFewWarps / 2 * 8 * NT * 32);  // [slot][tile row][kStride]
   uint32_t* zbuf = sbuf + g.stages * kFewTile * kStride;
-  FewBars& bars = *reinterpret_cast<FewBars*>(zbuf + g.stages * kFewTile * zstride);
+  FewBars& bars = *reinterpret_cast<FewBars*>(zbuf + g.stages * kFewTile * kZStride);
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < g.stages; ++s) {
@@ -201,12 +201,12 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
         if (use > 0) ok = __all_sync(0xFFFFFFFFu, few_wait(bars, &bars.empty[s], (use - 1) & 1, g.err));
         if (!ok) break;
         const int n = min(kPer, g.G - ks * kPer);
-        fetch_words<kPer>(reinterpret_cast<uintptr_t>(g.scales) + (v0 * g.G + ks * kPer) * kElem,
-                          static_cast<long long>(g.G) * kElem, n * kElem, sbuf + s * kFewTile * kStride, kStride, n_rows,
+        fetch_words<kPer>(reinterpret_cast<uintptr_t>(g.scales) + (v0 * g.G + ks * kPer) * elem,
+                          static_cast<long long>(g.G) * elem, n * elem, sbuf + s * kFewTile * kStride, kStride, n_rows,
                           lane, warp - kFewWarps);
-        if (g.zeros)
+        if constexpr (Z)
           fetch_words<kPer == 1 ? 1 : 2>(reinterpret_cast<uintptr_t>(g.zeros) + v0 * g.G + ks * kPer, g.G, n,
-                                         zbuf + s * kFewTile * zstride, zstride, n_rows, lane, warp - kFewWarps);
+                                         zbuf + s * kFewTile * kZStride, kZStride, n_rows, lane, warp - kFewWarps);
         cp_async_arrive(&bars.full[s]);
         if (++s == g.stages) {
           s = 0;
@@ -276,16 +276,19 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
     }
   bar_sync<1>();
   const int swz = gq >> 1 & 3;
-  const unsigned char* my_codes = smem + (rw * 32 + gq) * 64;
-  const unsigned char* my_frag[NT];  // columns of an MMA past the last row repeat it, unused
+  const uint32_t codes0 = smem_u32(smem) + (rw * 32 + gq) * 64;
+  const uint32_t srow0 = smem_u32(sbuf) + (rw * 32 + gq) * kStride * 4, zrow0 = smem_u32(zbuf) + (rw * 32 + gq) * kZStride * 4;
+  uint32_t frag0[NT];  // columns of an MMA past the last row repeat it, unused
 #pragma unroll
-  for (int n = 0; n < NT; ++n) my_frag[n] = frag + min(n * 8 + gq, rows - 1) * 64 + t4 * 16;
+  for (int n = 0; n < NT; ++n) frag0[n] = smem_u32(frag) + min(n * 8 + gq, rows - 1) * 64 + t4 * 16;
+  const int scale_dtype = g.scale_dtype, G_all = g.G, nk = g.nk, stages = g.stages;
+  const uint32_t frag_step = rows * 64;
   bool ok = true;
   int tile_no = 0;
   for (int t = blockIdx.x; t < g.tiles; t += gridDim.x, ++tile_no) {
     const long long v0 = static_cast<long long>(t) * g.R + rw * 32;
     // place of a row's first scale in its word; the rows of a lane lie 8 apart, so it is theirs all
-    const int s_par = S == SV_F32 ? 0 : static_cast<int>((reinterpret_cast<uintptr_t>(g.scales) / 2 + (v0 + gq) * g.G) & 1);
+    const int s_par = scale_dtype == SV_F32 ? 0 : static_cast<int>((reinterpret_cast<uintptr_t>(g.scales) / 2 + (v0 + gq) * g.G) & 1);
     const int z_par = static_cast<int>((reinterpret_cast<uintptr_t>(g.zeros) + (v0 + gq) * g.G) & 3);
     float acc[2][NT][4];
 #pragma unroll
@@ -296,14 +299,13 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
         for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.f;
     const long long count = static_cast<long long>(tile_no) * g.nk + kh;
     int s = static_cast<int>(count % g.stages), use = static_cast<int>(count / g.stages & 1);
-    for (int ks = kh; ks < g.nk; ks += 2) {
+    for (int ks = kh; ks < nk; ks += 2) {
       ok = __all_sync(0xFFFFFFFFu, ok && few_wait(bars, &bars.full[s], use, g.err));
       if (ok && active) {
-        const unsigned char* codes = my_codes + s * stage_bytes;
-        const uint32_t* srow = sbuf + (s * kFewTile + rw * 32 + gq) * kStride;
-        const unsigned char* zrow = reinterpret_cast<const unsigned char*>(zbuf + (s * kFewTile + rw * 32 + gq) * zstride) + (z_par + ks * kPer & 3);
-        const int s_at = s_par + ks * kPer & 1;
-        const int n_groups = min(kPer, g.G - ks * kPer);
+        const uint32_t codes = codes0 + s * stage_bytes;
+        const uint32_t srow = srow0 + s * (kFewTile * kStride * 4) + (scale_dtype == SV_F32 ? 0 : (s_par + ks * kPer & 1) * 2);
+        const uint32_t zrow = zrow0 + s * (kFewTile * kZStride * 4) + (z_par + ks * kPer & 3);
+        const int n_groups = min(kPer, G_all - ks * kPer);
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
           if (j >= n_groups) break;
@@ -312,34 +314,34 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
           for (int m = 0; m < 2; ++m)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const unsigned char* p = codes + (m * 16 + h * 8) * 64;
+              const uint32_t p = codes + (m * 16 + h * 8) * 64;
               if constexpr (G == 128) {
-                const uint4 q = *reinterpret_cast<const uint4*>(p + ((t4 ^ swz) << 4));
+                const uint4 q = lds128(p + ((t4 ^ swz) << 4));
                 w[m][h][0] = q.x, w[m][h][1] = q.y, w[m][h][2] = q.z, w[m][h][3] = q.w;
               } else if constexpr (G == 64) {
-                const uint2 q = *reinterpret_cast<const uint2*>(p + (((2 * j + t4 / 2) ^ swz) << 4) + t4 % 2 * 8);
+                const uint2 q = lds64(p + (((2 * j + t4 / 2) ^ swz) << 4) + t4 % 2 * 8);
                 w[m][h][0] = q.x, w[m][h][1] = q.y;
               } else {
-                w[m][h][0] = *reinterpret_cast<const uint32_t*>(p + ((j ^ swz) << 4) + t4 * 4);
+                w[m][h][0] = lds32(p + ((j ^ swz) << 4) + t4 * 4);
               }
             }
           float scale[2][2];
+          if (scale_dtype == SV_F32) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) scale[i / 2][i % 2] = __uint_as_float(lds32(srow + (i * 8 * kStride + j) * 4));
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) scale[i / 2][i % 2] = scale16(lds16(srow + i * 8 * kStride * 4 + j * 2), scale_dtype);
+          }
           uint32_t z[2][2], z16[2][2];
 #pragma unroll
           for (int m = 0; m < 2; ++m)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const uint32_t* p = srow + (m * 16 + h * 8) * kStride;
-              if constexpr (S == SV_F32)
-                scale[m][h] = __uint_as_float(p[j]);
-              else if constexpr (S == SV_BF16)
-                scale[m][h] = __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const unsigned short*>(p)[s_at + j]) << 16);
-              else
-                scale[m][h] = __half2float(reinterpret_cast<const __half*>(p)[s_at + j]);
               z[m][h] = 0x64086408u;    // 1024 + 8
               z16[m][h] = 0xD480D480u;  // -(64 + 8)
-              if (g.zeros) {
-                const uint32_t zero = zrow[(m * 16 + h * 8) * zstride * 4 + j] & 15u;
+              if constexpr (Z) {
+                const uint32_t zero = lds8(zrow + (m * 16 + h * 8) * kZStride * 4 + j) & 15u;
                 z[m][h] = (zero | zero << 16) + Code<__half>::kBase;
                 z16[m][h] = 0xD400D400u + ((zero | zero << 16) << 4);  // -64 has 1/16 as its last bit
               }
@@ -350,7 +352,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
             uint4 b[NT];
 #pragma unroll
             for (int n = 0; n < NT; ++n)
-              b[n] = *reinterpret_cast<const uint4*>(my_frag[n] + (ks * 4 + j * kLen + i) * rows * 64);
+              b[n] = lds128(frag0[n] + (ks * 4 + j * kLen + i) * frag_step);
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
               uint32_t lo[4], hi[4];
@@ -378,8 +380,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
       __syncwarp();
       if (lane == 0) mbar_arrive_local(&bars.empty[s]);
       s += 2;
-      if (s >= g.stages) {
-        s -= g.stages;
+      if (s >= stages) {
+        s -= stages;
         use ^= 1;
       }
     }
@@ -435,7 +437,7 @@ inline int few_smem(const Args& g, int group, int stages, int nt) {
 
 // Launches the call here if its states fit beside a ring of four stages
 // (SV_ERR_UNSUPPORTED otherwise, with nothing enqueued).
-template <int NT, int G, int S>
+template <int NT, int G, bool Z>
 sv_status start_few(Args g, bool bf16, const sv_q4_proj* proj, const void* s0, const void* s1, cudaStream_t stream) {
   int dev = 0;
   const int sms = sm_count(&dev);
@@ -452,24 +454,27 @@ sv_status start_few(Args g, bool bf16, const sv_q4_proj* proj, const void* s0, c
     return svh::fail(SV_ERR_ARG, "tensor map encoding failed (alignment or size)");
   static bool attr_set[64] = {false};
   if (!attr_set[dev]) {
-    const cudaError_t e = cudaFuncSetAttribute(few_kernel<NT, G, S>, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewBudget);
+    const cudaError_t e = cudaFuncSetAttribute(few_kernel<NT, G, Z>, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewBudget);
     if (e != cudaSuccess) return svh::fail(SV_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
     attr_set[dev] = true;
   }
   FewArgs f{g, static_cast<const uint4*>(s0), static_cast<const uint4*>(s1), bf16};
-  few_kernel<NT, G, S><<<static_cast<unsigned>(g.tiles < sms ? g.tiles : sms), kFewThreads,
+  few_kernel<NT, G, Z><<<static_cast<unsigned>(g.tiles < sms ? g.tiles : sms), kFewThreads,
                          few_smem(g, G, g.stages, NT), stream>>>(mw, f);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return svh::fail(SV_ERR_CUDA, "kernel launch: %s", cudaGetErrorString(e));
   return SV_OK;
 }
 
-template <int S>
-sv_status start_few_scale(const Args& g, bool bf16, const sv_q4_proj* proj, const void* s0, const void* s1, cudaStream_t st) {
-  const bool one = g.rows0 + g.rows1 <= 8;
-  if (proj->group == 32) return one ? start_few<1, 32, S>(g, bf16, proj, s0, s1, st) : start_few<2, 32, S>(g, bf16, proj, s0, s1, st);
-  if (proj->group == 64) return one ? start_few<1, 64, S>(g, bf16, proj, s0, s1, st) : start_few<2, 64, S>(g, bf16, proj, s0, s1, st);
-  return one ? start_few<1, 128, S>(g, bf16, proj, s0, s1, st) : start_few<2, 128, S>(g, bf16, proj, s0, s1, st);
+template <int NT, int G>
+sv_status start_few_zeros(const Args& g, bool bf16, const sv_q4_proj* proj, const void* s0, const void* s1, cudaStream_t st) {
+  return g.zeros ? start_few<NT, G, true>(g, bf16, proj, s0, s1, st) : start_few<NT, G, false>(g, bf16, proj, s0, s1, st);
+}
+
+template <int G>
+sv_status start_few_group(const Args& g, bool bf16, const sv_q4_proj* proj, const void* s0, const void* s1, cudaStream_t st) {
+  return g.rows0 + g.rows1 <= 8 ? start_few_zeros<1, G>(g, bf16, proj, s0, s1, st)
+                                : start_few_zeros<2, G>(g, bf16, proj, s0, s1, st);
 }
 
 }  // namespace svq
