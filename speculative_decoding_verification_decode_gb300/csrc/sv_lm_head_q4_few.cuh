@@ -12,16 +12,18 @@
 //
 //   - W rows are the MMA's 16 rows; a warp has 32 of them (two m tiles) of
 //     every other 128-column stage, sixteen warps in all.
-//   - Eight codes of a word make the pairs (0,4) (1,5) (2,6) (3,7).  In f16
-//     that is nine instructions: a code at the bottom of a half word is
-//     1024 + q under a fixed exponent, one four bits up 1024 + 16 q, and one
-//     subtraction or multiply-add gives q - z exactly.  (bf16, with three
-//     mantissa bits less, needs eleven.)  So bf16 states become f16 under a
-//     power of two per row, which takes the row's largest to 2^14: exact for
-//     whatever is above 2^-28 of it, within 2^-39 of it below, far under the
-//     f32 sums' roundings; the logits take the power back.
-//   - The states lie in shared memory as operands in the pairs' order, all of
-//     them, for the kernel's life.
+//   - Eight codes of a word make the pairs (0,4) (1,5) (2,6) (3,7), by one
+//     mask each and one shift: a code in the lowest bits of a half word IS the
+//     f16 number q 2^-24, four bits up q 2^-20 (subnormal; tensor cores take
+//     them as they are).  The states that meet the second kind are kept 16
+//     times smaller.  The zeros come in as what a group's sum starts from,
+//     -z sum_k h, the sums kept from the beginning.  Five instructions for
+//     eight weights, and the product is exact as before up to f32 sums.
+//   - So the states are f16 under a power of two per row that takes the row's
+//     largest to 2^14: exact for whatever is above 2^-24 of it, within 2^-35
+//     of it below, far under the f32 sums' roundings; the logits take the
+//     power back.  They lie in shared memory as operands in the pairs' order,
+//     all of them, for the kernel's life.
 //   - The sums of a group are f32 accumulators of their own, added to the
 //     row's with the group's scale: no weight is rounded.  A lane's codes of a
 //     stage are those of whole groups (32, 16 or 8 in a row for groups of 128,
@@ -69,22 +71,6 @@ __device__ __forceinline__ void bar_arrive() {
   asm volatile("bar.arrive %0, %1;" ::"n"(ID), "n"(32 * kFewWarps) : "memory");
 }
 
-// A word's eight codes as the pairs (0,4) (1,5) (2,6) (3,7) of q - zero in
-// f16, with z = 1024 + zero and z16 = -(64 + zero), twice each.
-__device__ __forceinline__ void pairs_of(uint32_t w, uint32_t z, uint32_t z16, uint32_t (&p)[4]) {
-  using C = Code<__half>;
-  auto high = [&](uint32_t x) {
-    uint32_t y = (x & 0x00F000F0u) | C::kBase;
-    const __half2 r = __hfma2(*reinterpret_cast<__half2*>(&y), __float2half2_rn(0.0625f), *reinterpret_cast<__half2*>(&z16));
-    return *reinterpret_cast<const uint32_t*>(&r);
-  };
-  const uint32_t x = w >> 8;
-  p[0] = C::sub((w & 0x000F000Fu) | C::kBase, z);
-  p[1] = high(w);
-  p[2] = C::sub((x & 0x000F000Fu) | C::kBase, z);
-  p[3] = high(x);
-}
-
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
   asm(
@@ -93,14 +79,13 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// The same from zero.
-__device__ __forceinline__ void mma16816_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                               uint32_t b0, uint32_t b1) {
-  asm(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%10, %10, %10, %10};"
+// The same from c.
+__device__ __forceinline__ void mma16816_from(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1, const float (&c)[4]) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %11, %12, %13};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 
 struct FewArgs {
@@ -149,8 +134,10 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
   const int stage_bytes = g.R * 64, rows = g.rows0 + g.rows1;
   constexpr int kZStride = Z ? few_zstride(kPer) : 0;
   const int elem = g.scale_dtype == SV_F32 ? 4 : 2;
-  unsigned char* frag = smem + g.stages * stage_bytes;                              // [stage][operand 0..3][row][4 x 16 bytes]
-  float* red = reinterpret_cast<float*>(frag + g.nk * 4 * rows * 64);               // [row warp][8 NT][32]
+  const int frag_row = g.nk * 256 + 64;  // (64 more: neighbouring rows in other banks)
+  unsigned char* frag = smem + g.stages * stage_bytes;                              // [row][stage][operand 0..3][4 x 16 bytes]
+  float* sums = reinterpret_cast<float*>(frag + rows * frag_row);                   // [group][NT][lane quarter][4]
+  float* red = sums + g.nk * kPer * NT * 16;                                        // [row warp][8 NT][32]
   uint32_t* sbuf = reinterpret_cast<uint32_t*>(red + kFewWarps / 2 * 8 * NT * 32);  // [slot][tile row][kStride]
   uint32_t* zbuf = sbuf + g.stages * kFewTile * kStride;
   FewBars& bars = *reinterpret_cast<FewBars*>(zbuf + g.stages * kFewTile * kZStride);
@@ -223,43 +210,58 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
     const uint4* src = warp < g.rows0 ? f.s0 + static_cast<long long>(warp) * (g.d / 8)
                                       : f.s1 + static_cast<long long>(warp - g.rows0) * (g.d / 8);
     const int chunks = g.d / 8;
-    int shift = 0;  // bf16: the power of two that takes the largest finite state to 2^14
-    if (f.bf16) {
-      uint32_t top = 0;
-      for (int j = lane; j < chunks; j += 32) {
-        const uint4 x = __ldg(src + j);
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    const bool bf16 = f.bf16;
+    auto value = [&](uint32_t w, int high) {
+      w = high ? w >> 16 : w & 0xFFFFu;
+      return bf16 ? __uint_as_float(w << 16) : __half2float(__ushort_as_half(static_cast<unsigned short>(w)));
+    };
+    // the power of two that takes the row's largest finite state to 2^14
+    const uint32_t limit = bf16 ? 0x7F80u : 0x7C00u;
+    uint32_t top = 0;
+    for (int j = lane; j < chunks; j += 32) {
+      const uint4 x = __ldg(src + j);
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t lo = w[i] & 0x7FFFu, hi = w[i] >> 16 & 0x7FFFu;
-          if (lo < 0x7F80u) top = max(top, lo);
-          if (hi < 0x7F80u) top = max(top, hi);
-        }
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t lo = w[i] & 0x7FFFu, hi = w[i] >> 16 & 0x7FFFu;
+        if (lo < limit) top = max(top, lo);
+        if (hi < limit) top = max(top, hi);
       }
-      top = __reduce_max_sync(0xFFFFFFFFu, top);
-      if (top) shift = 14 - ilogbf(__uint_as_float(top << 16));
     }
+    top = __reduce_max_sync(0xFFFFFFFFu, top);
+    const int shift = top ? 14 - ilogbf(value(top, 0)) : 0;
     if (lane == 0) red[warp] = static_cast<float>(shift);  // until the first tile ends
-    for (int j = lane; j < g.nk * 16; j += 32) {
+    for (int j = lane; j < g.nk * 16; j += 32) {  // (nk * 16 a multiple of 16: half a warp stays together)
+      const unsigned mask = __activemask();
       uint4 x = make_uint4(0, 0, 0, 0);
       if (j < chunks) x = __ldg(src + j);
-      if (f.bf16) {
-        uint32_t* w = &x.x;
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+      __half h[8];
+      float sum = 0.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const __half2 h = __floats2half2_rn(scalbnf(__uint_as_float(w[i] << 16), shift), scalbnf(__uint_as_float(w[i] & 0xFFFF0000u), shift));
-          w[i] = *reinterpret_cast<const uint32_t*>(&h);
-        }
+      for (int i = 0; i < 8; ++i) {
+        h[i] = __float2half_rn(scalbnf(value(w[i / 2], i % 2), shift - (i % 2) * 4));
+        sum += __half2float(h[i]) * (i % 2 ? 16.f : 1.f);
       }
-      uint4 y;
-      y.x = __byte_perm(x.x, x.z, 0x5410);
-      y.y = __byte_perm(x.x, x.z, 0x7632);
-      y.z = __byte_perm(x.y, x.w, 0x5410);
-      y.w = __byte_perm(x.y, x.w, 0x7632);
+      uint32_t y[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const __half2 p = __halves2half2(h[i], h[i + 4]);
+        y[i] = *reinterpret_cast<const uint32_t*>(&p);
+      }
       // which lane quarter multiplies these 8 columns, and as its how manieth word
       const int c = j % 16, q = G == 128 ? c / 4 : G == 64 ? c % 8 / 2 : c % 4,
                 i = G == 128 ? c % 4 : G == 64 ? c / 8 * 2 + c % 2 : c / 4;
-      *reinterpret_cast<uint4*>(frag + (((j / 16) * 4 + i) * rows + warp) * 64 + q * 16) = y;
+      *reinterpret_cast<uint4*>(frag + warp * frag_row + j / 16 * 256 + i * 64 + q * 16) = make_uint4(y[0], y[1], y[2], y[3]);
+      // the group's sum, in the units of the products, with the zero of 8 or 1
+#pragma unroll
+      for (int o = 1; o < G / 8; o *= 2) sum += __shfl_xor_sync(mask, sum, o);
+      if (j % (G / 8) == 0) {
+        sum *= Z ? -0x1p-24f : -0x1p-21f;
+        float* to = sums + (j / (G / 8) * NT + warp / 8) * 16 + warp % 8 / 2 * 4 + warp % 2;
+        to[0] = sum;
+        to[2] = sum;
+      }
     }
   }
   bar_sync<1>();
@@ -272,7 +274,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int r = n * 8 + 2 * t4 + e;
-      back[n][e] = r < rows ? -static_cast<int>(red[r]) : 0;
+      back[n][e] = r < rows ? 24 - static_cast<int>(red[r]) : 0;
     }
   bar_sync<1>();
   const int swz = gq >> 1 & 3;
@@ -280,9 +282,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
   const uint32_t srow0 = smem_u32(sbuf) + (rw * 32 + gq) * kStride * 4, zrow0 = smem_u32(zbuf) + (rw * 32 + gq) * kZStride * 4;
   uint32_t frag0[NT];  // columns of an MMA past the last row repeat it, unused
 #pragma unroll
-  for (int n = 0; n < NT; ++n) frag0[n] = smem_u32(frag) + min(n * 8 + gq, rows - 1) * 64 + t4 * 16;
+  for (int n = 0; n < NT; ++n) frag0[n] = smem_u32(frag) + min(n * 8 + gq, rows - 1) * frag_row + t4 * 16;
   const int scale_dtype = g.scale_dtype, G_all = g.G, nk = g.nk, stages = g.stages;
-  const uint32_t frag_step = rows * 64;
+  const uint32_t sums0 = smem_u32(sums) + t4 * 16;
   bool ok = true;
   int tile_no = 0;
   for (int t = blockIdx.x; t < g.tiles; t += gridDim.x, ++tile_no) {
@@ -333,40 +335,45 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
 #pragma unroll
             for (int i = 0; i < 4; ++i) scale[i / 2][i % 2] = scale16(lds16(srow + i * 8 * kStride * 4 + j * 2), scale_dtype);
           }
-          uint32_t z[2][2], z16[2][2];
+          float from[NT][4];  // -(zero or 1) sum h
 #pragma unroll
-          for (int m = 0; m < 2; ++m)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              z[m][h] = 0x64086408u;    // 1024 + 8
-              z16[m][h] = 0xD480D480u;  // -(64 + 8)
-              if constexpr (Z) {
-                const uint32_t zero = lds8(zrow + (m * 16 + h * 8) * kZStride * 4 + j) & 15u;
-                z[m][h] = (zero | zero << 16) + Code<__half>::kBase;
-                z16[m][h] = 0xD400D400u + ((zero | zero << 16) << 4);  // -64 has 1/16 as its last bit
-              }
-            }
+          for (int n = 0; n < NT; ++n) {
+            const uint4 x = lds128(sums0 + ((ks * kPer + j) * NT + n) * 64);
+            from[n][0] = __uint_as_float(x.x), from[n][1] = __uint_as_float(x.y);
+            from[n][2] = __uint_as_float(x.z), from[n][3] = __uint_as_float(x.w);
+          }
           float part[2][NT][4];
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            if constexpr (Z) {
+              float z[2];
+#pragma unroll
+              for (int h = 0; h < 2; ++h)  // small integers: 2^23 + z less 2^23
+                z[h] = __uint_as_float(0x4B000000u | (lds8(zrow + (m * 16 + h * 8) * kZStride * 4 + j) & 15u)) - 8388608.f;
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) part[m][n][e] = from[n][e] * z[e / 2];
+            }
+          }
 #pragma unroll
           for (int i = 0; i < kLen; ++i) {
             uint4 b[NT];
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-              b[n] = lds128(frag0[n] + (ks * 4 + j * kLen + i) * frag_step);
+            for (int n = 0; n < NT; ++n) b[n] = lds128(frag0[n] + ks * 256 + (j * kLen + i) * 64);
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
-              uint32_t lo[4], hi[4];
-              pairs_of(w[m][0][i], z[m][0], z16[m][0], lo);
-              pairs_of(w[m][1][i], z[m][1], z16[m][1], hi);
+              const uint32_t lo = w[m][0][i], hi = w[m][1][i], lo8 = lo >> 8, hi8 = hi >> 8;
 #pragma unroll
               for (int n = 0; n < NT; ++n) {
-                if (i == 0)
-                  mma16816_first(part[m][n], lo[0], hi[0], lo[1], hi[1], b[n].x, b[n].y);
+                if (i == 0 && !Z)
+                  mma16816_from(part[m][n], lo & 0x000F000Fu, hi & 0x000F000Fu, lo & 0x00F000F0u, hi & 0x00F000F0u, b[n].x, b[n].y, from[n]);
                 else
-                  mma16816(part[m][n], lo[0], hi[0], lo[1], hi[1], b[n].x, b[n].y);
+                  mma16816(part[m][n], lo & 0x000F000Fu, hi & 0x000F000Fu, lo & 0x00F000F0u, hi & 0x00F000F0u, b[n].x, b[n].y);
               }
 #pragma unroll
-              for (int n = 0; n < NT; ++n) mma16816(part[m][n], lo[2], hi[2], lo[3], hi[3], b[n].z, b[n].w);
+              for (int n = 0; n < NT; ++n)
+                mma16816(part[m][n], lo8 & 0x000F000Fu, hi8 & 0x000F000Fu, lo8 & 0x00F000F0u, hi8 & 0x00F000F0u, b[n].z, b[n].w);
             }
           }
 #pragma unroll
@@ -432,7 +439,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
 inline int few_smem(const Args& g, int group, int stages, int nt) {
   const int per = kFewK / group;
   return 1024 + stages * (g.R * 64 + kFewTile * 4 * (few_stride(per) + (g.zeros ? few_zstride(per) : 0))) +
-         g.nk * 4 * (g.rows0 + g.rows1) * 64 + kFewWarps / 2 * 8 * nt * 32 * 4 + static_cast<int>(sizeof(FewBars));
+         (g.rows0 + g.rows1) * (g.nk * 256 + 64) + g.nk * per * nt * 64 + kFewWarps / 2 * 8 * nt * 32 * 4 + static_cast<int>(sizeof(FewBars));
 }
 
 // Launches the call here if its states fit beside a ring of four stages
