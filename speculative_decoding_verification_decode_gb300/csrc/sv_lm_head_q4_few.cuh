@@ -31,7 +31,7 @@
 //   - Codes come by TMA, scales by cp.async from two warps of their own, in
 //     one ring of stages.
 //   - The two stage parities' sums are joined through shared memory at the
-//     tile's end, in a fixed order.
+//     tile's end, in a fixed order, pair by pair of warps.
 // Every mbarrier wait is bounded; one that gives up sets bit 0 of *err, and
 // the warps then run through their remaining barriers without computing.
 #pragma once
@@ -62,14 +62,11 @@ __device__ __forceinline__ bool few_wait(FewBars& bars, uint64_t* bar, uint32_t 
   return false;
 }
 
-template <int ID>
-__device__ __forceinline__ void bar_sync() {
-  asm volatile("bar.sync %0, %1;" ::"n"(ID), "n"(32 * kFewWarps) : "memory");
-}
-template <int ID>
-__device__ __forceinline__ void bar_arrive() {
-  asm volatile("bar.arrive %0, %1;" ::"n"(ID), "n"(32 * kFewWarps) : "memory");
-}
+__device__ __forceinline__ void all_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kFewWarps) : "memory"); }
+// The two warps of row group `rw`.
+__device__ __forceinline__ void pair_sync(int rw) { asm volatile("bar.sync %0, 64;" ::"r"(rw + 2) : "memory"); }
+// 2^e, -126 <= e <= 127.
+__device__ __forceinline__ float power(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
@@ -137,8 +134,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
   const int frag_row = g.nk * 256 + 64;  // (64 more: neighbouring rows in other banks)
   unsigned char* frag = smem + g.stages * stage_bytes;                              // [row][stage][operand 0..3][4 x 16 bytes]
   float* sums = reinterpret_cast<float*>(frag + rows * frag_row);                   // [group][NT][lane quarter][4]
-  float* red = sums + g.nk * kPer * NT * 16;                                        // [row warp][8 NT][32]
-  uint32_t* sbuf = reinterpret_cast<uint32_t*>(red + kFewWarps / 2 * 8 * NT * 32);  // [slot][tile row][kStride]
+  float* red = sums + g.nk * kPer * NT * 16;                                        // [row warp][parity][4 NT][32]
+  uint32_t* sbuf = reinterpret_cast<uint32_t*>(red + kFewWarps * NT * 128);  // [slot][tile row][kStride]
   uint32_t* zbuf = sbuf + g.stages * kFewTile * kStride;
   FewBars& bars = *reinterpret_cast<FewBars*>(zbuf + g.stages * kFewTile * kZStride);
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -205,20 +202,24 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
     return;
   }
 
-  // ---- the states as operands; columns past dim are 0.  A warp has a row.
-  if (warp < rows) {
-    const uint4* src = warp < g.rows0 ? f.s0 + static_cast<long long>(warp) * (g.d / 8)
-                                      : f.s1 + static_cast<long long>(warp - g.rows0) * (g.d / 8);
-    const int chunks = g.d / 8;
-    const bool bf16 = f.bf16;
-    auto value = [&](uint32_t w, int high) {
-      w = high ? w >> 16 : w & 0xFFFFu;
-      return bf16 ? __uint_as_float(w << 16) : __half2float(__ushort_as_half(static_cast<unsigned short>(w)));
-    };
-    // the power of two that takes the row's largest finite state to 2^14
+  // ---- the states as operands; columns past dim are 0.  The sixteen warps
+  // share the rows evenly, and keep several loads in flight: everything waits
+  // for this.
+  const int shares = rows > 8 ? 1 : rows > 4 ? 2 : rows > 2 ? 4 : rows > 1 ? 8 : 16;  // warps per row
+  const int my_row = warp / shares, from_j = warp % shares * 32 + lane, step_j = 32 * shares;
+  const bool bf16 = f.bf16;
+  const int chunks = g.d / 8;
+  const uint4* src = nullptr;
+  uint32_t* tops = reinterpret_cast<uint32_t*>(red);  // the rows' largest finite states (until the first tile ends)
+  if (threadIdx.x < 16) tops[threadIdx.x] = 0;
+  all_sync();
+  if (my_row < rows) {
+    src = my_row < g.rows0 ? f.s0 + static_cast<long long>(my_row) * chunks
+                           : f.s1 + static_cast<long long>(my_row - g.rows0) * chunks;
     const uint32_t limit = bf16 ? 0x7F80u : 0x7C00u;
     uint32_t top = 0;
-    for (int j = lane; j < chunks; j += 32) {
+#pragma unroll 8
+    for (int j = from_j; j < chunks; j += step_j) {
       const uint4 x = __ldg(src + j);
       const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
@@ -229,10 +230,19 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
       }
     }
     top = __reduce_max_sync(0xFFFFFFFFu, top);
-    const int shift = top ? 14 - ilogbf(value(top, 0)) : 0;
-    if (lane == 0) red[warp] = static_cast<float>(shift);  // until the first tile ends
-    for (int j = lane; j < g.nk * 16; j += 32) {  // (nk * 16 a multiple of 16: half a warp stays together)
-      const unsigned mask = __activemask();
+    if (lane == 0) atomicMax(&tops[my_row], top);
+  }
+  all_sync();
+  // the power of two that takes a row's largest finite state to 2^14
+  auto value = [&](uint32_t half_word) {
+    return bf16 ? __uint_as_float(half_word << 16) : __half2float(__ushort_as_half(static_cast<unsigned short>(half_word)));
+  };
+  auto shift_of = [&](int r) { return tops[r] ? 14 - ilogbf(value(tops[r])) : 0; };
+  if (my_row < rows) {
+    const int shift = shift_of(my_row);
+    const float up_a = power(shift / 2), up_b = power(shift - shift / 2);
+#pragma unroll 4
+    for (int j = from_j; j < g.nk * 16; j += step_j) {
       uint4 x = make_uint4(0, 0, 0, 0);
       if (j < chunks) x = __ldg(src + j);
       const uint32_t w[4] = {x.x, x.y, x.z, x.w};
@@ -240,7 +250,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
       float sum = 0.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        h[i] = __float2half_rn(scalbnf(value(w[i / 2], i % 2), shift - (i % 2) * 4));
+        h[i] = __float2half_rn(value(i % 2 ? w[i / 2] >> 16 : w[i / 2] & 0xFFFFu) * up_a * up_b * (i % 2 ? 0.0625f : 1.f));
         sum += __half2float(h[i]) * (i % 2 ? 16.f : 1.f);
       }
       uint32_t y[4];
@@ -252,19 +262,21 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
       // which lane quarter multiplies these 8 columns, and as its how manieth word
       const int c = j % 16, q = G == 128 ? c / 4 : G == 64 ? c % 8 / 2 : c % 4,
                 i = G == 128 ? c % 4 : G == 64 ? c / 8 * 2 + c % 2 : c / 4;
-      *reinterpret_cast<uint4*>(frag + warp * frag_row + j / 16 * 256 + i * 64 + q * 16) = make_uint4(y[0], y[1], y[2], y[3]);
+      *reinterpret_cast<uint4*>(frag + my_row * frag_row + j / 16 * 256 + i * 64 + q * 16) = make_uint4(y[0], y[1], y[2], y[3]);
       // the group's sum, in the units of the products, with the zero of 8 or 1
+      // (its lanes are neighbours in one half of a warp, and in or out together)
+      const unsigned half_warp = 0xFFFFu << (lane & 16);
 #pragma unroll
-      for (int o = 1; o < G / 8; o *= 2) sum += __shfl_xor_sync(mask, sum, o);
+      for (int o = 1; o < G / 8; o *= 2) sum += __shfl_xor_sync(half_warp, sum, o);
       if (j % (G / 8) == 0) {
         sum *= Z ? -0x1p-24f : -0x1p-21f;
-        float* to = sums + (j / (G / 8) * NT + warp / 8) * 16 + warp % 8 / 2 * 4 + warp % 2;
+        float* to = sums + (j / (G / 8) * NT + my_row / 8) * 16 + my_row % 8 / 2 * 4 + my_row % 2;
         to[0] = sum;
         to[2] = sum;
       }
     }
   }
-  bar_sync<1>();
+  all_sync();
 
   const int rw = warp % 8, kh = warp / 8, gq = lane / 4, t4 = lane % 4;
   const bool active = rw * 32 < g.R;
@@ -274,9 +286,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int r = n * 8 + 2 * t4 + e;
-      back[n][e] = r < rows ? 24 - static_cast<int>(red[r]) : 0;
+      back[n][e] = r < rows ? 24 - shift_of(r) : 0;
     }
-  bar_sync<1>();
+  all_sync();
   const int swz = gq >> 1 & 3;
   const uint32_t codes0 = smem_u32(smem) + (rw * 32 + gq) * 64;
   const uint32_t srow0 = smem_u32(sbuf) + (rw * 32 + gq) * kStride * 4, zrow0 = smem_u32(zbuf) + (rw * 32 + gq) * kZStride * 4;
@@ -299,9 +311,14 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.f;
-    const long long count = static_cast<long long>(tile_no) * g.nk + kh;
-    int s = static_cast<int>(count % g.stages), use = static_cast<int>(count / g.stages & 1);
-    for (int ks = kh; ks < nk; ks += 2) {
+    // stages go to the warp groups by the parity of their count since the
+    // start, and the ring's length is even: a slot has one group for good, so
+    // a group sees every phase of its slots (a parity wait that skips one
+    // could pass on the phase before)
+    const int odd = tile_no & nk & 1;
+    const long long count = static_cast<long long>(tile_no) * nk + (kh ^ odd);
+    int s = static_cast<int>(count % stages), use = static_cast<int>(count / stages & 1);
+    for (int ks = kh ^ odd; ks < nk; ks += 2) {
       ok = __all_sync(0xFFFFFFFFu, ok && few_wait(bars, &bars.full[s], use, g.err));
       if (ok && active) {
         const uint32_t codes = codes0 + s * stage_bytes;
@@ -361,9 +378,10 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
             uint4 b[NT];
 #pragma unroll
             for (int n = 0; n < NT; ++n) b[n] = lds128(frag0[n] + ks * 256 + (j * kLen + i) * 64);
+            // (a tile's two MMAs apart: the second waits for the first)
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
-              const uint32_t lo = w[m][0][i], hi = w[m][1][i], lo8 = lo >> 8, hi8 = hi >> 8;
+              const uint32_t lo = w[m][0][i], hi = w[m][1][i];
 #pragma unroll
               for (int n = 0; n < NT; ++n) {
                 if (i == 0 && !Z)
@@ -371,9 +389,13 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
                 else
                   mma16816(part[m][n], lo & 0x000F000Fu, hi & 0x000F000Fu, lo & 0x00F000F0u, hi & 0x00F000F0u, b[n].x, b[n].y);
               }
+            }
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+              const uint32_t lo = w[m][0][i] >> 8, hi = w[m][1][i] >> 8;
 #pragma unroll
               for (int n = 0; n < NT; ++n)
-                mma16816(part[m][n], lo8 & 0x000F000Fu, hi8 & 0x000F000Fu, lo8 & 0x00F000F0u, hi8 & 0x00F000F0u, b[n].z, b[n].w);
+                mma16816(part[m][n], lo & 0x000F000Fu, hi & 0x000F000Fu, lo & 0x00F000F0u, hi & 0x00F000F0u, b[n].z, b[n].w);
             }
           }
 #pragma unroll
@@ -392,45 +414,38 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
         use ^= 1;
       }
     }
-    // join the parities; the first one's warps write the logits
-    float* mine = red + rw * 8 * NT * 32 + lane;
-    if (kh == 1) {
-      if (tile_no) bar_sync<3>();  // the last tile's sums have been read
+    // join the parities: each warp of a pair gives away one m tile's sums and
+    // finishes the other
+    float* theirs = red + (rw * 2 + 1 - kh) * NT * 128 + lane;
+    const float* mine = red + (rw * 2 + kh) * NT * 128 + lane;
 #pragma unroll
-      for (int m = 0; m < 2; ++m)
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) mine[((m * NT + n) * 4 + e) * 32] = acc[m][n][e];
-      __syncwarp();
-      bar_arrive<2>();
-    } else {
-      bar_sync<2>();
-#pragma unroll
-      for (int m = 0; m < 2; ++m)
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[m][n][e] += mine[((m * NT + n) * 4 + e) * 32];
-      __syncwarp();
-      if (t + static_cast<int>(gridDim.x) < g.tiles) bar_arrive<3>();
-      if (ok && active) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int r = n * 8 + 2 * t4 + e;
-            if (r >= rows) continue;
-            float* out = r < g.rows0 ? g.out0 + r * g.ld : g.out1 + (r - g.rows0) * g.ld;
-#pragma unroll
-            for (int m = 0; m < 2; ++m)
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const long long v = v0 + m * 16 + h * 8 + gq;
-                if (v < g.V) out[v] = scalbnf(acc[m][n][2 * h + e], back[n][e]);
-              }
-          }
+      for (int e = 0; e < 4; ++e) {
+        theirs[(n * 4 + e) * 32] = kh ? acc[0][n][e] : acc[1][n][e];
+        if (kh) acc[0][n][e] = acc[1][n][e];
       }
+    pair_sync(rw);
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[0][n][e] += mine[(n * 4 + e) * 32];
+    pair_sync(rw);  // read before the next tile's are written
+    if (ok && active) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = n * 8 + 2 * t4 + e;
+          if (r >= rows) continue;
+          float* out = r < g.rows0 ? g.out0 + r * g.ld : g.out1 + (r - g.rows0) * g.ld;
+          const float a = power(back[n][e] / 2), b = power(back[n][e] - back[n][e] / 2);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const long long v = v0 + kh * 16 + h * 8 + gq;
+            if (v < g.V) out[v] = acc[0][n][2 * h + e] * a * b;
+          }
+        }
     }
   }
 }
@@ -439,7 +454,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
 inline int few_smem(const Args& g, int group, int stages, int nt) {
   const int per = kFewK / group;
   return 1024 + stages * (g.R * 64 + kFewTile * 4 * (few_stride(per) + (g.zeros ? few_zstride(per) : 0))) +
-         (g.rows0 + g.rows1) * (g.nk * 256 + 64) + g.nk * per * nt * 64 + kFewWarps / 2 * 8 * nt * 32 * 4 + static_cast<int>(sizeof(FewBars));
+         (g.rows0 + g.rows1) * (g.nk * 256 + 64) + g.nk * per * nt * 64 + kFewWarps * nt * 128 * 4 + static_cast<int>(sizeof(FewBars));
 }
 
 // Launches the call here if its states fit beside a ring of four stages
@@ -454,7 +469,7 @@ sv_status start_few(Args g, bool bf16, const sv_q4_proj* proj, const void* s0, c
   g.tiles = (g.V + g.R - 1) / g.R;
   g.nk = (g.d + kFewK - 1) / kFewK;
   g.stages = kFewStages;
-  while (g.stages >= 4 && few_smem(g, G, g.stages, NT) > kFewBudget) --g.stages;
+  while (g.stages >= 4 && few_smem(g, G, g.stages, NT) > kFewBudget) g.stages -= 2;  // (even: see the kernel)
   if (g.stages < 4) return SV_ERR_UNSUPPORTED;
   CUtensorMap mw;
   if (!encode(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, proj->packed, g.V, g.d / 2, g.R, 64))
