@@ -51,12 +51,18 @@ using svk::smem_u32;
 
 constexpr int kStageK = 256;    // weights of a row per ring stage: 128 bytes
 constexpr int kMaxStages = 6;
-constexpr int kHalfCols = 256;  // tensor-memory columns of a half: `ring` operands of group / 2 columns and results of N
-constexpr int kMaxRing = 4;
+constexpr int kHalfCols = 256;  // tensor-memory columns of a half: `ring` operands of step / 2 columns and a result of N per group
+constexpr int kMaxRing = 2;
 
 __host__ __device__ constexpr int per_stage_of(int group) { return kStageK / group; }
-// Operand / result buffers that fit; two or four.
-__host__ __device__ constexpr int ring_of(int group, int n) { return group < 128 && 4 * (group / 2 + n) <= kHalfCols ? 4 : 2; }
+// Columns of W that pass between the warps and the MMA at a time: a hand-over
+// costs some 900 clocks whatever its size, so as many as the results of all
+// their groups leave room for.
+__host__ __device__ constexpr int step_of(int group, int n) { return group == 32 && n == 64 ? 64 : 128; }
+// Operand / result buffers that fit.
+__host__ __device__ constexpr int ring_of(int group, int n) {
+  return 2 * (step_of(group, n) / 2 + step_of(group, n) / group * n) <= kHalfCols ? 2 : 1;
+}
 
 struct Args {
   const void* scales;
@@ -121,16 +127,18 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
       : "memory");
 }
 
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(v[0]),
-               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-               : "memory");
-}
-
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* v) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
                : "r"(taddr));
+}
+
+// (a0, a1) += s (x0, x1), both in one instruction.
+__device__ __forceinline__ void fma2(float& a0, float& a1, float s, float x0, float x1) {
+  asm("{\n .reg .b64 a, x, s;\n mov.b64 a, {%0, %1};\n mov.b64 x, {%3, %4};\n mov.b64 s, {%2, %2};\n"
+      " fma.rn.f32x2 a, s, x, a;\n mov.b64 {%0, %1}, a;\n}"
+      : "+f"(a0), "+f"(a1)
+      : "f"(s), "f"(x0), "f"(x1));
 }
 
 __device__ __forceinline__ void give_up(Bars& bars, unsigned* err) {
@@ -267,7 +275,8 @@ __global__ void __launch_bounds__(288 * H + 64, H == 1 ? 2 : 1)
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = bars.tmem;
   constexpr int per_stage = per_stage_of(G), ring = ring_of(G, N);
-  constexpr int a_cols = G / 2, d_at = ring * a_cols;  // a half's columns: operands, then results
+  constexpr int kStep = step_of(G, N), kGroups = kStep / G, kSteps = kStageK / kStep;
+  constexpr int a_cols = kStep / 2, d_cols = kGroups * N, d_at = ring * a_cols;  // a half's columns: operands, then results
 
   if (warp == kWarps + kHelp) {
     // ---- producer: one thread
@@ -353,19 +362,20 @@ __global__ void __launch_bounds__(288 * H + 64, H == 1 ? 2 : 1)
             const uint32_t b_lo = desc_lo(smem_u32(smem + s * stage_bytes) + w_bytes);
             const int n = min(per_stage, g.G - ks * per_stage);
 #pragma unroll
-            for (int i = 0; i < per_stage; ++i) {
-              if (!ok || i >= n) break;
+            for (int i = 0; i < kSteps; ++i) {
+              if (!ok || i * kGroups >= n) break;
 #pragma unroll
               for (int h = 0; h < H; ++h) {
                 ok = ok && wait_or_abort(bars, &bars.a_full[h][buf], turn_no & 1, g.err);
                 if (!ok) break;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                const uint32_t a = tmem + h * kHalfCols + buf * a_cols, dd = tmem + h * kHalfCols + d_at + buf * N;
+                const uint32_t a = tmem + h * kHalfCols + buf * a_cols, dd = tmem + h * kHalfCols + d_at + buf * d_cols;
 #pragma unroll
-                for (int kk = 0; kk < G / 16; ++kk) {
+                for (int kk = 0; kk < kStep / 16; ++kk) {
                   constexpr int kChunk = N * 128 / 16;  // 64 columns of the states, in descriptor units
-                  const int k = i * G + kk * 16;
-                  mma_ts(dd, a + kk * 8, desc_of(b_lo + (k / 64) * kChunk + (k % 64) / 8), kIdesc, kk ? 1u : 0u);
+                  const int k = i * kStep + kk * 16;
+                  mma_ts(dd + kk * 16 / G * N, a + kk * 8, desc_of(b_lo + (k / 64) * kChunk + (k % 64) / 8), kIdesc,
+                         kk * 16 % G ? 1u : 0u);
                 }
                 mma_commit(&bars.d_full[h][buf]);
               }
@@ -390,7 +400,7 @@ __global__ void __launch_bounds__(288 * H + 64, H == 1 ? 2 : 1)
     const int row = min(in_tile, g.R - 1);  // rows past the tile repeat its last one, unused
     const uint32_t ta = tmem + half * kHalfCols + (static_cast<uint32_t>(warp % 4 * 32) << 16) + wg * (a_cols / 2);
     const uint32_t td = tmem + half * kHalfCols + (static_cast<uint32_t>(warp % 4 * 32) << 16) + d_at + wg * (N / 2);
-    const int lag = ring - 1;  // results are added this many groups later
+    constexpr int kLag = ring - 1;  // a step's results are added this many steps later
     int s = 0, use = 0, buf = 0, turn_no = 0;
     bool ok = true;
     for (int t = blockIdx.x; ok && t < g.tiles; t += gridDim.x) {
@@ -403,19 +413,20 @@ __global__ void __launch_bounds__(288 * H + 64, H == 1 ? 2 : 1)
         float acc[N / 2];
 #pragma unroll
         for (int n = 0; n < N / 2; ++n) acc[n] = 0.f;
-        float sc[kMaxRing - 1] = {};  // scales of the groups whose results are still to be added, newest first
+        float late[kGroups] = {};  // scales of the step whose results are still to be added
         int pending = 0, rbuf = buf, rturn = turn_no;
-        auto add_oldest = [&]() {
-          const float scale = pending == 1 ? sc[0] : pending == 2 ? sc[1] : sc[2];
+        auto add = [&](const float (&scale)[kGroups]) {
           if (!__all_sync(0xFFFFFFFFu, wait_or_abort(bars, &bars.d_full[half][rbuf], rturn & 1, g.err))) return false;
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-          uint32_t d[N / 2];
 #pragma unroll
-          for (int n = 0; n < N / 2; n += 8) tmem_ld8(td + rbuf * N + n, d + n);
-          asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+          for (int p = 0; p < kGroups; ++p) {
+            uint32_t d[N / 2];
 #pragma unroll
-          for (int n = 0; n < N / 2; ++n) acc[n] = fmaf(scale, __uint_as_float(d[n]), acc[n]);
-          --pending;
+            for (int n = 0; n < N / 2; n += 8) tmem_ld8(td + rbuf * d_cols + p * N + n, d + n);
+            asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+            for (int n = 0; n < N / 2; n += 2) fma2(acc[n], acc[n + 1], scale[p], __uint_as_float(d[n]), __uint_as_float(d[n + 1]));
+          }
           if (++rbuf == ring) {
             rbuf = 0;
             ++rturn;
@@ -428,69 +439,57 @@ __global__ void __launch_bounds__(288 * H + 64, H == 1 ? 2 : 1)
           const uint32_t srow = smem_u32(sbuf) + (s * 128 * H + row) * kSWords * 4;
           const uint32_t zrow = smem_u32(zbuf) + (s * 128 * H + row) * z_words * 4 + ((z_off + ks * per_stage) & 3);
           const int n = min(per_stage, g.G - ks * per_stage);
-          float scales[per_stage];
-          if (g.scale_dtype == SV_F32) {
 #pragma unroll
-            for (int i = 0; i < per_stage; ++i) scales[i] = __uint_as_float(lds32(srow + i * 4));
-          } else {
+          for (int i = 0; i < kSteps; ++i) {
+            if (!ok || i * kGroups >= n) break;
+            float scale[kGroups];
 #pragma unroll
-            for (int i = 0; i < per_stage; ++i) scales[i] = scale16(lds16(srow + (s_off + i) * 2), g.scale_dtype);
-          }
-#pragma unroll
-          for (int i = 0; i < per_stage; ++i) {
-            if (!ok || i >= n) break;
-            const uint32_t z0 = g.zeros ? lds8(zrow + i) & 15u : 8u;
-            const uint32_t z = (z0 | z0 << 16) + Code<T>::kBase;
+            for (int p = 0; p < kGroups; ++p) {
+              const int j = i * kGroups + p;
+              const float x = g.scale_dtype == SV_F32 ? __uint_as_float(lds32(srow + j * 4)) : scale16(lds16(srow + (s_off + j) * 2), g.scale_dtype);
+              scale[p] = j < n ? x : 0.f;  // past the row's last group the codes are padding
+            }
             const uint32_t dst = ta + buf * a_cols;
-            if constexpr (a_cols == 64) {
 #pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                const uint4 q = lds128(codes + (((4 * i + 2 * wg + c) ^ (row & 7)) << 4));
-                uint32_t a[16];
-                turn<T>(q.x, z, a);
-                turn<T>(q.y, z, a + 4);
-                turn<T>(q.z, z, a + 8);
-                turn<T>(q.w, z, a + 12);
-                tmem_st16(dst + c * 16, a);
-              }
-            } else if constexpr (a_cols == 32) {
-              const uint4 q = lds128(codes + (((2 * i + wg) ^ (row & 7)) << 4));
+            for (int c = 0; c < kStep / 64; ++c) {  // 32 codes: 16 bytes
+              const int at = i * kStep / 32 + wg * (kStep / 64) + c;
+              const int j = i * kGroups + (G == 128 ? 0 : G == 64 ? (kStep == 128 ? wg : 0) : wg * (kStep / 64) + c);
+              const uint32_t z0 = g.zeros ? lds8(zrow + j) & 15u : 8u;
+              const uint32_t z = (z0 | z0 << 16) + Code<T>::kBase;
+              const uint4 q = lds128(codes + ((at ^ (row & 7)) << 4));
               uint32_t a[16];
               turn<T>(q.x, z, a);
               turn<T>(q.y, z, a + 4);
               turn<T>(q.z, z, a + 8);
               turn<T>(q.w, z, a + 12);
-              tmem_st16(dst, a);
-            } else {
-              const uint2 q = lds64(codes + ((i ^ (row & 7)) << 4) + wg * 8);
-              uint32_t a[8];
-              turn<T>(q.x, z, a);
-              turn<T>(q.y, z, a + 4);
-              tmem_st8(dst, a);
+              tmem_st16(dst + c * 16, a);
             }
             asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
             asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
             __syncwarp();
             if (lane == 0) {
               mbar_arrive_local(&bars.a_full[half][buf]);
-              if (i + 1 == n) mbar_arrive_local(&bars.empty[s]);
+              if ((i + 1) * kGroups >= n) mbar_arrive_local(&bars.empty[s]);
             }
             if (++buf == ring) {
               buf = 0;
               ++turn_no;
             }
-            if (pending == lag) ok = add_oldest();
-            sc[2] = sc[1];
-            sc[1] = sc[0];
-            sc[0] = scales[i];
-            ++pending;
+            if constexpr (kLag == 0) {
+              ok = add(scale);
+            } else {
+              if (pending) ok = add(late);
+              pending = 1;
+#pragma unroll
+              for (int p = 0; p < kGroups; ++p) late[p] = scale[p];
+            }
           }
           if (++s == g.stages) {
             s = 0;
             ++use;
           }
         }
-        while (ok && pending > 0) ok = add_oldest();
+        if (ok && pending) ok = add(late);
         if (ok && in_tile < g.R && v < g.V) {
 #pragma unroll
           for (int n = 0; n < N / 2; ++n) {
