@@ -146,10 +146,30 @@ __device__ __forceinline__ void give_up(Bars& bars, unsigned* err) {
   if (err) atomicOr(err, 1u);
 }
 
+// Some 512 polls of a phase, two instructions each: a warp that waits takes
+// its polls' issue slots from the warps that work (a loop of ten instructions
+// took half of all).
+__device__ __forceinline__ bool poll(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p, q;\n .reg .u32 n;\n mov.u32 n, 128;\n"
+      "again:\n"
+      " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n @p bra done;\n"
+      " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n @p bra done;\n"
+      " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n @p bra done;\n"
+      " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n @p bra done;\n"
+      " sub.u32 n, n, 1;\n setp.ne.u32 q, n, 0;\n @q bra again;\n"
+      "done:\n selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "n"(svk::kSuspendNs)
+      : "memory");
+  return ok != 0;
+}
+
 // A bounded wait that also gives up once another role has.
 __device__ __forceinline__ bool wait_or_abort(Bars& bars, uint64_t* bar, uint32_t parity, unsigned* err) {
-  for (uint32_t i = 0; i < svk::kWaitPolls; ++i) {
-    if (svk::mbar_try_wait(bar, parity)) return true;
+  for (uint32_t i = 0; i < svk::kWaitPolls / 512; ++i) {
+    if (poll(bar, parity)) return true;
     if (bars.abort) return false;
   }
   give_up(bars, err);
@@ -232,7 +252,8 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
 template <typename T, int N, int G, int H>
 __global__ void __launch_bounds__(288 * H + 64, H == 1 ? 2 : 1)
     q4_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap h0,
-              const __grid_constant__ CUtensorMap h1, const __grid_constant__ Args g) {
+              const __grid_constant__ CUtensorMap h1, const __grid_constant__ CUtensorMap whole,
+              const __grid_constant__ Args g) {
   constexpr int kWarps = 8 * H;  // that turn codes
   constexpr int kHelp = H;       // that fetch scales
   constexpr int kSWords = per_stage_of(G) + 1;  // 32-bit words of a row's scales in a stage (odd: no bank conflicts)
@@ -289,15 +310,21 @@ __global__ void __launch_bounds__(288 * H + 64, H == 1 ? 2 : 1)
             const uint32_t dst = smem_u32(smem + s * stage_bytes);
             mbar_arrive_expect_tx(&bars.full[s], stage_bytes);
             tma_load_2d(dst, &wmap, ks * 128, t * g.R, &bars.full[s]);
-#pragma unroll 2
-            for (int r = 0; r < N; r += 8) {  // 8 rows of one of the two row sets
-              const int v = blk * N + r;
-              const bool second = v >= g.split;
-              const CUtensorMap* map = second ? &h1 : &h0;
-              const int y = second ? v - g.split : v;
+            if (blk * N + N <= g.split) {  // the first set's rows alone, in boxes of N
 #pragma unroll
               for (int c = 0; c < kStageK / 64; ++c)
-                tma_load_2d(dst + w_bytes + c * N * 128 + r * 128, map, ks * kStageK + c * 64, y, &bars.full[s]);
+                tma_load_2d(dst + w_bytes + c * N * 128, &whole, ks * kStageK + c * 64, blk * N, &bars.full[s]);
+            } else {
+#pragma unroll 2
+              for (int r = 0; r < N; r += 8) {  // 8 rows of one of the two row sets
+                const int v = blk * N + r;
+                const bool second = v >= g.split;
+                const CUtensorMap* map = second ? &h1 : &h0;
+                const int y = second ? v - g.split : v;
+#pragma unroll
+                for (int c = 0; c < kStageK / 64; ++c)
+                  tma_load_2d(dst + w_bytes + c * N * 128 + r * 128, map, ks * kStageK + c * 64, y, &bars.full[s]);
+              }
             }
             if (++s == g.stages) {
               s = 0;
@@ -567,12 +594,13 @@ sv_status start(Args g, const sv_q4_proj* proj, const void* s0, const void* s1, 
   g.stages = (kBudget - kFixed) / stage_bytes;
   if (g.stages > kMaxStages) g.stages = kMaxStages;
   g.nk = (g.d + kStageK - 1) / kStageK;
-  CUtensorMap mw, m0, m1;
+  CUtensorMap mw, m0, m1, mn;
   const CUtensorMapDataType type =
       Code<T>::kBase == 0x43004300u ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   if (!encode(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, proj->packed, g.V, g.d / 2, g.R) ||
       !encode(&m0, type, 2, g.rows0 ? s0 : s1, g.rows0 ? g.rows0 : g.rows1, g.d, 8) ||
-      !encode(&m1, type, 2, g.rows1 ? s1 : s0, g.rows1 ? g.rows1 : g.rows0, g.d, 8))
+      !encode(&m1, type, 2, g.rows1 ? s1 : s0, g.rows1 ? g.rows1 : g.rows0, g.d, 8) ||
+      !encode(&mn, type, 2, g.rows0 ? s0 : s1, g.rows0 ? g.rows0 : g.rows1, g.d, N))
     return svh::fail(SV_ERR_ARG, "tensor map encoding failed (alignment or size)");
   const int smem = kFixed + g.stages * stage_bytes;
   static bool attr_set[64] = {false};
@@ -582,7 +610,7 @@ sv_status start(Args g, const sv_q4_proj* proj, const void* s0, const void* s1, 
     attr_set[dev] = true;
   }
   const unsigned grid = static_cast<unsigned>(g.tiles < slots ? g.tiles : slots);
-  q4_kernel<T, N, G, H><<<grid, 288 * H + 64, smem, stream>>>(mw, m0, m1, g);
+  q4_kernel<T, N, G, H><<<grid, 288 * H + 64, smem, stream>>>(mw, m0, m1, mn, g);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return svh::fail(SV_ERR_CUDA, "kernel launch: %s", cudaGetErrorString(e));
   return SV_OK;

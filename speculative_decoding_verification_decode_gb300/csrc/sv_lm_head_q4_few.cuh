@@ -53,8 +53,8 @@ struct __align__(8) FewBars {
 };
 
 __device__ __forceinline__ bool few_wait(FewBars& bars, uint64_t* bar, uint32_t parity, unsigned* err) {
-  for (uint32_t i = 0; i < svk::kWaitPolls; ++i) {
-    if (svk::mbar_try_wait(bar, parity)) return true;
+  for (uint32_t i = 0; i < svk::kWaitPolls / 512; ++i) {
+    if (poll(bar, parity)) return true;
     if (bars.abort) return false;
   }
   bars.abort = 1;
