@@ -77,7 +77,7 @@ SIGNATURES = {
     # logits, dtype, stride, scores, finished, eos, B, W, V, n, scores, parents, tokens, status, workspace, stream
     "sv_beam_select": (_i32, [_vp, _i32, _i64, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp,
                               _vp, ctypes.c_size_t, _vp]),
-    "sv_beam_reorder": (_i32, [ctypes.POINTER(BeamState), _i32, _vp, _vp, _i32, _i32, _vp, _vp]),
+    "sv_beam_reorder": (_i32, [_vp, _i32, _vp, _vp, _i32, _i32, _vp, _vp]),
     "sv_lm_head_q4_logits": (_i32, [_vp, _i32, ctypes.POINTER(Q4Proj), _i32, _i32, _i32, _vp, _i64, _vp, _vp]),
     "sv_lm_head_q4_verify": (_i32, [_vp, _vp, _i32, ctypes.POINTER(Q4Proj), _i32, _vp, _vp, _vp, _vp, _i32, _i32,
                                     _i32, _i32, _vp, _vp, _vp, _vp, ctypes.c_size_t, _u32, _vp]),

@@ -10,6 +10,7 @@ results back, which is how an end-to-end caller with host buffers uses it.
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import NamedTuple, Optional, Sequence, Union
 
 import torch
@@ -388,42 +389,34 @@ def q4_quantize(weight: torch.Tensor, group: int = 128, zeros: bool = False,
     return Q4Projection(packed.contiguous(), scale, z.to(torch.uint8) if zeros else None, group)
 
 
-class _Head:
-    """A bf16 or a 4-bit projection checked against the states' width: the
-    calls below are the same for both but for the entry point and the
-    arguments that describe the projection."""
-
-    def __init__(self, proj: Union[torch.Tensor, "Q4Projection"], m: "_Marshal"):
-        self.lib = _lib.load()
-        self.q4 = isinstance(proj, Q4Projection)
-        if not self.q4:
-            self.w = _bf16_rows(proj, m)
-            self.V, self.d = self.w.shape
-            return
-        if proj.packed.dim() != 2 or proj.packed.dtype != torch.uint8:
-            raise ValueError("packed must be uint8 [V, d / 2]")
-        self.V, self.d = proj.packed.shape[0], 2 * proj.packed.shape[1]
-        if proj.group not in (32, 64, 128):
-            raise ValueError("group must be 32, 64 or 128")
-        shape = (self.V, -(-self.d // proj.group))
-        if proj.scales.dtype not in _DTYPES or tuple(proj.scales.shape) != shape:
-            raise ValueError(f"scales must be f32, bf16 or f16 {list(shape)}")
-        if proj.zeros is not None and (proj.zeros.dtype != torch.uint8 or tuple(proj.zeros.shape) != shape):
+def _q4_arg(p: Q4Projection, dev: torch.device):
+    """(V, d, sv_q4_proj, tensors it points into) of a checked projection."""
+    packed, scales, zeros, group = p
+    if packed.dim() != 2 or packed.dtype != torch.uint8:
+        raise ValueError("packed must be uint8 [V, d / 2]")
+    V, d = packed.shape
+    d *= 2
+    if group not in (32, 64, 128):
+        raise ValueError("group must be 32, 64 or 128")
+    shape = (V, -(-d // group))
+    code = _DTYPES.get(scales.dtype)
+    if code is None or scales.shape != shape:
+        raise ValueError(f"scales must be f32, bf16 or f16 {list(shape)}")
+    if zeros is not None:
+        if zeros.dtype != torch.uint8 or zeros.shape != shape:
             raise ValueError(f"zeros must be uint8 {list(shape)}")
-        self.keep = tuple(None if t is None else m.dev(t).contiguous() for t in proj[:3])
-        self.arg = ctypes.byref(_lib.Q4Proj(*(_p(t) for t in self.keep), _DTYPES[proj.scales.dtype], proj.group))
+        zeros = _like(zeros, dev, torch.uint8)
+    packed, scales = _like(packed, dev, torch.uint8), _like(scales, dev, scales.dtype)
+    arg = _lib.Q4Proj(packed.data_ptr(), scales.data_ptr(), None if zeros is None else zeros.data_ptr(), code, group)
+    return V, d, arg, (packed, scales, zeros)
 
-    def states(self, x: torch.Tensor, m: "_Marshal") -> torch.Tensor:
-        if not self.q4:
-            x = _bf16_rows(x, m)
-        else:
-            x = m.dev(x)
-            if x.dtype not in (torch.bfloat16, torch.float16):
-                raise ValueError("states must be bfloat16 or float16")
-            x = x.reshape(-1, x.shape[-1]).contiguous()
-        if x.numel() and x.shape[1] != self.d:
-            raise ValueError("states and projection must have the same last dimension")
-        return x
+
+def _q4_states(x: torch.Tensor, d: int) -> torch.Tensor:
+    if x.dtype != torch.bfloat16 and x.dtype != torch.float16:
+        raise ValueError("states must be bfloat16 or float16")
+    if x.shape[-1] != d:
+        raise ValueError("states and projection must have the same last dimension")
+    return (x if x.dim() == 2 else x.reshape(-1, d)).contiguous()
 
 
 def lm_head_logits(states: torch.Tensor, proj: Union[torch.Tensor, Q4Projection], out: Optional[torch.Tensor] = None,
@@ -434,21 +427,24 @@ def lm_head_logits(states: torch.Tensor, proj: Union[torch.Tensor, Q4Projection]
     optional f32 ``[rows, >= V]`` device tensor with unit stride along V;
     ``err``: optional int32 ``[1]`` device word that receives bit 0 if a
     device wait gave up."""
-    m = _Marshal(states)
     if isinstance(proj, Q4Projection):
-        head = _Head(proj, m)
-        h = head.states(states, m)
-        rows, V = h.shape[0], head.V
+        if not states.is_cuda:
+            return lm_head_logits(_Marshal(states).dev(states), proj, out, err).cpu()
+        dev = states.device
+        V, d, arg, keep = _q4_arg(proj, dev)
+        h = _q4_states(states, d)
+        rows = h.shape[0]
         if out is None:
-            out = torch.empty((rows, (V + 3) // 4 * 4), dtype=torch.float32, device=m.device)
+            out = torch.empty((rows, (V + 3) // 4 * 4), dtype=torch.float32, device=dev)
             if V % 4:  # rows start on 16-byte boundaries
                 out = out[:, :V]
-        elif (out.device != m.device or out.dtype != torch.float32 or out.dim() != 2 or out.shape[0] < rows
+        elif (out.device != dev or out.dtype != torch.float32 or out.dim() != 2 or out.shape[0] < rows
               or out.shape[1] < V or out.stride(1) != 1):
             raise ValueError("out must be f32 [rows, >= V] on the states' device with unit stride along V")
-        _launch(m.device, head.lib.sv_lm_head_q4_logits, h.data_ptr(), _DTYPES[h.dtype], head.arg, rows, V, head.d,
-                out.data_ptr(), max(out.stride(0), V), _p(err))
-        return out.cpu() if m.host else out
+        _launch(dev, _lib.load().sv_lm_head_q4_logits, h.data_ptr(), _DTYPES[h.dtype], arg, rows, V, d,
+                out.data_ptr(), max(out.stride(0), V), None if err is None else err.data_ptr())
+        return out
+    m = _Marshal(states)
     h = _bf16_rows(states, m)
     w = _bf16_rows(proj, m)
     if h.shape[1] != w.shape[1]:
@@ -488,17 +484,24 @@ def lm_head_verify(target_states: torch.Tensor, draft_states: torch.Tensor,
     Returns the verification results and, for device inputs, the fp32 logits
     it read (views of the workspace, valid until it is reused)."""
     m = _Marshal(target_states)
-    head = _Head(proj, m)
-    ht = head.states(target_states, m)
-    hd = head.states(draft_states, m)
-    if hd.dtype != ht.dtype:
-        raise ValueError("target and draft states must have the same dtype")
+    q4 = isinstance(proj, Q4Projection)
+    if q4:
+        V, d, arg, keep = _q4_arg(proj, m.device)
+        ht, hd = _q4_states(m.dev(target_states), d), m.dev(draft_states)
+        hd = _q4_states(hd, d) if hd.numel() else hd
+        if hd.dtype != ht.dtype:
+            raise ValueError("target and draft states must have the same dtype")
+    else:
+        ht, hd, w = _bf16_rows(target_states, m), _bf16_rows(draft_states, m), _bf16_rows(proj, m)
+        V, d = w.shape
+        if ht.shape[1] != d or (hd.numel() and hd.shape[1] != d):
+            raise ValueError("states and projection must have the same last dimension")
     tok = m.dev(draft_tokens.reshape(-1), torch.int32)
     u = m.dev(uniforms.reshape(-1), torch.float32)
     T = m.dev(temperature.reshape(-1), torch.float32)
     cu = m.dev(cu_k, torch.int32)
     B, K, sum_k = _layout(ht.shape[0], tok, cu, k)
-    V, d, lib = head.V, head.d, head.lib
+    lib = _lib.load()
     need = int(lib.sv_lm_head_workspace_size(B, sum_k, V))
     if workspace is None or workspace.numel() * workspace.element_size() < need:
         workspace = lm_head_workspace(B, sum_k, V, m.device)
@@ -506,10 +509,10 @@ def lm_head_verify(target_states: torch.Tensor, draft_states: torch.Tensor,
     with torch.cuda.device(m.device):
         tail = (d, _p(T), _p(tok), _p(u), _p(cu), B, K, sum_k, V, _p(n), _p(nxt), _p(st), _p(workspace),
                 workspace.numel() * workspace.element_size(), flags, m.stream())
-        if head.q4:
-            _check(lib.sv_lm_head_q4_verify(_p(ht), _p(hd), _DTYPES[ht.dtype], head.arg, *tail))
+        if q4:
+            _check(lib.sv_lm_head_q4_verify(_p(ht), _p(hd), _DTYPES[ht.dtype], arg, *tail))
         else:
-            _check(lib.sv_lm_head_verify(_p(ht), _p(hd), _p(head.w), *tail))
+            _check(lib.sv_lm_head_verify(_p(ht), _p(hd), _p(w), *tail))
     res = m.finish(VerifyResult(n, nxt, st))
     lt = ld = None
     if not m.host:
@@ -591,10 +594,21 @@ class BeamCandidates(NamedTuple):
     status: torch.Tensor  # int32 [B]; SEQ_BAD_VALUE or 0
 
 
+@functools.lru_cache(maxsize=256)
+def _select_bytes(batch: int, beams: int, vocab: int, n: int) -> int:
+    return int(_lib.load().sv_beam_select_workspace_size(batch, beams, vocab, n))
+
+
+def _like(t: torch.Tensor, dev: torch.device, dtype: torch.dtype) -> torch.Tensor:
+    """``t`` contiguous on ``dev`` in ``dtype`` (itself where it is)."""
+    if t.dtype != dtype or t.device != dev:
+        t = t.to(device=dev, dtype=dtype)
+    return t.contiguous()
+
+
 def beam_select_workspace(batch: int, beams: int, vocab: int, n: int, device=None) -> torch.Tensor:
     """A workspace for sv_beam_select of this size (uninitialised bytes)."""
-    size = int(_lib.load().sv_beam_select_workspace_size(batch, beams, vocab, n))
-    return torch.empty(size, dtype=torch.uint8, device=device or torch.device("cuda", torch.cuda.current_device()))
+    return torch.empty(_select_bytes(batch, beams, vocab, n), dtype=torch.uint8, device=device or torch.device("cuda", torch.cuda.current_device()))
 
 
 def beam_select(logits: torch.Tensor, scores: torch.Tensor, n: Optional[int] = None,
@@ -611,24 +625,39 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, n: Optional[int] = N
     one."""
     if scores.dim() != 2:
         raise ValueError("scores must be [B, W]")
+    if not logits.is_cuda:
+        m = _Marshal(logits)
+        r = beam_select(m.dev(logits), m.dev(scores), n, m.dev(finished), eos, workspace)
+        return BeamCandidates(*(x.cpu() for x in r))
     B, W = scores.shape
-    m = _Marshal(logits)
-    dev = m.device
-    rows = _rows(m.dev(logits))
-    dtype = _DTYPES.get(rows.dtype)
+    dev, dtype = logits.device, _DTYPES.get(logits.dtype)
     if dtype is None:
         raise ValueError("logits must be float32, bfloat16 or float16")
-    R, V = rows.shape
-    if R != B * W:
-        raise ValueError(f"logits must hold one row for each of the {B} x {W} scores (got {R})")
+    if logits.dim() == 3 and logits.shape[0] == B and logits.shape[1] == W:
+        V = logits.shape[2]
+        s0, stride, s2 = logits.stride()
+        if (s2 != 1 and V > 1) or (s0 != W * stride and B > 1):
+            logits = logits.contiguous()
+            stride = V
+    else:
+        logits = _rows(logits)
+        if logits.shape[0] != B * W:
+            raise ValueError(f"logits must hold one row for each of the {B} x {W} scores (got {logits.shape[0]})")
+        V, stride = logits.shape[1], logits.stride(0)
+    if stride < V:  # one row, or rows that share memory
+        if B * W > 1 and W * B != 0:
+            logits = logits.contiguous()
+        stride = V
     if finished is not None:
         if finished.shape != scores.shape:
             raise ValueError("finished must have the shape of scores")
-        finished = m.dev(finished if finished.dtype == torch.bool else finished != 0).contiguous()
-    c = m.dev(scores, torch.float32).contiguous()
+        if finished.dtype != torch.bool:
+            finished = finished != 0
+        finished = _like(finished, dev, torch.bool)
+    scores = _like(scores, dev, torch.float32)
     n = W if n is None else int(n)
     lib = _lib.load()
-    need = lib.sv_beam_select_workspace_size(B, W, V, n)
+    need = _select_bytes(B, W, V, n)
     have = 0 if workspace is None else workspace.numel() * workspace.element_size()
     if have < need:
         workspace, have = torch.empty(need, dtype=torch.uint8, device=dev), need
@@ -637,24 +666,22 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, n: Optional[int] = N
     par = torch.empty(shape, dtype=torch.int32, device=dev)
     tok = torch.empty(shape, dtype=torch.int32, device=dev)
     st = torch.empty(B, dtype=torch.int32, device=dev)
-    _launch(dev, lib.sv_beam_select, rows.data_ptr(), dtype, max(rows.stride(0), V) if R < 2 else rows.stride(0),
-            c.data_ptr(), _p(finished), int(eos), B, W, V, n, out.data_ptr(), par.data_ptr(), tok.data_ptr(),
-            st.data_ptr(), _p(workspace), have)
-    if m.host:
-        return BeamCandidates(out.cpu(), par.cpu(), tok.cpu(), st.cpu())
+    _launch(dev, lib.sv_beam_select, logits.data_ptr(), dtype, stride, scores.data_ptr(),
+            None if finished is None else finished.data_ptr(), int(eos), B, W, V, n, out.data_ptr(), par.data_ptr(),
+            tok.data_ptr(), st.data_ptr(), None if workspace is None else workspace.data_ptr(), have)
     return BeamCandidates(out, par, tok, st)
 
 
-def _flat_stride(t: torch.Tensor, lo: int, hi: int, what: str):
+def _flat_stride(shape, strides, lo: int, hi: int, what: str):
     """Extent and stride (elements) of dimensions lo..hi-1 taken as one."""
     size, stride = 1, None
     for d in range(hi - 1, lo - 1, -1):
-        if t.shape[d] == 1:
+        if shape[d] == 1:
             continue
         if stride is None:
-            size, stride = t.shape[d], t.stride(d)
-        elif t.stride(d) == size * stride:
-            size *= t.shape[d]
+            size, stride = shape[d], strides[d]
+        elif strides[d] == size * stride:
+            size *= shape[d]
         else:
             raise ValueError(f"{what} are not addressable in place with one stride")
     return size, 0 if stride is None else stride
@@ -663,23 +690,25 @@ def _flat_stride(t: torch.Tensor, lo: int, hi: int, what: str):
 def _beam_layout(t: torch.Tensor, time_dim: Optional[int]) -> tuple:
     """The words of sv_beam_state after its pointer: four strides and sizes in
     bytes, then (segs, tokens) and (timed, 0) as pairs of 32 bits."""
-    if any(n > 1 and s == 0 for n, s in zip(t.shape, t.stride())):
-        raise ValueError("a state is a broadcast view (modified in place)")
-    e = t.element_size()
+    shape, strides, e = tuple(t.shape), t.stride(), t.element_size()
+    dims = len(shape)
+    for n, s in zip(shape, strides):
+        if s == 0 and n > 1:
+            raise ValueError("a state is a broadcast view (modified in place)")
     if time_dim is None:
-        span, k = 1, t.dim()  # the run of memory at the end of the shape, then segments of it
-        while k > 2 and (t.shape[k - 1] == 1 or t.stride(k - 1) == span):
-            span *= t.shape[k - 1]
+        span, k = 1, dims  # the run of memory at the end of the shape, then segments of it
+        while k > 2 and (shape[k - 1] == 1 or strides[k - 1] == span):
+            span *= shape[k - 1]
             k -= 1
-        if k == t.dim() and k > 2:
+        if k == dims and k > 2:
             raise ValueError("a state's last dimension must have unit stride (moved in place)")
-        segs, seg = _flat_stride(t, 2, k, "a state's dimensions after [B, W]")
-        return (t.stride(0) * e, t.stride(1) * e, seg * e, span * e, segs | 1 << 32, 0)
-    segs, seg = _flat_stride(t, 2, time_dim, "a state's dimensions between the beams and the time")
-    span, stride = _flat_stride(t, time_dim + 1, t.dim(), "a state's dimensions after the time")
-    if (span > 1 and stride != 1) or (t.shape[time_dim] > 1 and t.stride(time_dim) != span):
+        segs, seg = _flat_stride(shape, strides, 2, k, "a state's dimensions after [B, W]")
+        return (strides[0] * e, strides[1] * e, seg * e, span * e, segs | 1 << 32, 0)
+    segs, seg = _flat_stride(shape, strides, 2, time_dim, "a state's dimensions between the beams and the time")
+    span, stride = _flat_stride(shape, strides, time_dim + 1, dims, "a state's dimensions after the time")
+    if (span > 1 and stride != 1) or (shape[time_dim] > 1 and strides[time_dim] != span):
         raise ValueError("a state's tokens must be contiguous: unit stride after the time, one after another along it")
-    return (t.stride(0) * e, t.stride(1) * e, seg * e, span * e, segs | t.shape[time_dim] << 32, 1)
+    return (strides[0] * e, strides[1] * e, seg * e, span * e, segs | shape[time_dim] << 32, 1)
 
 
 def beam_reorder(states: Union[torch.Tensor, Sequence[torch.Tensor]], parents: torch.Tensor,
@@ -693,8 +722,9 @@ def beam_reorder(states: Union[torch.Tensor, Sequence[torch.Tensor]], parents: t
     all states, or one per state, None for a state without time): only the
     first ``lengths[b]`` positions along it are in use and move.  Returns the
     per-sequence status (int32 ``[B]``)."""
-    states = [states] if isinstance(states, torch.Tensor) else list(states)
-    dims = list(time_dim) if isinstance(time_dim, (list, tuple)) else [time_dim] * len(states)
+    if isinstance(states, torch.Tensor):
+        states = [states]
+    dims = time_dim if isinstance(time_dim, (list, tuple)) else [time_dim] * len(states)
     if not states or len(dims) != len(states):
         raise ValueError("at least one state is needed, and one time_dim for all or for each")
     if parents.dim() != 2:
@@ -703,11 +733,11 @@ def beam_reorder(states: Union[torch.Tensor, Sequence[torch.Tensor]], parents: t
     dev = states[0].device
     if dev.type != "cuda":
         raise ValueError("the states must be CUDA tensors (modified in place)")
-    words, layouts, seen = [], {}, set()
+    grad = torch.is_grad_enabled()
+    words, seen, layout, last = [], set(), None, None
     for t, td in zip(states, dims):
-        key = (t.shape, t.stride(), t.dtype, t.device, td)
-        layout = layouts.get(key)
-        if layout is None:  # a layer's states are alike: their layout is worked out once
+        key = (t.shape, t.stride(), t.dtype, td)
+        if key != last or t.device != dev:  # a layer's states are alike: one layout serves them all
             if t.device != dev or t.dim() < 2 or t.shape[0] != B or t.shape[1] != W:
                 raise ValueError(f"a state must be a CUDA tensor [{B}, {W}, ...] on {dev} (got {list(t.shape)} on {t.device})")
             d = td
@@ -717,20 +747,22 @@ def beam_reorder(states: Union[torch.Tensor, Sequence[torch.Tensor]], parents: t
                     raise ValueError("time_dim must be a dimension after the beams")
                 if lengths is None:
                     raise ValueError("time_dim needs lengths")
-            layout = layouts[key] = _beam_layout(t, d)
-        if t.requires_grad and torch.is_grad_enabled():
+            layout, last = _beam_layout(t, d), key
+        if grad and t.requires_grad:
             raise ValueError("a state requires a gradient: it is modified in place")
         p = t.data_ptr()
-        if p in seen and p:
-            raise ValueError("a state is listed twice")
-        seen.add(p)
         words.append(p)
         words.extend(layout)
-    if lengths is not None and lengths.numel() != B:
-        raise ValueError("lengths must be [B]")
-    par = parents.to(device=dev, dtype=torch.int32).contiguous()
-    ln = None if lengths is None else lengths.reshape(-1).to(device=dev, dtype=torch.int32).contiguous()
+        if p:
+            if p in seen:
+                raise ValueError("a state is listed twice")
+            seen.add(p)
+    parents = _like(parents, dev, torch.int32)
+    if lengths is not None:
+        if lengths.numel() != B:
+            raise ValueError("lengths must be [B]")
+        lengths = _like(lengths, dev, torch.int32)
     st = torch.empty(B, dtype=torch.int32, device=dev)
-    descs = ctypes.cast((ctypes.c_int64 * len(words))(*words), ctypes.POINTER(_lib.BeamState))
-    _launch(dev, _lib.load().sv_beam_reorder, descs, len(states), par.data_ptr(), _p(ln), B, W, st.data_ptr())
+    _launch(dev, _lib.load().sv_beam_reorder, (ctypes.c_int64 * len(words))(*words), len(states), parents.data_ptr(),
+            None if lengths is None else lengths.data_ptr(), B, W, st.data_ptr())
     return st
