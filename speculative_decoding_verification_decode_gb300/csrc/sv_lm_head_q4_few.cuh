@@ -210,6 +210,13 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
   const bool bf16 = f.bf16;
   const int chunks = g.d / 8;
   const uint4* src = nullptr;
+  // columns 8 j .. of row r: which lane quarter multiplies them, and as its
+  // how manieth word
+  auto place = [&](int r, int j) {
+    const int c = j % 16, q = G == 128 ? c / 4 : G == 64 ? c % 8 / 2 : c % 4,
+              i = G == 128 ? c % 4 : G == 64 ? c / 8 * 2 + c % 2 : c / 4;
+    return frag + r * frag_row + j / 16 * 256 + i * 64 + q * 16;
+  };
   uint32_t* tops = reinterpret_cast<uint32_t*>(red);  // the rows' largest finite states (until the first tile ends)
   if (threadIdx.x < 16) tops[threadIdx.x] = 0;
   all_sync();
@@ -219,8 +226,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
     const uint32_t limit = bf16 ? 0x7F80u : 0x7C00u;
     uint32_t top = 0;
 #pragma unroll 8
-    for (int j = from_j; j < chunks; j += step_j) {
-      const uint4 x = __ldg(src + j);
+    for (int j = from_j; j < g.nk * 16; j += step_j) {  // first as they are, for their largest
+      uint4 x = make_uint4(0, 0, 0, 0);
+      if (j < chunks) x = __ldg(src + j);
       const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -228,6 +236,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
         if (lo < limit) top = max(top, lo);
         if (hi < limit) top = max(top, hi);
       }
+      *reinterpret_cast<uint4*>(place(my_row, j)) = x;
     }
     top = __reduce_max_sync(0xFFFFFFFFu, top);
     if (lane == 0) atomicMax(&tops[my_row], top);
@@ -240,31 +249,30 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
   auto shift_of = [&](int r) { return tops[r] ? 14 - ilogbf(value(tops[r])) : 0; };
   if (my_row < rows) {
     const int shift = shift_of(my_row);
-    const float up_a = power(shift / 2), up_b = power(shift - shift / 2);
+    const int more = shift > 126 ? shift - 126 : 0;  // (tiny bf16 rows: two factors)
+    const float first = power(more), up = power(shift - more), up16 = up * 0.0625f;
 #pragma unroll 4
     for (int j = from_j; j < g.nk * 16; j += step_j) {
-      uint4 x = make_uint4(0, 0, 0, 0);
-      if (j < chunks) x = __ldg(src + j);
+      unsigned char* at = place(my_row, j);
+      const uint4 x = *reinterpret_cast<const uint4*>(at);
       const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-      __half h[8];
-      float sum = 0.f;
+      float h[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        h[i] = __float2half_rn(value(i % 2 ? w[i / 2] >> 16 : w[i / 2] & 0xFFFFu) * up_a * up_b * (i % 2 ? 0.0625f : 1.f));
-        sum += __half2float(h[i]) * (i % 2 ? 16.f : 1.f);
+        float v = value(i % 2 ? w[i / 2] >> 16 : w[i / 2] & 0xFFFFu);
+        if (more) v *= first;
+        h[i] = v * (i % 2 ? up16 : up);
       }
       uint32_t y[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const __half2 p = __halves2half2(h[i], h[i + 4]);
+        const __half2 p = __floats2half2_rn(h[i], h[i + 4]);
         y[i] = *reinterpret_cast<const uint32_t*>(&p);
       }
-      // which lane quarter multiplies these 8 columns, and as its how manieth word
-      const int c = j % 16, q = G == 128 ? c / 4 : G == 64 ? c % 8 / 2 : c % 4,
-                i = G == 128 ? c % 4 : G == 64 ? c / 8 * 2 + c % 2 : c / 4;
-      *reinterpret_cast<uint4*>(frag + my_row * frag_row + j / 16 * 256 + i * 64 + q * 16) = make_uint4(y[0], y[1], y[2], y[3]);
+      *reinterpret_cast<uint4*>(at) = make_uint4(y[0], y[1], y[2], y[3]);
       // the group's sum, in the units of the products, with the zero of 8 or 1
       // (its lanes are neighbours in one half of a warp, and in or out together)
+      float sum = fmaf(16.f, (h[1] + h[3]) + (h[5] + h[7]), (h[0] + h[2]) + (h[4] + h[6]));
       const unsigned half_warp = 0xFFFFu << (lane & 16);
 #pragma unroll
       for (int o = 1; o < G / 8; o *= 2) sum += __shfl_xor_sync(half_warp, sum, o);
@@ -297,6 +305,10 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
   for (int n = 0; n < NT; ++n) frag0[n] = smem_u32(frag) + min(n * 8 + gq, rows - 1) * frag_row + t4 * 16;
   const int scale_dtype = g.scale_dtype, G_all = g.G, nk = g.nk, stages = g.stages;
   const uint32_t sums0 = smem_u32(sums) + t4 * 16;
+  auto release = [&](int slot) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive_local(&bars.empty[slot]);
+  };
   bool ok = true;
   int tile_no = 0;
   for (int t = blockIdx.x; t < g.tiles; t += gridDim.x, ++tile_no) {
@@ -359,6 +371,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
             from[n][0] = __uint_as_float(x.x), from[n][1] = __uint_as_float(x.y);
             from[n][2] = __uint_as_float(x.z), from[n][3] = __uint_as_float(x.w);
           }
+          // groups of 128: everything the warp needs of the slot is in registers
+          if constexpr (kPer == 1 && !Z) release(s);
           float part[2][NT][4];
 #pragma unroll
           for (int m = 0; m < 2; ++m) {
@@ -406,8 +420,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
               for (int e = 0; e < 4; ++e) acc[m][n][e] = fmaf(scale[m][e / 2], part[m][n][e], acc[m][n][e]);
         }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive_local(&bars.empty[s]);
+      if (!(kPer == 1 && !Z && ok && active)) release(s);
       s += 2;
       if (s >= stages) {
         s -= stages;
