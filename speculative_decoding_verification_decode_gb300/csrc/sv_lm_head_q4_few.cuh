@@ -225,18 +225,24 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
                            : f.s1 + static_cast<long long>(my_row - g.rows0) * chunks;
     const uint32_t limit = bf16 ? 0x7F80u : 0x7C00u;
     uint32_t top = 0;
-#pragma unroll 8
-    for (int j = from_j; j < g.nk * 16; j += step_j) {  // first as they are, for their largest
-      uint4 x = make_uint4(0, 0, 0, 0);
-      if (j < chunks) x = __ldg(src + j);
-      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    constexpr int kAhead = 8;  // loads in flight, whatever the branches below
+    for (int j0 = from_j; j0 < g.nk * 16; j0 += kAhead * step_j) {  // first as they are, for their largest
+      uint4 x[kAhead];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t lo = w[i] & 0x7FFFu, hi = w[i] >> 16 & 0x7FFFu;
-        if (lo < limit) top = max(top, lo);
-        if (hi < limit) top = max(top, hi);
+      for (int k = 0; k < kAhead; ++k) x[k] = __ldg(src + min(j0 + k * step_j, chunks - 1));
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int j = j0 + k * step_j;
+        if (j >= chunks) x[k] = make_uint4(0, 0, 0, 0);
+        const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t lo = w[i] & 0x7FFFu, hi = w[i] >> 16 & 0x7FFFu;
+          if (lo < limit) top = max(top, lo);
+          if (hi < limit) top = max(top, hi);
+        }
+        if (j < g.nk * 16) *reinterpret_cast<uint4*>(place(my_row, j)) = x[k];
       }
-      *reinterpret_cast<uint4*>(place(my_row, j)) = x;
     }
     top = __reduce_max_sync(0xFFFFFFFFu, top);
     if (lane == 0) atomicMax(&tops[my_row], top);
