@@ -7,6 +7,13 @@
 // touches those bytes, so the permutation with repetitions needs no second
 // buffer, no order among the slots and no barrier.  A slot that keeps its
 // parent costs nothing.
+//
+// That wants 16-byte accesses: the bytes in flight carry a copy (151 MB whose
+// beams lie 4 bytes off one another took 69 us with one 4-byte register per
+// access, 49 with four times as many).  Where addresses or extents forbid them,
+// a CTA owns a range of columns instead: it brings the range of every parent to
+// shared memory in the aligned 16-byte blocks that hold it, waits, and writes
+// every moving slot in its own aligned blocks, put together from 32-bit words.
 #include <cuda_runtime.h>
 
 #include "../../include/sv_beam.h"
@@ -15,15 +22,20 @@
 namespace svb {
 
 constexpr int kThreads = 256;
+constexpr int kStageBytes = 96 * 1024;  // shared memory of the staged path: two CTAs per SM
 constexpr int kStates = 48;    // per launch: their descriptions are kernel parameters
-constexpr int kColBytes = 65536;  // bytes of one segment that a CTA takes (of every beam)
+// Bytes of one segment that a CTA takes (of every beam): large ones where there
+// are many (few CTAs to start), small ones where a handful of large ones would
+// leave SMs without work at the end (151 MB in 420 large ones: 44 us).
+constexpr int kLargeChunk = 65536, kSmallChunk = 16384;
+constexpr long long kManyCtas = 152 * 2 * 8;
 
 struct State {
   char* data;
   long long seq, beam, seg;  // strides, bytes
   long long token_bytes;
   int segs, tokens, timed;
-  int unit;    // bytes of one access: divides every address, stride and extent
+  int unit;    // bytes that divide every address, stride and extent; 16 at most
   int chunks;  // CTAs per segment
   unsigned first;  // first CTA of this state
 };
@@ -33,7 +45,7 @@ struct Params {
   const int* parents;
   const int* lengths;
   unsigned* status;  // NULL: another launch writes it
-  int n, B, W, min_tokens, status_ctas;
+  int n, B, W, min_tokens, status_ctas, chunk_bytes;
 };
 
 // Columns lo + tid, lo + tid + kThreads, ... < hi of one segment, M moves at
@@ -58,27 +70,81 @@ __device__ __forceinline__ void move_columns(char* base, const long long* src, c
   }
 }
 
-// 64 registers of data per thread whatever the number of moves; more moves
-// than fit at this access width take a narrower one.
-template <typename U>
-__device__ __forceinline__ void move_all(char* base, const long long* src, const long long* dst, int m, long long lo,
-                                         long long hi) {
+// Bytes lo..hi of one segment in 16-byte accesses: 64 registers of data per
+// thread whatever the number of moves; more moves take narrower accesses.
+__device__ __forceinline__ void move_aligned(char* base, const long long* src, const long long* dst, int m,
+                                             long long lo, long long hi) {
   if (m <= 2)
-    move_columns<U, 2, 8>(base, src, dst, m, lo, hi);
+    move_columns<uint4, 2, 8>(base, src, dst, m, lo / 16, hi / 16);
   else if (m <= 4)
-    move_columns<U, 4, 4>(base, src, dst, m, lo, hi);
+    move_columns<uint4, 4, 4>(base, src, dst, m, lo / 16, hi / 16);
   else if (m <= 8)
-    move_columns<U, 8, 2>(base, src, dst, m, lo, hi);
+    move_columns<uint4, 8, 2>(base, src, dst, m, lo / 16, hi / 16);
   else if (m <= 16)
-    move_columns<U, 16, 1>(base, src, dst, m, lo, hi);
-  else if constexpr (sizeof(U) == 16)
-    m <= 32 ? move_columns<uint2, 32, 1>(base, src, dst, m, 2 * lo, 2 * hi)
-            : move_columns<unsigned, 64, 1>(base, src, dst, m, 4 * lo, 4 * hi);
-  else if constexpr (sizeof(U) == 8)
-    m <= 32 ? move_columns<uint2, 32, 1>(base, src, dst, m, lo, hi)
-            : move_columns<unsigned, 64, 1>(base, src, dst, m, 2 * lo, 2 * hi);
+    move_columns<uint4, 16, 1>(base, src, dst, m, lo / 16, hi / 16);
+  else if (m <= 32)
+    move_columns<uint2, 32, 1>(base, src, dst, m, lo / 8, hi / 8);
   else
-    move_columns<U, 64, 1>(base, src, dst, m, lo, hi);
+    move_columns<unsigned, 64, 1>(base, src, dst, m, lo / 4, hi / 4);
+}
+
+// Bytes lo..hi of one segment at any alignment, through shared memory.  The
+// blocks at a range's ends may hold neighbours' bytes; those are not used.
+__device__ __noinline__ void move_staged(char* base, const long long* src, const long long* dst, int m, long long lo,
+                                         long long hi, int unit) {
+  extern __shared__ __align__(16) unsigned char stage[];
+  const int room = kStageBytes / m / 16 * 16;  // per move, the blocks at both ends included
+  for (long long at = lo; at < hi; at += room - 32) {
+    const int bytes = static_cast<int>(hi - at < room - 32 ? hi - at : room - 32);
+    for (int j = 0; j < m; ++j) {
+      const uintptr_t from = reinterpret_cast<uintptr_t>(base) + src[j] + at;
+      const uintptr_t first = from & ~static_cast<uintptr_t>(15);
+      const int blocks = static_cast<int>((from + bytes - first + 15) / 16);
+      const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(stage + j * room));
+      for (int k = threadIdx.x; k < blocks; k += kThreads)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + 16 * k), "l"(first + 16 * k) : "memory");
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
+    for (int j = 0; j < m; ++j) {
+      const uintptr_t from = reinterpret_cast<uintptr_t>(base) + src[j] + at;
+      const uintptr_t to = reinterpret_cast<uintptr_t>(base) + dst[j] + at, end = to + bytes;
+      const uintptr_t first = to & ~static_cast<uintptr_t>(15);
+      const unsigned char* held = stage + j * room + (from & 15);  // the byte for `to`
+      const int blocks = static_cast<int>((end - first + 15) / 16);
+      for (int k = threadIdx.x; k < blocks; k += kThreads) {
+        const uintptr_t p = first + 16 * static_cast<uintptr_t>(k);
+        if (p >= to && p + 16 <= end) {
+          const unsigned char* q = held + (p - to);
+          const unsigned o = static_cast<unsigned>(reinterpret_cast<uintptr_t>(q) & 3);
+          const unsigned* w = reinterpret_cast<const unsigned*>(q - o);
+          uint4 v;
+          if (o == 0) {
+            v = make_uint4(w[0], w[1], w[2], w[3]);
+          } else {
+            v.x = __funnelshift_r(w[0], w[1], 8 * o);
+            v.y = __funnelshift_r(w[1], w[2], 8 * o);
+            v.z = __funnelshift_r(w[2], w[3], 8 * o);
+            v.w = __funnelshift_r(w[3], w[4], 8 * o);
+          }
+          *reinterpret_cast<uint4*>(p) = v;
+        } else {
+          for (uintptr_t x = p > to ? p : to; x < p + 16 && x < end; x += unit) {
+            const unsigned char* q = held + (x - to);
+            if (unit == 8)
+              *reinterpret_cast<uint2*>(x) = *reinterpret_cast<const uint2*>(q);
+            else if (unit == 4)
+              *reinterpret_cast<unsigned*>(x) = *reinterpret_cast<const unsigned*>(q);
+            else if (unit == 2)
+              *reinterpret_cast<unsigned short*>(x) = *reinterpret_cast<const unsigned short*>(q);
+            else
+              *reinterpret_cast<unsigned char*>(x) = *q;
+          }
+        }
+      }
+    }
+    __syncthreads();  // read before the next range arrives
+  }
 }
 
 __device__ __forceinline__ bool sequence_ok(const Params& P, int b) {
@@ -91,7 +157,7 @@ __device__ __forceinline__ bool sequence_ok(const Params& P, int b) {
   return true;
 }
 
-__global__ void __launch_bounds__(kThreads) reorder_kernel(const __grid_constant__ Params P) {
+__global__ void __launch_bounds__(kThreads, 2) reorder_kernel(const __grid_constant__ Params P) {
   __shared__ long long src[SV_BEAM_MAX_BEAMS], dst[SV_BEAM_MAX_BEAMS];
   __shared__ int s_moves;
   unsigned cta = blockIdx.x;
@@ -111,10 +177,9 @@ __global__ void __launch_bounds__(kThreads) reorder_kernel(const __grid_constant
   const int b = static_cast<int>(cta / static_cast<unsigned>(S.segs));
 
   const int len = S.timed ? P.lengths[b] : S.tokens;
-  const long long per = kColBytes / S.unit;
-  const long long lo = chunk * per;
-  long long hi = static_cast<long long>(len) * S.token_bytes / S.unit;
-  if (hi > lo + per) hi = lo + per;
+  const long long lo = static_cast<long long>(chunk) * P.chunk_bytes;
+  long long hi = static_cast<long long>(len) * S.token_bytes;
+  if (hi > lo + P.chunk_bytes) hi = lo + P.chunk_bytes;
   if (lo >= hi) return;  // also a negative length
   // the sequence's moves, by the first warp
   if (threadIdx.x < 32) {
@@ -139,13 +204,10 @@ __global__ void __launch_bounds__(kThreads) reorder_kernel(const __grid_constant
   const int m = s_moves;
   if (m == 0) return;
   char* base = S.data + b * S.seq + seg * S.seg;
-  switch (S.unit) {
-    case 16: move_all<uint4>(base, src, dst, m, lo, hi); break;
-    case 8: move_all<uint2>(base, src, dst, m, lo, hi); break;
-    case 4: move_all<unsigned>(base, src, dst, m, lo, hi); break;
-    case 2: move_all<unsigned short>(base, src, dst, m, lo, hi); break;
-    default: move_all<unsigned char>(base, src, dst, m, lo, hi); break;
-  }
+  if (S.unit == 16)
+    move_aligned(base, src, dst, m, lo, hi);
+  else
+    move_staged(base, src, dst, m, lo, hi, S.unit);
 }
 
 }  // namespace svb
@@ -175,7 +237,7 @@ extern "C" sv_status sv_beam_reorder(const sv_beam_state* states, int32_t n_stat
       if ((s.segs > 1 && s.seg_stride < bytes) || (beams > 1 && s.beam_stride < bytes))
         return svh::fail(SV_ERR_ARG, "state %d: a stride is shorter than a segment", i);
     }
-    const long long chunks = (bytes + svb::kColBytes - 1) / svb::kColBytes;
+    const long long chunks = (bytes + svb::kLargeChunk - 1) / svb::kLargeChunk;
     all_ctas += chunks > 0x7FFFFFFFLL ? 0x7FFFFFFFLL : chunks * s.segs;
     if (all_ctas > 0x7FFFFFFFLL || (batch > 0 && all_ctas > 0x7FFFFFFFLL / batch))
       return svh::fail(SV_ERR_UNSUPPORTED, "the states are too large for one call");
@@ -187,6 +249,7 @@ extern "C" sv_status sv_beam_reorder(const sv_beam_state* states, int32_t n_stat
   if (batch == 0) return SV_OK;
   if (!parents || !status) return svh::fail(SV_ERR_ARG, "parents or status is NULL");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int chunk = all_ctas * batch < svb::kManyCtas ? svb::kSmallChunk : svb::kLargeChunk;
   for (int at = 0; at < n_states; at += svb::kStates) {
     svb::Params p;
     p.parents = parents;
@@ -195,9 +258,11 @@ extern "C" sv_status sv_beam_reorder(const sv_beam_state* states, int32_t n_stat
     p.B = batch;
     p.W = beams;
     p.min_tokens = min_tokens;
+    p.chunk_bytes = chunk;
     p.status_ctas = at == 0 ? (batch + svb::kThreads - 1) / svb::kThreads : 0;
     p.n = 0;
     long long ctas = 0;
+    int smem = 0;
     for (int i = at; i < n_states && i < at + svb::kStates; ++i) {
       const sv_beam_state& s = states[i];
       const long long bytes = s.tokens * s.token_bytes;
@@ -211,7 +276,7 @@ extern "C" sv_status sv_beam_reorder(const sv_beam_state* states, int32_t n_stat
       q.segs = s.segs;
       q.tokens = s.tokens;
       q.timed = s.timed != 0;
-      // the widest access that every address and extent allows
+      // what divides every address and extent
       // (a timed state may end after any token, another one only at its end)
       unsigned long long any = reinterpret_cast<uintptr_t>(s.data) | 16u |
                                static_cast<unsigned long long>(q.timed ? s.token_bytes : bytes);
@@ -219,13 +284,24 @@ extern "C" sv_status sv_beam_reorder(const sv_beam_state* states, int32_t n_stat
       if (beams > 1) any |= static_cast<unsigned long long>(s.beam_stride);
       if (s.segs > 1) any |= static_cast<unsigned long long>(s.seg_stride);
       q.unit = static_cast<int>(any & (~any + 1));
-      q.chunks = static_cast<int>((bytes + svb::kColBytes - 1) / svb::kColBytes);
+      if (q.unit < 16) smem = svb::kStageBytes;
+      q.chunks = static_cast<int>((bytes + chunk - 1) / chunk);
       q.first = static_cast<unsigned>(ctas);
       ctas += static_cast<long long>(q.chunks) * s.segs * batch;
     }
     const long long grid = ctas + p.status_ctas;
     if (grid == 0) continue;
-    svb::reorder_kernel<<<static_cast<unsigned>(grid), svb::kThreads, 0, st>>>(p);
+    if (smem) {  // the shared-memory opt-in, once per device
+      static bool attr_set[64] = {};
+      int dev = 0;
+      if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 0;
+      if (!attr_set[dev]) {
+        const cudaError_t e = cudaFuncSetAttribute(svb::reorder_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return svh::fail(SV_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+        attr_set[dev] = true;
+      }
+    }
+    svb::reorder_kernel<<<static_cast<unsigned>(grid), svb::kThreads, smem, st>>>(p);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return svh::fail(SV_ERR_CUDA, "kernel launch: %s", cudaGetErrorString(e));
   }
