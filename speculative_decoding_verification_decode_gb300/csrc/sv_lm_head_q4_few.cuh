@@ -11,7 +11,8 @@
 // here and not beyond.
 //
 //   - W rows are the MMA's 16 rows; a warp has 32 of them (two m tiles) of
-//     every other 128-column stage, sixteen warps in all.
+//     every other 128-column stage, fourteen warps in all.  A warp reads the
+//     codes of its next stage before it multiplies this one's.
 //   - Eight codes of a word make the pairs (0,4) (1,5) (2,6) (3,7), by one
 //     mask each and one shift: a code in the lowest bits of a half word IS the
 //     f16 number q 2^-24, four bits up q 2^-20 (subnormal; tensor cores take
@@ -28,7 +29,7 @@
 //     row's with the group's scale: no weight is rounded.  A lane's codes of a
 //     stage are those of whole groups (32, 16 or 8 in a row for groups of 128,
 //     64, 32), so an MMA never mixes two.
-//   - Codes come by TMA, scales by cp.async from two warps of their own, in
+//   - Codes come by TMA, scales by cp.async from a warp of their own, in
 //     one ring of stages.
 //   - The two stage parities' sums are joined through shared memory at the
 //     tile's end, in a fixed order, pair by pair of warps.
@@ -40,9 +41,10 @@
 namespace svq {
 
 constexpr int kFewK = 128;       // columns per stage: 64 bytes of a row
-constexpr int kFewTile = 256;    // rows per tile at most
-constexpr int kFewWarps = 16;    // that compute: 8 row groups x 2 stage parities
-constexpr int kFewHelp = 2;      // that fetch scales
+constexpr int kFewGroups = 7;    // row groups of a tile
+constexpr int kFewTile = 32 * kFewGroups;  // rows per tile at most
+constexpr int kFewWarps = 2 * kFewGroups;  // that compute: row groups x 2 stage parities
+constexpr int kFewHelp = 1;      // that fetches scales; with the producer sixteen warps: 128 registers each
 constexpr int kFewThreads = 32 * (kFewWarps + kFewHelp + 1);
 constexpr int kFewStages = 8;    // at most
 constexpr int kFewBudget = 227 * 1024;
@@ -202,97 +204,124 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
     return;
   }
 
-  // ---- the states as operands; columns past dim are 0.  The sixteen warps
-  // share the rows evenly, and keep several loads in flight: everything waits
-  // for this.
-  const int shares = rows > 8 ? 1 : rows > 4 ? 2 : rows > 2 ? 4 : rows > 1 ? 8 : 16;  // warps per row
-  const int my_row = warp / shares, from_j = warp % shares * 32 + lane, step_j = 32 * shares;
+  // ---- the states as operands; columns past dim are 0.  The threads share
+  // all rows' 8-column chunks evenly, several loads in flight: everything waits
+  // for this.  A half warp stays in one row and its places 16 columns apart.
   const bool bf16 = f.bf16;
-  const int chunks = g.d / 8;
-  const uint4* src = nullptr;
-  // columns 8 j .. of row r: which lane quarter multiplies them, and as its
-  // how manieth word
-  auto place = [&](int r, int j) {
-    const int c = j % 16, q = G == 128 ? c / 4 : G == 64 ? c % 8 / 2 : c % 4,
-              i = G == 128 ? c % 4 : G == 64 ? c / 8 * 2 + c % 2 : c / 4;
-    return frag + r * frag_row + j / 16 * 256 + i * 64 + q * 16;
-  };
+  const int chunks = g.d / 8, all_chunks = g.nk * 16;
   uint32_t* tops = reinterpret_cast<uint32_t*>(red);  // the rows' largest finite states (until the first tile ends)
   if (threadIdx.x < 16) tops[threadIdx.x] = 0;
+  // chunk c of a stage: which lane quarter multiplies it, and as its how manieth word
+  const int c = lane % 16, quarter = G == 128 ? c / 4 : G == 64 ? c % 8 / 2 : c % 4,
+            word = G == 128 ? c % 4 : G == 64 ? c / 8 * 2 + c % 2 : c / 4;
+  unsigned char* const my_frag = frag + word * 64 + quarter * 16;
+  const unsigned half_warp = 0xFFFFu << (lane & 16);
+  int row0 = 0, chunk0 = threadIdx.x;
+  auto step = [&](int& r, int& j) {
+    while (j >= all_chunks) {
+      j -= all_chunks;
+      ++r;
+    }
+  };
+  step(row0, chunk0);
   all_sync();
-  if (my_row < rows) {
-    src = my_row < g.rows0 ? f.s0 + static_cast<long long>(my_row) * chunks
-                           : f.s1 + static_cast<long long>(my_row - g.rows0) * chunks;
+  {
+    constexpr int kAhead = 8;
     const uint32_t limit = bf16 ? 0x7F80u : 0x7C00u;
-    uint32_t top = 0;
-    constexpr int kAhead = 8;  // loads in flight, whatever the branches below
-    for (int j0 = from_j; j0 < g.nk * 16; j0 += kAhead * step_j) {  // first as they are, for their largest
+    for (int r = row0, j = chunk0; r < rows;) {
       uint4 x[kAhead];
-#pragma unroll
-      for (int k = 0; k < kAhead; ++k) x[k] = __ldg(src + min(j0 + k * step_j, chunks - 1));
+      int rr[kAhead], jj[kAhead];
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
-        const int j = j0 + k * step_j;
-        if (j >= chunks) x[k] = make_uint4(0, 0, 0, 0);
+        rr[k] = r, jj[k] = j;
+        const int in = min(r, rows - 1);
+        const uint4* src = in < g.rows0 ? f.s0 + static_cast<long long>(in) * chunks
+                                        : f.s1 + static_cast<long long>(in - g.rows0) * chunks;
+        x[k] = __ldg(src + min(j, chunks - 1));
+        j += 32 * kFewWarps;
+        step(r, j);
+      }
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        if (rr[k] >= rows) break;
+        if (jj[k] >= chunks) x[k] = make_uint4(0, 0, 0, 0);
         const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+        uint32_t top = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const uint32_t lo = w[i] & 0x7FFFu, hi = w[i] >> 16 & 0x7FFFu;
           if (lo < limit) top = max(top, lo);
           if (hi < limit) top = max(top, hi);
         }
-        if (j < g.nk * 16) *reinterpret_cast<uint4*>(place(my_row, j)) = x[k];
+        *reinterpret_cast<uint4*>(my_frag + rr[k] * frag_row + jj[k] / 16 * 256) = x[k];
+        top = __reduce_max_sync(half_warp, top);
+        if (lane % 16 == 0) atomicMax(&tops[rr[k]], top);
       }
     }
-    top = __reduce_max_sync(0xFFFFFFFFu, top);
-    if (lane == 0) atomicMax(&tops[my_row], top);
   }
   all_sync();
   // the power of two that takes a row's largest finite state to 2^14
-  auto value = [&](uint32_t half_word) {
-    return bf16 ? __uint_as_float(half_word << 16) : __half2float(__ushort_as_half(static_cast<unsigned short>(half_word)));
+  auto shift_of = [&](int r) {
+    const uint32_t t = tops[r];
+    return t ? 14 - ilogbf(bf16 ? __uint_as_float(t << 16) : __half2float(__ushort_as_half(static_cast<unsigned short>(t)))) : 0;
   };
-  auto shift_of = [&](int r) { return tops[r] ? 14 - ilogbf(value(tops[r])) : 0; };
-  if (my_row < rows) {
-    const int shift = shift_of(my_row);
-    const int more = shift > 126 ? shift - 126 : 0;  // (tiny bf16 rows: two factors)
-    const float first = power(more), up = power(shift - more), up16 = up * 0.0625f;
-#pragma unroll 4
-    for (int j = from_j; j < g.nk * 16; j += step_j) {
-      unsigned char* at = place(my_row, j);
-      const uint4 x = *reinterpret_cast<const uint4*>(at);
-      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-      float h[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        float v = value(i % 2 ? w[i / 2] >> 16 : w[i / 2] & 0xFFFFu);
-        if (more) v *= first;
-        h[i] = v * (i % 2 ? up16 : up);
-      }
-      uint32_t y[4];
+  int shift_row = -1, shift = 0;
+#pragma unroll 1
+  for (int r = row0, j = chunk0; r < rows;) {
+    if (r != shift_row) {
+      shift = shift_of(r);
+      shift_row = r;
+    }
+    unsigned char* at = my_frag + r * frag_row + j / 16 * 256;
+    const uint4 x = *reinterpret_cast<const uint4*>(at);
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    float h[8];
+    if (bf16) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const __half2 p = __floats2half2_rn(h[i], h[i + 4]);
-        y[i] = *reinterpret_cast<const uint32_t*>(&p);
+        h[2 * i] = __uint_as_float(w[i] << 16);
+        h[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
       }
-      *reinterpret_cast<uint4*>(at) = make_uint4(y[0], y[1], y[2], y[3]);
-      // the group's sum, in the units of the products, with the zero of 8 or 1
-      // (its lanes are neighbours in one half of a warp, and in or out together)
-      float sum = fmaf(16.f, (h[1] + h[3]) + (h[5] + h[7]), (h[0] + h[2]) + (h[4] + h[6]));
-      const unsigned half_warp = 0xFFFFu << (lane & 16);
+    } else {
 #pragma unroll
-      for (int o = 1; o < G / 8; o *= 2) sum += __shfl_xor_sync(half_warp, sum, o);
-      if (j % (G / 8) == 0) {
-        sum *= Z ? -0x1p-24f : -0x1p-21f;
-        float* to = sums + (j / (G / 8) * NT + my_row / 8) * 16 + my_row % 8 / 2 * 4 + my_row % 2;
-        to[0] = sum;
-        to[2] = sum;
+      for (int i = 0; i < 4; ++i) {
+        const float2 two = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+        h[2 * i] = two.x;
+        h[2 * i + 1] = two.y;
       }
     }
+    int left = shift;
+    if (shift > 126) {  // (tiny bf16 rows: two factors)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) h[i] *= 0x1p40f;
+      left -= 40;
+    }
+    const float up = power(left), up16 = power(left - 4);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] *= i % 2 ? up16 : up;
+    uint32_t y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __half2 p = __floats2half2_rn(h[i], h[i + 4]);
+      y[i] = *reinterpret_cast<const uint32_t*>(&p);
+    }
+    *reinterpret_cast<uint4*>(at) = make_uint4(y[0], y[1], y[2], y[3]);
+    // the group's sum, in the units of the products, with the zero of 8 or 1
+    float sum = fmaf(16.f, (h[1] + h[3]) + (h[5] + h[7]), (h[0] + h[2]) + (h[4] + h[6]));
+#pragma unroll
+    for (int o = 1; o < G / 8; o *= 2) sum += __shfl_xor_sync(half_warp, sum, o);
+    if (j % (G / 8) == 0) {
+      sum *= Z ? -0x1p-24f : -0x1p-21f;
+      float* to = sums + (j / (G / 8) * NT + r / 8) * 16 + r % 8 / 2 * 4 + r % 2;
+      to[0] = sum;
+      to[2] = sum;
+    }
+    j += 32 * kFewWarps;
+    step(r, j);
   }
   all_sync();
 
-  const int rw = warp % 8, kh = warp / 8, gq = lane / 4, t4 = lane % 4;
+  const int rw = warp % kFewGroups, kh = warp / kFewGroups, gq = lane / 4, t4 = lane % 4;
   const bool active = rw * 32 < g.R;
   int back[NT][2];  // the rows' powers of two, to take back
 #pragma unroll
@@ -336,32 +365,40 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
     const int odd = tile_no & nk & 1;
     const long long count = static_cast<long long>(tile_no) * nk + (kh ^ odd);
     int s = static_cast<int>(count % stages), use = static_cast<int>(count / stages & 1);
-    for (int ks = kh ^ odd; ks < nk; ks += 2) {
-      ok = __all_sync(0xFFFFFFFFu, ok && few_wait(bars, &bars.full[s], use, g.err));
+    const int my_stages = (nk - (kh ^ odd) + 1) / 2;
+    uint32_t w[2][2][2][4];  // [this stage's, the next one's][m tile][row half][word]
+    auto fetch = [&](uint32_t (&to)[2][2][4], int slot, int phase) {
+      ok = __all_sync(0xFFFFFFFFu, ok && few_wait(bars, &bars.full[slot], phase, g.err));
+      if (!ok || !active) return;
+      const uint32_t codes = codes0 + slot * stage_bytes;
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t p = codes + (m * 16 + h * 8) * 64;
+          if constexpr (G == 128) {
+            const uint4 q = lds128(p + ((t4 ^ swz) << 4));
+            to[m][h][0] = q.x, to[m][h][1] = q.y, to[m][h][2] = q.z, to[m][h][3] = q.w;
+          } else if constexpr (G == 64) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const uint2 q = lds64(p + (((2 * j + t4 / 2) ^ swz) << 4) + t4 % 2 * 8);
+              to[m][h][2 * j] = q.x, to[m][h][2 * j + 1] = q.y;
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) to[m][h][j] = lds32(p + ((j ^ swz) << 4) + t4 * 4);
+          }
+        }
+    };
+    auto multiply = [&](const uint32_t (&w)[2][2][4], int ks, int slot) {
       if (ok && active) {
-        const uint32_t codes = codes0 + s * stage_bytes;
-        const uint32_t srow = srow0 + s * (kFewTile * kStride * 4) + (scale_dtype == SV_F32 ? 0 : (s_par + ks * kPer & 1) * 2);
-        const uint32_t zrow = zrow0 + s * (kFewTile * kZStride * 4) + (z_par + ks * kPer & 3);
+        const uint32_t srow = srow0 + slot * (kFewTile * kStride * 4) + (scale_dtype == SV_F32 ? 0 : (s_par + ks * kPer & 1) * 2);
+        const uint32_t zrow = zrow0 + slot * (kFewTile * kZStride * 4) + (z_par + ks * kPer & 3);
         const int n_groups = min(kPer, G_all - ks * kPer);
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
           if (j >= n_groups) break;
-          uint32_t w[2][2][kLen];  // [m tile][row half][word]
-#pragma unroll
-          for (int m = 0; m < 2; ++m)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint32_t p = codes + (m * 16 + h * 8) * 64;
-              if constexpr (G == 128) {
-                const uint4 q = lds128(p + ((t4 ^ swz) << 4));
-                w[m][h][0] = q.x, w[m][h][1] = q.y, w[m][h][2] = q.z, w[m][h][3] = q.w;
-              } else if constexpr (G == 64) {
-                const uint2 q = lds64(p + (((2 * j + t4 / 2) ^ swz) << 4) + t4 % 2 * 8);
-                w[m][h][0] = q.x, w[m][h][1] = q.y;
-              } else {
-                w[m][h][0] = lds32(p + ((j ^ swz) << 4) + t4 * 4);
-              }
-            }
           float scale[2][2];
           if (scale_dtype == SV_F32) {
 #pragma unroll
@@ -378,7 +415,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
             from[n][2] = __uint_as_float(x.z), from[n][3] = __uint_as_float(x.w);
           }
           // groups of 128: everything the warp needs of the slot is in registers
-          if constexpr (kPer == 1 && !Z) release(s);
+          if constexpr (kPer == 1 && !Z) release(slot);
           float part[2][NT][4];
 #pragma unroll
           for (int m = 0; m < 2; ++m) {
@@ -401,7 +438,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
             // (a tile's two MMAs apart: the second waits for the first)
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
-              const uint32_t lo = w[m][0][i], hi = w[m][1][i];
+              const uint32_t lo = w[m][0][j * kLen + i], hi = w[m][1][j * kLen + i];
 #pragma unroll
               for (int n = 0; n < NT; ++n) {
                 if (i == 0 && !Z)
@@ -412,7 +449,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
             }
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
-              const uint32_t lo = w[m][0][i] >> 8, hi = w[m][1][i] >> 8;
+              const uint32_t lo = w[m][0][j * kLen + i] >> 8, hi = w[m][1][j * kLen + i] >> 8;
 #pragma unroll
               for (int n = 0; n < NT; ++n)
                 mma16816(part[m][n], lo & 0x000F000Fu, hi & 0x000F000Fu, lo & 0x00F000F0u, hi & 0x00F000F0u, b[n].z, b[n].w);
@@ -426,12 +463,29 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
               for (int e = 0; e < 4; ++e) acc[m][n][e] = fmaf(scale[m][e / 2], part[m][n][e], acc[m][n][e]);
         }
       }
-      if (!(kPer == 1 && !Z && ok && active)) release(s);
+      if (!(kPer == 1 && !Z && ok && active)) release(slot);
+    };
+    auto next = [&]() {
       s += 2;
       if (s >= stages) {
         s -= stages;
         use ^= 1;
       }
+    };
+    int ks = kh ^ odd;
+    if (my_stages > 0) fetch(w[0], s, use);
+    for (int i = 0; i < my_stages; i += 2) {
+      int slot = s;
+      next();
+      if (i + 1 < my_stages) fetch(w[1], s, use);
+      multiply(w[0], ks, slot);
+      ks += 2;
+      if (i + 1 >= my_stages) break;
+      slot = s;
+      next();
+      if (i + 2 < my_stages) fetch(w[0], s, use);
+      multiply(w[1], ks, slot);
+      ks += 2;
     }
     // join the parities: each warp of a pair gives away one m tile's sums and
     // finishes the other
