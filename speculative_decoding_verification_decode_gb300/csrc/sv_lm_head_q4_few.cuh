@@ -141,6 +141,36 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
   uint32_t* zbuf = sbuf + g.stages * kFewTile * kStride;
   FewBars& bars = *reinterpret_cast<FewBars*>(zbuf + g.stages * kFewTile * kZStride);
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  // The states' 8-column chunks, shared evenly by the computing threads (a half
+  // warp stays in one row, its places 16 columns apart).  The first loads go out
+  // before the codes' own.
+  constexpr int kAhead = 8;
+  const bool bf16 = f.bf16;
+  const int chunks = g.d / 8, all_chunks = g.nk * 16;
+  auto step = [&](int& r, int& j) {
+    while (j >= all_chunks) {
+      j -= all_chunks;
+      ++r;
+    }
+  };
+  uint4 raw[kAhead];
+  auto load = [&](int r, int j) {
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int in = min(r, rows - 1);
+      const uint4* src = in < g.rows0 ? f.s0 + static_cast<long long>(in) * chunks
+                                      : f.s1 + static_cast<long long>(in - g.rows0) * chunks;
+      raw[k] = __ldg(src + min(j, chunks - 1));
+      j += 32 * kFewWarps;
+      step(r, j);
+    }
+  };
+  const int turns = (rows * all_chunks + 32 * kFewWarps - 1) / (32 * kFewWarps);  // chunks of a thread, at most
+  int row0 = 0, chunk0 = threadIdx.x;
+  if (warp < kFewWarps) {
+    step(row0, chunk0);
+    load(row0, chunk0);
+  }
   if (threadIdx.x == 0) {
     for (int s = 0; s < g.stages; ++s) {
       mbar_init(&bars.full[s], 1 + 32 * kFewHelp);
@@ -149,6 +179,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
     bars.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  if (threadIdx.x < 16) reinterpret_cast<uint32_t*>(red)[threadIdx.x] = 0;
   __syncthreads();
 
   if (warp == kFewWarps + kFewHelp) {
@@ -204,48 +235,25 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
     return;
   }
 
-  // ---- the states as operands; columns past dim are 0.  The threads share
-  // all rows' 8-column chunks evenly, several loads in flight: everything waits
-  // for this.  A half warp stays in one row and its places 16 columns apart.
-  const bool bf16 = f.bf16;
-  const int chunks = g.d / 8, all_chunks = g.nk * 16;
-  uint32_t* tops = reinterpret_cast<uint32_t*>(red);  // the rows' largest finite states (until the first tile ends)
-  if (threadIdx.x < 16) tops[threadIdx.x] = 0;
-  // chunk c of a stage: which lane quarter multiplies it, and as its how manieth word
+  // ---- the states as operands; columns past dim are 0.  Everything waits for
+  // this: several loads are in flight, and several chunks in the making.
+  uint32_t* tops = reinterpret_cast<uint32_t*>(red);   // the rows' largest finite states
+  int* shifts = reinterpret_cast<int*>(red) + 16;      // and their powers of two (both until the first tile ends)
   const int c = lane % 16, quarter = G == 128 ? c / 4 : G == 64 ? c % 8 / 2 : c % 4,
             word = G == 128 ? c % 4 : G == 64 ? c / 8 * 2 + c % 2 : c / 4;
-  unsigned char* const my_frag = frag + word * 64 + quarter * 16;
-  const unsigned half_warp = 0xFFFFu << (lane & 16);
-  int row0 = 0, chunk0 = threadIdx.x;
-  auto step = [&](int& r, int& j) {
-    while (j >= all_chunks) {
-      j -= all_chunks;
-      ++r;
-    }
-  };
-  step(row0, chunk0);
-  all_sync();
+  // chunk c of a stage: which lane quarter multiplies it, and as its how manieth word
+  const uint32_t my_frag = smem_u32(frag) + word * 64 + quarter * 16;
+  auto place = [&](int r, int j) { return my_frag + r * frag_row + j / 16 * 256; };
   {
-    constexpr int kAhead = 8;
     const uint32_t limit = bf16 ? 0x7F80u : 0x7C00u;
-    for (int r = row0, j = chunk0; r < rows;) {
-      uint4 x[kAhead];
-      int rr[kAhead], jj[kAhead];
+    int r = row0, j = chunk0;
+    for (int i0 = 0; i0 < turns; i0 += kAhead) {
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
-        rr[k] = r, jj[k] = j;
-        const int in = min(r, rows - 1);
-        const uint4* src = in < g.rows0 ? f.s0 + static_cast<long long>(in) * chunks
-                                        : f.s1 + static_cast<long long>(in - g.rows0) * chunks;
-        x[k] = __ldg(src + min(j, chunks - 1));
-        j += 32 * kFewWarps;
-        step(r, j);
-      }
-#pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        if (rr[k] >= rows) break;
-        if (jj[k] >= chunks) x[k] = make_uint4(0, 0, 0, 0);
-        const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+        if (i0 + k >= turns) break;
+        const bool in = r < rows;
+        if (in && j >= chunks) raw[k] = make_uint4(0, 0, 0, 0);
+        const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
         uint32_t top = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -253,71 +261,87 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
           if (lo < limit) top = max(top, lo);
           if (hi < limit) top = max(top, hi);
         }
-        *reinterpret_cast<uint4*>(my_frag + rr[k] * frag_row + jj[k] / 16 * 256) = x[k];
-        top = __reduce_max_sync(half_warp, top);
-        if (lane % 16 == 0) atomicMax(&tops[rr[k]], top);
+#pragma unroll
+        for (int o = 8; o > 0; o /= 2) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+        if (in) {
+          sts128(place(r, j), raw[k]);
+          if (lane % 16 == 0) atomicMax(&tops[r], top);
+        }
+        j += 32 * kFewWarps;
+        step(r, j);
       }
+      if (i0 + kAhead < turns) load(r, j);
     }
   }
   all_sync();
   // the power of two that takes a row's largest finite state to 2^14
-  auto shift_of = [&](int r) {
-    const uint32_t t = tops[r];
-    return t ? 14 - ilogbf(bf16 ? __uint_as_float(t << 16) : __half2float(__ushort_as_half(static_cast<unsigned short>(t)))) : 0;
-  };
-  int shift_row = -1, shift = 0;
+  if (threadIdx.x < 16) {
+    const uint32_t t = tops[threadIdx.x];
+    shifts[threadIdx.x] =
+        t ? 14 - ilogbf(bf16 ? __uint_as_float(t << 16) : __half2float(__ushort_as_half(static_cast<unsigned short>(t)))) : 0;
+  }
+  all_sync();
+  constexpr int kMake = 4;
+  int r = row0, j = chunk0;
 #pragma unroll 1
-  for (int r = row0, j = chunk0; r < rows;) {
-    if (r != shift_row) {
-      shift = shift_of(r);
-      shift_row = r;
-    }
-    unsigned char* at = my_frag + r * frag_row + j / 16 * 256;
-    const uint4 x = *reinterpret_cast<const uint4*>(at);
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-    float h[8];
-    if (bf16) {
+  for (int i0 = 0; i0 < turns; i0 += kMake) {
+    uint4 x[kMake];
+    int rr[kMake], jj[kMake], shift[kMake];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        h[2 * i] = __uint_as_float(w[i] << 16);
-        h[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-      }
-    } else {
+    for (int k = 0; k < kMake; ++k) {  // (past the last row: the last one again, unused)
+      rr[k] = r, jj[k] = j;
+      const int in = min(r, rows - 1);
+      x[k] = lds128(place(in, j));
+      shift[k] = shifts[in];
+      j += 32 * kFewWarps;
+      step(r, j);
+    }
+    float sum[kMake];
+    uint4 y[kMake];
+#pragma unroll
+    for (int k = 0; k < kMake; ++k) {
+      const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+      float h[8];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float2 two = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-        h[2 * i] = two.x;
-        h[2 * i + 1] = two.y;
+        h[2 * i] = bf16 ? __uint_as_float(w[i] << 16) : two.x;
+        h[2 * i + 1] = bf16 ? __uint_as_float(w[i] & 0xFFFF0000u) : two.y;
       }
-    }
-    int left = shift;
-    if (shift > 126) {  // (tiny bf16 rows: two factors)
+      int left = shift[k];
+      if (left > 126) {  // (tiny bf16 rows: two factors)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) h[i] *= 0x1p40f;
-      left -= 40;
-    }
-    const float up = power(left), up16 = power(left - 4);
+        for (int i = 0; i < 8; ++i) h[i] *= 0x1p40f;
+        left -= 40;
+      }
+      const float up = power(left), up16 = power(left - 4);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] *= i % 2 ? up16 : up;
-    uint32_t y[4];
+      for (int i = 0; i < 8; ++i) h[i] *= i % 2 ? up16 : up;
+      uint32_t p[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __half2 p = __floats2half2_rn(h[i], h[i + 4]);
-      y[i] = *reinterpret_cast<const uint32_t*>(&p);
+      for (int i = 0; i < 4; ++i) {
+        const __half2 two = __floats2half2_rn(h[i], h[i + 4]);
+        p[i] = *reinterpret_cast<const uint32_t*>(&two);
+      }
+      y[k] = make_uint4(p[0], p[1], p[2], p[3]);
+      sum[k] = fmaf(16.f, (h[1] + h[3]) + (h[5] + h[7]), (h[0] + h[2]) + (h[4] + h[6]));
     }
-    *reinterpret_cast<uint4*>(at) = make_uint4(y[0], y[1], y[2], y[3]);
-    // the group's sum, in the units of the products, with the zero of 8 or 1
-    float sum = fmaf(16.f, (h[1] + h[3]) + (h[5] + h[7]), (h[0] + h[2]) + (h[4] + h[6]));
+    // the groups' sums, in the units of the products, with the zero of 8 or 1
 #pragma unroll
-    for (int o = 1; o < G / 8; o *= 2) sum += __shfl_xor_sync(half_warp, sum, o);
-    if (j % (G / 8) == 0) {
-      sum *= Z ? -0x1p-24f : -0x1p-21f;
-      float* to = sums + (j / (G / 8) * NT + r / 8) * 16 + r % 8 / 2 * 4 + r % 2;
-      to[0] = sum;
-      to[2] = sum;
-    }
-    j += 32 * kFewWarps;
-    step(r, j);
+    for (int o = 1; o < G / 8; o *= 2)
+#pragma unroll
+      for (int k = 0; k < kMake; ++k) sum[k] += __shfl_xor_sync(0xFFFFFFFFu, sum[k], o);
+#pragma unroll
+    for (int k = 0; k < kMake; ++k)
+      if (rr[k] < rows) {
+        sts128(place(rr[k], jj[k]), y[k]);
+        if (jj[k] % (G / 8) == 0) {
+          const float total = sum[k] * (Z ? -0x1p-24f : -0x1p-21f);
+          float* to = sums + (jj[k] / (G / 8) * NT + rr[k] / 8) * 16 + rr[k] % 8 / 2 * 4 + rr[k] % 2;
+          to[0] = total;
+          to[2] = total;
+        }
+      }
   }
   all_sync();
 
@@ -329,7 +353,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int r = n * 8 + 2 * t4 + e;
-      back[n][e] = r < rows ? 24 - shift_of(r) : 0;
+      back[n][e] = r < rows ? 24 - shifts[r] : 0;
     }
   all_sync();
   const int swz = gq >> 1 & 3;
