@@ -87,6 +87,11 @@ __device__ __forceinline__ void mma16816_from(float (&d)[4], uint32_t a0, uint32
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 
+template <bool V>
+struct Flag {
+  static constexpr bool value = V;
+};
+
 struct FewArgs {
   Args g;
   const uint4* s0;
@@ -246,30 +251,31 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
   auto place = [&](int r, int j) { return my_frag + r * frag_row + j / 16 * 256; };
   {
     const uint32_t limit = bf16 ? 0x7F80u : 0x7C00u;
-    int r = row0, j = chunk0;
+    int r = row0, j = chunk0, rows_of[kAhead];
     for (int i0 = 0; i0 < turns; i0 += kAhead) {
+      uint32_t top[kAhead];
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
-        if (i0 + k >= turns) break;
-        const bool in = r < rows;
-        if (in && j >= chunks) raw[k] = make_uint4(0, 0, 0, 0);
+        if (j >= chunks) raw[k] = make_uint4(0, 0, 0, 0);
         const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
-        uint32_t top = 0;
+        top[k] = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const uint32_t lo = w[i] & 0x7FFFu, hi = w[i] >> 16 & 0x7FFFu;
-          if (lo < limit) top = max(top, lo);
-          if (hi < limit) top = max(top, hi);
+          top[k] = max(top[k], max(lo < limit ? lo : 0u, hi < limit ? hi : 0u));
         }
-#pragma unroll
-        for (int o = 8; o > 0; o /= 2) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-        if (in) {
-          sts128(place(r, j), raw[k]);
-          if (lane % 16 == 0) atomicMax(&tops[r], top);
-        }
+        rows_of[k] = r;
+        if (r < rows) sts128(place(r, j), raw[k]);
         j += 32 * kFewWarps;
         step(r, j);
       }
+#pragma unroll
+      for (int o = 8; o > 0; o /= 2)
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) top[k] = max(top[k], __shfl_xor_sync(0xFFFFFFFFu, top[k], o));
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k)
+        if (lane % 16 == 0 && rows_of[k] < rows) atomicMax(&tops[rows_of[k]], top[k]);
       if (i0 + kAhead < turns) load(r, j);
     }
   }
@@ -282,67 +288,80 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
   }
   all_sync();
   constexpr int kMake = 4;
-  int r = row0, j = chunk0;
+  auto make = [&](auto is_bf16) {
+    constexpr bool kBf16 = decltype(is_bf16)::value;
+    int r = row0, j = chunk0;
 #pragma unroll 1
-  for (int i0 = 0; i0 < turns; i0 += kMake) {
-    uint4 x[kMake];
-    int rr[kMake], jj[kMake], shift[kMake];
+    for (int i0 = 0; i0 < turns; i0 += kMake) {
+      uint4 x[kMake];
+      int rr[kMake], jj[kMake], shift[kMake];
 #pragma unroll
-    for (int k = 0; k < kMake; ++k) {  // (past the last row: the last one again, unused)
-      rr[k] = r, jj[k] = j;
-      const int in = min(r, rows - 1);
-      x[k] = lds128(place(in, j));
-      shift[k] = shifts[in];
-      j += 32 * kFewWarps;
-      step(r, j);
-    }
-    float sum[kMake];
-    uint4 y[kMake];
-#pragma unroll
-    for (int k = 0; k < kMake; ++k) {
-      const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-      float h[8];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 two = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-        h[2 * i] = bf16 ? __uint_as_float(w[i] << 16) : two.x;
-        h[2 * i + 1] = bf16 ? __uint_as_float(w[i] & 0xFFFF0000u) : two.y;
+      for (int k = 0; k < kMake; ++k) {  // (past the last row: the last one again, unused)
+        rr[k] = r, jj[k] = j;
+        const int in = min(r, rows - 1);
+        x[k] = lds128(place(in, j));
+        shift[k] = shifts[in];
+        j += 32 * kFewWarps;
+        step(r, j);
       }
-      int left = shift[k];
-      if (left > 126) {  // (tiny bf16 rows: two factors)
+      float sum[kMake];
+      uint4 y[kMake];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) h[i] *= 0x1p40f;
-        left -= 40;
-      }
-      const float up = power(left), up16 = power(left - 4);
+      for (int k = 0; k < kMake; ++k) {
+        const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+        float h[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) h[i] *= i % 2 ? up16 : up;
-      uint32_t p[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const __half2 two = __floats2half2_rn(h[i], h[i + 4]);
-        p[i] = *reinterpret_cast<const uint32_t*>(&two);
-      }
-      y[k] = make_uint4(p[0], p[1], p[2], p[3]);
-      sum[k] = fmaf(16.f, (h[1] + h[3]) + (h[5] + h[7]), (h[0] + h[2]) + (h[4] + h[6]));
-    }
-    // the groups' sums, in the units of the products, with the zero of 8 or 1
-#pragma unroll
-    for (int o = 1; o < G / 8; o *= 2)
-#pragma unroll
-      for (int k = 0; k < kMake; ++k) sum[k] += __shfl_xor_sync(0xFFFFFFFFu, sum[k], o);
-#pragma unroll
-    for (int k = 0; k < kMake; ++k)
-      if (rr[k] < rows) {
-        sts128(place(rr[k], jj[k]), y[k]);
-        if (jj[k] % (G / 8) == 0) {
-          const float total = sum[k] * (Z ? -0x1p-24f : -0x1p-21f);
-          float* to = sums + (jj[k] / (G / 8) * NT + rr[k] / 8) * 16 + rr[k] % 8 / 2 * 4 + rr[k] % 2;
-          to[0] = total;
-          to[2] = total;
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (kBf16) {
+            h[2 * i] = __uint_as_float(w[i] << 16);
+            h[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+          } else {
+            const float2 two = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+            h[2 * i] = two.x;
+            h[2 * i + 1] = two.y;
+          }
         }
+        int left = shift[k];
+        if constexpr (kBf16)
+          if (left > 126) {  // (tiny rows: two factors)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) h[i] *= 0x1p40f;
+            left -= 40;
+          }
+        const float up = power(left), up16 = power(left - 4);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[i] *= i % 2 ? up16 : up;
+        uint32_t p[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const __half2 two = __floats2half2_rn(h[i], h[i + 4]);
+          p[i] = *reinterpret_cast<const uint32_t*>(&two);
+        }
+        y[k] = make_uint4(p[0], p[1], p[2], p[3]);
+        sum[k] = fmaf(16.f, (h[1] + h[3]) + (h[5] + h[7]), (h[0] + h[2]) + (h[4] + h[6]));
       }
-  }
+      // the groups' sums, in the units of the products, with the zero of 8 or 1
+#pragma unroll
+      for (int o = 1; o < G / 8; o *= 2)
+#pragma unroll
+        for (int k = 0; k < kMake; ++k) sum[k] += __shfl_xor_sync(0xFFFFFFFFu, sum[k], o);
+#pragma unroll
+      for (int k = 0; k < kMake; ++k)
+        if (rr[k] < rows) {
+          sts128(place(rr[k], jj[k]), y[k]);
+          if (jj[k] % (G / 8) == 0) {
+            const float total = sum[k] * (Z ? -0x1p-24f : -0x1p-21f);
+            float* to = sums + (jj[k] / (G / 8) * NT + rr[k] / 8) * 16 + rr[k] % 8 / 2 * 4 + rr[k] % 2;
+            to[0] = total;
+            to[2] = total;
+          }
+        }
+    }
+  };
+  if (bf16)
+    make(Flag<true>());
+  else
+    make(Flag<false>());
   all_sync();
 
   const int rw = warp % kFewGroups, kh = warp / kFewGroups, gq = lane / 4, t4 = lane % 4;
