@@ -6,7 +6,8 @@
 namespace svq {
 
 sv_status start_bf16(const Args& g, int n, const sv_q4_proj* proj, const void* s0, const void* s1, cudaStream_t st);
-sv_status start_few_any(const Args& g, bool bf16, const sv_q4_proj* proj, const void* s0, const void* s1, cudaStream_t st);
+sv_status start_few_bf16(const Args& g, const sv_q4_proj* proj, const void* s0, const void* s1, cudaStream_t st);
+sv_status start_few_f16(const Args& g, const sv_q4_proj* proj, const void* s0, const void* s1, cudaStream_t st);
 sv_status start_f16(const Args& g, int n, const sv_q4_proj* proj, const void* s0, const void* s1, cudaStream_t st);
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -54,7 +55,7 @@ sv_status launch(const void* s0, int rows0, const void* s1, int rows1, sv_dtype 
   g.d = dim;
   // up to 16 rows whose states fit in shared memory: the kernel for few rows
   if (static_cast<long long>(rows0) + rows1 <= 16) {
-    const sv_status few = start_few_any(g, dtype == SV_BF16, proj, s0, s1, stream);
+    const sv_status few = dtype == SV_BF16 ? start_few_bf16(g, proj, s0, s1, stream) : start_few_f16(g, proj, s0, s1, stream);
     if (few != SV_ERR_UNSUPPORTED) return few;
   }
   const long long split = rows1 ? (static_cast<long long>(rows0) + 7) / 8 * 8 : 0x40000000LL;

@@ -19,7 +19,12 @@
 //     them as they are).  The states that meet the second kind are kept 16
 //     times smaller.  The zeros come in as what a group's sum starts from,
 //     -z sum_k h, the sums kept from the beginning.  Five instructions for
-//     eight weights, and the product is exact as before up to f32 sums.
+//     eight weights, and every product is exact.
+//     Codes that low lose bits of the products' ends (measured: as if the
+//     MMA aligned every subnormal's products by 2^-14): nothing to speak of
+//     with bf16's eight significant bits (3.4e-7 of the logits' norm, as much
+//     as a sum in f32), but 8.5e-7 with f16's eleven.  With f16 states
+//     all four pairs therefore stand four bits up, two more shifts per word.
 //   - So the states are f16 under a power of two per row that takes the row's
 //     largest to 2^14: exact for whatever is above 2^-24 of it, within 2^-35
 //     of it below, far under the f32 sums' roundings; the logits take the
@@ -87,16 +92,10 @@ __device__ __forceinline__ void mma16816_from(float (&d)[4], uint32_t a0, uint32
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 
-template <bool V>
-struct Flag {
-  static constexpr bool value = V;
-};
-
 struct FewArgs {
   Args g;
   const uint4* s0;
   const uint4* s1;
-  int bf16;  // the states' type
 };
 
 // The odd stride at which a row's scales (zeros) of a stage of n groups lie, in words.
@@ -124,8 +123,8 @@ __device__ __forceinline__ void fetch_words(uintptr_t from, long long row_bytes,
   }
 }
 
-// NT tiles of 8 states, groups of G, Z: zeros are given.
-template <int NT, int G, bool Z>
+// NT tiles of 8 states, groups of G, Z: zeros are given, BF: bf16 states (else f16).
+template <int NT, int G, bool Z, bool BF>
 __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_constant__ CUtensorMap wmap,
                                                              const __grid_constant__ FewArgs f) {
   constexpr int kPer = kFewK / G;       // groups per stage
@@ -150,7 +149,6 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
   // warp stays in one row, its places 16 columns apart).  The first loads go out
   // before the codes' own.
   constexpr int kAhead = 8;
-  const bool bf16 = f.bf16;
   const int chunks = g.d / 8, all_chunks = g.nk * 16;
   auto step = [&](int& r, int& j) {
     while (j >= all_chunks) {
@@ -250,7 +248,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
   const uint32_t my_frag = smem_u32(frag) + word * 64 + quarter * 16;
   auto place = [&](int r, int j) { return my_frag + r * frag_row + j / 16 * 256; };
   {
-    const uint32_t limit = bf16 ? 0x7F80u : 0x7C00u;
+    const uint32_t limit = BF ? 0x7F80u : 0x7C00u;
     int r = row0, j = chunk0, rows_of[kAhead];
     for (int i0 = 0; i0 < turns; i0 += kAhead) {
       uint32_t top[kAhead];
@@ -284,84 +282,77 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
   if (threadIdx.x < 16) {
     const uint32_t t = tops[threadIdx.x];
     shifts[threadIdx.x] =
-        t ? 14 - ilogbf(bf16 ? __uint_as_float(t << 16) : __half2float(__ushort_as_half(static_cast<unsigned short>(t)))) : 0;
+        t ? 14 - ilogbf(BF ? __uint_as_float(t << 16) : __half2float(__ushort_as_half(static_cast<unsigned short>(t)))) : 0;
   }
   all_sync();
   constexpr int kMake = 4;
-  auto make = [&](auto is_bf16) {
-    constexpr bool kBf16 = decltype(is_bf16)::value;
-    int r = row0, j = chunk0;
+  int r = row0, j = chunk0;
 #pragma unroll 1
-    for (int i0 = 0; i0 < turns; i0 += kMake) {
-      uint4 x[kMake];
-      int rr[kMake], jj[kMake], shift[kMake];
+  for (int i0 = 0; i0 < turns; i0 += kMake) {
+    uint4 x[kMake];
+    int rr[kMake], jj[kMake], shift[kMake];
 #pragma unroll
-      for (int k = 0; k < kMake; ++k) {  // (past the last row: the last one again, unused)
-        rr[k] = r, jj[k] = j;
-        const int in = min(r, rows - 1);
-        x[k] = lds128(place(in, j));
-        shift[k] = shifts[in];
-        j += 32 * kFewWarps;
-        step(r, j);
-      }
-      float sum[kMake];
-      uint4 y[kMake];
-#pragma unroll
-      for (int k = 0; k < kMake; ++k) {
-        const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-        float h[8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if constexpr (kBf16) {
-            h[2 * i] = __uint_as_float(w[i] << 16);
-            h[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-          } else {
-            const float2 two = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-            h[2 * i] = two.x;
-            h[2 * i + 1] = two.y;
-          }
-        }
-        int left = shift[k];
-        if constexpr (kBf16)
-          if (left > 126) {  // (tiny rows: two factors)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) h[i] *= 0x1p40f;
-            left -= 40;
-          }
-        const float up = power(left), up16 = power(left - 4);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) h[i] *= i % 2 ? up16 : up;
-        uint32_t p[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const __half2 two = __floats2half2_rn(h[i], h[i + 4]);
-          p[i] = *reinterpret_cast<const uint32_t*>(&two);
-        }
-        y[k] = make_uint4(p[0], p[1], p[2], p[3]);
-        sum[k] = fmaf(16.f, (h[1] + h[3]) + (h[5] + h[7]), (h[0] + h[2]) + (h[4] + h[6]));
-      }
-      // the groups' sums, in the units of the products, with the zero of 8 or 1
-#pragma unroll
-      for (int o = 1; o < G / 8; o *= 2)
-#pragma unroll
-        for (int k = 0; k < kMake; ++k) sum[k] += __shfl_xor_sync(0xFFFFFFFFu, sum[k], o);
-#pragma unroll
-      for (int k = 0; k < kMake; ++k)
-        if (rr[k] < rows) {
-          sts128(place(rr[k], jj[k]), y[k]);
-          if (jj[k] % (G / 8) == 0) {
-            const float total = sum[k] * (Z ? -0x1p-24f : -0x1p-21f);
-            float* to = sums + (jj[k] / (G / 8) * NT + rr[k] / 8) * 16 + rr[k] % 8 / 2 * 4 + rr[k] % 2;
-            to[0] = total;
-            to[2] = total;
-          }
-        }
+    for (int k = 0; k < kMake; ++k) {  // (past the last row: the last one again, unused)
+      rr[k] = r, jj[k] = j;
+      const int in = min(r, rows - 1);
+      x[k] = lds128(place(in, j));
+      shift[k] = shifts[in];
+      j += 32 * kFewWarps;
+      step(r, j);
     }
-  };
-  if (bf16)
-    make(Flag<true>());
-  else
-    make(Flag<false>());
+    float sum[kMake];
+    uint4 y[kMake];
+#pragma unroll
+    for (int k = 0; k < kMake; ++k) {
+      const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+      float h[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (BF) {
+          h[2 * i] = __uint_as_float(w[i] << 16);
+          h[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        } else {
+          const float2 two = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+          h[2 * i] = two.x;
+          h[2 * i + 1] = two.y;
+        }
+      }
+      int left = shift[k];
+      if constexpr (BF)
+        if (left > 126) {  // (tiny rows: two factors)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) h[i] *= 0x1p40f;
+          left -= 40;
+        }
+      const float up = power(left), up_odd = BF ? power(left - 4) : up;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) h[i] *= i % 2 ? up_odd : up;
+      uint32_t p[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const __half2 two = __floats2half2_rn(h[i], h[i + 4]);
+        p[i] = *reinterpret_cast<const uint32_t*>(&two);
+      }
+      y[k] = make_uint4(p[0], p[1], p[2], p[3]);
+      sum[k] = fmaf(BF ? 16.f : 1.f, (h[1] + h[3]) + (h[5] + h[7]), (h[0] + h[2]) + (h[4] + h[6]));
+    }
+    // the groups' sums, in the units of the products, with the zero of 8 or 1
+#pragma unroll
+    for (int o = 1; o < G / 8; o *= 2)
+#pragma unroll
+      for (int k = 0; k < kMake; ++k) sum[k] += __shfl_xor_sync(0xFFFFFFFFu, sum[k], o);
+#pragma unroll
+    for (int k = 0; k < kMake; ++k)
+      if (rr[k] < rows) {
+        sts128(place(rr[k], jj[k]), y[k]);
+        if (jj[k] % (G / 8) == 0) {
+          const float total = sum[k] * (BF ? (Z ? -0x1p-24f : -0x1p-21f) : (Z ? -0x1p-20f : -0x1p-17f));
+          float* to = sums + (jj[k] / (G / 8) * NT + rr[k] / 8) * 16 + rr[k] % 8 / 2 * 4 + rr[k] % 2;
+          to[0] = total;
+          to[2] = total;
+        }
+      }
+  }
   all_sync();
 
   const int rw = warp % kFewGroups, kh = warp / kFewGroups, gq = lane / 4, t4 = lane % 4;
@@ -372,7 +363,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int r = n * 8 + 2 * t4 + e;
-      back[n][e] = r < rows ? 24 - shifts[r] : 0;
+      back[n][e] = r < rows ? (BF ? 24 : 20) - shifts[r] : 0;
     }
   all_sync();
   const int swz = gq >> 1 & 3;
@@ -479,23 +470,26 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
 #pragma unroll
             for (int n = 0; n < NT; ++n) b[n] = lds128(frag0[n] + ks * 256 + (j * kLen + i) * 64);
             // (a tile's two MMAs apart: the second waits for the first)
+            constexpr uint32_t kLow = 0x000F000Fu, kHigh = 0x00F000F0u, kEven = BF ? kLow : kHigh;
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
               const uint32_t lo = w[m][0][j * kLen + i], hi = w[m][1][j * kLen + i];
+              const uint32_t lo0 = BF ? lo : lo << 4, hi0 = BF ? hi : hi << 4;
 #pragma unroll
               for (int n = 0; n < NT; ++n) {
                 if (i == 0 && !Z)
-                  mma16816_from(part[m][n], lo & 0x000F000Fu, hi & 0x000F000Fu, lo & 0x00F000F0u, hi & 0x00F000F0u, b[n].x, b[n].y, from[n]);
+                  mma16816_from(part[m][n], lo0 & kEven, hi0 & kEven, lo & kHigh, hi & kHigh, b[n].x, b[n].y, from[n]);
                 else
-                  mma16816(part[m][n], lo & 0x000F000Fu, hi & 0x000F000Fu, lo & 0x00F000F0u, hi & 0x00F000F0u, b[n].x, b[n].y);
+                  mma16816(part[m][n], lo0 & kEven, hi0 & kEven, lo & kHigh, hi & kHigh, b[n].x, b[n].y);
               }
             }
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
               const uint32_t lo = w[m][0][j * kLen + i] >> 8, hi = w[m][1][j * kLen + i] >> 8;
+              const uint32_t lo2 = BF ? lo : w[m][0][j * kLen + i] >> 4, hi2 = BF ? hi : w[m][1][j * kLen + i] >> 4;
 #pragma unroll
               for (int n = 0; n < NT; ++n)
-                mma16816(part[m][n], lo & 0x000F000Fu, hi & 0x000F000Fu, lo & 0x00F000F0u, hi & 0x00F000F0u, b[n].z, b[n].w);
+                mma16816(part[m][n], lo2 & kEven, hi2 & kEven, lo & kHigh, hi & kHigh, b[n].z, b[n].w);
             }
           }
 #pragma unroll
@@ -575,8 +569,8 @@ inline int few_smem(const Args& g, int group, int stages, int nt) {
 
 // Launches the call here if its states fit beside a ring of four stages
 // (SV_ERR_UNSUPPORTED otherwise, with nothing enqueued).
-template <int NT, int G, bool Z>
-sv_status start_few(Args g, bool bf16, const sv_q4_proj* proj, const void* s0, const void* s1, cudaStream_t stream) {
+template <int NT, int G, bool Z, bool BF>
+sv_status start_few(Args g, const sv_q4_proj* proj, const void* s0, const void* s1, cudaStream_t stream) {
   int dev = 0;
   const int sms = sm_count(&dev);
   // tile rows: as few rounds as tiles of 256 allow, then spread evenly, in warps' 32 rows
@@ -592,27 +586,34 @@ sv_status start_few(Args g, bool bf16, const sv_q4_proj* proj, const void* s0, c
     return svh::fail(SV_ERR_ARG, "tensor map encoding failed (alignment or size)");
   static bool attr_set[64] = {false};
   if (!attr_set[dev]) {
-    const cudaError_t e = cudaFuncSetAttribute(few_kernel<NT, G, Z>, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewBudget);
+    const cudaError_t e = cudaFuncSetAttribute(few_kernel<NT, G, Z, BF>, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewBudget);
     if (e != cudaSuccess) return svh::fail(SV_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
     attr_set[dev] = true;
   }
-  FewArgs f{g, static_cast<const uint4*>(s0), static_cast<const uint4*>(s1), bf16};
-  few_kernel<NT, G, Z><<<static_cast<unsigned>(g.tiles < sms ? g.tiles : sms), kFewThreads,
+  FewArgs f{g, static_cast<const uint4*>(s0), static_cast<const uint4*>(s1)};
+  few_kernel<NT, G, Z, BF><<<static_cast<unsigned>(g.tiles < sms ? g.tiles : sms), kFewThreads,
                          few_smem(g, G, g.stages, NT), stream>>>(mw, f);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return svh::fail(SV_ERR_CUDA, "kernel launch: %s", cudaGetErrorString(e));
   return SV_OK;
 }
 
-template <int NT, int G>
-sv_status start_few_zeros(const Args& g, bool bf16, const sv_q4_proj* proj, const void* s0, const void* s1, cudaStream_t st) {
-  return g.zeros ? start_few<NT, G, true>(g, bf16, proj, s0, s1, st) : start_few<NT, G, false>(g, bf16, proj, s0, s1, st);
+template <int NT, int G, bool BF>
+sv_status start_few_zeros(const Args& g, const sv_q4_proj* proj, const void* s0, const void* s1, cudaStream_t st) {
+  return g.zeros ? start_few<NT, G, true, BF>(g, proj, s0, s1, st) : start_few<NT, G, false, BF>(g, proj, s0, s1, st);
 }
 
-template <int G>
-sv_status start_few_group(const Args& g, bool bf16, const sv_q4_proj* proj, const void* s0, const void* s1, cudaStream_t st) {
-  return g.rows0 + g.rows1 <= 8 ? start_few_zeros<1, G>(g, bf16, proj, s0, s1, st)
-                                : start_few_zeros<2, G>(g, bf16, proj, s0, s1, st);
+template <int G, bool BF>
+sv_status start_few_group(const Args& g, const sv_q4_proj* proj, const void* s0, const void* s1, cudaStream_t st) {
+  return g.rows0 + g.rows1 <= 8 ? start_few_zeros<1, G, BF>(g, proj, s0, s1, st)
+                                : start_few_zeros<2, G, BF>(g, proj, s0, s1, st);
+}
+
+template <bool BF>
+sv_status start_few_any(const Args& g, const sv_q4_proj* proj, const void* s0, const void* s1, cudaStream_t st) {
+  if (proj->group == 32) return start_few_group<32, BF>(g, proj, s0, s1, st);
+  if (proj->group == 64) return start_few_group<64, BF>(g, proj, s0, s1, st);
+  return start_few_group<128, BF>(g, proj, s0, s1, st);
 }
 
 }  // namespace svq
