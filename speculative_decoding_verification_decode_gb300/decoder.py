@@ -161,7 +161,8 @@ class BeamDecoder:
     ``step_fn(tokens, lengths) -> [B, W, V]``: logits of the next token after
     the first ``lengths[b]`` tokens of each beam; deterministic and
     graph-capturable.  What it keeps per beam (caches, recurrent states) is
-    given in ``states`` and moves with the beams."""
+    given in ``states`` and moves with the beams.  A sequence whose tokens
+    fill ``max_len`` stays as it is from then on."""
 
     def __init__(self, step_fn: Callable, tokens: torch.Tensor, lengths: torch.Tensor, eos: int = -1,
                  states=(), time_dims=()):
@@ -188,12 +189,14 @@ class BeamDecoder:
         """One token for every beam; returns the selection."""
         logits = self.step_fn(self.tokens, self.lengths)
         sel = api.beam_select(logits, self.scores, finished=self.finished if self.eos >= 0 else None, eos=self.eos)
+        full = (self.lengths >= self.max_len)[:, None]
+        sel.parents.masked_fill_(full, -1)
         api.beam_reorder(self.states, sel.parents, self.lengths, self.time_dims)
         at = self.lengths.long().clamp(max=self.max_len - 1)
-        self.tokens[self.rows, :, at] = sel.tokens.clamp(min=0)
+        self.tokens[self.rows, :, at] = torch.where(full, self.tokens[self.rows, :, at], sel.tokens.clamp(min=0))
         if self.eos >= 0:  # a finished beam's one candidate is eos again, so the token tells
-            self.finished.copy_(sel.tokens == self.eos)
-        self.scores.copy_(sel.scores)
+            self.finished.copy_(torch.where(full, self.finished, sel.tokens == self.eos))
+        self.scores.copy_(torch.where(full, self.scores, sel.scores))
         self.lengths.add_(1).clamp_(max=self.max_len)
         return sel
 

@@ -99,3 +99,32 @@ def test_search(B, W, V, eos, graph):
     for b in range(B):
         n = int(ln[b]) - 1
         assert torch.equal(m.cache[b, :, :, :n], ref.cache[b, :, :, :n])
+
+
+@pytest.mark.parametrize("eos", [-1, 5])
+def test_full_sequences_stay(eos):
+    """A sequence that has filled its room stays as it is; the others go on as
+    they would alone."""
+    B, W, V, T, d, steps = 2, 4, 997, 10, 128, 6
+    tokens = torch.zeros(B, W, T, dtype=torch.int32, device=DEV)
+    tokens[:, :, :7] = torch.randint(0, V, (B, 1, 7), generator=torch.Generator().manual_seed(3), dtype=torch.int32).to(DEV)
+    lengths = torch.tensor([4, 7], dtype=torch.int32, device=DEV)
+
+    def table(tokens, lengths):  # logits by the last token and the position
+        at = lengths.long() - 1
+        last = tokens[torch.arange(B, device=DEV), :, at].long()
+        return base[(last + 31 * at[:, None]) % 64]
+
+    base = (3 * torch.randn(64, V, generator=torch.Generator().manual_seed(4))).to(DEV)
+    short = sv().BeamDecoder(table, tokens.clone(), lengths.clone(), eos)
+    short.run(3, graph=False)  # sequence 1 is full now
+    kept = [t[1].clone() for t in (short.tokens, short.scores, short.finished)]
+    wide = torch.zeros(B, W, 2 * T, dtype=torch.int32, device=DEV)
+    wide[:, :, :T] = tokens
+    ref = sv().BeamDecoder(table, wide, lengths.clone(), eos)
+    ref.run(steps, graph=False)
+    short.run(steps - 3, graph=False)
+    for a, b in zip((short.tokens, short.scores, short.finished), kept):
+        assert torch.equal(a[1], b)
+    assert short.lengths.tolist() == [10, 10]
+    assert torch.equal(short.tokens[0], ref.tokens[0, :, :T]) and torch.equal(short.scores[0], ref.scores[0])
