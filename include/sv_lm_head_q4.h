@@ -48,6 +48,8 @@ typedef struct {
  * [rows, ld] f32, ld >= vocab; `err`, optional device word: bit 0 is OR-ed in
  * if a bounded device wait of the kernel gave up (the logits are then
  * invalid); the caller zeroes it.  One launch.
+ * A row of states with an infinity or a NaN in it has logits that are not
+ * finite (infinite or NaN); the other rows' are as they would be without it.
  */
 sv_status sv_lm_head_q4_logits(const void* states, sv_dtype dtype, const sv_q4_proj* proj, int32_t rows,
                                int32_t vocab, int32_t dim, float* logits, int64_t ld, uint32_t* err,

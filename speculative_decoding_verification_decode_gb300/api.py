@@ -396,6 +396,8 @@ def _q4_arg(p: Q4Projection, dev: torch.device):
         raise ValueError("packed must be uint8 [V, d / 2]")
     V, d = packed.shape
     d *= 2
+    if V >= 2**31 or d >= 2**31:
+        raise ValueError("a projection's sizes must be below 2^31")
     if group not in (32, 64, 128):
         raise ValueError("group must be 32, 64 or 128")
     shape = (V, -(-d // group))
@@ -439,8 +441,11 @@ def lm_head_logits(states: torch.Tensor, proj: Union[torch.Tensor, Q4Projection]
             if V % 4:  # rows start on 16-byte boundaries
                 out = out[:, :V]
         elif (out.device != dev or out.dtype != torch.float32 or out.dim() != 2 or out.shape[0] < rows
-              or out.shape[1] < V or out.stride(1) != 1):
-            raise ValueError("out must be f32 [rows, >= V] on the states' device with unit stride along V")
+              or out.shape[1] < V or (out.stride(1) != 1 and V > 1) or (out.stride(0) < V and rows > 1)):
+            raise ValueError("out must be f32 [rows, >= V] on the states' device with unit stride along V, "
+                             "its rows apart from one another")
+        if err is not None and (err.device != dev or err.dtype != torch.int32 or err.numel() < 1):
+            raise ValueError("err must be an int32 word on the states' device")
         _launch(dev, _lib.load().sv_lm_head_q4_logits, h.data_ptr(), _DTYPES[h.dtype], arg, rows, V, d,
                 out.data_ptr(), max(out.stride(0), V), None if err is None else err.data_ptr())
         return out
@@ -608,7 +613,8 @@ def _like(t: torch.Tensor, dev: torch.device, dtype: torch.dtype) -> torch.Tenso
 
 def beam_select_workspace(batch: int, beams: int, vocab: int, n: int, device=None) -> torch.Tensor:
     """A workspace for sv_beam_select of this size (uninitialised bytes)."""
-    return torch.empty(_select_bytes(batch, beams, vocab, n), dtype=torch.uint8, device=device or torch.device("cuda", torch.cuda.current_device()))
+    return torch.empty(_select_bytes(batch, beams, vocab, n), dtype=torch.uint8,
+                       device=device or torch.device("cuda", torch.cuda.current_device()))
 
 
 def beam_select(logits: torch.Tensor, scores: torch.Tensor, n: Optional[int] = None,
@@ -656,12 +662,18 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, n: Optional[int] = N
         finished = _like(finished, dev, torch.bool)
     scores = _like(scores, dev, torch.float32)
     n = W if n is None else int(n)
+    if max(V, W, abs(n), abs(eos)) >= 2**31:
+        raise ValueError("sizes, n and eos must be below 2^31")
     lib = _lib.load()
     need = _select_bytes(B, W, V, n)
-    have = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    have = 0
+    if workspace is not None:
+        if workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous on the logits' device")
+        have = workspace.numel() * workspace.element_size()
     if have < need:
         workspace, have = torch.empty(need, dtype=torch.uint8, device=dev), need
-    shape = (B, max(n, 0))
+    shape = (B, n if 0 < n <= 128 else 0)  # (any other n is refused below)
     out = torch.empty(shape, dtype=torch.float32, device=dev)
     par = torch.empty(shape, dtype=torch.int32, device=dev)
     tok = torch.empty(shape, dtype=torch.int32, device=dev)
@@ -703,8 +715,12 @@ def _beam_layout(t: torch.Tensor, time_dim: Optional[int]) -> tuple:
         if k == dims and k > 2:
             raise ValueError("a state's last dimension must have unit stride (moved in place)")
         segs, seg = _flat_stride(shape, strides, 2, k, "a state's dimensions after [B, W]")
+        if segs >= 2**31:
+            raise ValueError("a state has too many segments")
         return (strides[0] * e, strides[1] * e, seg * e, span * e, segs | 1 << 32, 0)
     segs, seg = _flat_stride(shape, strides, 2, time_dim, "a state's dimensions between the beams and the time")
+    if max(segs, shape[time_dim]) >= 2**31:
+        raise ValueError("a state has too many segments or tokens")
     span, stride = _flat_stride(shape, strides, time_dim + 1, dims, "a state's dimensions after the time")
     if (span > 1 and stride != 1) or (shape[time_dim] > 1 and strides[time_dim] != span):
         raise ValueError("a state's tokens must be contiguous: unit stride after the time, one after another along it")

@@ -561,10 +561,10 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
 }
 
 // Shared memory of a call with `stages` stages.
-inline int few_smem(const Args& g, int group, int stages, int nt) {
+inline long long few_smem(const Args& g, int group, int stages, int nt) {
   const int per = kFewK / group;
-  return 1024 + stages * (g.R * 64 + kFewTile * 4 * (few_stride(per) + (g.zeros ? few_zstride(per) : 0))) +
-         (g.rows0 + g.rows1) * (g.nk * 256 + 64) + g.nk * per * nt * 64 + kFewWarps * nt * 128 * 4 + static_cast<int>(sizeof(FewBars));
+  return 1024LL + stages * (g.R * 64 + kFewTile * 4 * (few_stride(per) + (g.zeros ? few_zstride(per) : 0))) +
+         (g.rows0 + g.rows1) * (g.nk * 256LL + 64) + static_cast<long long>(g.nk) * per * nt * 64 + kFewWarps * nt * 128 * 4 + static_cast<int>(sizeof(FewBars));
 }
 
 // Launches the call here if its states fit beside a ring of four stages
@@ -592,7 +592,7 @@ sv_status start_few(Args g, const sv_q4_proj* proj, const void* s0, const void* 
   }
   FewArgs f{g, static_cast<const uint4*>(s0), static_cast<const uint4*>(s1)};
   few_kernel<NT, G, Z, BF><<<static_cast<unsigned>(g.tiles < sms ? g.tiles : sms), kFewThreads,
-                         few_smem(g, G, g.stages, NT), stream>>>(mw, f);
+                         static_cast<size_t>(few_smem(g, G, g.stages, NT)), stream>>>(mw, f);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return svh::fail(SV_ERR_CUDA, "kernel launch: %s", cudaGetErrorString(e));
   return SV_OK;

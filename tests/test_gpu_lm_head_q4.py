@@ -187,6 +187,22 @@ def test_refusals():
         sv().lm_head_verify_static(h, h, p, torch.ones(1), torch.zeros(1), torch.zeros(2))
 
 
+def test_output_refusals():
+    """Rows of `out` that share memory, and words elsewhere, are refused."""
+    h, p = make(8, 3, 40, 64, 32)
+    h, p = h.to(DEV), on_dev(p)
+    with pytest.raises(ValueError, match="out"):
+        sv().lm_head_logits(h, p, out=torch.empty(1, 40, device=DEV).expand(3, 40))
+    with pytest.raises(ValueError, match="out"):
+        sv().lm_head_logits(h, p, out=torch.empty(200, device=DEV).as_strided((3, 40), (32, 1)))
+    with pytest.raises(ValueError, match="err"):
+        sv().lm_head_logits(h, p, err=torch.zeros(1, dtype=torch.int32))
+    with pytest.raises(ValueError, match="err"):
+        sv().lm_head_logits(h, p, err=torch.zeros(1, dtype=torch.uint8, device=DEV))
+    one = sv().lm_head_logits(h[:1], p, out=torch.empty(1, 40, device=DEV).expand(1, 40))
+    assert torch.equal(one, sv().lm_head_logits(h[:1], p))
+
+
 def test_streams_and_graphs():
     cases = [make(30 + i, 6, 8000, 1024, 64, zeros=bool(i)) for i in range(2)]
     cases = [(h.to(DEV), on_dev(p)) for h, p in cases]
