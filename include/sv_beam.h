@@ -48,7 +48,8 @@ size_t sv_beam_select_workspace_size(int32_t batch, int32_t beams, int32_t vocab
  * finished [batch, beams] bytes, or NULL: a beam marked nonzero has ended; its
  *          one candidate is (eos, its score unchanged) and its row is not read.
  * A logit of -Inf (a masked token) is no candidate; a row of nothing else has
- * none.  A sequence with fewer than n candidates gets score -Inf, parent -1,
+ * none; nor is a score below f32's range one (a beam and a token both at the
+ * lowest finite value).  A sequence with fewer than n candidates gets score -Inf, parent -1,
  * token -1 in the places left over.
  * out_scores, out_parents, out_tokens [batch, n].
  * status   [batch]: 0, or SV_SEQ_BAD_VALUE (NaN or +Inf among the logits of a
@@ -57,6 +58,7 @@ size_t sv_beam_select_workspace_size(int32_t batch, int32_t beams, int32_t vocab
  * workspace: sv_beam_select_workspace_size() bytes, 16-byte aligned, no
  *          initial contents needed.  Calls that share one must not overlap on
  *          the GPU.
+ * Two launches; nothing is enqueued when the call is refused.
  * 1 <= beams <= SV_BEAM_MAX_BEAMS, 1 <= n <= SV_BEAM_MAX_CANDIDATES,
  * beams * vocab < 2^31.
  */

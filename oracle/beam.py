@@ -10,7 +10,8 @@ Definitions this file fixes:
   ``math.fsum``, correctly rounded, so that rows that are permutations of one
   another have equal sums and their candidates tie exactly).
 * a finished beam offers ``(eos, c_w)`` alone; a beam at -inf and a token at
-  -inf offer nothing; places left over are (-inf, -1, -1).
+  -inf offer nothing, nor does a score that rounds to -inf in f32; places left
+  over are (-inf, -1, -1).
 * NaN or +inf among a live beam's logits, or a score that is NaN or +inf:
   the sequence is bad and every place is (-inf, -1, -1).
 * reordering: slot w of sequence b takes what slot ``parents[b, w]`` held; a
@@ -66,6 +67,8 @@ def beam_select(logits: np.ndarray, scores: np.ndarray, n: int, finished: Option
             elif live[w] and (x[w] > -np.inf).any():
                 s[w] = c[w] + (x[w] - _lse(x[w]))
         s = s.reshape(-1)
+        with np.errstate(over="ignore"):
+            s[s.astype(np.float32) == -np.inf] = -np.inf
         order = np.argsort(-s, kind="stable")[:n + 1]
         order = order[s[order] > -np.inf]
         steps = -np.diff(s[order])

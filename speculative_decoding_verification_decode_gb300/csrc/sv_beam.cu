@@ -12,13 +12,18 @@
 //   in registers, ended as soon as between n and 2n of them lie above): n
 //   candidates lie at or above tau, so only groups whose maximum reaches it
 //   are read again, about n of them, and of those the logits that reach it
-//   are ranked.
+//   are ranked.  An f32 score of row w is off by the row's margin (its
+//   logarithm's error and roundings at the size of c_w - lse_w); a row is held
+//   against tau less the largest margin among the rows that reach tau and less
+//   its own, so beams far below (kept alive at -1e9, or at the lowest f32)
+//   widen nobody's threshold.
 //
 // Order.  Scores of one beam are ordered by its logits, exactly.  Between
 // beams the logarithms' f32 errors count, so pairs of different beams that lie
-// closer than their bound (eps each) send their rows through precise_lse: the sum in 64-bit fixed point from terms good to 2^-37, equal
-// for rows that are permutations of one another, whatever the order.  All
-// scores are then compared as doubles.
+// closer than their bound (eps each) send their rows through precise_lse: the
+// sum in 64-bit fixed point from terms good to 2^-37, equal for rows that are
+// permutations of one another, whatever the order.  All scores are then
+// compared as doubles.
 //
 // eps, relative error of a row's sum (hence absolute error of its log), in
 // units of 2^-24: an exponent's rounding, 1 per unit of its size, which is
@@ -260,6 +265,8 @@ struct Shared {
   double cum[SV_BEAM_MAX_BEAMS];
   float M[SV_BEAM_MAX_BEAMS];
   float add[SV_BEAM_MAX_BEAMS];  // f32 score = logit + add; -inf: no candidates
+  float margin[SV_BEAM_MAX_BEAMS];  // by which that score may be off
+  float thr[SV_BEAM_MAX_BEAMS];     // f32 scores below are not among the n best
   unsigned char ended[SV_BEAM_MAX_BEAMS], precise[SV_BEAM_MAX_BEAMS], again[SV_BEAM_MAX_BEAMS];
   unsigned long long table[33];  // 2^(j / 32), j = -16..16, units of 2^-61
   unsigned long long sum_hi[kPickWarps], sum_lo[kPickWarps];
@@ -451,9 +458,14 @@ __device__ __forceinline__ void score_entries(Shared& sm, int from, int L) {
   __syncthreads();
 }
 
-// f32 scores of logit l of row w may be off the exact ones by this much.
-__device__ __forceinline__ float margin(double eps, float add_max, float tau) {
-  return static_cast<float>(eps) + (add_max + fabsf(tau)) * 0x1p-22f;
+// A row's f32 addend and margin from its score and logarithm.  An addend that
+// leaves f32's range says nothing.
+__device__ __forceinline__ float set_add(Shared& sm, int w, double eps) {
+  const double a = sm.cum[w] - sm.lse[w];
+  const bool fits = a >= -3.4028234663852886e38;
+  sm.add[w] = fits ? static_cast<float>(a) : -3.4028234663852886e38f;
+  sm.margin[w] = fits ? static_cast<float>(eps) + fabsf(sm.add[w]) * 0x1p-22f : INFINITY;
+  return sm.add[w];
 }
 
 // More candidates than the lists hold (many equal logits, rows in ascending
@@ -461,7 +473,7 @@ __device__ __forceinline__ float margin(double eps, float add_max, float tau) {
 // best so far.  Later equals lose their ties, so a full list only admits
 // strictly better entries.
 template <typename T>
-__device__ __noinline__ int ordered_pass(Shared& sm, const Params& P, int b, float thr) {
+__device__ __noinline__ int ordered_pass(Shared& sm, const Params& P, int b) {
   constexpr int E = Elem<T>::E, kTileVecs = 256;  // 4 groups; at most 2048 entries
   constexpr int kTileGroups = kTileVecs / kGroupVecs;
   const int tiles = (P.groups + kTileGroups - 1) / kTileGroups;
@@ -484,7 +496,7 @@ __device__ __noinline__ int ordered_pass(Shared& sm, const Params& P, int b, flo
         const float* gm = P.gmax + (static_cast<long long>(b) * P.W + w) * P.groups;
         float m = -INFINITY;
         for (int g = tile * kTileGroups; g < min(P.groups, (tile + 1) * kTileGroups); ++g) m = fmaxf(m, gm[g]);
-        may = m > -INFINITY && m + sm.add[w] >= thr && (have < P.n || f64_key(score_of(sm, w, m)) > worst);
+        may = m > -INFINITY && m + sm.add[w] >= sm.thr[w] && (have < P.n || f64_key(score_of(sm, w, m)) > worst);
       }
     }
     if (may) atomicMin(&sm.next, static_cast<int>(threadIdx.x));
@@ -568,7 +580,6 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const __grid_constan
   unsigned top = 0, low = 0xFFFFFFFFu;
   int finite = 0;
   bool bad = false, large = false;
-  float add_max = 0.f;
   auto put = [&](int at, float x) {
     const unsigned k = f32_key(x);
     sm.unit[at] = k;
@@ -611,8 +622,9 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const __grid_constan
       sm.cum[w] = c;
       sm.lse[w] = lse;
       sm.M[w] = M;
-      if (M > -INFINITY) add = static_cast<float>(static_cast<double>(c) - lse);
-      sm.add[w] = add;
+      sm.add[w] = -INFINITY;
+      sm.margin[w] = 0.f;
+      if (M > -INFINITY) add = set_add(sm, w, P.eps);
       sm.ended[w] = ended;
       sm.precise[w] = 0;
       sm.again[w] = M > -INFINITY && fabsf(M) > kLarge;
@@ -620,7 +632,6 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const __grid_constan
     bad |= isnan(c) || c == INFINITY || isnan(M) || M == INFINITY;
     large |= M > -INFINITY && fabsf(M) > kLarge;
     add = __shfl_sync(0xFFFFFFFFu, add, 0);
-    if (add > -INFINITY) add_max = fmaxf(add_max, fabsf(add));
     if (ended && lane == 0) m[0] = c;
     const float plus = ended ? 0.f : add;
 #pragma unroll
@@ -638,17 +649,15 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const __grid_constan
     return;
   }
   if (__syncthreads_or(large)) {  // rows whose fast sum says nothing: precisely, and their scores again
-    add_max = 0.f;
     top = 0;
     low = 0xFFFFFFFFu;
     finite = 0;
     for (int w = 0; w < P.W; ++w) {
       if (sm.again[w]) {
         precise_lse<T>(sm, P, b, w);
-        if (tid == 0) sm.add[w] = static_cast<float>(sm.cum[w] - sm.lse[w]);
+        if (tid == 0) set_add(sm, w, P.eps);
         __syncthreads();
       }
-      if (sm.add[w] > -INFINITY) add_max = fmaxf(add_max, fabsf(sm.add[w]));
       for (int u = tid; u < units; u += kPickThreads)
         put(w * units + u, sm.ended[w] ? (u == 0 ? static_cast<float>(sm.cum[w]) : -INFINITY)
                                        : sm.add[w] > -INFINITY ? unit_max(w, u) + sm.add[w] : -INFINITY);
@@ -658,20 +667,15 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const __grid_constan
   // tau: at least n units reach it, and hardly more than 2 n
   top = __reduce_max_sync(0xFFFFFFFFu, top);
   low = __reduce_min_sync(0xFFFFFFFFu, low);
-  add_max = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(add_max)));
-  if (lane == 0) {
-    sm.sum_hi[warp] = static_cast<unsigned long long>(__float_as_uint(add_max)) << 32 | top;
-    sm.sum_lo[warp] = low;
-  }
+  if (lane == 0) sm.sum_lo[warp] = static_cast<unsigned long long>(top) << 32 | low;
   int turn = 0;
   const int all = block_sum(sm, finite, turn);
 #pragma unroll 1
   for (int w = 0; w < kPickWarps; ++w) {
-    top = max(top, static_cast<unsigned>(sm.sum_hi[w]));
+    top = max(top, static_cast<unsigned>(sm.sum_lo[w] >> 32));
     low = min(low, static_cast<unsigned>(sm.sum_lo[w]));
-    add_max = fmaxf(add_max, __uint_as_float(static_cast<unsigned>(sm.sum_hi[w] >> 32)));
   }
-  float thr = -INFINITY;
+  unsigned thr_key = none + 1;  // of the lowest threshold of a row
   if (all >= P.n) {
     unsigned lo = low, hi = top + 1;  // at least n units >= lo, fewer than n >= hi
     int above = all;
@@ -690,21 +694,37 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const __grid_constan
       }
     }
     const float tau = key_f32(lo);
-    thr = tau - 2.f * margin(P.eps, add_max, tau);
+    // (every warp computes, and writes, the same)
+    float widest = 0.f, all_widest = 0.f;
+#pragma unroll 1
+    for (int w = lane; w < P.W; w += 32) {
+      const float best = sm.ended[w] ? static_cast<float>(sm.cum[w]) : sm.M[w] + sm.add[w];  // (-inf where it has none)
+      if (best >= tau) widest = fmaxf(widest, sm.margin[w]);
+      all_widest = fmaxf(all_widest, sm.margin[w]);
+    }
+    widest = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(widest)));
+    all_widest = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(all_widest)));
+    const float base = tau - fabsf(tau) * 0x1p-21f - widest;
+#pragma unroll 1
+    for (int w = lane; w < P.W; w += 32) sm.thr[w] = base - sm.margin[w];
+    thr_key = max(thr_key, f32_key(base - all_widest));
+  } else {
+    for (int w = lane; w < P.W; w += 32) sm.thr[w] = -INFINITY;
   }
+  __syncwarp();
 
   // the groups that reach it, then their logits that do
-  const unsigned thr_key = max(f32_key(thr), none + 1);
 #pragma unroll 1
   for (int i = tid; i < total; i += kPickThreads)
     if (sm.unit[i] >= thr_key) {
       const int w = i / units, u = i - w * units;
+      if (!(key_f32(sm.unit[i]) >= sm.thr[w])) continue;
       if (sm.ended[w]) {
         append(sm, P.V, w, P.eos, 0.f);
       } else {
 #pragma unroll 1
         for (int g = u * q; g < min(P.groups, u * q + q); ++g)
-          if (q == 1 || P.gmax[(r0 + w) * P.groups + g] + sm.add[w] >= thr) {
+          if (q == 1 || P.gmax[(r0 + w) * P.groups + g] + sm.add[w] >= sm.thr[w]) {
             const int at = atomicAdd(&sm.n_groups, 1);
             if (at < kGroupList) sm.group[at] = make_int2(w, g);
           }
@@ -718,7 +738,7 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const __grid_constan
       const int2 wg = sm.group[j / 2];
       const Row<T> row(static_cast<const T*>(P.logits) + (r0 + wg.x) * P.stride, P.V);
       const long long v = static_cast<long long>(wg.y) * kGroupVecs + 32 * (j & 1) + lane;
-      const float add = sm.add[wg.x];
+      const float add = sm.add[wg.x], thr = sm.thr[wg.x];
       float x[E];
       Elem<T>::unpack(row.load(v), x);
       const int e = static_cast<int>(row.first(v));
@@ -736,7 +756,7 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const __grid_constan
     __syncthreads();
     for (int w = 0; w < P.W; ++w)
       if (sm.again[w] && !sm.ended[w] && !sm.precise[w]) precise_lse<T>(sm, P, b, w);
-    L = ordered_pass<T>(sm, P, b, thr);
+    L = ordered_pass<T>(sm, P, b);
     score_entries(sm, 0, L);
     sort_entries(sm, L, P.n);
   } else {
@@ -774,8 +794,10 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const __grid_constan
     if (tid < L) {
       const int i = sm.order[tid];
       s = static_cast<float>(key_f64(sm.key[i]));
-      p = sm.row[i];
-      t = sm.index[i] - p * P.V;
+      if (s > -INFINITY) {  // (or it lies below f32's range)
+        p = sm.row[i];
+        t = sm.index[i] - p * P.V;
+      }
     }
     const long long o = static_cast<long long>(b) * P.n + tid;
     P.out_s[o] = s;

@@ -175,6 +175,35 @@ def test_select_extreme_logits():
     check(x, c, 5, need_gap=False)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("low", [-1e9, -1e30, float(torch.finfo(torch.float32).min)])
+def test_select_beams_at_the_lowest(dtype, low):
+    """Beams held off by a huge negative score (a search's first step): they
+    change nothing while the others have candidates enough, and follow them
+    where they have not.  With tokens at the type's lowest value as well, a
+    score can lie below f32's range: that is no candidate."""
+    x, c = make(14, 4, 4, 20000, dtype)
+    c[:, 1:] = low
+    c[1, 2] = c[0, 0]
+    x[2, 0, 5:] = -float("inf")
+    x[3] = torch.finfo(DT[dtype]).min
+    x[3, :, 77] = 1.0
+    check(x, c, 8, need_gap=False)
+    check(x, c, 128, need_gap=False)
+
+
+def test_select_refusals():
+    x, c = make(15, 2, 3, 500, "bf16")
+    with pytest.raises(ValueError, match="workspace"):
+        sv().beam_select(x, c, 4, workspace=torch.empty(1 << 20, dtype=torch.uint8))
+    for kw in (dict(n=1 << 32), dict(n=4, eos=(1 << 32) + 5)):
+        with pytest.raises(ValueError, match="below"):
+            sv().beam_select(x, c, **kw)
+    for n in (0, -1, 129, 1 << 30):
+        with pytest.raises(sv().SVError):
+            sv().beam_select(x, c, n)
+
+
 def test_select_far_offsets():
     """Rows beyond 2^31 elements from the first."""
     V, stride = 1500, (1 << 28) + 8
