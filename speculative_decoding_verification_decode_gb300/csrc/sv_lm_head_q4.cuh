@@ -176,6 +176,21 @@ __device__ __forceinline__ bool wait_or_abort(Bars& bars, uint64_t* bar, uint32_
   return false;
 }
 
+// The same for a warp.
+__device__ __forceinline__ bool warp_wait(Bars& bars, uint64_t* bar, uint32_t parity, unsigned* err) {
+  return __all_sync(0xFFFFFFFFu, wait_or_abort(bars, bar, parity, err));
+}
+__device__ __forceinline__ bool warp_wait_bounded(uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xFFFFFFFFu, svk::mbar_wait_bounded(bar, parity));
+}
+
+// One lane of the warp, the same every time.
+__device__ __forceinline__ bool elected() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+  return p != 0;
+}
+
 // Two codes as 16-bit integers in a word: base + code, where base is a power
 // of two whose unit in the last place is 1, then minus (base + zero), exact.
 template <typename T>
@@ -252,8 +267,30 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
+// Words `from + 4 k` of every row of a tile to shared memory by `warps` warps,
+// this the `first`: word k of row r for the lanes' (r, k), a lane's next rows
+// 32 / kWords times `warps` on.  Those lie 4 apart or more, 8 for bytes, so
+// their places within a word are alike.
+template <int kWords>
+__device__ __forceinline__ void fetch_words(uintptr_t from, long long row_bytes, int bytes, uint32_t* to, int stride,
+                                            int rows, int lane, int warps, int first = 0) {
+  constexpr int kRows = 32 / kWords;  // per load
+  const int k = lane % kWords;
+  int r = first * kRows + lane / kWords;
+  const uintptr_t at = from + r * row_bytes;
+  uintptr_t word = (at & ~static_cast<uintptr_t>(3)) + 4 * k;
+  if (word >= at + bytes) return;
+  uint32_t dst = smem_u32(to + r * stride + k);
+#pragma unroll 4
+  for (; r < rows; r += warps * kRows) {
+    cp_async4(dst, reinterpret_cast<const void*>(word));
+    word += warps * kRows * row_bytes;
+    dst += warps * kRows * stride * 4;
+  }
+}
+
 template <typename T, int N, int G, int H>
-__global__ void __launch_bounds__(288 * H + 64, H == 1 ? 2 : 1)
+__global__ void __launch_bounds__(32 * 10 * H, H == 1 ? 2 : 1)
     q4_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap h0,
               const __grid_constant__ CUtensorMap h1, const __grid_constant__ CUtensorMap whole,
               const __grid_constant__ Args g) {
@@ -277,18 +314,18 @@ __global__ void __launch_bounds__(288 * H + 64, H == 1 ? 2 : 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < g.stages; ++s) {
       mbar_init(&bars.full[s], 1 + 32 * kHelp);
-      mbar_init(&bars.empty[s], kWarps + 1);
+      mbar_init(&bars.empty[s], kWarps + H);
     }
     for (int h = 0; h < 2; ++h)
       for (int i = 0; i < kMaxRing; ++i) {
         mbar_init(&bars.a_full[h][i], 8);
         mbar_init(&bars.d_full[h][i], 1);
       }
-    mbar_init(&bars.done, 1);
+    mbar_init(&bars.done, H);
     bars.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == kWarps + kHelp + 1) {
+  if (warp == kWarps + kHelp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&bars.tmem)),
                  "r"(H * kHalfCols)
                  : "memory");
@@ -302,15 +339,23 @@ __global__ void __launch_bounds__(288 * H + 64, H == 1 ? 2 : 1)
   constexpr int kStep = step_of(G, N), kGroups = kStep / G, kSteps = kStageK / kStep;
   constexpr int a_cols = kStep / 2, d_cols = kGroups * N, d_at = ring * a_cols;  // a half's columns: operands, then results
 
-  if (warp == kWarps + kHelp) {
-    // ---- producer: one thread
-    if (lane == 0) {
-      int gk = 0, s = 0, use = 0;  // stages issued, slot, times round
-      for (int t = blockIdx.x; t < g.tiles && !bars.abort; t += gridDim.x)
-        for (int blk = 0; blk < g.blocks && !bars.abort; ++blk)
-          for (int ks = 0; ks < g.nk; ++ks, ++gk) {
-            if (use > 0 && !wait_or_abort(bars, &bars.empty[s], (use - 1) & 1, g.err)) break;
-            const uint32_t dst = smem_u32(smem + s * stage_bytes);
+  if (warp >= kWarps && warp < kWarps + kHelp) {
+    // ---- supply: codes and states by TMA (one lane of the first warp), the
+    // scales and zeros of 128 rows each as the 32-bit words that hold them
+    const int base_row = (warp - kWarps) * 128;
+    const int elem = g.scale_dtype == SV_F32 ? 4 : 2;
+    const bool copies = warp == kWarps && elected();
+    int s = 0, use = 0, issued = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; ok && t < g.tiles; t += gridDim.x) {
+      const long long v0 = static_cast<long long>(t) * g.R + base_row;
+      const int rows = static_cast<int>(min(static_cast<long long>(min(128, g.R - base_row)), g.V - v0));
+      for (int blk = 0; ok && blk < g.blocks; ++blk)
+        for (int ks = 0; ok && ks < g.nk; ++ks) {
+          if (use > 0) ok = warp_wait(bars, &bars.empty[s], (use - 1) & 1, g.err);
+          if (!ok) break;
+          if (copies) {
+            const uint32_t dst = smem_u32(smem) + s * stage_bytes;
             mbar_arrive_expect_tx(&bars.full[s], stage_bytes);
             tma_load_2d(dst, &wmap, ks * 128, t * g.R, &bars.full[s]);
             if (blk * N + N <= g.split) {  // the first set's rows alone, in boxes of N
@@ -318,7 +363,7 @@ __global__ void __launch_bounds__(288 * H + 64, H == 1 ? 2 : 1)
               for (int c = 0; c < kStageK / 64; ++c)
                 tma_load_2d(dst + w_bytes + c * N * 128, &whole, ks * kStageK + c * 64, blk * N, &bars.full[s]);
             } else {
-#pragma unroll 2
+#pragma unroll 1
               for (int r = 0; r < N; r += 8) {  // 8 rows of one of the two row sets
                 const int v = blk * N + r;
                 const bool second = v >= g.split;
@@ -329,49 +374,16 @@ __global__ void __launch_bounds__(288 * H + 64, H == 1 ? 2 : 1)
                   tma_load_2d(dst + w_bytes + c * N * 128 + r * 128, map, ks * kStageK + c * 64, y, &bars.full[s]);
               }
             }
-            if (++s == g.stages) {
-              s = 0;
-              ++use;
-            }
           }
-      // no copy may still be writing shared memory at exit; once a role has
-      // given up, a stage may lack the scale warps' arrivals for good
-      for (int k = gk - g.stages > 0 ? gk - g.stages : 0; k < gk; ++k)
-        if (!svk::mbar_wait_bounded(&bars.full[k % g.stages], (k / g.stages) & 1)) give_up(bars, g.err);
-    }
-  } else if (warp >= kWarps && warp < kWarps + kHelp) {
-    // ---- scales (and zeros) of 128 rows, as the 32-bit words that hold them:
-    // lanes take neighbouring words of a row
-    const int base_row = (warp - kWarps) * 128;
-    const int elem = g.scale_dtype == SV_F32 ? 4 : 2;
-    const int sw = 31 - __clz(per_stage);            // log2 of the words looked at per row: per_stage covers both types
-    const int zw = per_stage == 8 ? 2 : 1;
-    int s = 0, use = 0;
-    bool ok = true;
-    for (int t = blockIdx.x; ok && t < g.tiles; t += gridDim.x) {
-      const int v0 = t * g.R + base_row;
-      const int rows = min(min(128, g.R - base_row), g.V - v0);
-      for (int blk = 0; ok && blk < g.blocks; ++blk)
-        for (int ks = 0; ok && ks < g.nk; ++ks) {
-          if (use > 0) ok = __all_sync(0xFFFFFFFFu, wait_or_abort(bars, &bars.empty[s], (use - 1) & 1, g.err));
-          if (!ok) break;
+          ++issued;
+          __syncwarp();
           const int j0 = ks * per_stage, n = min(per_stage, g.G - j0);
-          uint32_t* sd = sbuf + (s * 128 * H + base_row) * kSWords;
-          for (int e = lane; e < rows << sw; e += 32) {
-            const int r = e >> sw, k = e & ((1 << sw) - 1);
-            const uintptr_t at = reinterpret_cast<uintptr_t>(g.scales) + (static_cast<long long>(v0 + r) * g.G + j0) * elem;
-            const uintptr_t word = (at & ~static_cast<uintptr_t>(3)) + 4 * k;
-            if (word < at + n * elem) cp_async4(smem_u32(sd + r * kSWords + k), reinterpret_cast<const void*>(word));
-          }
-          if (g.zeros) {
-            uint32_t* zd = zbuf + (s * 128 * H + base_row) * z_words;
-            for (int e = lane; e < rows << zw; e += 32) {
-              const int r = e >> zw, k = e & ((1 << zw) - 1);
-              const uintptr_t at = reinterpret_cast<uintptr_t>(g.zeros) + static_cast<long long>(v0 + r) * g.G + j0;
-              const uintptr_t word = (at & ~static_cast<uintptr_t>(3)) + 4 * k;
-              if (word < at + n) cp_async4(smem_u32(zd + r * z_words + k), reinterpret_cast<const void*>(word));
-            }
-          }
+          fetch_words<per_stage>(reinterpret_cast<uintptr_t>(g.scales) + (v0 * g.G + j0) * elem,
+                                 static_cast<long long>(g.G) * elem, n * elem, sbuf + (s * 128 * H + base_row) * kSWords,
+                                 kSWords, rows, lane, 1);
+          if (g.zeros)
+            fetch_words<per_stage == 8 ? 4 : 2>(reinterpret_cast<uintptr_t>(g.zeros) + v0 * g.G + j0, g.G, n,
+                                                zbuf + (s * 128 * H + base_row) * z_words, z_words, rows, lane, 1);
           cp_async_arrive(&bars.full[s]);
           if (++s == g.stages) {
             s = 0;
@@ -380,49 +392,57 @@ __global__ void __launch_bounds__(288 * H + 64, H == 1 ? 2 : 1)
         }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
-  } else if (warp == kWarps + kHelp + 1) {
-    // ---- MMA: one thread issues
-    if (lane == 0) {
-      int s = 0, use = 0, buf = 0, turn_no = 0;
-      bool ok = true;
-      for (int t = blockIdx.x; ok && t < g.tiles; t += gridDim.x)
-        for (int blk = 0; ok && blk < g.blocks; ++blk)
-          for (int ks = 0; ok && ks < g.nk; ++ks) {
-            ok = wait_or_abort(bars, &bars.full[s], use & 1, g.err);
-            const uint32_t b_lo = desc_lo(smem_u32(smem + s * stage_bytes) + w_bytes);
-            const int n = min(per_stage, g.G - ks * per_stage);
+    // no copy may still be writing shared memory at exit; once a role has
+    // given up, a stage may lack the other scale warp's arrivals for good
+    if (copies)
+      for (int k = issued - g.stages > 0 ? issued - g.stages : 0; k < issued; ++k)
+        if (!svk::mbar_wait_bounded(&bars.full[k % g.stages], (k / g.stages) & 1)) give_up(bars, g.err);
+    __syncwarp();
+  } else if (warp >= kWarps + kHelp) {
+    // ---- MMA: a warp per half; all its lanes run the loops, so that addresses
+    // stay in uniform registers, and one issues
+    const int h = warp - (kWarps + kHelp);
+    const uint32_t a0 = tmem + h * kHalfCols, d0 = a0 + d_at;
+    const bool issues = elected();
+    int s = 0, use = 0, buf = 0, turn_no = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; ok && t < g.tiles; t += gridDim.x)
+      for (int blk = 0; ok && blk < g.blocks; ++blk)
+        for (int ks = 0; ok && ks < g.nk; ++ks) {
+          ok = warp_wait(bars, &bars.full[s], use & 1, g.err);
+          const uint32_t b_lo = desc_lo(smem_u32(smem) + s * stage_bytes + w_bytes);
+          const int n = min(per_stage, g.G - ks * per_stage);
+#pragma unroll 1
+          for (int i = 0; i < kSteps; ++i) {
+            if (!ok || i * kGroups >= n) break;
+            ok = warp_wait(bars, &bars.a_full[h][buf], turn_no & 1, g.err);
+            if (!ok) break;
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            constexpr uint32_t kChunk = N * 128 / 16;  // 64 columns of the states, in descriptor units
+            const uint32_t a = a0 + buf * a_cols, dd = d0 + buf * d_cols, b = b_lo + i * (kStep / 64) * kChunk;
+            if (issues) {
 #pragma unroll
-            for (int i = 0; i < kSteps; ++i) {
-              if (!ok || i * kGroups >= n) break;
-#pragma unroll
-              for (int h = 0; h < H; ++h) {
-                ok = ok && wait_or_abort(bars, &bars.a_full[h][buf], turn_no & 1, g.err);
-                if (!ok) break;
-                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                const uint32_t a = tmem + h * kHalfCols + buf * a_cols, dd = tmem + h * kHalfCols + d_at + buf * d_cols;
-#pragma unroll
-                for (int kk = 0; kk < kStep / 16; ++kk) {
-                  constexpr int kChunk = N * 128 / 16;  // 64 columns of the states, in descriptor units
-                  const int k = i * kStep + kk * 16;
-                  mma_ts(dd + kk * 16 / G * N, a + kk * 8, desc_of(b_lo + (k / 64) * kChunk + (k % 64) / 8), kIdesc,
-                         kk * 16 % G ? 1u : 0u);
-                }
-                mma_commit(&bars.d_full[h][buf]);
-              }
-              if (++buf == ring) {
-                buf = 0;
-                ++turn_no;
-              }
+              for (int kk = 0; kk < kStep / 16; ++kk)
+                mma_ts(dd + kk * 16 / G * N, a + kk * 8, desc_of(b + (kk * 16 / 64) * kChunk + (kk * 16 % 64) / 8), kIdesc,
+                       kk * 16 % G ? 1u : 0u);
+              mma_commit(&bars.d_full[h][buf]);
             }
-            if (ok) mma_commit(&bars.empty[s]);
-            if (++s == g.stages) {
-              s = 0;
-              ++use;
+            __syncwarp();
+            if (++buf == ring) {
+              buf = 0;
+              ++turn_no;
             }
           }
-      mma_commit(&bars.done);
-      if (!svk::mbar_wait_bounded(&bars.done, 0)) give_up(bars, g.err);
-    }
+          if (ok && issues) mma_commit(&bars.empty[s]);
+          __syncwarp();
+          if (++s == g.stages) {
+            s = 0;
+            ++use;
+          }
+        }
+    if (issues) mma_commit(&bars.done);
+    __syncwarp();
+    if (!warp_wait_bounded(&bars.done, 0)) give_up(bars, g.err);
   } else {
     // ---- a thread per vocabulary row and warpgroup
     const int half = warp / 8, wg = warp / 4 % 2;
@@ -446,7 +466,7 @@ __global__ void __launch_bounds__(288 * H + 64, H == 1 ? 2 : 1)
         float late[kGroups] = {};  // scales of the step whose results are still to be added
         int pending = 0, rbuf = buf, rturn = turn_no;
         auto add = [&](const float (&scale)[kGroups]) {
-          if (!__all_sync(0xFFFFFFFFu, wait_or_abort(bars, &bars.d_full[half][rbuf], rturn & 1, g.err))) return false;
+          if (!warp_wait(bars, &bars.d_full[half][rbuf], rturn & 1, g.err)) return false;
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 #pragma unroll
           for (int p = 0; p < kGroups; ++p) {
@@ -464,12 +484,12 @@ __global__ void __launch_bounds__(288 * H + 64, H == 1 ? 2 : 1)
           return true;
         };
         for (int ks = 0; ok && ks < g.nk; ++ks) {
-          ok = __all_sync(0xFFFFFFFFu, wait_or_abort(bars, &bars.full[s], use & 1, g.err));
+          ok = warp_wait(bars, &bars.full[s], use & 1, g.err);
           const uint32_t codes = smem_u32(smem) + s * stage_bytes + row * 128;
           const uint32_t srow = smem_u32(sbuf) + (s * 128 * H + row) * kSWords * 4;
           const uint32_t zrow = smem_u32(zbuf) + (s * 128 * H + row) * z_words * 4 + ((z_off + ks * per_stage) & 3);
           const int n = min(per_stage, g.G - ks * per_stage);
-#pragma unroll
+#pragma unroll 1
           for (int i = 0; i < kSteps; ++i) {
             if (!ok || i * kGroups >= n) break;
             float scale[kGroups];
@@ -534,7 +554,7 @@ __global__ void __launch_bounds__(288 * H + 64, H == 1 ? 2 : 1)
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
-  if (warp == kWarps + kHelp + 1) {
+  if (warp == kWarps + kHelp) {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(H * kHalfCols) : "memory");
   }
@@ -613,7 +633,7 @@ sv_status start(Args g, const sv_q4_proj* proj, const void* s0, const void* s1, 
     attr_set[dev] = true;
   }
   const unsigned grid = static_cast<unsigned>(g.tiles < slots ? g.tiles : slots);
-  q4_kernel<T, N, G, H><<<grid, 288 * H + 64, smem, stream>>>(mw, m0, m1, mn, g);
+  q4_kernel<T, N, G, H><<<grid, 32 * 10 * H, smem, stream>>>(mw, m0, m1, mn, g);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return svh::fail(SV_ERR_CUDA, "kernel launch: %s", cudaGetErrorString(e));
   return SV_OK;

@@ -102,27 +102,6 @@ struct FewArgs {
 __host__ __device__ constexpr int few_stride(int n) { return n == 1 ? 1 : n + 1; }
 __host__ __device__ constexpr int few_zstride(int n) { return n == 1 ? 1 : 3; }
 
-// Words `from + 4 k` of every row of a tile to shared memory: word k of row r
-// for the lanes' (r, k), the next rows 32 / kWords on.  The rows of a lane lie
-// 8 apart or more, so their places within a word are alike.
-template <int kWords>
-__device__ __forceinline__ void fetch_words(uintptr_t from, long long row_bytes, int bytes, uint32_t* to, int stride,
-                                            int rows, int lane, int first) {
-  constexpr int kRows = 32 / kWords;  // per load
-  const int k = lane % kWords;
-  int r = first * kRows + lane / kWords;
-  const uintptr_t at = from + r * row_bytes;
-  uintptr_t word = (at & ~static_cast<uintptr_t>(3)) + 4 * k;
-  if (word >= at + bytes) return;
-  uint32_t dst = smem_u32(to + r * stride + k);
-#pragma unroll 4
-  for (; r < rows; r += kFewHelp * kRows) {
-    cp_async4(dst, reinterpret_cast<const void*>(word));
-    word += kFewHelp * kRows * row_bytes;
-    dst += kFewHelp * kRows * stride * 4;
-  }
-}
-
 // NT tiles of 8 states, groups of G, Z: zeros are given, BF: bf16 states (else f16).
 template <int NT, int G, bool Z, bool BF>
 __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_constant__ CUtensorMap wmap,
@@ -223,10 +202,10 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
         const int n = min(kPer, g.G - ks * kPer);
         fetch_words<kPer>(reinterpret_cast<uintptr_t>(g.scales) + (v0 * g.G + ks * kPer) * elem,
                           static_cast<long long>(g.G) * elem, n * elem, sbuf + s * kFewTile * kStride, kStride, n_rows,
-                          lane, warp - kFewWarps);
+                          lane, kFewHelp, warp - kFewWarps);
         if constexpr (Z)
           fetch_words<kPer == 1 ? 1 : 2>(reinterpret_cast<uintptr_t>(g.zeros) + v0 * g.G + ks * kPer, g.G, n,
-                                         zbuf + s * kFewTile * kZStride, kZStride, n_rows, lane, warp - kFewWarps);
+                                         zbuf + s * kFewTile * kZStride, kZStride, n_rows, lane, kFewHelp, warp - kFewWarps);
         cp_async_arrive(&bars.full[s]);
         if (++s == g.stages) {
           s = 0;
