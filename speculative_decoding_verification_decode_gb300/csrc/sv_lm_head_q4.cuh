@@ -20,12 +20,26 @@
 //     has read the result that the MMA will overwrite.
 //   - two warpgroups share the rows: each turns half of a group's codes and
 //     keeps half of the N sums, so an SM has sixteen warps to hide the steps'
-//     latencies with.  Turning is 1.1 ALU operations per weight, 0.8 of the
-//     memory's rate on this machine, and nothing else may wait in its way:
-//     scales come by cp.async from a warp of their own.
-// A CTA has H halves of 128 rows (8 warps each), H scale warps, a producer
-// and an MMA warp.  Its tiles have R <= 128 H rows, R chosen so that the
-// vocabulary divides evenly over the CTAs (the MMA's idle rows cost nothing).
+//     latencies with.  Nothing else may wait in their way: scales come by
+//     cp.async from warps of their own.
+//   - each half has an MMA warp whose lanes all run the loop, so that
+//     descriptors stay in uniform registers.  One thread that issued for both
+//     halves took 1700 clocks per 128 columns and half, and all waited for it
+//     (44 rows x 152064 x 4096, groups of 128: 177 us, now 135).
+// A CTA has H halves of 128 rows (8 warps each), H warps that supply (the first
+// also starts the copies) and H that issue.  Twenty warps per SM leave 96
+// registers each; a twenty-first left 80 and spilled.  Its tiles have R <= 128 H
+// rows, R chosen so that the vocabulary divides evenly over the CTAs (the MMA's
+// idle rows cost nothing).
+//
+// Measured: 44 rows x 152064 x 4096 of bf16 states, groups of 32: 200 us (28% of
+// the memory's rate), 64: 175, 128: 135.  Without the stores to tensor memory
+// and the turning 127 / - / 89 us, with neither turning nor adding nor MMA 78 /
+// - / 73: what the hand-overs and the stream itself take.  Measured and not
+// taken: warps of their own for the adding (215 / 196 / 157 us), one polling
+// warp per half with the others at a barrier (223 / 198 / 159), 64 columns per
+// step with two buffers for groups of 32 and 64 (207 / 180), four chains of 64
+// rows (254 against 214 then).
 //
 // Every wait is bounded; one that gives up sets bit 0 of *err.
 #pragma once
@@ -43,7 +57,6 @@
 
 namespace svq {
 
-
 using svk::mbar_arrive_expect_tx;
 using svk::mbar_arrive_local;
 using svk::mbar_init;
@@ -57,7 +70,8 @@ constexpr int kMaxRing = 2;
 __host__ __device__ constexpr int per_stage_of(int group) { return kStageK / group; }
 // Columns of W that pass between the warps and the MMA at a time: a hand-over
 // costs some 900 clocks whatever its size, so as many as the results of all
-// their groups leave room for.
+// their groups leave room for (groups of 32, 44 rows: 200 us with one buffer of
+// 128 columns, 207 with two of 64).
 __host__ __device__ constexpr int step_of(int group, int n) { return group == 32 && n == 64 ? 64 : 128; }
 // Operand / result buffers that fit.
 __host__ __device__ constexpr int ring_of(int group, int n) {
