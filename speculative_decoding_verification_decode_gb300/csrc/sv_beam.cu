@@ -12,7 +12,13 @@
 //   in registers, ended as soon as between n and 2n of them lie above): n
 //   candidates lie at or above tau, so only groups whose maximum reaches it
 //   are read again, about n of them, and of those the logits that reach it
-//   are ranked.  An f32 score of row w is off by the row's margin (its
+//   are ranked.
+//
+// A small call (a launch and the host's time for it are what it costs) is one
+// kernel instead: a cluster of eight CTAs per sequence, whose warps each stream
+// a slice of a row; the first CTA goes on as the second kernel does.
+//
+// An f32 score of row w is off by the row's margin (its
 //   logarithm's error and roundings at the size of c_w - lse_w); a row is held
 //   against tau less the largest margin among the rows that reach tau and less
 //   its own, so beams far below (kept alive at -1e9, or at the lowest f32)
@@ -45,6 +51,7 @@ namespace svs {
 
 constexpr int kRowThreads = 256, kRowWarps = kRowThreads / 32;
 constexpr int kPickThreads = 512, kPickWarps = kPickThreads / 32;
+constexpr int kCluster = 8;      // CTAs of a small call's sequence
 constexpr int kGroupVecs = 64;   // 16-byte vectors per group: two per lane of a warp
 constexpr int kCap = 4096;       // candidate entries a CTA holds (power of two)
 constexpr int kGroupList = 1024; // groups read again before the ordered pass takes over
@@ -200,19 +207,13 @@ __device__ __forceinline__ void join(float& M, float& s, float M2, float s2) {
   M = m;
 }
 
+// Groups g, g + 1, then `step` further on, up to `end` of a row by a warp: their
+// maxima, and (M, s) of what the warp saw (s per lane).
 template <typename T>
-__global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant__ Params P) {
+__device__ __forceinline__ void stream_groups(const Row<T>& row, float* gmax, int groups, int g, int end, int step, int lane,
+                                              float& M, float& s) {
   constexpr int E = Elem<T>::E;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const long long r = blockIdx.x / static_cast<unsigned>(P.slices);
-  const int slice = static_cast<int>(blockIdx.x % static_cast<unsigned>(P.slices));
-  if ((P.finished && P.finished[r]) || P.scores[r] == -INFINITY) return;
-  const Row<T> row(static_cast<const T*>(P.logits) + r * P.stride, P.V);
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int g_end = min(P.groups, (slice + 1) * P.per_slice);
-  float* gmax = P.gmax + r * P.groups;
-  float M = -INFINITY, s = 0.f;
-  for (int g = slice * P.per_slice + 2 * warp; g < g_end; g += 2 * kRowWarps) {
+  for (; g < end; g += step) {
     const long long v0 = static_cast<long long>(g) * kGroupVecs + lane;
     uint4 q[4];
     if (row.inside(v0 - lane, v0 - lane + 2 * kGroupVecs - 1)) {
@@ -225,7 +226,7 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
     const float ma = warp_max_nan(Elem<T>::max_of(q[0], q[1])), mb = warp_max_nan(Elem<T>::max_of(q[2], q[3]));
     if (lane == 0) {
       gmax[g] = ma;
-      if (g + 1 < P.groups) gmax[g + 1] = mb;
+      if (g + 1 < groups) gmax[g + 1] = mb;
     }
     const float m = svk::fmax_nan(M, svk::fmax_nan(ma, mb));
     if (m > -INFINITY && m < INFINITY) {
@@ -244,6 +245,19 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
   }
 #pragma unroll
   for (int o = 16; o > 0; o /= 2) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant__ Params P) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const long long r = blockIdx.x / static_cast<unsigned>(P.slices);
+  const int slice = static_cast<int>(blockIdx.x % static_cast<unsigned>(P.slices));
+  if ((P.finished && P.finished[r]) || P.scores[r] == -INFINITY) return;
+  const Row<T> row(static_cast<const T*>(P.logits) + r * P.stride, P.V);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int g_end = min(P.groups, (slice + 1) * P.per_slice);
+  float M = -INFINITY, s = 0.f;
+  stream_groups(row, P.gmax + r * P.groups, P.groups, slice * P.per_slice + 2 * warp, g_end, 2 * kRowWarps, lane, M, s);
   __shared__ float2 part[kRowWarps];
   if (lane == 0) part[warp] = make_float2(M, s);
   __syncthreads();
@@ -562,19 +576,19 @@ __device__ __noinline__ int ordered_pass(Shared& sm, const Params& P, int b) {
 // values: what it takes is barriers, trips to L2 and instruction fetches.  So
 // a warp takes a row's maxima and sums together, in one round of loads; loops
 // stay rolled; and nothing divides.
-template <typename T>
-__global__ void __launch_bounds__(kPickThreads) pick_kernel(const __grid_constant__ Params P) {
+template <typename T, bool kOne>
+__device__ __forceinline__ void pick(const Params& P, int b) {
   constexpr int E = Elem<T>::E;
   extern __shared__ __align__(16) unsigned char raw[];
   Shared& sm = *reinterpret_cast<Shared*>(raw);
-  const int b = blockIdx.x, tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const long long r0 = static_cast<long long>(b) * P.W;
   if (tid == 0) sm.n_groups = sm.n_entries = sm.redo = 0;
   int q = 1;  // a unit of the bisection: q groups of a row
   while (static_cast<long long>((P.groups + q - 1) / q) * P.W > kUnits) ++q;
   const int units = q == 1 ? P.groups : (P.groups + q - 1) / q, total = units * P.W;
   const unsigned none = f32_key(-INFINITY);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if constexpr (!kOne) asm volatile("griddepcontrol.wait;" ::: "memory");
 
   // the rows' logarithms, and the units' best scores
   unsigned top = 0, low = 0xFFFFFFFFu;
@@ -807,9 +821,31 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const __grid_constan
   if (tid == 0) P.st[b] = 0u;
 }
 
+template <typename T>
+__global__ void __launch_bounds__(kPickThreads) pick_kernel(const __grid_constant__ Params P) {
+  pick<T, false>(P, blockIdx.x);
+}
+
+template <typename T>
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPickThreads) one_kernel(const __grid_constant__ Params P) {
+  const int b = blockIdx.x / kCluster, rank = blockIdx.x % kCluster, lane = threadIdx.x % 32;
+  for (int i = rank * kPickWarps + threadIdx.x / 32; i < P.W * P.slices; i += kCluster * kPickWarps) {
+    const int w = i / P.slices, slice = i - w * P.slices;
+    const long long r = static_cast<long long>(b) * P.W + w;
+    if ((P.finished && P.finished[r]) || P.scores[r] == -INFINITY) continue;
+    const Row<T> row(static_cast<const T*>(P.logits) + r * P.stride, P.V);
+    float M = -INFINITY, s = 0.f;
+    stream_groups(row, P.gmax + r * P.groups, P.groups, slice * P.per_slice, min(P.groups, (slice + 1) * P.per_slice), 2, lane, M, s);
+    if (lane == 0) P.part[r * P.slices + slice] = make_float2(M, s);
+  }
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  if (rank == 0) pick<T, true>(P, b);
+}
+
 // Sizes of a call: groups of a row at the worst alignment, slices, workspace.
 struct Plan {
   int groups, per_slice, slices;
+  bool one;  // one kernel
   size_t part_bytes, bytes;
 };
 
@@ -823,6 +859,13 @@ Plan plan_of(int batch, int beams, int vocab, int elem) {
   // two per warp (one load round) and sixteen
   int per = 2 * kRowWarps;
   while (per < 16 * kRowWarps && rows * ((p.groups + per - 1) / per) > 152 * 5 * 4) per *= 2;
+  // one kernel where a cluster streams a sequence about as fast as the host
+  // issues a call, and the clusters find room at once
+  p.one = batch <= 152 / kCluster && static_cast<long long>(beams) * vocab * elem <= kCluster * 196608;
+  if (p.one) {
+    const int s = kCluster * kPickWarps / beams;  // slices of a row: a warp each
+    per = ((p.groups + s - 1) / s + 1) / 2 * 2;
+  }
   p.per_slice = per;
   p.slices = (p.groups + per - 1) / per;
   p.part_bytes = (static_cast<size_t>(rows) * p.slices * sizeof(float2) + 15) / 16 * 16;
@@ -898,14 +941,22 @@ sv_status sv_beam_select(const void* logits, sv_dtype dtype, int64_t row_stride,
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   // the shared-memory opt-in, once per (device, element type)
   static bool attr_set[64][3] = {};
-  auto go = [&](void (*rows)(svs::Params), void (*pick)(svs::Params)) -> sv_status {
+  auto go = [&](void (*rows)(svs::Params), void (*pick)(svs::Params), void (*one)(svs::Params)) -> sv_status {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 0;
     if (!attr_set[dev][dtype]) {
-      const cudaError_t e = cudaFuncSetAttribute(pick, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 static_cast<int>(sizeof(svs::Shared)));
+      cudaError_t e = cudaFuncSetAttribute(pick, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           static_cast<int>(sizeof(svs::Shared)));
+      if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(one, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(sizeof(svs::Shared)));
       if (e != cudaSuccess) return svh::fail(SV_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
       attr_set[dev][dtype] = true;
+    }
+    if (plan.one) {
+      one<<<static_cast<unsigned>(batch * svs::kCluster), svs::kPickThreads, sizeof(svs::Shared), st>>>(p);
+      const cudaError_t e = cudaGetLastError();
+      if (e != cudaSuccess) return svh::fail(SV_ERR_CUDA, "kernel launch: %s", cudaGetErrorString(e));
+      return SV_OK;
     }
     rows<<<static_cast<unsigned>(ctas), svs::kRowThreads, 0, st>>>(p);
     cudaError_t e = cudaGetLastError();
@@ -927,9 +978,9 @@ sv_status sv_beam_select(const void* logits, sv_dtype dtype, int64_t row_stride,
     return SV_OK;
   };
   switch (dtype) {
-    case SV_F32: return go(svs::rows_kernel<float>, svs::pick_kernel<float>);
-    case SV_BF16: return go(svs::rows_kernel<__nv_bfloat16>, svs::pick_kernel<__nv_bfloat16>);
-    default: return go(svs::rows_kernel<__half>, svs::pick_kernel<__half>);
+    case SV_F32: return go(svs::rows_kernel<float>, svs::pick_kernel<float>, svs::one_kernel<float>);
+    case SV_BF16: return go(svs::rows_kernel<__nv_bfloat16>, svs::pick_kernel<__nv_bfloat16>, svs::one_kernel<__nv_bfloat16>);
+    default: return go(svs::rows_kernel<__half>, svs::pick_kernel<__half>, svs::one_kernel<__half>);
   }
 }
 
