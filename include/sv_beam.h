@@ -58,7 +58,7 @@ size_t sv_beam_select_workspace_size(int32_t batch, int32_t beams, int32_t vocab
  * workspace: sv_beam_select_workspace_size() bytes, 16-byte aligned, no
  *          initial contents needed.  Calls that share one must not overlap on
  *          the GPU.
- * Two launches; nothing is enqueued when the call is refused.
+ * One or two launches; nothing is enqueued when the call is refused.
  * 1 <= beams <= SV_BEAM_MAX_BEAMS, 1 <= n <= SV_BEAM_MAX_CANDIDATES,
  * beams * vocab < 2^31.
  */
