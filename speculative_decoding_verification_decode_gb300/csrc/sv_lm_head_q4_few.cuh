@@ -2,9 +2,9 @@
 //
 // With so few rows the product is a stream of codes, and what must not stall
 // it is the way from a code to an operand.  The tensor-memory kernel pays a
-// store to tensor memory and two barrier trips per group on that way (61 us of
-// its 150 at 11 rows, V = 128256, d = 4096 are left with the arithmetic taken
-// out); here a code goes from a register straight into an mma.sync operand
+// store to tensor memory and two barrier trips per 128 columns on that way (135
+// us at 11 rows, V = 128256, d = 4096, groups of 128; here 80, and 56 to 62 up
+// to 8 rows); here a code goes from a register straight into an mma.sync operand
 // and nothing waits but on the stream itself.  mma.sync runs at 1006
 // multiply-adds per clock and SM (measured): 16 rows use 16 per weight, and
 // the memory delivers 45 weights per clock and SM, so it is fast enough up to
