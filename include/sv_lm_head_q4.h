@@ -18,6 +18,9 @@
  * The logits are those of these weights: products of the states with the
  * integers q - zero, summed in f32 within a group, then scaled and summed over
  * the groups in f32 (no weight is rounded to 16 bits on the way).
+ * Every 64 rows are a pass over the projection: past 64 rows the bf16 projection
+ * of sv_lm_head.h is the faster one (128256 x 4096, groups of 128: 64 rows 148
+ * against 193 us, 96 rows 266 against 205).
  * Requirements: dim a multiple of 32 (16-byte rows), group 32, 64 or 128 (the
  * last group may be cut by dim), states and packed 16-byte aligned.
  */

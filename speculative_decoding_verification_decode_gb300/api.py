@@ -484,8 +484,9 @@ def lm_head_verify(target_states: torch.Tensor, draft_states: torch.Tensor,
                    cu_k: Optional[torch.Tensor] = None, k: Optional[int] = None, flags: int = 0,
                    workspace: Optional[torch.Tensor] = None) -> LMHeadResult:
     """Verification from hidden states (include/sv_lm_head.h): the target and
-    draft positions' logits through the one bf16 projection ``proj [V, d]``,
-    then the mixed greedy / sampled verification of accept_from_logits.
+    draft positions' logits through the one projection ``proj`` (bf16
+    ``[V, d]``, or a ``Q4Projection``, include/sv_lm_head_q4.h, whose states may
+    be f16 too), then the mixed greedy / sampled verification of accept_from_logits.
     Returns the verification results and, for device inputs, the fp32 logits
     it read (views of the workspace, valid until it is reused)."""
     m = _Marshal(target_states)

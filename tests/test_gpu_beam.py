@@ -192,6 +192,31 @@ def test_select_beams_at_the_lowest(dtype, low):
     check(x, c, 128, need_gap=False)
 
 
+def test_select_empty_and_single():
+    """No sequences; one beam whose rows lie apart; scores and flags of other types."""
+    r = sv().beam_select(torch.zeros(0, 3, 50, device=DEV), torch.zeros(0, 3, device=DEV), 5)
+    assert r.scores.shape == (0, 5) and r.status.shape == (0,)
+    x, c = make(16, 4, 5, 900, "bf16")
+    check(x[:, 2:3], c[:, 2:3], 3)  # [4, 1, 900], rows five apart
+    fin = torch.zeros(4, 5, dtype=torch.int64, device=DEV)
+    fin[1, 2] = 3
+    a = sv().beam_select(x, c.double(), 6, fin, 4)
+    b = sv().beam_select(x, c, 6, fin != 0, 4)
+    assert all(torch.equal(u, v) for u, v in zip(a, b))
+
+
+@pytest.mark.parametrize("B,W,V", [(1, 4, 32000), (19, 2, 4000), (20, 2, 4000), (3, 16, 48000), (3, 16, 52000)])
+def test_select_one_kernel_and_two(B, W, V):
+    """Both sides of the rule that takes small calls in one kernel, the
+    workspace asked for being enough and nothing written behind it."""
+    x, c = make(17, B, W, V, "bf16")
+    n = 2 * W
+    need = sv().beam_select_workspace(B, W, V, n).numel()
+    buf = torch.full((need + 4096,), 171, dtype=torch.uint8, device=DEV)
+    check(x, c, n, need_gap=False, workspace=buf[:need])
+    assert (buf[need:] == 171).all()
+
+
 def test_select_refusals():
     x, c = make(15, 2, 3, 500, "bf16")
     with pytest.raises(ValueError, match="workspace"):

@@ -252,3 +252,37 @@ def test_verify_from_states():
                                 cu_k=cu, k=3)
     for a, b in zip(r[:3], v):
         assert torch.equal(a, b)
+
+
+def test_empty_and_single():
+    """No rows, one row given as a vector, no drafts, no sequences."""
+    h, p = make(50, 3, 300, 128, 64)
+    h, q = h.to(DEV), on_dev(p)
+    assert sv().lm_head_logits(h[:0], q).shape == (0, 300)
+    all_rows = sv().lm_head_logits(h, q)
+    assert torch.equal(sv().lm_head_logits(h[1], q), sv().lm_head_logits(h[1:2], q))
+    T = torch.zeros(3, device=DEV)
+    none = torch.zeros(0, dtype=torch.int32, device=DEV)
+    r = sv().lm_head_verify(h, h[:0], q, T, none, torch.rand(3, device=DEV))
+    assert torch.equal(r.next_token.long(), all_rows.argmax(1)) and (r.n_accepted == 0).all()
+    r = sv().lm_head_verify(h[:0], h[:0], q, T[:0], none, T[:0])
+    assert r.n_accepted.shape == (0,)
+
+
+@pytest.mark.parametrize("rows", [3, 30])
+def test_a_workspace_is_enough(rows):
+    """A verification in the caller's workspace, twice: the same results, and
+    nothing written behind it."""
+    V, d, B = 1003, 256, rows
+    h, p = make(51, 2 * B, V, d, 128)
+    h, q = h.to(DEV), on_dev(p)
+    tok = torch.randint(0, V, (B,), generator=torch.Generator().manual_seed(2), dtype=torch.int32).to(DEV)
+    u = torch.rand(2 * B, generator=torch.Generator().manual_seed(3)).to(DEV)
+    T = torch.full((B,), 0.7, device=DEV)
+    need = sv().lm_head_workspace(B, B, V).numel()
+    buf = torch.full((need + 4096,), 171, dtype=torch.uint8, device=DEV)
+    a = sv().lm_head_verify(h, h[:B], q, T, tok, u)
+    for _ in range(2):
+        b = sv().lm_head_verify(h, h[:B], q, T, tok, u, workspace=buf[:need])
+        assert all(torch.equal(x, y) for x, y in zip(a[:3], b[:3]))
+    assert (buf[need:] == 171).all()
