@@ -98,7 +98,8 @@ typedef struct {
  * status   [batch]: 0, or SV_SEQ_BAD_LAYOUT (a parent >= beams, or a length
  *          outside [0, tokens of the shortest timed state]): nothing of that
  *          sequence moves.
- * One launch per 48 states.  1 <= beams <= SV_BEAM_MAX_BEAMS.
+ * One launch per 48 states, those whose addresses, strides and extents are
+ * multiples of 16 bytes apart from the others.  1 <= beams <= SV_BEAM_MAX_BEAMS.
  */
 sv_status sv_beam_reorder(const sv_beam_state* states, int32_t n_states, const int32_t* parents,
                           const int32_t* lengths, int32_t batch, int32_t beams, uint32_t* status,

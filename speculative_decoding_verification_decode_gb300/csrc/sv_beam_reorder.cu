@@ -22,12 +22,16 @@
 namespace svb {
 
 constexpr int kThreads = 256;
-constexpr int kStageBytes = 96 * 1024;  // shared memory of the staged path: two CTAs per SM
+// The staged path's CTAs per SM and shared memory of each: many small ones, whose
+// reading and writing overlap (151 MB whose beams lie 4 bytes off one another:
+// two of 96 KB 38 us, four of 48 KB 35, eight of 24 KB 33.8).
+constexpr int kStagedCtas = 8, kStageBytes = 24 * 1024;
 constexpr int kStates = 48;    // per launch: their descriptions are kernel parameters
 // Bytes of one segment that a CTA takes (of every beam): large ones where there
 // are many (few CTAs to start), small ones where a handful of large ones would
-// leave SMs without work at the end (151 MB in 420 large ones: 44 us).
-constexpr int kLargeChunk = 65536, kSmallChunk = 16384;
+// leave SMs without work at the end (151 MB in 420 large ones 44 us; 0.9 GB of
+// 16 beams' caches with 16 KB 135 us, with 8 KB 132, with 4 KB 138).
+constexpr int kLargeChunk = 65536, kSmallChunk = 8192;
 constexpr long long kManyCtas = 152 * 2 * 8;
 
 struct State {
@@ -49,9 +53,11 @@ struct Params {
 };
 
 // Columns lo + tid, lo + tid + kThreads, ... < hi of one segment, M moves at
-// most, N columns at a time per thread: N x M accesses in flight.
+// most, N columns at a time per thread: N x M accesses in flight.  (`volatile`:
+// offsets kept in registers over the loop would push the data out of them; 16
+// moves took 276 us where they take 132.)
 template <typename U, int M, int N>
-__device__ __forceinline__ void move_columns(char* base, const long long* src, const long long* dst, int m,
+__device__ __forceinline__ void move_columns(char* base, const volatile long long* src, const volatile long long* dst, int m,
                                              long long lo, long long hi) {
   for (long long c = lo + threadIdx.x; c < hi; c += N * kThreads) {
     U v[N][M];
@@ -72,7 +78,7 @@ __device__ __forceinline__ void move_columns(char* base, const long long* src, c
 
 // Bytes lo..hi of one segment in 16-byte accesses: 64 registers of data per
 // thread whatever the number of moves; more moves take narrower accesses.
-__device__ __forceinline__ void move_aligned(char* base, const long long* src, const long long* dst, int m,
+__device__ __forceinline__ void move_aligned(char* base, const volatile long long* src, const volatile long long* dst, int m,
                                              long long lo, long long hi) {
   if (m <= 2)
     move_columns<uint4, 2, 8>(base, src, dst, m, lo / 16, hi / 16);
@@ -90,7 +96,7 @@ __device__ __forceinline__ void move_aligned(char* base, const long long* src, c
 
 // Bytes lo..hi of one segment at any alignment, through shared memory.  The
 // blocks at a range's ends may hold neighbours' bytes; those are not used.
-__device__ __noinline__ void move_staged(char* base, const long long* src, const long long* dst, int m, long long lo,
+__device__ __forceinline__ void move_staged(char* base, const long long* src, const long long* dst, int m, long long lo,
                                          long long hi, int unit) {
   extern __shared__ __align__(16) unsigned char stage[];
   const int room = kStageBytes / m / 16 * 16;  // per move, the blocks at both ends included
@@ -157,7 +163,8 @@ __device__ __forceinline__ bool sequence_ok(const Params& P, int b) {
   return true;
 }
 
-__global__ void __launch_bounds__(kThreads, 2) reorder_kernel(const __grid_constant__ Params P) {
+template <bool kStaged>
+__global__ void __launch_bounds__(kThreads, kStaged ? kStagedCtas : 2) reorder_kernel(const __grid_constant__ Params P) {
   __shared__ long long src[SV_BEAM_MAX_BEAMS], dst[SV_BEAM_MAX_BEAMS];
   __shared__ int s_moves;
   unsigned cta = blockIdx.x;
@@ -204,10 +211,10 @@ __global__ void __launch_bounds__(kThreads, 2) reorder_kernel(const __grid_const
   const int m = s_moves;
   if (m == 0) return;
   char* base = S.data + b * S.seq + seg * S.seg;
-  if (S.unit == 16)
-    move_aligned(base, src, dst, m, lo, hi);
-  else
+  if constexpr (kStaged)
     move_staged(base, src, dst, m, lo, hi, S.unit);
+  else
+    move_aligned(base, src, dst, m, lo, hi);
 }
 
 }  // namespace svb
@@ -250,23 +257,59 @@ extern "C" sv_status sv_beam_reorder(const sv_beam_state* states, int32_t n_stat
   if (!parents || !status) return svh::fail(SV_ERR_ARG, "parents or status is NULL");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int chunk = all_ctas * batch < svb::kManyCtas ? svb::kSmallChunk : svb::kLargeChunk;
-  for (int at = 0; at < n_states; at += svb::kStates) {
-    svb::Params p;
-    p.parents = parents;
-    p.lengths = lengths;
-    p.status = at == 0 ? status : nullptr;
-    p.B = batch;
-    p.W = beams;
-    p.min_tokens = min_tokens;
-    p.chunk_bytes = chunk;
-    p.status_ctas = at == 0 ? (batch + svb::kThreads - 1) / svb::kThreads : 0;
+  // what divides every address and extent of a state
+  // (a timed state may end after any token, another one only at its end)
+  auto unit_of = [&](const sv_beam_state& s) {
+    unsigned long long any = reinterpret_cast<uintptr_t>(s.data) | 16u |
+                             static_cast<unsigned long long>(s.timed ? s.token_bytes : s.tokens * s.token_bytes);
+    if (batch > 1) any |= static_cast<unsigned long long>(s.seq_stride);
+    if (beams > 1) any |= static_cast<unsigned long long>(s.beam_stride);
+    if (s.segs > 1) any |= static_cast<unsigned long long>(s.seg_stride);
+    return static_cast<int>(any & (~any + 1));
+  };
+  svb::Params p;
+  p.parents = parents;
+  p.lengths = lengths;
+  p.status = status;
+  p.B = batch;
+  p.W = beams;
+  p.min_tokens = min_tokens;
+  p.chunk_bytes = chunk;
+  p.status_ctas = (batch + svb::kThreads - 1) / svb::kThreads;
+  p.n = 0;
+  long long ctas = 0;
+  auto launch = [&](bool staged) -> sv_status {
+    const long long grid = ctas + p.status_ctas;
+    if (grid == 0) return SV_OK;
+    if (staged) {  // the shared-memory opt-in, once per device
+      static bool attr_set[64] = {};
+      int dev = 0;
+      if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 0;
+      if (!attr_set[dev]) {
+        const cudaError_t e = cudaFuncSetAttribute(svb::reorder_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   svb::kStageBytes);
+        if (e != cudaSuccess) return svh::fail(SV_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+        attr_set[dev] = true;
+      }
+      svb::reorder_kernel<true><<<static_cast<unsigned>(grid), svb::kThreads, svb::kStageBytes, st>>>(p);
+    } else {
+      svb::reorder_kernel<false><<<static_cast<unsigned>(grid), svb::kThreads, 0, st>>>(p);
+    }
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return svh::fail(SV_ERR_CUDA, "kernel launch: %s", cudaGetErrorString(e));
+    p.status = nullptr;
+    p.status_ctas = 0;
     p.n = 0;
-    long long ctas = 0;
-    int smem = 0;
-    for (int i = at; i < n_states && i < at + svb::kStates; ++i) {
+    ctas = 0;
+    return SV_OK;
+  };
+  for (int kind = 0; kind < 2; ++kind) {  // aligned states, then the others
+    for (int i = 0; i < n_states; ++i) {
       const sv_beam_state& s = states[i];
       const long long bytes = s.tokens * s.token_bytes;
       if (s.segs == 0 || bytes == 0) continue;
+      const int unit = unit_of(s);
+      if ((unit < 16) != (kind == 1)) continue;
       svb::State& q = p.s[p.n++];
       q.data = static_cast<char*>(s.data);
       q.seq = s.seq_stride;
@@ -276,34 +319,19 @@ extern "C" sv_status sv_beam_reorder(const sv_beam_state* states, int32_t n_stat
       q.segs = s.segs;
       q.tokens = s.tokens;
       q.timed = s.timed != 0;
-      // what divides every address and extent
-      // (a timed state may end after any token, another one only at its end)
-      unsigned long long any = reinterpret_cast<uintptr_t>(s.data) | 16u |
-                               static_cast<unsigned long long>(q.timed ? s.token_bytes : bytes);
-      if (batch > 1) any |= static_cast<unsigned long long>(s.seq_stride);
-      if (beams > 1) any |= static_cast<unsigned long long>(s.beam_stride);
-      if (s.segs > 1) any |= static_cast<unsigned long long>(s.seg_stride);
-      q.unit = static_cast<int>(any & (~any + 1));
-      if (q.unit < 16) smem = svb::kStageBytes;
+      q.unit = unit;
       q.chunks = static_cast<int>((bytes + chunk - 1) / chunk);
       q.first = static_cast<unsigned>(ctas);
       ctas += static_cast<long long>(q.chunks) * s.segs * batch;
-    }
-    const long long grid = ctas + p.status_ctas;
-    if (grid == 0) continue;
-    if (smem) {  // the shared-memory opt-in, once per device
-      static bool attr_set[64] = {};
-      int dev = 0;
-      if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 0;
-      if (!attr_set[dev]) {
-        const cudaError_t e = cudaFuncSetAttribute(svb::reorder_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) return svh::fail(SV_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
-        attr_set[dev] = true;
+      if (p.n == svb::kStates) {
+        const sv_status r = launch(kind == 1);
+        if (r != SV_OK) return r;
       }
     }
-    svb::reorder_kernel<<<static_cast<unsigned>(grid), svb::kThreads, smem, st>>>(p);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return svh::fail(SV_ERR_CUDA, "kernel launch: %s", cudaGetErrorString(e));
+    if (p.n || (kind == 1 && p.status_ctas)) {
+      const sv_status r = launch(kind == 1 && p.n);
+      if (r != SV_OK) return r;
+    }
   }
   return SV_OK;
 }
