@@ -278,6 +278,7 @@ struct Shared {
   double lse[SV_BEAM_MAX_BEAMS];
   double cum[SV_BEAM_MAX_BEAMS];
   float M[SV_BEAM_MAX_BEAMS];
+  float whole[SV_BEAM_MAX_BEAMS], rest[SV_BEAM_MAX_BEAMS];  // the logarithm to base 2: an integer and log2 of [1, 2)
   float add[SV_BEAM_MAX_BEAMS];  // f32 score = logit + add; -inf: no candidates
   float margin[SV_BEAM_MAX_BEAMS];  // by which that score may be off
   float thr[SV_BEAM_MAX_BEAMS];     // f32 scores below are not among the n best
@@ -472,14 +473,15 @@ __device__ __forceinline__ void score_entries(Shared& sm, int from, int L) {
   __syncthreads();
 }
 
-// A row's f32 addend and margin from its score and logarithm.  An addend that
-// leaves f32's range says nothing.
-__device__ __forceinline__ float set_add(Shared& sm, int w, double eps) {
-  const double a = sm.cum[w] - sm.lse[w];
-  const bool fits = a >= -3.4028234663852886e38;
-  sm.add[w] = fits ? static_cast<float>(a) : -3.4028234663852886e38f;
-  sm.margin[w] = fits ? static_cast<float>(eps) + fabsf(sm.add[w]) * 0x1p-22f : INFINITY;
-  return sm.add[w];
+// A row's f32 addend and margin from its score and its logarithm in f32.  An
+// addend that leaves f32's range says nothing.
+__device__ __forceinline__ float set_add(Shared& sm, int w, float c, float lse, double eps) {
+  const float a = __fsub_rn(c, lse);
+  const bool fits = a >= -3.4028234663852886e38f;
+  const float add = fits ? a : -3.4028234663852886e38f;
+  sm.add[w] = add;
+  sm.margin[w] = fits ? static_cast<float>(eps) + (fabsf(add) * 0x1p-22f + fabsf(c) * 0x1p-22f + fabsf(lse) * 0x1p-22f) : INFINITY;
+  return add;
 }
 
 // More candidates than the lists hold (many equal logits, rows in ascending
@@ -628,17 +630,17 @@ __device__ __forceinline__ void pick(const Params& P, int b) {
     }
     float add = -INFINITY;
     if (lane == 0) {
-      // log2 s = exponent + log2 of the significand
+      // log2 s = exponent + log2 of the significand; in f32 for the addend, the
+      // doubles (a sixteenth of a warp at a time on this machine) all at once later
       const int e = static_cast<int>(__float_as_uint(s) >> 23) - 127;
       const float f = __uint_as_float((__float_as_uint(s) & 0x7FFFFFu) | 0x3F800000u);
-      constexpr double kBack = 1.0 / static_cast<double>(kLog2e);
-      const double lse = (static_cast<double>(base_of(M) + static_cast<float>(e)) + static_cast<double>(log2f(f))) * kBack;
-      sm.cum[w] = c;
-      sm.lse[w] = lse;
+      const float whole = base_of(M) + static_cast<float>(e), rest = log2f(f);
       sm.M[w] = M;
+      sm.whole[w] = whole;
+      sm.rest[w] = rest;
       sm.add[w] = -INFINITY;
       sm.margin[w] = 0.f;
-      if (M > -INFINITY) add = set_add(sm, w, P.eps);
+      if (M > -INFINITY) add = set_add(sm, w, c, (whole + rest) * 0.6931471805599453f, P.eps);
       sm.ended[w] = ended;
       sm.precise[w] = 0;
       sm.again[w] = M > -INFINITY && fabsf(M) > kLarge;
@@ -669,13 +671,19 @@ __device__ __forceinline__ void pick(const Params& P, int b) {
     for (int w = 0; w < P.W; ++w) {
       if (sm.again[w]) {
         precise_lse<T>(sm, P, b, w);
-        if (tid == 0) set_add(sm, w, P.eps);
+        if (tid == 0) set_add(sm, w, P.scores[r0 + w], static_cast<float>(sm.lse[w]), P.eps);
         __syncthreads();
       }
       for (int u = tid; u < units; u += kPickThreads)
-        put(w * units + u, sm.ended[w] ? (u == 0 ? static_cast<float>(sm.cum[w]) : -INFINITY)
+        put(w * units + u, sm.ended[w] ? (u == 0 ? P.scores[r0 + w] : -INFINITY)
                                        : sm.add[w] > -INFINITY ? unit_max(w, u) + sm.add[w] : -INFINITY);
     }
+  }
+
+  if (tid < P.W) {
+    constexpr double kBack = 1.0 / static_cast<double>(kLog2e);
+    sm.cum[tid] = P.scores[r0 + tid];
+    if (!sm.precise[tid]) sm.lse[tid] = (static_cast<double>(sm.whole[tid]) + static_cast<double>(sm.rest[tid])) * kBack;
   }
 
   // tau: at least n units reach it, and hardly more than 2 n
@@ -712,7 +720,7 @@ __device__ __forceinline__ void pick(const Params& P, int b) {
     float widest = 0.f, all_widest = 0.f;
 #pragma unroll 1
     for (int w = lane; w < P.W; w += 32) {
-      const float best = sm.ended[w] ? static_cast<float>(sm.cum[w]) : sm.M[w] + sm.add[w];  // (-inf where it has none)
+      const float best = sm.ended[w] ? P.scores[r0 + w] : sm.M[w] + sm.add[w];  // (-inf where it has none)
       if (best >= tau) widest = fmaxf(widest, sm.margin[w]);
       all_widest = fmaxf(all_widest, sm.margin[w]);
     }
@@ -747,18 +755,39 @@ __device__ __forceinline__ void pick(const Params& P, int b) {
   __syncthreads();
   const int n_groups = sm.n_groups;
   if (n_groups <= kGroupList) {
+    // half a group at a time, four loads per lane in flight; most vectors have
+    // nothing, which their maximum tells
+    constexpr int kBatch = 4;
 #pragma unroll 1
-    for (int j = 2 * warp; j < 2 * n_groups; j += j & 1 ? 2 * kPickWarps - 1 : 1) {  // half a group at a time
-      const int2 wg = sm.group[j / 2];
-      const Row<T> row(static_cast<const T*>(P.logits) + (r0 + wg.x) * P.stride, P.V);
-      const long long v = static_cast<long long>(wg.y) * kGroupVecs + 32 * (j & 1) + lane;
-      const float add = sm.add[wg.x], thr = sm.thr[wg.x];
-      float x[E];
-      Elem<T>::unpack(row.load(v), x);
-      const int e = static_cast<int>(row.first(v));
+    for (int j0 = warp; j0 < 2 * n_groups; j0 += kBatch * kPickWarps) {
+      uint4 q[kBatch];
 #pragma unroll
-      for (int i = 0; i < E; ++i)
-        if (x[i] > -INFINITY && x[i] + add >= thr) append(sm, P.V, wg.x, e + i, x[i]);
+      for (int i = 0; i < kBatch; ++i) {
+        const int j = j0 + i * kPickWarps;
+        q[i] = Elem<T>::neg_inf();
+        if (j < 2 * n_groups) {
+          const int2 wg = sm.group[j / 2];
+          const Row<T> row(static_cast<const T*>(P.logits) + (r0 + wg.x) * P.stride, P.V);
+          const long long v = static_cast<long long>(wg.y) * kGroupVecs + 32 * (j & 1) + lane;
+          q[i] = row.inside(v, v) ? row.whole(v) : row.load(v);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int j = j0 + i * kPickWarps;
+        if (j >= 2 * n_groups) break;
+        const int2 wg = sm.group[j / 2];
+        const float add = sm.add[wg.x], thr = sm.thr[wg.x], top_of = Elem<T>::max_of(q[i], q[i]);
+        if (top_of > -INFINITY && top_of + add >= thr) {
+          const Row<T> row(static_cast<const T*>(P.logits) + (r0 + wg.x) * P.stride, P.V);
+          const int e = static_cast<int>(row.first(static_cast<long long>(wg.y) * kGroupVecs + 32 * (j & 1) + lane));
+          float x[E];
+          Elem<T>::unpack(q[i], x);
+#pragma unroll
+          for (int k = 0; k < E; ++k)
+            if (x[k] > -INFINITY && x[k] + add >= thr) append(sm, P.V, wg.x, e + k, x[k]);
+        }
+      }
     }
   }
   __syncthreads();
@@ -822,12 +851,12 @@ __device__ __forceinline__ void pick(const Params& P, int b) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kPickThreads) pick_kernel(const __grid_constant__ Params P) {
+__global__ void __launch_bounds__(kPickThreads, 1) pick_kernel(const __grid_constant__ Params P) {
   pick<T, false>(P, blockIdx.x);
 }
 
 template <typename T>
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPickThreads) one_kernel(const __grid_constant__ Params P) {
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPickThreads, 1) one_kernel(const __grid_constant__ Params P) {
   const int b = blockIdx.x / kCluster, rank = blockIdx.x % kCluster, lane = threadIdx.x % 32;
   for (int i = rank * kPickWarps + threadIdx.x / 32; i < P.W * P.slices; i += kCluster * kPickWarps) {
     const int w = i / P.slices, slice = i - w * P.slices;
