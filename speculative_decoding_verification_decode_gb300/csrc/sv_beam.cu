@@ -56,7 +56,7 @@ constexpr int kGroupVecs = 64;   // 16-byte vectors per group: two per lane of a
 constexpr int kCap = 4096;       // candidate entries a CTA holds (power of two)
 constexpr int kGroupList = 1024; // groups read again before the ordered pass takes over
 constexpr int kUnits = 8192;     // maxima in the bisection
-constexpr int kAhead = 8;        // of a row's maxima, loads per lane in flight
+constexpr int kAhead = 12;        // of a row's maxima, loads per lane in flight
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLarge = 1048576.f;  // |M| above this: the row's sum is taken precisely (l k - c would lose bits)
 
