@@ -136,9 +136,10 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
     }
   };
   uint4 raw[kAhead];
-  auto load = [&](int r, int j) {
+  auto load = [&](uint4 (&raw)[kAhead], int r, int j, int n) {  // the first n
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
+      if (k >= n) break;
       const int in = min(r, rows - 1);
       const uint4* src = in < g.rows0 ? f.s0 + static_cast<long long>(in) * chunks
                                       : f.s1 + static_cast<long long>(in - g.rows0) * chunks;
@@ -151,7 +152,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
   int row0 = 0, chunk0 = threadIdx.x;
   if (warp < kFewWarps) {
     step(row0, chunk0);
-    load(row0, chunk0);
+    load(raw, row0, chunk0, turns);
   }
   if (threadIdx.x == 0) {
     for (int s = 0; s < g.stages; ++s) {
@@ -230,30 +231,34 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
     const uint32_t limit = BF ? 0x7F80u : 0x7C00u;
     int r = row0, j = chunk0, rows_of[kAhead];
     for (int i0 = 0; i0 < turns; i0 += kAhead) {
+      const int left = turns - i0;
       uint32_t top[kAhead];
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
-        if (j >= chunks) raw[k] = make_uint4(0, 0, 0, 0);
-        const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
         top[k] = 0;
+        if (k < left) {
+          if (j >= chunks) raw[k] = make_uint4(0, 0, 0, 0);
+          const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t lo = w[i] & 0x7FFFu, hi = w[i] >> 16 & 0x7FFFu;
-          top[k] = max(top[k], max(lo < limit ? lo : 0u, hi < limit ? hi : 0u));
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t lo = w[i] & 0x7FFFu, hi = w[i] >> 16 & 0x7FFFu;
+            top[k] = max(top[k], max(lo < limit ? lo : 0u, hi < limit ? hi : 0u));
+          }
+          rows_of[k] = r;
+          if (r < rows) sts128(place(r, j), raw[k]);
+          j += 32 * kFewWarps;
+          step(r, j);
         }
-        rows_of[k] = r;
-        if (r < rows) sts128(place(r, j), raw[k]);
-        j += 32 * kFewWarps;
-        step(r, j);
       }
 #pragma unroll
       for (int o = 8; o > 0; o /= 2)
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) top[k] = max(top[k], __shfl_xor_sync(0xFFFFFFFFu, top[k], o));
+        for (int k = 0; k < kAhead; ++k)
+          if (k < left) top[k] = max(top[k], __shfl_xor_sync(0xFFFFFFFFu, top[k], o));
 #pragma unroll
       for (int k = 0; k < kAhead; ++k)
-        if (lane % 16 == 0 && rows_of[k] < rows) atomicMax(&tops[rows_of[k]], top[k]);
-      if (i0 + kAhead < turns) load(r, j);
+        if (k < left && lane % 16 == 0 && rows_of[k] < rows) atomicMax(&tops[rows_of[k]], top[k]);
+      if (left > kAhead) load(raw, r, j, left - kAhead);
     }
   }
   all_sync();
@@ -264,7 +269,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
         t ? 14 - ilogbf(BF ? __uint_as_float(t << 16) : __half2float(__ushort_as_half(static_cast<unsigned short>(t)))) : 0;
   }
   all_sync();
-  constexpr int kMake = 4;
+  constexpr int kMake = 2;
   int r = row0, j = chunk0;
 #pragma unroll 1
   for (int i0 = 0; i0 < turns; i0 += kMake) {
