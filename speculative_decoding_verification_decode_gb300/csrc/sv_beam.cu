@@ -27,7 +27,7 @@
 // Order.  Scores of one beam are ordered by its logits, exactly.  Between
 // beams the logarithms' f32 errors count, so pairs of different beams that lie
 // closer than their bound (eps each) send their rows through precise_lse: the
-// sum in 64-bit fixed point from terms good to 2^-37, equal for rows that are
+// sum in 64-bit fixed point from terms good to 2^-36, equal for rows that are
 // permutations of one another, whatever the order.  All scores are then
 // compared as doubles.
 //
@@ -283,7 +283,7 @@ struct Shared {
   float margin[SV_BEAM_MAX_BEAMS];  // by which that score may be off
   float thr[SV_BEAM_MAX_BEAMS];     // f32 scores below are not among the n best
   unsigned char ended[SV_BEAM_MAX_BEAMS], precise[SV_BEAM_MAX_BEAMS], again[SV_BEAM_MAX_BEAMS];
-  unsigned long long table[33];  // 2^(j / 32), j = -16..16, units of 2^-61
+  unsigned long long table[32];  // 2^(j / 32), units of 2^-61
   unsigned long long sum_hi[kPickWarps], sum_lo[kPickWarps];
   int cnt[2][kPickWarps];
   int n_groups, n_entries, redo, next;
@@ -326,51 +326,68 @@ __device__ __forceinline__ int block_sum(Shared& sm, int x, int& turn) {
   return t;
 }
 
-// e^(x - M) in units of 2^-60, within 2^-37 of it: x - M exactly as a sum of
-// two floats; times log2 e likewise; the fraction as j / 32 + g; 2^(j/32)
-// from the table, 2^g - 1 by the first terms of its series (g ln 2 <= 0.011,
-// the fifth power's term is the last above 2^-40).
+// The integer next to x scale (|x scale| < 2^22), from the low bits of a sum with
+// 1.5 2^23; x keeps what is left, exactly.  (Conversions to 64-bit integers run
+// at the rate of doubles here, a sixty-fourth: the sum of a row took 70 us with two.)
+__device__ __forceinline__ int take_int(float& x, float scale, float unit) {
+  const float u = fmaf(x, scale, 12582912.f);
+  x = fmaf(__fsub_rn(u, 12582912.f), -unit, x);
+  return __float_as_int(u) - 0x4B400000;
+}
+
+// e^(x - M) in units of 2^-60, within 2^-36 of it: x - M exactly as a sum of
+// two floats; times log2 e likewise, as n + j / 32 + g; 2^(j/32) from the table,
+// 2^g - 1 by the first terms of its series (g ln 2 <= 0.011, the fifth power's
+// term is the last above 2^-40) to 2^-38 as an integer.
 __device__ __forceinline__ unsigned long long precise_term(float x, float M, const unsigned long long* table) {
   constexpr double kL = 1.4426950408889634, kN = 0.6931471805599453;
   constexpr float L1 = static_cast<float>(kL), L2 = static_cast<float>(kL - static_cast<double>(L1));
   constexpr float N1 = static_cast<float>(kN), N2 = static_cast<float>(kN - static_cast<double>(N1));
   const float y = __fsub_rn(x, M);
-  if (!(y > -45.f)) return 0;  // below 2^-64; -inf
+  const bool counts = y > -42.f;  // (or it is below 2^-60: less than a unit; -inf)
   const float bb = __fsub_rn(y, x);
   const float yl = __fadd_rn(__fsub_rn(x, __fsub_rn(y, bb)), __fsub_rn(-M, bb));
   const float t = __fmul_rn(y, L1);
   const float tl = fmaf(yl, L1, fmaf(y, L2, fmaf(y, L1, -t)));
-  const float n = rintf(t), f = __fsub_rn(t, n), j = rintf(f * 32.f), g = fmaf(j, -0.03125f, f);
+  float g = t;
+  const int k = take_int(g, 32.f, 0.03125f);  // |t| <= 61 where it counts
   const float z = __fmul_rn(g, N1);
   const float zl = fmaf(tl, N1, fmaf(g, N2, fmaf(g, N1, -z)));
   const float a = z + zl;
-  const float w = fmaf(a * a, fmaf(a, fmaf(a, fmaf(a, 1.f / 120.f, 1.f / 24.f), 1.f / 6.f), 0.5f), zl);
-  const long long Z = __float2ll_rn(z * 1125899906842624.f) + __float2ll_rn(w * 1125899906842624.f);  // units of 2^-50
-  const long long e = static_cast<long long>(table[static_cast<int>(j) + 16]);
-  const int shift = 1 - static_cast<int>(n);
-  return shift < 64 ? static_cast<unsigned long long>(e + __mul64hi(e, Z * 16384)) >> shift : 0ull;
+  float w = fmaf(a * a, fmaf(a, fmaf(a, fmaf(a, 1.f / 120.f, 1.f / 24.f), 1.f / 6.f), 0.5f), zl), zr = z;
+  // z + w in units of 2^-37, from |z| < 0.0114 in units of 2^-28, |w| < 6.6e-5 of 2^-35, and what is left
+  int Z = take_int(zr, 0x1p28f, 0x1p-28f) * 512;
+  Z += take_int(w, 0x1p35f, 0x1p-35f) * 4;
+  float left = zr + w;
+  Z += take_int(left, 0x1p37f, 0x1p-37f);
+  const long long e = static_cast<long long>(table[k & 31]);
+  const int shift = 1 - (k >> 5);
+  const unsigned long long q = static_cast<unsigned long long>(e + (static_cast<long long>(static_cast<int>(e >> 31)) * Z >> 6));
+  return counts ? q >> (shift & 63) : 0ull;
 }
 
-// The row's logarithm to better than 2^-36, by the whole CTA.
+// The row's logarithm to better than 2^-35, by the whole CTA.
+// (A call of 64 x 8 x 128256 with two equal beams in one sequence: 114 us, where
+// 64-bit conversions, a branch per term and loads without a successor took 187.)
 template <typename T>
 __device__ __noinline__ void precise_lse(Shared& sm, const Params& P, int b, int w) {
   constexpr int E = Elem<T>::E;
   const Row<T> row(static_cast<const T*>(P.logits) + (static_cast<long long>(b) * P.W + w) * P.stride, P.V);
-  if (threadIdx.x < 33)
-    sm.table[threadIdx.x] = static_cast<unsigned long long>(exp2((static_cast<int>(threadIdx.x) - 16) / 32.0) * 0x1p61);
+  if (threadIdx.x < 32) sm.table[threadIdx.x] = static_cast<unsigned long long>(exp2(threadIdx.x / 32.0) * 0x1p61);
   __syncthreads();
   const float M = sm.M[w];
   unsigned long long hi = 0, lo = 0;
   const long long vecs = (static_cast<long long>(row.head) + P.V + E - 1) / E;
+  uint4 next = threadIdx.x < vecs ? row.load(threadIdx.x) : Elem<T>::neg_inf();
   for (long long v = threadIdx.x; v < vecs; v += kPickThreads) {
     float x[E];
-    Elem<T>::unpack(row.load(v), x);
+    Elem<T>::unpack(next, x);
+    if (v + kPickThreads < vecs) next = row.load(v + kPickThreads);
+    unsigned long long q = 0;  // of eight terms up to 2^60 each
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-      const unsigned long long q = precise_term(x[i], M, sm.table);
-      hi += q >> 32;
-      lo += q & 0xFFFFFFFFu;
-    }
+    for (int i = 0; i < E; ++i) q += precise_term(x[i], M, sm.table);
+    hi += q >> 32;
+    lo += q & 0xFFFFFFFFu;
   }
 #pragma unroll
   for (int o = 16; o > 0; o /= 2) {
