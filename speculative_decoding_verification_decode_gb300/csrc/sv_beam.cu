@@ -705,74 +705,110 @@ __device__ __forceinline__ void pick(const Params& P, int b) {
     if (!sm.precise[tid]) sm.lse[tid] = (static_cast<double>(sm.whole[tid]) + static_cast<double>(sm.rest[tid])) * kBack;
   }
 
-  // tau: at least n units reach it, and hardly more than 2 n
-  top = __reduce_max_sync(0xFFFFFFFFu, top);
-  low = __reduce_min_sync(0xFFFFFFFFu, low);
-  if (lane == 0) sm.sum_lo[warp] = static_cast<unsigned long long>(top) << 32 | low;
-  int turn = 0;
-  const int all = block_sum(sm, finite, turn);
-#pragma unroll 1
-  for (int w = 0; w < kPickWarps; ++w) {
-    top = max(top, static_cast<unsigned>(sm.sum_lo[w] >> 32));
-    low = min(low, static_cast<unsigned>(sm.sum_lo[w]));
-  }
+  // tau: at least n units reach it, and hardly more than 2 n.  Where there are
+  // fewer units with candidates than that (one live beam, as in a search's first
+  // step), all their groups are listed, and a second round takes smaller units of
+  // those: without it 70 to 540 us went into the ordered pass.
+  int turn = 0, n_groups = 0, in = total;
+  bool finer = false;
   unsigned thr_key = none + 1;  // of the lowest threshold of a row
-  if (all >= P.n) {
-    unsigned lo = low, hi = top + 1;  // at least n units >= lo, fewer than n >= hi
-    int above = all;
 #pragma unroll 1
-    while (hi - lo > 1 && above > 2 * P.n) {
-      const unsigned mid = lo + (hi - lo) / 2;
-      int c = 0;
+  for (;;) {
+    top = __reduce_max_sync(0xFFFFFFFFu, top);
+    low = __reduce_min_sync(0xFFFFFFFFu, low);
+    if (lane == 0) sm.sum_lo[warp] = static_cast<unsigned long long>(top) << 32 | low;
+    const int all = block_sum(sm, finite, turn);
+#pragma unroll 1
+    for (int w = 0; w < kPickWarps; ++w) {
+      top = max(top, static_cast<unsigned>(sm.sum_lo[w] >> 32));
+      low = min(low, static_cast<unsigned>(sm.sum_lo[w]));
+    }
+    if (all >= P.n) {
+      unsigned lo = low, hi = top + 1;  // at least n units >= lo, fewer than n >= hi
+      int above = all;
+#pragma unroll 1
+      while (hi - lo > 1 && above > 2 * P.n) {
+        const unsigned mid = lo + (hi - lo) / 2;
+        int c = 0;
 #pragma unroll 4
-      for (int i = tid; i < total; i += kPickThreads) c += sm.unit[i] >= mid;
-      c = block_sum(sm, c, turn);
-      if (c >= P.n) {
-        lo = mid;
-        above = c;
-      } else {
-        hi = mid;
+        for (int i = tid; i < in; i += kPickThreads) c += sm.unit[i] >= mid;
+        c = block_sum(sm, c, turn);
+        if (c >= P.n) {
+          lo = mid;
+          above = c;
+        } else {
+          hi = mid;
+        }
       }
-    }
-    const float tau = key_f32(lo);
-    // (every warp computes, and writes, the same)
-    float widest = 0.f, all_widest = 0.f;
+      const float tau = key_f32(lo);
+      // (every warp computes, and writes, the same)
+      float widest = 0.f, all_widest = 0.f;
 #pragma unroll 1
-    for (int w = lane; w < P.W; w += 32) {
-      const float best = sm.ended[w] ? P.scores[r0 + w] : sm.M[w] + sm.add[w];  // (-inf where it has none)
-      if (best >= tau) widest = fmaxf(widest, sm.margin[w]);
-      all_widest = fmaxf(all_widest, sm.margin[w]);
-    }
-    widest = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(widest)));
-    all_widest = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(all_widest)));
-    const float base = tau - fabsf(tau) * 0x1p-21f - widest;
+      for (int w = lane; w < P.W; w += 32) {
+        const float best = sm.ended[w] ? P.scores[r0 + w] : sm.M[w] + sm.add[w];  // (-inf where it has none)
+        if (best >= tau) widest = fmaxf(widest, sm.margin[w]);
+        all_widest = fmaxf(all_widest, sm.margin[w]);
+      }
+      widest = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(widest)));
+      all_widest = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(all_widest)));
+      const float base = tau - fabsf(tau) * 0x1p-21f - widest;
 #pragma unroll 1
-    for (int w = lane; w < P.W; w += 32) sm.thr[w] = base - sm.margin[w];
-    thr_key = max(thr_key, f32_key(base - all_widest));
-  } else {
-    for (int w = lane; w < P.W; w += 32) sm.thr[w] = -INFINITY;
-  }
-  __syncwarp();
+      for (int w = lane; w < P.W; w += 32) sm.thr[w] = base - sm.margin[w];
+      thr_key = max(thr_key, f32_key(base - all_widest));
+    } else {
+      for (int w = lane; w < P.W; w += 32) sm.thr[w] = -INFINITY;
+    }
+    __syncwarp();
 
-  // the groups that reach it, then their logits that do
+    // the groups that reach it
+    if (!finer) {
 #pragma unroll 1
-  for (int i = tid; i < total; i += kPickThreads)
-    if (sm.unit[i] >= thr_key) {
-      const int w = i / units, u = i - w * units;
-      if (!(key_f32(sm.unit[i]) >= sm.thr[w])) continue;
-      if (sm.ended[w]) {
-        append(sm, P.V, w, P.eos, 0.f);
-      } else {
+      for (int i = tid; i < total; i += kPickThreads)
+        if (sm.unit[i] >= thr_key) {
+          const int w = i / units, u = i - w * units;
+          if (!(key_f32(sm.unit[i]) >= sm.thr[w])) continue;
+          if (sm.ended[w]) {
+            append(sm, P.V, w, P.eos, 0.f);
+          } else {
 #pragma unroll 1
-        for (int g = u * q; g < min(P.groups, u * q + q); ++g)
-          if (q == 1 || P.gmax[(r0 + w) * P.groups + g] + sm.add[w] >= sm.thr[w]) {
-            const int at = atomicAdd(&sm.n_groups, 1);
-            if (at < kGroupList) sm.group[at] = make_int2(w, g);
+            for (int g = u * q; g < min(P.groups, u * q + q); ++g)
+              if (q == 1 || P.gmax[(r0 + w) * P.groups + g] + sm.add[w] >= sm.thr[w]) {
+                const int at = atomicAdd(&sm.n_groups, 1);
+                if (at < kGroupList) sm.group[at] = make_int2(w, g);
+              }
           }
+        }
+    }
+    __syncthreads();
+    n_groups = sm.n_groups;
+    if (finer || all >= P.n || n_groups == 0 || n_groups > kGroupList) break;
+    finer = true;
+    int sub = 64;  // units of a group
+    while (n_groups * sub > kUnits) sub /= 2;
+    in = n_groups * sub;
+    top = 0;
+    low = 0xFFFFFFFFu;
+    finite = 0;
+#pragma unroll 1
+    for (int j = warp; j < n_groups; j += kPickWarps) {
+      const int2 wg = sm.group[j];
+      const Row<T> row(static_cast<const T*>(P.logits) + (r0 + wg.x) * P.stride, P.V);
+      const long long v = static_cast<long long>(wg.y) * kGroupVecs + lane;
+      const uint4 v0 = row.load(v), v1 = row.load(v + 32);
+      const float add = sm.add[wg.x], m0 = Elem<T>::max_of(v0, v0), m1 = Elem<T>::max_of(v1, v1);
+      if (sub == 64) {
+        put(j * 64 + lane, m0 + add);
+        put(j * 64 + 32 + lane, m1 + add);
+      } else {
+        float m = fmaxf(m0, m1);
+        const int lanes = 32 / sub;
+        for (int o = 1; o < lanes; o *= 2) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+        if (lane % lanes == 0) put(j * sub + lane / lanes, m + add);
       }
     }
-  __syncthreads();
-  const int n_groups = sm.n_groups;
+  }
+
+  // their logits that do
   if (n_groups <= kGroupList) {
     // half a group at a time, four loads per lane in flight; most vectors have
     // nothing, which their maximum tells
@@ -813,8 +849,12 @@ __device__ __forceinline__ void pick(const Params& P, int b) {
   int L = sm.n_entries;
   if (L > kCap || n_groups > kGroupList) {
     // every row that may hold candidates, precisely; then the ordered pass
-    for (int i = tid; i < total; i += kPickThreads)
-      if (sm.unit[i] >= thr_key) sm.again[i / units] = 1;
+    if (finer) {
+      for (int i = tid; i < n_groups; i += kPickThreads) sm.again[sm.group[i].x] = 1;
+    } else {
+      for (int i = tid; i < total; i += kPickThreads)
+        if (sm.unit[i] >= thr_key) sm.again[i / units] = 1;
+    }
     __syncthreads();
     for (int w = 0; w < P.W; ++w)
       if (sm.again[w] && !sm.ended[w] && !sm.precise[w]) precise_lse<T>(sm, P, b, w);

@@ -217,6 +217,23 @@ def test_select_one_kernel_and_two(B, W, V):
     assert (buf[need:] == 171).all()
 
 
+@pytest.mark.parametrize("dtype,W,V,n", [
+    ("bf16", 8, 2402, 16), ("f16", 64, 32000, 128), ("bf16", 64, 128256, 128), ("f32", 64, 128256, 128),
+    ("f32", 64, 200001, 128), ("f32", 64, 300000, 128), ("f32", 16, 8000, 32), ("bf16", 4, 300, 8),
+])
+def test_select_one_live_beam(dtype, W, V, n):
+    """A search's first step: one beam alive, so fewer groups of logits than
+    candidates asked for; beside it, in another sequence, ended beams and a
+    masked row."""
+    x, c = make(18, 2, W, V, dtype)
+    c[0, 1:] = -float("inf")
+    c[1, 3:] = -float("inf")
+    fin = torch.zeros(2, W, dtype=torch.bool, device=DEV)
+    fin[1, 1] = True
+    x[1, 2] = -float("inf")
+    check(x, c, n, fin, 2, need_gap=False)
+
+
 def test_select_refusals():
     x, c = make(15, 2, 3, 500, "bf16")
     with pytest.raises(ValueError, match="workspace"):
