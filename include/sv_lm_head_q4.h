@@ -17,7 +17,10 @@
  *           everywhere.
  * The logits are those of these weights: products of the states with the
  * integers q - zero, summed in f32 within a group, then scaled and summed over
- * the groups in f32 (no weight is rounded to 16 bits on the way).
+ * the groups in f32 (no weight is rounded to 16 bits on the way, no state to
+ * fewer bits than it has; a state that meets a code equal to its zero adds
+ * nothing).  A group's sum is taken before its scale, so it stays in f32's range
+ * for states below 2^116.
  * Every 64 rows are a pass over the projection: past 64 rows the bf16 projection
  * of sv_lm_head.h is the faster one (128256 x 4096, groups of 128: 64 rows 148
  * against 193 us, 96 rows 266 against 205).

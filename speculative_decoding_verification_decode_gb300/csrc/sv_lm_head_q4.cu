@@ -54,9 +54,9 @@ sv_status launch(const void* s0, int rows0, const void* s1, int rows1, sv_dtype 
   g.V = vocab;
   g.d = dim;
   // up to 16 rows whose states fit in shared memory: the kernel for few rows
-  // (128256 x 4096, groups of 128: 1 row 55 us against the other's 134, 11 rows
-  // 80 against 135, 16 rows 100 against 136; groups of 32: 80, 144, 160 against
-  // 158, 158, 160)
+  // (128256 x 4096, groups of 128: 1 row 60 us against the other's 134, 11 rows
+  // 79 against 134, 16 rows 97 against 136; groups of 32: 82, 100, 139 against
+  // 157, 157, 159)
   if (static_cast<long long>(rows0) + rows1 <= 16) {
     const sv_status few = dtype == SV_BF16 ? start_few_bf16(g, proj, s0, s1, stream) : start_few_f16(g, proj, s0, s1, stream);
     if (few != SV_ERR_UNSUPPORTED) return few;

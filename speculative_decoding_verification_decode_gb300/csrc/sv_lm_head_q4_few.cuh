@@ -3,7 +3,7 @@
 // With so few rows the product is a stream of codes, and what must not stall
 // it is the way from a code to an operand.  The tensor-memory kernel pays a
 // store to tensor memory and two barrier trips per 128 columns on that way (135
-// us at 11 rows, V = 128256, d = 4096, groups of 128; here 80, and 56 to 62 up
+// us at 11 rows, V = 128256, d = 4096, groups of 128; here 79, and 60 to 62 up
 // to 8 rows); here a code goes from a register straight into an mma.sync operand
 // and nothing waits but on the stream itself.  mma.sync runs at 1006
 // multiply-adds per clock and SM (measured): 16 rows use 16 per weight, and
@@ -14,22 +14,21 @@
 //     every other 128-column stage, fourteen warps in all.  A warp reads the
 //     codes of its next stage before it multiplies this one's.
 //   - Eight codes of a word make the pairs (0,4) (1,5) (2,6) (3,7), by one
-//     mask each and one shift: a code in the lowest bits of a half word IS the
-//     f16 number q 2^-24, four bits up q 2^-20 (subnormal; tensor cores take
-//     them as they are).  The states that meet the second kind are kept 16
-//     times smaller.  The zeros come in as what a group's sum starts from,
-//     -z sum_k h, the sums kept from the beginning.  Five instructions for
-//     eight weights, and every product is exact.
-//     Codes that low lose bits of the products' ends (measured: as if the
-//     MMA aligned every subnormal's products by 2^-14): nothing to speak of
-//     with bf16's eight significant bits (3.4e-7 of the logits' norm, as much
-//     as a sum in f32), but 8.5e-7 with f16's eleven.  With f16 states
-//     all four pairs therefore stand four bits up, two more shifts per word.
-//   - So the states are f16 under a power of two per row that takes the row's
-//     largest to 2^14: exact for whatever is above 2^-24 of it, within 2^-35
-//     of it below, far under the f32 sums' roundings; the logits take the
-//     power back.  They lie in shared memory as operands in the pairs' order,
-//     all of them, for the kernel's life.
+//     mask each and one shift: a code in the lowest bits of a half word IS a
+//     subnormal number, q times the type's smallest, and four bits up 16 q
+//     times it.  One packed multiply-add takes that to q - z in units of 1/64
+//     (1/512 in f16), exact, a normal number: nine instructions for eight
+//     weights.  The operands are of the states' own type, and the states go in
+//     as they are, so every product is exact, and a state that meets a code
+//     equal to its zero adds nothing, however large it is (8e-8 of the logits'
+//     norm, with states of 30000 on such codes as without).  Codes as they lie,
+//     with the zero as what a group's sum starts from, are four instructions
+//     less (1 row 54.5 us where this takes 60; 11 rows 79 both; with groups of
+//     32 142 where this takes 100), but q h and z h then cancel only as far as
+//     either is rounded: a state of 1000 on such a code took logits off by more
+//     than 2^-16 of sum |h W|.
+//   - The states lie in shared memory as operands in the pairs' order, all of
+//     them, for the kernel's life.
 //   - The sums of a group are f32 accumulators of their own, added to the
 //     row's with the group's scale: no weight is rounded.  A lane's codes of a
 //     stage are those of whole groups (32, 16 or 8 in a row for groups of 128,
@@ -72,25 +71,60 @@ __device__ __forceinline__ bool few_wait(FewBars& bars, uint64_t* bar, uint32_t 
 __device__ __forceinline__ void all_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kFewWarps) : "memory"); }
 // The two warps of row group `rw`.
 __device__ __forceinline__ void pair_sync(int rw) { asm volatile("bar.sync %0, 64;" ::"r"(rw + 2) : "memory"); }
-// 2^e, -126 <= e <= 127.
-__device__ __forceinline__ float power(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 
+// D += A x B, K = 16: bf16 or f16 operands.
+template <bool BF>
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
-  asm(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  if constexpr (BF)
+    asm(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// The same from c.
-__device__ __forceinline__ void mma16816_from(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                              uint32_t b0, uint32_t b1, const float (&c)[4]) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%10, %11, %12, %13};"
-      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
-}
+
+// Operand words of codes less their zero, (q - z) / kUnit, exactly.  A code in
+// the lowest bits of a half word is the number q u (u the type's smallest
+// subnormal), four bits up 16 q u (of both types' numbers, those up to 255 u are
+// evenly spaced): one multiply-add by a power of two and -z / kUnit.
+template <bool BF>
+struct Operand {
+  static constexpr float kUnit = BF ? 64.f : 512.f;  // 2^127 u and 2^15 u, the largest powers that fit
+  uint32_t zero;
+  __device__ explicit Operand(uint32_t z) {
+    const float f = -1.f / kUnit * static_cast<float>(z);
+    if constexpr (BF) {
+      const __nv_bfloat162 two = __float2bfloat162_rn(f);
+      zero = *reinterpret_cast<const uint32_t*>(&two);
+    } else {
+      const __half2 two = __float2half2_rn(f);
+      zero = *reinterpret_cast<const uint32_t*>(&two);
+    }
+  }
+  // codes P and P + 4 of a word
+  template <int P>
+  __device__ uint32_t of(uint32_t w) const {
+    const uint32_t at = (P < 2 ? w : w >> 8) & (P % 2 ? 0x00F000F0u : 0x000F000Fu);
+    if constexpr (BF) {
+      const uint32_t k = P % 2 ? 0x7D007D00u : 0x7F007F00u;
+      const __nv_bfloat162 r = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&at), *reinterpret_cast<const __nv_bfloat162*>(&k),
+                                       *reinterpret_cast<const __nv_bfloat162*>(&zero));
+      return *reinterpret_cast<const uint32_t*>(&r);
+    } else {
+      const uint32_t k = P % 2 ? 0x68006800u : 0x78007800u;
+      const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&at), *reinterpret_cast<const __half2*>(&k),
+                                *reinterpret_cast<const __half2*>(&zero));
+      return *reinterpret_cast<const uint32_t*>(&r);
+    }
+  }
+};
 
 struct FewArgs {
   Args g;
@@ -108,6 +142,10 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
                                                              const __grid_constant__ FewArgs f) {
   constexpr int kPer = kFewK / G;       // groups per stage
   constexpr int kLen = G / 32;          // words of a lane in a group
+  // chains of MMAs per m tile (V = 128256, d = 4096, groups of 128: 11 rows 78.6
+  // us, with one 81.3; with zeros 16 rows 132 and 126, groups of 64 11 rows 117
+  // and 111)
+  constexpr int kChains = G == 128 && !Z ? 2 : 1;
   constexpr int kStride = few_stride(kPer);
   const Args& g = f.g;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -118,8 +156,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
   const int elem = g.scale_dtype == SV_F32 ? 4 : 2;
   const int frag_row = g.nk * 256 + 64;  // (64 more: neighbouring rows in other banks)
   unsigned char* frag = smem + g.stages * stage_bytes;                              // [row][stage][operand 0..3][4 x 16 bytes]
-  float* sums = reinterpret_cast<float*>(frag + rows * frag_row);                   // [group][NT][lane quarter][4]
-  float* red = sums + g.nk * kPer * NT * 16;                                        // [row warp][parity][4 NT][32]
+  float* red = reinterpret_cast<float*>(frag + rows * frag_row);                    // [row warp][parity][4 NT][32]
   uint32_t* sbuf = reinterpret_cast<uint32_t*>(red + kFewWarps * NT * 128);  // [slot][tile row][kStride]
   uint32_t* zbuf = sbuf + g.stages * kFewTile * kStride;
   FewBars& bars = *reinterpret_cast<FewBars*>(zbuf + g.stages * kFewTile * kZStride);
@@ -162,7 +199,6 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
     bars.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (threadIdx.x < 16) reinterpret_cast<uint32_t*>(red)[threadIdx.x] = 0;
   __syncthreads();
 
   if (warp == kFewWarps + kFewHelp) {
@@ -219,137 +255,33 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
   }
 
   // ---- the states as operands; columns past dim are 0.  Everything waits for
-  // this: several loads are in flight, and several chunks in the making.
-  uint32_t* tops = reinterpret_cast<uint32_t*>(red);   // the rows' largest finite states
-  int* shifts = reinterpret_cast<int*>(red) + 16;      // and their powers of two (both until the first tile ends)
-  const int c = lane % 16, quarter = G == 128 ? c / 4 : G == 64 ? c % 8 / 2 : c % 4,
-            word = G == 128 ? c % 4 : G == 64 ? c / 8 * 2 + c % 2 : c / 4;
-  // chunk c of a stage: which lane quarter multiplies it, and as its how manieth word
-  const uint32_t my_frag = smem_u32(frag) + word * 64 + quarter * 16;
-  auto place = [&](int r, int j) { return my_frag + r * frag_row + j / 16 * 256; };
+  // this: several loads are in flight.
   {
-    const uint32_t limit = BF ? 0x7F80u : 0x7C00u;
-    int r = row0, j = chunk0, rows_of[kAhead];
+    const int c = lane % 16, quarter = G == 128 ? c / 4 : G == 64 ? c % 8 / 2 : c % 4,
+              word = G == 128 ? c % 4 : G == 64 ? c / 8 * 2 + c % 2 : c / 4;
+    // chunk c of a stage: which lane quarter multiplies it, and as its how manieth word
+    const uint32_t my_frag = smem_u32(frag) + word * 64 + quarter * 16;
+    int r = row0, j = chunk0;
     for (int i0 = 0; i0 < turns; i0 += kAhead) {
       const int left = turns - i0;
-      uint32_t top[kAhead];
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        top[k] = 0;
+      for (int k = 0; k < kAhead; ++k)
         if (k < left) {
           if (j >= chunks) raw[k] = make_uint4(0, 0, 0, 0);
-          const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t lo = w[i] & 0x7FFFu, hi = w[i] >> 16 & 0x7FFFu;
-            top[k] = max(top[k], max(lo < limit ? lo : 0u, hi < limit ? hi : 0u));
-          }
-          rows_of[k] = r;
-          if (r < rows) sts128(place(r, j), raw[k]);
+          if (r < rows)
+            sts128(my_frag + r * frag_row + j / 16 * 256,
+                   make_uint4(__byte_perm(raw[k].x, raw[k].z, 0x5410), __byte_perm(raw[k].x, raw[k].z, 0x7632),
+                              __byte_perm(raw[k].y, raw[k].w, 0x5410), __byte_perm(raw[k].y, raw[k].w, 0x7632)));
           j += 32 * kFewWarps;
           step(r, j);
         }
-      }
-#pragma unroll
-      for (int o = 8; o > 0; o /= 2)
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k)
-          if (k < left) top[k] = max(top[k], __shfl_xor_sync(0xFFFFFFFFu, top[k], o));
-#pragma unroll
-      for (int k = 0; k < kAhead; ++k)
-        if (k < left && lane % 16 == 0 && rows_of[k] < rows) atomicMax(&tops[rows_of[k]], top[k]);
       if (left > kAhead) load(raw, r, j, left - kAhead);
     }
-  }
-  all_sync();
-  // the power of two that takes a row's largest finite state to 2^14
-  if (threadIdx.x < 16) {
-    const uint32_t t = tops[threadIdx.x];
-    shifts[threadIdx.x] =
-        t ? 14 - ilogbf(BF ? __uint_as_float(t << 16) : __half2float(__ushort_as_half(static_cast<unsigned short>(t)))) : 0;
-  }
-  all_sync();
-  constexpr int kMake = 2;
-  int r = row0, j = chunk0;
-#pragma unroll 1
-  for (int i0 = 0; i0 < turns; i0 += kMake) {
-    uint4 x[kMake];
-    int rr[kMake], jj[kMake], shift[kMake];
-#pragma unroll
-    for (int k = 0; k < kMake; ++k) {  // (past the last row: the last one again, unused)
-      rr[k] = r, jj[k] = j;
-      const int in = min(r, rows - 1);
-      x[k] = lds128(place(in, j));
-      shift[k] = shifts[in];
-      j += 32 * kFewWarps;
-      step(r, j);
-    }
-    float sum[kMake];
-    uint4 y[kMake];
-#pragma unroll
-    for (int k = 0; k < kMake; ++k) {
-      const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-      float h[8];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if constexpr (BF) {
-          h[2 * i] = __uint_as_float(w[i] << 16);
-          h[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-        } else {
-          const float2 two = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-          h[2 * i] = two.x;
-          h[2 * i + 1] = two.y;
-        }
-      }
-      int left = shift[k];
-      if constexpr (BF)
-        if (left > 126) {  // (tiny rows: two factors)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) h[i] *= 0x1p40f;
-          left -= 40;
-        }
-      const float up = power(left), up_odd = BF ? power(left - 4) : up;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) h[i] *= i % 2 ? up_odd : up;
-      uint32_t p[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const __half2 two = __floats2half2_rn(h[i], h[i + 4]);
-        p[i] = *reinterpret_cast<const uint32_t*>(&two);
-      }
-      y[k] = make_uint4(p[0], p[1], p[2], p[3]);
-      sum[k] = fmaf(BF ? 16.f : 1.f, (h[1] + h[3]) + (h[5] + h[7]), (h[0] + h[2]) + (h[4] + h[6]));
-    }
-    // the groups' sums, in the units of the products, with the zero of 8 or 1
-#pragma unroll
-    for (int o = 1; o < G / 8; o *= 2)
-#pragma unroll
-      for (int k = 0; k < kMake; ++k) sum[k] += __shfl_xor_sync(0xFFFFFFFFu, sum[k], o);
-#pragma unroll
-    for (int k = 0; k < kMake; ++k)
-      if (rr[k] < rows) {
-        sts128(place(rr[k], jj[k]), y[k]);
-        if (jj[k] % (G / 8) == 0) {
-          const float total = sum[k] * (BF ? (Z ? -0x1p-24f : -0x1p-21f) : (Z ? -0x1p-20f : -0x1p-17f));
-          float* to = sums + (jj[k] / (G / 8) * NT + rr[k] / 8) * 16 + rr[k] % 8 / 2 * 4 + rr[k] % 2;
-          to[0] = total;
-          to[2] = total;
-        }
-      }
   }
   all_sync();
 
   const int rw = warp % kFewGroups, kh = warp / kFewGroups, gq = lane / 4, t4 = lane % 4;
   const bool active = rw * 32 < g.R;
-  int back[NT][2];  // the rows' powers of two, to take back
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int r = n * 8 + 2 * t4 + e;
-      back[n][e] = r < rows ? (BF ? 24 : 20) - shifts[r] : 0;
-    }
-  all_sync();
   const int swz = gq >> 1 & 3;
   const uint32_t codes0 = smem_u32(smem) + (rw * 32 + gq) * 64;
   const uint32_t srow0 = smem_u32(sbuf) + (rw * 32 + gq) * kStride * 4, zrow0 = smem_u32(zbuf) + (rw * 32 + gq) * kZStride * 4;
@@ -357,7 +289,6 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
 #pragma unroll
   for (int n = 0; n < NT; ++n) frag0[n] = smem_u32(frag) + min(n * 8 + gq, rows - 1) * frag_row + t4 * 16;
   const int scale_dtype = g.scale_dtype, G_all = g.G, nk = g.nk, stages = g.stages;
-  const uint32_t sums0 = smem_u32(sums) + t4 * 16;
   auto release = [&](int slot) {
     __syncwarp();
     if (lane == 0) mbar_arrive_local(&bars.empty[slot]);
@@ -425,55 +356,34 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
 #pragma unroll
             for (int i = 0; i < 4; ++i) scale[i / 2][i % 2] = scale16(lds16(srow + i * 8 * kStride * 4 + j * 2), scale_dtype);
           }
-          float from[NT][4];  // -(zero or 1) sum h
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            const uint4 x = lds128(sums0 + ((ks * kPer + j) * NT + n) * 64);
-            from[n][0] = __uint_as_float(x.x), from[n][1] = __uint_as_float(x.y);
-            from[n][2] = __uint_as_float(x.z), from[n][3] = __uint_as_float(x.w);
-          }
           // groups of 128: everything the warp needs of the slot is in registers
           if constexpr (kPer == 1 && !Z) release(slot);
-          float part[2][NT][4];
+          uint32_t z[2][2];  // of each m tile's row halves
 #pragma unroll
-          for (int m = 0; m < 2; ++m) {
-            if constexpr (Z) {
-              float z[2];
-#pragma unroll
-              for (int h = 0; h < 2; ++h)  // small integers: 2^23 + z less 2^23
-                z[h] = __uint_as_float(0x4B000000u | (lds8(zrow + (m * 16 + h * 8) * kZStride * 4 + j) & 15u)) - 8388608.f;
-#pragma unroll
-              for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) part[m][n][e] = from[n][e] * z[e / 2];
-            }
-          }
+          for (int i = 0; i < 4; ++i) z[i / 2][i % 2] = Z ? lds8(zrow + i * 8 * kZStride * 4 + j) & 15u : 8u;
+          float part[kChains][2][NT][4] = {};
 #pragma unroll
           for (int i = 0; i < kLen; ++i) {
             uint4 b[NT];
 #pragma unroll
             for (int n = 0; n < NT; ++n) b[n] = lds128(frag0[n] + ks * 256 + (j * kLen + i) * 64);
-            // (a tile's two MMAs apart: the second waits for the first)
-            constexpr uint32_t kLow = 0x000F000Fu, kHigh = 0x00F000F0u, kEven = BF ? kLow : kHigh;
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
               const uint32_t lo = w[m][0][j * kLen + i], hi = w[m][1][j * kLen + i];
-              const uint32_t lo0 = BF ? lo : lo << 4, hi0 = BF ? hi : hi << 4;
+              const Operand<BF> z_lo(z[m][0]), z_hi(z[m][1]);
+              const uint32_t a0 = z_lo.template of<0>(lo), a1 = z_hi.template of<0>(hi), a2 = z_lo.template of<1>(lo),
+                             a3 = z_hi.template of<1>(hi);
 #pragma unroll
-              for (int n = 0; n < NT; ++n) {
-                if (i == 0 && !Z)
-                  mma16816_from(part[m][n], lo0 & kEven, hi0 & kEven, lo & kHigh, hi & kHigh, b[n].x, b[n].y, from[n]);
-                else
-                  mma16816(part[m][n], lo0 & kEven, hi0 & kEven, lo & kHigh, hi & kHigh, b[n].x, b[n].y);
-              }
+              for (int n = 0; n < NT; ++n) mma16816<BF>(part[0][m][n], a0, a1, a2, a3, b[n].x, b[n].y);
             }
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
-              const uint32_t lo = w[m][0][j * kLen + i] >> 8, hi = w[m][1][j * kLen + i] >> 8;
-              const uint32_t lo2 = BF ? lo : w[m][0][j * kLen + i] >> 4, hi2 = BF ? hi : w[m][1][j * kLen + i] >> 4;
+              const uint32_t lo = w[m][0][j * kLen + i], hi = w[m][1][j * kLen + i];
+              const Operand<BF> z_lo(z[m][0]), z_hi(z[m][1]);
+              const uint32_t a0 = z_lo.template of<2>(lo), a1 = z_hi.template of<2>(hi), a2 = z_lo.template of<3>(lo),
+                             a3 = z_hi.template of<3>(hi);
 #pragma unroll
-              for (int n = 0; n < NT; ++n)
-                mma16816(part[m][n], lo2 & kEven, hi2 & kEven, lo & kHigh, hi & kHigh, b[n].z, b[n].w);
+              for (int n = 0; n < NT; ++n) mma16816<BF>(part[kChains - 1][m][n], a0, a1, a2, a3, b[n].z, b[n].w);
             }
           }
 #pragma unroll
@@ -481,7 +391,10 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) acc[m][n][e] = fmaf(scale[m][e / 2], part[m][n][e], acc[m][n][e]);
+              for (int e = 0; e < 4; ++e) {
+                const float sum = kChains == 2 ? part[0][m][n][e] + part[1][m][n][e] : part[0][m][n][e];
+                acc[m][n][e] = fmaf(scale[m][e / 2], sum, acc[m][n][e]);
+              }
         }
       }
       if (!(kPer == 1 && !Z && ok && active)) release(slot);
@@ -533,11 +446,10 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
           const int r = n * 8 + 2 * t4 + e;
           if (r >= rows) continue;
           float* out = r < g.rows0 ? g.out0 + r * g.ld : g.out1 + (r - g.rows0) * g.ld;
-          const float a = power(back[n][e] / 2), b = power(back[n][e] - back[n][e] / 2);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const long long v = v0 + kh * 16 + h * 8 + gq;
-            if (v < g.V) out[v] = acc[0][n][2 * h + e] * a * b;
+            if (v < g.V) out[v] = acc[0][n][2 * h + e] * Operand<BF>::kUnit;
           }
         }
     }
@@ -548,7 +460,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
 inline long long few_smem(const Args& g, int group, int stages, int nt) {
   const int per = kFewK / group;
   return 1024LL + stages * (g.R * 64 + kFewTile * 4 * (few_stride(per) + (g.zeros ? few_zstride(per) : 0))) +
-         (g.rows0 + g.rows1) * (g.nk * 256LL + 64) + static_cast<long long>(g.nk) * per * nt * 64 + kFewWarps * nt * 128 * 4 + static_cast<int>(sizeof(FewBars));
+         (g.rows0 + g.rows1) * (g.nk * 256LL + 64) + kFewWarps * nt * 128 * 4 + static_cast<int>(sizeof(FewBars));
 }
 
 // Launches the call here if its states fit beside a ring of four stages
@@ -557,7 +469,7 @@ template <int NT, int G, bool Z, bool BF>
 sv_status start_few(Args g, const sv_q4_proj* proj, const void* s0, const void* s1, cudaStream_t stream) {
   int dev = 0;
   const int sms = sm_count(&dev);
-  // tile rows: as few rounds as tiles of 256 allow, then spread evenly, in warps' 32 rows
+  // tile rows: as few rounds as tiles of kFewTile allow, then spread evenly, in warps' 32 rows
   const long long rounds = (g.V + static_cast<long long>(sms) * kFewTile - 1) / (static_cast<long long>(sms) * kFewTile);
   g.R = static_cast<int>(((g.V + sms * rounds - 1) / (sms * rounds) + 31) / 32 * 32);
   g.tiles = (g.V + g.R - 1) / g.R;
