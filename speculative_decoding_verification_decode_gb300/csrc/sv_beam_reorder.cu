@@ -27,12 +27,13 @@ constexpr int kThreads = 256;
 // two of 96 KB 38 us, four of 48 KB 35, eight of 24 KB 33.8).
 constexpr int kStagedCtas = 8, kStageBytes = 24 * 1024;
 constexpr int kStates = 48;    // per launch: their descriptions are kernel parameters
-// Bytes of one segment that a CTA takes (of every beam): large ones where there
-// are many (few CTAs to start), small ones where a handful of large ones would
-// leave SMs without work at the end (151 MB in 420 large ones 44 us; 0.9 GB of
-// 16 beams' caches with 16 KB 135 us, with 8 KB 132, with 4 KB 138).
-constexpr int kLargeChunk = 65536, kSmallChunk = 8192;
-constexpr long long kManyCtas = 152 * 2 * 8;
+// Bytes of one segment that a CTA takes (of every beam).  Staged: 8 KB (64 x 4
+// beams of 64 KB 10 us, with 64 KB 33; 16 x 4 of 512 KB in 16 states 129 and
+// 135, with 4 KB 153).  Aligned: some 128 KB of all beams together, a few rounds
+// of a CTA's registers (4 beams, 16 states of 512 KB: 32 KB 106 us, 64 KB 109,
+// 8 KB 157; 16 beams, 4 states of 2 MB: 8 KB 98, 32 KB 110), but less where that
+// would leave SMs without a CTA (64 x 4 beams of 32 KB: 8 KB 4.3, 32 KB 5.9).
+constexpr int kMinChunk = 8192, kMaxChunk = 65536, kChunkOfAll = 131072, kSms = 152;
 
 struct State {
   char* data;
@@ -229,7 +230,18 @@ extern "C" sv_status sv_beam_reorder(const sv_beam_state* states, int32_t n_stat
   if (n_states < 1 || !states) return svh::fail(SV_ERR_ARG, "at least one state is needed");
   if (static_cast<long long>(batch) * beams > 0x7FFFFFFFLL) return svh::fail(SV_ERR_ARG, "batch * beams too large");
   int min_tokens = 0x7FFFFFFF;
-  long long all_ctas = batch;
+  const int status_ctas = static_cast<int>((static_cast<long long>(batch) + svb::kThreads - 1) / svb::kThreads);
+  // what divides every address and extent of a state
+  // (a timed state may end after any token, another one only at its end)
+  auto unit_of = [&](const sv_beam_state& s) {
+    unsigned long long any = reinterpret_cast<uintptr_t>(s.data) | 16u |
+                             static_cast<unsigned long long>(s.timed ? s.token_bytes : s.tokens * s.token_bytes);
+    if (batch > 1) any |= static_cast<unsigned long long>(s.seq_stride);
+    if (beams > 1) any |= static_cast<unsigned long long>(s.beam_stride);
+    if (s.segs > 1) any |= static_cast<unsigned long long>(s.seg_stride);
+    return static_cast<int>(any & (~any + 1));
+  };
+  long long all_ctas = 0, aligned_ctas = 0;  // of a sequence, in chunks of kMinChunk
   for (int i = 0; i < n_states; ++i) {
     const sv_beam_state& s = states[i];
     if (s.segs < 0 || s.tokens < 0 || s.token_bytes < 0)
@@ -244,10 +256,12 @@ extern "C" sv_status sv_beam_reorder(const sv_beam_state* states, int32_t n_stat
       if ((s.segs > 1 && s.seg_stride < bytes) || (beams > 1 && s.beam_stride < bytes))
         return svh::fail(SV_ERR_ARG, "state %d: a stride is shorter than a segment", i);
     }
-    const long long chunks = (bytes + svb::kLargeChunk - 1) / svb::kLargeChunk;
-    all_ctas += chunks > 0x7FFFFFFFLL ? 0x7FFFFFFFLL : chunks * s.segs;
-    if (all_ctas > 0x7FFFFFFFLL || (batch > 0 && all_ctas > 0x7FFFFFFFLL / batch))
+    const long long chunks = (bytes + svb::kMinChunk - 1) / svb::kMinChunk;
+    const long long ctas = s.segs == 0 ? 0 : chunks > 0x7FFFFFFFLL ? chunks : chunks * s.segs;
+    all_ctas += ctas;
+    if (all_ctas > 0x7FFFFFFFLL || (batch > 0 && all_ctas > (0x7FFFFFFFLL - status_ctas) / batch))
       return svh::fail(SV_ERR_UNSUPPORTED, "the states are too large for one call");
+    if (unit_of(s) == 16) aligned_ctas += ctas;
     if (s.timed) {
       if (!lengths) return svh::fail(SV_ERR_ARG, "state %d is timed: lengths is NULL", i);
       if (s.tokens < min_tokens) min_tokens = s.tokens;
@@ -256,17 +270,10 @@ extern "C" sv_status sv_beam_reorder(const sv_beam_state* states, int32_t n_stat
   if (batch == 0) return SV_OK;
   if (!parents || !status) return svh::fail(SV_ERR_ARG, "parents or status is NULL");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int chunk = all_ctas * batch < svb::kManyCtas ? svb::kSmallChunk : svb::kLargeChunk;
-  // what divides every address and extent of a state
-  // (a timed state may end after any token, another one only at its end)
-  auto unit_of = [&](const sv_beam_state& s) {
-    unsigned long long any = reinterpret_cast<uintptr_t>(s.data) | 16u |
-                             static_cast<unsigned long long>(s.timed ? s.token_bytes : s.tokens * s.token_bytes);
-    if (batch > 1) any |= static_cast<unsigned long long>(s.seq_stride);
-    if (beams > 1) any |= static_cast<unsigned long long>(s.beam_stride);
-    if (s.segs > 1) any |= static_cast<unsigned long long>(s.seg_stride);
-    return static_cast<int>(any & (~any + 1));
-  };
+  int aligned_chunk = svb::kMaxChunk;
+  while (aligned_chunk > svb::kMinChunk && (aligned_chunk * beams > svb::kChunkOfAll ||
+                                            aligned_ctas * batch * svb::kMinChunk < static_cast<long long>(svb::kSms) * aligned_chunk))
+    aligned_chunk /= 2;
   svb::Params p;
   p.parents = parents;
   p.lengths = lengths;
@@ -274,8 +281,7 @@ extern "C" sv_status sv_beam_reorder(const sv_beam_state* states, int32_t n_stat
   p.B = batch;
   p.W = beams;
   p.min_tokens = min_tokens;
-  p.chunk_bytes = chunk;
-  p.status_ctas = (batch + svb::kThreads - 1) / svb::kThreads;
+  p.status_ctas = status_ctas;
   p.n = 0;
   long long ctas = 0;
   auto launch = [&](bool staged) -> sv_status {
@@ -304,6 +310,8 @@ extern "C" sv_status sv_beam_reorder(const sv_beam_state* states, int32_t n_stat
     return SV_OK;
   };
   for (int kind = 0; kind < 2; ++kind) {  // aligned states, then the others
+    const int chunk = kind == 0 ? aligned_chunk : svb::kMinChunk;
+    p.chunk_bytes = chunk;
     for (int i = 0; i < n_states; ++i) {
       const sv_beam_state& s = states[i];
       const long long bytes = s.tokens * s.token_bytes;
