@@ -162,7 +162,11 @@ class BeamDecoder:
     the first ``lengths[b]`` tokens of each beam; deterministic and
     graph-capturable.  What it keeps per beam (caches, recurrent states) is
     given in ``states`` and moves with the beams.  A sequence whose tokens
-    fill ``max_len`` stays as it is from then on."""
+    fill ``max_len`` stays as it is from then on, and so does one that cannot
+    go on: ``status`` (int32 ``[B]``, SEQ_* bits, 0 where all is well) then
+    tells why, SEQ_BAD_VALUE for a NaN or +inf logit, SEQ_BAD_LAYOUT for a
+    length past the positions of a state with time (a state of ``max_len - 1``
+    positions holds every sequence).  Set to 0, the sequence goes on."""
 
     def __init__(self, step_fn: Callable, tokens: torch.Tensor, lengths: torch.Tensor, eos: int = -1,
                  states=(), time_dims=()):
@@ -182,28 +186,32 @@ class BeamDecoder:
         self.scores = torch.full((self.B, self.W), float("-inf"), device=dev)
         self.scores[:, 0] = 0.0
         self.finished = torch.zeros(self.B, self.W, dtype=torch.bool, device=dev)
-        self.rows = torch.arange(self.B, device=dev)
+        self.status = torch.zeros(self.B, dtype=torch.int32, device=dev)
         self.graph = None
 
     def step(self):
         """One token for every beam; returns the selection."""
         logits = self.step_fn(self.tokens, self.lengths)
         sel = api.beam_select(logits, self.scores, finished=self.finished if self.eos >= 0 else None, eos=self.eos)
-        full = (self.lengths >= self.max_len)[:, None]
-        sel.parents.masked_fill_(full, -1)
-        api.beam_reorder(self.states, sel.parents, self.lengths, self.time_dims)
-        at = self.lengths.long().clamp(max=self.max_len - 1)
-        self.tokens[self.rows, :, at] = torch.where(full, self.tokens[self.rows, :, at], sel.tokens.clamp(min=0))
+        length, status = self.lengths[:, None], self.status[:, None]
+        go = (length < self.max_len) & (status == 0)
+        sel = sel._replace(parents=torch.where(go, sel.parents, -1))
+        bad = (sel.status | api.beam_reorder(self.states, sel.parents, self.lengths, self.time_dims))[:, None]
+        torch.where(go, bad, status, out=status)
+        go = go & (bad == 0)
+        at = length.long().clamp_(0, self.max_len - 1)[:, None].expand(-1, self.W, -1)
+        kept = self.tokens.gather(2, at)
+        self.tokens.scatter_(2, at, torch.where(go, sel.tokens.clamp(min=0), kept[:, :, 0])[:, :, None])
         if self.eos >= 0:  # a finished beam's one candidate is eos again, so the token tells
-            self.finished.copy_(torch.where(full, self.finished, sel.tokens == self.eos))
-        self.scores.copy_(torch.where(full, self.scores, sel.scores))
-        self.lengths.add_(1).clamp_(max=self.max_len)
+            torch.where(go, sel.tokens == self.eos, self.finished, out=self.finished)
+        torch.where(go, sel.scores, self.scores, out=self.scores)
+        length.add_(go)
         return sel
 
     def capture(self):
         """Capture one step as a CUDA graph (after a warm-up step on a saved
         copy of the state, restored before the capture)."""
-        kept = [*self.states, self.lengths, self.scores, self.finished]
+        kept = [*self.states, self.lengths, self.scores, self.finished, self.status]
         saved = [t.clone() for t in kept]
         s = torch.cuda.Stream(self.tokens.device)
         s.wait_stream(torch.cuda.current_stream(self.tokens.device))
@@ -221,7 +229,8 @@ class BeamDecoder:
 
     def run(self, steps: int, graph: bool = True):
         """``steps`` steps, replaying the captured graph when ``graph``;
-        returns (tokens, lengths, scores), beams best first."""
+        returns (tokens, lengths, scores), beams best first (``status`` says
+        which sequences stopped)."""
         if graph and self.graph is None:
             self.capture()
         for _ in range(steps):
