@@ -58,6 +58,7 @@ constexpr int kGroupList = 1024; // groups read again before the ordered pass ta
 constexpr int kUnits = 8192;     // maxima in the bisection
 constexpr int kAhead = 12;        // of a row's maxima, loads per lane in flight
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kMaxF32 = 3.4028234663852886e38f;
 constexpr float kLarge = 1048576.f;  // |M| above this: the row's sum is taken precisely (l k - c would lose bits)
 
 struct Params {
@@ -491,11 +492,12 @@ __device__ __forceinline__ void score_entries(Shared& sm, int from, int L) {
 }
 
 // A row's f32 addend and margin from its score and its logarithm in f32.  An
-// addend that leaves f32's range says nothing.
+// addend that leaves f32's range, at either end (a score of 1e32 on a row whose
+// logits are all near the lowest f32), says nothing.
 __device__ __forceinline__ float set_add(Shared& sm, int w, float c, float lse, double eps) {
   const float a = __fsub_rn(c, lse);
-  const bool fits = a >= -3.4028234663852886e38f;
-  const float add = fits ? a : -3.4028234663852886e38f;
+  const bool fits = fabsf(a) <= kMaxF32;
+  const float add = fits ? a : copysignf(kMaxF32, a);
   sm.add[w] = add;
   sm.margin[w] = fits ? static_cast<float>(eps) + (fabsf(add) * 0x1p-22f + fabsf(c) * 0x1p-22f + fabsf(lse) * 0x1p-22f) : INFINITY;
   return add;
@@ -740,7 +742,7 @@ __device__ __forceinline__ void pick(const Params& P, int b) {
           hi = mid;
         }
       }
-      const float tau = key_f32(lo);
+      const float tau = fminf(key_f32(lo), kMaxF32);  // (a sum may round past f32's range: its row's margin is as wide)
       // (every warp computes, and writes, the same)
       float widest = 0.f, all_widest = 0.f;
 #pragma unroll 1
