@@ -38,9 +38,12 @@ size_t sv_beam_select_workspace_size(int32_t batch, int32_t beams, int32_t vocab
  * The n best continuations of every sequence.
  *   score(w, v) = scores[w] + logits[w][v] - ln sum_u exp(logits[w][u])
  *   best first; equal scores by the lower beam, then the lower token.  The
- *   order is that of the scores in 64 bits (the logarithm to better than
- *   2^-34), not of the rounded f32 outputs: candidates of two beams whose
- *   scores differ by less than that may come out in either order.
+ *   order is that of the scores in 64 bits, not of the rounded f32 outputs:
+ *   scores[w] + ((logits[w][v] - the row's maximum) - the logarithm of the sum
+ *   below that maximum), the logarithm to better than 2^-34 and the two sums
+ *   rounded once each.  Candidates of two beams whose scores differ by less
+ *   than 2^-34, or 2^-52 of the larger of |scores[w]| and |score|, may come out
+ *   in either order.
  * logits   [batch * beams] rows of `dtype`, `row_stride` elements apart
  *          (any element alignment); beam w of sequence b is row b * beams + w.
  * scores   [batch, beams] f32: the beams' accumulated log-probabilities; a

@@ -41,9 +41,12 @@ class BeamResult:
     gap: np.ndarray      # f64 [B]: smallest nonzero distance between neighbours of the order, the first left out included
 
 
-def _lse(row: np.ndarray) -> float:
-    m = float(row.max())
-    return m + math.log(math.fsum(np.exp(row - m)))
+def _log_softmax(row: np.ndarray) -> np.ndarray:
+    """``l - ln sum exp l``, the maximum taken off first: added to the
+    logarithm it would round that away where it is large (a row all at the
+    lowest f32 is uniform: -ln V each, not 0)."""
+    x = row - row.max()
+    return x - math.log(math.fsum(np.exp(x)))
 
 
 def beam_select(logits: np.ndarray, scores: np.ndarray, n: int, finished: Optional[np.ndarray] = None,
@@ -65,7 +68,7 @@ def beam_select(logits: np.ndarray, scores: np.ndarray, n: int, finished: Option
             if ended[w]:
                 s[w, eos] = c[w]
             elif live[w] and (x[w] > -np.inf).any():
-                s[w] = c[w] + (x[w] - _lse(x[w]))
+                s[w] = c[w] + _log_softmax(x[w])
         s = s.reshape(-1)
         with np.errstate(over="ignore"):
             s[s.astype(np.float32) == -np.inf] = -np.inf

@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
 // ---------------------------------------------------------------- the second kernel
 
 struct Shared {
-  double lse[SV_BEAM_MAX_BEAMS];
+  double log_sum[SV_BEAM_MAX_BEAMS];  // the row's logarithm less its maximum: ln sum e^(l - M)
   double cum[SV_BEAM_MAX_BEAMS];
   float M[SV_BEAM_MAX_BEAMS];
   float whole[SV_BEAM_MAX_BEAMS], rest[SV_BEAM_MAX_BEAMS];  // the logarithm to base 2: an integer and log2 of [1, 2)
@@ -367,7 +367,8 @@ __device__ __forceinline__ unsigned long long precise_term(float x, float M, con
   return counts ? q >> (shift & 63) : 0ull;
 }
 
-// The row's logarithm to better than 2^-35, by the whole CTA.
+// The row's logarithm less its maximum to better than 2^-35, by the whole CTA.
+// (Their sum would keep that only up to |M| = 2^18.)
 // (A call of 64 x 8 x 128256 with two equal beams in one sequence: 114 us, where
 // 64-bit conversions, a branch per term and loads without a successor took 187.)
 template <typename T>
@@ -407,7 +408,7 @@ __device__ __noinline__ void precise_lse(Shared& sm, const Params& P, int b, int
       lo += sm.sum_lo[i];
     }
     const double total = static_cast<double>(hi + (lo >> 32)) + static_cast<double>(lo & 0xFFFFFFFFu) * 0x1p-32;
-    sm.lse[w] = static_cast<double>(M) + log(total * 0x1p-28);
+    sm.log_sum[w] = log(total * 0x1p-28);
     sm.precise[w] = 1;
     sm.again[w] = 0;
   }
@@ -415,7 +416,7 @@ __device__ __noinline__ void precise_lse(Shared& sm, const Params& P, int b, int
 }
 
 __device__ __forceinline__ double score_of(const Shared& sm, int w, float l) {
-  return sm.ended[w] ? sm.cum[w] : sm.cum[w] + (static_cast<double>(l) - sm.lse[w]);
+  return sm.ended[w] ? sm.cum[w] : sm.cum[w] + ((static_cast<double>(l) - static_cast<double>(sm.M[w])) - sm.log_sum[w]);
 }
 
 __device__ __forceinline__ bool before(unsigned long long ka, int ia, unsigned long long kb, int ib) {
@@ -692,7 +693,7 @@ __device__ __forceinline__ void pick(const Params& P, int b) {
     for (int w = 0; w < P.W; ++w) {
       if (sm.again[w]) {
         precise_lse<T>(sm, P, b, w);
-        if (tid == 0) set_add(sm, w, P.scores[r0 + w], static_cast<float>(sm.lse[w]), P.eps);
+        if (tid == 0) set_add(sm, w, P.scores[r0 + w], static_cast<float>(static_cast<double>(sm.M[w]) + sm.log_sum[w]), P.eps);
         __syncthreads();
       }
       for (int u = tid; u < units; u += kPickThreads)
@@ -704,7 +705,8 @@ __device__ __forceinline__ void pick(const Params& P, int b) {
   if (tid < P.W) {
     constexpr double kBack = 1.0 / static_cast<double>(kLog2e);
     sm.cum[tid] = P.scores[r0 + tid];
-    if (!sm.precise[tid]) sm.lse[tid] = (static_cast<double>(sm.whole[tid]) + static_cast<double>(sm.rest[tid])) * kBack;
+    if (!sm.precise[tid])
+      sm.log_sum[tid] = (static_cast<double>(sm.whole[tid]) + static_cast<double>(sm.rest[tid])) * kBack - static_cast<double>(sm.M[tid]);
   }
 
   // tau: at least n units reach it, and hardly more than 2 n.  Where there are

@@ -48,6 +48,54 @@ def test_select_high_scores_on_the_lowest_logits(high, W, V, dtype):
                   <= 2.0 ** -24 * np.abs(o.scores[o.parents >= 0]) + 2.0 ** -17)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("at", [2.0 ** 20, 2.0 ** 30, 2.0 ** 40, -2.0 ** 40, 2.0 ** 100])
+def test_select_order_with_logits_far_from_zero(at, dtype):
+    """Rows of `count` equal maxima at a power of two, the other tokens twice
+    as far down or more: log-probabilities -ln count, exactly, whatever the
+    power.  Running scores take the beams to within an f32 step of one another;
+    the order is that of c - ln count in 64 bits."""
+    B, W, V, n = 16, 8, 700, 16
+    rng = np.random.default_rng(5)
+    low = -3.0 * abs(at)
+    x = np.full((B, W, V), low)
+    count = rng.integers(2, 60, (B, W))
+    first = np.zeros((B, W, 16), np.int64)
+    for b in range(B):
+        for w in range(W):
+            where = rng.permutation(V)[:count[b, w]]
+            x[b, w, where] = at
+            where.sort()
+            first[b, w, :min(16, count[b, w])] = where[:16]
+    c = (np.log(count) - 1.0).astype(np.float32)
+    score = c.astype(np.float64) - np.log(count)
+    for b in range(B):  # equal counts tie; the others are apart by more than 64-bit scores may be off
+        assert np.diff(np.unique(score[b])).min(initial=1.0) >= 1e-10
+    r = sv().beam_select(torch.from_numpy(x).to(dtype).to(DEV), torch.from_numpy(c).to(DEV), n)
+    p, t = r.parents.cpu().numpy(), r.tokens.cpu().numpy()
+    for b in range(B):
+        want = sorted((-score[b, w], w, int(first[b, w, i])) for w in range(W) for i in range(min(16, count[b, w])))[:n]
+        assert [(a, k) for a, k in zip(p[b].tolist(), t[b].tolist())] == [(w, v) for _, w, v in want]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("W,V", [(2, 3001), (4, 70000)])
+def test_select_rows_all_at_the_lowest(W, V, dtype):
+    """A row that a mask of the type's lowest value leaves nothing of is
+    uniform: its candidates have log-probability -ln V."""
+    n = 2 * W
+    x = torch.randn(3, W, V, generator=torch.Generator().manual_seed(W)).to(dtype)
+    x[0, 0] = x[1, 1] = x[2] = torch.finfo(dtype).min
+    c = torch.full((3, W), -1.0)
+    c[1, 1] = 20.0
+    r = sv().beam_select(x.to(DEV), c.to(DEV), n)
+    score = (c[:, :, None].double() + torch.log_softmax(x.double(), 2)).flatten(1)
+    s, i = score.sort(dim=1, descending=True, stable=True)
+    assert torch.equal(r.parents.cpu().long(), i[:, :n] // V) and torch.equal(r.tokens.cpu().long(), i[:, :n] % V)
+    assert ((r.scores.cpu().double() - s[:, :n]).abs() <= 2.0 ** -24 * s[:, :n].abs() + 2.0 ** -17).all()
+    assert (i[1, :n] // V == 1).all() and abs(float(s[1, 0]) - 20.0 + np.log(V)) < 1e-9
+
+
 def test_reorder_many_sequences():
     """More sequences than 46340: their square is no size of anything."""
     B, W = 50000, 3
