@@ -364,8 +364,9 @@ def q4_quantize(weight: torch.Tensor, group: int = 128, zeros: bool = False,
     """A ``[V, d]`` matrix in 4 bits, each weight rounded to the nearest step
     of its group.  Without ``zeros`` the steps are -8..7 times the scale, the
     largest magnitude at 7; with them 0..15 from the group's smallest to its
-    largest value (0 always among them).  Done once, where the weights are
-    laid out; any device."""
+    largest value (0 always among them).  A weight that is not finite, or a
+    group whose scale is past ``scale_dtype``'s largest number, is refused.
+    Done once, where the weights are laid out; any device."""
     if weight.dim() != 2 or group not in (32, 64, 128):
         raise ValueError("weight must be [V, d], group 32, 64 or 128")
     if weight.shape[1] % 32:
@@ -384,6 +385,8 @@ def q4_quantize(weight: torch.Tensor, group: int = 128, zeros: bool = False,
         scale = (w.abs().amax(2) / 7).to(scale_dtype)
         step = torch.where(scale > 0, scale.float(), 1.0)
         z = torch.full_like(step, 8.0)
+    if not bool(torch.isfinite(scale).all()):  # (an infinite scale would make every weight of its group NaN)
+        raise ValueError(f"a group of weights is not finite, or too large for scales in {scale_dtype}")
     q = ((w / step[..., None]).round() + z[..., None]).clamp(0, 15).to(torch.uint8).view(V, G * group)[:, :d]
     packed = q[:, 0::2] | (q[:, 1::2] << 4)
     return Q4Projection(packed.contiguous(), scale, z.to(torch.uint8) if zeros else None, group)
