@@ -95,7 +95,8 @@ typedef struct {
  * whose parent is negative (no candidate), keeps its contents, and so does
  * everything past the length.
  * states   host array of n_states descriptions (copied by the call).  Two
- *          states must not share memory, nor two beams of one.
+ *          states must not share memory, nor two beams of one, nor a state
+ *          with parents, lengths or status.
  * parents  [batch, beams] int32; lengths [batch] int32, or NULL when no state
  *          is timed.
  * status   [batch]: 0, or SV_SEQ_BAD_LAYOUT (a parent >= beams, or a length

@@ -738,7 +738,7 @@ def beam_reorder(states: Union[torch.Tensor, Sequence[torch.Tensor]], parents: t
     slot ``w`` of sequence ``b`` receives what slot ``parents[b, w]`` held
     before the call; a negative parent leaves its slot as it is.  ``states``:
     one CUDA tensor ``[B, W, ...]`` or several, of any types; none may share
-    memory with another.  ``lengths [B]`` with ``time_dim`` (one dimension for
+    memory with another, nor with ``parents`` or ``lengths``.  ``lengths [B]`` with ``time_dim`` (one dimension for
     all states, or one per state, None for a state without time): only the
     first ``lengths[b]`` positions along it are in use and move.  Returns the
     per-sequence status (int32 ``[B]``)."""
@@ -782,6 +782,8 @@ def beam_reorder(states: Union[torch.Tensor, Sequence[torch.Tensor]], parents: t
         if lengths.numel() != B:
             raise ValueError("lengths must be [B]")
         lengths = _like(lengths, dev, torch.int32)
+    if parents.data_ptr() in seen or lengths is not None and lengths.data_ptr() in seen:
+        raise ValueError("parents or lengths is a state too: it would move while it is read")
     st = torch.empty(B, dtype=torch.int32, device=dev)
     _launch(dev, _lib.load().sv_beam_reorder, (ctypes.c_int64 * len(words))(*words), len(states), parents.data_ptr(),
             None if lengths is None else lengths.data_ptr(), B, W, st.data_ptr())

@@ -124,3 +124,15 @@ def test_reorder_one_segment_per_beam(B, elements):
     d = t.to(DEV)
     assert (sv().beam_reorder(d, parents.to(DEV)) == 0).all()
     assert torch.equal(d.cpu(), t[torch.arange(B)[:, None], parents.long()])
+
+
+def test_reorder_refuses_its_own_arguments_as_states():
+    """Parents or lengths that would move while they are read."""
+    p = torch.zeros(2, 3, dtype=torch.int32, device=DEV)
+    ln = torch.zeros(2, dtype=torch.int32, device=DEV)
+    q = torch.zeros(2, 1, dtype=torch.int32, device=DEV)
+    t = torch.zeros(2, 3, 8, device=DEV)
+    for states, kw in (([t, p], {}), (p, {}), (ln[:, None], dict(parents=q, lengths=ln))):
+        with pytest.raises(ValueError, match="while it is read"):
+            sv().beam_reorder(states, **{"parents": p, **kw})
+    assert (sv().beam_reorder([t, p], p.long()) == 0).all()  # (a copy of them is read)
