@@ -60,6 +60,11 @@ constexpr int kAhead = 12;        // of a row's maxima, loads per lane in flight
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMaxF32 = 3.4028234663852886e38f;
 constexpr float kLarge = 1048576.f;  // |M| above this: the row's sum is taken precisely (l k - c would lose bits)
+// A maximum below this (a stretch of masked logits) leaves no sum: its base is off
+// by 64 and more, so terms could be infinite, and so that a join's power of two,
+// 0, would make NaN of them.  Beside a larger maximum they are nothing; a row of
+// such alone is taken precisely.
+constexpr float kMasked = -1073741824.f;
 
 struct Params {
   const void* logits;
@@ -201,7 +206,7 @@ __device__ __forceinline__ void join(float& M, float& s, float M2, float s2) {
   const float m = svk::fmax_nan(M, M2);
   if (m == M2 && M == M2) {
     s += s2;
-  } else if (m > -INFINITY && m < INFINITY) {
+  } else if (m > kMasked && m < INFINITY) {
     const float c = base_of(m);
     s = (M > -INFINITY ? s * svk::ex2_ftz(base_of(M) - c) : 0.f) + (M2 > -INFINITY ? s2 * svk::ex2_ftz(base_of(M2) - c) : 0.f);
   }
@@ -230,7 +235,7 @@ __device__ __forceinline__ void stream_groups(const Row<T>& row, float* gmax, in
       if (g + 1 < groups) gmax[g + 1] = mb;
     }
     const float m = svk::fmax_nan(M, svk::fmax_nan(ma, mb));
-    if (m > -INFINITY && m < INFINITY) {
+    if (m > kMasked && m < INFINITY) {
       const float c = base_of(m);
       if (M > -INFINITY && M < m) s *= svk::ex2_ftz(base_of(M) - c);
       float t[4];

@@ -96,6 +96,35 @@ def test_select_rows_all_at_the_lowest(W, V, dtype):
     assert (i[1, :n] // V == 1).all() and abs(float(s[1, 0]) - 20.0 + np.log(V)) < 1e-9
 
 
+@pytest.mark.parametrize("low", [-1e9, -1e10, -1e20, -1e30, "lowest"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("B,W,V", [(3, 1, 513), (4, 3, 20000), (24, 2, 40000), (2, 8, 129281)])
+def test_select_masked_stretches(B, W, V, dtype, low):
+    """Stretches of a row at a mask's value, before, behind and around the
+    tokens that are left: the masked ones add nothing to the row's sum,
+    wherever a warp or a slice begins.  Beams far apart, so that no pair of
+    them is near enough to have its logarithms taken again."""
+    if low == "lowest" or dtype == torch.float16:
+        low = torch.finfo(dtype).min
+    n = 6
+    g = torch.Generator().manual_seed(V)
+    x = torch.randn(B, W, V, generator=g)
+    left = [slice(V - V // 5, V), slice(0, V // 7), slice(V // 2, V // 2 + 9), slice(V - 7, V)]
+    for b in range(B):
+        for w in range(W):
+            keep = x[b, w, left[(b + w) % 4]].clone()
+            x[b, w] = low
+            x[b, w, left[(b + w) % 4]] = keep
+    x = x.to(dtype)
+    c = -20.0 * torch.arange(W)[None, :] - torch.rand(B, W, generator=g)
+    r = sv().beam_select(x.to(DEV), c.to(DEV), n)
+    o = oracle.beam_select(x.double().numpy(), c.numpy(), n)
+    assert (r.status == 0).all()
+    assert np.array_equal(r.parents.cpu().numpy(), o.parents) and np.array_equal(r.tokens.cpu().numpy(), o.tokens)
+    d = np.abs(r.scores.cpu().numpy().astype(np.float64) - o.scores)
+    assert (d <= 2.0 ** -24 * np.abs(o.scores) + 2.0 ** -17).all(), d.max()
+
+
 def test_reorder_many_sequences():
     """More sequences than 46340: their square is no size of anything."""
     B, W = 50000, 3
