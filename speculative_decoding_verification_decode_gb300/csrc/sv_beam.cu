@@ -624,7 +624,7 @@ __device__ __forceinline__ void pick(const Params& P, int b) {
   int finite = 0;
   bool bad = false, large = false;
   auto put = [&](int at, float x) {
-    const unsigned k = f32_key(x);
+    const unsigned k = f32_key(x + 0.f);  // (-0 is 0)
     sm.unit[at] = k;
     if (k > none) {
       ++finite;
@@ -709,7 +709,7 @@ __device__ __forceinline__ void pick(const Params& P, int b) {
 
   if (tid < P.W) {
     constexpr double kBack = 1.0 / static_cast<double>(kLog2e);
-    sm.cum[tid] = P.scores[r0 + tid];
+    sm.cum[tid] = P.scores[r0 + tid] + 0.f;  // (a score of -0 is one of 0)
     if (!sm.precise[tid])
       sm.log_sum[tid] = (static_cast<double>(sm.whole[tid]) + static_cast<double>(sm.rest[tid])) * kBack - static_cast<double>(sm.M[tid]);
   }

@@ -125,6 +125,19 @@ def test_select_masked_stretches(B, W, V, dtype, low):
     assert (d <= 2.0 ** -24 * np.abs(o.scores) + 2.0 ** -17).all(), d.max()
 
 
+@pytest.mark.parametrize("ended", [False, True])
+def test_select_minus_zero(ended):
+    """A score of -0 ties with one of 0: the lower beam first."""
+    W, V = 4, 3
+    x = torch.full((2, W, V), -float("inf"))
+    x[:, :, 1] = torch.tensor([-0.0, 0.0, 0.0, -0.0])
+    c = torch.tensor([[-0.0, 0.0, -0.0, 0.0], [0.0, -0.0, 0.0, -0.0]])
+    fin = torch.tensor([[True, False, True, False], [True, True, True, True]]) if ended else None
+    for n in (1, 2, 4):
+        r = sv().beam_select(x.to(DEV), c.to(DEV), n, None if fin is None else fin.to(DEV), 1 if ended else -1)
+        assert r.parents.tolist() == [list(range(n))] * 2 and (r.tokens == 1).all() and (r.scores == 0).all()
+
+
 def test_reorder_many_sequences():
     """More sequences than 46340: their square is no size of anything."""
     B, W = 50000, 3
