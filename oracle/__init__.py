@@ -12,7 +12,8 @@ front of the verification.  ``sampler_filter`` holds the top-k / top-p filters a
 before verification (llmstudio.ru section 38); ``penalties`` the repetition,
 frequency and presence penalties ahead of them, with the sampler state of
 each row following the speculative branch (sections 38-39).  ``lm_head_q4`` is the LM head on weights in 4 bits,
-``beam`` beam search's selection and the reordering of its states.  ``draft_gate`` is the
+``beam`` beam search's selection and the reordering of its states, ``tree`` drafted trees and their attention over a paged cache,
+``cache`` the pages of such caches.  ``draft_gate`` is the
 draft-length gate that produces the ragged ``cu_k``
 (PocketLLM docs/dspark.md, the draft-length gate section).
 
@@ -75,6 +76,12 @@ from .beam import (  # noqa: F401
     BeamResult,
     beam_select,
     beam_reorder,
+)
+from . import cache  # noqa: F401
+from .tree import (  # noqa: F401
+    tree_attention,
+    verify_tree,
+    verify_tree_greedy,
 )
 from .penalties import (  # noqa: F401
     penalize_value,

@@ -16,6 +16,7 @@ from ._lib import (  # noqa: F401
     SEQ_BAD_VALUE,
     SEQ_EXACT_PATH,
     SEQ_NEAR_BOUNDARY,
+    SEQ_NO_PAGES,
     SEQ_TIMEOUT,
     SEQ_ZERO_MASS,
     load as load_library,
@@ -24,8 +25,11 @@ from .api import (  # noqa: F401
     BeamCandidates,
     GateResult,
     LMHeadResult,
+    PagedCache,
     Q4Projection,
     SVError,
+    TreeAttention,
+    TreeResult,
     VerifyResult,
     accept,
     accept_from_logits,
@@ -33,15 +37,22 @@ from .api import (  # noqa: F401
     beam_reorder,
     beam_select,
     beam_select_workspace,
+    cache_append,
+    cache_fork,
+    cache_truncate,
     gate_draft_lengths,
     gate_update,
     lm_head_logits,
     lm_head_verify,
     lm_head_verify_static,
     lm_head_workspace,
+    paged_cache,
     q4_quantize,
     sampler_floors,
+    tree_attention,
     verify_greedy,
+    verify_tree,
+    verify_tree_greedy,
 )
 from ._build import build  # noqa: F401
 from .decoder import BeamDecoder, SpeculativeDecoder  # noqa: F401,E402

@@ -10,9 +10,11 @@ LIB_DIR = os.path.join(PKG_DIR, "lib")
 LIB_PATH = os.path.join(LIB_DIR, "libsv.so")
 SOURCES = [os.path.join(CSRC, f) for f in ("sv_api.cu", "sv_gate.cu", "sv_filter.cu", "sv_lm_head.cu", "sv_static.cu", "sv_penalties.cu", "sv_rows.cu",
                                             "sv_beam.cu", "sv_beam_reorder.cu", "sv_lm_head_q4.cu", "sv_lm_head_q4_bf16.cu", "sv_lm_head_q4_f16.cu",
-                                            "sv_lm_head_q4_few_bf16.cu", "sv_lm_head_q4_few_f16.cu")]
+                                            "sv_lm_head_q4_few_bf16.cu", "sv_lm_head_q4_few_f16.cu", "sv_verify_tree.cu", "sv_tree_attention.cu",
+                                            "sv_cache.cu")]
 HEADERS = [os.path.join(CSRC, f) for f in ("sv_kernel.cuh", "sv_verify.cuh", "sv_rows.cuh", "sv_topk.cuh", "sv_ptx.cuh", "sv_host.h", "sv_lm_head_q4.cuh", "sv_lm_head_q4_few.cuh")] + [
-    os.path.join(os.path.dirname(PKG_DIR), "include", h) for h in ("sv.h", "sv_gate.h", "sv_filter.h", "sv_lm_head.h", "sv_penalties.h", "sv_beam.h", "sv_lm_head_q4.h")]
+    os.path.join(os.path.dirname(PKG_DIR), "include", h) for h in ("sv.h", "sv_gate.h", "sv_filter.h", "sv_lm_head.h", "sv_penalties.h", "sv_beam.h", "sv_lm_head_q4.h",
+                                                                "sv_tree.h", "sv_cache.h")]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",

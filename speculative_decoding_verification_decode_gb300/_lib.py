@@ -7,12 +7,13 @@ import re
 from ._build import LIB_PATH, PKG_DIR
 
 HEADERS = [os.path.join(os.path.dirname(PKG_DIR), "include", h) for h in ("sv.h", "sv_gate.h", "sv_filter.h", "sv_lm_head.h", "sv_penalties.h",
-                                                                                   "sv_beam.h", "sv_lm_head_q4.h")]
+                                                                                   "sv_beam.h", "sv_lm_head_q4.h", "sv_tree.h", "sv_cache.h")]
 
 SV_F32, SV_BF16, SV_F16 = 0, 1, 2
 SV_OK, SV_ERR_ARG, SV_ERR_CUDA, SV_ERR_UNSUPPORTED = 0, 1, 2, 3
 SEQ_BAD_TOKEN, SEQ_BAD_VALUE, SEQ_ZERO_MASS, SEQ_NEAR_BOUNDARY = 1, 2, 4, 8
 SEQ_EXACT_PATH, SEQ_TIMEOUT, SEQ_BAD_LAYOUT = 16, 32, 64
+SEQ_NO_PAGES = 128  # cache_append: not enough free pages, or no room in the table row
 FLAG_FORCE_EXACT = 1
 FLAG_EXPIRE_EXCHANGE = 2  # testing aid: exchange waits give up at once (SV_SEQ_TIMEOUT)
 FLAG_PLAN_ROWS = 4  # the row-parallel plan where the shape allows it
@@ -81,6 +82,20 @@ SIGNATURES = {
     "sv_lm_head_q4_logits": (_i32, [_vp, _i32, ctypes.POINTER(Q4Proj), _i32, _i32, _i32, _vp, _i64, _vp, _vp]),
     "sv_lm_head_q4_verify": (_i32, [_vp, _vp, _i32, ctypes.POINTER(Q4Proj), _i32, _vp, _vp, _vp, _vp, _i32, _i32,
                                     _i32, _i32, _vp, _vp, _vp, _vp, ctypes.c_size_t, _u32, _vp]),
+    "sv_verify_tree_workspace_size": (ctypes.c_size_t, [_i32]),
+    # target, dtype, stride, tokens, parents, cu_nodes, B, n, total, V, n_accepted, next, path, status, workspace, stream
+    "sv_verify_tree_greedy": (_i32, [_vp, _i32, _i64, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp,
+                                     _vp, ctypes.c_size_t, _vp]),
+    "sv_verify_tree": (_i32, [_vp, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp]),
+    "sv_tree_attention_workspace_size": (ctypes.c_size_t, [_i32]),
+    # sv_tree_attn (words of 64 bits), scale, workspace, stream
+    "sv_tree_attention": (_i32, [_vp, ctypes.c_float, _vp, ctypes.c_size_t, _vp]),
+    "sv_cache_append_workspace_size": (ctypes.c_size_t, [_i32, _i32, _i32, _i32]),
+    # sv_cache_pages and sv_cache_rows (words of 64 bits), pools, rows, n_pools, counts, path, cu_nodes, n, total,
+    # status, workspace, stream
+    "sv_cache_append": (_i32, [_vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _i32, _i32, _vp, _vp, ctypes.c_size_t, _vp]),
+    "sv_cache_truncate": (_i32, [_vp, _vp, _vp, _vp]),
+    "sv_cache_fork": (_i32, [_vp, _vp, _i32, _vp, _vp]),
     "sv_status_string": (ctypes.c_char_p, [_i32]),
     "sv_last_error": (ctypes.c_char_p, []),
     "sv_version": (_i32, []),

@@ -788,3 +788,387 @@ def beam_reorder(states: Union[torch.Tensor, Sequence[torch.Tensor]], parents: t
     _launch(dev, _lib.load().sv_beam_reorder, (ctypes.c_int64 * len(words))(*words), len(states), parents.data_ptr(),
             None if lengths is None else lengths.data_ptr(), B, W, st.data_ptr())
     return st
+
+
+# ---------------------------------------------------------------- trees of drafted tokens
+
+class TreeResult(NamedTuple):
+    n_accepted: torch.Tensor  # int32 [B]: nodes accepted after node 0
+    next_token: torch.Tensor  # int32 [B]: the target's token after the last of them; -1 where there is none
+    path: torch.Tensor  # int32 [B, n]: node 0, then the accepted nodes, then -1
+    status: torch.Tensor  # int32 [B]; OR of SEQ_* bits
+
+
+class TreeAttention(NamedTuple):
+    out: torch.Tensor  # [total, Hq, D], the queries' type
+    lse: torch.Tensor  # f32 [total, Hq]: natural logarithm of each row's sum of exponentials
+    status: torch.Tensor  # int32 [B]; SEQ_BAD_LAYOUT or 0
+
+
+def _words(t: Optional[torch.Tensor], dev: torch.device, what: str) -> Optional[torch.Tensor]:
+    """``t`` as contiguous int32 on ``dev``."""
+    if t is None:
+        return None
+    if t.is_floating_point() or t.dtype == torch.bool:
+        raise ValueError(f"{what} must be whole numbers")
+    return _like(t, dev, torch.int32)
+
+
+def _tree_layout(total: int, B: Optional[int], cu_nodes: Optional[torch.Tensor], n: Optional[int], what: str):
+    """(B, n) of ``total`` rows of nodes."""
+    if cu_nodes is not None:
+        if n is None:
+            raise ValueError("n (the most nodes of a sequence) is required with cu_nodes")
+        if cu_nodes.numel() < 1 or B is not None and cu_nodes.numel() != B + 1:
+            raise ValueError("cu_nodes must be [B + 1]")
+        return cu_nodes.numel() - 1, int(n)
+    if n is None:
+        if not B:
+            raise ValueError("n (the nodes of a sequence) is required")
+        n = total // B
+    n = int(n)
+    if B is None:
+        B = total // n if n > 0 else 0
+    if n < 0 or B * n != total:
+        raise ValueError(f"without cu_nodes, {what} must hold n rows for every sequence")
+    return B, n
+
+
+def _verify_tree(rows, choices, tokens, parents, cu_nodes, n) -> TreeResult:
+    ref = rows if choices is None else choices
+    if not ref.is_cuda:
+        m = _Marshal(ref)
+        r = _verify_tree(m.dev(rows), m.dev(choices), m.dev(tokens), m.dev(parents), m.dev(cu_nodes), n)
+        return TreeResult(*(x.cpu() for x in r))
+    dev = ref.device
+    B = None
+    if tokens.dim() == 2:
+        B = tokens.shape[0]
+    if n is None and tokens.dim() == 2:
+        n = tokens.shape[1]
+    total = tokens.numel()
+    B, n = _tree_layout(total, B, cu_nodes, n, "tokens")
+    if max(total, n) >= 2**31:
+        raise ValueError("sizes must be below 2^31")
+    tokens, cu = _words(tokens, dev, "tokens"), _words(cu_nodes, dev, "cu_nodes")
+    if parents is not None:
+        if parents.numel() != total:
+            raise ValueError("parents must have one entry for each token")
+        parents = _words(parents, dev, "parents")
+    out = torch.empty((3, B), dtype=torch.int32, device=dev)
+    path = torch.empty((B, n), dtype=torch.int32, device=dev)
+    lib = _lib.load()
+    if choices is None:
+        dtype = _DTYPES.get(rows.dtype)
+        if dtype is None:
+            raise ValueError("target must be float32, bfloat16 or float16")
+        if rows.dim() != 3 and rows.dim() != 2:
+            raise ValueError("target must be [total, V] or [B, n, V]")
+        rows = _rows(rows)
+        V, stride = rows.shape[1], rows.stride(0)
+        if rows.shape[0] != total:
+            raise ValueError(f"target must hold one row for each of the {total} tokens (got {rows.shape[0]})")
+        if V >= 2**31:
+            raise ValueError("sizes must be below 2^31")
+        if stride < V and total > 1:
+            rows, stride = rows.contiguous(), V
+        _launch(dev, lib.sv_verify_tree_greedy, rows.data_ptr(), dtype, stride, tokens.data_ptr(), _p(parents), _p(cu),
+                B, n, total, V, out.data_ptr(), out.data_ptr() + 4 * B, path.data_ptr(), out.data_ptr() + 8 * B, None, 0)
+    else:
+        if choices.numel() != total:
+            raise ValueError("choices must have one entry for each token")
+        choices = _words(choices, dev, "choices")
+        _launch(dev, lib.sv_verify_tree, choices.data_ptr(), tokens.data_ptr(), _p(parents), _p(cu), B, n, total,
+                out.data_ptr(), out.data_ptr() + 4 * B, path.data_ptr(), out.data_ptr() + 8 * B)
+    return TreeResult(out[0], out[1], path, out[2])
+
+
+def verify_tree_greedy(target: torch.Tensor, tokens: torch.Tensor, parents: Optional[torch.Tensor] = None,
+                       cu_nodes: Optional[torch.Tensor] = None, n: Optional[int] = None) -> TreeResult:
+    """Greedy verification of a drafted tree (include/sv_tree.h): from node 0 of
+    every sequence, whose children's tokens follow the target's argmax the
+    furthest.  ``target [total, V]`` (or ``[B, n, V]``): the rows after each
+    node, probabilities or logits, f32 / bf16 / f16.  ``tokens`` and
+    ``parents``, ``[total]`` or ``[B, n]``: a node's token (node 0's is not
+    looked at) and the earlier node it continues, -1 for none; without
+    ``parents`` every node continues the one before.  ``cu_nodes [B + 1]`` with
+    ``n`` (the most nodes of a sequence): ragged trees.  At most 256 nodes each."""
+    return _verify_tree(target, None, tokens, parents, cu_nodes, n)
+
+
+def verify_tree(choices: torch.Tensor, tokens: torch.Tensor, parents: Optional[torch.Tensor] = None,
+                cu_nodes: Optional[torch.Tensor] = None, n: Optional[int] = None) -> TreeResult:
+    """verify_tree_greedy for choices that have been drawn: ``choices`` (int32,
+    one per node) is the target's token after it.  For sampling they come from
+    ``accept_from_logits`` on the nodes' rows without drafts (its
+    ``next_token``); what is emitted then follows the target's distribution
+    whatever the tree holds."""
+    return _verify_tree(None, choices, tokens, parents, cu_nodes, n)
+
+
+@functools.lru_cache(maxsize=64)
+def _attention_bytes(dim: int) -> int:
+    return int(_lib.load().sv_tree_attention_workspace_size(dim))
+
+
+def _aligned(t: torch.Tensor) -> torch.Tensor:
+    """``t [., H, D]`` itself where its last dimension has unit stride and the
+    others, and its address, are multiples of 16 bytes; else a copy."""
+    s = t.stride()
+    if (s[2] != 1 and t.shape[2] > 1) or s[0] % 8 or s[1] % 8 or t.data_ptr() % 16:
+        t = t.contiguous()
+        if t.data_ptr() % 16:
+            t = t.clone()
+    return t
+
+
+def tree_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                   table: torch.Tensor, lengths: torch.Tensor, parents: Optional[torch.Tensor] = None,
+                   cu_nodes: Optional[torch.Tensor] = None, n: Optional[int] = None, scale: Optional[float] = None,
+                   out: Optional[torch.Tensor] = None) -> TreeAttention:
+    """Attention of drafted nodes over their sequence's cached tokens and their
+    own ancestors (include/sv_tree.h).  ``q [total, Hq, D]``, ``k``, ``v
+    [total, Hkv, D]`` (or ``[B, n, H, D]``): the nodes' own; ``k_cache``,
+    ``v_cache [pages, page_size, Hkv, D]`` with ``table [B, max_pages]`` and
+    ``lengths [B]``: token t of sequence b is in page ``table[b, t //
+    page_size]``.  All in bf16 or all in f16.  ``parents``, ``cu_nodes``, ``n``
+    as ``verify_tree_greedy`` takes them (without ``parents`` a chain, so one
+    token per sequence is plain decoding); at most 256 nodes per sequence.
+    ``scale``: default ``D ** -0.5``.  ``out``: optional tensor for the result;
+    rows past the last sequence are left as they are."""
+    dev = q.device
+    if dev.type != "cuda":
+        raise ValueError("q must be a CUDA tensor (the caches stay where they are)")
+    if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad
+                                    or k_cache.requires_grad or v_cache.requires_grad):
+        raise ValueError("tree_attention has no backward pass: call it under torch.no_grad()")
+    dtype = _DTYPES.get(q.dtype)
+    if dtype is None or dtype == _lib.SV_F32:
+        raise ValueError("q must be bfloat16 or float16")
+    for t, what in ((k, "k"), (v, "v"), (k_cache, "k_cache"), (v_cache, "v_cache")):
+        if t.dtype != q.dtype or t.device != dev:
+            raise ValueError(f"{what} must have the type and device of q")
+    if q.dim() == 4 and k.dim() == 4 and v.dim() == 4 and cu_nodes is None:
+        if n is None:
+            n = q.shape[1]
+        q, k, v = q.flatten(0, 1), k.flatten(0, 1), v.flatten(0, 1)
+    if q.dim() != 3 or k.dim() != 3 or v.shape != k.shape or k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2]:
+        raise ValueError("q must be [total, Hq, D], k and v [total, Hkv, D]")
+    total, Hq, D = q.shape
+    Hkv = k.shape[1]
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape or k_cache.shape[2] != Hkv or k_cache.shape[3] != D:
+        raise ValueError(f"the caches must be [pages, page_size, {Hkv}, {D}]")
+    if table.dim() != 2 or table.dtype != torch.int32 or table.device != dev or table.stride(1) != 1 and table.shape[1] > 1:
+        raise ValueError("table must be int32 [B, max_pages] on q's device with unit stride along a row")
+    B = table.shape[0]
+    if lengths.numel() != B:
+        raise ValueError("lengths must be [B]")
+    _, n = _tree_layout(total, B, cu_nodes, n, "q")
+    if max(total, abs(n), Hq) >= 2**31:
+        raise ValueError("sizes must be below 2^31")
+    lengths, cu = _words(lengths, dev, "lengths"), _words(cu_nodes, dev, "cu_nodes")
+    if parents is not None:
+        if parents.numel() != total:
+            raise ValueError("parents must have one entry for each row of q")
+        parents = _words(parents, dev, "parents")
+    q, k, v = _aligned(q), _aligned(k), _aligned(v)
+    for t, what in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        s = t.stride()
+        if (s[3] != 1 and D > 1) or s[0] % 8 or s[1] % 8 or s[2] % 8 or t.data_ptr() % 16:
+            raise ValueError(f"{what} must have unit stride along the head dimension, its address and other strides multiples of 16 bytes")
+    if out is None:
+        out = torch.empty((total, Hq, D), dtype=q.dtype, device=dev)
+    elif (out.shape[0] < total or out.shape[1:] != q.shape[1:] or out.dtype != q.dtype or out.device != dev or out.stride(2) != 1
+          or out.stride(0) % 8 or out.stride(1) % 8 or out.data_ptr() % 16):
+        raise ValueError("out must be like q with at least its rows, its address and strides multiples of 16 bytes")
+    lse = torch.empty((total, Hq), dtype=torch.float32, device=dev)
+    status = torch.empty(B, dtype=torch.int32, device=dev)
+    need = _attention_bytes(D)
+    workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    qs, ks, vs, os, kc, vc = q.stride(), k.stride(), v.stride(), out.stride(), k_cache.stride(), v_cache.stride()
+    words = (dtype, Hq, Hkv, D, q.data_ptr(), k.data_ptr(), v.data_ptr(), qs[0], qs[1], ks[0], ks[1], vs[0], vs[1],
+             k_cache.data_ptr(), v_cache.data_ptr(), kc[0], kc[1], kc[2], vc[0], vc[1], vc[2], k_cache.shape[0],
+             k_cache.shape[1], table.data_ptr(), table.stride(0), table.shape[1], lengths.data_ptr(), _p(parents) or 0,
+             _p(cu) or 0, B, n, total, out.data_ptr(), os[0], os[1], lse.data_ptr(), status.data_ptr())
+    _launch(dev, _lib.load().sv_tree_attention, (ctypes.c_int64 * 37)(*words),
+            D ** -0.5 if scale is None else float(scale), workspace.data_ptr(), need)
+    return TreeAttention(out, lse, status)
+
+
+# ---------------------------------------------------------------- paged caches
+
+class PagedCache(NamedTuple):
+    """A model's key / value caches in pages (include/sv_cache.h).  One page
+    table serves the pools of all layers; ``paged_cache`` makes an empty one."""
+    keys: Sequence[torch.Tensor]  # per layer [pages, page_size, Hkv, D]
+    values: Sequence[torch.Tensor]
+    table: torch.Tensor  # int32 [..., max_pages], a row per sequence; entries past its length mean nothing
+    lengths: torch.Tensor  # int32 [...]: tokens of each sequence
+    refs: torch.Tensor  # int32 [pages]: table entries in use that name each page; 0: free
+
+
+def paged_cache(layers: int, pages: int, page_size: int, heads: int, dim: int, sequences: Union[int, Sequence[int]],
+                max_pages: int, dtype: torch.dtype = torch.bfloat16, device=None) -> PagedCache:
+    """An empty cache of ``layers`` layers; ``sequences``: their number, or
+    ``(groups, width)`` for the groups that ``cache_fork`` takes (beams).  The
+    pools are not initialised: nothing past a sequence's length is ever used."""
+    dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
+    shape = (sequences,) if isinstance(sequences, int) else tuple(sequences)
+    pool = lambda: [torch.empty(pages, page_size, heads, dim, dtype=dtype, device=dev) for _ in range(layers)]
+    word = lambda *s: torch.zeros(s, dtype=torch.int32, device=dev)
+    return PagedCache(pool(), pool(), word(*shape, max_pages), word(*shape), word(pages))
+
+
+def _pages_arg(c: PagedCache) -> tuple:
+    """(words of sv_cache_pages, sequences, device) of a checked cache."""
+    table, lengths, refs = c.table, c.lengths, c.refs
+    dev = table.device
+    if dev.type != "cuda":
+        raise ValueError("the cache must be CUDA tensors (modified in place)")
+    for t, what in ((table, "table"), (lengths, "lengths"), (refs, "refs")):
+        if t.dtype != torch.int32 or t.device != dev:
+            raise ValueError(f"{what} must be int32 on the cache's device")
+    if lengths.shape != table.shape[:-1] or not lengths.is_contiguous() or refs.dim() != 1 or not refs.is_contiguous():
+        raise ValueError("lengths must be contiguous with one entry per table row, refs contiguous [pages]")
+    if not table.is_contiguous():
+        if table.dim() != 2 or table.stride(1) != 1 or table.stride(0) < table.shape[1]:
+            raise ValueError("table must be contiguous, or [sequences, max_pages] with rows apart from one another")
+        stride = table.stride(0)
+    else:
+        stride = table.shape[-1]
+    if len(c.keys) < 1 or len(c.values) != len(c.keys):
+        raise ValueError("the cache needs at least one layer, keys and values of each")
+    pool = c.keys[0]
+    if pool.dim() != 4 or pool.shape[0] != refs.shape[0] or pool.shape[1] < 1:
+        raise ValueError("the pools must be [pages, page_size, Hkv, D], one page for each entry of refs")
+    sequences = lengths.numel()
+    if max(sequences, pool.shape[0], pool.shape[1], table.shape[-1]) >= 2**31:
+        raise ValueError("sizes must be below 2^31")
+    words = (ctypes.c_int64 * 8)(table.data_ptr(), stride, table.shape[-1], lengths.data_ptr(), refs.data_ptr(),
+                                 pool.shape[0], pool.shape[1], sequences)
+    return words, sequences, dev
+
+
+@functools.lru_cache(maxsize=256)
+def _append_bytes(sequences: int, n: int, pages: int, page: int) -> int:
+    return int(_lib.load().sv_cache_append_workspace_size(sequences, n, pages, page))
+
+
+def cache_append(cache: PagedCache, keys: Union[torch.Tensor, Sequence[torch.Tensor]],
+                 values: Union[torch.Tensor, Sequence[torch.Tensor]], counts: Optional[torch.Tensor] = None,
+                 path: Optional[torch.Tensor] = None, cu_nodes: Optional[torch.Tensor] = None,
+                 n: Optional[int] = None) -> torch.Tensor:
+    """Appends tokens to every sequence of a paged cache, in place
+    (include/sv_cache.h): ``keys[layer]``, ``values[layer]`` hold the rows
+    ``[total, Hkv, D]`` (or ``[sequences, n, Hkv, D]``) of the new tokens, as
+    ``tree_attention`` took them; the first ``counts`` of ``path`` (``path
+    [sequences, n]`` and ``n_accepted + 1`` of a verification) go behind the
+    sequence; without ``path`` its first ``counts`` rows, without ``counts`` all.
+    New pages are the lowest free ones, in sequence order; a shared last page is
+    copied first.  ``lengths`` grow by ``counts``.  Returns the per-sequence
+    status: SEQ_NO_PAGES where pages or table entries do not suffice,
+    SEQ_BAD_LAYOUT; such a sequence is left as it is."""
+    if isinstance(keys, torch.Tensor):
+        keys = [keys]
+    if isinstance(values, torch.Tensor):
+        values = [values]
+    pages, S, dev = _pages_arg(cache)
+    layers = len(cache.keys)
+    if len(keys) != layers or len(values) != layers:
+        raise ValueError(f"keys and values must hold rows for each of the {layers} layers")
+    pool = cache.keys[0]
+    P, page, H, D = pool.shape
+    strides, dtype = pool.stride(), pool.dtype
+    if strides[3] != 1 and D > 1:
+        raise ValueError("the pools must have unit stride along the head dimension")
+    first = keys[0]
+    if first.dim() == 4 and cu_nodes is None:
+        if n is None:
+            n = first.shape[1]
+        total = first.shape[0] * first.shape[1]
+    else:
+        total = first.shape[0]
+    if n is None and path is not None:
+        n = path.shape[-1]
+    _, n = _tree_layout(total, S, cu_nodes, n, "keys")
+    grad = torch.is_grad_enabled()
+    pools, rows, keep, seen, layout = [], [], [], set(), None
+    for t, x in ((a, b) for both in ((cache.keys, keys), (cache.values, values)) for a, b in zip(*both)):
+        if t.shape != pool.shape or t.stride() != strides or t.dtype != dtype or t.device != dev:
+            raise ValueError("the pools must be alike: shape, strides, type, device")
+        if x.dim() == 4 and cu_nodes is None:
+            x = x.flatten(0, 1)
+        if x.shape != (total, H, D) or x.dtype != dtype or x.device != dev:
+            raise ValueError(f"new rows must be [{total}, {H}, {D}] of the pools' type, on their device")
+        if grad and (t.requires_grad or x.requires_grad):
+            raise ValueError("the cache is modified in place: no gradients")
+        s = x.stride()
+        if layout is None and (s[2] == 1 or D <= 1):
+            layout = s
+        if s != layout:
+            x = x.contiguous()
+            if layout is None:
+                layout = x.stride()
+            elif x.stride() != layout:  # the first rows' strides serve all
+                y = torch.empty_strided((total, H, D), layout, dtype=dtype, device=dev)
+                x = y.copy_(x)
+            keep.append(x)
+        p = t.data_ptr()
+        if p in seen:
+            raise ValueError("a pool is listed twice")
+        seen.add(p)
+        pools.append(p)
+        rows.append(x.data_ptr())
+    if any(r in seen for r in rows if r):
+        raise ValueError("new rows are a pool too: they would change while they are read")
+    counts, path, cu = _words(counts, dev, "counts"), _words(path, dev, "path"), _words(cu_nodes, dev, "cu_nodes")
+    if counts is not None and counts.numel() != S:
+        raise ValueError("counts must have one entry per sequence")
+    if path is not None and path.numel() != S * n:
+        raise ValueError(f"path must be [{S}, {n}]")
+    if max(total, n) >= 2**31:
+        raise ValueError("sizes must be below 2^31")
+    e = pool.element_size()
+    status = torch.empty(cache.lengths.shape, dtype=torch.int32, device=dev)
+    need = _append_bytes(S, n, P, page)
+    workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    where = (ctypes.c_int64 * 7)(strides[0] * e, strides[1] * e, strides[2] * e, layout[0] * e, layout[1] * e, H, D * e)
+    _launch(dev, _lib.load().sv_cache_append, pages, where, (ctypes.c_int64 * len(pools))(*pools),
+            (ctypes.c_int64 * len(rows))(*rows), len(pools), _p(counts), _p(path), _p(cu), n, total, status.data_ptr(),
+            workspace.data_ptr(), need)
+    return status
+
+
+def cache_truncate(cache: PagedCache, lengths: torch.Tensor) -> torch.Tensor:
+    """Takes every sequence of a paged cache back to ``lengths`` tokens, in
+    place (include/sv_cache.h): the pages past them are given up; 0 frees the
+    sequence.  Returns the per-sequence status: SEQ_BAD_LAYOUT for a length
+    below 0 or above the sequence's (it is left as it is)."""
+    pages, S, dev = _pages_arg(cache)
+    if lengths.numel() != S:
+        raise ValueError("lengths must have one entry per sequence")
+    to = _words(lengths, dev, "lengths")
+    status = torch.empty(cache.lengths.shape, dtype=torch.int32, device=dev)
+    _launch(dev, _lib.load().sv_cache_truncate, pages, to.data_ptr(), status.data_ptr())
+    return status
+
+
+def cache_fork(cache: PagedCache, parents: torch.Tensor) -> torch.Tensor:
+    """Lets sequences share others' pages, in place (include/sv_cache.h): slot
+    ``w`` of group ``g`` takes what slot ``parents[g, w]`` of the group held
+    before the call (its pages, shared, and its length) and gives up its own; a
+    negative parent, or ``w``, leaves it as it is.  ``parents [groups, width]``,
+    or ``[sequences]`` for one group of all; at most 1024 slots per group.
+    Nothing is copied until a shared last page is appended to.  Returns the
+    status per group (int32 ``[groups]``)."""
+    pages, S, dev = _pages_arg(cache)
+    if parents.dim() not in (1, 2) or parents.numel() != S:
+        raise ValueError("parents must be [groups, width] or [sequences], one entry per sequence")
+    width = parents.shape[-1]
+    par = _words(parents, dev, "parents")
+    if par.data_ptr() == cache.lengths.data_ptr() and S:
+        raise ValueError("parents is the cache's lengths: it would change while it is read")
+    status = torch.empty(S // width if width else 0, dtype=torch.int32, device=dev)
+    if S:
+        _launch(dev, _lib.load().sv_cache_fork, pages, par.data_ptr(), width, status.data_ptr())
+    return status
