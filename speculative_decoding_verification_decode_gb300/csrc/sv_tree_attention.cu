@@ -1,9 +1,49 @@
 // Attention of a tree of drafted tokens over a paged cache
 // (include/sv_tree.h).
 //
-// A warp takes a node and a query head and walks the keys that the node sees,
-// with the running maximum and sum of a softmax.
+// One key head's queries of a sequence (its nodes times the query heads that
+// share the key head) are rows of tiles of 128; a key tile is 128 tokens of the
+// cache, or 128 of the nodes.  S = Q K^T and O += P V run on the tensor cores
+// (tcgen05, f32 accumulators in tensor memory); a softmax thread owns a row, so
+// its maximum and sum need no exchange.  Few rows leave the MMA's other rows
+// idle, which costs nothing while the cache's bytes bound the call.
+//
+// A CTA, one per SM, has
+//   warps 0-3, 4-7  two softmax streams, each with a score tile and an output
+//                   tile in tensor memory (4 x 128 columns, all there are);
+//   warp 8          producer: TMA loads, one box per page (or part of a page)
+//                   and 64 elements, 128-byte swizzle, into a ring of slots that
+//                   keys and values share;
+//   warp 9          issues the MMAs (two more warps make its warpgroup full, so
+//                   that the softmax warps can have its registers).
+// A step is one query tile against one key tile, step g on stream g % 2.  With
+// one query tile to an item the streams take its key tiles in turn and their
+// results are joined at the end; with two, each takes one, and a key tile is
+// loaded once for both.  The MMA warp issues QK(g + 2) right behind PV(g), into
+// the score tile that PV(g) has just read the weights from (they lie over the
+// scores), so that the tensor cores work on one stream while the other's warps
+// take exponentials.
+//
+// The weights are taken against a reference that follows the row's maximum: it
+// moves when the maximum passes it by 8 (in powers of two), and only then the
+// output is rescaled, which keeps that off the ordinary step; weights up to 2^8
+// lose nothing in either type.
+//
+// The key tiles of all items, sequence after sequence, are cut into one equal
+// piece per CTA, so ragged lengths balance and one long context uses every SM.
+// An item that a cut divides leaves its parts (f32 outputs, maximum, sum) in the
+// workspace, at most two per CTA, and a second kernel joins them in order: the
+// result depends on the inputs and the number of CTAs only.  That kernel also
+// looks the sequences' layouts over while the first still runs.
+//
+// What a node must not see may hold anything: scores are masked by selection,
+// the values past a length are set to 0 before the MMA, and a drafted value that
+// is no finite number is replaced by 0 and added to the rows that see it at
+// the end (it is inf or NaN times a positive weight, so the weight's size does
+// not matter).
+#include <cuda.h>
 #include <cuda_runtime.h>
+#include <cudaTypedefs.h>
 
 #include <cstdint>
 
@@ -13,85 +53,1074 @@
 
 namespace sva {
 
-constexpr int kWarps = 4;
+using svk::mbar_arrive_expect_tx;
+using svk::mbar_arrive_local;
+using svk::mbar_init;
+using svk::smem_u32;
 
-__device__ __forceinline__ float value(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ float value(__half x) { return __half2float(x); }
-template <typename T>
-__device__ __forceinline__ T rounded(float x);
-template <>
-__device__ __forceinline__ __nv_bfloat16 rounded(float x) {
-  return __float2bfloat16_rn(x);
-}
-template <>
-__device__ __forceinline__ __half rounded(float x) {
-  return __float2half_rn(x);
+constexpr int kThreads = 384, kSoftWarps = 8;
+// Registers a thread: 384 of 168 are 64512 at launch; 256 of 200 and 128 of 96 are 63488.
+constexpr int kSoftRegs = 200, kOtherRegs = 96;
+constexpr int kTile = 128;     // rows of a query tile, keys of a key tile
+constexpr int kMaxCtas = 152;  // one per SM
+constexpr int kFinishThreads = 256;
+constexpr int kFinishRows = 32;  // rows that a CTA of the second kernel joins
+constexpr float kSlack = 8.0f;   // how far the maximum may pass the reference, powers of two
+
+__host__ __device__ constexpr int tile_bytes(int dp) { return kTile * dp * 2; }
+// Slots of the ring: two query tiles and these fill the shared memory.
+__host__ __device__ constexpr int slots_of(int dp) { return dp == 128 ? 5 : 10; }
+
+struct Args {
+  int G, per_tile;  // query heads per key head; nodes per query tile
+  int Hkv, D, page, box, tree_box;  // keys per box, of the cache and of the nodes
+  int batch, n, total, pages;
+  long long max_pages, table_stride;
+  const int* table;
+  const int* lengths;
+  const int* parents;
+  const int* cu;
+  const void* v;
+  long long v_row, v_head;
+  void* out;
+  long long out_row, out_head;
+  float* lse;
+  int q_heads;
+  float c;          // scale in powers of two, not negative
+  bool flip;        // the scores' sign is turned (a negative scale)
+  float* part;      // [2 CTAs][256][dp]
+  float2* part_ml;  // [2 CTAs][256]: maximum (powers of two), sum
+  unsigned* err;    // [CTAs]
+  unsigned* status;
+};
+
+// ------------------------------------------------------------------ the plan
+
+struct Sequence {
+  int first, N, len;
+  int cached, tiles, items;  // key tiles of the cache, all key tiles of an item, items (pairs of query tiles) per key head
+};
+
+// Sequence b; N = 0 where it has nothing to do or its offsets or length are bad.
+__device__ __forceinline__ Sequence sequence(const Args& A, int b) {
+  Sequence s;
+  s.first = b * A.n;
+  s.N = A.n;
+  if (A.cu) {
+    s.first = A.cu[b];
+    const int end = A.cu[b + 1];
+    s.N = s.first >= 0 && end >= s.first && end <= A.total && end - s.first <= A.n ? end - s.first : 0;
+  }
+  s.len = A.lengths[b];
+  if (s.len < 0 || s.len > A.max_pages * A.page) s.N = 0;
+  s.cached = (s.len + kTile - 1) / kTile;
+  s.tiles = s.cached + (s.N + kTile - 1) / kTile;
+  s.items = (s.N + 2 * A.per_tile - 1) / (2 * A.per_tile);
+  return s;
 }
 
+__device__ __forceinline__ long long units_of(const Args& A, const Sequence& s) {
+  return s.N > 0 ? static_cast<long long>(s.tiles) * s.items * A.Hkv : 0;
+}
+
+// CTA c of C takes units [begin(c), begin(c + 1)) of W.
+__device__ __forceinline__ long long begin_of(long long W, int C, int c) { return W * c / C; }
+// The CTA that has unit u.
+__device__ __forceinline__ int owner_of(long long W, int C, long long u) { return static_cast<int>(((u + 1) * C - 1) / W); }
+
+struct PlanMem {
+  long long warp_sums[kThreads / 32];
+  long long W, off;
+  int b;
+};
+
+// All of a CTA's threads: the number of units, and the sequence that unit
+// begin_of(c) lies in, with the units before it there.  `T` threads.
+template <int T>
+__device__ __forceinline__ void make_plan(const Args& A, int C, int c, PlanMem& m) {
+  const int t = static_cast<int>(threadIdx.x), lane = t & 31, warp = t >> 5;
+  const int per = (A.batch + T - 1) / T;
+  const int lo = t * per < A.batch ? t * per : A.batch, hi = lo + per < A.batch ? lo + per : A.batch;
+  long long mine = 0;
+  for (int b = lo; b < hi; ++b) mine += units_of(A, sequence(A, b));
+  long long x = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const long long y = __shfl_up_sync(0xFFFFFFFFu, x, d);
+    if (lane >= d) x += y;
+  }
+  if (lane == 31) m.warp_sums[warp] = x;
+  if (t == 0) m.b = A.batch;
+  __syncthreads();
+  long long before = x - mine, W = 0;
+  for (int w = 0; w < T / 32; ++w) {
+    if (w < warp) before += m.warp_sums[w];
+    W += m.warp_sums[w];
+  }
+  const long long u = begin_of(W, C, c);
+  if (t == 0) m.W = W;
+  if (u >= before && u < before + mine)
+    for (int b = lo; b < hi; ++b) {
+      const long long k = units_of(A, sequence(A, b));
+      if (u < before + k) {
+        m.b = b;
+        m.off = u - before;
+        break;
+      }
+      before += k;
+    }
+  __syncthreads();
+}
+
+// A run of key tiles of one item, on this CTA.
+struct Segment {
+  Sequence q;
+  int b, head, pair;  // item: key head, pair of query tiles
+  int t0, t1;         // key tiles
+  bool two;           // both query tiles of the pair exist
+  bool whole;         // all key tiles of the item
+  int steps;
+};
+
+struct Walk {
+  int b;
+  long long off, left;
+  int count;  // segments so far
+
+  __device__ __forceinline__ bool next(const Args& A, Segment& s) {
+    if (left <= 0) return false;
+    for (;; ++b, off = 0) {
+      if (b >= A.batch) return false;
+      s.q = sequence(A, b);
+      if (off < units_of(A, s.q)) break;
+    }
+    const int item = static_cast<int>(off / s.q.tiles);
+    s.b = b;
+    s.t0 = static_cast<int>(off - static_cast<long long>(item) * s.q.tiles);
+    s.t1 = s.q.tiles - s.t0 < left ? s.q.tiles : s.t0 + static_cast<int>(left);
+    s.head = item / s.q.items;
+    s.pair = item % s.q.items;
+    s.two = s.q.N > (2 * s.pair + 1) * A.per_tile;
+    s.whole = s.t0 == 0 && s.t1 == s.q.tiles;
+    s.steps = (s.t1 - s.t0) * (s.two ? 2 : 1);
+    off += s.t1 - s.t0;
+    left -= s.t1 - s.t0;
+    ++count;
+    return true;
+  }
+};
+
+// Steps of a CTA one after another.
+struct Steps {
+  Walk w;
+  Segment s;
+  int k;   // step of the segment
+  bool ok;
+
+  __device__ __forceinline__ void start(const Args& A, const PlanMem& m, int C, int c) {
+    w.b = m.b;
+    w.off = m.off;
+    w.left = begin_of(m.W, C, c + 1) - begin_of(m.W, C, c);
+    w.count = 0;
+    k = 0;
+    ok = w.next(A, s);
+  }
+  __device__ __forceinline__ void advance(const Args& A) {
+    if (++k == s.steps) {
+      k = 0;
+      ok = w.next(A, s);
+    }
+  }
+  __device__ __forceinline__ int tile() const { return s.t0 + (s.two ? k >> 1 : k); }
+  __device__ __forceinline__ bool fresh() const { return !s.two || !(k & 1); }  // the first step with its key tile
+  __device__ __forceinline__ bool last() const { return !s.two || (k & 1); }    // and the last
+};
+
+// Keys of tile t that exist.
+__device__ __forceinline__ int keys_of(const Segment& s, int t) {
+  const int left = t < s.q.cached ? s.q.len - t * kTile : s.q.N - (t - s.q.cached) * kTile;
+  return left < kTile ? left : kTile;
+}
+
+// ------------------------------------------------------------------ instructions
+
 template <typename T>
-__global__ void __launch_bounds__(32 * kWarps) simple_kernel(const __grid_constant__ sv_tree_attn A, float scale) {
-  const int lane = threadIdx.x & 31;
-  const long long id = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  const int h = static_cast<int>(id % A.q_heads), i = static_cast<int>(id / A.q_heads % A.n);
-  const int b = static_cast<int>(id / A.q_heads / A.n);
-  if (b >= A.batch) return;
-  long long first = b * A.n, N = A.total ? A.n : 0;
-  if (A.cu_nodes) {
-    first = A.cu_nodes[b];
-    const long long end = A.cu_nodes[b + 1];
-    N = end - first;
-    if (first < 0 || end < first || end > A.total || N > A.n) {
-      if (lane == 0 && i == 0 && h == 0) A.status[b] = SV_SEQ_BAD_LAYOUT;
+struct Num;
+template <>
+struct Num<__nv_bfloat16> {
+  static constexpr uint32_t kType = 1, kExp = 0x7F80;
+  static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+  }
+  static __device__ __forceinline__ float value(uint16_t x) { return __uint_as_float(static_cast<uint32_t>(x) << 16); }
+};
+template <>
+struct Num<__half> {
+  static constexpr uint32_t kType = 0, kExp = 0x7C00;
+  static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+  }
+  static __device__ __forceinline__ float value(uint16_t x) { return __half2float(__ushort_as_half(x)); }
+};
+
+// Descriptors of tiles with 128-byte swizzle, panels of 64 elements (128-byte
+// rows): low word the address in 16-byte units and the leading stride, high
+// word the stride of 8 rows (1024 bytes), version 1 and the swizzle.  Query and
+// key tiles are K-major; value tiles are N-major, their leading stride is that
+// of the panels.
+__device__ __forceinline__ uint64_t desc(uint32_t saddr, uint32_t leading) {
+  return static_cast<uint64_t>((1024u >> 4) | 1u << 14 | 2u << 29) << 32 | ((saddr & 0x3FFFFu) >> 4) | leading << 16;
+}
+// Instruction descriptor: D f32, A and B of the type, M = 128, N; B N-major.
+template <typename T>
+__host__ __device__ constexpr uint32_t idesc(int N, bool n_major) {
+  return (1u << 4) | (Num<T>::kType << 7) | (Num<T>::kType << 10) | (n_major ? 1u << 16 : 0u) |
+         ((static_cast<uint32_t>(N) >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+      "r"(a), "l"(b), "r"(id), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+__device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+
+#define SVA_R8(v, i) "=r"(v[i]), "=r"(v[i + 1]), "=r"(v[i + 2]), "=r"(v[i + 3]), "=r"(v[i + 4]), "=r"(v[i + 5]), "=r"(v[i + 6]), "=r"(v[i + 7])
+#define SVA_W8(v, i) "r"(v[i]), "r"(v[i + 1]), "r"(v[i + 2]), "r"(v[i + 3]), "r"(v[i + 4]), "r"(v[i + 5]), "r"(v[i + 6]), "r"(v[i + 7])
+
+// 32 consecutive columns of this thread's lane, waited for.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, "
+      "%13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : SVA_R8(v, 0), SVA_R8(v, 8), SVA_R8(v, 16), SVA_R8(v, 24)
+      : "r"(taddr)
+      : "memory");
+}
+// 64 of them.
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, "
+      "%13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
+      "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, "
+      "%52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : SVA_R8(v, 0), SVA_R8(v, 8), SVA_R8(v, 16), SVA_R8(v, 24), SVA_R8(v, 32), SVA_R8(v, 40), SVA_R8(v, 48), SVA_R8(v, 56)
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, "
+      "%13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::SVA_W8(v, 0),
+      SVA_W8(v, 8), SVA_W8(v, 16), SVA_W8(v, 24), "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// (x0, x1) = (x0, x1) * (c, c) + (a, a)
+__device__ __forceinline__ void fma2(float& x0, float& x1, float c, float a) {
+  asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%0, %1};\n mov.b64 y, {%2, %2};\n mov.b64 z, {%3, %3};\n"
+      " fma.rn.f32x2 x, x, y, z;\n mov.b64 {%0, %1}, x;\n}"
+      : "+f"(x0), "+f"(x1)
+      : "f"(c), "f"(a));
+}
+__device__ __forceinline__ void add2(float& a0, float& a1, float x0, float x1) {
+  asm("{\n .reg .b64 x, y;\n mov.b64 x, {%0, %1};\n mov.b64 y, {%2, %3};\n add.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}"
+      : "+f"(a0), "+f"(a1)
+      : "f"(x0), "f"(x1));
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// ------------------------------------------------------------------ the kernel
+
+struct __align__(8) Shared {
+  uint64_t full[10], empty[10];      // ring: producer -> MMA, MMA -> producer
+  uint64_t q_full[2], q_empty[2];    // query tiles
+  uint64_t s_full[2];                // MMA -> softmax: the stream's scores
+  uint64_t p_full[2];                // softmax -> MMA: its weights
+  uint64_t o_full, o_empty;          // MMA -> softmax: a segment's outputs; softmax -> MMA: read
+  uint64_t done;                     // every MMA has completed
+  uint32_t tmem;
+  volatile int abort;
+  PlanMem plan;
+  uint32_t odd[8];                   // nodes of the segment with values that are no finite numbers
+  float2 ex[2][kTile];               // [stream]: maximum, sum of each row
+};
+
+__device__ __forceinline__ bool wait(Shared& sm, uint64_t* bar, uint32_t parity) {
+  for (uint32_t i = 0; i < svk::kWaitPolls; ++i) {
+    if (svk::mbar_try_wait(bar, parity)) return true;
+    if (sm.abort) return false;
+  }
+  sm.abort = 1;
+  return false;
+}
+__device__ __forceinline__ bool warp_wait(Shared& sm, uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xFFFFFFFFu, wait(sm, bar, parity));
+}
+__device__ __forceinline__ void bar_soft() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kSoftWarps) : "memory"); }
+
+template <int DP>
+__host__ __device__ constexpr int smem_bytes() {
+  return (2 + slots_of(DP)) * tile_bytes(DP) + static_cast<int>(sizeof(Shared));
+}
+
+static_assert(smem_bytes<128>() <= 232448 && smem_bytes<64>() <= 232448, "a CTA's shared memory");
+
+template <typename T, int DP>
+__device__ __forceinline__ void produce(const Args& A, Shared& sm, uint32_t q_smem, uint32_t ring, int C, int c,
+                                        const CUtensorMap* qm, const CUtensorMap* km, const CUtensorMap* vm,
+                                        const CUtensorMap* kcm, const CUtensorMap* vcm) {
+  constexpr int kPanels = DP / 64, kSlots = slots_of(DP);
+  const int lane = static_cast<int>(threadIdx.x & 31);
+  Steps qk, pv;
+  qk.start(A, sm.plan, C, c);
+  pv.start(A, sm.plan, C, c);
+  uint32_t slot = 0, turn = 0, qs = 0;
+  bool alive = true;
+  // a key or value tile into the next slot: every lane its boxes
+  auto load = [&](const Segment& s, int t, const CUtensorMap* cache, const CUtensorMap* own) {
+    if (turn && !warp_wait(sm, &sm.empty[slot], (turn - 1) & 1)) {
+      alive = false;
       return;
     }
-  }
-  const int len = A.lengths[b], page = static_cast<int>(A.page_size);
-  bool ok = len >= 0 && len <= A.max_pages * A.page_size;
-  if (ok)
-    for (int j = lane; j < (len + page - 1) / page; j += 32) {
-      const int p = A.table[b * A.table_stride + j];
-      ok = ok && p >= 0 && p < A.pages;
+    const uint32_t dst = ring + slot * tile_bytes(DP);
+    uint64_t* bar = &sm.full[slot];
+    const int keys = keys_of(s, t);
+    if (t < s.q.cached) {
+      const int boxes = (keys + A.box - 1) / A.box;
+      if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(boxes * A.box * 128 * kPanels));
+      __syncwarp();
+      for (int i = lane; i < boxes * kPanels; i += 32) {
+        const int x = kPanels == 2 ? i & 1 : 0, k = kPanels == 2 ? i >> 1 : i;
+        const int at = t * kTile + k * A.box, p = at / A.page;
+        const int id = A.table[s.b * A.table_stride + p];
+        tma_4d(dst + x * (kTile * 128) + k * A.box * 128, cache, x * 64, at - p * A.page, s.head, id, bar);
+      }
+    } else {
+      if (lane == 0) {
+        mbar_arrive_expect_tx(bar, static_cast<uint32_t>(A.tree_box * 128 * kPanels));
+        for (int x = 0; x < kPanels; ++x)
+          tma_3d(dst + x * (kTile * 128), own, x * 64, s.q.first + (t - s.q.cached) * kTile, s.head, bar);
+      }
     }
-  if (A.parents)
-    for (int j = lane; j < N; j += 32) ok = ok && A.parents[first + j] >= -1 && A.parents[first + j] < j;
-  ok = __all_sync(0xFFFFFFFFu, ok);
-  if (lane == 0 && i == 0 && h == 0) A.status[b] = ok ? 0u : SV_SEQ_BAD_LAYOUT;
-  if (i >= N) return;
-  const int D = static_cast<int>(A.dim), kh = h / static_cast<int>(A.q_heads / A.kv_heads);
-  T* out = static_cast<T*>(A.out) + (first + i) * A.out_row + h * A.out_head;
-  float* lse = A.lse ? A.lse + (first + i) * A.q_heads + h : nullptr;
-  if (!ok) {
-    for (int d = lane; d < D; d += 32) out[d] = rounded<T>(0.0f);
-    if (lse && lane == 0) *lse = -INFINITY;
+    __syncwarp();
+    if (++slot == kSlots) slot = 0, ++turn;
+  };
+  auto scores = [&]() {  // what QK of the next step needs
+    if (!qk.ok || !alive) return;
+    if (qk.k < (qk.s.two ? 2 : 1)) {
+      const uint32_t buf = qs & 1;
+      if (qs >= 2 && !warp_wait(sm, &sm.q_empty[buf], ((qs >> 1) - 1) & 1)) {
+        alive = false;
+        return;
+      }
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&sm.q_full[buf], static_cast<uint32_t>(A.per_tile * A.G * 128 * kPanels));
+        for (int x = 0; x < kPanels; ++x)
+          tma_3d(q_smem + buf * tile_bytes(DP) + x * (kTile * 128), qm, x * 64, qk.s.head * A.G,
+                 qk.s.q.first + (2 * qk.s.pair + qk.k) * A.per_tile, &sm.q_full[buf]);
+      }
+      __syncwarp();
+      ++qs;
+    }
+    if (qk.fresh()) load(qk.s, qk.tile(), kcm, km);
+    qk.advance(A);
+  };
+  scores();
+  scores();
+  while (pv.ok && alive) {
+    if (pv.fresh()) load(pv.s, pv.tile(), vcm, vm);
+    if (!alive) break;
+    pv.advance(A);
+    scores();
+  }
+  // no copy may still be writing shared memory at exit
+  const uint32_t loads = turn * kSlots + slot;
+  for (uint32_t i = loads > kSlots ? loads - kSlots : 0; i < loads; ++i) svk::mbar_wait_bounded(&sm.full[i % kSlots], (i / kSlots) & 1);
+  for (uint32_t i = qs > 2 ? qs - 2 : 0; i < qs; ++i) svk::mbar_wait_bounded(&sm.q_full[i & 1], (i >> 1) & 1);
+}
+
+template <typename T, int DP>
+__device__ __forceinline__ void issue(const Args& A, Shared& sm, unsigned char* ring_ptr, uint32_t q_smem, uint32_t ring,
+                                      uint32_t tmem, int C, int c) {
+  constexpr int kPanels = DP / 64, kSlots = slots_of(DP);
+  const int lane = static_cast<int>(threadIdx.x & 31);
+  Steps qk, pv;
+  qk.start(A, sm.plan, C, c);
+  pv.start(A, sm.plan, C, c);
+  uint32_t slot = 0, turn = 0, qs = 0, gq = 0, gp = 0;
+  uint32_t k_slot = 0, v_slot = 0, q_first = 0;  // of the steps at hand; the segment's first query tile
+  uint32_t segments = 0;
+  bool alive = true;
+  auto take = [&](uint32_t& mine) {  // the next slot of the ring, landed
+    if (!warp_wait(sm, &sm.full[slot], turn & 1)) {
+      alive = false;
+      return;
+    }
+    mine = slot;
+    if (++slot == kSlots) slot = 0, ++turn;
+  };
+  auto scores = [&]() {
+    if (!qk.ok || !alive) return;
+    const int queries = qk.s.two ? 2 : 1;
+    if (qk.k == 0) q_first = qs;
+    if (qk.k < queries) {
+      if (!warp_wait(sm, &sm.q_full[qs & 1], (qs >> 1) & 1)) {
+        alive = false;
+        return;
+      }
+      ++qs;
+    }
+    if (qk.fresh()) take(k_slot);
+    if (!alive) return;
+    fence_after();
+    if (lane == 0) {
+      const uint32_t q = (q_first + (qk.s.two ? qk.k & 1 : 0)) & 1;
+      const uint32_t a = q_smem + q * tile_bytes(DP), b = ring + k_slot * tile_bytes(DP);
+#pragma unroll
+      for (int i = 0; i < DP / 16; ++i) {
+        const uint32_t at = (i / 4) * (kTile * 128) + (i % 4) * 32;
+        mma_ss(tmem + (gq & 1) * kTile, desc(a + at, 1), desc(b + at, 1), idesc<T>(kTile, false), i > 0);
+      }
+      if (qk.last()) mma_commit(&sm.empty[k_slot]);
+      if (qk.k >= qk.s.steps - queries) mma_commit(&sm.q_empty[q]);
+      mma_commit(&sm.s_full[gq & 1]);
+    }
+    __syncwarp();
+    ++gq;
+    qk.advance(A);
+  };
+  scores();
+  scores();
+  while (pv.ok && alive) {
+    const uint32_t st = gp & 1;
+    if (pv.k == 0) {  // the outputs of the segment before have been read
+      if (segments && !warp_wait(sm, &sm.o_empty, (segments - 1) & 1)) break;
+      if (lane < 8) sm.odd[lane] = 0;
+      ++segments;
+      __syncwarp();
+    }
+    const int t = pv.tile(), keys = keys_of(pv.s, t);
+    if (pv.fresh()) {
+      take(v_slot);
+      if (!alive) break;
+      unsigned char* v = ring_ptr + v_slot * tile_bytes(DP);
+      bool wrote = false;
+      if (t >= pv.s.q.cached) {  // drafted values that are no finite numbers
+        constexpr uint32_t kE = Num<T>::kExp;
+        for (int i = lane; i < keys * 8 * kPanels; i += 32) {
+          const int r = i / (8 * kPanels), x = i % (8 * kPanels);
+          uint4* p = reinterpret_cast<uint4*>(v + (x / 8) * (kTile * 128) + r * 128 + (x % 8) * 16);
+          uint4 u = *p;
+          uint32_t* w = reinterpret_cast<uint32_t*>(&u);
+          bool odd = false;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if ((w[j] & kE) == kE) w[j] &= 0xFFFF0000u, odd = true;
+            if ((w[j] >> 16 & kE) == kE) w[j] &= 0xFFFFu, odd = true;
+          }
+          if (odd) {
+            *p = u;
+            const int node = (t - pv.s.q.cached) * kTile + r;
+            atomicOr(&sm.odd[node / 32], 1u << (node % 32));
+            wrote = true;
+          }
+        }
+      }
+      for (int i = keys * 8 * kPanels + lane; i < (keys + 15) / 16 * 16 * 8 * kPanels; i += 32) {  // past the last key
+        const int r = i / (8 * kPanels), x = i % (8 * kPanels);
+        *reinterpret_cast<uint4*>(v + (x / 8) * (kTile * 128) + r * 128 + (x % 8) * 16) = make_uint4(0, 0, 0, 0);
+        wrote = true;
+      }
+      if (__any_sync(0xFFFFFFFFu, wrote)) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+    }
+    if (!warp_wait(sm, &sm.p_full[st], (gp >> 1) & 1)) break;
+    fence_after();
+    if (lane == 0) {
+      const uint32_t b = ring + v_slot * tile_bytes(DP);
+      const int n16 = (keys + 15) / 16;
+      for (int i = 0; i < n16; ++i)
+        mma_ts(tmem + 256 + st * 128, tmem + st * kTile + i * 8, desc(b + i * 2048, kTile * 128 / 16),
+               idesc<T>(DP, true), (i > 0 || pv.k >= 2) ? 1u : 0u);
+      if (pv.last()) mma_commit(&sm.empty[v_slot]);
+      if (pv.k == pv.s.steps - 1) mma_commit(&sm.o_full);
+    }
+    __syncwarp();
+    ++gp;
+    pv.advance(A);
+    scores();
+  }
+  if (lane == 0) mma_commit(&sm.done);
+  __syncwarp();
+  svk::mbar_wait_bounded(&sm.done, 0);
+}
+
+// Bits of the nodes of tree tile j that node i sees.
+__device__ __forceinline__ void seen_bits(const Args& A, int first, int i, int j, uint32_t (&w)[4]) {
+#pragma unroll
+  for (int x = 0; x < 4; ++x) w[x] = 0;
+  auto set = [&](int k) {
+    k -= j * kTile;
+    if (k >= 0 && k < kTile) {
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        if (k >> 5 == x) w[x] |= 1u << (k & 31);
+    }
+  };
+  if (!A.parents) {  // 0 .. i
+    const int k = i - j * kTile;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) w[x] = k >= 32 * x + 31 ? 0xFFFFFFFFu : k >= 32 * x ? (2u << (k & 31)) - 1u : 0u;
     return;
   }
-  float q[4] = {}, o[4] = {}, m = -INFINITY, z = 0;
-  for (int d = 0; d < 4; ++d)
-    if (lane + 32 * d < D) q[d] = value(static_cast<const T*>(A.q)[(first + i) * A.q_row + h * A.q_head + lane + 32 * d]);
-  auto step = [&](const T* k, const T* v) {
-    float s = 0;
-    for (int d = 0; d < 4; ++d)
-      if (lane + 32 * d < D) s += q[d] * value(k[lane + 32 * d]);
-    for (int x = 16; x; x /= 2) s += __shfl_xor_sync(0xFFFFFFFFu, s, x);
-    s *= scale;
-    const float was = m;
-    m = fmaxf(m, s);
-    const float keep = was == m ? 1.0f : expf(was - m), p = expf(s - m);
-    z = z * keep + p;
-    for (int d = 0; d < 4; ++d)
-      if (lane + 32 * d < D) o[d] = o[d] * keep + p * value(v[lane + 32 * d]);
-  };
-  for (int t = 0; t < len; ++t) {
-    const long long p = A.table[b * A.table_stride + t / page], at = t % page;
-    step(static_cast<const T*>(A.k_cache) + p * A.kc_page + at * A.kc_token + kh * A.kc_head,
-         static_cast<const T*>(A.v_cache) + p * A.vc_page + at * A.vc_token + kh * A.vc_head);
+  set(i);
+  for (int p = A.parents[first + i], was = i; p >= 0 && p < was;) {
+    set(p);
+    was = p;
+    p = A.parents[first + p];
   }
-  for (int j = i; j >= 0; j = A.parents ? A.parents[first + j] : j - 1)
-    step(static_cast<const T*>(A.k) + (first + j) * A.k_row + kh * A.k_head,
-         static_cast<const T*>(A.v) + (first + j) * A.v_row + kh * A.v_head);
-  for (int d = 0; d < 4; ++d)
-    if (lane + 32 * d < D) out[lane + 32 * d] = rounded<T>(o[d] / z);
-  if (lse && lane == 0) *lse = m + logf(z);
+}
+
+template <typename T>
+__device__ __forceinline__ void store_out(T* dst, const float* o, float f) {
+  uint4 u;
+  u.x = Num<T>::pack(o[0] * f, o[1] * f);
+  u.y = Num<T>::pack(o[2] * f, o[3] * f);
+  u.z = Num<T>::pack(o[4] * f, o[5] * f);
+  u.w = Num<T>::pack(o[6] * f, o[7] * f);
+  *reinterpret_cast<uint4*>(dst) = u;
+}
+
+// A softmax warp.
+template <typename T, int DP>
+__device__ __forceinline__ void soften(const Args& A, Shared& sm, uint32_t tmem, int C, int c) {
+  const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
+  const int stream = warp >> 2, row = (warp & 3) * 32 + lane;
+  const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+  const uint32_t s_col = tmem + lanes + stream * kTile, o_col = tmem + lanes + 256;
+  Walk w;
+  w.b = sm.plan.b;
+  w.off = sm.plan.off;
+  w.left = begin_of(sm.plan.W, C, c + 1) - begin_of(sm.plan.W, C, c);
+  w.count = 0;
+  uint32_t g = 0;          // steps before the segment, both streams
+  uint32_t turns = 0;      // of this stream
+  bool alive = true;
+  Segment s;
+  while (w.next(A, s)) {
+    // this stream's steps of the segment: k = k0, k0 + 2, ...
+    const int k0 = static_cast<int>((stream ^ g) & 1);
+    const int query = 2 * s.pair + (s.two ? k0 : 0);
+    const int rows = (s.q.N - query * A.per_tile < A.per_tile ? s.q.N - query * A.per_tile : A.per_tile) * A.G;
+    const bool busy = (warp & 3) * 32 < rows;  // the warp has a row
+    const int node = query * A.per_tile + row / A.G;
+    float ref = -INFINITY, sum = 0;
+    for (int k = k0; k < s.steps; k += 2) {
+      const int t = s.t0 + (s.two ? k >> 1 : k);
+      const int keys = keys_of(s, t);
+      const bool tree = t >= s.q.cached;
+      uint32_t bits[4] = {0, 0, 0, 0};
+      if (busy && tree && row < rows) seen_bits(A, s.q.first, node, t - s.q.cached, bits);
+      if (alive) alive = warp_wait(sm, &sm.s_full[stream], turns & 1);
+      ++turns;
+      fence_after();
+      if (busy && alive) {
+        uint32_t u[kTile];
+        tmem_ld64(s_col, u);
+        tmem_ld64(s_col + 64, u + 64);
+        float* x = reinterpret_cast<float*>(u);
+        if (A.flip) {
+#pragma unroll
+          for (int j = 0; j < kTile; ++j) x[j] = -x[j];
+        }
+        const bool masked = tree || keys < kTile;
+        if (masked) {
+          if (!tree) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int n = keys - 32 * i;
+              bits[i] = n >= 32 ? 0xFFFFFFFFu : n > 0 ? (1u << n) - 1u : 0u;
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < kTile; ++j)
+            if (!(bits[j / 32] >> (j % 32) & 1)) x[j] = -INFINITY;
+        }
+        float m0 = x[0], m1 = x[1], m2 = x[2], m3 = x[3];
+#pragma unroll
+        for (int j = 4; j < kTile; j += 8) {
+          m0 = max3(m0, x[j], x[j + 1]);
+          m1 = max3(m1, x[j + 2], x[j + 3]);
+          if (j + 4 < kTile) {
+            m2 = max3(m2, x[j + 4], x[j + 5]);
+            m3 = max3(m3, x[j + 6], x[j + 7]);
+          }
+        }
+        const float top = max3(fmaxf(m0, m1), m2, m3) * A.c;
+        const bool move = top > ref + kSlack || (ref == -INFINITY && top > -INFINITY);
+        if (__any_sync(0xFFFFFFFFu, move)) {
+          const float to = move ? top : ref;
+          const float f = ref == -INFINITY ? 0.0f : svk::ex2_ftz(ref - to);
+          ref = to;
+          sum *= f;
+          if (k >= 2) {
+#pragma unroll
+            for (int i = 0; i < DP / 32; ++i) {
+              uint32_t o[32];
+              tmem_ld32(o_col + stream * 128 + i * 32, o);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+              tmem_st32(o_col + stream * 128 + i * 32, o);
+            }
+          }
+        }
+        const float minus = ref == -INFINITY ? 0.0f : -ref;
+        float a0 = 0, a1 = 0, b0 = 0, b1 = 0;
+        uint32_t p[kTile / 2];
+#pragma unroll
+        for (int j = 0; j < kTile; j += 4) {
+          fma2(x[j], x[j + 1], A.c, minus);
+          fma2(x[j + 2], x[j + 3], A.c, minus);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[j + i] = svk::ex2_ftz(x[j + i]);
+          if (masked) {  // (-inf times a scale of 0 is no number)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (!(bits[(j + i) / 32] >> ((j + i) % 32) & 1)) x[j + i] = 0;
+          }
+          add2(a0, a1, x[j], x[j + 1]);
+          add2(b0, b1, x[j + 2], x[j + 3]);
+          p[j / 2] = Num<T>::pack(x[j], x[j + 1]);
+          p[j / 2 + 1] = Num<T>::pack(x[j + 2], x[j + 3]);
+        }
+        sum += (a0 + a1) + (b0 + b1);
+        tmem_st32(s_col, p);
+        tmem_st32(s_col + 32, p + 32);
+        tmem_st_wait();
+      }
+      fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_local(&sm.p_full[stream]);
+    }
+    // ---- the segment's end
+    // what this stream's output and the other's are multiplied by; the step that
+    // comes first is this stream's where k0 is 0
+    float keep = 1.0f, keep_other = 0.0f;
+    const bool have = s.two || k0 == 0 || s.steps > 1, have_other = !s.two && (k0 == 1 || s.steps > 1);
+    if (!s.two) {
+      sm.ex[stream][row] = make_float2(ref, sum);
+      bar_soft();
+      const float2 other = sm.ex[stream ^ 1][row];
+      bar_soft();
+      const float m = fmaxf(ref, other.x);
+      const float mine = ref == -INFINITY ? 0.0f : svk::ex2_ftz(ref - m);
+      const float theirs = other.x == -INFINITY ? 0.0f : svk::ex2_ftz(other.x - m);
+      sum = sum * mine + other.y * theirs;
+      ref = m;
+      keep = mine;
+      keep_other = theirs;
+    }
+    if (alive) alive = warp_wait(sm, &sm.o_full, (w.count - 1) & 1);
+    fence_after();
+    const int begin = s.two ? 0 : stream * (DP / 2), width = s.two ? DP : DP / 2;
+    const bool mine = alive && busy && row < rows;
+    const long long at = static_cast<long long>(s.q.first) + node;
+    const int qh = s.head * A.G + row % A.G;
+    const int slot = 2 * c + (w.count > 1 ? 1 : 0);
+    float* part = A.part + (static_cast<long long>(slot) * 256 + (s.two ? k0 * kTile : 0) + row) * DP;
+    const float inv = sum > 0 || sum != sum ? 1.0f / sum : 0.0f;
+    uint32_t odd_any = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) odd_any |= sm.odd[i];
+    if (busy && alive) {
+      for (int col = begin; col < begin + width; col += 32) {
+        float o[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) o[j] = 0;
+        if (have) {
+          uint32_t u[32];
+          tmem_ld32(o_col + stream * 128 + col, u);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) o[j] = __uint_as_float(u[j]) * keep;
+        }
+        if (have_other) {
+          uint32_t u[32];
+          tmem_ld32(o_col + (stream ^ 1) * 128 + col, u);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) o[j] = fmaf(__uint_as_float(u[j]), keep_other, o[j]);
+        }
+        if (odd_any && row < rows) {  // drafted values that are no finite numbers, of the nodes this one sees
+          for (int tt = 0; tt < 2; ++tt) {
+            if (s.q.cached + tt < s.t0 || s.q.cached + tt >= s.t1) continue;
+            uint32_t bits[4];
+            seen_bits(A, s.q.first, node, tt, bits);
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              for (uint32_t left = bits[x] & sm.odd[tt * 4 + x]; left; left &= left - 1) {
+                const int k = tt * kTile + x * 32 + __ffs(left) - 1;
+                const uint16_t* v = static_cast<const uint16_t*>(A.v) + (static_cast<long long>(s.q.first) + k) * A.v_row + s.head * A.v_head;
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                  if (col + j < A.D && (v[col + j] & Num<T>::kExp) == Num<T>::kExp) o[j] += Num<T>::value(v[col + j]);
+              }
+          }
+        }
+        if (mine && s.whole) {
+          T* dst = static_cast<T*>(A.out) + at * A.out_row + static_cast<long long>(qh) * A.out_head + col;
+#pragma unroll
+          for (int j = 0; j < 32; j += 8)
+            if (col + j < A.D) store_out<T>(dst + j, o + j, inv);
+        } else if (mine) {
+#pragma unroll
+          for (int j = 0; j < 32; j += 4)
+            *reinterpret_cast<float4*>(part + col + j) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+        }
+      }
+    }
+    if (mine && (s.two || stream == 0)) {
+      if (!s.whole)
+        A.part_ml[slot * 256 + (s.two ? k0 * kTile : 0) + row] = make_float2(ref, sum);
+      else if (A.lse)
+        A.lse[at * A.q_heads + qh] = (ref + log2f(sum)) * 0.69314718055994531f;
+    }
+    fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive_local(&sm.o_empty);
+    g += static_cast<uint32_t>(s.steps);
+  }
+}
+
+template <typename T, int DP>
+__global__ void __launch_bounds__(kThreads, 1)
+    attend_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtensorMap qm, const __grid_constant__ CUtensorMap km,
+                  const __grid_constant__ CUtensorMap vm, const __grid_constant__ CUtensorMap kcm,
+                  const __grid_constant__ CUtensorMap vcm) {
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* base = smem_raw;  // (the swizzle wants 1024 bytes, and there is no room to move up)
+  if (smem_u32(base) & 1023) {
+    if (threadIdx.x == 0) A.err[blockIdx.x] = 1u;
+    return;
+  }
+  unsigned char* ring_ptr = base + 2 * tile_bytes(DP);
+  Shared& sm = *reinterpret_cast<Shared*>(ring_ptr + slots_of(DP) * tile_bytes(DP));
+  const uint32_t q_smem = smem_u32(base), ring = smem_u32(ring_ptr);
+  const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0);
+  const int C = static_cast<int>(gridDim.x), c = static_cast<int>(blockIdx.x);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < slots_of(DP); ++i) {
+      mbar_init(&sm.full[i], 1);
+      mbar_init(&sm.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.q_full[i], 1);
+      mbar_init(&sm.q_empty[i], 1);
+      mbar_init(&sm.s_full[i], 1);
+      mbar_init(&sm.p_full[i], 4);
+    }
+    mbar_init(&sm.o_full, 1);
+    mbar_init(&sm.o_empty, kSoftWarps);
+    mbar_init(&sm.done, 1);
+    sm.abort = 0;
+    svk::fence_mbar_init_cluster();
+  }
+  if (warp == 9) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sm.tmem)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  fence_before();
+  make_plan<kThreads>(A, C, c, sm.plan);  // (two barriers of the CTA)
+  fence_after();
+  const uint32_t tmem = sm.tmem;
+  if (warp >= kSoftWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == 8)
+      produce<T, DP>(A, sm, q_smem, ring, C, c, &qm, &km, &vm, &kcm, &vcm);
+    else if (warp == 9)
+      issue<T, DP>(A, sm, ring_ptr, q_smem, ring, tmem, C, c);
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+    soften<T, DP>(A, sm, tmem, C, c);
+  }
+  fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  }
+  if (threadIdx.x == 0) A.err[c] = sm.abort ? 1u : 0u;
+}
+
+// Whether sequence b's layout is bad, by a CTA's threads t, t + T, ...
+__device__ __forceinline__ bool bad_layout(const Args& A, int b, int t, int T) {
+  int first = b * A.n, N = A.n;
+  if (A.cu) {
+    first = A.cu[b];
+    const int end = A.cu[b + 1];
+    N = end - first;
+    if (first < 0 || end < first || end > A.total || N > A.n) return true;
+  }
+  const int len = A.lengths[b];
+  if (len < 0 || len > A.max_pages * A.page) return true;
+  bool bad = false;
+  for (int j = t; j < (len + A.page - 1) / A.page; j += T) {
+    const int p = A.table[b * A.table_stride + j];
+    bad = bad || p < 0 || p >= A.pages;
+  }
+  if (A.parents)
+    for (int j = t; j < N; j += T) {
+      const int p = A.parents[first + j];
+      bad = bad || p < -1 || p >= j;
+    }
+  return bad;
+}
+
+// Joins the parts of items that several CTAs had, and writes the statuses.
+template <typename T, int DP>
+__global__ void __launch_bounds__(kFinishThreads) finish_kernel(const __grid_constant__ Args A, int C, int chunks, int join) {
+  __shared__ PlanMem m;
+  const int t = static_cast<int>(threadIdx.x);
+  if (static_cast<int>(blockIdx.x) >= join) {  // a warp per sequence
+    const int b = (static_cast<int>(blockIdx.x) - join) * (kFinishThreads / 32) + t / 32, lane = t & 31;
+    if (b >= A.batch) return;
+    const bool bad = __any_sync(0xFFFFFFFFu, bad_layout(A, b, lane, 32));
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    unsigned late = 0;
+    for (int i = lane; i < C; i += 32) late |= A.err[i];
+    late = __any_sync(0xFFFFFFFFu, late != 0);
+    if (lane == 0) A.status[b] = (bad ? SV_SEQ_BAD_LAYOUT : 0u) | (late ? SV_SEQ_TIMEOUT : 0u);
+    if (!bad) return;
+    int first = b * A.n, N = A.n;
+    if (A.cu) {
+      first = A.cu[b];
+      const int end = A.cu[b + 1];
+      N = end - first;
+      if (first < 0 || end < first || end > A.total || N > A.n) return;
+    }
+    for (int r = 0; r < N; ++r)
+      for (int h = 0; h < A.q_heads; ++h) {
+        T* o = static_cast<T*>(A.out) + static_cast<long long>(first + r) * A.out_row + static_cast<long long>(h) * A.out_head;
+        for (int d = lane; d < A.D / 8; d += 32) *reinterpret_cast<uint4*>(o + 8 * d) = make_uint4(0, 0, 0, 0);
+        if (A.lse && lane == 0) A.lse[static_cast<long long>(first + r) * A.q_heads + h] = -INFINITY;
+      }
+    return;
+  }
+  // the cut before CTA c, rows of chunk k
+  const int c = 1 + static_cast<int>(blockIdx.x) / chunks, k = static_cast<int>(blockIdx.x) % chunks;
+  make_plan<kFinishThreads>(A, C, c, m);
+  const long long W = m.W, u = begin_of(W, C, c);
+  if (m.b >= A.batch || u >= W) return;
+  const Sequence q = sequence(A, m.b);
+  const int item = static_cast<int>(m.off / q.tiles), into = static_cast<int>(m.off - static_cast<long long>(item) * q.tiles);
+  const long long a = u - into;
+  if (into == 0 || begin_of(W, C, c - 1) > a) return;  // no item is cut here, or it was cut before
+  const int first = owner_of(W, C, a), last = owner_of(W, C, a + q.tiles - 1);
+  const int head = item / q.items, pair = item % q.items;
+  // a thread has kCols columns of a row
+  constexpr int kPer = kFinishThreads / kFinishRows, kCols = DP / kPer;
+  const int r = k * kFinishRows + t / kPer, col = t % kPer * kCols;
+  const int query = 2 * pair + (r >= kTile ? 1 : 0), rr = r % kTile;
+  const int node = query * A.per_tile + rr / A.G;
+  const bool mine = rr < A.per_tile * A.G && node < q.N;
+  const bool bad = __syncthreads_or(bad_layout(A, m.b, t, kFinishThreads));
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (bad || !mine) return;
+  // the first part is the last segment of its CTA, the others are their CTAs' first
+  auto slot = [&](int x) { return 2 * x + (x == first && begin_of(W, C, x) < a ? 1 : 0); };
+  auto live = [&](int x) { return begin_of(W, C, x + 1) > begin_of(W, C, x); };
+  float top = -INFINITY;
+  for (int x = first; x <= last; ++x)
+    if (live(x)) top = fmaxf(top, A.part_ml[slot(x) * 256 + r].x);
+  float sum = 0, o[kCols] = {};
+#pragma unroll 4
+  for (int x = first; x <= last; ++x) {
+    if (!live(x)) continue;
+    const float2 ml = A.part_ml[slot(x) * 256 + r];
+    const float f = ml.x == -INFINITY ? 0.0f : svk::ex2_ftz(ml.x - top);
+    sum += ml.y * f;
+    const float* p = A.part + (static_cast<long long>(slot(x)) * 256 + r) * DP + col;
+#pragma unroll
+    for (int j = 0; j < kCols; j += 4) {
+      const float4 v = *reinterpret_cast<const float4*>(p + j);
+      o[j] += v.x * f;
+      o[j + 1] += v.y * f;
+      o[j + 2] += v.z * f;
+      o[j + 3] += v.w * f;
+    }
+  }
+  const float inv = 1.0f / sum;
+  const int qh = head * A.G + rr % A.G;
+  const long long at = static_cast<long long>(q.first) + node;
+  T* dst = static_cast<T*>(A.out) + at * A.out_row + static_cast<long long>(qh) * A.out_head;
+#pragma unroll
+  for (int j = 0; j < kCols; j += 8)
+    if (col + j < A.D) store_out<T>(dst + col + j, o + j, inv);
+  if (A.lse && col == 0) A.lse[at * A.q_heads + qh] = (top + log2f(sum)) * 0.69314718055994531f;
+}
+
+// ------------------------------------------------------------------ host
+
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  if (!fn) {
+    cudaDriverEntryPointQueryResult q;
+    void* p = nullptr;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  }
+  return fn;
+}
+
+// Dimensions innermost first; strides in elements of all but the first.  A
+// dimension of 1 may have any stride: one that the encoding takes is put in.
+bool encode(CUtensorMap* map, int64_t dtype, const void* data, int dims, const int64_t* size, const int64_t* stride,
+            const int* box) {
+  cuuint64_t d[4], s[3];
+  cuuint32_t b[4], e[4] = {1, 1, 1, 1};
+  for (int i = 0; i < dims; ++i) {
+    d[i] = static_cast<cuuint64_t>(size[i]);
+    b[i] = static_cast<cuuint32_t>(box[i]);
+    if (i) s[i - 1] = static_cast<cuuint64_t>(size[i] > 1 || stride[i - 1] > 0 ? stride[i - 1] * 2 : 16);
+    if (i && s[i - 1] == 0) s[i - 1] = 16;
+  }
+  return encoder()(map, dtype == SV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                   static_cast<cuuint32_t>(dims), const_cast<void*>(data), d, s, b, e, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+size_t workspace_bytes_of(int dim) {
+  const size_t rows = 2 * kMaxCtas * 256;
+  return rows * (dim <= 64 ? 64 : 128) * 4 + rows * 8 + (kMaxCtas * 4 + 15) / 16 * 16;
+}
+
+template <typename T, int DP>
+sv_status launch(const sv_tree_attn& a, float scale, unsigned char* ws, cudaStream_t st) {
+  if (!encoder()) return svh::fail(SV_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+  Args A;
+  A.G = static_cast<int>(a.q_heads / a.kv_heads);
+  A.per_tile = kTile / A.G;
+  A.Hkv = static_cast<int>(a.kv_heads);
+  A.D = static_cast<int>(a.dim);
+  A.page = static_cast<int>(a.page_size);
+  A.box = 8;
+  while (A.box < kTile && A.page % (2 * A.box) == 0) A.box *= 2;
+  A.tree_box = 8;
+  while (A.tree_box < kTile && A.tree_box < a.n) A.tree_box *= 2;
+  A.batch = static_cast<int>(a.batch);
+  A.n = a.total > 0 ? static_cast<int>(a.n) : 0;
+  A.total = static_cast<int>(a.total);
+  A.pages = static_cast<int>(a.pages);
+  A.max_pages = a.max_pages;
+  A.table_stride = a.table_stride;
+  A.table = a.table;
+  A.lengths = a.lengths;
+  A.parents = a.parents;
+  A.cu = a.cu_nodes;
+  A.v = a.v;
+  A.v_row = a.v_row;
+  A.v_head = a.v_head;
+  A.out = a.out;
+  A.out_row = a.out_row;
+  A.out_head = a.out_head;
+  A.lse = a.lse;
+  A.q_heads = static_cast<int>(a.q_heads);
+  A.c = (scale < 0 ? -scale : scale) * 1.4426950408889634f;
+  A.flip = scale < 0;
+  const size_t rows = 2 * kMaxCtas * 256;
+  A.part = reinterpret_cast<float*>(ws);
+  A.part_ml = reinterpret_cast<float2*>(ws + rows * DP * 4);
+  A.err = reinterpret_cast<unsigned*>(ws + rows * DP * 4 + rows * 8);
+  A.status = a.status;
+  CUtensorMap qm, km, vm, kcm, vcm;
+  if (a.total > 0) {
+    const int64_t qd[] = {a.dim, a.q_heads, a.total}, qs[] = {a.q_head, a.q_row};
+    const int64_t kd[] = {a.dim, a.total, a.kv_heads}, ks[] = {a.k_row, a.k_head}, vs[] = {a.v_row, a.v_head};
+    const int64_t cd[] = {a.dim, a.page_size, a.kv_heads, a.pages}, kcs[] = {a.kc_token, a.kc_head, a.kc_page},
+                  vcs[] = {a.vc_token, a.vc_head, a.vc_page};
+    const int qb[] = {64, A.G, A.per_tile}, kb[] = {64, A.tree_box, 1}, cb[] = {64, A.box, 1, 1};
+    if (!encode(&qm, a.dtype, a.q, 3, qd, qs, qb) || !encode(&km, a.dtype, a.k, 3, kd, ks, kb) ||
+        !encode(&vm, a.dtype, a.v, 3, kd, vs, kb) || !encode(&kcm, a.dtype, a.k_cache, 4, cd, kcs, cb) ||
+        !encode(&vcm, a.dtype, a.v_cache, 4, cd, vcs, cb))
+      return svh::fail(SV_ERR_ARG, "tensor map encoding failed (a stride or size is out of range)");
+  }
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 0;
+  static bool attr_set[64] = {false};
+  static int sms[64] = {0};
+  if (!attr_set[dev]) {
+    const cudaError_t e = cudaFuncSetAttribute(attend_kernel<T, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<DP>());
+    if (e != cudaSuccess) return svh::fail(SV_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+    int n = 0;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = kMaxCtas;
+    sms[dev] = n < kMaxCtas ? n : kMaxCtas;
+    attr_set[dev] = true;
+  }
+  const int C = sms[dev];
+  if (a.total > 0) {
+    attend_kernel<T, DP><<<C, kThreads, smem_bytes<DP>(), st>>>(A, qm, km, vm, kcm, vcm);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return svh::fail(SV_ERR_CUDA, "kernel launch: %s", cudaGetErrorString(e));
+  }
+  // rows of a pair of query tiles, the second's from kTile on
+  const int most = static_cast<int>(a.n > A.per_tile ? kTile + (a.n - A.per_tile < A.per_tile ? a.n - A.per_tile : A.per_tile) * A.G
+                                                     : a.n * A.G);
+  const int chunks = (most + kFinishRows - 1) / kFinishRows;
+  const int join = a.total > 0 ? (C - 1) * chunks : 0;
+  const int grid = join + static_cast<int>((a.batch + kFinishThreads / 32 - 1) / (kFinishThreads / 32));
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(kFinishThreads);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.total > 0 ? 1 : 0;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, finish_kernel<T, DP>, A, a.total > 0 ? C : 0, chunks, join);
+  return e == cudaSuccess ? SV_OK : svh::fail(SV_ERR_CUDA, "kernel launch: %s", cudaGetErrorString(e));
 }
 
 }  // namespace sva
@@ -99,8 +1128,7 @@ __global__ void __launch_bounds__(32 * kWarps) simple_kernel(const __grid_consta
 extern "C" {
 
 size_t sv_tree_attention_workspace_size(int32_t dim) {
-  (void)dim;
-  return 0;
+  return dim < 1 ? 0 : sva::workspace_bytes_of(dim);
 }
 
 sv_status sv_tree_attention(const sv_tree_attn* args, float scale, void* workspace, size_t workspace_bytes,
@@ -135,20 +1163,16 @@ sv_status sv_tree_attention(const sv_tree_attn* args, float scale, void* workspa
     if (x < 0 || x % 8) return svh::fail(SV_ERR_ARG, "strides must be multiples of 8 elements, not negative");
   for (const void* p : {a.q, a.k, a.v, a.k_cache, a.v_cache, static_cast<const void*>(a.out)})
     if (reinterpret_cast<uintptr_t>(p) & 15) return svh::fail(SV_ERR_ARG, "q, k, v, the caches and out must be 16-byte aligned");
-  const long long warps = a.batch * (a.n > 0 ? a.n : 1) * a.q_heads;
-  sv_tree_attn b = a;
-  if (b.n == 0) {  // (one warp per sequence and head writes the status)
-    b.n = 1;
-    b.total = 0;
-  }
-  const long long grid = (warps + sva::kWarps - 1) / sva::kWarps;
-  if (grid > kMax) return svh::fail(SV_ERR_UNSUPPORTED, "the call is too large");
+  const size_t need = sva::workspace_bytes_of(static_cast<int>(a.dim));
+  if (!workspace || workspace_bytes < need)
+    return svh::fail(SV_ERR_ARG, "workspace_bytes (%zu) < the %zu bytes sv_tree_attention_workspace_size() asks for",
+                     workspace_bytes, need);
+  if (reinterpret_cast<uintptr_t>(workspace) & 15) return svh::fail(SV_ERR_ARG, "workspace must be 16-byte aligned");
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (a.dtype == SV_BF16)
-    sva::simple_kernel<__nv_bfloat16><<<static_cast<unsigned>(grid), 32 * sva::kWarps, 0, static_cast<cudaStream_t>(stream)>>>(b, scale);
-  else
-    sva::simple_kernel<__half><<<static_cast<unsigned>(grid), 32 * sva::kWarps, 0, static_cast<cudaStream_t>(stream)>>>(b, scale);
-  const cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess ? SV_OK : svh::fail(SV_ERR_CUDA, "kernel launch: %s", cudaGetErrorString(e));
+    return a.dim <= 64 ? sva::launch<__nv_bfloat16, 64>(a, scale, ws, st) : sva::launch<__nv_bfloat16, 128>(a, scale, ws, st);
+  return a.dim <= 64 ? sva::launch<__half, 64>(a, scale, ws, st) : sva::launch<__half, 128>(a, scale, ws, st);
 }
 
 }  // extern "C"
