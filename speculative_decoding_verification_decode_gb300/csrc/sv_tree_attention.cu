@@ -11,11 +11,13 @@
 // A CTA, one per SM, has
 //   warps 0-3, 4-7  two softmax streams, each with a score tile and an output
 //                   tile in tensor memory (4 x 128 columns, all there are);
-//   warp 8          producer: TMA loads, one box per page (or part of a page)
-//                   and 64 elements, 128-byte swizzle, into a ring of slots that
-//                   keys and values share;
-//   warp 9          issues the MMAs (two more warps make its warpgroup full, so
-//                   that the softmax warps can have its registers).
+//   warp 8, 11      producers of queries and keys, of values: TMA loads, one box
+//                   per page (or part of a page) and 64 elements, 128-byte
+//                   swizzle, into rings of tiles;
+//   warp 9          issues the MMAs;
+//   warp 10         mends value tiles: zeros past the last key, and what is no
+//                   finite number among the drafted values (below).
+// The softmax warps take registers that the others have no use for.
 // A step is one query tile against one key tile, step g on stream g % 2.  With
 // one query tile to an item the streams take its key tiles in turn and their
 // results are joined at the end; with two, each takes one, and a key tile is
@@ -68,12 +70,16 @@ constexpr int kFinishRows = 32;  // rows that a CTA of the second kernel joins
 constexpr float kSlack = 8.0f;   // how far the maximum may pass the reference, powers of two
 
 __host__ __device__ constexpr int tile_bytes(int dp) { return kTile * dp * 2; }
-// Slots of the ring: two query tiles and these fill the shared memory.
-__host__ __device__ constexpr int slots_of(int dp) { return dp == 128 ? 5 : 10; }
+// Slots of the rings of keys and values: with two query tiles they fill the
+// shared memory.
+__host__ __device__ constexpr int k_slots(int dp) { return dp == 128 ? 3 : 5; }
+__host__ __device__ constexpr int v_slots(int dp) { return dp == 128 ? 2 : 5; }
 
 struct Args {
   int G, per_tile;  // query heads per key head; nodes per query tile
-  int Hkv, D, page, box, tree_box;  // keys per box, of the cache and of the nodes
+  uint32_t per_pair_inv;  // ceil(2^32 / (nodes per pair of query tiles)): exact for as few nodes as there are
+  int Hkv, D, page, box, tree_box;  // keys per box (a power of two), of the cache and of the nodes
+  int box_shift;
   int batch, n, total, pages;
   long long max_pages, table_stride;
   const int* table;
@@ -115,7 +121,7 @@ __device__ __forceinline__ Sequence sequence(const Args& A, int b) {
   if (s.len < 0 || s.len > A.max_pages * A.page) s.N = 0;
   s.cached = (s.len + kTile - 1) / kTile;
   s.tiles = s.cached + (s.N + kTile - 1) / kTile;
-  s.items = (s.N + 2 * A.per_tile - 1) / (2 * A.per_tile);
+  s.items = static_cast<int>(__umulhi(static_cast<uint32_t>(s.N + 2 * A.per_tile - 1), A.per_pair_inv));
   return s;
 }
 
@@ -123,19 +129,34 @@ __device__ __forceinline__ long long units_of(const Args& A, const Sequence& s) 
   return s.N > 0 ? static_cast<long long>(s.tiles) * s.items * A.Hkv : 0;
 }
 
-// CTA c of C takes units [begin(c), begin(c + 1)) of W.
-__device__ __forceinline__ long long begin_of(long long W, int C, int c) { return W * c / C; }
-// The CTA that has unit u.
-__device__ __forceinline__ int owner_of(long long W, int C, long long u) { return static_cast<int>(((u + 1) * C - 1) / W); }
+// W units over C CTAs, the first `more` of which take one more than `each`.
+struct Cut {
+  long long each;
+  int more;
+  __device__ __forceinline__ long long begin(int c) const { return each * c + (c < more ? c : more); }
+  __device__ __forceinline__ long long count(int c) const { return each + (c < more ? 1 : 0); }
+  // the CTA that has unit u
+  __device__ __forceinline__ int owner(long long u) const {
+    const long long wide = (each + 1) * more;
+    if (u < wide) return divide(u, each + 1);
+    return more + divide(u - wide, each);
+  }
+  // (a division of 64 bits is some hundred instructions)
+  static __device__ __forceinline__ int divide(long long a, long long b) {
+    if ((a | b) >> 32) return static_cast<int>(a / b);
+    return static_cast<int>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b));
+  }
+};
 
 struct PlanMem {
   long long warp_sums[kThreads / 32];
-  long long W, off;
+  long long off;
+  Cut cut;
   int b;
 };
 
-// All of a CTA's threads: the number of units, and the sequence that unit
-// begin_of(c) lies in, with the units before it there.  `T` threads.
+// All of a CTA's T threads: the cut, and the sequence that CTA c's first unit
+// lies in, with the units before it there.
 template <int T>
 __device__ __forceinline__ void make_plan(const Args& A, int C, int c, PlanMem& m) {
   const int t = static_cast<int>(threadIdx.x), lane = t & 31, warp = t >> 5;
@@ -157,8 +178,11 @@ __device__ __forceinline__ void make_plan(const Args& A, int C, int c, PlanMem& 
     if (w < warp) before += m.warp_sums[w];
     W += m.warp_sums[w];
   }
-  const long long u = begin_of(W, C, c);
-  if (t == 0) m.W = W;
+  Cut cut;
+  cut.each = Cut::divide(W, C);
+  cut.more = static_cast<int>(W - cut.each * C);
+  const long long u = cut.begin(c);
+  if (t == 0) m.cut = cut;
   if (u >= before && u < before + mine)
     for (int b = lo; b < hi; ++b) {
       const long long k = units_of(A, sequence(A, b));
@@ -194,12 +218,12 @@ struct Walk {
       s.q = sequence(A, b);
       if (off < units_of(A, s.q)) break;
     }
-    const int item = static_cast<int>(off / s.q.tiles);
+    const int item = off < s.q.tiles ? 0 : Cut::divide(off, s.q.tiles);
     s.b = b;
     s.t0 = static_cast<int>(off - static_cast<long long>(item) * s.q.tiles);
     s.t1 = s.q.tiles - s.t0 < left ? s.q.tiles : s.t0 + static_cast<int>(left);
-    s.head = item / s.q.items;
-    s.pair = item % s.q.items;
+    s.head = s.q.items == 1 ? item : item / s.q.items;
+    s.pair = item - s.head * s.q.items;
     s.two = s.q.N > (2 * s.pair + 1) * A.per_tile;
     s.whole = s.t0 == 0 && s.t1 == s.q.tiles;
     s.steps = (s.t1 - s.t0) * (s.two ? 2 : 1);
@@ -217,10 +241,10 @@ struct Steps {
   int k;   // step of the segment
   bool ok;
 
-  __device__ __forceinline__ void start(const Args& A, const PlanMem& m, int C, int c) {
+  __device__ __forceinline__ void start(const Args& A, const PlanMem& m, int c) {
     w.b = m.b;
     w.off = m.off;
-    w.left = begin_of(m.W, C, c + 1) - begin_of(m.W, C, c);
+    w.left = m.cut.count(c);
     w.count = 0;
     k = 0;
     ok = w.next(A, s);
@@ -272,9 +296,6 @@ struct Num<__half> {
 // word the stride of 8 rows (1024 bytes), version 1 and the swizzle.  Query and
 // key tiles are K-major; value tiles are N-major, their leading stride is that
 // of the panels.
-__device__ __forceinline__ uint64_t desc(uint32_t saddr, uint32_t leading) {
-  return static_cast<uint64_t>((1024u >> 4) | 1u << 14 | 2u << 29) << 32 | ((saddr & 0x3FFFFu) >> 4) | leading << 16;
-}
 // Instruction descriptor: D f32, A and B of the type, M = 128, N; B N-major.
 template <typename T>
 __host__ __device__ constexpr uint32_t idesc(int N, bool n_major) {
@@ -331,16 +352,11 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* v) {
       : "r"(taddr)
       : "memory");
 }
-// 64 of them.
-__device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t* v) {
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* v) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, "
-      "%13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
-      "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, "
-      "%52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];\n"
-      "tcgen05.wait::ld.sync.aligned;"
-      : SVA_R8(v, 0), SVA_R8(v, 8), SVA_R8(v, 16), SVA_R8(v, 24), SVA_R8(v, 32), SVA_R8(v, 40), SVA_R8(v, 48), SVA_R8(v, 56)
-      : "r"(taddr)
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, "
+      "%13, %14, %15};" ::SVA_W8(v, 0),
+      SVA_W8(v, 8), "r"(taddr)
       : "memory");
 }
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* v) {
@@ -373,7 +389,9 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 // ------------------------------------------------------------------ the kernel
 
 struct __align__(8) Shared {
-  uint64_t full[10], empty[10];      // ring: producer -> MMA, MMA -> producer
+  uint64_t k_full[5], k_empty[5];    // keys: producer -> MMA, MMA -> producer
+  uint64_t v_full[5], v_empty[5];    // values: producer -> MMA and mender, both -> producer
+  uint64_t v_mended[5];              // mender -> MMA
   uint64_t q_full[2], q_empty[2];    // query tiles
   uint64_t s_full[2];                // MMA -> softmax: the stream's scores
   uint64_t p_full[2];                // softmax -> MMA: its weights
@@ -382,7 +400,8 @@ struct __align__(8) Shared {
   uint32_t tmem;
   volatile int abort;
   PlanMem plan;
-  uint32_t odd[8];                   // nodes of the segment with values that are no finite numbers
+  uint32_t v_odd[5][4];              // keys of a value tile of nodes whose values are no finite numbers
+  uint32_t odd[8];                   // the segment's nodes with such values
   float2 ex[2][kTile];               // [stream]: maximum, sum of each row
 };
 
@@ -401,197 +420,241 @@ __device__ __forceinline__ void bar_soft() { asm volatile("bar.sync 1, %0;" ::"n
 
 template <int DP>
 __host__ __device__ constexpr int smem_bytes() {
-  return (2 + slots_of(DP)) * tile_bytes(DP) + static_cast<int>(sizeof(Shared));
+  return (2 + k_slots(DP) + v_slots(DP)) * tile_bytes(DP) + static_cast<int>(sizeof(Shared));
 }
 
 static_assert(smem_bytes<128>() <= 232448 && smem_bytes<64>() <= 232448, "a CTA's shared memory");
 
-template <typename T, int DP>
-__device__ __forceinline__ void produce(const Args& A, Shared& sm, uint32_t q_smem, uint32_t ring, int C, int c,
-                                        const CUtensorMap* qm, const CUtensorMap* km, const CUtensorMap* vm,
-                                        const CUtensorMap* kcm, const CUtensorMap* vcm) {
-  constexpr int kPanels = DP / 64, kSlots = slots_of(DP);
-  const int lane = static_cast<int>(threadIdx.x & 31);
-  Steps qk, pv;
-  qk.start(A, sm.plan, C, c);
-  pv.start(A, sm.plan, C, c);
-  uint32_t slot = 0, turn = 0, qs = 0;
-  bool alive = true;
-  // a key or value tile into the next slot: every lane its boxes
-  auto load = [&](const Segment& s, int t, const CUtensorMap* cache, const CUtensorMap* own) {
-    if (turn && !warp_wait(sm, &sm.empty[slot], (turn - 1) & 1)) {
-      alive = false;
-      return;
-    }
-    const uint32_t dst = ring + slot * tile_bytes(DP);
-    uint64_t* bar = &sm.full[slot];
-    const int keys = keys_of(s, t);
-    if (t < s.q.cached) {
-      const int boxes = (keys + A.box - 1) / A.box;
-      if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(boxes * A.box * 128 * kPanels));
-      __syncwarp();
-      for (int i = lane; i < boxes * kPanels; i += 32) {
-        const int x = kPanels == 2 ? i & 1 : 0, k = kPanels == 2 ? i >> 1 : i;
-        const int at = t * kTile + k * A.box, p = at / A.page;
-        const int id = A.table[s.b * A.table_stride + p];
-        tma_4d(dst + x * (kTile * 128) + k * A.box * 128, cache, x * 64, at - p * A.page, s.head, id, bar);
-      }
-    } else {
-      if (lane == 0) {
-        mbar_arrive_expect_tx(bar, static_cast<uint32_t>(A.tree_box * 128 * kPanels));
-        for (int x = 0; x < kPanels; ++x)
-          tma_3d(dst + x * (kTile * 128), own, x * 64, s.q.first + (t - s.q.cached) * kTile, s.head, bar);
-      }
-    }
+// One lane of the warp, the same every time.
+__device__ __forceinline__ bool elected() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+  return p != 0;
+}
+
+__device__ __forceinline__ Walk walk_of(const PlanMem& m, int c) {
+  Walk w;
+  w.b = m.b;
+  w.off = m.off;
+  w.left = m.cut.count(c);
+  w.count = 0;
+  return w;
+}
+
+// Tile t of keys or values to shared memory at `dst`: every lane its boxes.
+template <int DP>
+__device__ __forceinline__ void load_tile(const Args& A, const Segment& s, int t, const CUtensorMap* cache,
+                                          const CUtensorMap* own, uint32_t dst, uint64_t* bar, int lane) {
+  constexpr int kPanels = DP / 64;
+  if (t < s.q.cached) {
+    const int boxes = (keys_of(s, t) + A.box - 1) >> A.box_shift;
+    int i = lane, id = 0;
+    const int at = t * kTile + ((i / kPanels) << A.box_shift), p = at / A.page;
+    if (i < boxes * kPanels) id = A.table[s.b * A.table_stride + p];
+    if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(boxes * A.box * 128 * kPanels));
     __syncwarp();
-    if (++slot == kSlots) slot = 0, ++turn;
-  };
-  auto scores = [&]() {  // what QK of the next step needs
-    if (!qk.ok || !alive) return;
-    if (qk.k < (qk.s.two ? 2 : 1)) {
+    if (i < boxes * kPanels)  // (at most 16 boxes of a panel)
+      tma_4d(dst + (i % kPanels) * (kTile * 128) + (i / kPanels) * A.box * 128, cache, (i % kPanels) * 64, at - p * A.page, s.head,
+             id, bar);
+  } else {
+    if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(A.tree_box * 128 * kPanels));
+    __syncwarp();
+    if (lane < kPanels)
+      tma_3d(dst + lane * (kTile * 128), own, lane * 64, s.q.first + (t - s.q.cached) * kTile, s.head, bar);
+  }
+  __syncwarp();
+}
+
+// Queries and keys.
+template <int DP>
+__device__ __forceinline__ void produce_keys(const Args& A, Shared& sm, uint32_t q_smem, uint32_t ring, int c, const CUtensorMap* qm,
+                                             const CUtensorMap* km, const CUtensorMap* kcm) {
+  constexpr int kPanels = DP / 64, kSlots = k_slots(DP);
+  const int lane = static_cast<int>(threadIdx.x & 31);
+  Walk w = walk_of(sm.plan, c);
+  Segment s;
+  uint32_t slot = 0, turn = 0, loads = 0, qs = 0;
+  bool alive = true;
+  while (alive && w.next(A, s)) {
+    for (int j = 0; alive && j < (s.two ? 2 : 1); ++j, ++qs) {
       const uint32_t buf = qs & 1;
-      if (qs >= 2 && !warp_wait(sm, &sm.q_empty[buf], ((qs >> 1) - 1) & 1)) {
-        alive = false;
-        return;
-      }
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&sm.q_full[buf], static_cast<uint32_t>(A.per_tile * A.G * 128 * kPanels));
-        for (int x = 0; x < kPanels; ++x)
-          tma_3d(q_smem + buf * tile_bytes(DP) + x * (kTile * 128), qm, x * 64, qk.s.head * A.G,
-                 qk.s.q.first + (2 * qk.s.pair + qk.k) * A.per_tile, &sm.q_full[buf]);
-      }
+      if (qs >= 2) alive = warp_wait(sm, &sm.q_empty[buf], ((qs >> 1) - 1) & 1);
+      if (!alive) break;
+      if (lane == 0) mbar_arrive_expect_tx(&sm.q_full[buf], static_cast<uint32_t>(A.per_tile * A.G * 128 * kPanels));
       __syncwarp();
-      ++qs;
+      if (lane < kPanels)
+        tma_3d(q_smem + buf * tile_bytes(DP) + lane * (kTile * 128), qm, lane * 64, s.head * A.G,
+               s.q.first + (2 * s.pair + j) * A.per_tile, &sm.q_full[buf]);
     }
-    if (qk.fresh()) load(qk.s, qk.tile(), kcm, km);
-    qk.advance(A);
-  };
-  scores();
-  scores();
-  while (pv.ok && alive) {
-    if (pv.fresh()) load(pv.s, pv.tile(), vcm, vm);
-    if (!alive) break;
-    pv.advance(A);
-    scores();
+    for (int t = s.t0; alive && t < s.t1; ++t) {
+      if (turn) alive = warp_wait(sm, &sm.k_empty[slot], (turn - 1) & 1);
+      if (!alive) break;
+      load_tile<DP>(A, s, t, kcm, km, ring + slot * tile_bytes(DP), &sm.k_full[slot], lane);
+      ++loads;
+      if (++slot == kSlots) slot = 0, ++turn;
+    }
   }
   // no copy may still be writing shared memory at exit
-  const uint32_t loads = turn * kSlots + slot;
-  for (uint32_t i = loads > kSlots ? loads - kSlots : 0; i < loads; ++i) svk::mbar_wait_bounded(&sm.full[i % kSlots], (i / kSlots) & 1);
+  for (uint32_t i = loads > kSlots ? loads - kSlots : 0; i < loads; ++i) svk::mbar_wait_bounded(&sm.k_full[i % kSlots], (i / kSlots) & 1);
   for (uint32_t i = qs > 2 ? qs - 2 : 0; i < qs; ++i) svk::mbar_wait_bounded(&sm.q_full[i & 1], (i >> 1) & 1);
 }
 
-template <typename T, int DP>
-__device__ __forceinline__ void issue(const Args& A, Shared& sm, unsigned char* ring_ptr, uint32_t q_smem, uint32_t ring,
-                                      uint32_t tmem, int C, int c) {
-  constexpr int kPanels = DP / 64, kSlots = slots_of(DP);
+template <int DP>
+__device__ __forceinline__ void produce_values(const Args& A, Shared& sm, uint32_t ring, int c, const CUtensorMap* vm,
+                                               const CUtensorMap* vcm) {
+  constexpr int kSlots = v_slots(DP);
   const int lane = static_cast<int>(threadIdx.x & 31);
-  Steps qk, pv;
-  qk.start(A, sm.plan, C, c);
-  pv.start(A, sm.plan, C, c);
-  uint32_t slot = 0, turn = 0, qs = 0, gq = 0, gp = 0;
-  uint32_t k_slot = 0, v_slot = 0, q_first = 0;  // of the steps at hand; the segment's first query tile
-  uint32_t segments = 0;
+  Walk w = walk_of(sm.plan, c);
+  Segment s;
+  uint32_t slot = 0, turn = 0, loads = 0;
   bool alive = true;
-  auto take = [&](uint32_t& mine) {  // the next slot of the ring, landed
-    if (!warp_wait(sm, &sm.full[slot], turn & 1)) {
-      alive = false;
-      return;
+  while (alive && w.next(A, s))
+    for (int t = s.t0; alive && t < s.t1; ++t) {
+      if (turn) alive = warp_wait(sm, &sm.v_empty[slot], (turn - 1) & 1);
+      if (!alive) break;
+      load_tile<DP>(A, s, t, vcm, vm, ring + slot * tile_bytes(DP), &sm.v_full[slot], lane);
+      ++loads;
+      if (++slot == kSlots) slot = 0, ++turn;
     }
-    mine = slot;
-    if (++slot == kSlots) slot = 0, ++turn;
-  };
-  auto scores = [&]() {
-    if (!qk.ok || !alive) return;
-    const int queries = qk.s.two ? 2 : 1;
-    if (qk.k == 0) q_first = qs;
-    if (qk.k < queries) {
-      if (!warp_wait(sm, &sm.q_full[qs & 1], (qs >> 1) & 1)) {
-        alive = false;
-        return;
+  for (uint32_t i = loads > kSlots ? loads - kSlots : 0; i < loads; ++i) svk::mbar_wait_bounded(&sm.v_full[i % kSlots], (i / kSlots) & 1);
+}
+
+// Whether a value tile is mended before it is used.
+__device__ __forceinline__ bool mends(const Segment& s, int t, int keys) { return t >= s.q.cached || keys % 16; }
+
+template <typename T, int DP>
+__device__ __forceinline__ void mend(const Args& A, Shared& sm, unsigned char* ring, int c) {
+  constexpr int kPanels = DP / 64, kSlots = v_slots(DP);
+  const int lane = static_cast<int>(threadIdx.x & 31);
+  Walk w = walk_of(sm.plan, c);
+  Segment s;
+  uint32_t slot = 0, turn = 0;
+  bool alive = true;
+  while (alive && w.next(A, s)) {
+    for (int t = s.t0; alive && t < s.t1; ++t) {
+      alive = warp_wait(sm, &sm.v_full[slot], turn & 1);
+      if (!alive) break;
+      const int keys = keys_of(s, t);
+      if (mends(s, t, keys)) {
+        unsigned char* v = ring + slot * tile_bytes(DP);
+        if (t >= s.q.cached) {
+          if (lane < 4) sm.v_odd[slot][lane] = 0;
+          __syncwarp();
+          constexpr uint32_t kE = Num<T>::kExp;
+          for (int i = lane; i < keys * 8 * kPanels; i += 32) {
+            const int r = i / (8 * kPanels), x = i % (8 * kPanels);
+            uint4* p = reinterpret_cast<uint4*>(v + (x / 8) * (kTile * 128) + r * 128 + (x % 8) * 16);
+            uint4 u = *p;
+            uint32_t* e = reinterpret_cast<uint32_t*>(&u);
+            bool odd = false;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              if ((e[j] & kE) == kE) e[j] &= 0xFFFF0000u, odd = true;
+              if ((e[j] >> 16 & kE) == kE) e[j] &= 0xFFFFu, odd = true;
+            }
+            if (odd) {
+              *p = u;
+              atomicOr(&sm.v_odd[slot][r / 32], 1u << (r % 32));
+            }
+          }
+        }
+        for (int i = keys * 8 * kPanels + lane; i < (keys + 15) / 16 * 16 * 8 * kPanels; i += 32) {
+          const int r = i / (8 * kPanels), x = i % (8 * kPanels);
+          *reinterpret_cast<uint4*>(v + (x / 8) * (kTile * 128) + r * 128 + (x % 8) * 16) = make_uint4(0, 0, 0, 0);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
       }
+      if (lane == 0) {
+        mbar_arrive_local(&sm.v_mended[slot]);
+        mbar_arrive_local(&sm.v_empty[slot]);
+      }
+      __syncwarp();
+      if (++slot == kSlots) slot = 0, ++turn;
+    }
+  }
+}
+
+template <typename T, int DP>
+__device__ __forceinline__ void issue(const Args& A, Shared& sm, uint32_t q_smem, uint32_t k_ring, uint32_t v_ring, uint32_t tmem, int c) {
+  constexpr uint32_t kUnits = tile_bytes(DP) / 16;  // of the descriptors' addresses
+  constexpr uint32_t kHi = (1024u >> 4) | 1u << 14 | 2u << 29;
+  const bool leads = elected();
+  const int lane = static_cast<int>(threadIdx.x & 31);
+  // (all lanes run the loops, so that addresses stay in uniform registers)
+  const uint32_t q_lo = ((q_smem & 0x3FFFFu) >> 4) | 1u << 16, k_lo = ((k_ring & 0x3FFFFu) >> 4) | 1u << 16;
+  const uint32_t v_lo = ((v_ring & 0x3FFFFu) >> 4) | (kTile * 128 / 16) << 16;
+  auto full = [](uint32_t lo) { return static_cast<uint64_t>(kHi) << 32 | lo; };
+  Steps qk, pv;
+  qk.start(A, sm.plan, c);
+  pv = qk;
+  uint32_t k_slot = 0, k_turn = 0, v_slot = 0, v_turn = 0, qs = 0, q_first = 0, gq = 0, gp = 0;
+  auto scores = [&]() {
+    if (!qk.ok) return true;
+    const bool two = qk.s.two;
+    const uint32_t j = two ? qk.k & 1 : 0;
+    if (qk.k == 0) q_first = qs;
+    if (qk.k <= (two ? 1 : 0)) {
+      if (!warp_wait(sm, &sm.q_full[qs & 1], (qs >> 1) & 1)) return false;
       ++qs;
     }
-    if (qk.fresh()) take(k_slot);
-    if (!alive) return;
+    if (j == 0 && !warp_wait(sm, &sm.k_full[k_slot], k_turn & 1)) return false;
     fence_after();
-    if (lane == 0) {
-      const uint32_t q = (q_first + (qk.s.two ? qk.k & 1 : 0)) & 1;
-      const uint32_t a = q_smem + q * tile_bytes(DP), b = ring + k_slot * tile_bytes(DP);
+    const bool last = j == 1 || !two;
+    const uint32_t buf = (q_first + j) & 1;
+    const uint32_t a = q_lo + buf * kUnits, b = k_lo + k_slot * kUnits, d = tmem + (gq & 1) * kTile;
+    if (leads) {
 #pragma unroll
       for (int i = 0; i < DP / 16; ++i) {
-        const uint32_t at = (i / 4) * (kTile * 128) + (i % 4) * 32;
-        mma_ss(tmem + (gq & 1) * kTile, desc(a + at, 1), desc(b + at, 1), idesc<T>(kTile, false), i > 0);
+        const uint32_t at = (i / 4) * (kTile * 128 / 16) + (i % 4) * 2;
+        mma_ss(d, full(a + at), full(b + at), idesc<T>(kTile, false), i > 0);
       }
-      if (qk.last()) mma_commit(&sm.empty[k_slot]);
-      if (qk.k >= qk.s.steps - queries) mma_commit(&sm.q_empty[q]);
       mma_commit(&sm.s_full[gq & 1]);
+      if (last) mma_commit(&sm.k_empty[k_slot]);
+      if (qk.k >= qk.s.steps - (two ? 2 : 1)) mma_commit(&sm.q_empty[buf]);
     }
     __syncwarp();
+    if (last && ++k_slot == k_slots(DP)) k_slot = 0, ++k_turn;
     ++gq;
     qk.advance(A);
+    return true;
   };
-  scores();
-  scores();
-  while (pv.ok && alive) {
+  bool alive = scores() && scores();
+  uint32_t segments = 0;
+  while (alive && pv.ok) {
     const uint32_t st = gp & 1;
     if (pv.k == 0) {  // the outputs of the segment before have been read
       if (segments && !warp_wait(sm, &sm.o_empty, (segments - 1) & 1)) break;
-      if (lane < 8) sm.odd[lane] = 0;
       ++segments;
+      if (lane < 8) sm.odd[lane] = 0;
       __syncwarp();
     }
     const int t = pv.tile(), keys = keys_of(pv.s, t);
-    if (pv.fresh()) {
-      take(v_slot);
-      if (!alive) break;
-      unsigned char* v = ring_ptr + v_slot * tile_bytes(DP);
-      bool wrote = false;
-      if (t >= pv.s.q.cached) {  // drafted values that are no finite numbers
-        constexpr uint32_t kE = Num<T>::kExp;
-        for (int i = lane; i < keys * 8 * kPanels; i += 32) {
-          const int r = i / (8 * kPanels), x = i % (8 * kPanels);
-          uint4* p = reinterpret_cast<uint4*>(v + (x / 8) * (kTile * 128) + r * 128 + (x % 8) * 16);
-          uint4 u = *p;
-          uint32_t* w = reinterpret_cast<uint32_t*>(&u);
-          bool odd = false;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if ((w[j] & kE) == kE) w[j] &= 0xFFFF0000u, odd = true;
-            if ((w[j] >> 16 & kE) == kE) w[j] &= 0xFFFFu, odd = true;
-          }
-          if (odd) {
-            *p = u;
-            const int node = (t - pv.s.q.cached) * kTile + r;
-            atomicOr(&sm.odd[node / 32], 1u << (node % 32));
-            wrote = true;
-          }
-        }
-      }
-      for (int i = keys * 8 * kPanels + lane; i < (keys + 15) / 16 * 16 * 8 * kPanels; i += 32) {  // past the last key
-        const int r = i / (8 * kPanels), x = i % (8 * kPanels);
-        *reinterpret_cast<uint4*>(v + (x / 8) * (kTile * 128) + r * 128 + (x % 8) * 16) = make_uint4(0, 0, 0, 0);
-        wrote = true;
-      }
-      if (__any_sync(0xFFFFFFFFu, wrote)) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncwarp();
-    }
+    if (pv.fresh() && !warp_wait(sm, mends(pv.s, t, keys) ? &sm.v_mended[v_slot] : &sm.v_full[v_slot], v_turn & 1)) break;
+    if (t >= pv.s.q.cached && lane < 4) sm.odd[(t - pv.s.q.cached) * 4 + lane] = sm.v_odd[v_slot][lane];
+    const bool last = pv.last(), end = pv.k == pv.s.steps - 1;
+    const uint32_t b = v_lo + v_slot * kUnits, d = tmem + 256 + st * 128, a = tmem + st * kTile;
+    const uint32_t acc = pv.k >= 2 ? 1u : 0u;
     if (!warp_wait(sm, &sm.p_full[st], (gp >> 1) & 1)) break;
     fence_after();
-    if (lane == 0) {
-      const uint32_t b = ring + v_slot * tile_bytes(DP);
-      const int n16 = (keys + 15) / 16;
-      for (int i = 0; i < n16; ++i)
-        mma_ts(tmem + 256 + st * 128, tmem + st * kTile + i * 8, desc(b + i * 2048, kTile * 128 / 16),
-               idesc<T>(DP, true), (i > 0 || pv.k >= 2) ? 1u : 0u);
-      if (pv.last()) mma_commit(&sm.empty[v_slot]);
-      if (pv.k == pv.s.steps - 1) mma_commit(&sm.o_full);
+    if (leads) {
+      if (keys > kTile - 16) {
+#pragma unroll
+        for (int i = 0; i < kTile / 16; ++i) mma_ts(d, a + i * 8, full(b + i * 128), idesc<T>(DP, true), i > 0 ? 1u : acc);
+      } else {
+#pragma unroll 1
+        for (int i = 0; i * 16 < keys; ++i) mma_ts(d, a + i * 8, full(b + i * 128), idesc<T>(DP, true), i > 0 ? 1u : acc);
+      }
+      if (last) mma_commit(&sm.v_empty[v_slot]);
+      if (end) mma_commit(&sm.o_full);
     }
     __syncwarp();
+    if (last && ++v_slot == v_slots(DP)) v_slot = 0, ++v_turn;
     ++gp;
     pv.advance(A);
-    scores();
+    alive = scores();
   }
-  if (lane == 0) mma_commit(&sm.done);
+  if (leads) mma_commit(&sm.done);
   __syncwarp();
   svk::mbar_wait_bounded(&sm.done, 0);
 }
@@ -634,18 +697,16 @@ __device__ __forceinline__ void store_out(T* dst, const float* o, float f) {
 
 // A softmax warp.
 template <typename T, int DP>
-__device__ __forceinline__ void soften(const Args& A, Shared& sm, uint32_t tmem, int C, int c) {
+__device__ __forceinline__ void soften(const Args& A, Shared& sm, uint32_t tmem, int c) {
   const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
   const int stream = warp >> 2, row = (warp & 3) * 32 + lane;
   const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
   const uint32_t s_col = tmem + lanes + stream * kTile, o_col = tmem + lanes + 256;
-  Walk w;
-  w.b = sm.plan.b;
-  w.off = sm.plan.off;
-  w.left = begin_of(sm.plan.W, C, c + 1) - begin_of(sm.plan.W, C, c);
-  w.count = 0;
+  Walk w = walk_of(sm.plan, c);
   uint32_t g = 0;          // steps before the segment, both streams
   uint32_t turns = 0;      // of this stream
+  // (a scale of 0 as one that makes every finite score 0 too, and -inf still -inf)
+  const float c2 = A.c > 0 ? A.c : 1e-45f;
   bool alive = true;
   Segment s;
   while (w.next(A, s)) {
@@ -666,38 +727,44 @@ __device__ __forceinline__ void soften(const Args& A, Shared& sm, uint32_t tmem,
       ++turns;
       fence_after();
       if (busy && alive) {
-        uint32_t u[kTile];
-        tmem_ld64(s_col, u);
-        tmem_ld64(s_col + 64, u + 64);
-        float* x = reinterpret_cast<float*>(u);
-        if (A.flip) {
-#pragma unroll
-          for (int j = 0; j < kTile; ++j) x[j] = -x[j];
-        }
         const bool masked = tree || keys < kTile;
-        if (masked) {
-          if (!tree) {
+        if (masked && !tree) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int n = keys - 32 * i;
-              bits[i] = n >= 32 ? 0xFFFFFFFFu : n > 0 ? (1u << n) - 1u : 0u;
-            }
-          }
-#pragma unroll
-          for (int j = 0; j < kTile; ++j)
-            if (!(bits[j / 32] >> (j % 32) & 1)) x[j] = -INFINITY;
-        }
-        float m0 = x[0], m1 = x[1], m2 = x[2], m3 = x[3];
-#pragma unroll
-        for (int j = 4; j < kTile; j += 8) {
-          m0 = max3(m0, x[j], x[j + 1]);
-          m1 = max3(m1, x[j + 2], x[j + 3]);
-          if (j + 4 < kTile) {
-            m2 = max3(m2, x[j + 4], x[j + 5]);
-            m3 = max3(m3, x[j + 6], x[j + 7]);
+          for (int i = 0; i < 4; ++i) {
+            const int n = keys - 32 * i;
+            bits[i] = n >= 32 ? 0xFFFFFFFFu : n > 0 ? (1u << n) - 1u : 0u;
           }
         }
-        const float top = max3(fmaxf(m0, m1), m2, m3) * A.c;
+        // 32 scores, those that the row does not see -inf
+        auto scores = [&](int i, uint32_t bit, float (&x)[32]) {
+          uint32_t u[32];
+          tmem_ld32(s_col + i * 32, u);
+          if (A.flip) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) u[j] ^= 0x80000000u;
+          }
+          if (masked) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (!(bit >> j & 1)) u[j] = 0xFF800000u;
+          }
+#pragma unroll
+          for (int j = 0; j < 32; ++j) x[j] = __uint_as_float(u[j]);
+        };
+        float top = -INFINITY;
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {
+          float x[32];
+          scores(i, i == 0 ? bits[0] : i == 1 ? bits[1] : i == 2 ? bits[2] : bits[3], x);
+          float m0 = max3(top, x[0], x[1]), m1 = max3(x[2], x[3], x[4]);
+#pragma unroll
+          for (int j = 5; j < 29; j += 4) {
+            m0 = max3(m0, x[j], x[j + 1]);
+            m1 = max3(m1, x[j + 2], x[j + 3]);
+          }
+          top = max3(max3(m0, x[29], x[30]), m1, x[31]);
+        }
+        top *= c2;
         const bool move = top > ref + kSlack || (ref == -INFINITY && top > -INFINITY);
         if (__any_sync(0xFFFFFFFFu, move)) {
           const float to = move ? top : ref;
@@ -705,7 +772,7 @@ __device__ __forceinline__ void soften(const Args& A, Shared& sm, uint32_t tmem,
           ref = to;
           sum *= f;
           if (k >= 2) {
-#pragma unroll
+#pragma unroll 1
             for (int i = 0; i < DP / 32; ++i) {
               uint32_t o[32];
               tmem_ld32(o_col + stream * 128 + i * 32, o);
@@ -717,26 +784,25 @@ __device__ __forceinline__ void soften(const Args& A, Shared& sm, uint32_t tmem,
         }
         const float minus = ref == -INFINITY ? 0.0f : -ref;
         float a0 = 0, a1 = 0, b0 = 0, b1 = 0;
-        uint32_t p[kTile / 2];
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {
+          float x[32];
+          scores(i, i == 0 ? bits[0] : i == 1 ? bits[1] : i == 2 ? bits[2] : bits[3], x);
+          uint32_t p[16];
 #pragma unroll
-        for (int j = 0; j < kTile; j += 4) {
-          fma2(x[j], x[j + 1], A.c, minus);
-          fma2(x[j + 2], x[j + 3], A.c, minus);
+          for (int j = 0; j < 32; j += 4) {
+            fma2(x[j], x[j + 1], c2, minus);
+            fma2(x[j + 2], x[j + 3], c2, minus);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) x[j + i] = svk::ex2_ftz(x[j + i]);
-          if (masked) {  // (-inf times a scale of 0 is no number)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (!(bits[(j + i) / 32] >> ((j + i) % 32) & 1)) x[j + i] = 0;
+            for (int e = 0; e < 4; ++e) x[j + e] = svk::ex2_ftz(x[j + e]);
+            add2(a0, a1, x[j], x[j + 1]);
+            add2(b0, b1, x[j + 2], x[j + 3]);
+            p[j / 2] = Num<T>::pack(x[j], x[j + 1]);
+            p[j / 2 + 1] = Num<T>::pack(x[j + 2], x[j + 3]);
           }
-          add2(a0, a1, x[j], x[j + 1]);
-          add2(b0, b1, x[j + 2], x[j + 3]);
-          p[j / 2] = Num<T>::pack(x[j], x[j + 1]);
-          p[j / 2 + 1] = Num<T>::pack(x[j + 2], x[j + 3]);
+          tmem_st16(s_col + i * 16, p);  // (over scores that have been read)
         }
         sum += (a0 + a1) + (b0 + b1);
-        tmem_st32(s_col, p);
-        tmem_st32(s_col + 32, p + 32);
         tmem_st_wait();
       }
       fence_before();
@@ -842,16 +908,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) A.err[blockIdx.x] = 1u;
     return;
   }
-  unsigned char* ring_ptr = base + 2 * tile_bytes(DP);
-  Shared& sm = *reinterpret_cast<Shared*>(ring_ptr + slots_of(DP) * tile_bytes(DP));
-  const uint32_t q_smem = smem_u32(base), ring = smem_u32(ring_ptr);
+  unsigned char* v_ptr = base + (2 + k_slots(DP)) * tile_bytes(DP);
+  Shared& sm = *reinterpret_cast<Shared*>(v_ptr + v_slots(DP) * tile_bytes(DP));
+  const uint32_t q_smem = smem_u32(base), k_ring = q_smem + 2 * tile_bytes(DP), v_ring = smem_u32(v_ptr);
   const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0);
   const int C = static_cast<int>(gridDim.x), c = static_cast<int>(blockIdx.x);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x == 0) {
-    for (int i = 0; i < slots_of(DP); ++i) {
-      mbar_init(&sm.full[i], 1);
-      mbar_init(&sm.empty[i], 1);
+    for (int i = 0; i < k_slots(DP); ++i) {
+      mbar_init(&sm.k_full[i], 1);
+      mbar_init(&sm.k_empty[i], 1);
+    }
+    for (int i = 0; i < v_slots(DP); ++i) {
+      mbar_init(&sm.v_full[i], 1);
+      mbar_init(&sm.v_empty[i], 2);
+      mbar_init(&sm.v_mended[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.q_full[i], 1);
@@ -876,12 +947,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp >= kSoftWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == 8)
-      produce<T, DP>(A, sm, q_smem, ring, C, c, &qm, &km, &vm, &kcm, &vcm);
+      produce_keys<DP>(A, sm, q_smem, k_ring, c, &qm, &km, &kcm);
     else if (warp == 9)
-      issue<T, DP>(A, sm, ring_ptr, q_smem, ring, tmem, C, c);
+      issue<T, DP>(A, sm, q_smem, k_ring, v_ring, tmem, c);
+    else if (warp == 10)
+      mend<T, DP>(A, sm, v_ptr, c);
+    else
+      produce_values<DP>(A, sm, v_ring, c, &vm, &vcm);
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
-    soften<T, DP>(A, sm, tmem, C, c);
+    soften<T, DP>(A, sm, tmem, c);
   }
   fence_before();
   __syncthreads();
@@ -949,13 +1024,14 @@ __global__ void __launch_bounds__(kFinishThreads) finish_kernel(const __grid_con
   // the cut before CTA c, rows of chunk k
   const int c = 1 + static_cast<int>(blockIdx.x) / chunks, k = static_cast<int>(blockIdx.x) % chunks;
   make_plan<kFinishThreads>(A, C, c, m);
-  const long long W = m.W, u = begin_of(W, C, c);
-  if (m.b >= A.batch || u >= W) return;
+  if (m.b >= A.batch) return;
+  const Cut cut = m.cut;
+  const long long u = cut.begin(c);
   const Sequence q = sequence(A, m.b);
-  const int item = static_cast<int>(m.off / q.tiles), into = static_cast<int>(m.off - static_cast<long long>(item) * q.tiles);
+  const int item = Cut::divide(m.off, q.tiles), into = static_cast<int>(m.off - static_cast<long long>(item) * q.tiles);
   const long long a = u - into;
-  if (into == 0 || begin_of(W, C, c - 1) > a) return;  // no item is cut here, or it was cut before
-  const int first = owner_of(W, C, a), last = owner_of(W, C, a + q.tiles - 1);
+  if (into == 0 || cut.begin(c - 1) > a) return;  // no item is cut here, or it was cut before
+  const int first = c - 1, last = cut.owner(a + q.tiles - 1);
   const int head = item / q.items, pair = item % q.items;
   // a thread has kCols columns of a row
   constexpr int kPer = kFinishThreads / kFinishRows, kCols = DP / kPer;
@@ -967,19 +1043,17 @@ __global__ void __launch_bounds__(kFinishThreads) finish_kernel(const __grid_con
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (bad || !mine) return;
   // the first part is the last segment of its CTA, the others are their CTAs' first
-  auto slot = [&](int x) { return 2 * x + (x == first && begin_of(W, C, x) < a ? 1 : 0); };
-  auto live = [&](int x) { return begin_of(W, C, x + 1) > begin_of(W, C, x); };
-  float top = -INFINITY;
-  for (int x = first; x <= last; ++x)
-    if (live(x)) top = fmaxf(top, A.part_ml[slot(x) * 256 + r].x);
+  const long long slot0 = 2LL * first + (cut.begin(first) < a ? 1 : 0);
+  const long long rest = 2LL * first;  // slot of CTA x: rest + 2 (x - first)
+  float top = A.part_ml[slot0 * 256 + r].x;
+#pragma unroll 8
+  for (int x = 1; x <= last - first; ++x) top = fmaxf(top, A.part_ml[(rest + 2 * x) * 256 + r].x);
   float sum = 0, o[kCols] = {};
-#pragma unroll 4
-  for (int x = first; x <= last; ++x) {
-    if (!live(x)) continue;
-    const float2 ml = A.part_ml[slot(x) * 256 + r];
+  auto add = [&](long long slot) {
+    const float2 ml = A.part_ml[slot * 256 + r];
     const float f = ml.x == -INFINITY ? 0.0f : svk::ex2_ftz(ml.x - top);
     sum += ml.y * f;
-    const float* p = A.part + (static_cast<long long>(slot(x)) * 256 + r) * DP + col;
+    const float* p = A.part + (slot * 256 + r) * DP + col;
 #pragma unroll
     for (int j = 0; j < kCols; j += 4) {
       const float4 v = *reinterpret_cast<const float4*>(p + j);
@@ -988,7 +1062,10 @@ __global__ void __launch_bounds__(kFinishThreads) finish_kernel(const __grid_con
       o[j + 2] += v.z * f;
       o[j + 3] += v.w * f;
     }
-  }
+  };
+  add(slot0);
+#pragma unroll 4
+  for (int x = 1; x <= last - first; ++x) add(rest + 2 * x);
   const float inv = 1.0f / sum;
   const int qh = head * A.G + rr % A.G;
   const long long at = static_cast<long long>(q.first) + node;
@@ -1042,11 +1119,13 @@ sv_status launch(const sv_tree_attn& a, float scale, unsigned char* ws, cudaStre
   Args A;
   A.G = static_cast<int>(a.q_heads / a.kv_heads);
   A.per_tile = kTile / A.G;
+  A.per_pair_inv = static_cast<uint32_t>((1ULL << 32) / (2 * A.per_tile) + 1);
   A.Hkv = static_cast<int>(a.kv_heads);
   A.D = static_cast<int>(a.dim);
   A.page = static_cast<int>(a.page_size);
   A.box = 8;
-  while (A.box < kTile && A.page % (2 * A.box) == 0) A.box *= 2;
+  A.box_shift = 3;
+  while (A.box < kTile && A.page % (2 * A.box) == 0) A.box *= 2, ++A.box_shift;
   A.tree_box = 8;
   while (A.tree_box < kTile && A.tree_box < a.n) A.tree_box *= 2;
   A.batch = static_cast<int>(a.batch);
