@@ -352,6 +352,25 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* v) {
       : "r"(taddr)
       : "memory");
 }
+// 128 of them: four loads in flight, one wait.
+__device__ __forceinline__ void tmem_ld32_issue(uint32_t taddr, uint32_t* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, "
+      "%13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : SVA_R8(v, 0), SVA_R8(v, 8), SVA_R8(v, 16), SVA_R8(v, 24)
+      : "r"(taddr)
+      : "memory");
+}
+#define SVA_RW8(v, i) "+r"(v[i]), "+r"(v[i + 1]), "+r"(v[i + 2]), "+r"(v[i + 3]), "+r"(v[i + 4]), "+r"(v[i + 5]), "+r"(v[i + 6]), "+r"(v[i + 7])
+__device__ __forceinline__ void tmem_ld32_wait(uint32_t* v) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : SVA_RW8(v, 0), SVA_RW8(v, 8), SVA_RW8(v, 16), SVA_RW8(v, 24)::"memory");
+}
+__device__ __forceinline__ void tmem_ld128(uint32_t taddr, uint32_t* v) {
+#pragma unroll
+  for (int i = 0; i < 128; i += 32) tmem_ld32_issue(taddr + i, v + i);
+#pragma unroll
+  for (int i = 0; i < 128; i += 32) tmem_ld32_wait(v + i);
+}
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* v) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, "
@@ -622,6 +641,62 @@ __device__ __forceinline__ void issue(const Args& A, Shared& sm, uint32_t q_smem
   bool alive = scores() && scores();
   uint32_t segments = 0;
   while (alive && pv.ok) {
+    // inside a segment, whole tiles of the cache: nothing to look up between the steps
+    if (pv.k >= 2 && !(pv.k & 1) && qk.ok && qk.w.count == pv.w.count) {
+      const int stride = pv.s.two ? 2 : 1;  // steps per key tile
+      // (the last scores against a query tile also give it back)
+      const int to_last = pv.s.steps - stride - 2 - pv.k, to_part = (pv.s.q.len / kTile - pv.s.t0) * stride - pv.k;
+      const int n = (to_last < to_part ? to_last : to_part) & ~1;
+      if (n > 0) {
+        const bool two = pv.s.two;
+        const uint32_t qa = q_lo + (q_first & 1) * kUnits, qb = two ? q_lo + ((q_first + 1) & 1) * kUnits : qa;
+        const uint32_t st = gp & 1;
+        const uint32_t s0 = tmem + st * kTile, s1 = tmem + (st ^ 1) * kTile;
+        const uint32_t o0 = tmem + 256 + st * 128, o1 = tmem + 256 + (st ^ 1) * 128;
+        uint64_t *const p0 = &sm.p_full[st], *const p1 = &sm.p_full[st ^ 1], *const f0 = &sm.s_full[st], *const f1 = &sm.s_full[st ^ 1];
+        auto both = [&](uint64_t* p_bar, uint32_t parity, uint32_t s, uint32_t o, uint32_t q, uint64_t* f, bool fresh, bool last) {
+          bool ok = !fresh || wait(sm, &sm.v_full[v_slot], v_turn & 1);
+          ok = wait(sm, p_bar, parity) && ok;
+          if (fresh) ok = wait(sm, &sm.k_full[k_slot], k_turn & 1) && ok;
+          ok = __all_sync(0xFFFFFFFFu, ok);
+          fence_after();
+          const uint32_t v = v_lo + v_slot * kUnits, k = k_lo + k_slot * kUnits;
+          if (leads && ok) {
+#pragma unroll
+            for (int i = 0; i < kTile / 16; ++i) mma_ts(o, s + i * 8, full(v + i * 128), idesc<T>(DP, true), 1u);
+            if (last) mma_commit(&sm.v_empty[v_slot]);
+#pragma unroll
+            for (int i = 0; i < DP / 16; ++i) {
+              const uint32_t at = (i / 4) * (kTile * 128 / 16) + (i % 4) * 2;
+              mma_ss(s, full(q + at), full(k + at), idesc<T>(kTile, false), i > 0);
+            }
+            mma_commit(f);
+            if (last) mma_commit(&sm.k_empty[k_slot]);
+          }
+          __syncwarp();
+          if (last) {
+            if (++v_slot == v_slots(DP)) v_slot = 0, ++v_turn;
+            if (++k_slot == k_slots(DP)) k_slot = 0, ++k_turn;
+          }
+          return ok;
+        };
+        uint32_t parity = (gp >> 1) & 1, parity1 = ((gp + 1) >> 1) & 1;
+        if (two) {
+          for (int i = 0; alive && i < n; i += 2) {
+            alive = both(p0, parity, s0, o0, qa, f0, true, false) && both(p1, parity1, s1, o1, qb, f1, false, true);
+            parity ^= 1, parity1 ^= 1;
+          }
+        } else {
+          for (int i = 0; alive && i < n; i += 2) {
+            alive = both(p0, parity, s0, o0, qa, f0, true, true) && both(p1, parity1, s1, o1, qa, f1, true, true);
+            parity ^= 1, parity1 ^= 1;
+          }
+        }
+        gp += n, gq += n;
+        pv.k += n, qk.k += n;
+        if (!alive) break;
+      }
+    }
     const uint32_t st = gp & 1;
     if (pv.k == 0) {  // the outputs of the segment before have been read
       if (segments && !warp_wait(sm, &sm.o_empty, (segments - 1) & 1)) break;
@@ -735,35 +810,29 @@ __device__ __forceinline__ void soften(const Args& A, Shared& sm, uint32_t tmem,
             bits[i] = n >= 32 ? 0xFFFFFFFFu : n > 0 ? (1u << n) - 1u : 0u;
           }
         }
-        // 32 scores, those that the row does not see -inf
-        auto scores = [&](int i, uint32_t bit, float (&x)[32]) {
-          uint32_t u[32];
-          tmem_ld32(s_col + i * 32, u);
-          if (A.flip) {
+        uint32_t u[kTile];
+        tmem_ld128(s_col, u);
+        if (A.flip) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) u[j] ^= 0x80000000u;
-          }
-          if (masked) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (!(bit >> j & 1)) u[j] = 0xFF800000u;
-          }
-#pragma unroll
-          for (int j = 0; j < 32; ++j) x[j] = __uint_as_float(u[j]);
-        };
-        float top = -INFINITY;
-#pragma unroll 1
-        for (int i = 0; i < 4; ++i) {
-          float x[32];
-          scores(i, i == 0 ? bits[0] : i == 1 ? bits[1] : i == 2 ? bits[2] : bits[3], x);
-          float m0 = max3(top, x[0], x[1]), m1 = max3(x[2], x[3], x[4]);
-#pragma unroll
-          for (int j = 5; j < 29; j += 4) {
-            m0 = max3(m0, x[j], x[j + 1]);
-            m1 = max3(m1, x[j + 2], x[j + 3]);
-          }
-          top = max3(max3(m0, x[29], x[30]), m1, x[31]);
+          for (int j = 0; j < kTile; ++j) u[j] ^= 0x80000000u;
         }
+        if (masked) {
+#pragma unroll
+          for (int j = 0; j < kTile; ++j)
+            if (!(bits[j / 32] >> (j % 32) & 1)) u[j] = 0xFF800000u;
+        }
+        float* x = reinterpret_cast<float*>(u);
+        float m0 = x[0], m1 = x[1], m2 = x[2], m3 = x[3];
+#pragma unroll
+        for (int j = 4; j < kTile - 4; j += 8) {
+          m0 = max3(m0, x[j], x[j + 1]);
+          m1 = max3(m1, x[j + 2], x[j + 3]);
+          m2 = max3(m2, x[j + 4], x[j + 5]);
+          m3 = max3(m3, x[j + 6], x[j + 7]);
+        }
+        m0 = max3(m0, x[kTile - 4], x[kTile - 3]);
+        m1 = max3(m1, x[kTile - 2], x[kTile - 1]);
+        float top = max3(fmaxf(m0, m1), m2, m3);
         top *= c2;
         const bool move = top > ref + kSlack || (ref == -INFINITY && top > -INFINITY);
         if (__any_sync(0xFFFFFFFFu, move)) {
@@ -784,21 +853,19 @@ __device__ __forceinline__ void soften(const Args& A, Shared& sm, uint32_t tmem,
         }
         const float minus = ref == -INFINITY ? 0.0f : -ref;
         float a0 = 0, a1 = 0, b0 = 0, b1 = 0;
-#pragma unroll 1
+#pragma unroll
         for (int i = 0; i < 4; ++i) {
-          float x[32];
-          scores(i, i == 0 ? bits[0] : i == 1 ? bits[1] : i == 2 ? bits[2] : bits[3], x);
           uint32_t p[16];
 #pragma unroll
-          for (int j = 0; j < 32; j += 4) {
+          for (int j = i * 32; j < i * 32 + 32; j += 4) {
             fma2(x[j], x[j + 1], c2, minus);
             fma2(x[j + 2], x[j + 3], c2, minus);
 #pragma unroll
             for (int e = 0; e < 4; ++e) x[j + e] = svk::ex2_ftz(x[j + e]);
             add2(a0, a1, x[j], x[j + 1]);
             add2(b0, b1, x[j + 2], x[j + 3]);
-            p[j / 2] = Num<T>::pack(x[j], x[j + 1]);
-            p[j / 2 + 1] = Num<T>::pack(x[j + 2], x[j + 3]);
+            p[(j - i * 32) / 2] = Num<T>::pack(x[j], x[j + 1]);
+            p[(j - i * 32) / 2 + 1] = Num<T>::pack(x[j + 2], x[j + 3]);
           }
           tmem_st16(s_col + i * 16, p);  // (over scores that have been read)
         }
