@@ -94,7 +94,7 @@ struct Args {
   int q_heads;
   float c;          // scale in powers of two, not negative
   bool flip;        // the scores' sign is turned (a negative scale)
-  float* part;      // [2 CTAs][256][dp]
+  float* part;      // [2 CTAs][dp / 4][256 rows][4]: a warp, a row per lane, writes and reads whole lines
   float2* part_ml;  // [2 CTAs][256]: maximum (powers of two), sum
   unsigned* err;    // [CTAs]
   unsigned* status;
@@ -155,12 +155,13 @@ struct PlanMem {
   int b;
 };
 
-// All of a CTA's T threads: the cut, and the sequence that CTA c's first unit
-// lies in, with the units before it there.
+// All of a CTA's T threads: the cut of the units over C CTAs, and where CTA c's
+// first unit lies (sequence m.b, m.off units into it); with `of_sequence`, m.off
+// is the units before sequence c instead.
 template <int T>
-__device__ __forceinline__ void make_plan(const Args& A, int C, int c, PlanMem& m) {
+__device__ __forceinline__ void make_plan(const Args& A, int C, int c, bool of_sequence, PlanMem& m) {
   const int t = static_cast<int>(threadIdx.x), lane = t & 31, warp = t >> 5;
-  const int per = (A.batch + T - 1) / T;
+  const int per = A.batch <= T ? 1 : (A.batch + T - 1) / T;
   const int lo = t * per < A.batch ? t * per : A.batch, hi = lo + per < A.batch ? lo + per : A.batch;
   long long mine = 0;
   for (int b = lo; b < hi; ++b) mine += units_of(A, sequence(A, b));
@@ -179,16 +180,16 @@ __device__ __forceinline__ void make_plan(const Args& A, int C, int c, PlanMem& 
     W += m.warp_sums[w];
   }
   Cut cut;
-  cut.each = Cut::divide(W, C);
+  cut.each = W < C ? 0 : Cut::divide(W, C);
   cut.more = static_cast<int>(W - cut.each * C);
   const long long u = cut.begin(c);
   if (t == 0) m.cut = cut;
-  if (u >= before && u < before + mine)
+  if (of_sequence ? c >= lo && c < hi : u >= before && u < before + mine)
     for (int b = lo; b < hi; ++b) {
-      const long long k = units_of(A, sequence(A, b));
-      if (u < before + k) {
+      const long long k = per == 1 ? mine : units_of(A, sequence(A, b));
+      if (of_sequence ? b == c : u < before + k) {
         m.b = b;
-        m.off = u - before;
+        m.off = of_sequence ? before : u - before;
         break;
       }
       before += k;
@@ -901,7 +902,7 @@ __device__ __forceinline__ void soften(const Args& A, Shared& sm, uint32_t tmem,
     const long long at = static_cast<long long>(s.q.first) + node;
     const int qh = s.head * A.G + row % A.G;
     const int slot = 2 * c + (w.count > 1 ? 1 : 0);
-    float* part = A.part + (static_cast<long long>(slot) * 256 + (s.two ? k0 * kTile : 0) + row) * DP;
+    float* part = A.part + static_cast<long long>(slot) * 256 * DP + ((s.two ? k0 * kTile : 0) + row) * 4;
     const float inv = sum > 0 || sum != sum ? 1.0f / sum : 0.0f;
     uint32_t odd_any = 0;
 #pragma unroll
@@ -947,7 +948,7 @@ __device__ __forceinline__ void soften(const Args& A, Shared& sm, uint32_t tmem,
         } else if (mine) {
 #pragma unroll
           for (int j = 0; j < 32; j += 4)
-            *reinterpret_cast<float4*>(part + col + j) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+            *reinterpret_cast<float4*>(part + (col + j) * 256) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
         }
       }
     }
@@ -1008,7 +1009,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   fence_before();
-  make_plan<kThreads>(A, C, c, sm.plan);  // (two barriers of the CTA)
+  make_plan<kThreads>(A, C, c, false, sm.plan);  // (two barriers of the CTA)
   fence_after();
   const uint32_t tmem = sm.tmem;
   if (warp >= kSoftWarps) {
@@ -1059,8 +1060,12 @@ __device__ __forceinline__ bool bad_layout(const Args& A, int b, int t, int T) {
 }
 
 // Joins the parts of items that several CTAs had, and writes the statuses.
+// A joining CTA has 32 rows and 8 kJoinCols columns of an item: the item's
+// number says which where there are no more items than cuts (`items` per
+// sequence), else the cut.
+constexpr int kJoinCols = 8;
 template <typename T, int DP>
-__global__ void __launch_bounds__(kFinishThreads) finish_kernel(const __grid_constant__ Args A, int C, int chunks, int join) {
+__global__ void __launch_bounds__(kFinishThreads) finish_kernel(const __grid_constant__ Args A, int C, int chunks, int join, int items) {
   __shared__ PlanMem m;
   const int t = static_cast<int>(threadIdx.x);
   if (static_cast<int>(blockIdx.x) >= join) {  // a warp per sequence
@@ -1088,42 +1093,55 @@ __global__ void __launch_bounds__(kFinishThreads) finish_kernel(const __grid_con
       }
     return;
   }
-  // the cut before CTA c, rows of chunk k
-  const int c = 1 + static_cast<int>(blockIdx.x) / chunks, k = static_cast<int>(blockIdx.x) % chunks;
-  make_plan<kFinishThreads>(A, C, c, m);
+  const int which = static_cast<int>(blockIdx.x) / chunks, k = static_cast<int>(blockIdx.x) % chunks;
+  constexpr int kColBlocks = DP / (8 * kJoinCols);  // CTAs for a row's columns
+  const int r = k / kColBlocks * kFinishRows + (t & 31);
+  const int col = (k % kColBlocks) * (8 * kJoinCols) + (t >> 5) * kJoinCols;
+  make_plan<kFinishThreads>(A, C, items ? which / items : which + 1, items > 0, m);
   if (m.b >= A.batch) return;
   const Cut cut = m.cut;
-  const long long u = cut.begin(c);
   const Sequence q = sequence(A, m.b);
-  const int item = Cut::divide(m.off, q.tiles), into = static_cast<int>(m.off - static_cast<long long>(item) * q.tiles);
-  const long long a = u - into;
-  if (into == 0 || cut.begin(c - 1) > a) return;  // no item is cut here, or it was cut before
-  const int first = c - 1, last = cut.owner(a + q.tiles - 1);
+  if (q.N <= 0) return;
+  int item, first;
+  long long a;  // the item's first unit
+  if (items) {
+    const int j = which % items, pairs = items / A.Hkv;
+    if (j % pairs >= q.items) return;
+    item = j / pairs * q.items + j % pairs;
+    a = m.off + static_cast<long long>(item) * q.tiles;
+    first = cut.owner(a);
+  } else {  // the cut before CTA which + 1
+    item = Cut::divide(m.off, q.tiles);
+    const int into = static_cast<int>(m.off - static_cast<long long>(item) * q.tiles);
+    a = cut.begin(which + 1) - into;
+    first = which;
+    if (into == 0 || cut.begin(first) > a) return;  // no item is cut here, or it was cut before
+  }
+  const int last = cut.owner(a + q.tiles - 1);
+  if (first == last) return;
   const int head = item / q.items, pair = item % q.items;
-  // a thread has kCols columns of a row
-  constexpr int kPer = kFinishThreads / kFinishRows, kCols = DP / kPer;
-  const int r = k * kFinishRows + t / kPer, col = t % kPer * kCols;
   const int query = 2 * pair + (r >= kTile ? 1 : 0), rr = r % kTile;
   const int node = query * A.per_tile + rr / A.G;
-  const bool mine = rr < A.per_tile * A.G && node < q.N;
+  const bool mine = rr < A.per_tile * A.G && node < q.N && col < A.D;
   const bool bad = __syncthreads_or(bad_layout(A, m.b, t, kFinishThreads));
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (bad || !mine) return;
   // the first part is the last segment of its CTA, the others are their CTAs' first
   const long long slot0 = 2LL * first + (cut.begin(first) < a ? 1 : 0);
-  const long long rest = 2LL * first;  // slot of CTA x: rest + 2 (x - first)
-  float top = A.part_ml[slot0 * 256 + r].x;
+  const int parts = last - first;
+  const float2* ml = A.part_ml + r;
+  const float* part = A.part + (col / 4 * 256 + r) * 4;
+  float top = ml[slot0 * 256].x;
 #pragma unroll 8
-  for (int x = 1; x <= last - first; ++x) top = fmaxf(top, A.part_ml[(rest + 2 * x) * 256 + r].x);
-  float sum = 0, o[kCols] = {};
+  for (int x = 1; x <= parts; ++x) top = fmaxf(top, ml[2LL * (first + x) * 256].x);
+  float sum = 0, o[kJoinCols] = {};
   auto add = [&](long long slot) {
-    const float2 ml = A.part_ml[slot * 256 + r];
-    const float f = ml.x == -INFINITY ? 0.0f : svk::ex2_ftz(ml.x - top);
-    sum += ml.y * f;
-    const float* p = A.part + (slot * 256 + r) * DP + col;
+    const float2 e = ml[slot * 256];
+    const float f = e.x == -INFINITY ? 0.0f : svk::ex2_ftz(e.x - top);
+    sum += e.y * f;
 #pragma unroll
-    for (int j = 0; j < kCols; j += 4) {
-      const float4 v = *reinterpret_cast<const float4*>(p + j);
+    for (int j = 0; j < kJoinCols; j += 4) {
+      const float4 v = *reinterpret_cast<const float4*>(part + slot * 256 * DP + j * 256);
       o[j] += v.x * f;
       o[j + 1] += v.y * f;
       o[j + 2] += v.z * f;
@@ -1131,15 +1149,14 @@ __global__ void __launch_bounds__(kFinishThreads) finish_kernel(const __grid_con
     }
   };
   add(slot0);
-#pragma unroll 4
-  for (int x = 1; x <= last - first; ++x) add(rest + 2 * x);
+#pragma unroll 8
+  for (int x = 1; x <= parts; ++x) add(2LL * (first + x));
   const float inv = 1.0f / sum;
   const int qh = head * A.G + rr % A.G;
   const long long at = static_cast<long long>(q.first) + node;
   T* dst = static_cast<T*>(A.out) + at * A.out_row + static_cast<long long>(qh) * A.out_head;
 #pragma unroll
-  for (int j = 0; j < kCols; j += 8)
-    if (col + j < A.D) store_out<T>(dst + col + j, o + j, inv);
+  for (int j = 0; j < kJoinCols; j += 8) store_out<T>(dst + col + j, o + j, inv);
   if (A.lse && col == 0) A.lse[at * A.q_heads + qh] = (top + log2f(sum)) * 0.69314718055994531f;
 }
 
@@ -1253,8 +1270,10 @@ sv_status launch(const sv_tree_attn& a, float scale, unsigned char* ws, cudaStre
   // rows of a pair of query tiles, the second's from kTile on
   const int most = static_cast<int>(a.n > A.per_tile ? kTile + (a.n - A.per_tile < A.per_tile ? a.n - A.per_tile : A.per_tile) * A.G
                                                      : a.n * A.G);
-  const int chunks = (most + kFinishRows - 1) / kFinishRows;
-  const int join = a.total > 0 ? (C - 1) * chunks : 0;
+  const int chunks = (most + kFinishRows - 1) / kFinishRows * (DP / (8 * kJoinCols));
+  const long long per_sequence = a.kv_heads * ((a.n + 2 * A.per_tile - 1) / (2 * A.per_tile));
+  const bool by_item = a.batch * per_sequence < C;
+  const int join = a.total > 0 ? static_cast<int>(by_item ? a.batch * per_sequence : C - 1) * chunks : 0;
   const int grid = join + static_cast<int>((a.batch + kFinishThreads / 32 - 1) / (kFinishThreads / 32));
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
@@ -1265,7 +1284,8 @@ sv_status launch(const sv_tree_attn& a, float scale, unsigned char* ws, cudaStre
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = a.total > 0 ? 1 : 0;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, finish_kernel<T, DP>, A, a.total > 0 ? C : 0, chunks, join);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, finish_kernel<T, DP>, A, a.total > 0 ? C : 0, chunks, join,
+                                           by_item ? static_cast<int>(per_sequence) : 0);
   return e == cudaSuccess ? SV_OK : svh::fail(SV_ERR_CUDA, "kernel launch: %s", cudaGetErrorString(e));
 }
 
