@@ -75,8 +75,19 @@ __host__ __device__ constexpr int tile_bytes(int dp) { return kTile * dp * 2; }
 __host__ __device__ constexpr int k_slots(int dp) { return dp == 128 ? 3 : 5; }
 __host__ __device__ constexpr int v_slots(int dp) { return dp == 128 ? 2 : 5; }
 
+// What a CTA leaves for the second kernel: the item whose first part, but not
+// whole, it had.
+struct __align__(16) Join {
+  int parts;  // the CTAs behind it that have the others; 0: no such item
+  int slot;   // of its part
+  int b, head, pair;
+  int first, N;
+  unsigned err;  // a wait gave up
+};
+
 struct Args {
   int G, per_tile;  // query heads per key head; nodes per query tile
+  uint32_t G_inv;         // floor(2^32 / G) + 1: row / G is exact for the rows of a tile
   uint32_t per_pair_inv;  // ceil(2^32 / (nodes per pair of query tiles)): exact for as few nodes as there are
   int Hkv, D, page, box, tree_box;  // keys per box (a power of two), of the cache and of the nodes
   int box_shift;
@@ -96,7 +107,7 @@ struct Args {
   bool flip;        // the scores' sign is turned (a negative scale)
   float* part;      // [2 CTAs][dp / 4][256 rows][4]: a warp, a row per lane, writes and reads whole lines
   float2* part_ml;  // [2 CTAs][256]: maximum (powers of two), sum
-  unsigned* err;    // [CTAs]
+  struct Join* join;  // [CTAs]
   unsigned* status;
 };
 
@@ -125,6 +136,12 @@ __device__ __forceinline__ Sequence sequence(const Args& A, int b) {
   return s;
 }
 
+// Row r of a query tile is query head row_head of the tile's node row_node.
+__device__ __forceinline__ int row_node(const Args& A, int r) {
+  return A.G == 1 ? r : static_cast<int>(__umulhi(static_cast<uint32_t>(r), A.G_inv));
+}
+__device__ __forceinline__ int row_head(const Args& A, int r) { return r - row_node(A, r) * A.G; }
+
 __device__ __forceinline__ long long units_of(const Args& A, const Sequence& s) {
   return s.N > 0 ? static_cast<long long>(s.tiles) * s.items * A.Hkv : 0;
 }
@@ -148,55 +165,6 @@ struct Cut {
   }
 };
 
-struct PlanMem {
-  long long warp_sums[kThreads / 32];
-  long long off;
-  Cut cut;
-  int b;
-};
-
-// All of a CTA's T threads: the cut of the units over C CTAs, and where CTA c's
-// first unit lies (sequence m.b, m.off units into it); with `of_sequence`, m.off
-// is the units before sequence c instead.
-template <int T>
-__device__ __forceinline__ void make_plan(const Args& A, int C, int c, bool of_sequence, PlanMem& m) {
-  const int t = static_cast<int>(threadIdx.x), lane = t & 31, warp = t >> 5;
-  const int per = A.batch <= T ? 1 : (A.batch + T - 1) / T;
-  const int lo = t * per < A.batch ? t * per : A.batch, hi = lo + per < A.batch ? lo + per : A.batch;
-  long long mine = 0;
-  for (int b = lo; b < hi; ++b) mine += units_of(A, sequence(A, b));
-  long long x = mine;
-#pragma unroll
-  for (int d = 1; d < 32; d *= 2) {
-    const long long y = __shfl_up_sync(0xFFFFFFFFu, x, d);
-    if (lane >= d) x += y;
-  }
-  if (lane == 31) m.warp_sums[warp] = x;
-  if (t == 0) m.b = A.batch;
-  __syncthreads();
-  long long before = x - mine, W = 0;
-  for (int w = 0; w < T / 32; ++w) {
-    if (w < warp) before += m.warp_sums[w];
-    W += m.warp_sums[w];
-  }
-  Cut cut;
-  cut.each = W < C ? 0 : Cut::divide(W, C);
-  cut.more = static_cast<int>(W - cut.each * C);
-  const long long u = cut.begin(c);
-  if (t == 0) m.cut = cut;
-  if (of_sequence ? c >= lo && c < hi : u >= before && u < before + mine)
-    for (int b = lo; b < hi; ++b) {
-      const long long k = per == 1 ? mine : units_of(A, sequence(A, b));
-      if (of_sequence ? b == c : u < before + k) {
-        m.b = b;
-        m.off = of_sequence ? before : u - before;
-        break;
-      }
-      before += k;
-    }
-  __syncthreads();
-}
-
 // A run of key tiles of one item, on this CTA.
 struct Segment {
   Sequence q;
@@ -219,6 +187,11 @@ struct Walk {
       s.q = sequence(A, b);
       if (off < units_of(A, s.q)) break;
     }
+    cut(A, s);
+    return true;
+  }
+  // The next segment, in sequence s.q
+  __device__ __forceinline__ void cut(const Args& A, Segment& s) {
     const int item = off < s.q.tiles ? 0 : Cut::divide(off, s.q.tiles);
     s.b = b;
     s.t0 = static_cast<int>(off - static_cast<long long>(item) * s.q.tiles);
@@ -231,9 +204,74 @@ struct Walk {
     off += s.t1 - s.t0;
     left -= s.t1 - s.t0;
     ++count;
-    return true;
   }
 };
+
+struct PlanMem {
+  long long warp_sums[kThreads / 32];
+  Cut cut;
+  Walk w;     // after the CTA's first segment
+  Segment s;  // that
+  int any;    // there is one
+};
+
+// All of a CTA's threads: the cut of the units over C CTAs, and CTA c's first
+// segment.
+__device__ __forceinline__ void make_plan(const Args& A, int C, int c, PlanMem& m) {
+  constexpr int T = kThreads;
+  const int t = static_cast<int>(threadIdx.x), lane = t & 31, warp = t >> 5;
+  const int per = A.batch <= T ? 1 : (A.batch + T - 1) / T;
+  const int lo = t * per < A.batch ? t * per : A.batch, hi = lo + per < A.batch ? lo + per : A.batch;
+  long long mine = 0;
+  Sequence q{};
+  for (int b = lo; b < hi; ++b) {
+    q = sequence(A, b);
+    mine += units_of(A, q);
+  }
+  long long x = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const long long y = __shfl_up_sync(0xFFFFFFFFu, x, d);
+    if (lane >= d) x += y;
+  }
+  if (lane == 31) m.warp_sums[warp] = x;
+  if (t == 0) m.any = 0;
+  __syncthreads();
+  long long before = x - mine, W = 0;
+#pragma unroll
+  for (int w = 0; w < T / 32; ++w) {
+    const long long v = m.warp_sums[w];
+    if (w < warp) before += v;
+    W += v;
+  }
+  Cut cut;
+  cut.each = W < C ? 0 : Cut::divide(W, C);
+  cut.more = static_cast<int>(W - cut.each * C);
+  const long long u = cut.begin(c);
+  if (t == 0) m.cut = cut;
+  if (u >= before && u < before + mine && cut.count(c) > 0) {
+    int b = lo;
+    if (per > 1)
+      for (;; ++b) {
+        q = sequence(A, b);
+        const long long k = units_of(A, q);
+        if (u < before + k) break;
+        before += k;
+      }
+    Walk w;
+    Segment s;
+    w.b = b;
+    w.off = u - before;
+    w.left = cut.count(c);
+    w.count = 0;
+    s.q = q;
+    w.cut(A, s);
+    m.w = w;
+    m.s = s;
+    m.any = 1;
+  }
+  __syncthreads();
+}
 
 // Steps of a CTA one after another.
 struct Steps {
@@ -242,13 +280,11 @@ struct Steps {
   int k;   // step of the segment
   bool ok;
 
-  __device__ __forceinline__ void start(const Args& A, const PlanMem& m, int c) {
-    w.b = m.b;
-    w.off = m.off;
-    w.left = m.cut.count(c);
-    w.count = 0;
+  __device__ __forceinline__ void start(const PlanMem& m) {
+    w = m.w;
+    s = m.s;
     k = 0;
-    ok = w.next(A, s);
+    ok = m.any != 0;
   }
   __device__ __forceinline__ void advance(const Args& A) {
     if (++k == s.steps) {
@@ -408,7 +444,7 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 
 // ------------------------------------------------------------------ the kernel
 
-struct __align__(8) Shared {
+struct __align__(16) Shared {
   uint64_t k_full[5], k_empty[5];    // keys: producer -> MMA, MMA -> producer
   uint64_t v_full[5], v_empty[5];    // values: producer -> MMA and mender, both -> producer
   uint64_t v_mended[5];              // mender -> MMA
@@ -419,6 +455,7 @@ struct __align__(8) Shared {
   uint64_t done;                     // every MMA has completed
   uint32_t tmem;
   volatile int abort;
+  Join join;
   PlanMem plan;
   uint32_t v_odd[5][4];              // keys of a value tile of nodes whose values are no finite numbers
   uint32_t odd[8];                   // the segment's nodes with such values
@@ -452,15 +489,6 @@ __device__ __forceinline__ bool elected() {
   return p != 0;
 }
 
-__device__ __forceinline__ Walk walk_of(const PlanMem& m, int c) {
-  Walk w;
-  w.b = m.b;
-  w.off = m.off;
-  w.left = m.cut.count(c);
-  w.count = 0;
-  return w;
-}
-
 // Tile t of keys or values to shared memory at `dst`: every lane its boxes.
 template <int DP>
 __device__ __forceinline__ void load_tile(const Args& A, const Segment& s, int t, const CUtensorMap* cache,
@@ -487,15 +515,15 @@ __device__ __forceinline__ void load_tile(const Args& A, const Segment& s, int t
 
 // Queries and keys.
 template <int DP>
-__device__ __forceinline__ void produce_keys(const Args& A, Shared& sm, uint32_t q_smem, uint32_t ring, int c, const CUtensorMap* qm,
+__device__ __forceinline__ void produce_keys(const Args& A, Shared& sm, uint32_t q_smem, uint32_t ring, const CUtensorMap* qm,
                                              const CUtensorMap* km, const CUtensorMap* kcm) {
   constexpr int kPanels = DP / 64, kSlots = k_slots(DP);
   const int lane = static_cast<int>(threadIdx.x & 31);
-  Walk w = walk_of(sm.plan, c);
-  Segment s;
+  Walk w = sm.plan.w;
+  Segment s = sm.plan.s;
   uint32_t slot = 0, turn = 0, loads = 0, qs = 0;
   bool alive = true;
-  while (alive && w.next(A, s)) {
+  for (bool go = sm.plan.any; alive && go; go = w.next(A, s)) {
     for (int j = 0; alive && j < (s.two ? 2 : 1); ++j, ++qs) {
       const uint32_t buf = qs & 1;
       if (qs >= 2) alive = warp_wait(sm, &sm.q_empty[buf], ((qs >> 1) - 1) & 1);
@@ -520,15 +548,15 @@ __device__ __forceinline__ void produce_keys(const Args& A, Shared& sm, uint32_t
 }
 
 template <int DP>
-__device__ __forceinline__ void produce_values(const Args& A, Shared& sm, uint32_t ring, int c, const CUtensorMap* vm,
+__device__ __forceinline__ void produce_values(const Args& A, Shared& sm, uint32_t ring, const CUtensorMap* vm,
                                                const CUtensorMap* vcm) {
   constexpr int kSlots = v_slots(DP);
   const int lane = static_cast<int>(threadIdx.x & 31);
-  Walk w = walk_of(sm.plan, c);
-  Segment s;
+  Walk w = sm.plan.w;
+  Segment s = sm.plan.s;
   uint32_t slot = 0, turn = 0, loads = 0;
   bool alive = true;
-  while (alive && w.next(A, s))
+  for (bool go = sm.plan.any; alive && go; go = w.next(A, s))
     for (int t = s.t0; alive && t < s.t1; ++t) {
       if (turn) alive = warp_wait(sm, &sm.v_empty[slot], (turn - 1) & 1);
       if (!alive) break;
@@ -543,14 +571,14 @@ __device__ __forceinline__ void produce_values(const Args& A, Shared& sm, uint32
 __device__ __forceinline__ bool mends(const Segment& s, int t, int keys) { return t >= s.q.cached || keys % 16; }
 
 template <typename T, int DP>
-__device__ __forceinline__ void mend(const Args& A, Shared& sm, unsigned char* ring, int c) {
+__device__ __forceinline__ void mend(const Args& A, Shared& sm, unsigned char* ring) {
   constexpr int kPanels = DP / 64, kSlots = v_slots(DP);
   const int lane = static_cast<int>(threadIdx.x & 31);
-  Walk w = walk_of(sm.plan, c);
-  Segment s;
+  Walk w = sm.plan.w;
+  Segment s = sm.plan.s;
   uint32_t slot = 0, turn = 0;
   bool alive = true;
-  while (alive && w.next(A, s)) {
+  for (bool go = sm.plan.any; alive && go; go = w.next(A, s)) {
     for (int t = s.t0; alive && t < s.t1; ++t) {
       alive = warp_wait(sm, &sm.v_full[slot], turn & 1);
       if (!alive) break;
@@ -596,7 +624,7 @@ __device__ __forceinline__ void mend(const Args& A, Shared& sm, unsigned char* r
 }
 
 template <typename T, int DP>
-__device__ __forceinline__ void issue(const Args& A, Shared& sm, uint32_t q_smem, uint32_t k_ring, uint32_t v_ring, uint32_t tmem, int c) {
+__device__ __forceinline__ void issue(const Args& A, Shared& sm, uint32_t q_smem, uint32_t k_ring, uint32_t v_ring, uint32_t tmem) {
   constexpr uint32_t kUnits = tile_bytes(DP) / 16;  // of the descriptors' addresses
   constexpr uint32_t kHi = (1024u >> 4) | 1u << 14 | 2u << 29;
   const bool leads = elected();
@@ -606,7 +634,7 @@ __device__ __forceinline__ void issue(const Args& A, Shared& sm, uint32_t q_smem
   const uint32_t v_lo = ((v_ring & 0x3FFFFu) >> 4) | (kTile * 128 / 16) << 16;
   auto full = [](uint32_t lo) { return static_cast<uint64_t>(kHi) << 32 | lo; };
   Steps qk, pv;
-  qk.start(A, sm.plan, c);
+  qk.start(sm.plan);
   pv = qk;
   uint32_t k_slot = 0, k_turn = 0, v_slot = 0, v_turn = 0, qs = 0, q_first = 0, gq = 0, gp = 0;
   auto scores = [&]() {
@@ -778,20 +806,20 @@ __device__ __forceinline__ void soften(const Args& A, Shared& sm, uint32_t tmem,
   const int stream = warp >> 2, row = (warp & 3) * 32 + lane;
   const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
   const uint32_t s_col = tmem + lanes + stream * kTile, o_col = tmem + lanes + 256;
-  Walk w = walk_of(sm.plan, c);
+  Walk w = sm.plan.w;
   uint32_t g = 0;          // steps before the segment, both streams
   uint32_t turns = 0;      // of this stream
   // (a scale of 0 as one that makes every finite score 0 too, and -inf still -inf)
   const float c2 = A.c > 0 ? A.c : 1e-45f;
   bool alive = true;
-  Segment s;
-  while (w.next(A, s)) {
+  Segment s = sm.plan.s;
+  for (bool go = sm.plan.any; go; go = w.next(A, s)) {
     // this stream's steps of the segment: k = k0, k0 + 2, ...
     const int k0 = static_cast<int>((stream ^ g) & 1);
     const int query = 2 * s.pair + (s.two ? k0 : 0);
     const int rows = (s.q.N - query * A.per_tile < A.per_tile ? s.q.N - query * A.per_tile : A.per_tile) * A.G;
     const bool busy = (warp & 3) * 32 < rows;  // the warp has a row
-    const int node = query * A.per_tile + row / A.G;
+    const int node = query * A.per_tile + row_node(A, row);
     float ref = -INFINITY, sum = 0;
     for (int k = k0; k < s.steps; k += 2) {
       const int t = s.t0 + (s.two ? k >> 1 : k);
@@ -900,7 +928,7 @@ __device__ __forceinline__ void soften(const Args& A, Shared& sm, uint32_t tmem,
     const int begin = s.two ? 0 : stream * (DP / 2), width = s.two ? DP : DP / 2;
     const bool mine = alive && busy && row < rows;
     const long long at = static_cast<long long>(s.q.first) + node;
-    const int qh = s.head * A.G + row % A.G;
+    const int qh = s.head * A.G + row_head(A, row);
     const int slot = 2 * c + (w.count > 1 ? 1 : 0);
     float* part = A.part + static_cast<long long>(slot) * 256 * DP + ((s.two ? k0 * kTile : 0) + row) * 4;
     const float inv = sum > 0 || sum != sum ? 1.0f / sum : 0.0f;
@@ -952,6 +980,18 @@ __device__ __forceinline__ void soften(const Args& A, Shared& sm, uint32_t tmem,
         }
       }
     }
+    if (!s.whole && s.t0 == 0 && threadIdx.x == 0) {
+      Join j;
+      j.parts = sm.plan.cut.owner(sm.plan.cut.begin(c + 1) + s.q.tiles - s.t1 - 1) - c;
+      j.slot = slot;
+      j.b = s.b;
+      j.head = s.head;
+      j.pair = s.pair;
+      j.first = s.q.first;
+      j.N = s.q.N;
+      j.err = 0;
+      sm.join = j;
+    }
     if (mine && (s.two || stream == 0)) {
       if (!s.whole)
         A.part_ml[slot * 256 + (s.two ? k0 * kTile : 0) + row] = make_float2(ref, sum);
@@ -973,7 +1013,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* base = smem_raw;  // (the swizzle wants 1024 bytes, and there is no room to move up)
   if (smem_u32(base) & 1023) {
-    if (threadIdx.x == 0) A.err[blockIdx.x] = 1u;
+    if (threadIdx.x == 0) A.join[blockIdx.x].parts = 0, A.join[blockIdx.x].err = 1u;
     return;
   }
   unsigned char* v_ptr = base + (2 + k_slots(DP)) * tile_bytes(DP);
@@ -1002,26 +1042,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&sm.o_empty, kSoftWarps);
     mbar_init(&sm.done, 1);
     sm.abort = 0;
+    sm.join.parts = 0;
     svk::fence_mbar_init_cluster();
   }
+  if (warp == 8 && (threadIdx.x & 31) == 0)
+    for (const CUtensorMap* m : {&qm, &km, &vm, &kcm, &vcm}) asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
   if (warp == 9) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sm.tmem)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   fence_before();
-  make_plan<kThreads>(A, C, c, false, sm.plan);  // (two barriers of the CTA)
+  make_plan(A, C, c, sm.plan);  // (two barriers of the CTA)
   fence_after();
   const uint32_t tmem = sm.tmem;
   if (warp >= kSoftWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == 8)
-      produce_keys<DP>(A, sm, q_smem, k_ring, c, &qm, &km, &kcm);
+      produce_keys<DP>(A, sm, q_smem, k_ring, &qm, &km, &kcm);
     else if (warp == 9)
-      issue<T, DP>(A, sm, q_smem, k_ring, v_ring, tmem, c);
+      issue<T, DP>(A, sm, q_smem, k_ring, v_ring, tmem);
     else if (warp == 10)
-      mend<T, DP>(A, sm, v_ptr, c);
+      mend<T, DP>(A, sm, v_ptr);
     else
-      produce_values<DP>(A, sm, v_ring, c, &vm, &vcm);
+      produce_values<DP>(A, sm, v_ring, &vm, &vcm);
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
     soften<T, DP>(A, sm, tmem, c);
@@ -1032,10 +1075,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
   }
-  if (threadIdx.x == 0) A.err[c] = sm.abort ? 1u : 0u;
+  if (threadIdx.x == 0) {
+    Join j = sm.join;
+    j.err = sm.abort ? 1u : 0u;
+    A.join[c] = j;
+  }
 }
 
-// Whether sequence b's layout is bad, by a CTA's threads t, t + T, ...
+// Whether what thread t of T looks at of sequence b's layout is bad.
 __device__ __forceinline__ bool bad_layout(const Args& A, int b, int t, int T) {
   int first = b * A.n, N = A.n;
   if (A.cu) {
@@ -1046,37 +1093,34 @@ __device__ __forceinline__ bool bad_layout(const Args& A, int b, int t, int T) {
   }
   const int len = A.lengths[b];
   if (len < 0 || len > A.max_pages * A.page) return true;
+  const int used = (len + A.page - 1) / A.page;
+  const int* row = A.table + b * A.table_stride;
   bool bad = false;
-  for (int j = t; j < (len + A.page - 1) / A.page; j += T) {
-    const int p = A.table[b * A.table_stride + j];
-    bad = bad || p < 0 || p >= A.pages;
+#pragma unroll 8
+  for (int j = t; j < used; j += T) {
+    const int p = row[j];
+    bad |= p < 0 || p >= A.pages;
   }
-  if (A.parents)
-    for (int j = t; j < N; j += T) {
-      const int p = A.parents[first + j];
-      bad = bad || p < -1 || p >= j;
-    }
+  if (A.parents && t < N) {  // (T is not less than the most nodes)
+    const int p = A.parents[first + t];
+    bad |= p < -1 || p >= t;
+  }
   return bad;
 }
+static_assert(kFinishThreads >= SV_TREE_MAX_NODES, "a thread per node");
 
-// Joins the parts of items that several CTAs had, and writes the statuses.
-// A joining CTA has 32 rows and 8 kJoinCols columns of an item: the item's
-// number says which where there are no more items than cuts (`items` per
-// sequence), else the cut.
-constexpr int kJoinCols = 8;
+// Joins the parts of items that several CTAs had, 32 rows and 64 columns to a
+// CTA, and writes the statuses.
+constexpr int kJoinCols = 8;  // columns of a thread; a lane per row
 template <typename T, int DP>
-__global__ void __launch_bounds__(kFinishThreads) finish_kernel(const __grid_constant__ Args A, int C, int chunks, int join, int items) {
-  __shared__ PlanMem m;
+__global__ void __launch_bounds__(kFinishThreads) finish_kernel(const __grid_constant__ Args A, int C, int chunks) {
   const int t = static_cast<int>(threadIdx.x);
-  if (static_cast<int>(blockIdx.x) >= join) {  // a warp per sequence
-    const int b = (static_cast<int>(blockIdx.x) - join) * (kFinishThreads / 32) + t / 32, lane = t & 31;
-    if (b >= A.batch) return;
-    const bool bad = __any_sync(0xFFFFFFFFu, bad_layout(A, b, lane, 32));
+  if (static_cast<int>(blockIdx.x) < A.batch) {  // a sequence's status
+    const int b = static_cast<int>(blockIdx.x);
+    const bool bad = __syncthreads_or(bad_layout(A, b, t, kFinishThreads));
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    unsigned late = 0;
-    for (int i = lane; i < C; i += 32) late |= A.err[i];
-    late = __any_sync(0xFFFFFFFFu, late != 0);
-    if (lane == 0) A.status[b] = (bad ? SV_SEQ_BAD_LAYOUT : 0u) | (late ? SV_SEQ_TIMEOUT : 0u);
+    const bool late = __syncthreads_or(t < C && A.join[t].err != 0);
+    if (t == 0) A.status[b] = (bad ? SV_SEQ_BAD_LAYOUT : 0u) | (late ? SV_SEQ_TIMEOUT : 0u);
     if (!bad) return;
     int first = b * A.n, N = A.n;
     if (A.cu) {
@@ -1085,79 +1129,74 @@ __global__ void __launch_bounds__(kFinishThreads) finish_kernel(const __grid_con
       N = end - first;
       if (first < 0 || end < first || end > A.total || N > A.n) return;
     }
-    for (int r = 0; r < N; ++r)
-      for (int h = 0; h < A.q_heads; ++h) {
-        T* o = static_cast<T*>(A.out) + static_cast<long long>(first + r) * A.out_row + static_cast<long long>(h) * A.out_head;
-        for (int d = lane; d < A.D / 8; d += 32) *reinterpret_cast<uint4*>(o + 8 * d) = make_uint4(0, 0, 0, 0);
-        if (A.lse && lane == 0) A.lse[static_cast<long long>(first + r) * A.q_heads + h] = -INFINITY;
-      }
+    for (int i = t / 16; i < N * A.q_heads; i += kFinishThreads / 16) {
+      const int r = i / A.q_heads, h = i % A.q_heads, d = t % 16;
+      T* o = static_cast<T*>(A.out) + static_cast<long long>(first + r) * A.out_row + static_cast<long long>(h) * A.out_head;
+      if (8 * d < A.D) *reinterpret_cast<uint4*>(o + 8 * d) = make_uint4(0, 0, 0, 0);
+      if (A.lse && d == 0) A.lse[static_cast<long long>(first + r) * A.q_heads + h] = -INFINITY;
+    }
     return;
   }
-  const int which = static_cast<int>(blockIdx.x) / chunks, k = static_cast<int>(blockIdx.x) % chunks;
-  constexpr int kColBlocks = DP / (8 * kJoinCols);  // CTAs for a row's columns
+  const int id = static_cast<int>(blockIdx.x) - A.batch, c = id / chunks, k = id % chunks;
+  constexpr int kColBlocks = DP / (8 * kJoinCols);  // chunks of a row's columns
   const int r = k / kColBlocks * kFinishRows + (t & 31);
   const int col = (k % kColBlocks) * (8 * kJoinCols) + (t >> 5) * kJoinCols;
-  make_plan<kFinishThreads>(A, C, items ? which / items : which + 1, items > 0, m);
-  if (m.b >= A.batch) return;
-  const Cut cut = m.cut;
-  const Sequence q = sequence(A, m.b);
-  if (q.N <= 0) return;
-  int item, first;
-  long long a;  // the item's first unit
-  if (items) {
-    const int j = which % items, pairs = items / A.Hkv;
-    if (j % pairs >= q.items) return;
-    item = j / pairs * q.items + j % pairs;
-    a = m.off + static_cast<long long>(item) * q.tiles;
-    first = cut.owner(a);
-  } else {  // the cut before CTA which + 1
-    item = Cut::divide(m.off, q.tiles);
-    const int into = static_cast<int>(m.off - static_cast<long long>(item) * q.tiles);
-    a = cut.begin(which + 1) - into;
-    first = which;
-    if (into == 0 || cut.begin(first) > a) return;  // no item is cut here, or it was cut before
-  }
-  const int last = cut.owner(a + q.tiles - 1);
-  if (first == last) return;
-  const int head = item / q.items, pair = item % q.items;
-  const int query = 2 * pair + (r >= kTile ? 1 : 0), rr = r % kTile;
-  const int node = query * A.per_tile + rr / A.G;
-  const bool mine = rr < A.per_tile * A.G && node < q.N && col < A.D;
-  const bool bad = __syncthreads_or(bad_layout(A, m.b, t, kFinishThreads));
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (bad || !mine) return;
-  // the first part is the last segment of its CTA, the others are their CTAs' first
-  const long long slot0 = 2LL * first + (cut.begin(first) < a ? 1 : 0);
-  const int parts = last - first;
-  const float2* ml = A.part_ml + r;
-  const float* part = A.part + (col / 4 * 256 + r) * 4;
-  float top = ml[slot0 * 256].x;
-#pragma unroll 8
-  for (int x = 1; x <= parts; ++x) top = fmaxf(top, ml[2LL * (first + x) * 256].x);
-  float sum = 0, o[kJoinCols] = {};
-  auto add = [&](long long slot) {
-    const float2 e = ml[slot * 256];
-    const float f = e.x == -INFINITY ? 0.0f : svk::ex2_ftz(e.x - top);
-    sum += e.y * f;
+  const Join j = A.join[c];
+  if (j.parts == 0) return;
+  const int query = 2 * j.pair + (r >= kTile ? 1 : 0), rr = r % kTile;
+  const int node = query * A.per_tile + row_node(A, rr);
+  const bool mine = rr < A.per_tile * A.G && node < j.N && col < A.D;
+  float m = -INFINITY, sum = 0, o[kJoinCols] = {};
+  if (mine) {
+    // the first part is the last segment of its CTA, the others are their CTAs'
+    // first; kWide at a time, all their loads in flight
+    constexpr int kWide = 4;
+    const float2* ml = A.part_ml + r;
+    const float* part = A.part + (col / 4 * 256 + r) * 4;
+    for (int x0 = 0; x0 <= j.parts; x0 += kWide) {
+      float2 e[kWide];
+      float4 v[kWide][kJoinCols / 4];
 #pragma unroll
-    for (int j = 0; j < kJoinCols; j += 4) {
-      const float4 v = *reinterpret_cast<const float4*>(part + slot * 256 * DP + j * 256);
-      o[j] += v.x * f;
-      o[j + 1] += v.y * f;
-      o[j + 2] += v.z * f;
-      o[j + 3] += v.w * f;
+      for (int x = 0; x < kWide; ++x) {
+        const long long slot = x0 + x == 0 ? j.slot : 2LL * (c + (x0 + x <= j.parts ? x0 + x : j.parts));
+        e[x] = ml[slot * 256];
+#pragma unroll
+        for (int i = 0; i < kJoinCols / 4; ++i) v[x][i] = *reinterpret_cast<const float4*>(part + slot * 256 * DP + i * 1024);
+      }
+      float top = m;
+#pragma unroll
+      for (int x = 0; x < kWide; ++x)
+        if (x0 + x <= j.parts) top = fmaxf(top, e[x].x);
+      const float f = m == -INFINITY ? 0.0f : svk::ex2_ftz(m - top);
+      m = top;
+      sum *= f;
+#pragma unroll
+      for (int i = 0; i < kJoinCols; ++i) o[i] *= f;
+#pragma unroll
+      for (int x = 0; x < kWide; ++x)
+        if (x0 + x <= j.parts) {
+          const float w = e[x].x == -INFINITY ? 0.0f : svk::ex2_ftz(e[x].x - top);
+          sum = fmaf(e[x].y, w, sum);
+#pragma unroll
+          for (int i = 0; i < kJoinCols / 4; ++i) {
+            o[4 * i] = fmaf(v[x][i].x, w, o[4 * i]);
+            o[4 * i + 1] = fmaf(v[x][i].y, w, o[4 * i + 1]);
+            o[4 * i + 2] = fmaf(v[x][i].z, w, o[4 * i + 2]);
+            o[4 * i + 3] = fmaf(v[x][i].w, w, o[4 * i + 3]);
+          }
+        }
     }
-  };
-  add(slot0);
-#pragma unroll 8
-  for (int x = 1; x <= parts; ++x) add(2LL * (first + x));
+  }
+  // (a bad sequence's rows are written where its status is)
+  if (__syncthreads_or(bad_layout(A, j.b, t, kFinishThreads)) || !mine) return;
   const float inv = 1.0f / sum;
-  const int qh = head * A.G + rr % A.G;
-  const long long at = static_cast<long long>(q.first) + node;
+  const int qh = j.head * A.G + row_head(A, rr);
+  const long long at = static_cast<long long>(j.first) + node;
   T* dst = static_cast<T*>(A.out) + at * A.out_row + static_cast<long long>(qh) * A.out_head;
 #pragma unroll
-  for (int j = 0; j < kJoinCols; j += 8) store_out<T>(dst + col + j, o + j, inv);
-  if (A.lse && col == 0) A.lse[at * A.q_heads + qh] = (top + log2f(sum)) * 0.69314718055994531f;
+  for (int i = 0; i < kJoinCols; i += 8) store_out<T>(dst + col + i, o + i, inv);
+  if (A.lse && col == 0) A.lse[at * A.q_heads + qh] = (m + log2f(sum)) * 0.69314718055994531f;
 }
 
 // ------------------------------------------------------------------ host
@@ -1194,7 +1233,7 @@ bool encode(CUtensorMap* map, int64_t dtype, const void* data, int dims, const i
 
 size_t workspace_bytes_of(int dim) {
   const size_t rows = 2 * kMaxCtas * 256;
-  return rows * (dim <= 64 ? 64 : 128) * 4 + rows * 8 + (kMaxCtas * 4 + 15) / 16 * 16;
+  return rows * (dim <= 64 ? 64 : 128) * 4 + rows * 8 + kMaxCtas * sizeof(Join);
 }
 
 template <typename T, int DP>
@@ -1203,6 +1242,7 @@ sv_status launch(const sv_tree_attn& a, float scale, unsigned char* ws, cudaStre
   Args A;
   A.G = static_cast<int>(a.q_heads / a.kv_heads);
   A.per_tile = kTile / A.G;
+  A.G_inv = A.G == 1 ? 0u : static_cast<uint32_t>((1ULL << 32) / A.G + 1);
   A.per_pair_inv = static_cast<uint32_t>((1ULL << 32) / (2 * A.per_tile) + 1);
   A.Hkv = static_cast<int>(a.kv_heads);
   A.D = static_cast<int>(a.dim);
@@ -1235,7 +1275,7 @@ sv_status launch(const sv_tree_attn& a, float scale, unsigned char* ws, cudaStre
   const size_t rows = 2 * kMaxCtas * 256;
   A.part = reinterpret_cast<float*>(ws);
   A.part_ml = reinterpret_cast<float2*>(ws + rows * DP * 4);
-  A.err = reinterpret_cast<unsigned*>(ws + rows * DP * 4 + rows * 8);
+  A.join = reinterpret_cast<Join*>(ws + rows * DP * 4 + rows * 8);
   A.status = a.status;
   CUtensorMap qm, km, vm, kcm, vcm;
   if (a.total > 0) {
@@ -1256,6 +1296,8 @@ sv_status launch(const sv_tree_attn& a, float scale, unsigned char* ws, cudaStre
   if (!attr_set[dev]) {
     const cudaError_t e = cudaFuncSetAttribute(attend_kernel<T, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<DP>());
     if (e != cudaSuccess) return svh::fail(SV_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+    // (the same split of the SM's memory as the first kernel's: no change between the two)
+    cudaFuncSetAttribute(finish_kernel<T, DP>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
     int n = 0;
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = kMaxCtas;
     sms[dev] = n < kMaxCtas ? n : kMaxCtas;
@@ -1271,10 +1313,9 @@ sv_status launch(const sv_tree_attn& a, float scale, unsigned char* ws, cudaStre
   const int most = static_cast<int>(a.n > A.per_tile ? kTile + (a.n - A.per_tile < A.per_tile ? a.n - A.per_tile : A.per_tile) * A.G
                                                      : a.n * A.G);
   const int chunks = (most + kFinishRows - 1) / kFinishRows * (DP / (8 * kJoinCols));
-  const long long per_sequence = a.kv_heads * ((a.n + 2 * A.per_tile - 1) / (2 * A.per_tile));
-  const bool by_item = a.batch * per_sequence < C;
-  const int join = a.total > 0 ? static_cast<int>(by_item ? a.batch * per_sequence : C - 1) * chunks : 0;
-  const int grid = join + static_cast<int>((a.batch + kFinishThreads / 32 - 1) / (kFinishThreads / 32));
+  const int join = a.total > 0 ? C * chunks : 0;
+  if (a.batch > 0x7FFFFFFF - join) return svh::fail(SV_ERR_UNSUPPORTED, "batch too large");
+  const int grid = join + static_cast<int>(a.batch);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1284,8 +1325,7 @@ sv_status launch(const sv_tree_attn& a, float scale, unsigned char* ws, cudaStre
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = a.total > 0 ? 1 : 0;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, finish_kernel<T, DP>, A, a.total > 0 ? C : 0, chunks, join,
-                                           by_item ? static_cast<int>(per_sequence) : 0);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, finish_kernel<T, DP>, A, a.total > 0 ? C : 0, chunks);
   return e == cudaSuccess ? SV_OK : svh::fail(SV_ERR_CUDA, "kernel launch: %s", cudaGetErrorString(e));
 }
 
