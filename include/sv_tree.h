@@ -35,7 +35,8 @@
 extern "C" {
 #endif
 
-#define SV_TREE_MAX_NODES 256 /* nodes per sequence */
+#define SV_TREE_MAX_NODES 256         /* nodes per sequence */
+#define SV_TREE_MAX_TOKENS 134217728  /* tokens that a row of a page table holds */
 
 /*
  * Greedy verification of a tree.
@@ -95,8 +96,9 @@ sv_status sv_verify_tree(const int32_t* choices, const int32_t* tokens, const in
  * Rows of out and lse past the last sequence are left as they are.
  * workspace: sv_tree_attention_workspace_size() bytes, 16-byte aligned, no
  *   initial contents needed.  Calls that share one must not overlap on the GPU.
- * dim a multiple of 8 up to 128; page_size a multiple of 8; q_heads a multiple
- * of kv_heads, at most 128 times as many.
+ * dim a multiple of 8 up to 128; page_size a multiple of 8; max_pages *
+ * page_size at most SV_TREE_MAX_TOKENS; q_heads a multiple of kv_heads, at most
+ * 128 times as many.
  */
 typedef struct {
   int64_t dtype, q_heads, kv_heads, dim;

@@ -11,7 +11,7 @@
 // A CTA, one per SM, has
 //   warps 0-3, 4-7  two softmax streams, each with a score tile and an output
 //                   tile in tensor memory (4 x 128 columns, all there are);
-//   warp 8, 11      producers of queries and keys, of values: TMA loads, one box
+//   warp 8, 11      producers of keys, of queries and values: TMA loads, one box
 //                   per page (or part of a page) and 64 elements, 128-byte
 //                   swizzle, into rings of tiles;
 //   warp 9          issues the MMAs;
@@ -31,12 +31,15 @@
 // output is rescaled, which keeps that off the ordinary step; weights up to 2^8
 // lose nothing in either type.
 //
-// The key tiles of all items, sequence after sequence, are cut into one equal
-// piece per CTA, so ragged lengths balance and one long context uses every SM.
-// An item that a cut divides leaves its parts (f32 outputs, maximum, sum) in the
-// workspace, at most two per CTA, and a second kernel joins them in order: the
-// result depends on the inputs and the number of CTAs only.  That kernel also
-// looks the sequences' layouts over while the first still runs.
+// The work is cut into one piece per CTA, so that ragged lengths balance and one
+// long context uses every SM.  Where CTAs have many steps the steps of all items,
+// sequence after sequence, are cut evenly, wherever that falls; where they have
+// few, an item's end inside a piece would cost more than it evens out (some 10000
+// clocks against 1800 a step), and each item is divided by itself, into pieces as
+// short as the CTAs allow.  An item that a cut divides leaves its parts (f32
+// outputs, maximum, sum) in the workspace, at most two per CTA, and a second
+// kernel joins them in order: the result depends on the inputs and the number of
+// CTAs only.
 //
 // What a node must not see may hold anything: scores are masked by selection,
 // the values past a length are set to 0 before the MMA, and a drafted value that
@@ -103,6 +106,7 @@ struct Args {
   long long out_row, out_head;
   float* lse;
   int q_heads;
+  bool wide;        // out in 32-byte stores
   float c;          // scale in powers of two, not negative
   bool flip;        // the scores' sign is turned (a negative scale)
   float* part;      // [2 CTAs][dp / 4][256 rows][4]: a warp, a row per lane, writes and reads whole lines
@@ -142,16 +146,23 @@ __device__ __forceinline__ int row_node(const Args& A, int r) {
 }
 __device__ __forceinline__ int row_head(const Args& A, int r) { return r - row_node(A, r) * A.G; }
 
+// Steps of one key head: two per key tile for a pair of query tiles; the last
+// pair of a sequence may lack its second.
+__device__ __forceinline__ int steps_of_head(const Args& A, const Sequence& s) {
+  const bool odd = s.N <= (2 * s.items - 1) * A.per_tile;
+  return s.tiles * (2 * s.items - (odd ? 1 : 0));
+}
 __device__ __forceinline__ long long units_of(const Args& A, const Sequence& s) {
-  return s.N > 0 ? static_cast<long long>(s.tiles) * s.items * A.Hkv : 0;
+  return s.N > 0 ? static_cast<long long>(steps_of_head(A, s)) * A.Hkv : 0;
 }
 
-// W units over C CTAs, the first `more` of which take one more than `each`.
+// W units over CTAs 0 .. ctas - 1, the first `more` of which take one more than
+// `each`.
 struct Cut {
   long long each;
-  int more;
+  int more, ctas;
   __device__ __forceinline__ long long begin(int c) const { return each * c + (c < more ? c : more); }
-  __device__ __forceinline__ long long count(int c) const { return each + (c < more ? 1 : 0); }
+  __device__ __forceinline__ long long count(int c) const { return c < ctas ? each + (c < more ? 1 : 0) : 0; }
   // the CTA that has unit u
   __device__ __forceinline__ int owner(long long u) const {
     const long long wide = (each + 1) * more;
@@ -178,7 +189,8 @@ struct Segment {
 struct Walk {
   int b;
   long long off, left;
-  int count;  // segments so far
+  int count;     // segments so far
+  bool odd_end;  // the last one's cut lies inside a key tile
 
   __device__ __forceinline__ bool next(const Args& A, Segment& s) {
     if (left <= 0) return false;
@@ -188,34 +200,58 @@ struct Walk {
       if (off < units_of(A, s.q)) break;
     }
     cut(A, s);
-    return true;
+    return s.steps > 0;  // (half a key tile at the end of a piece is none)
   }
-  // The next segment, in sequence s.q
+  // The next segment, in sequence s.q; a cut inside a pair's key tile leaves the
+  // tile to the piece behind it.
   __device__ __forceinline__ void cut(const Args& A, Segment& s) {
-    const int item = off < s.q.tiles ? 0 : Cut::divide(off, s.q.tiles);
+    const int per_head = steps_of_head(A, s.q);
+    s.head = off < per_head ? 0 : Cut::divide(off, per_head);
+    const int in_head = static_cast<int>(off - static_cast<long long>(s.head) * per_head), pair_steps = 2 * s.q.tiles;
+    s.pair = in_head < pair_steps ? 0 : in_head / pair_steps;
+    const int in = in_head - s.pair * pair_steps;
     s.b = b;
-    s.t0 = static_cast<int>(off - static_cast<long long>(item) * s.q.tiles);
-    s.t1 = s.q.tiles - s.t0 < left ? s.q.tiles : s.t0 + static_cast<int>(left);
-    s.head = s.q.items == 1 ? item : item / s.q.items;
-    s.pair = item - s.head * s.q.items;
     s.two = s.q.N > (2 * s.pair + 1) * A.per_tile;
+    const int all = s.two ? pair_steps : s.q.tiles, end = all - in < left ? all : in + static_cast<int>(left);
+    s.t0 = s.two ? in >> 1 : in;
+    s.t1 = s.two ? end >> 1 : end;
     s.whole = s.t0 == 0 && s.t1 == s.q.tiles;
     s.steps = (s.t1 - s.t0) * (s.two ? 2 : 1);
-    off += s.t1 - s.t0;
-    left -= s.t1 - s.t0;
+    odd_end = s.two && (end & 1);
+    off += end - in;
+    left -= end - in;
     ++count;
   }
 };
 
 struct PlanMem {
   long long warp_sums[kThreads / 32];
+  int warp_counts[kThreads / 32];
   Cut cut;
   Walk w;     // after the CTA's first segment
   Segment s;  // that
   int any;    // there is one
+  int parts;  // where items are divided by themselves: the parts behind this one; else -1
 };
 
-// All of a CTA's threads: the cut of the units over C CTAs, and CTA c's first
+// Pieces of at most `limit` steps that the sequence's items are divided into:
+// those of a pair of query tiles, of a last single one, of a key head.
+struct Pieces {
+  int pair, single, head;
+};
+__device__ __forceinline__ Pieces pieces_of(const Args& A, const Sequence& s, int limit) {
+  Pieces p;
+  const bool odd = s.N <= (2 * s.items - 1) * A.per_tile;
+  const int tiles = limit / 2;  // of a pair
+  p.pair = (s.tiles + tiles - 1) / tiles;
+  p.single = (s.tiles + limit - 1) / limit;
+  p.head = p.pair * (s.items - (odd ? 1 : 0)) + (odd ? p.single : 0);
+  return p;
+}
+
+constexpr int kFewSteps = 24;  // a piece with no more steps is of one item
+
+// All of a CTA's threads: how the units are cut over C CTAs, and CTA c's first
 // segment.
 __device__ __forceinline__ void make_plan(const Args& A, int C, int c, PlanMem& m) {
   constexpr int T = kThreads;
@@ -235,7 +271,7 @@ __device__ __forceinline__ void make_plan(const Args& A, int C, int c, PlanMem& 
     if (lane >= d) x += y;
   }
   if (lane == 31) m.warp_sums[warp] = x;
-  if (t == 0) m.any = 0;
+  if (t == 0) m.any = 0, m.parts = -1;
   __syncthreads();
   long long before = x - mine, W = 0;
 #pragma unroll
@@ -244,9 +280,64 @@ __device__ __forceinline__ void make_plan(const Args& A, int C, int c, PlanMem& 
     if (w < warp) before += v;
     W += v;
   }
-  Cut cut;
-  cut.each = W < C ? 0 : Cut::divide(W, C);
-  cut.more = static_cast<int>(W - cut.each * C);
+  if (W <= static_cast<long long>(kFewSteps) * C && A.batch <= T) {
+    // each item by itself, in the shortest pieces that C CTAs can take
+    const int least = W <= 2LL * C ? 2 : static_cast<int>((static_cast<uint32_t>(W) + C - 1) / C);
+    bool fits = false;
+    for (int limit = 2 * kFewSteps;;) {  // (whether the longest fit, then from the shortest on)
+      const Pieces p = t < A.batch && q.N > 0 ? pieces_of(A, q, limit) : Pieces{0, 0, 0};
+      const int count = p.head * A.Hkv;  // (no more than units)
+      int y = count;
+#pragma unroll
+      for (int d = 1; d < 32; d *= 2) {
+        const int z = __shfl_up_sync(0xFFFFFFFFu, y, d);
+        if (lane >= d) y += z;
+      }
+      if (lane == 31) m.warp_counts[warp] = y;
+      __syncthreads();
+      int ahead = y - count, all = 0;
+#pragma unroll
+      for (int w = 0; w < T / 32; ++w) {
+        const int v = m.warp_counts[w];
+        if (w < warp) ahead += v;
+        all += v;
+      }
+      if (all > C && !fits) break;
+      if (all <= C && fits) {
+        if (c >= ahead && c < ahead + count) {
+          Segment s;
+          s.q = q;
+          s.b = t;
+          const int i = c - ahead;
+          s.head = i / p.head;
+          const int in = i - s.head * p.head;
+          s.pair = in / p.pair < q.items ? in / p.pair : q.items - 1;
+          s.two = q.N > (2 * s.pair + 1) * A.per_tile;
+          const int piece = in - s.pair * p.pair, n = s.two ? p.pair : p.single;
+          s.t0 = static_cast<int>(static_cast<long long>(q.tiles) * piece / n);
+          s.t1 = static_cast<int>(static_cast<long long>(q.tiles) * (piece + 1) / n);
+          s.whole = n == 1;
+          s.steps = (s.t1 - s.t0) * (s.two ? 2 : 1);
+          m.s = s;
+          m.w.b = t;
+          m.w.off = m.w.left = 0;
+          m.w.count = 1;
+          m.any = 1;
+          m.parts = n - 1 - piece;
+        }
+        __syncthreads();
+        return;
+      }
+      limit = fits ? limit + 1 : least;
+      fits = true;
+      __syncthreads();  // the counts have been read
+    }
+    __syncthreads();
+  }
+  Cut cut;  // (two steps at least: a piece of one may be half of a pair's key tile, none)
+  cut.ctas = W >= 2LL * C ? C : W >= 2 ? static_cast<int>(W / 2) : 1;
+  cut.each = Cut::divide(W, cut.ctas);
+  cut.more = static_cast<int>(W - cut.each * cut.ctas);
   const long long u = cut.begin(c);
   if (t == 0) m.cut = cut;
   if (u >= before && u < before + mine && cut.count(c) > 0) {
@@ -268,7 +359,7 @@ __device__ __forceinline__ void make_plan(const Args& A, int C, int c, PlanMem& 
     w.cut(A, s);
     m.w = w;
     m.s = s;
-    m.any = 1;
+    m.any = s.steps > 0;
   }
   __syncthreads();
 }
@@ -513,15 +604,38 @@ __device__ __forceinline__ void load_tile(const Args& A, const Segment& s, int t
   __syncwarp();
 }
 
-// Queries and keys.
 template <int DP>
-__device__ __forceinline__ void produce_keys(const Args& A, Shared& sm, uint32_t q_smem, uint32_t ring, const CUtensorMap* qm,
-                                             const CUtensorMap* km, const CUtensorMap* kcm) {
-  constexpr int kPanels = DP / 64, kSlots = k_slots(DP);
+__device__ __forceinline__ void produce_keys(const Args& A, Shared& sm, uint32_t ring, const CUtensorMap* km, const CUtensorMap* kcm) {
+  constexpr int kSlots = k_slots(DP);
   const int lane = static_cast<int>(threadIdx.x & 31);
   Walk w = sm.plan.w;
   Segment s = sm.plan.s;
-  uint32_t slot = 0, turn = 0, loads = 0, qs = 0;
+  uint32_t slot = 0, turn = 0, loads = 0;
+  bool alive = true;
+  for (bool go = sm.plan.any; alive && go; go = w.next(A, s)) {
+    for (int t = s.t0; alive && t < s.t1; ++t) {
+      if (turn) alive = warp_wait(sm, &sm.k_empty[slot], (turn - 1) & 1);
+      if (!alive) break;
+      load_tile<DP>(A, s, t, kcm, km, ring + slot * tile_bytes(DP), &sm.k_full[slot], lane);
+      ++loads;
+      if (++slot == kSlots) slot = 0, ++turn;
+    }
+  }
+  // no copy may still be writing shared memory at exit
+  for (uint32_t i = loads > kSlots ? loads - kSlots : 0; i < loads; ++i) svk::mbar_wait_bounded(&sm.k_full[i % kSlots], (i / kSlots) & 1);
+}
+
+// Queries and values (a query tile waits for a buffer that the segment before
+// gives back; the keys behind it must not wait with it).
+template <int DP>
+__device__ __forceinline__ void produce_values(const Args& A, Shared& sm, uint32_t q_smem, uint32_t ring, const CUtensorMap* qm,
+                                               const CUtensorMap* vm, const CUtensorMap* vcm) {
+  constexpr int kSlots = v_slots(DP), kPanels = DP / 64;
+  uint32_t qs = 0;
+  const int lane = static_cast<int>(threadIdx.x & 31);
+  Walk w = sm.plan.w;
+  Segment s = sm.plan.s;
+  uint32_t slot = 0, turn = 0, loads = 0;
   bool alive = true;
   for (bool go = sm.plan.any; alive && go; go = w.next(A, s)) {
     for (int j = 0; alive && j < (s.two ? 2 : 1); ++j, ++qs) {
@@ -535,36 +649,15 @@ __device__ __forceinline__ void produce_keys(const Args& A, Shared& sm, uint32_t
                s.q.first + (2 * s.pair + j) * A.per_tile, &sm.q_full[buf]);
     }
     for (int t = s.t0; alive && t < s.t1; ++t) {
-      if (turn) alive = warp_wait(sm, &sm.k_empty[slot], (turn - 1) & 1);
-      if (!alive) break;
-      load_tile<DP>(A, s, t, kcm, km, ring + slot * tile_bytes(DP), &sm.k_full[slot], lane);
-      ++loads;
-      if (++slot == kSlots) slot = 0, ++turn;
-    }
-  }
-  // no copy may still be writing shared memory at exit
-  for (uint32_t i = loads > kSlots ? loads - kSlots : 0; i < loads; ++i) svk::mbar_wait_bounded(&sm.k_full[i % kSlots], (i / kSlots) & 1);
-  for (uint32_t i = qs > 2 ? qs - 2 : 0; i < qs; ++i) svk::mbar_wait_bounded(&sm.q_full[i & 1], (i >> 1) & 1);
-}
-
-template <int DP>
-__device__ __forceinline__ void produce_values(const Args& A, Shared& sm, uint32_t ring, const CUtensorMap* vm,
-                                               const CUtensorMap* vcm) {
-  constexpr int kSlots = v_slots(DP);
-  const int lane = static_cast<int>(threadIdx.x & 31);
-  Walk w = sm.plan.w;
-  Segment s = sm.plan.s;
-  uint32_t slot = 0, turn = 0, loads = 0;
-  bool alive = true;
-  for (bool go = sm.plan.any; alive && go; go = w.next(A, s))
-    for (int t = s.t0; alive && t < s.t1; ++t) {
       if (turn) alive = warp_wait(sm, &sm.v_empty[slot], (turn - 1) & 1);
       if (!alive) break;
       load_tile<DP>(A, s, t, vcm, vm, ring + slot * tile_bytes(DP), &sm.v_full[slot], lane);
       ++loads;
       if (++slot == kSlots) slot = 0, ++turn;
     }
+  }
   for (uint32_t i = loads > kSlots ? loads - kSlots : 0; i < loads; ++i) svk::mbar_wait_bounded(&sm.v_full[i % kSlots], (i / kSlots) & 1);
+  for (uint32_t i = qs > 2 ? qs - 2 : 0; i < qs; ++i) svk::mbar_wait_bounded(&sm.q_full[i & 1], (i >> 1) & 1);
 }
 
 // Whether a value tile is mended before it is used.
@@ -799,6 +892,15 @@ __device__ __forceinline__ void store_out(T* dst, const float* o, float f) {
   *reinterpret_cast<uint4*>(dst) = u;
 }
 
+// 32 bytes, a whole sector.
+template <typename T>
+__device__ __forceinline__ void store_out16(T* dst, const float* o, float f) {
+  uint32_t u[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) u[i] = Num<T>::pack(o[2 * i] * f, o[2 * i + 1] * f);
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), SVA_W8(u, 0) : "memory");
+}
+
 // A softmax warp.
 template <typename T, int DP>
 __device__ __forceinline__ void soften(const Args& A, Shared& sm, uint32_t tmem, int c) {
@@ -970,9 +1072,15 @@ __device__ __forceinline__ void soften(const Args& A, Shared& sm, uint32_t tmem,
         }
         if (mine && s.whole) {
           T* dst = static_cast<T*>(A.out) + at * A.out_row + static_cast<long long>(qh) * A.out_head + col;
+          if (A.wide) {
 #pragma unroll
-          for (int j = 0; j < 32; j += 8)
-            if (col + j < A.D) store_out<T>(dst + j, o + j, inv);
+            for (int j = 0; j < 32; j += 16)
+              if (col + j < A.D) store_out16<T>(dst + j, o + j, inv);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; j += 8)
+              if (col + j < A.D) store_out<T>(dst + j, o + j, inv);
+          }
         } else if (mine) {
 #pragma unroll
           for (int j = 0; j < 32; j += 4)
@@ -982,7 +1090,12 @@ __device__ __forceinline__ void soften(const Args& A, Shared& sm, uint32_t tmem,
     }
     if (!s.whole && s.t0 == 0 && threadIdx.x == 0) {
       Join j;
-      j.parts = sm.plan.cut.owner(sm.plan.cut.begin(c + 1) + s.q.tiles - s.t1 - 1) - c;
+      j.parts = sm.plan.parts;
+      if (j.parts < 0) {  // the CTA that has the item's last step
+        const long long end = sm.plan.cut.begin(c + 1);
+        const int done = s.two ? 2 * s.t1 + static_cast<int>(w.odd_end) : s.t1;
+        j.parts = sm.plan.cut.owner(end + (s.two ? 2 : 1) * s.q.tiles - done - 1) - c;
+      }
       j.slot = slot;
       j.b = s.b;
       j.head = s.head;
@@ -1058,13 +1171,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp >= kSoftWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == 8)
-      produce_keys<DP>(A, sm, q_smem, k_ring, &qm, &km, &kcm);
+      produce_keys<DP>(A, sm, k_ring, &km, &kcm);
     else if (warp == 9)
       issue<T, DP>(A, sm, q_smem, k_ring, v_ring, tmem);
     else if (warp == 10)
       mend<T, DP>(A, sm, v_ptr);
     else
-      produce_values<DP>(A, sm, v_ring, &vm, &vcm);
+      produce_values<DP>(A, sm, q_smem, v_ring, &qm, &vm, &vcm);
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
     soften<T, DP>(A, sm, tmem, c);
@@ -1112,8 +1225,10 @@ static_assert(kFinishThreads >= SV_TREE_MAX_NODES, "a thread per node");
 // Joins the parts of items that several CTAs had, 32 rows and 64 columns to a
 // CTA, and writes the statuses.
 constexpr int kJoinCols = 8;  // columns of a thread; a lane per row
-template <typename T, int DP>
-__global__ void __launch_bounds__(kFinishThreads) finish_kernel(const __grid_constant__ Args A, int C, int chunks) {
+// kWide parts at a time, all their loads in flight: two where there are CTAs for
+// all the SM's room, eight where few items are in many parts.
+template <typename T, int DP, int kWide>
+__global__ void __launch_bounds__(kFinishThreads, kWide > 2 ? 2 : 5) finish_kernel(const __grid_constant__ Args A, int C, int chunks) {
   const int t = static_cast<int>(threadIdx.x);
   if (static_cast<int>(blockIdx.x) < A.batch) {  // a sequence's status
     const int b = static_cast<int>(blockIdx.x);
@@ -1149,9 +1264,7 @@ __global__ void __launch_bounds__(kFinishThreads) finish_kernel(const __grid_con
   const bool mine = rr < A.per_tile * A.G && node < j.N && col < A.D;
   float m = -INFINITY, sum = 0, o[kJoinCols] = {};
   if (mine) {
-    // the first part is the last segment of its CTA, the others are their CTAs'
-    // first; kWide at a time, all their loads in flight
-    constexpr int kWide = 4;
+    // the first part is the last segment of its CTA, the others are their CTAs' first
     const float2* ml = A.part_ml + r;
     const float* part = A.part + (col / 4 * 256 + r) * 4;
     for (int x0 = 0; x0 <= j.parts; x0 += kWide) {
@@ -1270,6 +1383,7 @@ sv_status launch(const sv_tree_attn& a, float scale, unsigned char* ws, cudaStre
   A.out_head = a.out_head;
   A.lse = a.lse;
   A.q_heads = static_cast<int>(a.q_heads);
+  A.wide = !((reinterpret_cast<uintptr_t>(a.out) & 31) | ((a.out_row | a.out_head | a.dim) & 15));
   A.c = (scale < 0 ? -scale : scale) * 1.4426950408889634f;
   A.flip = scale < 0;
   const size_t rows = 2 * kMaxCtas * 256;
@@ -1297,7 +1411,8 @@ sv_status launch(const sv_tree_attn& a, float scale, unsigned char* ws, cudaStre
     const cudaError_t e = cudaFuncSetAttribute(attend_kernel<T, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<DP>());
     if (e != cudaSuccess) return svh::fail(SV_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
     // (the same split of the SM's memory as the first kernel's: no change between the two)
-    cudaFuncSetAttribute(finish_kernel<T, DP>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    cudaFuncSetAttribute(finish_kernel<T, DP, 2>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    cudaFuncSetAttribute(finish_kernel<T, DP, 8>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
     int n = 0;
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = kMaxCtas;
     sms[dev] = n < kMaxCtas ? n : kMaxCtas;
@@ -1325,7 +1440,9 @@ sv_status launch(const sv_tree_attn& a, float scale, unsigned char* ws, cudaStre
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = a.total > 0 ? 1 : 0;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, finish_kernel<T, DP>, A, a.total > 0 ? C : 0, chunks);
+  const bool few = a.batch * a.kv_heads * ((a.n + 2 * A.per_tile - 1) / (2 * A.per_tile)) * 4 <= C;
+  const cudaError_t e = few ? cudaLaunchKernelEx(&cfg, finish_kernel<T, DP, 8>, A, a.total > 0 ? C : 0, chunks)
+                            : cudaLaunchKernelEx(&cfg, finish_kernel<T, DP, 2>, A, a.total > 0 ? C : 0, chunks);
   return e == cudaSuccess ? SV_OK : svh::fail(SV_ERR_CUDA, "kernel launch: %s", cudaGetErrorString(e));
 }
 
@@ -1357,6 +1474,8 @@ sv_status sv_tree_attention(const sv_tree_attn* args, float scale, void* workspa
   if (!a.cu_nodes && a.batch * a.n != a.total) return svh::fail(SV_ERR_ARG, "without cu_nodes, total must equal batch * n");
   if (a.pages < 1 || a.pages > kMax || a.max_pages < 0 || a.max_pages > kMax)
     return svh::fail(SV_ERR_ARG, "pages or max_pages out of range");
+  if (a.max_pages > 0 && a.page_size > SV_TREE_MAX_TOKENS / a.max_pages)
+    return svh::fail(SV_ERR_UNSUPPORTED, "max_pages * page_size is more than %d tokens", SV_TREE_MAX_TOKENS);
   if (a.table_stride < a.max_pages && a.batch > 1) return svh::fail(SV_ERR_ARG, "table_stride (%lld) is less than max_pages", (long long)a.table_stride);
   if (!(scale == scale) || scale - scale != 0) return svh::fail(SV_ERR_ARG, "scale must be finite");
   if (a.batch == 0) return SV_OK;

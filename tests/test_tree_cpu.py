@@ -111,6 +111,7 @@ def test_attention_argument_errors(lib, kw, frag):
     (dict(page_size=4), b"page_size"),
     (dict(n=257, total=514), b"256"),
     (dict(q_heads=258), b"128"),
+    (dict(max_pages=1 << 24, table_stride=1 << 24), b"tokens"),
 ])
 def test_attention_limits(lib, kw, frag):
     assert attention(lib, **kw) == _lib.SV_ERR_UNSUPPORTED
