@@ -242,7 +242,7 @@ struct Pieces {
 __device__ __forceinline__ Pieces pieces_of(const Args& A, const Sequence& s, int limit) {
   Pieces p;
   const bool odd = s.N <= (2 * s.items - 1) * A.per_tile;
-  const int tiles = limit / 2;  // of a pair
+  const int tiles = limit < 2 ? 1 : limit / 2;  // of a pair
   p.pair = (s.tiles + tiles - 1) / tiles;
   p.single = (s.tiles + limit - 1) / limit;
   p.head = p.pair * (s.items - (odd ? 1 : 0)) + (odd ? p.single : 0);
@@ -250,12 +250,21 @@ __device__ __forceinline__ Pieces pieces_of(const Args& A, const Sequence& s, in
 }
 
 constexpr int kFewSteps = 24;  // a piece with no more steps is of one item
+constexpr int kFewSequences = 32;
 
-// All of a CTA's threads: how the units are cut over C CTAs, and CTA c's first
-// segment.
+// How the units are cut over C CTAs, and CTA c's first segment: by all of the
+// CTA's threads, or by every warp for itself (few sequences: all write the same
+// words, and none waits for another).
+template <bool kWarp>
 __device__ __forceinline__ void make_plan(const Args& A, int C, int c, PlanMem& m) {
-  constexpr int T = kThreads;
-  const int t = static_cast<int>(threadIdx.x), lane = t & 31, warp = t >> 5;
+  constexpr int T = kWarp ? 32 : kThreads;
+  const int lane = static_cast<int>(threadIdx.x & 31), warp = static_cast<int>(threadIdx.x >> 5), t = kWarp ? lane : static_cast<int>(threadIdx.x);
+  auto sync = [] {
+    if (kWarp)
+      __syncwarp();
+    else
+      __syncthreads();
+  };
   const int per = A.batch <= T ? 1 : (A.batch + T - 1) / T;
   const int lo = t * per < A.batch ? t * per : A.batch, hi = lo + per < A.batch ? lo + per : A.batch;
   long long mine = 0;
@@ -270,21 +279,24 @@ __device__ __forceinline__ void make_plan(const Args& A, int C, int c, PlanMem& 
     const long long y = __shfl_up_sync(0xFFFFFFFFu, x, d);
     if (lane >= d) x += y;
   }
-  if (lane == 31) m.warp_sums[warp] = x;
-  if (t == 0) m.any = 0, m.parts = -1;
-  __syncthreads();
   long long before = x - mine, W = 0;
+  if (kWarp) {
+    W = __shfl_sync(0xFFFFFFFFu, x, 31);
+  } else {
+    if (lane == 31) m.warp_sums[warp] = x;
+    __syncthreads();
 #pragma unroll
-  for (int w = 0; w < T / 32; ++w) {
-    const long long v = m.warp_sums[w];
-    if (w < warp) before += v;
-    W += v;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      const long long v = m.warp_sums[w];
+      if (w < warp) before += v;
+      W += v;
+    }
   }
   if (W <= static_cast<long long>(kFewSteps) * C && A.batch <= T) {
     // each item by itself, in the shortest pieces that C CTAs can take
-    const int least = W <= 2LL * C ? 2 : static_cast<int>((static_cast<uint32_t>(W) + C - 1) / C);
-    bool fits = false;
-    for (int limit = 2 * kFewSteps;;) {  // (whether the longest fit, then from the shortest on)
+    const int least = W <= C ? 1 : static_cast<int>((static_cast<uint32_t>(W) + C - 1) / C);
+    bool fits = W <= C;
+    for (int limit = fits ? 1 : 2 * kFewSteps;;) {  // (whether the longest fit, then from the shortest on)
       const Pieces p = t < A.batch && q.N > 0 ? pieces_of(A, q, limit) : Pieces{0, 0, 0};
       const int count = p.head * A.Hkv;  // (no more than units)
       int y = count;
@@ -293,14 +305,18 @@ __device__ __forceinline__ void make_plan(const Args& A, int C, int c, PlanMem& 
         const int z = __shfl_up_sync(0xFFFFFFFFu, y, d);
         if (lane >= d) y += z;
       }
-      if (lane == 31) m.warp_counts[warp] = y;
-      __syncthreads();
       int ahead = y - count, all = 0;
+      if (kWarp) {
+        all = __shfl_sync(0xFFFFFFFFu, y, 31);
+      } else {
+        if (lane == 31) m.warp_counts[warp] = y;
+        __syncthreads();
 #pragma unroll
-      for (int w = 0; w < T / 32; ++w) {
-        const int v = m.warp_counts[w];
-        if (w < warp) ahead += v;
-        all += v;
+        for (int w = 0; w < kThreads / 32; ++w) {
+          const int v = m.warp_counts[w];
+          if (w < warp) ahead += v;
+          all += v;
+        }
       }
       if (all > C && !fits) break;
       if (all <= C && fits) {
@@ -325,14 +341,14 @@ __device__ __forceinline__ void make_plan(const Args& A, int C, int c, PlanMem& 
           m.any = 1;
           m.parts = n - 1 - piece;
         }
-        __syncthreads();
+        sync();
         return;
       }
       limit = fits ? limit + 1 : least;
       fits = true;
-      __syncthreads();  // the counts have been read
+      sync();  // the counts have been read
     }
-    __syncthreads();
+    sync();
   }
   Cut cut;  // (two steps at least: a piece of one may be half of a pair's key tile, none)
   cut.ctas = W >= 2LL * C ? C : W >= 2 ? static_cast<int>(W / 2) : 1;
@@ -361,7 +377,7 @@ __device__ __forceinline__ void make_plan(const Args& A, int C, int c, PlanMem& 
     m.s = s;
     m.any = s.steps > 0;
   }
-  __syncthreads();
+  sync();
 }
 
 // Steps of a CTA one after another.
@@ -580,21 +596,35 @@ __device__ __forceinline__ bool elected() {
   return p != 0;
 }
 
-// Tile t of keys or values to shared memory at `dst`: every lane its boxes.
+// The page of this lane's box of key tile t (looked up before the slot that the
+// tile waits for is free), and its first token there.
+struct Box {
+  int id, at;
+};
 template <int DP>
-__device__ __forceinline__ void load_tile(const Args& A, const Segment& s, int t, const CUtensorMap* cache,
+__device__ __forceinline__ Box look_up(const Args& A, const Segment& s, int t, int lane) {
+  constexpr int kPanels = DP / 64;
+  Box x = {0, 0};
+  if (t < s.q.cached && (lane / kPanels) << A.box_shift < keys_of(s, t)) {  // (at most 16 boxes of a panel)
+    const int at = t * kTile + ((lane / kPanels) << A.box_shift), p = at / A.page;
+    x.id = A.table[s.b * A.table_stride + p];
+    x.at = at - p * A.page;
+  }
+  return x;
+}
+
+// Tile t of keys or values to shared memory at `dst`: every lane its box.
+template <int DP>
+__device__ __forceinline__ void load_tile(const Args& A, const Segment& s, int t, const Box& x, const CUtensorMap* cache,
                                           const CUtensorMap* own, uint32_t dst, uint64_t* bar, int lane) {
   constexpr int kPanels = DP / 64;
   if (t < s.q.cached) {
     const int boxes = (keys_of(s, t) + A.box - 1) >> A.box_shift;
-    int i = lane, id = 0;
-    const int at = t * kTile + ((i / kPanels) << A.box_shift), p = at / A.page;
-    if (i < boxes * kPanels) id = A.table[s.b * A.table_stride + p];
     if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(boxes * A.box * 128 * kPanels));
     __syncwarp();
-    if (i < boxes * kPanels)  // (at most 16 boxes of a panel)
-      tma_4d(dst + (i % kPanels) * (kTile * 128) + (i / kPanels) * A.box * 128, cache, (i % kPanels) * 64, at - p * A.page, s.head,
-             id, bar);
+    if (lane < boxes * kPanels)
+      tma_4d(dst + (lane % kPanels) * (kTile * 128) + (lane / kPanels) * A.box * 128, cache, (lane % kPanels) * 64, x.at, s.head, x.id,
+             bar);
   } else {
     if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(A.tree_box * 128 * kPanels));
     __syncwarp();
@@ -614,9 +644,10 @@ __device__ __forceinline__ void produce_keys(const Args& A, Shared& sm, uint32_t
   bool alive = true;
   for (bool go = sm.plan.any; alive && go; go = w.next(A, s)) {
     for (int t = s.t0; alive && t < s.t1; ++t) {
+      const Box x = look_up<DP>(A, s, t, lane);
       if (turn) alive = warp_wait(sm, &sm.k_empty[slot], (turn - 1) & 1);
       if (!alive) break;
-      load_tile<DP>(A, s, t, kcm, km, ring + slot * tile_bytes(DP), &sm.k_full[slot], lane);
+      load_tile<DP>(A, s, t, x, kcm, km, ring + slot * tile_bytes(DP), &sm.k_full[slot], lane);
       ++loads;
       if (++slot == kSlots) slot = 0, ++turn;
     }
@@ -649,9 +680,10 @@ __device__ __forceinline__ void produce_values(const Args& A, Shared& sm, uint32
                s.q.first + (2 * s.pair + j) * A.per_tile, &sm.q_full[buf]);
     }
     for (int t = s.t0; alive && t < s.t1; ++t) {
+      const Box x = look_up<DP>(A, s, t, lane);
       if (turn) alive = warp_wait(sm, &sm.v_empty[slot], (turn - 1) & 1);
       if (!alive) break;
-      load_tile<DP>(A, s, t, vcm, vm, ring + slot * tile_bytes(DP), &sm.v_full[slot], lane);
+      load_tile<DP>(A, s, t, x, vcm, vm, ring + slot * tile_bytes(DP), &sm.v_full[slot], lane);
       ++loads;
       if (++slot == kSlots) slot = 0, ++turn;
     }
@@ -1156,6 +1188,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&sm.done, 1);
     sm.abort = 0;
     sm.join.parts = 0;
+    sm.plan.any = 0;
+    sm.plan.parts = -1;
     svk::fence_mbar_init_cluster();
   }
   if (warp == 8 && (threadIdx.x & 31) == 0)
@@ -1165,8 +1199,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   fence_before();
-  make_plan(A, C, c, sm.plan);  // (two barriers of the CTA)
+  __syncthreads();
   fence_after();
+  if (A.batch <= kFewSequences)
+    make_plan<true>(A, C, c, sm.plan);
+  else
+    make_plan<false>(A, C, c, sm.plan);
   const uint32_t tmem = sm.tmem;
   if (warp >= kSoftWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
