@@ -11,6 +11,8 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import struct
+from operator import attrgetter
 from typing import NamedTuple, Optional, Sequence, Union
 
 import torch
@@ -809,9 +811,13 @@ def _words(t: Optional[torch.Tensor], dev: torch.device, what: str) -> Optional[
     """``t`` as contiguous int32 on ``dev``."""
     if t is None:
         return None
-    if t.is_floating_point() or t.dtype == torch.bool:
-        raise ValueError(f"{what} must be whole numbers")
-    return _like(t, dev, torch.int32)
+    if t.dtype is not torch.int32:
+        if t.is_floating_point() or t.dtype == torch.bool:
+            raise ValueError(f"{what} must be whole numbers")
+        t = t.to(torch.int32)
+    if t.device != dev:
+        t = t.to(dev)
+    return t.contiguous()
 
 
 def _tree_layout(total: int, B: Optional[int], cu_nodes: Optional[torch.Tensor], n: Optional[int], what: str):
@@ -855,8 +861,11 @@ def _verify_tree(rows, choices, tokens, parents, cu_nodes, n) -> TreeResult:
         if parents.numel() != total:
             raise ValueError("parents must have one entry for each token")
         parents = _words(parents, dev, "parents")
-    out = torch.empty((3, B), dtype=torch.int32, device=dev)
-    path = torch.empty((B, n), dtype=torch.int32, device=dev)
+    # one buffer for all results: n_accepted, next_token, status, path
+    out = torch.empty((3 + max(n, 0)) * B, dtype=torch.int32, device=dev)
+    acc, nxt, status, path = out.split((B, B, B, max(n, 0) * B))
+    p = out.data_ptr()
+    where = (p, p + 4 * B, p + 12 * B, p + 8 * B)  # n_accepted, next_token, path, status
     lib = _lib.load()
     if choices is None:
         dtype = _DTYPES.get(rows.dtype)
@@ -873,14 +882,13 @@ def _verify_tree(rows, choices, tokens, parents, cu_nodes, n) -> TreeResult:
         if stride < V and total > 1:
             rows, stride = rows.contiguous(), V
         _launch(dev, lib.sv_verify_tree_greedy, rows.data_ptr(), dtype, stride, tokens.data_ptr(), _p(parents), _p(cu),
-                B, n, total, V, out.data_ptr(), out.data_ptr() + 4 * B, path.data_ptr(), out.data_ptr() + 8 * B, None, 0)
+                B, n, total, V, *where, None, 0)
     else:
         if choices.numel() != total:
             raise ValueError("choices must have one entry for each token")
         choices = _words(choices, dev, "choices")
-        _launch(dev, lib.sv_verify_tree, choices.data_ptr(), tokens.data_ptr(), _p(parents), _p(cu), B, n, total,
-                out.data_ptr(), out.data_ptr() + 4 * B, path.data_ptr(), out.data_ptr() + 8 * B)
-    return TreeResult(out[0], out[1], path, out[2])
+        _launch(dev, lib.sv_verify_tree, choices.data_ptr(), tokens.data_ptr(), _p(parents), _p(cu), B, n, total, *where)
+    return TreeResult(acc, nxt, path.view(B, n), status)
 
 
 def verify_tree_greedy(target: torch.Tensor, tokens: torch.Tensor, parents: Optional[torch.Tensor] = None,
@@ -904,6 +912,9 @@ def verify_tree(choices: torch.Tensor, tokens: torch.Tensor, parents: Optional[t
     ``next_token``); what is emitted then follows the target's distribution
     whatever the tree holds."""
     return _verify_tree(None, choices, tokens, parents, cu_nodes, n)
+
+
+_ATTENTION = struct.Struct("37q")  # sv_tree_attn (include/sv_tree.h)
 
 
 @functools.lru_cache(maxsize=64)
@@ -945,9 +956,10 @@ def tree_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_cache: t
     dtype = _DTYPES.get(q.dtype)
     if dtype is None or dtype == _lib.SV_F32:
         raise ValueError("q must be bfloat16 or float16")
-    for t, what in ((k, "k"), (v, "v"), (k_cache, "k_cache"), (v_cache, "v_cache")):
-        if t.dtype != q.dtype or t.device != dev:
-            raise ValueError(f"{what} must have the type and device of q")
+    kind = q.dtype
+    if not (k.dtype == v.dtype == k_cache.dtype == v_cache.dtype == kind
+            and k.device == v.device == k_cache.device == v_cache.device == dev):
+        raise ValueError("k, v, k_cache and v_cache must have the type and device of q")
     if q.dim() == 4 and k.dim() == 4 and v.dim() == 4 and cu_nodes is None:
         if n is None:
             n = q.shape[1]
@@ -972,10 +984,10 @@ def tree_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_cache: t
             raise ValueError("parents must have one entry for each row of q")
         parents = _words(parents, dev, "parents")
     q, k, v = _aligned(q), _aligned(k), _aligned(v)
-    for t, what in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        s = t.stride()
-        if (s[3] != 1 and D > 1) or s[0] % 8 or s[1] % 8 or s[2] % 8 or t.data_ptr() % 16:
-            raise ValueError(f"{what} must have unit stride along the head dimension, its address and other strides multiples of 16 bytes")
+    kc, vc = k_cache.stride(), v_cache.stride()
+    kp, vp = k_cache.data_ptr(), v_cache.data_ptr()
+    if (kc[3] != 1 or vc[3] != 1) and D > 1 or (kc[0] | kc[1] | kc[2] | vc[0] | vc[1] | vc[2]) % 8 or (kp | vp) % 16:
+        raise ValueError("the caches must have unit stride along the head dimension, their addresses and other strides multiples of 16 bytes")
     if out is None:
         out = torch.empty((total, Hq, D), dtype=q.dtype, device=dev)
     elif (out.shape[0] < total or out.shape[1:] != q.shape[1:] or out.dtype != q.dtype or out.device != dev or out.stride(2) != 1
@@ -985,12 +997,12 @@ def tree_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_cache: t
     status = torch.empty(B, dtype=torch.int32, device=dev)
     need = _attention_bytes(D)
     workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    qs, ks, vs, os, kc, vc = q.stride(), k.stride(), v.stride(), out.stride(), k_cache.stride(), v_cache.stride()
-    words = (dtype, Hq, Hkv, D, q.data_ptr(), k.data_ptr(), v.data_ptr(), qs[0], qs[1], ks[0], ks[1], vs[0], vs[1],
-             k_cache.data_ptr(), v_cache.data_ptr(), kc[0], kc[1], kc[2], vc[0], vc[1], vc[2], k_cache.shape[0],
+    qs, ks, vs, os = q.stride(), k.stride(), v.stride(), out.stride()
+    words = _ATTENTION.pack(dtype, Hq, Hkv, D, q.data_ptr(), k.data_ptr(), v.data_ptr(), qs[0], qs[1], ks[0], ks[1], vs[0], vs[1],
+             kp, vp, kc[0], kc[1], kc[2], vc[0], vc[1], vc[2], k_cache.shape[0],
              k_cache.shape[1], table.data_ptr(), table.stride(0), table.shape[1], lengths.data_ptr(), _p(parents) or 0,
              _p(cu) or 0, B, n, total, out.data_ptr(), os[0], os[1], lse.data_ptr(), status.data_ptr())
-    _launch(dev, _lib.load().sv_tree_attention, (ctypes.c_int64 * 37)(*words),
+    _launch(dev, _lib.load().sv_tree_attention, words,
             D ** -0.5 if scale is None else float(scale), workspace.data_ptr(), need)
     return TreeAttention(out, lse, status)
 
@@ -1019,6 +1031,13 @@ def paged_cache(layers: int, pages: int, page_size: int, heads: int, dim: int, s
     return PagedCache(pool(), pool(), word(*shape, max_pages), word(*shape), word(pages))
 
 
+_PAGES = struct.Struct("8q")  # sv_cache_pages (include/sv_cache.h)
+_ROWS = struct.Struct("7q")  # sv_cache_rows
+_kind = attrgetter("dtype")
+_shape = attrgetter("shape")
+_grad = attrgetter("requires_grad")
+
+
 def _pages_arg(c: PagedCache) -> tuple:
     """(words of sv_cache_pages, sequences, device) of a checked cache."""
     table, lengths, refs = c.table, c.lengths, c.refs
@@ -1044,8 +1063,8 @@ def _pages_arg(c: PagedCache) -> tuple:
     sequences = lengths.numel()
     if max(sequences, pool.shape[0], pool.shape[1], table.shape[-1]) >= 2**31:
         raise ValueError("sizes must be below 2^31")
-    words = (ctypes.c_int64 * 8)(table.data_ptr(), stride, table.shape[-1], lengths.data_ptr(), refs.data_ptr(),
-                                 pool.shape[0], pool.shape[1], sequences)
+    words = _PAGES.pack(table.data_ptr(), stride, table.shape[-1], lengths.data_ptr(), refs.data_ptr(), pool.shape[0],
+                        pool.shape[1], sequences)
     return words, sequences, dev
 
 
@@ -1079,8 +1098,8 @@ def cache_append(cache: PagedCache, keys: Union[torch.Tensor, Sequence[torch.Ten
     pool = cache.keys[0]
     P, page, H, D = pool.shape
     strides, dtype = pool.stride(), pool.dtype
-    if strides[3] != 1 and D > 1:
-        raise ValueError("the pools must have unit stride along the head dimension")
+    if strides[3] != 1 and D > 1 or any(s == 0 and n > 1 for n, s in zip(pool.shape, strides)):
+        raise ValueError("the pools must have unit stride along the head dimension, and be no broadcast views")
     first = keys[0]
     if first.dim() == 4 and cu_nodes is None:
         if n is None:
@@ -1091,35 +1110,28 @@ def cache_append(cache: PagedCache, keys: Union[torch.Tensor, Sequence[torch.Ten
     if n is None and path is not None:
         n = path.shape[-1]
     _, n = _tree_layout(total, S, cu_nodes, n, "keys")
-    grad = torch.is_grad_enabled()
-    pools, rows, keep, seen, layout = [], [], [], set(), None
-    for t, x in ((a, b) for both in ((cache.keys, keys), (cache.values, values)) for a, b in zip(*both)):
-        if t.shape != pool.shape or t.stride() != strides or t.dtype != dtype or t.device != dev:
-            raise ValueError("the pools must be alike: shape, strides, type, device")
-        if x.dim() == 4 and cu_nodes is None:
-            x = x.flatten(0, 1)
-        if x.shape != (total, H, D) or x.dtype != dtype or x.device != dev:
-            raise ValueError(f"new rows must be [{total}, {H}, {D}] of the pools' type, on their device")
-        if grad and (t.requires_grad or x.requires_grad):
-            raise ValueError("the cache is modified in place: no gradients")
-        s = x.stride()
-        if layout is None and (s[2] == 1 or D <= 1):
-            layout = s
-        if s != layout:
-            x = x.contiguous()
-            if layout is None:
-                layout = x.stride()
-            elif x.stride() != layout:  # the first rows' strides serve all
-                y = torch.empty_strided((total, H, D), layout, dtype=dtype, device=dev)
-                x = y.copy_(x)
-            keep.append(x)
-        p = t.data_ptr()
-        if p in seen:
-            raise ValueError("a pool is listed twice")
-        seen.add(p)
-        pools.append(p)
-        rows.append(x.data_ptr())
-    if any(r in seen for r in rows if r):
+    # (the same few questions to every tensor of every layer: asked in C, the answers gathered in sets)
+    held, new = (*cache.keys, *cache.values), [*keys, *values]
+    kinds = {dtype}
+    if (set(map(_shape, held)) != {pool.shape} or set(map(torch.Tensor.stride, held)) != {strides}
+            or set(map(_kind, held)) != kinds or set(map(torch.Tensor.get_device, held)) != {dev.index}):
+        raise ValueError("the pools must be alike: shape, strides, type, device")
+    if first.dim() == 4 and cu_nodes is None:
+        new = [x.flatten(0, 1) for x in new]
+    if (set(map(_shape, new)) != {(total, H, D)} or set(map(_kind, new)) != kinds
+            or set(map(torch.Tensor.get_device, new)) != {dev.index}):
+        raise ValueError(f"new rows must be [{total}, {H}, {D}] of the pools' type, on their device")
+    if torch.is_grad_enabled() and (any(map(_grad, held)) or any(map(_grad, new))):
+        raise ValueError("the cache is modified in place: no gradients")
+    if len(set(map(torch.Tensor.stride, new))) > 1 or new[0].stride(2) != 1 and D > 1:
+        new = [x.contiguous() for x in new]  # (one layout serves all)
+        new = [x if x.stride() == new[0].stride() else torch.empty_like(new[0]).copy_(x) for x in new]
+    layout = new[0].stride()
+    pools, rows = list(map(torch.Tensor.data_ptr, held)), list(map(torch.Tensor.data_ptr, new))
+    seen = set(pools)
+    if len(seen) != len(pools):
+        raise ValueError("a pool is listed twice")
+    if not seen.isdisjoint(rows) and total:
         raise ValueError("new rows are a pool too: they would change while they are read")
     counts, path, cu = _words(counts, dev, "counts"), _words(path, dev, "path"), _words(cu_nodes, dev, "cu_nodes")
     if counts is not None and counts.numel() != S:
@@ -1132,10 +1144,10 @@ def cache_append(cache: PagedCache, keys: Union[torch.Tensor, Sequence[torch.Ten
     status = torch.empty(cache.lengths.shape, dtype=torch.int32, device=dev)
     need = _append_bytes(S, n, P, page)
     workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    where = (ctypes.c_int64 * 7)(strides[0] * e, strides[1] * e, strides[2] * e, layout[0] * e, layout[1] * e, H, D * e)
-    _launch(dev, _lib.load().sv_cache_append, pages, where, (ctypes.c_int64 * len(pools))(*pools),
-            (ctypes.c_int64 * len(rows))(*rows), len(pools), _p(counts), _p(path), _p(cu), n, total, status.data_ptr(),
-            workspace.data_ptr(), need)
+    where = _ROWS.pack(strides[0] * e, strides[1] * e, strides[2] * e, layout[0] * e, layout[1] * e, H, D * e)
+    addresses = struct.Struct(f"{len(pools)}q")
+    _launch(dev, _lib.load().sv_cache_append, pages, where, addresses.pack(*pools), addresses.pack(*rows), len(pools),
+            _p(counts), _p(path), _p(cu), n, total, status.data_ptr(), workspace.data_ptr(), need)
     return status
 
 
