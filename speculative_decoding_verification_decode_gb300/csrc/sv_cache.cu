@@ -24,7 +24,9 @@
 namespace svc {
 
 constexpr int kPlanThreads = 1024;
+constexpr int kScan = 16;  // pages that a thread looks at in a round
 constexpr int kCopyThreads = 256;
+constexpr int kGroup = 4;    // pools that a CTA copies side by side
 constexpr int kPools = 64;  // per launch: their addresses are kernel parameters
 
 struct Pages {
@@ -141,6 +143,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
   __shared__ int s_last[kPlanThreads], s_start[kPlanThreads];
   const Pages& c = P.c;
   const int t = static_cast<int>(threadIdx.x);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // requests
   int any = 0;
   for (int b = t; b < c.S; b += kPlanThreads) {
@@ -183,21 +186,25 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     if (b < c.S) P.seq[b].offset = want + at;
     want += all;
   }
-  // the lowest free pages
+  // the lowest free pages, 16 per thread and round
   int found = 0;
-  for (int p0 = 0; p0 < c.pages && found < want; p0 += 4 * kPlanThreads) {
-    const int p = p0 + 4 * t;
-    int free = 0;
+  const bool vec = (reinterpret_cast<uintptr_t>(c.refs) & 15) == 0;
+  for (int p0 = 0; p0 < c.pages && found < want; p0 += kScan * kPlanThreads) {
+    const int p = p0 + kScan * t;
+    unsigned free = 0;
+    if (vec && p + kScan <= c.pages) {
+      int4 r[kScan / 4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) free |= p + j < c.pages && c.refs[p + j] == 0 ? 1 << j : 0;
+      for (int j = 0; j < kScan / 4; ++j) r[j] = *reinterpret_cast<const int4*>(c.refs + p + 4 * j);
+#pragma unroll
+      for (int j = 0; j < kScan / 4; ++j)
+        free |= ((r[j].x == 0) | (r[j].y == 0) << 1 | (r[j].z == 0) << 2 | (r[j].w == 0) << 3) << (4 * j);
+    } else {
+      for (int j = 0; j < kScan; ++j) free |= p + j < c.pages && c.refs[p + j] == 0 ? 1u << j : 0u;
+    }
     int all;
     int at = found + block_scan(__popc(free), all, warp_sums);
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (free >> j & 1) {
-        if (at < P.cap) P.list[at] = p + j;
-        ++at;
-      }
+    for (; free && at < P.cap; free &= free - 1) P.list[at++] = p + __ffs(free) - 1;
     found += all;
   }
   __syncthreads();
@@ -258,27 +265,33 @@ struct Copy {
   const int* table;
   long long table_stride;
   long long page_stride, token_stride, head_stride, row_stride, row_head_stride;
-  int heads, units, page, n, pools, group;
+  int heads, units, page, n, pools;
   unsigned groups, splits;
 };
 
-// A CTA takes a sequence's rows in `group` pools: units of U, consecutive
-// threads on consecutive units of a row.
+// A CTA takes a share of a sequence's rows in up to kGroup pools: units of U,
+// consecutive threads on consecutive units of a row, the group's loads in flight
+// together.
 template <typename U>
 __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constant__ Copy P) {
   unsigned cta = blockIdx.x;
-  const int g = static_cast<int>(cta % P.groups) * P.group;
+  const int g = static_cast<int>(cta % P.groups) * kGroup;
   cta /= P.groups;
   const int split = static_cast<int>(cta % P.splits), b = static_cast<int>(cta / P.splits);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const Seq q = P.seq[b];
   if (q.count == 0) return;
   const int part = q.from >= 0 ? q.start % P.page : 0;
   const int* table = P.table + b * P.table_stride;
+  const int n = P.pools - g < kGroup ? P.pools - g : kGroup;
+  // (fewer than 2^31 units in a token, and the tokens' product in 64 bits)
   const int per_token = P.heads * P.units;
   const long long items = static_cast<long long>(q.count + part) * per_token;
   for (long long i = static_cast<long long>(split) * kCopyThreads + threadIdx.x; i < items;
        i += static_cast<long long>(P.splits) * kCopyThreads) {
-    const int t = static_cast<int>(i / per_token), r = static_cast<int>(i - static_cast<long long>(t) * per_token);
+    const int t = items < 0x7FFFFFFF ? static_cast<int>(static_cast<unsigned>(i) / static_cast<unsigned>(per_token))
+                                     : static_cast<int>(i / per_token);
+    const int r = static_cast<int>(i - static_cast<long long>(t) * per_token);
     const int h = r / P.units, x = r - h * P.units;
     long long src, dst;
     const bool fresh = t < q.count;
@@ -294,9 +307,13 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constan
     }
     src += x * static_cast<long long>(sizeof(U));
     dst += x * static_cast<long long>(sizeof(U));
-    const int end = g + P.group < P.pools ? g + P.group : P.pools;
-    for (int k = g; k < end; ++k)
-      *reinterpret_cast<U*>(P.pool[k] + dst) = *reinterpret_cast<const U*>((fresh ? P.rows[k] : P.pool[k]) + src);
+    U v[kGroup];
+#pragma unroll
+    for (int k = 0; k < kGroup; ++k)
+      if (k < n) v[k] = *reinterpret_cast<const U*>((fresh ? P.rows[g + k] : P.pool[g + k]) + src);
+#pragma unroll
+    for (int k = 0; k < kGroup; ++k)
+      if (k < n) *reinterpret_cast<U*>(P.pool[g + k] + dst) = v[k];
   }
 }
 
@@ -508,27 +525,34 @@ sv_status sv_cache_append(const sv_cache_pages* cache, const sv_cache_rows* layo
   C.page = P.c.page;
   C.n = n;
   C.splits = static_cast<unsigned>(splits);
-  C.group = 1;
   for (int i = 0; i < n_pools; i += svc::kPools) {
     C.pools = n_pools - i < svc::kPools ? n_pools - i : svc::kPools;
     for (int k = 0; k < C.pools; ++k) {
       C.pool[k] = static_cast<char*>(pools[i + k]);
       C.rows[k] = static_cast<const char*>(rows[i + k]);
     }
-    C.groups = static_cast<unsigned>((C.pools + C.group - 1) / C.group);
-    const unsigned grid = C.groups * static_cast<unsigned>(splits * S);
+    C.groups = static_cast<unsigned>((C.pools + svc::kGroup - 1) / svc::kGroup);
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(C.groups * static_cast<unsigned>(splits * S));
+    cfg.blockDim = dim3(svc::kCopyThreads);
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = i == 0 ? 1 : 0;  // (behind the first kernel; a later launch waits for all before it)
+    cudaError_t e;
     if (unit == 16)
-      svc::copy_kernel<uint4><<<grid, svc::kCopyThreads, 0, st>>>(C);
+      e = cudaLaunchKernelEx(&cfg, svc::copy_kernel<uint4>, C);
     else if (unit == 8)
-      svc::copy_kernel<uint2><<<grid, svc::kCopyThreads, 0, st>>>(C);
+      e = cudaLaunchKernelEx(&cfg, svc::copy_kernel<uint2>, C);
     else if (unit == 4)
-      svc::copy_kernel<unsigned><<<grid, svc::kCopyThreads, 0, st>>>(C);
+      e = cudaLaunchKernelEx(&cfg, svc::copy_kernel<unsigned>, C);
     else if (unit == 2)
-      svc::copy_kernel<unsigned short><<<grid, svc::kCopyThreads, 0, st>>>(C);
+      e = cudaLaunchKernelEx(&cfg, svc::copy_kernel<unsigned short>, C);
     else
-      svc::copy_kernel<unsigned char><<<grid, svc::kCopyThreads, 0, st>>>(C);
-    s = svc::launched();
-    if (s != SV_OK) return s;
+      e = cudaLaunchKernelEx(&cfg, svc::copy_kernel<unsigned char>, C);
+    if (e != cudaSuccess) return svh::fail(SV_ERR_CUDA, "kernel launch: %s", cudaGetErrorString(e));
   }
   return SV_OK;
 }

@@ -57,14 +57,71 @@ __device__ __forceinline__ float value(float x) { return x; }
 __device__ __forceinline__ float value(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float value(__half x) { return __half2float(x); }
 
-// Best of elements lo..hi of a row for this thread; `nan` tells of any NaN.
-template <typename T>
-__device__ __forceinline__ uint64_t best_of(const T* row, int lo, int hi, bool& nan) {
+// Largest of a 16-byte vector's elements; NaN if there is one among them.
+template <typename E>
+__device__ __forceinline__ float top_of(uint4 v);
+template <>
+__device__ __forceinline__ float top_of<float>(uint4 v) {
+  return svk::fmax_nan(svk::fmax_nan(__uint_as_float(v.x), __uint_as_float(v.y)),
+                       svk::fmax_nan(__uint_as_float(v.z), __uint_as_float(v.w)));
+}
+template <>
+__device__ __forceinline__ float top_of<__nv_bfloat16>(uint4 v) {
+  const uint32_t m = svk::bf16x2_max_nan(svk::bf16x2_max_nan(v.x, v.y), svk::bf16x2_max_nan(v.z, v.w));
+  return svk::fmax_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
+}
+template <>
+__device__ __forceinline__ float top_of<__half>(uint4 v) {
+  const uint32_t m = svk::f16x2_max_nan(svk::f16x2_max_nan(v.x, v.y), svk::f16x2_max_nan(v.z, v.w));
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&m));
+  return svk::fmax_nan(f.x, f.y);
+}
+
+// Best of elements lo..hi of a row for this thread; `nan` tells of any NaN.  A
+// 16-byte vector counts through its largest element; only the vector that
+// holds the thread's best is looked at again.
+template <typename E>
+__device__ __forceinline__ uint64_t best_of(const E* row, int lo, int hi, bool& nan) {
+  constexpr int kVec = 16 / static_cast<int>(sizeof(E));
   uint64_t best = 0;
-  for (int i = lo + static_cast<int>(threadIdx.x); i < hi; i += kThreads) {
+  auto one = [&](int i) {
     const float x = value(row[i]);
     nan = nan || x != x;
     const uint64_t k = x != x ? 0 : key_of(x, i);
+    best = best > k ? best : k;
+  };
+  const int t = static_cast<int>(threadIdx.x);
+  // elements before the first 16-byte boundary, and behind the last
+  const int off = static_cast<int>((reinterpret_cast<uintptr_t>(row + lo) & 15) / sizeof(E));
+  int first = lo + (off ? kVec - off : 0);
+  first = first < hi ? first : hi;
+  const int vectors = (hi - first) / kVec, rest = first + vectors * kVec;
+  if (t < first - lo) one(lo + t);
+  if (t < hi - rest) one(rest + t);
+  const uint4* p = reinterpret_cast<const uint4*>(row + first);
+  float top = -INFINITY;
+  int at = -1;
+  constexpr int kFly = 8;  // loads in flight
+  for (int i = t; i < vectors; i += kFly * kThreads) {
+    uint4 v[kFly];
+#pragma unroll
+    for (int j = 0; j < kFly; ++j)
+      if (i + j * kThreads < vectors) v[j] = __ldg(p + i + j * kThreads);
+#pragma unroll
+    for (int j = 0; j < kFly; ++j) {
+      if (i + j * kThreads >= vectors) break;
+      float x = top_of<E>(v[j]);
+      if (x != x) {  // one element at a time
+        for (int e = 0; e < kVec; ++e) one(first + (i + j * kThreads) * kVec + e);
+        continue;
+      }
+      if (at < 0 || x > top) top = x, at = i + j * kThreads;
+    }
+  }
+  if (at >= 0) {
+    int e = 0;
+    while (e < kVec - 1 && value(row[first + at * kVec + e]) != top) ++e;
+    const uint64_t k = key_of(top, first + at * kVec + e);
     best = best > k ? best : k;
   }
   return best;
