@@ -140,7 +140,8 @@ __device__ __forceinline__ void assign(const Plan& P, int b, const Seq& q) {
 
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ Plan P) {
   __shared__ int warp_sums[32];
-  __shared__ int s_last[kPlanThreads], s_start[kPlanThreads];
+  __shared__ __align__(16) int s_last[kPlanThreads];
+  __shared__ int s_start[kPlanThreads];
   const Pages& c = P.c;
   const int t = static_cast<int>(threadIdx.x);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -166,11 +167,17 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
         __syncthreads();
         const int end = a0 == b0 ? t : kPlanThreads;
         if (mine >= 0)
-          for (int a = 0; a < end; ++a)
-            if (s_last[a] == mine) {
-              ++before;
-              further = further || s_start[a] > start % c.page;
-            }
+          for (int a = 0; a < end; a += 4) {
+            const int4 four = *reinterpret_cast<const int4*>(s_last + a);
+            const bool same[4] = {four.x == mine, four.y == mine, four.z == mine, four.w == mine};
+            if (same[0] | same[1] | same[2] | same[3])
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                if (same[j] && a + j < end) {
+                  ++before;
+                  further = further || s_start[a + j] > start % c.page;
+                }
+          }
         __syncthreads();
       }
       if (mine >= 0 && (c.refs[mine] - before > 1 || further)) take_copy(P.seq[b]);  // (counts change further down)
@@ -341,6 +348,7 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(const __grid_constan
                                                              unsigned* status) {
   __shared__ int s_len[SV_CACHE_MAX_WIDTH], s_parent[SV_CACHE_MAX_WIDTH];
   __shared__ int s_held[kStaged];
+  __shared__ unsigned char s_used[SV_CACHE_MAX_WIDTH];  // the slot moves, or another takes what it has
   __shared__ int s_bad[8], s_most;
   const int rank = static_cast<int>(svk::cluster_rank()), size = static_cast<int>(svk::cluster_size());
   const int group = static_cast<int>(blockIdx.x) / size;
@@ -356,12 +364,14 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(const __grid_constan
     if (p < 0 || p >= W) p = w;
     s_parent[w] = p;
     s_len[w] = c.lengths[slot0 + w];
+    s_used[w] = 0;
   }
   __syncthreads();
   // slots that take part: those that move and their parents
   for (int w = t; w < W; w += kForkThreads) {
     const int p = s_parent[w];
     if (p == w) continue;
+    s_used[w] = s_used[p] = 1;
     const int a = s_len[w], d = s_len[p];
     const bool good = a >= 0 && d >= 0 && a <= c.max_pages * c.page && d <= c.max_pages * c.page;
     ok = ok && good;
@@ -370,19 +380,36 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(const __grid_constan
   ok = __syncthreads_and(ok);
   const int most = s_most;
   const int cols = kStaged / W;
+  // columns j0 .. j0 + k - 1 of every slot to shared memory, -1 past its length;
+  // false: a page that would be counted does not exist
+  auto stage = [&](int j0, int k) {
+    bool good = true;
+    for (int i = t; i < W * k; i += kForkThreads) {
+      const int w = i / k, j = j0 + i % k;
+      int e = -1;
+      if (j < pages_of(s_len[w], c.page)) {
+        e = table[w * c.stride + j];
+        if (s_used[w]) good = good && e >= 0 && e < c.pages;
+      }
+      s_held[i] = e;
+    }
+    return good;
+  };
+  auto width_of = [&](int j0) { return most - j0 < cols ? most - j0 : cols; };
+  const bool once = most <= size * cols;  // every CTA holds all its columns at a time
+  const int j_own = rank * cols;
   if (ok) {  // every page that would be counted exists
-    for (int j0 = rank * cols; j0 < most; j0 += size * cols) {
-      const int k = most - j0 < cols ? most - j0 : cols;
-      for (int i = t; i < W * k; i += kForkThreads) {
-        const int w = i / k, j = j0 + i % k, p = s_parent[w];
-        if (p == w) continue;
-        if (j < pages_of(s_len[w], c.page)) {
-          const int e = table[w * c.stride + j];
-          ok = ok && e >= 0 && e < c.pages;
-        }
-        if (j < pages_of(s_len[p], c.page)) {
-          const int e = table[p * c.stride + j];
-          ok = ok && e >= 0 && e < c.pages;
+    if (once) {
+      if (j_own < most) ok = stage(j_own, width_of(j_own));
+    } else {
+      for (int j0 = j_own; j0 < most; j0 += size * cols) {
+        const int k = width_of(j0);
+        for (int i = t; i < W * k; i += kForkThreads) {
+          const int w = i / k, j = j0 + i % k;
+          if (s_used[w] && j < pages_of(s_len[w], c.page)) {
+            const int e = table[w * c.stride + j];
+            ok = ok && e >= 0 && e < c.pages;
+          }
         }
       }
     }
@@ -393,13 +420,12 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(const __grid_constan
   for (int r = 0; r < size; ++r) ok = ok && s_bad[r] == 0;
   if (rank == 0 && t == 0) status[group] = ok ? 0u : SV_SEQ_BAD_LAYOUT;
   if (!ok) return;
-  for (int j0 = rank * cols; j0 < most; j0 += size * cols) {
-    const int k = most - j0 < cols ? most - j0 : cols;
-    for (int i = t; i < W * k; i += kForkThreads) {
-      const int w = i / k, j = i % k;
-      s_held[i] = j0 + j < pages_of(s_len[w], c.page) ? table[w * c.stride + j0 + j] : -1;
+  for (int j0 = j_own; j0 < most; j0 += size * cols) {
+    const int k = width_of(j0);
+    if (!once) {
+      stage(j0, k);
+      __syncthreads();
     }
-    __syncthreads();
     for (int i = t; i < W * k; i += kForkThreads) {
       const int w = i / k, j = i % k, p = s_parent[w];
       if (p == w) continue;

@@ -14,7 +14,7 @@
 
 namespace svt {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32, kMaxCluster = 8;
+constexpr int kThreads = 256, kWarps = kThreads / 32, kMaxCluster = 8;
 
 struct Tree {
   const int* tokens;
@@ -127,11 +127,9 @@ __device__ __forceinline__ uint64_t best_of(const E* row, int lo, int hi, bool& 
   return best;
 }
 
-struct Shared {
+struct __align__(16) Shared {
+  uint4 slot[2][kMaxCluster * kWarps];  // [step parity][warp of the cluster]: its best, whether it saw a NaN
   int token[SV_TREE_MAX_NODES], parent[SV_TREE_MAX_NODES];
-  uint64_t warp_best[kWarps];
-  uint64_t slot[2][kMaxCluster];  // [step parity][CTA]
-  uint32_t slot_nan[2][kMaxCluster];
   int next;
 };
 
@@ -182,7 +180,7 @@ __global__ void __launch_bounds__(256) walk_kernel(const __grid_constant__ Tree 
 }
 
 template <typename E>
-__global__ void __launch_bounds__(kThreads) greedy_kernel(const __grid_constant__ Tree T, const __grid_constant__ Rows R) {
+__global__ void __launch_bounds__(kThreads, 4) greedy_kernel(const __grid_constant__ Tree T, const __grid_constant__ Rows R) {
   __shared__ Shared sm;
   const int rank = static_cast<int>(svk::cluster_rank()), size = static_cast<int>(svk::cluster_size());
   const int b = static_cast<int>(blockIdx.x) / size, t = static_cast<int>(threadIdx.x), lane = t & 31;
@@ -203,45 +201,44 @@ __global__ void __launch_bounds__(kThreads) greedy_kernel(const __grid_constant_
       ++steps;
       bool nan = false;
       uint64_t best = best_of(static_cast<const E*>(R.data) + (static_cast<long long>(first) + at) * R.stride, lo, hi, nan);
+      nan = __any_sync(0xFFFFFFFFu, nan);
 #pragma unroll
       for (int d = 16; d; d /= 2) {
         const uint64_t o = __shfl_xor_sync(0xFFFFFFFFu, best, d);
         best = best > o ? best : o;
       }
-      if (lane == 0) sm.warp_best[t / 32] = best;
-      if (t == 0) sm.next = N;
-      const bool any_nan = __syncthreads_or(nan);
-      if (t < 32) {
-        best = lane < kWarps ? sm.warp_best[lane] : 0;
-#pragma unroll
-        for (int d = kWarps / 2; d; d /= 2) {
-          const uint64_t o = __shfl_xor_sync(0xFFFFFFFFu, best, d);
-          best = best > o ? best : o;
-        }
-        best = __shfl_sync(0xFFFFFFFFu, best, 0);
-        if (lane < size) {
-          svk::dsmem_st_v2(svk::dsmem_addr(&sm.slot[par][rank], lane),
-                           make_uint2(static_cast<uint32_t>(best), static_cast<uint32_t>(best >> 32)));
-          svk::dsmem_st_u32(svk::dsmem_addr(&sm.slot_nan[par][rank], lane), any_nan);
-        }
-      }
+      // every warp tells every CTA of the cluster, and every warp there works
+      // out the same: one barrier of the cluster a step, none of the CTA
+      if (lane < size)
+        svk::dsmem_st_v4(svk::dsmem_addr(&sm.slot[par][rank * kWarps + t / 32], lane),
+                         make_uint4(static_cast<uint32_t>(best), static_cast<uint32_t>(best >> 32), nan, 0));
       svk::cluster_sync_all();
       uint64_t top = 0;
-      for (int r = 0; r < size; ++r) {
-        top = top > sm.slot[par][r] ? top : sm.slot[par][r];
-        if (sm.slot_nan[par][r]) status |= SV_SEQ_BAD_VALUE;
+      nan = false;
+      for (int i = lane; i < size * kWarps; i += 32) {
+        const uint4 v = sm.slot[par][i];
+        const uint64_t k = static_cast<uint64_t>(v.y) << 32 | v.x;
+        top = top > k ? top : k;
+        nan = nan || v.z;
       }
+#pragma unroll
+      for (int d = 16; d; d /= 2) {
+        const uint64_t o = __shfl_xor_sync(0xFFFFFFFFu, top, d);
+        top = top > o ? top : o;
+      }
+      if (__any_sync(0xFFFFFFFFu, nan)) status |= SV_SEQ_BAD_VALUE;
       next = index_of(top);
       bool bad = false;
-      if (t > at && t < N && sm.parent[t] == at) {
-        bad = sm.token[t] < 0 || sm.token[t] >= R.V;
-        if (sm.token[t] == next) atomicMin(&sm.next, t);
-      }
-      if (__syncthreads_or(bad)) status |= SV_SEQ_BAD_TOKEN;
-      const int to = sm.next;
+      int to = N;
+      for (int i = at + 1 + lane; i < N; i += 32)
+        if (sm.parent[i] == at) {
+          bad = bad || sm.token[i] < 0 || sm.token[i] >= R.V;
+          if (sm.token[i] == next) to = to < i ? to : i;
+        }
+      if (__any_sync(0xFFFFFFFFu, bad)) status |= SV_SEQ_BAD_TOKEN;
+      to = __reduce_min_sync(0xFFFFFFFFu, to);
       if (to >= N) break;
       at = to;
-      __syncthreads();
     }
   }
   if (rank) return;
