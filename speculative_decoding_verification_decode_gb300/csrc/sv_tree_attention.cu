@@ -441,6 +441,8 @@ struct Num<__half> {
 // key tiles are K-major; value tiles are N-major, their leading stride is that
 // of the panels.
 // Instruction descriptor: D f32, A and B of the type, M = 128, N; B N-major.
+// kNegateA turns A's sign.
+constexpr uint32_t kNegateA = 1u << 13;
 template <typename T>
 __host__ __device__ constexpr uint32_t idesc(int N, bool n_major) {
   return (1u << 4) | (Num<T>::kType << 7) | (Num<T>::kType << 10) | (n_major ? 1u << 16 : 0u) |
@@ -757,6 +759,7 @@ __device__ __forceinline__ void issue(const Args& A, Shared& sm, uint32_t q_smem
   // (all lanes run the loops, so that addresses stay in uniform registers)
   const uint32_t q_lo = ((q_smem & 0x3FFFFu) >> 4) | 1u << 16, k_lo = ((k_ring & 0x3FFFFu) >> 4) | 1u << 16;
   const uint32_t v_lo = ((v_ring & 0x3FFFFu) >> 4) | (kTile * 128 / 16) << 16;
+  const uint32_t qk_desc = idesc<T>(kTile, false) | (A.flip ? kNegateA : 0u);  // (scores of a negative scale)
   auto full = [](uint32_t lo) { return static_cast<uint64_t>(kHi) << 32 | lo; };
   Steps qk, pv;
   qk.start(sm.plan);
@@ -780,7 +783,7 @@ __device__ __forceinline__ void issue(const Args& A, Shared& sm, uint32_t q_smem
 #pragma unroll
       for (int i = 0; i < DP / 16; ++i) {
         const uint32_t at = (i / 4) * (kTile * 128 / 16) + (i % 4) * 2;
-        mma_ss(d, full(a + at), full(b + at), idesc<T>(kTile, false), i > 0);
+        mma_ss(d, full(a + at), full(b + at), qk_desc, i > 0);
       }
       mma_commit(&sm.s_full[gq & 1]);
       if (last) mma_commit(&sm.k_empty[k_slot]);
@@ -822,7 +825,7 @@ __device__ __forceinline__ void issue(const Args& A, Shared& sm, uint32_t q_smem
 #pragma unroll
             for (int i = 0; i < DP / 16; ++i) {
               const uint32_t at = (i / 4) * (kTile * 128 / 16) + (i % 4) * 2;
-              mma_ss(s, full(q + at), full(k + at), idesc<T>(kTile, false), i > 0);
+              mma_ss(s, full(q + at), full(k + at), qk_desc, i > 0);
             }
             mma_commit(f);
             if (last) mma_commit(&sm.k_empty[k_slot]);
@@ -889,9 +892,8 @@ __device__ __forceinline__ void issue(const Args& A, Shared& sm, uint32_t q_smem
 }
 
 // Bits of the nodes of tree tile j that node i sees.
-__device__ __forceinline__ void seen_bits(const Args& A, int first, int i, int j, uint32_t (&w)[4]) {
-#pragma unroll
-  for (int x = 0; x < 4; ++x) w[x] = 0;
+__device__ __forceinline__ uint4 seen_bits(const Args& A, int first, int i, int j) {
+  uint32_t w[4] = {0, 0, 0, 0};
   auto set = [&](int k) {
     k -= j * kTile;
     if (k >= 0 && k < kTile) {
@@ -904,14 +906,15 @@ __device__ __forceinline__ void seen_bits(const Args& A, int first, int i, int j
     const int k = i - j * kTile;
 #pragma unroll
     for (int x = 0; x < 4; ++x) w[x] = k >= 32 * x + 31 ? 0xFFFFFFFFu : k >= 32 * x ? (2u << (k & 31)) - 1u : 0u;
-    return;
+  } else {
+    set(i);
+    for (int p = A.parents[first + i], was = i; p >= 0 && p < was;) {
+      set(p);
+      was = p;
+      p = A.parents[first + p];
+    }
   }
-  set(i);
-  for (int p = A.parents[first + i], was = i; p >= 0 && p < was;) {
-    set(p);
-    was = p;
-    p = A.parents[first + p];
-  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 template <typename T>
@@ -960,7 +963,10 @@ __device__ __forceinline__ void soften(const Args& A, Shared& sm, uint32_t tmem,
       const int keys = keys_of(s, t);
       const bool tree = t >= s.q.cached;
       uint32_t bits[4] = {0, 0, 0, 0};
-      if (busy && tree && row < rows) seen_bits(A, s.q.first, node, t - s.q.cached, bits);
+      if (busy && tree && row < rows) {
+        const uint4 seen = seen_bits(A, s.q.first, node, t - s.q.cached);
+        bits[0] = seen.x, bits[1] = seen.y, bits[2] = seen.z, bits[3] = seen.w;
+      }
       if (alive) alive = warp_wait(sm, &sm.s_full[stream], turns & 1);
       ++turns;
       fence_after();
@@ -973,17 +979,23 @@ __device__ __forceinline__ void soften(const Args& A, Shared& sm, uint32_t tmem,
             bits[i] = n >= 32 ? 0xFFFFFFFFu : n > 0 ? (1u << n) - 1u : 0u;
           }
         }
+        // what the row does not see becomes -inf, in tensor memory: few tiles need
+        // it, and the code of the others stays short
+        if (masked) {
+#pragma unroll 1
+          for (int i = 0; i < 4; ++i) {
+            uint32_t u[32];
+            tmem_ld32(s_col + i * 32, u);
+            const uint32_t bit = i == 0 ? bits[0] : i == 1 ? bits[1] : i == 2 ? bits[2] : bits[3];
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (!(bit >> j & 1)) u[j] = 0xFF800000u;
+            tmem_st32(s_col + i * 32, u);
+          }
+          tmem_st_wait();
+        }
         uint32_t u[kTile];
         tmem_ld128(s_col, u);
-        if (A.flip) {
-#pragma unroll
-          for (int j = 0; j < kTile; ++j) u[j] ^= 0x80000000u;
-        }
-        if (masked) {
-#pragma unroll
-          for (int j = 0; j < kTile; ++j)
-            if (!(bits[j / 32] >> (j % 32) & 1)) u[j] = 0xFF800000u;
-        }
         float* x = reinterpret_cast<float*>(u);
         float m0 = x[0], m1 = x[1], m2 = x[2], m3 = x[3];
 #pragma unroll
@@ -1089,11 +1101,10 @@ __device__ __forceinline__ void soften(const Args& A, Shared& sm, uint32_t tmem,
         if (odd_any && row < rows) {  // drafted values that are no finite numbers, of the nodes this one sees
           for (int tt = 0; tt < 2; ++tt) {
             if (s.q.cached + tt < s.t0 || s.q.cached + tt >= s.t1) continue;
-            uint32_t bits[4];
-            seen_bits(A, s.q.first, node, tt, bits);
-#pragma unroll
+            const uint4 seen = seen_bits(A, s.q.first, node, tt);
+#pragma unroll 1
             for (int x = 0; x < 4; ++x)
-              for (uint32_t left = bits[x] & sm.odd[tt * 4 + x]; left; left &= left - 1) {
+              for (uint32_t left = (x == 0 ? seen.x : x == 1 ? seen.y : x == 2 ? seen.z : seen.w) & sm.odd[tt * 4 + x]; left; left &= left - 1) {
                 const int k = tt * kTile + x * 32 + __ffs(left) - 1;
                 const uint16_t* v = static_cast<const uint16_t*>(A.v) + (static_cast<long long>(s.q.first) + k) * A.v_row + s.head * A.v_head;
 #pragma unroll
