@@ -83,8 +83,9 @@ __host__ __device__ constexpr int v_slots(int dp) { return dp == 128 ? 2 : 5; }
 struct __align__(16) Join {
   int parts;  // the CTAs behind it that have the others; 0: no such item
   int slot;   // of its part
+  int cta;
   int b, head, pair;
-  int first, N;
+  int unused;
   unsigned err;  // a wait gave up
 };
 
@@ -111,7 +112,8 @@ struct Args {
   bool flip;        // the scores' sign is turned (a negative scale)
   float* part;      // [2 CTAs][dp / 4][256 rows][4]: a warp, a row per lane, writes and reads whole lines
   float2* part_ml;  // [2 CTAs][256]: maximum (powers of two), sum
-  struct Join* join;  // [CTAs]
+  struct Join* join;  // [CTAs], then one per item where `pairs` > 0
+  int pairs;          // pairs of query tiles per key head, 0: more items than CTAs
   unsigned* status;
 };
 
@@ -146,14 +148,17 @@ __device__ __forceinline__ int row_node(const Args& A, int r) {
 }
 __device__ __forceinline__ int row_head(const Args& A, int r) { return r - row_node(A, r) * A.G; }
 
-// Steps of one key head: two per key tile for a pair of query tiles; the last
-// pair of a sequence may lack its second.
-__device__ __forceinline__ int steps_of_head(const Args& A, const Sequence& s) {
+// What a key tile costs: four units for a pair of query tiles (two steps of some
+// 1800 clocks), three for a single one (one step, but its 64 KB take the memory
+// 2800 clocks when all SMs ask).
+constexpr int kPairCost = 4, kSingleCost = 3;
+// Units of one key head; the last pair of a sequence may lack its second tile.
+__device__ __forceinline__ int units_of_head(const Args& A, const Sequence& s) {
   const bool odd = s.N <= (2 * s.items - 1) * A.per_tile;
-  return s.tiles * (2 * s.items - (odd ? 1 : 0));
+  return s.tiles * (kPairCost * s.items - (odd ? kPairCost - kSingleCost : 0));
 }
 __device__ __forceinline__ long long units_of(const Args& A, const Sequence& s) {
-  return s.N > 0 ? static_cast<long long>(steps_of_head(A, s)) * A.Hkv : 0;
+  return s.N > 0 ? static_cast<long long>(units_of_head(A, s)) * A.Hkv : 0;
 }
 
 // W units over CTAs 0 .. ctas - 1, the first `more` of which take one more than
@@ -190,7 +195,7 @@ struct Walk {
   int b;
   long long off, left;
   int count;     // segments so far
-  bool odd_end;  // the last one's cut lies inside a key tile
+  int rest;      // units of the last one's item behind it
 
   __device__ __forceinline__ bool next(const Args& A, Segment& s) {
     if (left <= 0) return false;
@@ -200,24 +205,24 @@ struct Walk {
       if (off < units_of(A, s.q)) break;
     }
     cut(A, s);
-    return s.steps > 0;  // (half a key tile at the end of a piece is none)
+    return s.steps > 0;  // (part of a key tile at the end of a piece is none)
   }
-  // The next segment, in sequence s.q; a cut inside a pair's key tile leaves the
-  // tile to the piece behind it.
+  // The next segment, in sequence s.q; a cut inside a key tile leaves the tile to
+  // the piece behind it.
   __device__ __forceinline__ void cut(const Args& A, Segment& s) {
-    const int per_head = steps_of_head(A, s.q);
+    const int per_head = units_of_head(A, s.q);
     s.head = off < per_head ? 0 : Cut::divide(off, per_head);
-    const int in_head = static_cast<int>(off - static_cast<long long>(s.head) * per_head), pair_steps = 2 * s.q.tiles;
-    s.pair = in_head < pair_steps ? 0 : in_head / pair_steps;
-    const int in = in_head - s.pair * pair_steps;
+    const int in_head = static_cast<int>(off - static_cast<long long>(s.head) * per_head), per_pair = kPairCost * s.q.tiles;
+    s.pair = in_head < per_pair ? 0 : in_head / per_pair;
+    const int in = in_head - s.pair * per_pair;
     s.b = b;
     s.two = s.q.N > (2 * s.pair + 1) * A.per_tile;
-    const int all = s.two ? pair_steps : s.q.tiles, end = all - in < left ? all : in + static_cast<int>(left);
-    s.t0 = s.two ? in >> 1 : in;
-    s.t1 = s.two ? end >> 1 : end;
+    const int all = s.two ? per_pair : kSingleCost * s.q.tiles, end = all - in < left ? all : in + static_cast<int>(left);
+    s.t0 = s.two ? in / kPairCost : in / kSingleCost;
+    s.t1 = s.two ? end / kPairCost : end / kSingleCost;
     s.whole = s.t0 == 0 && s.t1 == s.q.tiles;
     s.steps = (s.t1 - s.t0) * (s.two ? 2 : 1);
-    odd_end = s.two && (end & 1);
+    rest = all - end;
     off += end - in;
     left -= end - in;
     ++count;
@@ -292,10 +297,11 @@ __device__ __forceinline__ void make_plan(const Args& A, int C, int c, PlanMem& 
       W += v;
     }
   }
-  if (W <= static_cast<long long>(kFewSteps) * C && A.batch <= T) {
+  if (W <= static_cast<long long>(kFewSteps) * kPairCost / 2 * C && A.batch <= T) {
     // each item by itself, in the shortest pieces that C CTAs can take
-    const int least = W <= C ? 1 : static_cast<int>((static_cast<uint32_t>(W) + C - 1) / C);
-    bool fits = W <= C;
+    // (a piece has a key tile, of three units or more; a step costs no more than three)
+    const int least = W <= 3LL * C ? 1 : static_cast<int>(static_cast<uint32_t>(W) / (3u * static_cast<uint32_t>(C)));
+    bool fits = W <= 3LL * C;
     for (int limit = fits ? 1 : 2 * kFewSteps;;) {  // (whether the longest fit, then from the shortest on)
       const Pieces p = t < A.batch && q.N > 0 ? pieces_of(A, q, limit) : Pieces{0, 0, 0};
       const int count = p.head * A.Hkv;  // (no more than units)
@@ -350,8 +356,8 @@ __device__ __forceinline__ void make_plan(const Args& A, int C, int c, PlanMem& 
     }
     sync();
   }
-  Cut cut;  // (two steps at least: a piece of one may be half of a pair's key tile, none)
-  cut.ctas = W >= 2LL * C ? C : W >= 2 ? static_cast<int>(W / 2) : 1;
+  Cut cut;  // (a key tile's cost at least: a smaller piece may hold the end of none)
+  cut.ctas = W >= static_cast<long long>(kPairCost) * C ? C : W >= kPairCost ? static_cast<int>(W / kPairCost) : 1;
   cut.each = Cut::divide(W, cut.ctas);
   cut.more = static_cast<int>(W - cut.each * cut.ctas);
   const long long u = cut.begin(c);
@@ -1131,22 +1137,22 @@ __device__ __forceinline__ void soften(const Args& A, Shared& sm, uint32_t tmem,
         }
       }
     }
-    if (!s.whole && s.t0 == 0 && threadIdx.x == 0) {
+    if (s.t0 == 0 && threadIdx.x == 0 && (!s.whole || A.pairs)) {
       Join j;
-      j.parts = sm.plan.parts;
-      if (j.parts < 0) {  // the CTA that has the item's last step
-        const long long end = sm.plan.cut.begin(c + 1);
-        const int done = s.two ? 2 * s.t1 + static_cast<int>(w.odd_end) : s.t1;
-        j.parts = sm.plan.cut.owner(end + (s.two ? 2 : 1) * s.q.tiles - done - 1) - c;
+      j.parts = s.whole ? 0 : sm.plan.parts;
+      if (j.parts < 0) {  // up to the CTA that has the item's last unit
+        j.parts = sm.plan.cut.owner(sm.plan.cut.begin(c + 1) + w.rest - 1) - c;
       }
       j.slot = slot;
+      j.cta = c;
       j.b = s.b;
       j.head = s.head;
       j.pair = s.pair;
-      j.first = s.q.first;
-      j.N = s.q.N;
       j.err = 0;
-      sm.join = j;
+      if (A.pairs)
+        A.join[gridDim.x + (s.b * A.Hkv + s.head) * A.pairs + s.pair] = j;
+      else
+        sm.join = j;
     }
     if (mine && (s.two || stream == 0)) {
       if (!s.whole)
@@ -1271,13 +1277,13 @@ __device__ __forceinline__ bool bad_layout(const Args& A, int b, int t, int T) {
 }
 static_assert(kFinishThreads >= SV_TREE_MAX_NODES, "a thread per node");
 
-// Joins the parts of items that several CTAs had, 32 rows and 64 columns to a
-// CTA, and writes the statuses.
-constexpr int kJoinCols = 8;  // columns of a thread; a lane per row
-// kWide parts at a time, all their loads in flight: two where there are CTAs for
-// all the SM's room, eight where few items are in many parts.
-template <typename T, int DP, int kWide>
-__global__ void __launch_bounds__(kFinishThreads, kWide > 2 ? 2 : 5) finish_kernel(const __grid_constant__ Args A, int C, int chunks) {
+// Joins the parts of items that several CTAs had, 32 rows to a CTA, and writes the
+// statuses.
+// kWide parts at a time, all their loads in flight, and kCols columns of a
+// thread (a lane per row): eight of eight where few items are in many parts, two
+// of sixteen where most CTAs leave an item in two.
+template <typename T, int DP, int kWide, int kCols>
+__global__ void __launch_bounds__(kFinishThreads, kWide > 2 ? 2 : 4) finish_kernel(const __grid_constant__ Args A, int C, int chunks) {
   const int t = static_cast<int>(threadIdx.x);
   if (static_cast<int>(blockIdx.x) < A.batch) {  // a sequence's status
     const int b = static_cast<int>(blockIdx.x);
@@ -1301,30 +1307,43 @@ __global__ void __launch_bounds__(kFinishThreads, kWide > 2 ? 2 : 5) finish_kern
     }
     return;
   }
-  const int id = static_cast<int>(blockIdx.x) - A.batch, c = id / chunks, k = id % chunks;
-  constexpr int kColBlocks = DP / (8 * kJoinCols);  // chunks of a row's columns
+  const int id = static_cast<int>(blockIdx.x) - A.batch, which = id / chunks, k = id % chunks;
+  constexpr int kColBlocks = DP / (8 * kCols);  // chunks of a row's columns
   const int r = k / kColBlocks * kFinishRows + (t & 31);
-  const int col = (k % kColBlocks) * (8 * kJoinCols) + (t >> 5) * kJoinCols;
+  const int col = (k % kColBlocks) * (8 * kCols) + (t >> 5) * kCols;
+  bool bad = false;
+  Sequence q;
+  if (A.pairs) {  // the item's sequence is known before its parts are there
+    const int b = which / (A.Hkv * A.pairs);
+    q = sequence(A, b);
+    if (q.N <= 0 || which % A.pairs >= q.items) return;
+    bad = __syncthreads_or(bad_layout(A, b, t, kFinishThreads));
+  }
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const Join j = A.join[c];
-  if (j.parts == 0) return;
+  const Join j = A.join[A.pairs ? C + which : which];
+  // (nothing is read by a record that a CTA which gave up has not written)
+  if (j.parts <= 0 || j.cta < 0 || j.parts >= C - j.cta || j.slot < 0 || j.slot >= 2 * C || j.b < 0 || j.b >= A.batch) return;
+  if (!A.pairs) {
+    q = sequence(A, j.b);
+    bad = __syncthreads_or(bad_layout(A, j.b, t, kFinishThreads));
+  }
   const int query = 2 * j.pair + (r >= kTile ? 1 : 0), rr = r % kTile;
   const int node = query * A.per_tile + row_node(A, rr);
-  const bool mine = rr < A.per_tile * A.G && node < j.N && col < A.D;
-  float m = -INFINITY, sum = 0, o[kJoinCols] = {};
-  if (mine) {
+  if (bad || rr >= A.per_tile * A.G || node >= q.N || col >= A.D) return;  // (a bad sequence's rows are written where its status is)
+  float m = -INFINITY, sum = 0, o[kCols] = {};
+  {
     // the first part is the last segment of its CTA, the others are their CTAs' first
     const float2* ml = A.part_ml + r;
     const float* part = A.part + (col / 4 * 256 + r) * 4;
     for (int x0 = 0; x0 <= j.parts; x0 += kWide) {
       float2 e[kWide];
-      float4 v[kWide][kJoinCols / 4];
+      float4 v[kWide][kCols / 4];
 #pragma unroll
       for (int x = 0; x < kWide; ++x) {
-        const long long slot = x0 + x == 0 ? j.slot : 2LL * (c + (x0 + x <= j.parts ? x0 + x : j.parts));
+        const long long slot = x0 + x == 0 ? j.slot : 2LL * (j.cta + (x0 + x <= j.parts ? x0 + x : j.parts));
         e[x] = ml[slot * 256];
 #pragma unroll
-        for (int i = 0; i < kJoinCols / 4; ++i) v[x][i] = *reinterpret_cast<const float4*>(part + slot * 256 * DP + i * 1024);
+        for (int i = 0; i < kCols / 4; ++i) v[x][i] = *reinterpret_cast<const float4*>(part + slot * 256 * DP + i * 1024);
       }
       float top = m;
 #pragma unroll
@@ -1334,14 +1353,14 @@ __global__ void __launch_bounds__(kFinishThreads, kWide > 2 ? 2 : 5) finish_kern
       m = top;
       sum *= f;
 #pragma unroll
-      for (int i = 0; i < kJoinCols; ++i) o[i] *= f;
+      for (int i = 0; i < kCols; ++i) o[i] *= f;
 #pragma unroll
       for (int x = 0; x < kWide; ++x)
         if (x0 + x <= j.parts) {
           const float w = e[x].x == -INFINITY ? 0.0f : svk::ex2_ftz(e[x].x - top);
           sum = fmaf(e[x].y, w, sum);
 #pragma unroll
-          for (int i = 0; i < kJoinCols / 4; ++i) {
+          for (int i = 0; i < kCols / 4; ++i) {
             o[4 * i] = fmaf(v[x][i].x, w, o[4 * i]);
             o[4 * i + 1] = fmaf(v[x][i].y, w, o[4 * i + 1]);
             o[4 * i + 2] = fmaf(v[x][i].z, w, o[4 * i + 2]);
@@ -1350,14 +1369,13 @@ __global__ void __launch_bounds__(kFinishThreads, kWide > 2 ? 2 : 5) finish_kern
         }
     }
   }
-  // (a bad sequence's rows are written where its status is)
-  if (__syncthreads_or(bad_layout(A, j.b, t, kFinishThreads)) || !mine) return;
   const float inv = 1.0f / sum;
   const int qh = j.head * A.G + row_head(A, rr);
-  const long long at = static_cast<long long>(j.first) + node;
+  const long long at = static_cast<long long>(q.first) + node;
   T* dst = static_cast<T*>(A.out) + at * A.out_row + static_cast<long long>(qh) * A.out_head;
 #pragma unroll
-  for (int i = 0; i < kJoinCols; i += 8) store_out<T>(dst + col + i, o + i, inv);
+  for (int i = 0; i < kCols; i += 8)
+    if (col + i < A.D) store_out<T>(dst + col + i, o + i, inv);
   if (A.lse && col == 0) A.lse[at * A.q_heads + qh] = (m + log2f(sum)) * 0.69314718055994531f;
 }
 
@@ -1395,7 +1413,7 @@ bool encode(CUtensorMap* map, int64_t dtype, const void* data, int dims, const i
 
 size_t workspace_bytes_of(int dim) {
   const size_t rows = 2 * kMaxCtas * 256;
-  return rows * (dim <= 64 ? 64 : 128) * 4 + rows * 8 + kMaxCtas * sizeof(Join);
+  return rows * (dim <= 64 ? 64 : 128) * 4 + rows * 8 + 2 * kMaxCtas * sizeof(Join);
 }
 
 template <typename T, int DP>
@@ -1460,14 +1478,16 @@ sv_status launch(const sv_tree_attn& a, float scale, unsigned char* ws, cudaStre
     const cudaError_t e = cudaFuncSetAttribute(attend_kernel<T, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<DP>());
     if (e != cudaSuccess) return svh::fail(SV_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
     // (the same split of the SM's memory as the first kernel's: no change between the two)
-    cudaFuncSetAttribute(finish_kernel<T, DP, 2>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
-    cudaFuncSetAttribute(finish_kernel<T, DP, 8>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    cudaFuncSetAttribute(finish_kernel<T, DP, 2, DP / 8>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    cudaFuncSetAttribute(finish_kernel<T, DP, 8, 8>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
     int n = 0;
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = kMaxCtas;
     sms[dev] = n < kMaxCtas ? n : kMaxCtas;
     attr_set[dev] = true;
   }
   const int C = sms[dev];
+  const long long pairs = (a.n + 2 * A.per_tile - 1) / (2 * A.per_tile);
+  A.pairs = a.batch <= C && a.batch * a.kv_heads * pairs <= C ? static_cast<int>(pairs) : 0;
   if (a.total > 0) {
     attend_kernel<T, DP><<<C, kThreads, smem_bytes<DP>(), st>>>(A, qm, km, vm, kcm, vcm);
     const cudaError_t e = cudaGetLastError();
@@ -1476,8 +1496,8 @@ sv_status launch(const sv_tree_attn& a, float scale, unsigned char* ws, cudaStre
   // rows of a pair of query tiles, the second's from kTile on
   const int most = static_cast<int>(a.n > A.per_tile ? kTile + (a.n - A.per_tile < A.per_tile ? a.n - A.per_tile : A.per_tile) * A.G
                                                      : a.n * A.G);
-  const int chunks = (most + kFinishRows - 1) / kFinishRows * (DP / (8 * kJoinCols));
-  const int join = a.total > 0 ? C * chunks : 0;
+  const int chunks = (most + kFinishRows - 1) / kFinishRows * (A.pairs ? DP / 64 : 1);
+  const int join = a.total == 0 ? 0 : (A.pairs ? static_cast<int>(a.batch) * A.Hkv * A.pairs : C) * chunks;
   if (a.batch > 0x7FFFFFFF - join) return svh::fail(SV_ERR_UNSUPPORTED, "batch too large");
   const int grid = join + static_cast<int>(a.batch);
   cudaLaunchConfig_t cfg = {};
@@ -1489,9 +1509,8 @@ sv_status launch(const sv_tree_attn& a, float scale, unsigned char* ws, cudaStre
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = a.total > 0 ? 1 : 0;
-  const bool few = a.batch * a.kv_heads * ((a.n + 2 * A.per_tile - 1) / (2 * A.per_tile)) * 4 <= C;
-  const cudaError_t e = few ? cudaLaunchKernelEx(&cfg, finish_kernel<T, DP, 8>, A, a.total > 0 ? C : 0, chunks)
-                            : cudaLaunchKernelEx(&cfg, finish_kernel<T, DP, 2>, A, a.total > 0 ? C : 0, chunks);
+  const cudaError_t e = A.pairs ? cudaLaunchKernelEx(&cfg, finish_kernel<T, DP, 8, 8>, A, a.total > 0 ? C : 0, chunks)
+                                : cudaLaunchKernelEx(&cfg, finish_kernel<T, DP, 2, DP / 8>, A, a.total > 0 ? C : 0, chunks);
   return e == cudaSuccess ? SV_OK : svh::fail(SV_ERR_CUDA, "kernel launch: %s", cudaGetErrorString(e));
 }
 
