@@ -229,9 +229,11 @@ struct Walk {
   }
 };
 
-struct PlanMem {
+struct PlanScratch {
   long long warp_sums[kThreads / 32];
   int warp_counts[kThreads / 32];
+};
+struct PlanMem {
   Cut cut;
   Walk w;     // after the CTA's first segment
   Segment s;  // that
@@ -261,7 +263,7 @@ constexpr int kFewSequences = 32;
 // CTA's threads, or by every warp for itself (few sequences: all write the same
 // words, and none waits for another).
 template <bool kWarp>
-__device__ __forceinline__ void make_plan(const Args& A, int C, int c, PlanMem& m) {
+__device__ __forceinline__ void make_plan(const Args& A, int C, int c, PlanMem& m, PlanScratch& scratch) {
   constexpr int T = kWarp ? 32 : kThreads;
   const int lane = static_cast<int>(threadIdx.x & 31), warp = static_cast<int>(threadIdx.x >> 5), t = kWarp ? lane : static_cast<int>(threadIdx.x);
   auto sync = [] {
@@ -288,11 +290,11 @@ __device__ __forceinline__ void make_plan(const Args& A, int C, int c, PlanMem& 
   if (kWarp) {
     W = __shfl_sync(0xFFFFFFFFu, x, 31);
   } else {
-    if (lane == 31) m.warp_sums[warp] = x;
+    if (lane == 31) scratch.warp_sums[warp] = x;
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) {
-      const long long v = m.warp_sums[w];
+      const long long v = scratch.warp_sums[w];
       if (w < warp) before += v;
       W += v;
     }
@@ -315,11 +317,11 @@ __device__ __forceinline__ void make_plan(const Args& A, int C, int c, PlanMem& 
       if (kWarp) {
         all = __shfl_sync(0xFFFFFFFFu, y, 31);
       } else {
-        if (lane == 31) m.warp_counts[warp] = y;
+        if (lane == 31) scratch.warp_counts[warp] = y;
         __syncthreads();
 #pragma unroll
         for (int w = 0; w < kThreads / 32; ++w) {
-          const int v = m.warp_counts[w];
+          const int v = scratch.warp_counts[w];
           if (w < warp) ahead += v;
           all += v;
         }
@@ -385,30 +387,6 @@ __device__ __forceinline__ void make_plan(const Args& A, int C, int c, PlanMem& 
   }
   sync();
 }
-
-// Steps of a CTA one after another.
-struct Steps {
-  Walk w;
-  Segment s;
-  int k;   // step of the segment
-  bool ok;
-
-  __device__ __forceinline__ void start(const PlanMem& m) {
-    w = m.w;
-    s = m.s;
-    k = 0;
-    ok = m.any != 0;
-  }
-  __device__ __forceinline__ void advance(const Args& A) {
-    if (++k == s.steps) {
-      k = 0;
-      ok = w.next(A, s);
-    }
-  }
-  __device__ __forceinline__ int tile() const { return s.t0 + (s.two ? k >> 1 : k); }
-  __device__ __forceinline__ bool fresh() const { return !s.two || !(k & 1); }  // the first step with its key tile
-  __device__ __forceinline__ bool last() const { return !s.two || (k & 1); }    // and the last
-};
 
 // Keys of tile t that exist.
 __device__ __forceinline__ int keys_of(const Segment& s, int t) {
@@ -559,10 +537,24 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 
 // ------------------------------------------------------------------ the kernel
 
+// The segments of a CTA are worked out once, by the keys' producer, and handed to
+// the MMA and softmax warps in a ring: segment i + 1, and whether there is one,
+// stand there before segment i's last key tile has landed.  The producer is at
+// most k_slots tiles ahead of the scores, those two steps of the softmax, that
+// one segment of its epilogue, and one segment is written ahead: k_slots + 4 at
+// most.
+struct Entry {
+  Segment s;
+  int rest;  // Walk::rest
+  int more;  // there is a segment behind this one
+};
+
+template <int DP>
 struct __align__(16) Shared {
-  uint64_t k_full[5], k_empty[5];    // keys: producer -> MMA, MMA -> producer
-  uint64_t v_full[5], v_empty[5];    // values: producer -> MMA and mender, both -> producer
-  uint64_t v_mended[5];              // mender -> MMA
+  static constexpr int kQueue = k_slots(DP) + 6;
+  uint64_t k_full[k_slots(DP)], k_empty[k_slots(DP)];  // keys: producer -> MMA, MMA -> producer
+  uint64_t v_full[v_slots(DP)], v_empty[v_slots(DP)];  // values: producer -> MMA and mender, both -> producer
+  uint64_t v_mended[v_slots(DP)];    // mender -> MMA
   uint64_t q_full[2], q_empty[2];    // query tiles
   uint64_t s_full[2];                // MMA -> softmax: the stream's scores
   uint64_t p_full[2];                // softmax -> MMA: its weights
@@ -572,12 +564,52 @@ struct __align__(16) Shared {
   volatile int abort;
   Join join;
   PlanMem plan;
-  uint32_t v_odd[5][4];              // keys of a value tile of nodes whose values are no finite numbers
+  Entry queue[kQueue];               // segments behind the first, by number
+  uint32_t v_odd[v_slots(DP)][4];    // keys of a value tile of nodes whose values are no finite numbers
   uint32_t odd[8];                   // the segment's nodes with such values
-  float2 ex[2][kTile];               // [stream]: maximum, sum of each row
+  union {
+    float2 ex[2][kTile];             // [stream]: maximum, sum of each row
+    PlanScratch scratch;             // (before that)
+  };
 };
 
-__device__ __forceinline__ bool wait(Shared& sm, uint64_t* bar, uint32_t parity) {
+// Segment i (0: the plan's), and what the queue says of it.
+template <class S>
+__device__ __forceinline__ const Segment& segment(const S& sm, int i) {
+  return i ? sm.queue[i % S::kQueue].s : sm.plan.s;
+}
+
+// Steps of a CTA one after another.
+struct Steps {
+  int i;  // segment
+  Segment s;
+  int k;  // step of the segment
+  bool ok;
+
+  template <class S>
+  __device__ __forceinline__ void start(const S& sm) {
+    i = 0;
+    s = sm.plan.s;
+    k = 0;
+    ok = sm.plan.any != 0;
+  }
+  // (the segment's last key tile has landed)
+  template <class S>
+  __device__ __forceinline__ void advance(const S& sm) {
+    if (++k == s.steps) {
+      k = 0;
+      ok = sm.queue[i % S::kQueue].more != 0;
+      ++i;
+      if (ok) s = segment(sm, i);
+    }
+  }
+  __device__ __forceinline__ int tile() const { return s.t0 + (s.two ? k >> 1 : k); }
+  __device__ __forceinline__ bool fresh() const { return !s.two || !(k & 1); }  // the first step with its key tile
+  __device__ __forceinline__ bool last() const { return !s.two || (k & 1); }    // and the last
+};
+
+template <class S>
+__device__ __forceinline__ bool wait(S& sm, uint64_t* bar, uint32_t parity) {
   for (uint32_t i = 0; i < svk::kWaitPolls; ++i) {
     if (svk::mbar_try_wait(bar, parity)) return true;
     if (sm.abort) return false;
@@ -585,14 +617,25 @@ __device__ __forceinline__ bool wait(Shared& sm, uint64_t* bar, uint32_t parity)
   sm.abort = 1;
   return false;
 }
-__device__ __forceinline__ bool warp_wait(Shared& sm, uint64_t* bar, uint32_t parity) {
+template <class S>
+__device__ __forceinline__ bool warp_wait(S& sm, uint64_t* bar, uint32_t parity) {
   return __all_sync(0xFFFFFFFFu, wait(sm, bar, parity));
 }
 __device__ __forceinline__ void bar_soft() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kSoftWarps) : "memory"); }
 
+__device__ __forceinline__ bool all_soft(bool mine) {
+  int r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.s32 p, %1, 0;\n bar.red.and.pred q, 1, %2, p;\n selp.s32 %0, 1, 0, q;\n}"
+      : "=r"(r)
+      : "r"(static_cast<int>(mine)), "n"(32 * kSoftWarps)
+      : "memory");
+  return r != 0;
+}
+
 template <int DP>
 __host__ __device__ constexpr int smem_bytes() {
-  return (2 + k_slots(DP) + v_slots(DP)) * tile_bytes(DP) + static_cast<int>(sizeof(Shared));
+  return (2 + k_slots(DP) + v_slots(DP)) * tile_bytes(DP) + static_cast<int>(sizeof(Shared<DP>));
 }
 
 static_assert(smem_bytes<128>() <= 232448 && smem_bytes<64>() <= 232448, "a CTA's shared memory");
@@ -643,14 +686,29 @@ __device__ __forceinline__ void load_tile(const Args& A, const Segment& s, int t
 }
 
 template <int DP>
-__device__ __forceinline__ void produce_keys(const Args& A, Shared& sm, uint32_t ring, const CUtensorMap* km, const CUtensorMap* kcm) {
+__device__ __forceinline__ void produce_keys(const Args& A, Shared<DP>& sm, uint32_t ring, const CUtensorMap* km, const CUtensorMap* kcm) {
   constexpr int kSlots = k_slots(DP);
   const int lane = static_cast<int>(threadIdx.x & 31);
   Walk w = sm.plan.w;
   Segment s = sm.plan.s;
   uint32_t slot = 0, turn = 0, loads = 0;
   bool alive = true;
-  for (bool go = sm.plan.any; alive && go; go = w.next(A, s)) {
+  int i = 0;
+  for (bool go = sm.plan.any; alive && go; ++i) {
+    Segment behind;
+    bool more = false;
+    auto hand_over = [&]() {
+      more = w.next(A, behind);
+      if (lane == 0) {
+        if (more) {
+          sm.queue[(i + 1) % Shared<DP>::kQueue].s = behind;
+          sm.queue[(i + 1) % Shared<DP>::kQueue].rest = w.rest;
+        }
+        sm.queue[i % Shared<DP>::kQueue].more = more;
+      }
+      __syncwarp();
+    };
+    if (s.t1 - s.t0 == 1) hand_over();
     for (int t = s.t0; alive && t < s.t1; ++t) {
       const Box x = look_up<DP>(A, s, t, lane);
       if (turn) alive = warp_wait(sm, &sm.k_empty[slot], (turn - 1) & 1);
@@ -658,7 +716,10 @@ __device__ __forceinline__ void produce_keys(const Args& A, Shared& sm, uint32_t
       load_tile<DP>(A, s, t, x, kcm, km, ring + slot * tile_bytes(DP), &sm.k_full[slot], lane);
       ++loads;
       if (++slot == kSlots) slot = 0, ++turn;
+      if (t == s.t0 && s.t1 - s.t0 > 1) hand_over();
     }
+    s = behind;
+    go = more;
   }
   // no copy may still be writing shared memory at exit
   for (uint32_t i = loads > kSlots ? loads - kSlots : 0; i < loads; ++i) svk::mbar_wait_bounded(&sm.k_full[i % kSlots], (i / kSlots) & 1);
@@ -667,7 +728,7 @@ __device__ __forceinline__ void produce_keys(const Args& A, Shared& sm, uint32_t
 // Queries and values (a query tile waits for a buffer that the segment before
 // gives back; the keys behind it must not wait with it).
 template <int DP>
-__device__ __forceinline__ void produce_values(const Args& A, Shared& sm, uint32_t q_smem, uint32_t ring, const CUtensorMap* qm,
+__device__ __forceinline__ void produce_values(const Args& A, Shared<DP>& sm, uint32_t q_smem, uint32_t ring, const CUtensorMap* qm,
                                                const CUtensorMap* vm, const CUtensorMap* vcm) {
   constexpr int kSlots = v_slots(DP), kPanels = DP / 64;
   uint32_t qs = 0;
@@ -704,7 +765,7 @@ __device__ __forceinline__ void produce_values(const Args& A, Shared& sm, uint32
 __device__ __forceinline__ bool mends(const Segment& s, int t, int keys) { return t >= s.q.cached || keys % 16; }
 
 template <typename T, int DP>
-__device__ __forceinline__ void mend(const Args& A, Shared& sm, unsigned char* ring) {
+__device__ __forceinline__ void mend(const Args& A, Shared<DP>& sm, unsigned char* ring) {
   constexpr int kPanels = DP / 64, kSlots = v_slots(DP);
   const int lane = static_cast<int>(threadIdx.x & 31);
   Walk w = sm.plan.w;
@@ -757,7 +818,7 @@ __device__ __forceinline__ void mend(const Args& A, Shared& sm, unsigned char* r
 }
 
 template <typename T, int DP>
-__device__ __forceinline__ void issue(const Args& A, Shared& sm, uint32_t q_smem, uint32_t k_ring, uint32_t v_ring, uint32_t tmem) {
+__device__ __forceinline__ void issue(const Args& A, Shared<DP>& sm, uint32_t q_smem, uint32_t k_ring, uint32_t v_ring, uint32_t tmem) {
   constexpr uint32_t kUnits = tile_bytes(DP) / 16;  // of the descriptors' addresses
   constexpr uint32_t kHi = (1024u >> 4) | 1u << 14 | 2u << 29;
   const bool leads = elected();
@@ -767,8 +828,8 @@ __device__ __forceinline__ void issue(const Args& A, Shared& sm, uint32_t q_smem
   const uint32_t v_lo = ((v_ring & 0x3FFFFu) >> 4) | (kTile * 128 / 16) << 16;
   const uint32_t qk_desc = idesc<T>(kTile, false) | (A.flip ? kNegateA : 0u);  // (scores of a negative scale)
   auto full = [](uint32_t lo) { return static_cast<uint64_t>(kHi) << 32 | lo; };
-  Steps qk, pv;
-  qk.start(sm.plan);
+  Steps qk = {}, pv;
+  qk.start(sm);
   pv = qk;
   uint32_t k_slot = 0, k_turn = 0, v_slot = 0, v_turn = 0, qs = 0, q_first = 0, gq = 0, gp = 0;
   auto scores = [&]() {
@@ -798,14 +859,14 @@ __device__ __forceinline__ void issue(const Args& A, Shared& sm, uint32_t q_smem
     __syncwarp();
     if (last && ++k_slot == k_slots(DP)) k_slot = 0, ++k_turn;
     ++gq;
-    qk.advance(A);
+    qk.advance(sm);
     return true;
   };
   bool alive = scores() && scores();
   uint32_t segments = 0;
   while (alive && pv.ok) {
     // inside a segment, whole tiles of the cache: nothing to look up between the steps
-    if (pv.k >= 2 && !(pv.k & 1) && qk.ok && qk.w.count == pv.w.count) {
+    if (pv.k >= 2 && !(pv.k & 1) && qk.ok && qk.i == pv.i) {
       const int stride = pv.s.two ? 2 : 1;  // steps per key tile
       // (the last scores against a query tile also give it back)
       const int to_last = pv.s.steps - stride - 2 - pv.k, to_part = (pv.s.q.len / kTile - pv.s.t0) * stride - pv.k;
@@ -889,7 +950,7 @@ __device__ __forceinline__ void issue(const Args& A, Shared& sm, uint32_t q_smem
     __syncwarp();
     if (last && ++v_slot == v_slots(DP)) v_slot = 0, ++v_turn;
     ++gp;
-    pv.advance(A);
+    pv.advance(sm);
     alive = scores();
   }
   if (leads) mma_commit(&sm.done);
@@ -944,19 +1005,19 @@ __device__ __forceinline__ void store_out16(T* dst, const float* o, float f) {
 
 // A softmax warp.
 template <typename T, int DP>
-__device__ __forceinline__ void soften(const Args& A, Shared& sm, uint32_t tmem, int c) {
+__device__ __forceinline__ void soften(const Args& A, Shared<DP>& sm, uint32_t tmem, int c) {
   const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
   const int stream = warp >> 2, row = (warp & 3) * 32 + lane;
   const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
   const uint32_t s_col = tmem + lanes + stream * kTile, o_col = tmem + lanes + 256;
-  Walk w = sm.plan.w;
   uint32_t g = 0;          // steps before the segment, both streams
   uint32_t turns = 0;      // of this stream
   // (a scale of 0 as one that makes every finite score 0 too, and -inf still -inf)
   const float c2 = A.c > 0 ? A.c : 1e-45f;
   bool alive = true;
   Segment s = sm.plan.s;
-  for (bool go = sm.plan.any; go; go = w.next(A, s)) {
+  int number = 0;
+  for (bool go = sm.plan.any; go; ++number) {
     // this stream's steps of the segment: k = k0, k0 + 2, ...
     const int k0 = static_cast<int>((stream ^ g) & 1);
     const int query = 2 * s.pair + (s.two ? k0 : 0);
@@ -1075,13 +1136,13 @@ __device__ __forceinline__ void soften(const Args& A, Shared& sm, uint32_t tmem,
       keep = mine;
       keep_other = theirs;
     }
-    if (alive) alive = warp_wait(sm, &sm.o_full, (w.count - 1) & 1);
+    if (alive) alive = warp_wait(sm, &sm.o_full, number & 1);
     fence_after();
     const int begin = s.two ? 0 : stream * (DP / 2), width = s.two ? DP : DP / 2;
     const bool mine = alive && busy && row < rows;
     const long long at = static_cast<long long>(s.q.first) + node;
     const int qh = s.head * A.G + row_head(A, row);
-    const int slot = 2 * c + (w.count > 1 ? 1 : 0);
+    const int slot = 2 * c + (number ? 1 : 0);
     float* part = A.part + static_cast<long long>(slot) * 256 * DP + ((s.two ? k0 * kTile : 0) + row) * 4;
     const float inv = sum > 0 || sum != sum ? 1.0f / sum : 0.0f;
     uint32_t odd_any = 0;
@@ -1141,7 +1202,7 @@ __device__ __forceinline__ void soften(const Args& A, Shared& sm, uint32_t tmem,
       Join j;
       j.parts = s.whole ? 0 : sm.plan.parts;
       if (j.parts < 0) {  // up to the CTA that has the item's last unit
-        j.parts = sm.plan.cut.owner(sm.plan.cut.begin(c + 1) + w.rest - 1) - c;
+        j.parts = sm.plan.cut.owner(sm.plan.cut.begin(c + 1) + (number ? sm.queue[number % Shared<DP>::kQueue].rest : sm.plan.w.rest) - 1) - c;
       }
       j.slot = slot;
       j.cta = c;
@@ -1164,6 +1225,10 @@ __device__ __forceinline__ void soften(const Args& A, Shared& sm, uint32_t tmem,
     __syncwarp();
     if (lane == 0) mbar_arrive_local(&sm.o_empty);
     g += static_cast<uint32_t>(s.steps);
+    // (all warps go on or none, or one would wait for the others at a barrier; a
+    // producer that gave up has not said whether there is more)
+    go = all_soft(alive) && sm.queue[number % Shared<DP>::kQueue].more != 0;
+    if (go) s = segment(sm, number + 1);
   }
 }
 
@@ -1179,7 +1244,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     return;
   }
   unsigned char* v_ptr = base + (2 + k_slots(DP)) * tile_bytes(DP);
-  Shared& sm = *reinterpret_cast<Shared*>(v_ptr + v_slots(DP) * tile_bytes(DP));
+  Shared<DP>& sm = *reinterpret_cast<Shared<DP>*>(v_ptr + v_slots(DP) * tile_bytes(DP));
   const uint32_t q_smem = smem_u32(base), k_ring = q_smem + 2 * tile_bytes(DP), v_ring = smem_u32(v_ptr);
   const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0);
   const int C = static_cast<int>(gridDim.x), c = static_cast<int>(blockIdx.x);
@@ -1219,9 +1284,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   fence_after();
   if (A.batch <= kFewSequences)
-    make_plan<true>(A, C, c, sm.plan);
+    make_plan<true>(A, C, c, sm.plan, sm.scratch);
   else
-    make_plan<false>(A, C, c, sm.plan);
+    make_plan<false>(A, C, c, sm.plan, sm.scratch);
   const uint32_t tmem = sm.tmem;
   if (warp >= kSoftWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
