@@ -150,12 +150,13 @@ __device__ __forceinline__ int row_head(const Args& A, int r) { return r - row_n
 
 // What a key tile costs: four units for a pair of query tiles (two steps of some
 // 1800 clocks), three for a single one (one step, but its 64 KB take the memory
-// 2800 clocks when all SMs ask).
-constexpr int kPairCost = 4, kSingleCost = 3;
+// 2800 clocks when all SMs ask); and what an item costs beside its tiles (the
+// pipeline's filling and the end).
+constexpr int kPairCost = 4, kSingleCost = 3, kItemCost = 8;
 // Units of one key head; the last pair of a sequence may lack its second tile.
 __device__ __forceinline__ int units_of_head(const Args& A, const Sequence& s) {
   const bool odd = s.N <= (2 * s.items - 1) * A.per_tile;
-  return s.tiles * (kPairCost * s.items - (odd ? kPairCost - kSingleCost : 0));
+  return s.tiles * (kPairCost * s.items - (odd ? kPairCost - kSingleCost : 0)) + kItemCost * s.items;
 }
 __device__ __forceinline__ long long units_of(const Args& A, const Sequence& s) {
   return s.N > 0 ? static_cast<long long>(units_of_head(A, s)) * A.Hkv : 0;
@@ -212,14 +213,15 @@ struct Walk {
   __device__ __forceinline__ void cut(const Args& A, Segment& s) {
     const int per_head = units_of_head(A, s.q);
     s.head = off < per_head ? 0 : Cut::divide(off, per_head);
-    const int in_head = static_cast<int>(off - static_cast<long long>(s.head) * per_head), per_pair = kPairCost * s.q.tiles;
+    const int in_head = static_cast<int>(off - static_cast<long long>(s.head) * per_head), per_pair = kItemCost + kPairCost * s.q.tiles;
     s.pair = in_head < per_pair ? 0 : in_head / per_pair;
     const int in = in_head - s.pair * per_pair;
     s.b = b;
     s.two = s.q.N > (2 * s.pair + 1) * A.per_tile;
-    const int all = s.two ? per_pair : kSingleCost * s.q.tiles, end = all - in < left ? all : in + static_cast<int>(left);
-    s.t0 = s.two ? in / kPairCost : in / kSingleCost;
-    s.t1 = s.two ? end / kPairCost : end / kSingleCost;
+    const int all = s.two ? per_pair : kItemCost + kSingleCost * s.q.tiles, end = all - in < left ? all : in + static_cast<int>(left);
+    const int from = in > kItemCost ? in - kItemCost : 0, to = end > kItemCost ? end - kItemCost : 0;
+    s.t0 = s.two ? from / kPairCost : from / kSingleCost;
+    s.t1 = s.two ? to / kPairCost : to / kSingleCost;
     s.whole = s.t0 == 0 && s.t1 == s.q.tiles;
     s.steps = (s.t1 - s.t0) * (s.two ? 2 : 1);
     rest = all - end;
@@ -299,10 +301,9 @@ __device__ __forceinline__ void make_plan(const Args& A, int C, int c, PlanMem& 
       W += v;
     }
   }
-  if (W <= static_cast<long long>(kFewSteps) * kPairCost / 2 * C && A.batch <= T) {
+  if (W <= static_cast<long long>(kFewSteps) * kPairCost / 2 * C && A.batch <= T) {  // (some of that is the items' own)
     // each item by itself, in the shortest pieces that C CTAs can take
-    // (a piece has a key tile, of three units or more; a step costs no more than three)
-    const int least = W <= 3LL * C ? 1 : static_cast<int>(static_cast<uint32_t>(W) / (3u * static_cast<uint32_t>(C)));
+    // (a piece has a key tile, of three units or more)
     bool fits = W <= 3LL * C;
     for (int limit = fits ? 1 : 2 * kFewSteps;;) {  // (whether the longest fit, then from the shortest on)
       const Pieces p = t < A.batch && q.N > 0 ? pieces_of(A, q, limit) : Pieces{0, 0, 0};
@@ -352,14 +353,15 @@ __device__ __forceinline__ void make_plan(const Args& A, int C, int c, PlanMem& 
         sync();
         return;
       }
-      limit = fits ? limit + 1 : least;
+      limit = fits ? limit + 1 : 1;
       fits = true;
       sync();  // the counts have been read
     }
     sync();
   }
-  Cut cut;  // (a key tile's cost at least: a smaller piece may hold the end of none)
-  cut.ctas = W >= static_cast<long long>(kPairCost) * C ? C : W >= kPairCost ? static_cast<int>(W / kPairCost) : 1;
+  Cut cut;  // (at least what an item and a key tile cost: a smaller piece may hold the end of no tile)
+  constexpr int kLeast = kItemCost + kPairCost;
+  cut.ctas = W >= static_cast<long long>(kLeast) * C ? C : W >= kLeast ? static_cast<int>(W / kLeast) : 1;
   cut.each = Cut::divide(W, cut.ctas);
   cut.more = static_cast<int>(W - cut.each * cut.ctas);
   const long long u = cut.begin(c);
