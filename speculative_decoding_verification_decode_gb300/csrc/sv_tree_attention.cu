@@ -303,9 +303,9 @@ __device__ __forceinline__ void make_plan(const Args& A, int C, int c, PlanMem& 
   }
   if (W <= static_cast<long long>(kFewSteps) * kPairCost / 2 * C && A.batch <= T) {  // (some of that is the items' own)
     // each item by itself, in the shortest pieces that C CTAs can take
-    // (a piece has a key tile, of three units or more)
-    bool fits = W <= 3LL * C;
-    for (int limit = fits ? 1 : 2 * kFewSteps;;) {  // (whether the longest fit, then from the shortest on)
+    // (by bisection, the longest first; a piece has a key tile, of three units or more)
+    int lo = 1, hi = W <= 3LL * C ? 1 : 2 * kFewSteps;
+    for (int limit = hi;;) {
       const Pieces p = t < A.batch && q.N > 0 ? pieces_of(A, q, limit) : Pieces{0, 0, 0};
       const int count = p.head * A.Hkv;  // (no more than units)
       int y = count;
@@ -327,8 +327,13 @@ __device__ __forceinline__ void make_plan(const Args& A, int C, int c, PlanMem& 
           all += v;
         }
       }
-      if (all > C && !fits) break;
-      if (all <= C && fits) {
+      if (all > C) {
+        if (limit == 2 * kFewSteps) break;
+        lo = limit + 1;
+      } else {
+        hi = limit;
+      }
+      if (all <= C && lo == hi) {
         if (c >= ahead && c < ahead + count) {
           Segment s;
           s.q = q;
@@ -353,8 +358,7 @@ __device__ __forceinline__ void make_plan(const Args& A, int C, int c, PlanMem& 
         sync();
         return;
       }
-      limit = fits ? limit + 1 : 1;
-      fits = true;
+      limit = (lo + hi) / 2;
       sync();  // the counts have been read
     }
     sync();
