@@ -55,4 +55,4 @@ from .api import (  # noqa: F401
     verify_tree_greedy,
 )
 from ._build import build  # noqa: F401
-from .decoder import BeamDecoder, SpeculativeDecoder  # noqa: F401,E402
+from .decoder import BeamDecoder, SpeculativeDecoder, TreeDecoder  # noqa: F401,E402

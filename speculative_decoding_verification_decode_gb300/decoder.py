@@ -239,3 +239,157 @@ class BeamDecoder:
             else:
                 self.step()
         return self.tokens, self.lengths, self.scores
+
+
+class TreeDecoder:
+    """Device-resident rounds of speculative decoding with drafted trees over a
+    paged cache: draft a tree, score its nodes in one target pass, follow the
+    target's choices, keep the path's keys and values (tree_attention,
+    verify_tree_greedy / verify_tree, cache_append).  A round has no host
+    synchronisation, so it can be captured once as a CUDA graph and replayed.
+
+    The callables are the caller's (deterministic and graph-capturable):
+
+    * ``draft_fn(tokens, lengths) -> [B, n]`` tokens of the tree's nodes (node
+      0's, the last committed token, is put in place here);
+    * ``target_fn(nodes, positions, attend) -> [B, n, V]`` logits after each
+      node: ``nodes [B, n]`` int32, ``positions [B, n]`` their places in the
+      sequence, ``attend(layer, q, k, v)`` the layer's attention, ``[B, n, Hq,
+      D]``, for its ``q [B, n, Hq, D]`` and ``k``, ``v [B, n, Hkv, D]``, called
+      once per layer of the cache.
+
+    ``cache`` holds the committed tokens but the last one (``prefill`` brings it
+    there).  A sequence that a whole tree could take past ``max_len`` stays as it
+    is from then on, and so does one that cannot go on: ``status`` (int32
+    ``[B]``, SEQ_* bits) tells why, SEQ_NO_PAGES where the cache is full,
+    SEQ_BAD_VALUE for a row that no token can be taken from."""
+
+    def __init__(self, draft_fn: Callable, target_fn: Callable, cache: api.PagedCache, tokens: torch.Tensor,
+                 lengths: torch.Tensor, parents, temperature: Optional[torch.Tensor] = None, seed: int = 0):
+        """``tokens`` [B, max_len] int32 (prompts in place, one token at least),
+        ``lengths`` [B] int32; ``parents``: the tree, the earlier node that each
+        node continues, -1 for node 0 (a chain: -1, 0, 1, ...); greedy when
+        ``temperature`` is None, else per-sequence temperatures [B] (0 =
+        greedy for that sequence)."""
+        if tokens.dim() != 2 or tokens.dtype != torch.int32 or lengths.dtype != torch.int32:
+            raise ValueError("tokens must be [B, max_len] int32 and lengths [B] int32")
+        parents = [int(p) for p in parents]
+        if not parents or parents[0] != -1 or any(not 0 <= p < i for i, p in enumerate(parents) if i):
+            raise ValueError("parents must be -1, then an earlier node for every node")
+        self.B, self.max_len = tokens.shape
+        if cache.lengths.numel() != self.B:
+            raise ValueError("the cache must have one sequence for each row of tokens")
+        dev = tokens.device
+        self.draft_fn, self.target_fn, self.cache = draft_fn, target_fn, cache
+        self.tokens, self.lengths, self.device, self.n = tokens, lengths, dev, len(parents)
+        depth = []
+        for p in parents:
+            depth.append(0 if p < 0 else depth[p] + 1)
+        self.depth = torch.tensor(depth, dtype=torch.int32, device=dev)
+        self.parents = torch.tensor(parents, dtype=torch.int32, device=dev).repeat(self.B, 1)
+        self.temperature = None if temperature is None else temperature.to(dev, torch.float32).repeat_interleave(self.n)
+        self.seed, self.counter = int(seed) & 0x7FFFFFFF, torch.zeros((), dtype=torch.int64, device=dev)
+        self.status = torch.zeros(self.B, dtype=torch.int32, device=dev)
+        self.column = torch.arange(self.n, device=dev)
+        self.last = None
+        self.graph = None
+
+    def _target(self, nodes: torch.Tensor, parents: Optional[torch.Tensor], depth: torch.Tensor):
+        """(logits, every layer's keys, values) of the nodes."""
+        c = self.cache
+        keys, values = [None] * len(c.keys), [None] * len(c.keys)
+        table, lengths = c.table.view(self.B, -1), c.lengths.view(-1)
+
+        def attend(layer, q, k, v):
+            keys[layer], values[layer] = k, v
+            return api.tree_attention(q, k, v, c.keys[layer], c.values[layer], table, lengths, parents).out.view(q.shape)
+
+        logits = self.target_fn(nodes, lengths[:, None] + depth, attend)
+        if any(k is None for k in keys):
+            raise ValueError("target_fn must call attend for every layer of the cache")
+        return logits, keys, values
+
+    def prefill(self, chunk: int = 128):
+        """Brings the committed tokens but the last one of every sequence into
+        the cache, from where it stands, up to ``chunk`` tokens at a time (the
+        one call that reads lengths on the host)."""
+        held = self.cache.lengths.view(-1)
+        want = self.lengths - 1
+        room = torch.arange(chunk, device=self.device, dtype=torch.int32)
+        for _ in range(-(-int((want - held).max()) // chunk)):
+            left = (want - held).clamp(0, chunk)
+            at = (held[:, None] + room).clamp(max=self.max_len - 1).long()
+            _, keys, values = self._target(self.tokens.gather(1, at), None, room)
+            self.status |= api.cache_append(self.cache, keys, values, counts=left).view(-1)
+
+    def _uniforms(self) -> torch.Tensor:
+        """[B * n] uniforms k * 2^-24 from a counter-based mix of (seed, round,
+        sequence, node): reproducible and graph-safe."""
+        x = torch.arange(self.B * self.n, device=self.device) + self.counter * 0x100000000 + self.seed * 0x1000000000000
+        for mul, sh in ((0x5851F42D4C957F2D, 33), (0x2545F4914F6CDD1D, 29), (0x14057B7EF767814F, 31)):
+            x = (x ^ ((x >> sh) & ((1 << (64 - sh)) - 1))) * mul
+        return ((x >> 40) & 0xFFFFFF).to(torch.float32) * (1.0 / (1 << 24))
+
+    def round(self):
+        """One round for every sequence (no host sync); returns the
+        verification's result."""
+        at = (self.lengths - 1).clamp(min=0).long()[:, None]
+        nodes = self.draft_fn(self.tokens, self.lengths).to(torch.int32)
+        nodes = torch.where(self.column == 0, self.tokens.gather(1, at), nodes)
+        logits, keys, values = self._target(nodes, self.parents, self.depth)
+        if self.temperature is None:
+            r = api.verify_tree_greedy(logits, nodes, self.parents)
+        else:  # each node's token drawn from its row, then matched
+            rows = logits.reshape(self.B * self.n, -1)
+            drawn = api.accept_from_logits(rows, rows[:0], self.temperature, nodes.reshape(-1)[:0], self._uniforms())
+            r = api.verify_tree(drawn.next_token, nodes, self.parents)
+        bad = torch.where(r.next_token < 0, r.status | api._lib.SEQ_BAD_VALUE, r.status & ~api._lib.SEQ_BAD_TOKEN)
+        go = (self.status == 0) & (bad == 0) & (self.lengths + self.n <= self.max_len)
+        counts = torch.where(go, r.n_accepted + 1, 0)
+        full = api.cache_append(self.cache, keys, values, counts=counts, path=r.path).view(-1)
+        self.status |= torch.where(self.status == 0, bad | full, 0)
+        go = go & (full == 0)
+        # the path's tokens after node 0, then the next one
+        said = nodes.gather(1, torch.cat((r.path[:, 1:], r.path[:, :1]), 1).clamp(min=0).long())
+        said = torch.where(self.column == r.n_accepted[:, None], r.next_token[:, None], said)
+        place = (self.lengths[:, None].long() + self.column).clamp(0, self.max_len - 1)
+        new = go[:, None] & (self.column <= r.n_accepted[:, None])
+        # (places past a sequence's own are written with what they hold; those at the end of the row that the clamp
+        # brings together belong to sequences that stay, and all hold the same)
+        self.tokens.scatter_(1, place, torch.where(new, said, self.tokens.gather(1, place)))
+        self.lengths.add_(torch.where(go, r.n_accepted + 1, 0))
+        self.counter += 1
+        self.last = r
+        return r
+
+    def capture(self):
+        """Capture one round as a CUDA graph (after a warm-up round whose changes
+        to tokens, lengths and pages are taken back)."""
+        c = self.cache
+        kept = [self.tokens, self.lengths, self.counter, self.status, c.table, c.lengths, c.refs]
+        saved = [t.clone() for t in kept]
+        s = torch.cuda.Stream(self.device)
+        s.wait_stream(torch.cuda.current_stream(self.device))
+        with torch.cuda.stream(s):
+            self.round()
+        torch.cuda.current_stream(self.device).wait_stream(s)
+        for t, o in zip(kept, saved):
+            t.copy_(o)
+        torch.cuda.synchronize(self.device)
+        self.graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(self.graph, stream=s, capture_error_mode="relaxed"):
+            self.round()
+        torch.cuda.synchronize(self.device)
+        return self.graph
+
+    def run(self, rounds: int, graph: bool = True):
+        """``rounds`` rounds, replaying the captured graph when ``graph``;
+        returns (tokens, lengths)."""
+        if graph and self.graph is None:
+            self.capture()
+        for _ in range(rounds):
+            if graph:
+                self.graph.replay()
+            else:
+                self.round()
+        return self.tokens, self.lengths
