@@ -871,69 +871,74 @@ __device__ __forceinline__ void issue(const Args& A, Shared<DP>& sm, uint32_t q_
   bool alive = scores() && scores();
   uint32_t segments = 0;
   while (alive && pv.ok) {
-    // inside a segment, whole tiles of the cache: nothing to look up between the steps
-    if (pv.k >= 2 && !(pv.k & 1) && qk.ok && qk.i == pv.i) {
-      const int stride = pv.s.two ? 2 : 1;  // steps per key tile
-      // (the last scores against a query tile also give it back)
-      const int to_last = pv.s.steps - stride - 2 - pv.k, to_part = (pv.s.q.len / kTile - pv.s.t0) * stride - pv.k;
-      const int n = (to_last < to_part ? to_last : to_part) & ~1;
-      if (n > 0) {
-        const bool two = pv.s.two;
-        const uint32_t qa = q_lo + (q_first & 1) * kUnits, qb = two ? q_lo + ((q_first + 1) & 1) * kUnits : qa;
-        const uint32_t st = gp & 1;
-        const uint32_t s0 = tmem + st * kTile, s1 = tmem + (st ^ 1) * kTile;
-        const uint32_t o0 = tmem + 256 + st * 128, o1 = tmem + 256 + (st ^ 1) * 128;
-        uint64_t *const p0 = &sm.p_full[st], *const p1 = &sm.p_full[st ^ 1], *const f0 = &sm.s_full[st], *const f1 = &sm.s_full[st ^ 1];
-        auto both = [&](uint64_t* p_bar, uint32_t parity, uint32_t s, uint32_t o, uint32_t q, uint64_t* f, bool fresh, bool last) {
-          bool ok = !fresh || wait(sm, &sm.v_full[v_slot], v_turn & 1);
-          ok = wait(sm, p_bar, parity) && ok;
-          if (fresh) ok = wait(sm, &sm.k_full[k_slot], k_turn & 1) && ok;
-          ok = __all_sync(0xFFFFFFFFu, ok);
-          fence_after();
-          const uint32_t v = v_lo + v_slot * kUnits, k = k_lo + k_slot * kUnits;
-          if (leads && ok) {
-#pragma unroll
-            for (int i = 0; i < kTile / 16; ++i) mma_ts(o, s + i * 8, full(v + i * 128), idesc<T>(DP, true), 1u);
-            if (last) mma_commit(&sm.v_empty[v_slot]);
-#pragma unroll
-            for (int i = 0; i < DP / 16; ++i) {
-              const uint32_t at = (i / 4) * (kTile * 128 / 16) + (i % 4) * 2;
-              mma_ss(s, full(q + at), full(k + at), qk_desc, i > 0);
-            }
-            mma_commit(f);
-            if (last) mma_commit(&sm.k_empty[k_slot]);
-          }
-          __syncwarp();
-          if (last) {
-            if (++v_slot == v_slots(DP)) v_slot = 0, ++v_turn;
-            if (++k_slot == k_slots(DP)) k_slot = 0, ++k_turn;
-          }
-          return ok;
-        };
-        uint32_t parity = (gp >> 1) & 1, parity1 = ((gp + 1) >> 1) & 1;
-        if (two) {
-          for (int i = 0; alive && i < n; i += 2) {
-            alive = both(p0, parity, s0, o0, qa, f0, true, false) && both(p1, parity1, s1, o1, qb, f1, false, true);
-            parity ^= 1, parity1 ^= 1;
-          }
-        } else {
-          for (int i = 0; alive && i < n; i += 2) {
-            alive = both(p0, parity, s0, o0, qa, f0, true, true) && both(p1, parity1, s1, o1, qa, f1, true, true);
-            parity ^= 1, parity1 ^= 1;
-          }
-        }
-        gp += n, gq += n;
-        pv.k += n, qk.k += n;
-        if (!alive) break;
-      }
-    }
-    const uint32_t st = gp & 1;
     if (pv.k == 0) {  // the outputs of the segment before have been read
       if (segments && !warp_wait(sm, &sm.o_empty, (segments - 1) & 1)) break;
       ++segments;
       if (lane < 8) sm.odd[lane] = 0;
       __syncwarp();
     }
+    // steps whose scores-to-come are of the segment too: PV(k) and QK(k + 2) at a time
+    if (qk.ok && qk.i == pv.i && pv.k < pv.s.steps - 2) {
+      const bool two = pv.s.two;
+      const int steps = pv.s.steps, whole = pv.s.q.len / kTile, cached = pv.s.q.cached;
+      const int gives_back = steps - (two ? 2 : 1);  // the last scores against a query tile
+      int keys = kTile;
+      for (int k = pv.k; alive && k < steps - 2; ++k) {
+        const uint32_t st = gp & 1, j = two ? k & 1 : 0;
+        const bool fresh = j == 0, last = j == 1 || !two;
+        bool ok = true;
+        if (fresh) {
+          const int t = pv.s.t0 + (two ? k >> 1 : k);
+          uint64_t* bar = &sm.v_full[v_slot];
+          keys = kTile;
+          if (t >= whole) {
+            keys = keys_of(pv.s, t);
+            if (mends(pv.s, t, keys)) bar = &sm.v_mended[v_slot];
+          }
+          ok = wait(sm, bar, v_turn & 1);
+          if (t >= cached && lane < 4) sm.odd[(t - cached) * 4 + lane] = sm.v_odd[v_slot][lane];
+        }
+        ok = wait(sm, &sm.p_full[st], (gp >> 1) & 1) && ok;
+        alive = __all_sync(0xFFFFFFFFu, ok);
+        fence_after();
+        const uint32_t v = v_lo + v_slot * kUnits, kk = k_lo + k_slot * kUnits, buf = (q_first + j) & 1, q = q_lo + buf * kUnits;
+        const uint32_t s = tmem + st * kTile, o = tmem + 256 + st * 128, acc = k >= 2 ? 1u : 0u;
+        if (leads && alive) {
+          if (keys > kTile - 16) {
+#pragma unroll
+            for (int i = 0; i < kTile / 16; ++i) mma_ts(o, s + i * 8, full(v + i * 128), idesc<T>(DP, true), i > 0 ? 1u : acc);
+          } else {
+#pragma unroll 1
+            for (int i = 0; i * 16 < keys; ++i) mma_ts(o, s + i * 8, full(v + i * 128), idesc<T>(DP, true), i > 0 ? 1u : acc);
+          }
+          if (last) mma_commit(&sm.v_empty[v_slot]);
+        }
+        if (fresh) alive = __all_sync(0xFFFFFFFFu, wait(sm, &sm.k_full[k_slot], k_turn & 1)) && alive;
+        if (leads && alive) {
+#pragma unroll
+          for (int i = 0; i < DP / 16; ++i) {
+            const uint32_t at = (i / 4) * (kTile * 128 / 16) + (i % 4) * 2;
+            mma_ss(s, full(q + at), full(kk + at), qk_desc, i > 0);
+          }
+          mma_commit(&sm.s_full[st]);
+          if (last) mma_commit(&sm.k_empty[k_slot]);
+          if (k + 2 >= gives_back) mma_commit(&sm.q_empty[buf]);
+        }
+        __syncwarp();
+        if (last) {
+          if (++v_slot == v_slots(DP)) v_slot = 0, ++v_turn;
+          if (++k_slot == k_slots(DP)) k_slot = 0, ++k_turn;
+        }
+        ++gp;
+      }
+      if (!alive) break;
+      gq += static_cast<uint32_t>(steps - 2 - pv.k);
+      pv.k = steps - 2;
+      qk.k = steps - 1;
+      qk.advance(sm);
+    }
+    // the last two: the scores behind them are the next segment's
+    const uint32_t st = gp & 1;
     const int t = pv.tile(), keys = keys_of(pv.s, t);
     if (pv.fresh() && !warp_wait(sm, mends(pv.s, t, keys) ? &sm.v_mended[v_slot] : &sm.v_full[v_slot], v_turn & 1)) break;
     if (t >= pv.s.q.cached && lane < 4) sm.odd[(t - pv.s.q.cached) * 4 + lane] = sm.v_odd[v_slot][lane];
