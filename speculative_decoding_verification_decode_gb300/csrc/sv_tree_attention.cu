@@ -148,11 +148,12 @@ __device__ __forceinline__ int row_node(const Args& A, int r) {
 }
 __device__ __forceinline__ int row_head(const Args& A, int r) { return r - row_node(A, r) * A.G; }
 
-// What a key tile costs: four units for a pair of query tiles (two steps of some
-// 1800 clocks), three for a single one (one step, but its 64 KB take the memory
-// 2800 clocks when all SMs ask); and what an item costs beside its tiles (the
-// pipeline's filling and the end).
-constexpr int kPairCost = 4, kSingleCost = 3, kItemCost = 8;
+// What a key tile costs: five units for a pair of query tiles (two steps), three
+// for a single one; and what an item costs beside its tiles (the pipeline's filling
+// and the end).  Fitted to the CTAs' clocks on 64 ragged sequences of up to 4096
+// tokens and 32 nodes: 3221, 1904, and 8000 to 10200 an item; with 4, 3 and 8 the
+// slowest CTA took 14% longer than the mean.
+constexpr int kPairCost = 5, kSingleCost = 3, kItemCost = 15;
 // Units of one key head; the last pair of a sequence may lack its second tile.
 __device__ __forceinline__ int units_of_head(const Args& A, const Sequence& s) {
   const bool odd = s.N <= (2 * s.items - 1) * A.per_tile;
