@@ -861,11 +861,10 @@ def _verify_tree(rows, choices, tokens, parents, cu_nodes, n) -> TreeResult:
         if parents.numel() != total:
             raise ValueError("parents must have one entry for each token")
         parents = _words(parents, dev, "parents")
-    # one buffer for all results: n_accepted, next_token, status, path
-    out = torch.empty((3 + max(n, 0)) * B, dtype=torch.int32, device=dev)
-    acc, nxt, status, path = out.split((B, B, B, max(n, 0) * B))
+    out = torch.empty((3, B), dtype=torch.int32, device=dev)
+    path = torch.empty((B, max(n, 0)), dtype=torch.int32, device=dev)
     p = out.data_ptr()
-    where = (p, p + 4 * B, p + 12 * B, p + 8 * B)  # n_accepted, next_token, path, status
+    where = (p, p + 4 * B, path.data_ptr(), p + 8 * B)  # n_accepted, next_token, path, status
     lib = _lib.load()
     if choices is None:
         dtype = _DTYPES.get(rows.dtype)
@@ -888,7 +887,8 @@ def _verify_tree(rows, choices, tokens, parents, cu_nodes, n) -> TreeResult:
             raise ValueError("choices must have one entry for each token")
         choices = _words(choices, dev, "choices")
         _launch(dev, lib.sv_verify_tree, choices.data_ptr(), tokens.data_ptr(), _p(parents), _p(cu), B, n, total, *where)
-    return TreeResult(acc, nxt, path.view(B, n), status)
+    acc, nxt, status = out.unbind()
+    return TreeResult(acc, nxt, path, status)
 
 
 def verify_tree_greedy(target: torch.Tensor, tokens: torch.Tensor, parents: Optional[torch.Tensor] = None,
@@ -927,9 +927,7 @@ def _aligned(t: torch.Tensor) -> torch.Tensor:
     others, and its address, are multiples of 16 bytes; else a copy."""
     s = t.stride()
     if (s[2] != 1 and t.shape[2] > 1) or s[0] % 8 or s[1] % 8 or t.data_ptr() % 16:
-        t = t.contiguous()
-        if t.data_ptr() % 16:
-            t = t.clone()
+        t = torch.empty(t.shape, dtype=t.dtype, device=t.device).copy_(t)
     return t
 
 
@@ -993,6 +991,8 @@ def tree_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_cache: t
     elif (out.shape[0] < total or out.shape[1:] != q.shape[1:] or out.dtype != q.dtype or out.device != dev or out.stride(2) != 1
           or out.stride(0) % 8 or out.stride(1) % 8 or out.data_ptr() % 16):
         raise ValueError("out must be like q with at least its rows, its address and strides multiples of 16 bytes")
+    elif total and out.data_ptr() in (q.data_ptr(), k.data_ptr(), v.data_ptr(), kp, vp):
+        raise ValueError("out is an input too: it would change while it is read")
     lse = torch.empty((total, Hq), dtype=torch.float32, device=dev)
     status = torch.empty(B, dtype=torch.int32, device=dev)
     need = _attention_bytes(D)
@@ -1113,7 +1113,9 @@ def cache_append(cache: PagedCache, keys: Union[torch.Tensor, Sequence[torch.Ten
     # (the same few questions to every tensor of every layer: asked in C, the answers gathered in sets)
     held, new = (*cache.keys, *cache.values), [*keys, *values]
     kinds = {dtype}
-    if (set(map(_shape, held)) != {pool.shape} or set(map(torch.Tensor.stride, held)) != {strides}
+    compact = torch.Tensor.is_contiguous  # (a cheaper question than the strides)
+    if (set(map(_shape, held)) != {pool.shape}
+            or not (pool.numel() and all(map(compact, held))) and set(map(torch.Tensor.stride, held)) != {strides}
             or set(map(_kind, held)) != kinds or set(map(torch.Tensor.get_device, held)) != {dev.index}):
         raise ValueError("the pools must be alike: shape, strides, type, device")
     if first.dim() == 4 and cu_nodes is None:
@@ -1123,7 +1125,8 @@ def cache_append(cache: PagedCache, keys: Union[torch.Tensor, Sequence[torch.Ten
         raise ValueError(f"new rows must be [{total}, {H}, {D}] of the pools' type, on their device")
     if torch.is_grad_enabled() and (any(map(_grad, held)) or any(map(_grad, new))):
         raise ValueError("the cache is modified in place: no gradients")
-    if len(set(map(torch.Tensor.stride, new))) > 1 or new[0].stride(2) != 1 and D > 1:
+    if not (total and all(map(compact, new))) and (len(set(map(torch.Tensor.stride, new))) > 1
+                                                   or new[0].stride(2) != 1 and D > 1):
         new = [x.contiguous() for x in new]  # (one layout serves all)
         new = [x if x.stride() == new[0].stride() else torch.empty_like(new[0]).copy_(x) for x in new]
     layout = new[0].stride()

@@ -196,8 +196,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
   // the lowest free pages, 16 per thread and round
   int found = 0;
   const bool vec = (reinterpret_cast<uintptr_t>(c.refs) & 15) == 0;
-  for (int p0 = 0; p0 < c.pages && found < want; p0 += kScan * kPlanThreads) {
-    const int p = p0 + kScan * t;
+  for (long long p0 = 0; p0 < c.pages && found < want; p0 += kScan * kPlanThreads) {
+    const long long p = p0 + kScan * t;
     unsigned free = 0;
     if (vec && p + kScan <= c.pages) {
       int4 r[kScan / 4];
@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     }
     int all;
     int at = found + block_scan(__popc(free), all, warp_sums);
-    for (; free && at < P.cap; free &= free - 1) P.list[at++] = p + __ffs(free) - 1;
+    for (; free && at < P.cap; free &= free - 1) P.list[at++] = static_cast<int>(p) + __ffs(free) - 1;
     found += all;
   }
   __syncthreads();

@@ -1622,7 +1622,8 @@ sv_status sv_tree_attention(const sv_tree_attn* args, float scale, void* workspa
   if (a.max_pages > 0 && a.page_size > SV_TREE_MAX_TOKENS / a.max_pages)
     return svh::fail(SV_ERR_UNSUPPORTED, "max_pages * page_size is more than %d tokens", SV_TREE_MAX_TOKENS);
   if (a.table_stride < a.max_pages && a.batch > 1) return svh::fail(SV_ERR_ARG, "table_stride (%lld) is less than max_pages", (long long)a.table_stride);
-  if (!(scale == scale) || scale - scale != 0) return svh::fail(SV_ERR_ARG, "scale must be finite");
+  const float c = scale * 1.4426950408889634f;  // (in powers of two)
+  if (!(c == c) || c - c != 0) return svh::fail(SV_ERR_ARG, "scale must be finite");
   if (a.batch == 0) return SV_OK;
   if (!a.status || !a.lengths || (!a.table && a.max_pages > 0)) return svh::fail(SV_ERR_ARG, "status, lengths or table is NULL");
   if (a.total > 0 && (!a.q || !a.k || !a.v || !a.out)) return svh::fail(SV_ERR_ARG, "q, k, v or out is NULL");
@@ -1631,6 +1632,8 @@ sv_status sv_tree_attention(const sv_tree_attn* args, float scale, void* workspa
                              a.kc_head, a.vc_page, a.vc_token, a.vc_head, a.out_row, a.out_head};
   for (const int64_t x : strides)
     if (x < 0 || x % 8) return svh::fail(SV_ERR_ARG, "strides must be multiples of 8 elements, not negative");
+  if ((a.out_row < a.dim && a.total > 1) || (a.out_head < a.dim && a.q_heads > 1))
+    return svh::fail(SV_ERR_ARG, "rows of out overlap");
   for (const void* p : {a.q, a.k, a.v, a.k_cache, a.v_cache, static_cast<const void*>(a.out)})
     if (reinterpret_cast<uintptr_t>(p) & 15) return svh::fail(SV_ERR_ARG, "q, k, v, the caches and out must be 16-byte aligned");
   const size_t need = sva::workspace_bytes_of(static_cast<int>(a.dim));

@@ -24,6 +24,7 @@ products are summed in f32); such rows are not compared, those beside them are.
 """
 
 import math
+from types import SimpleNamespace
 
 import numpy as np
 import pytest
@@ -161,6 +162,27 @@ def test_many_sequences():
     c.check(run(c))
     c = Case(2, rng.integers(20, 60, 40), rng.integers(0, 300, 40), 16, 2, 128, 32, HF)
     c.check(run(c))
+
+
+@pytest.mark.parametrize("B", [385, 1100])
+def test_more_sequences_than_threads(B):
+    """Several sequences to a thread of the plan; long ones among short ones and
+    idle ones."""
+    rng = np.random.default_rng(B)
+    lengths = rng.integers(0, 40, B)
+    lengths[rng.integers(0, B, 5)] = 3000
+    c = Case(B, rng.integers(0, 4, B), lengths, 4, 2, 64, 32, BF)
+    c.check(run(c))
+    c = Case(B + 1, rng.integers(0, 70, B) * (rng.random(B) < 0.1), lengths, 8, 1, 64, 32, BF)
+    c.check(run(c))
+
+
+def test_one_sequence_among_idle_ones():
+    for at in (0, 31, 32, 200, 399):
+        N, lengths = np.zeros(400, int), np.full(400, 50)
+        N[at], lengths[at] = 37, 2000
+        c = Case(at, N, lengths, 8, 2, 128, 16, BF)
+        c.check(run(c))
 
 
 def test_equal_trees_in_four_dimensions():
@@ -352,6 +374,47 @@ def test_streams_and_graphs():
         assert torch.equal(eager, want[0])
 
 
+def test_a_graph_follows_its_inputs():
+    """Lengths, nodes and pages change between replays: from one long sequence to
+    many short ones and back."""
+    rng = np.random.default_rng(5)
+    B = 12
+    shapes = [(rng.integers(0, 20, B), rng.integers(0, 3000, B)) for _ in range(4)]
+    shapes[1][0][:] = 0
+    shapes[1][0][7] = 20
+    total, width, P = 20 * B, 200, 12 * 200
+    g = torch.Generator().manual_seed(3)
+    a = dict(q=torch.randn(total, 8, 64, generator=g), k=torch.randn(total, 2, 64, generator=g), v=torch.randn(total, 2, 64, generator=g),
+             k_cache=torch.randn(P, 16, 2, 64, generator=g), v_cache=torch.randn(P, 16, 2, 64, generator=g))
+    a = {k: v.to(HF).to(DEV) for k, v in a.items()}
+    i32 = lambda x: torch.as_tensor(np.asarray(x, np.int32)).to(DEV)
+    a.update(table=i32(rng.permutation(P).reshape(B, width)), lengths=i32(np.zeros(B)), cu_nodes=i32(np.zeros(B + 1)), n=20,
+             parents=i32(np.zeros(total)))
+
+    def fill(N, lengths):
+        a["lengths"].copy_(i32(lengths))
+        a["cu_nodes"].copy_(i32(np.concatenate(([0], np.cumsum(N)))))
+        up = [int(rng.integers(-1, i)) for n in N for i in range(n)]
+        a["parents"].copy_(i32(up + [0] * (total - len(up))))
+
+    fill(*shapes[0])
+    out = torch.zeros_like(a["q"])
+    sv().tree_attention(**a, out=out)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, capture_error_mode="relaxed"):
+        r = sv().tree_attention(**a, out=out)
+    for N, lengths in shapes + shapes[:1]:
+        fill(N, lengths)
+        graph.replay()
+        again = sv().tree_attention(**a)
+        rows = int(sum(N))
+        assert torch.equal(r.out[:rows], again.out[:rows]) and not r.status.any()
+        ref = oracle.tree_attention(*(f64(a[k]) for k in ("q", "k", "v", "k_cache", "v_cache")), a["table"].cpu().numpy(), lengths,
+                                    a["parents"].cpu().numpy(), a["cu_nodes"].cpu().numpy(), 20, 0.125)
+        Case.check(SimpleNamespace(lengths=np.array(lengths), n=20, dtype=HF, D=64, scale=0.125, v=a["v"].cpu(), vc=a["v_cache"].cpu()),
+                   SimpleNamespace(out=r.out, lse=r.lse, status=r.status), ref)
+
+
 def test_refusals():
     m = sv()
     c = Case(17, [2, 2], [10, 20], 4, 2, 64, 16, BF)
@@ -362,6 +425,7 @@ def test_refusals():
                      (dict(table=a["table"].long()), "table"), (dict(lengths=a["lengths"][:1]), "lengths"),
                      (dict(n=None), "n "), (dict(cu_nodes=a["cu_nodes"][:2]), "cu_nodes"), (dict(parents=a["parents"][:3]), "parents"),
                      (dict(out=torch.empty(3, 4, 64, dtype=BF, device=DEV)), "out"),
+                     (dict(out=a["q"]), "input"),
                      (dict(q=a["q"].clone().requires_grad_()), "backward")):
         with pytest.raises(ValueError, match=what):
             call(**kw)

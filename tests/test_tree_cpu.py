@@ -96,6 +96,9 @@ def attention(lib, scale=0.125, ws=P, wb=1 << 34, **kw):
     (dict(v_cache=P + 2), b"aligned"),
     (dict(q_row=516), b"multiples of 8"),
     (dict(vc_token=-128), b"negative"),
+    (dict(out_row=56), b"overlap"),
+    (dict(out_head=0), b"overlap"),
+    (dict(scale=3e38), b"scale"),
     (dict(scale=float("nan")), b"scale"),
     (dict(scale=float("inf")), b"scale"),
 ])
