@@ -261,6 +261,7 @@ __device__ __forceinline__ Pieces pieces_of(const Args& A, const Sequence& s, in
 
 constexpr int kFewSteps = 24;  // a piece with no more steps is of one item
 constexpr int kFewSequences = 32;
+constexpr int kLaneSequences = 8;
 
 // How the units are cut over C CTAs, and CTA c's first segment: by all of the
 // CTA's threads, or by every warp for itself (few sequences: all write the same
@@ -306,6 +307,22 @@ __device__ __forceinline__ void make_plan(const Args& A, int C, int c, PlanMem& 
     // each item by itself, in the shortest pieces that C CTAs can take
     // (by bisection, the longest first; a piece has a key tile, of three units or more)
     int lo = 1, hi = W <= 3LL * C ? 1 : 2 * kFewSteps;
+    if (kWarp && hi > 1 && A.batch <= kLaneSequences) {
+      // (few sequences: a lane per length, all looked at together)
+      unsigned fit = 0;
+      for (int base = 0; base < 2 * kFewSteps && !fit; base += 32) {
+        int all = 0;
+        for (int b = 0; b < A.batch; ++b) {
+          Sequence o;
+          o.N = __shfl_sync(0xFFFFFFFFu, q.N, b);
+          o.tiles = __shfl_sync(0xFFFFFFFFu, q.tiles, b);
+          o.items = __shfl_sync(0xFFFFFFFFu, q.items, b);
+          if (o.N > 0) all += pieces_of(A, o, base + lane + 1).head * A.Hkv;
+        }
+        fit = __ballot_sync(0xFFFFFFFFu, all <= C && base + lane < 2 * kFewSteps);
+        if (fit) lo = hi = base + __ffs(fit);
+      }
+    }
     for (int limit = hi;;) {
       const Pieces p = t < A.batch && q.N > 0 ? pieces_of(A, q, limit) : Pieces{0, 0, 0};
       const int count = p.head * A.Hkv;  // (no more than units)
