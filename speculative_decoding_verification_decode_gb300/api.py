@@ -887,8 +887,7 @@ def _verify_tree(rows, choices, tokens, parents, cu_nodes, n) -> TreeResult:
             raise ValueError("choices must have one entry for each token")
         choices = _words(choices, dev, "choices")
         _launch(dev, lib.sv_verify_tree, choices.data_ptr(), tokens.data_ptr(), _p(parents), _p(cu), B, n, total, *where)
-    acc, nxt, status = out.unbind()
-    return TreeResult(acc, nxt, path, status)
+    return TreeResult(out[0], out[1], path, out[2])
 
 
 def verify_tree_greedy(target: torch.Tensor, tokens: torch.Tensor, parents: Optional[torch.Tensor] = None,
@@ -987,7 +986,7 @@ def tree_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_cache: t
     if (kc[3] != 1 or vc[3] != 1) and D > 1 or (kc[0] | kc[1] | kc[2] | vc[0] | vc[1] | vc[2]) % 8 or (kp | vp) % 16:
         raise ValueError("the caches must have unit stride along the head dimension, their addresses and other strides multiples of 16 bytes")
     if out is None:
-        out = torch.empty((total, Hq, D), dtype=q.dtype, device=dev)
+        out = torch.empty_like(q) if q.is_contiguous() else torch.empty((total, Hq, D), dtype=kind, device=dev)
     elif (out.shape[0] < total or out.shape[1:] != q.shape[1:] or out.dtype != q.dtype or out.device != dev or out.stride(2) != 1
           or out.stride(0) % 8 or out.stride(1) % 8 or out.data_ptr() % 16):
         raise ValueError("out must be like q with at least its rows, its address and strides multiples of 16 bytes")
@@ -1035,37 +1034,35 @@ _PAGES = struct.Struct("8q")  # sv_cache_pages (include/sv_cache.h)
 _ROWS = struct.Struct("7q")  # sv_cache_rows
 _kind = attrgetter("dtype")
 _shape = attrgetter("shape")
-_grad = attrgetter("requires_grad")
 
 
 def _pages_arg(c: PagedCache) -> tuple:
     """(words of sv_cache_pages, sequences, device) of a checked cache."""
-    table, lengths, refs = c.table, c.lengths, c.refs
-    dev = table.device
-    if dev.type != "cuda":
+    table, lengths, refs, pool = c.table, c.lengths, c.refs, c.keys[0] if len(c.keys) else None
+    at, i32 = table.get_device(), torch.int32
+    if at < 0:
         raise ValueError("the cache must be CUDA tensors (modified in place)")
-    for t, what in ((table, "table"), (lengths, "lengths"), (refs, "refs")):
-        if t.dtype != torch.int32 or t.device != dev:
-            raise ValueError(f"{what} must be int32 on the cache's device")
-    if lengths.shape != table.shape[:-1] or not lengths.is_contiguous() or refs.dim() != 1 or not refs.is_contiguous():
+    if (table.dtype is not i32 or lengths.dtype is not i32 or refs.dtype is not i32 or lengths.get_device() != at
+            or refs.get_device() != at):
+        raise ValueError("table, lengths and refs must be int32 on one device")
+    shape, sequences, pages = table.shape, lengths.numel(), refs.numel()
+    width = shape[-1]
+    if lengths.shape != shape[:-1] or not lengths.is_contiguous() or refs.dim() != 1 or not refs.is_contiguous():
         raise ValueError("lengths must be contiguous with one entry per table row, refs contiguous [pages]")
+    stride = width
     if not table.is_contiguous():
-        if table.dim() != 2 or table.stride(1) != 1 or table.stride(0) < table.shape[1]:
+        if table.dim() != 2 or table.stride(1) != 1 or table.stride(0) < width:
             raise ValueError("table must be contiguous, or [sequences, max_pages] with rows apart from one another")
         stride = table.stride(0)
-    else:
-        stride = table.shape[-1]
-    if len(c.keys) < 1 or len(c.values) != len(c.keys):
+    if pool is None or len(c.values) != len(c.keys):
         raise ValueError("the cache needs at least one layer, keys and values of each")
-    pool = c.keys[0]
-    if pool.dim() != 4 or pool.shape[0] != refs.shape[0] or pool.shape[1] < 1:
+    if pool.dim() != 4 or pool.shape[0] != pages or pool.shape[1] < 1:
         raise ValueError("the pools must be [pages, page_size, Hkv, D], one page for each entry of refs")
-    sequences = lengths.numel()
-    if max(sequences, pool.shape[0], pool.shape[1], table.shape[-1]) >= 2**31:
+    page = pool.shape[1]
+    if max(sequences, pages, page, width) >= 2**31:
         raise ValueError("sizes must be below 2^31")
-    words = _PAGES.pack(table.data_ptr(), stride, table.shape[-1], lengths.data_ptr(), refs.data_ptr(), pool.shape[0],
-                        pool.shape[1], sequences)
-    return words, sequences, dev
+    words = _PAGES.pack(table.data_ptr(), stride, width, lengths.data_ptr(), refs.data_ptr(), pages, page, sequences)
+    return words, sequences, table.device
 
 
 @functools.lru_cache(maxsize=256)
@@ -1123,8 +1120,8 @@ def cache_append(cache: PagedCache, keys: Union[torch.Tensor, Sequence[torch.Ten
     if (set(map(_shape, new)) != {(total, H, D)} or set(map(_kind, new)) != kinds
             or set(map(torch.Tensor.get_device, new)) != {dev.index}):
         raise ValueError(f"new rows must be [{total}, {H}, {D}] of the pools' type, on their device")
-    if torch.is_grad_enabled() and (any(map(_grad, held)) or any(map(_grad, new))):
-        raise ValueError("the cache is modified in place: no gradients")
+    if torch.is_grad_enabled() and (pool.requires_grad or held[-1].requires_grad or new[0].requires_grad or new[-1].requires_grad):
+        raise ValueError("the cache is modified in place: no gradients")  # (layers are alike)
     if not (total and all(map(compact, new))) and (len(set(map(torch.Tensor.stride, new))) > 1
                                                    or new[0].stride(2) != 1 and D > 1):
         new = [x.contiguous() for x in new]  # (one layout serves all)
@@ -1144,7 +1141,7 @@ def cache_append(cache: PagedCache, keys: Union[torch.Tensor, Sequence[torch.Ten
     if max(total, n) >= 2**31:
         raise ValueError("sizes must be below 2^31")
     e = pool.element_size()
-    status = torch.empty(cache.lengths.shape, dtype=torch.int32, device=dev)
+    status = torch.empty_like(cache.lengths)
     need = _append_bytes(S, n, P, page)
     workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     where = _ROWS.pack(strides[0] * e, strides[1] * e, strides[2] * e, layout[0] * e, layout[1] * e, H, D * e)
@@ -1163,7 +1160,7 @@ def cache_truncate(cache: PagedCache, lengths: torch.Tensor) -> torch.Tensor:
     if lengths.numel() != S:
         raise ValueError("lengths must have one entry per sequence")
     to = _words(lengths, dev, "lengths")
-    status = torch.empty(cache.lengths.shape, dtype=torch.int32, device=dev)
+    status = torch.empty_like(cache.lengths)
     _launch(dev, _lib.load().sv_cache_truncate, pages, to.data_ptr(), status.data_ptr())
     return status
 
