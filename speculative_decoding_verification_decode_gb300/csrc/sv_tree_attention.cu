@@ -259,9 +259,8 @@ __device__ __forceinline__ Pieces pieces_of(const Args& A, const Sequence& s, in
   return p;
 }
 
-constexpr int kFewSteps = 24;  // a piece with no more steps is of one item
-constexpr int kFewSequences = 32;
-constexpr int kLaneSequences = 8;
+constexpr int kFewSequences = 32;  // worked out by every warp for itself
+constexpr int kLaneSequences = 8, kLaneSteps = 256;
 
 // How the units are cut over C CTAs, and CTA c's first segment: by all of the
 // CTA's threads, or by every warp for itself (few sequences: all write the same
@@ -303,14 +302,21 @@ __device__ __forceinline__ void make_plan(const Args& A, int C, int c, PlanMem& 
       W += v;
     }
   }
-  if (W <= static_cast<long long>(kFewSteps) * kPairCost / 2 * C && A.batch <= T) {  // (some of that is the items' own)
-    // each item by itself, in the shortest pieces that C CTAs can take
+  // Each item by itself, in the shortest pieces that C CTAs can take, if the longest
+  // of them (three units a step) costs no more than an even cut and the item's end
+  // inside a piece, which that has.  2 sequences of 100000 tokens, 16 items in 9
+  // pieces each: 116 us, cut evenly 120; 8 items of 8 tiles 14.8 and 20.6; of 65
+  // tiles, two query tiles, 35 both ways.
+  const long long longest = (Cut::divide(W, C) + kItemCost) / kSingleCost;
+  const int most = longest < 1 << 20 ? static_cast<int>(longest) : 1 << 20;
+  if (A.pairs && A.batch <= T) {  // (no more items than CTAs)
     // (by bisection, the longest first; a piece has a key tile, of three units or more)
-    int lo = 1, hi = W <= 3LL * C ? 1 : 2 * kFewSteps;
-    if (kWarp && hi > 1 && A.batch <= kLaneSequences) {
-      // (few sequences: a lane per length, all looked at together)
+    int lo = 1, hi = most;
+    if (kWarp && A.batch <= kLaneSequences && most <= kLaneSteps) {
+      // (few sequences: a lane per length, all looked at together; one tree after
+      // 8191 tokens: 34.4 us, by bisection 37.1)
       unsigned fit = 0;
-      for (int base = 0; base < 2 * kFewSteps && !fit; base += 32) {
+      for (int base = 0; base < most && !fit; base += 32) {
         int all = 0;
         for (int b = 0; b < A.batch; ++b) {
           Sequence o;
@@ -319,13 +325,13 @@ __device__ __forceinline__ void make_plan(const Args& A, int C, int c, PlanMem& 
           o.items = __shfl_sync(0xFFFFFFFFu, q.items, b);
           if (o.N > 0) all += pieces_of(A, o, base + lane + 1).head * A.Hkv;
         }
-        fit = __ballot_sync(0xFFFFFFFFu, all <= C && base + lane < 2 * kFewSteps);
+        fit = __ballot_sync(0xFFFFFFFFu, all <= C && base + lane < most);
         if (fit) lo = hi = base + __ffs(fit);
       }
     }
     for (int limit = hi;;) {
       const Pieces p = t < A.batch && q.N > 0 ? pieces_of(A, q, limit) : Pieces{0, 0, 0};
-      const int count = p.head * A.Hkv;  // (no more than units)
+      const int count = p.head * A.Hkv;  // (of at most as many items as CTAs, 2^20 tiles each)
       int y = count;
 #pragma unroll
       for (int d = 1; d < 32; d *= 2) {
@@ -346,7 +352,7 @@ __device__ __forceinline__ void make_plan(const Args& A, int C, int c, PlanMem& 
         }
       }
       if (all > C) {
-        if (limit == 2 * kFewSteps) break;
+        if (limit == most) break;
         lo = limit + 1;
       } else {
         hi = limit;
