@@ -24,19 +24,24 @@
 // loaded once for both.  The MMA warp issues QK(g + 2) right behind PV(g), into
 // the score tile that PV(g) has just read the weights from (they lie over the
 // scores), so that the tensor cores work on one stream while the other's warps
-// take exponentials.
+// take exponentials.  A step takes 1600 to 1800 clocks (the products alone 1070):
+// score, softmax (1550), weights and output follow one another in a stream.
+//
+// Measured (both kernels): 64 sequences of up to 32 nodes and 4096 tokens, 64 / 8
+// heads of 128: 167 us (the bytes alone 125); 2 of 100000 tokens with chains of 6:
+// 116 us (106), 6.2 TB/s; one tree of 60 after 8191 tokens 35 us, one token after 777
+// 15 us, both of them latencies one after another and code that is not yet fetched.
 //
 // The weights are taken against a reference that follows the row's maximum: it
 // moves when the maximum passes it by 8 (in powers of two), and only then the
-// output is rescaled, which keeps that off the ordinary step; weights up to 2^8
-// lose nothing in either type.
+// output is rescaled, which keeps that off the ordinary step (167 us, moved with
+// every new maximum 171); weights up to 2^8 lose nothing in either type.
 //
 // The work is cut into one piece per CTA, so that ragged lengths balance and one
-// long context uses every SM.  Where CTAs have many steps the steps of all items,
-// sequence after sequence, are cut evenly, wherever that falls; where they have
-// few, an item's end inside a piece would cost more than it evens out (some 10000
-// clocks against 1800 a step), and each item is divided by itself, into pieces as
-// short as the CTAs allow.  An item that a cut divides leaves its parts (f32
+// long context uses every SM.  Either the items, sequence after sequence, are cut
+// evenly by what their tiles and ends cost, wherever that falls; or, where that
+// costs no more, each item is divided by itself, into pieces as short as the CTAs
+// allow (an item's end inside a piece takes some 10000 clocks).  An item that a cut divides leaves its parts (f32
 // outputs, maximum, sum) in the workspace, at most two per CTA, and a second
 // kernel joins them in order: the result depends on the inputs and the number of
 // CTAs only.
@@ -259,7 +264,7 @@ __device__ __forceinline__ Pieces pieces_of(const Args& A, const Sequence& s, in
   return p;
 }
 
-constexpr int kFewSequences = 32;  // worked out by every warp for itself
+constexpr int kFewSequences = 32;  // worked out by every warp for itself (one tree 35.0 us, by the CTA 36.9)
 constexpr int kLaneSequences = 8, kLaneSteps = 256;
 
 // How the units are cut over C CTAs, and CTA c's first segment: by all of the
