@@ -54,16 +54,12 @@ extern "C" {
  *          path, node 0 first, n_accepted + 1 of them, then -1.
  * A NaN in a row on the path sets SV_SEQ_BAD_VALUE (an all-NaN row's choice is
  * 0).  A sequence with no nodes, or with SV_SEQ_BAD_LAYOUT, has 0, -1 and an
- * empty path.
- * workspace: sv_verify_tree_workspace_size() bytes, 16-byte aligned, no initial
- *          contents needed.  Calls that share one must not overlap on the GPU.
+ * empty path.  One launch.
  */
-size_t sv_verify_tree_workspace_size(int32_t total);
 sv_status sv_verify_tree_greedy(const void* target, sv_dtype dtype, int64_t row_stride, const int32_t* tokens,
                                 const int32_t* parents, const int32_t* cu_nodes, int32_t batch, int32_t n,
                                 int32_t total, int32_t vocab, int32_t* n_accepted, int32_t* next_token,
-                                int32_t* path, uint32_t* status, void* workspace, size_t workspace_bytes,
-                                void* stream);
+                                int32_t* path, uint32_t* status, void* stream);
 
 /*
  * The same for choices that the caller has drawn: choices[row] is the

@@ -82,10 +82,8 @@ SIGNATURES = {
     "sv_lm_head_q4_logits": (_i32, [_vp, _i32, ctypes.POINTER(Q4Proj), _i32, _i32, _i32, _vp, _i64, _vp, _vp]),
     "sv_lm_head_q4_verify": (_i32, [_vp, _vp, _i32, ctypes.POINTER(Q4Proj), _i32, _vp, _vp, _vp, _vp, _i32, _i32,
                                     _i32, _i32, _vp, _vp, _vp, _vp, ctypes.c_size_t, _u32, _vp]),
-    "sv_verify_tree_workspace_size": (ctypes.c_size_t, [_i32]),
-    # target, dtype, stride, tokens, parents, cu_nodes, B, n, total, V, n_accepted, next, path, status, workspace, stream
-    "sv_verify_tree_greedy": (_i32, [_vp, _i32, _i64, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp,
-                                     _vp, ctypes.c_size_t, _vp]),
+    # target, dtype, stride, tokens, parents, cu_nodes, B, n, total, V, n_accepted, next, path, status, stream
+    "sv_verify_tree_greedy": (_i32, [_vp, _i32, _i64, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp]),
     "sv_verify_tree": (_i32, [_vp, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp]),
     "sv_tree_attention_workspace_size": (ctypes.c_size_t, [_i32]),
     # sv_tree_attn (words of 64 bits), scale, workspace, stream

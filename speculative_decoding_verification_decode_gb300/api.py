@@ -881,7 +881,7 @@ def _verify_tree(rows, choices, tokens, parents, cu_nodes, n) -> TreeResult:
         if stride < V and total > 1:
             rows, stride = rows.contiguous(), V
         _launch(dev, lib.sv_verify_tree_greedy, rows.data_ptr(), dtype, stride, tokens.data_ptr(), _p(parents), _p(cu),
-                B, n, total, V, *where, None, 0)
+                B, n, total, V, *where)
     else:
         if choices.numel() != total:
             raise ValueError("choices must have one entry for each token")

@@ -292,19 +292,11 @@ sv_status launch(const Tree& T, const Rows& R, int batch, cudaStream_t st) {
 
 extern "C" {
 
-size_t sv_verify_tree_workspace_size(int32_t total) {
-  (void)total;
-  return 0;
-}
-
 sv_status sv_verify_tree_greedy(const void* target, sv_dtype dtype, int64_t row_stride, const int32_t* tokens,
                                 const int32_t* parents, const int32_t* cu_nodes, int32_t batch, int32_t n,
                                 int32_t total, int32_t vocab, int32_t* n_accepted, int32_t* next_token,
-                                int32_t* path, uint32_t* status, void* workspace, size_t workspace_bytes,
-                                void* stream) {
+                                int32_t* path, uint32_t* status, void* stream) {
   svh::clear_error();
-  (void)workspace;
-  (void)workspace_bytes;
   const svt::Tree T = {tokens, parents, cu_nodes, n, total, n_accepted, next_token, path, status};
   const sv_status s = svt::check(T, batch);
   if (s != SV_OK) return s;

@@ -319,7 +319,8 @@ class TreeDecoder:
         for _ in range(-(-int((want - held).max()) // chunk)):
             left = (want - held).clamp(0, chunk)
             at = (held[:, None] + room).clamp(max=self.max_len - 1).long()
-            _, keys, values = self._target(self.tokens.gather(1, at), None, room)
+            nodes = torch.where(room < left[:, None], self.tokens.gather(1, at), 0)  # (what lies past a prompt is no token)
+            _, keys, values = self._target(nodes, None, room)
             self.status |= api.cache_append(self.cache, keys, values, counts=left).view(-1)
 
     def _uniforms(self) -> torch.Tensor:

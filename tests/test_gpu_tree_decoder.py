@@ -202,6 +202,24 @@ def test_sequences_that_cannot_go_on():
     check_greedy(model, d, (40, 4))
 
 
+def test_what_lies_past_a_prompt_is_not_looked_at():
+    model, prompts = Model(4), (40, 1, 7, 130, 17)
+    d = decoder(model)
+    e = decoder(model)
+    for b, p in enumerate(prompts):
+        e.tokens[b, p:] = -10 ** 6
+    seen = []
+    target = e.target_fn
+    e.target_fn = lambda nodes, positions, attend: seen.append((int(nodes.min()), int(nodes.max()))) or target(nodes, positions, attend)
+    for x in (d, e):
+        x.prefill(chunk=50)
+        x.run(5, graph=False)
+    assert all(0 <= lo and hi < V for lo, hi in seen)
+    assert torch.equal(d.lengths, e.lengths)
+    for b in range(len(prompts)):
+        assert torch.equal(d.tokens[b, :int(d.lengths[b])], e.tokens[b, :int(d.lengths[b])])
+
+
 def test_refusals():
     model = Model()
     c = sv().paged_cache(1, 4, 8, Hkv, D, 2, 4, device=DEV)

@@ -21,8 +21,7 @@ def lib():
 
 
 def greedy(lib, **kw):
-    a = dict(x=P, dt=1, stride=1000, tok=P, par=P, cu=None, B=2, n=4, total=8, V=1000, acc=P, nxt=P, path=P, st=P, ws=P,
-             wb=1 << 30, stream=None)
+    a = dict(x=P, dt=1, stride=1000, tok=P, par=P, cu=None, B=2, n=4, total=8, V=1000, acc=P, nxt=P, path=P, st=P, stream=None)
     a.update(kw)
     return lib.sv_verify_tree_greedy(*a.values())
 
