@@ -90,7 +90,7 @@ struct __align__(16) Join {
   int slot;   // of its part
   int cta;
   int b, head, pair;
-  int unused;
+  int nodes;     // of the sequence
   unsigned err;  // a wait gave up
 };
 
@@ -1249,6 +1249,7 @@ __device__ __forceinline__ void soften(const Args& A, Shared<DP>& sm, uint32_t t
       j.b = s.b;
       j.head = s.head;
       j.pair = s.pair;
+      j.nodes = s.q.N;
       j.err = 0;
       if (A.pairs)
         A.join[gridDim.x + (s.b * A.Hkv + s.head) * A.pairs + s.pair] = j;
@@ -1428,15 +1429,12 @@ __global__ void __launch_bounds__(kFinishThreads, kWide > 2 ? 2 : 4) finish_kern
   const Join j = A.join[A.pairs ? C + which : which];
   // (nothing is read by a record that a CTA which gave up has not written)
   if (j.parts <= 0 || j.cta < 0 || j.parts >= C - j.cta || j.slot < 0 || j.slot >= 2 * C || j.b < 0 || j.b >= A.batch) return;
-  if (!A.pairs) {
-    q = sequence(A, j.b);
-    bad = __syncthreads_or(bad_layout(A, j.b, t, kFinishThreads));
-  }
+  if (!A.pairs) q = sequence(A, j.b);  // (needed at the end: its loads are in flight with the parts')
   const int query = 2 * j.pair + (r >= kTile ? 1 : 0), rr = r % kTile;
   const int node = query * A.per_tile + row_node(A, rr);
-  if (bad || rr >= A.per_tile * A.G || node >= q.N || col >= A.D) return;  // (a bad sequence's rows are written where its status is)
+  const bool mine = rr < A.per_tile * A.G && node < j.nodes && col < A.D;
   float m = -INFINITY, sum = 0, o[kCols] = {};
-  {
+  if (mine) {
     // the first part is the last segment of its CTA, the others are their CTAs' first
     const float2* ml = A.part_ml + r;
     const float* part = A.part + (col / 4 * 256 + r) * 4;
@@ -1474,6 +1472,8 @@ __global__ void __launch_bounds__(kFinishThreads, kWide > 2 ? 2 : 4) finish_kern
         }
     }
   }
+  if (!A.pairs) bad = __syncthreads_or(bad_layout(A, j.b, t, kFinishThreads));
+  if (bad || !mine || node >= q.N) return;  // (a bad sequence's rows are written where its status is)
   const float inv = 1.0f / sum;
   const int qh = j.head * A.G + row_head(A, rr);
   const long long at = static_cast<long long>(q.first) + node;
