@@ -334,7 +334,8 @@ __device__ __forceinline__ void make_plan(const Args& A, int C, int c, PlanMem& 
         if (fit) lo = hi = base + __ffs(fit);
       }
     }
-    for (int limit = hi;;) {
+    // (at most 22 turns halve 2^20 lengths; whatever the counts, the search ends)
+    for (int turn = 0, limit = hi; turn < 24 && lo <= hi; ++turn) {
       const Pieces p = t < A.batch && q.N > 0 ? pieces_of(A, q, limit) : Pieces{0, 0, 0};
       const int count = p.head * A.Hkv;  // (of at most as many items as CTAs, 2^20 tiles each)
       int y = count;
@@ -405,7 +406,7 @@ __device__ __forceinline__ void make_plan(const Args& A, int C, int c, PlanMem& 
       for (;; ++b) {
         q = sequence(A, b);
         const long long k = units_of(A, q);
-        if (u < before + k) break;
+        if (u < before + k || b + 1 >= hi) break;
         before += k;
       }
     Walk w;
