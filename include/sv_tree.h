@@ -85,8 +85,9 @@ sv_status sv_verify_tree(const int32_t* choices, const int32_t* tokens, const in
  * sum passes it before the division, weights being up to 2^8, has no defined
  * result); the weights are rounded to `dtype` before they multiply the values.
  * All strides in ELEMENTS; the head dimension has unit stride.  Addresses and
- * strides of q, k, v, out and the caches are multiples of 16 bytes; out shares no
- * memory with another array.
+ * strides of q, k, v, out and the caches are multiples of 16 bytes, and no stride is
+ * 0 along a dimension of more than one entry; out shares no memory with another
+ * array.
  * status [batch]: 0, or SV_SEQ_BAD_LAYOUT (offsets or parents as above, a
  *   length outside [0, max_pages * page_size], a page outside [0, pages)): the
  *   rows of such a sequence (where its offsets are good) are 0, their lse -Inf.

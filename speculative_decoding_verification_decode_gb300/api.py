@@ -923,9 +923,11 @@ def _attention_bytes(dim: int) -> int:
 
 def _aligned(t: torch.Tensor) -> torch.Tensor:
     """``t [., H, D]`` itself where its last dimension has unit stride and the
-    others, and its address, are multiples of 16 bytes; else a copy."""
+    others, and its address, are multiples of 16 bytes, none broadcast; else a
+    copy."""
     s = t.stride()
-    if (s[2] != 1 and t.shape[2] > 1) or s[0] % 8 or s[1] % 8 or t.data_ptr() % 16:
+    if ((s[2] != 1 and t.shape[2] > 1) or s[0] % 8 or s[1] % 8 or t.data_ptr() % 16
+            or s[0] == 0 and t.shape[0] > 1 or s[1] == 0 and t.shape[1] > 1):
         t = torch.empty(t.shape, dtype=t.dtype, device=t.device).copy_(t)
     return t
 
@@ -939,7 +941,9 @@ def tree_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_cache: t
     [total, Hkv, D]`` (or ``[B, n, H, D]``): the nodes' own; ``k_cache``,
     ``v_cache [pages, page_size, Hkv, D]`` with ``table [B, max_pages]`` and
     ``lengths [B]``: token t of sequence b is in page ``table[b, t //
-    page_size]``.  All in bf16 or all in f16.  ``parents``, ``cu_nodes``, ``n``
+    page_size]``.  All in bf16 or all in f16; ``q``, ``k``, ``v`` views of any
+    strides (copied where the kernel cannot take them), the caches no broadcast
+    views.  ``parents``, ``cu_nodes``, ``n``
     as ``verify_tree_greedy`` takes them (without ``parents`` a chain, so one
     token per sequence is plain decoding); at most 256 nodes per sequence.
     ``scale``: default ``D ** -0.5``.  ``out``: optional tensor for the result;
@@ -985,6 +989,10 @@ def tree_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_cache: t
     kp, vp = k_cache.data_ptr(), v_cache.data_ptr()
     if (kc[3] != 1 or vc[3] != 1) and D > 1 or (kc[0] | kc[1] | kc[2] | vc[0] | vc[1] | vc[2]) % 8 or (kp | vp) % 16:
         raise ValueError("the caches must have unit stride along the head dimension, their addresses and other strides multiples of 16 bytes")
+    if 0 in kc or 0 in vc:
+        for s in (kc, vc):
+            if any(x == 0 and size > 1 for x, size in zip(s, k_cache.shape)):
+                raise ValueError("the caches must be no broadcast views (one key head serves several query heads as it is)")
     if out is None:
         out = torch.empty_like(q) if q.is_contiguous() else torch.empty((total, Hq, D), dtype=kind, device=dev)
     elif (out.shape[0] < total or out.shape[1:] != q.shape[1:] or out.dtype != q.dtype or out.device != dev or out.stride(2) != 1

@@ -1500,7 +1500,8 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
 }
 
 // Dimensions innermost first; strides in elements of all but the first.  A
-// dimension of 1 may have any stride: one that the encoding takes is put in.
+// dimension of one entry may have any stride: one that the encoding takes is put
+// in (the others' are not 0).
 bool encode(CUtensorMap* map, int64_t dtype, const void* data, int dims, const int64_t* size, const int64_t* stride,
             const int* box) {
   cuuint64_t d[4], s[3];
@@ -1508,8 +1509,7 @@ bool encode(CUtensorMap* map, int64_t dtype, const void* data, int dims, const i
   for (int i = 0; i < dims; ++i) {
     d[i] = static_cast<cuuint64_t>(size[i]);
     b[i] = static_cast<cuuint32_t>(box[i]);
-    if (i) s[i - 1] = static_cast<cuuint64_t>(size[i] > 1 || stride[i - 1] > 0 ? stride[i - 1] * 2 : 16);
-    if (i && s[i - 1] == 0) s[i - 1] = 16;
+    if (i) s[i - 1] = static_cast<cuuint64_t>(stride[i - 1] > 0 ? stride[i - 1] * 2 : 16);
   }
   return encoder()(map, dtype == SV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
                    static_cast<cuuint32_t>(dims), const_cast<void*>(data), d, s, b, e, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -1661,6 +1661,16 @@ sv_status sv_tree_attention(const sv_tree_attn* args, float scale, void* workspa
                              a.kc_head, a.vc_page, a.vc_token, a.vc_head, a.out_row, a.out_head};
   for (const int64_t x : strides)
     if (x < 0 || x % 8) return svh::fail(SV_ERR_ARG, "strides must be multiples of 8 elements, not negative");
+  const struct {
+    const char* name;
+    int64_t stride, size;
+  } steps[] = {{"q_row", a.q_row, a.total},      {"q_head", a.q_head, a.q_heads},    {"k_row", a.k_row, a.total},
+               {"k_head", a.k_head, a.kv_heads}, {"v_row", a.v_row, a.total},        {"v_head", a.v_head, a.kv_heads},
+               {"kc_page", a.kc_page, a.pages},  {"kc_token", a.kc_token, a.page_size}, {"kc_head", a.kc_head, a.kv_heads},
+               {"vc_page", a.vc_page, a.pages},  {"vc_token", a.vc_token, a.page_size}, {"vc_head", a.vc_head, a.kv_heads}};
+  for (const auto& x : steps)
+    if (x.stride == 0 && x.size > 1 && a.total > 0)
+      return svh::fail(SV_ERR_ARG, "%s: a stride of 0 along a dimension of %lld (a broadcast view)", x.name, (long long)x.size);
   if ((a.out_row < a.dim && a.total > 1) || (a.out_head < a.dim && a.q_heads > 1))
     return svh::fail(SV_ERR_ARG, "rows of out overlap");
   for (const void* p : {a.q, a.k, a.v, a.k_cache, a.v_cache, static_cast<const void*>(a.out)})
