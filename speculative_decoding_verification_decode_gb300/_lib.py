@@ -88,6 +88,7 @@ SIGNATURES = {
     "sv_tree_attention_workspace_size": (ctypes.c_size_t, [_i32]),
     # sv_tree_attn (words of 64 bits), scale, workspace, stream
     "sv_tree_attention": (_i32, [_vp, ctypes.c_float, _vp, ctypes.c_size_t, _vp]),
+    "sv_tree_attention_flagged": (_i32, [_vp, ctypes.c_float, _u32, _vp, ctypes.c_size_t, _vp]),
     "sv_cache_append_workspace_size": (ctypes.c_size_t, [_i32, _i32, _i32, _i32]),
     # sv_cache_pages and sv_cache_rows (words of 64 bits), pools, rows, n_pools, counts, path, cu_nodes, n, total,
     # status, workspace, stream

@@ -935,7 +935,7 @@ def _aligned(t: torch.Tensor) -> torch.Tensor:
 def tree_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                    table: torch.Tensor, lengths: torch.Tensor, parents: Optional[torch.Tensor] = None,
                    cu_nodes: Optional[torch.Tensor] = None, n: Optional[int] = None, scale: Optional[float] = None,
-                   out: Optional[torch.Tensor] = None) -> TreeAttention:
+                   out: Optional[torch.Tensor] = None, flags: int = 0) -> TreeAttention:
     """Attention of drafted nodes over their sequence's cached tokens and their
     own ancestors (include/sv_tree.h).  ``q [total, Hq, D]``, ``k``, ``v
     [total, Hkv, D]`` (or ``[B, n, H, D]``): the nodes' own; ``k_cache``,
@@ -947,7 +947,8 @@ def tree_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_cache: t
     as ``verify_tree_greedy`` takes them (without ``parents`` a chain, so one
     token per sequence is plain decoding); at most 256 nodes per sequence.
     ``scale``: default ``D ** -0.5``.  ``out``: optional tensor for the result;
-    rows past the last sequence are left as they are."""
+    rows past the last sequence are left as they are.  ``flags``:
+    FLAG_EXPIRE_EXCHANGE is a testing aid."""
     dev = q.device
     if dev.type != "cuda":
         raise ValueError("q must be a CUDA tensor (the caches stay where they are)")
@@ -1009,8 +1010,8 @@ def tree_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_cache: t
              kp, vp, kc[0], kc[1], kc[2], vc[0], vc[1], vc[2], k_cache.shape[0],
              k_cache.shape[1], table.data_ptr(), table.stride(0), table.shape[1], lengths.data_ptr(), _p(parents) or 0,
              _p(cu) or 0, B, n, total, out.data_ptr(), os[0], os[1], lse.data_ptr(), status.data_ptr())
-    _launch(dev, _lib.load().sv_tree_attention, words,
-            D ** -0.5 if scale is None else float(scale), workspace.data_ptr(), need)
+    _launch(dev, _lib.load().sv_tree_attention_flagged, words,
+            D ** -0.5 if scale is None else float(scale), flags, workspace.data_ptr(), need)
     return TreeAttention(out, lse, status)
 
 

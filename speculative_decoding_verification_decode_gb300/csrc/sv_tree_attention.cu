@@ -84,7 +84,9 @@ __host__ __device__ constexpr int k_slots(int dp) { return dp == 128 ? 3 : 5; }
 __host__ __device__ constexpr int v_slots(int dp) { return dp == 128 ? 2 : 5; }
 
 // What a CTA leaves for the second kernel: the item whose first part, but not
-// whole, it had.
+// whole, it had.  A record per item (`pairs` > 0) is not written where its CTA gave
+// up before it: the second kernel knows such an item from its own place, and what
+// else it takes from the record only chooses among the parts.
 struct __align__(16) Join {
   int parts;  // the CTAs behind it that have the others; 0: no such item
   int slot;   // of its part
@@ -115,6 +117,7 @@ struct Args {
   bool wide;        // out in 32-byte stores
   float c;          // scale in powers of two, not negative
   bool flip;        // the scores' sign is turned (a negative scale)
+  bool expire;      // testing aid: waits for a segment's outputs give up at once
   float* part;      // [2 CTAs][dp / 4][256 rows][4]: a warp, a row per lane, writes and reads whole lines
   float2* part_ml;  // [2 CTAs][256]: maximum (powers of two), sum
   struct Join* join;  // [CTAs], then one per item where `pairs` > 0
@@ -645,8 +648,8 @@ struct Steps {
 };
 
 template <class S>
-__device__ __forceinline__ bool wait(S& sm, uint64_t* bar, uint32_t parity) {
-  for (uint32_t i = 0; i < svk::kWaitPolls; ++i) {
+__device__ __forceinline__ bool wait(S& sm, uint64_t* bar, uint32_t parity, uint32_t polls = svk::kWaitPolls) {
+  for (uint32_t i = 0; i < polls; ++i) {
     if (svk::mbar_try_wait(bar, parity)) return true;
     if (sm.abort) return false;
   }
@@ -654,8 +657,8 @@ __device__ __forceinline__ bool wait(S& sm, uint64_t* bar, uint32_t parity) {
   return false;
 }
 template <class S>
-__device__ __forceinline__ bool warp_wait(S& sm, uint64_t* bar, uint32_t parity) {
-  return __all_sync(0xFFFFFFFFu, wait(sm, bar, parity));
+__device__ __forceinline__ bool warp_wait(S& sm, uint64_t* bar, uint32_t parity, uint32_t polls = svk::kWaitPolls) {
+  return __all_sync(0xFFFFFFFFu, wait(sm, bar, parity, polls));
 }
 __device__ __forceinline__ void bar_soft() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kSoftWarps) : "memory"); }
 
@@ -1177,7 +1180,7 @@ __device__ __forceinline__ void soften(const Args& A, Shared<DP>& sm, uint32_t t
       keep = mine;
       keep_other = theirs;
     }
-    if (alive) alive = warp_wait(sm, &sm.o_full, number & 1);
+    if (alive) alive = warp_wait(sm, &sm.o_full, number & 1, A.expire ? 0u : svk::kWaitPolls);
     fence_after();
     const int begin = s.two ? 0 : stream * (DP / 2), width = s.two ? DP : DP / 2;
     const bool mine = alive && busy && row < rows;
@@ -1427,8 +1430,14 @@ __global__ void __launch_bounds__(kFinishThreads, kWide > 2 ? 2 : 4) finish_kern
     bad = __syncthreads_or(bad_layout(A, b, t, kFinishThreads));
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const Join j = A.join[A.pairs ? C + which : which];
-  // (nothing is read by a record that a CTA which gave up has not written)
+  Join j = A.join[A.pairs ? C + which : which];
+  if (A.pairs) {  // (the record may be what the workspace held before)
+    const int item = which / A.pairs;
+    j.b = item / A.Hkv;
+    j.head = item % A.Hkv;
+    j.pair = which % A.pairs;
+    j.nodes = q.N;
+  }
   if (j.parts <= 0 || j.cta < 0 || j.parts >= C - j.cta || j.slot < 0 || j.slot >= 2 * C || j.b < 0 || j.b >= A.batch) return;
   if (!A.pairs) q = sequence(A, j.b);  // (needed at the end: its loads are in flight with the parts')
   const int query = 2 * j.pair + (r >= kTile ? 1 : 0), rr = r % kTile;
@@ -1523,7 +1532,7 @@ size_t workspace_bytes_of(int dim) {
 }
 
 template <typename T, int DP>
-sv_status launch(const sv_tree_attn& a, float scale, unsigned char* ws, cudaStream_t st) {
+sv_status launch(const sv_tree_attn& a, float scale, uint32_t flags, unsigned char* ws, cudaStream_t st) {
   if (!encoder()) return svh::fail(SV_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
   Args A;
   A.G = static_cast<int>(a.q_heads / a.kv_heads);
@@ -1559,6 +1568,7 @@ sv_status launch(const sv_tree_attn& a, float scale, unsigned char* ws, cudaStre
   A.wide = !((reinterpret_cast<uintptr_t>(a.out) & 31) | ((a.out_row | a.out_head | a.dim) & 15));
   A.c = (scale < 0 ? -scale : scale) * 1.4426950408889634f;
   A.flip = scale < 0;
+  A.expire = (flags & SV_FLAG_EXPIRE_EXCHANGE) != 0;
   const size_t rows = 2 * kMaxCtas * 256;
   A.part = reinterpret_cast<float*>(ws);
   A.part_ml = reinterpret_cast<float2*>(ws + rows * DP * 4);
@@ -1630,7 +1640,13 @@ size_t sv_tree_attention_workspace_size(int32_t dim) {
 
 sv_status sv_tree_attention(const sv_tree_attn* args, float scale, void* workspace, size_t workspace_bytes,
                             void* stream) {
+  return sv_tree_attention_flagged(args, scale, 0, workspace, workspace_bytes, stream);
+}
+
+sv_status sv_tree_attention_flagged(const sv_tree_attn* args, float scale, uint32_t flags, void* workspace,
+                                    size_t workspace_bytes, void* stream) {
   svh::clear_error();
+  if (flags & ~static_cast<uint32_t>(SV_FLAG_EXPIRE_EXCHANGE)) return svh::fail(SV_ERR_ARG, "unknown flag (%u)", flags);
   if (!args) return svh::fail(SV_ERR_ARG, "args is NULL");
   const sv_tree_attn& a = *args;
   constexpr long long kMax = 0x7FFFFFFFLL;
@@ -1683,8 +1699,8 @@ sv_status sv_tree_attention(const sv_tree_attn* args, float scale, void* workspa
   unsigned char* ws = static_cast<unsigned char*>(workspace);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (a.dtype == SV_BF16)
-    return a.dim <= 64 ? sva::launch<__nv_bfloat16, 64>(a, scale, ws, st) : sva::launch<__nv_bfloat16, 128>(a, scale, ws, st);
-  return a.dim <= 64 ? sva::launch<__half, 64>(a, scale, ws, st) : sva::launch<__half, 128>(a, scale, ws, st);
+    return a.dim <= 64 ? sva::launch<__nv_bfloat16, 64>(a, scale, flags, ws, st) : sva::launch<__nv_bfloat16, 128>(a, scale, flags, ws, st);
+  return a.dim <= 64 ? sva::launch<__half, 64>(a, scale, flags, ws, st) : sva::launch<__half, 128>(a, scale, flags, ws, st);
 }
 
 }  // extern "C"
