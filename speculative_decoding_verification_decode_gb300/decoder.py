@@ -262,7 +262,8 @@ class TreeDecoder:
     there).  A sequence that a whole tree could take past ``max_len`` stays as it
     is from then on, and so does one that cannot go on: ``status`` (int32
     ``[B]``, SEQ_* bits) tells why, SEQ_NO_PAGES where the cache is full,
-    SEQ_BAD_VALUE for a row that no token can be taken from."""
+    SEQ_BAD_VALUE for a row that no token can be taken from, SEQ_BAD_LAYOUT or
+    SEQ_TIMEOUT where a layer's attention gave no result."""
 
     def __init__(self, draft_fn: Callable, target_fn: Callable, cache: api.PagedCache, tokens: torch.Tensor,
                  lengths: torch.Tensor, parents, temperature: Optional[torch.Tensor] = None, seed: int = 0):
@@ -295,19 +296,23 @@ class TreeDecoder:
         self.graph = None
 
     def _target(self, nodes: torch.Tensor, parents: Optional[torch.Tensor], depth: torch.Tensor):
-        """(logits, every layer's keys, values) of the nodes."""
+        """(logits, every layer's keys, values, per-sequence status of the
+        attention) of the nodes."""
         c = self.cache
-        keys, values = [None] * len(c.keys), [None] * len(c.keys)
+        keys, values, statuses = [None] * len(c.keys), [None] * len(c.keys), []
         table, lengths = c.table.view(self.B, -1), c.lengths.view(-1)
 
         def attend(layer, q, k, v):
             keys[layer], values[layer] = k, v
-            return api.tree_attention(q, k, v, c.keys[layer], c.values[layer], table, lengths, parents).out.view(q.shape)
+            r = api.tree_attention(q, k, v, c.keys[layer], c.values[layer], table, lengths, parents)
+            statuses.append(r.status)
+            return r.out.view(q.shape)
 
         logits = self.target_fn(nodes, lengths[:, None] + depth, attend)
         if any(k is None for k in keys):
             raise ValueError("target_fn must call attend for every layer of the cache")
-        return logits, keys, values
+        # (a layout is bad in all layers or in none, so that the largest word has every layer's bits)
+        return logits, keys, values, torch.stack(statuses).amax(0)
 
     def prefill(self, chunk: int = 128):
         """Brings the committed tokens but the last one of every sequence into
@@ -320,7 +325,9 @@ class TreeDecoder:
             left = (want - held).clamp(0, chunk)
             at = (held[:, None] + room).clamp(max=self.max_len - 1).long()
             nodes = torch.where(room < left[:, None], self.tokens.gather(1, at), 0)  # (what lies past a prompt is no token)
-            _, keys, values = self._target(nodes, None, room)
+            _, keys, values, failed = self._target(nodes, None, room)
+            self.status |= failed
+            left = torch.where(self.status == 0, left, 0)  # (nothing behind what is not there)
             self.status |= api.cache_append(self.cache, keys, values, counts=left).view(-1)
 
     def _uniforms(self) -> torch.Tensor:
@@ -337,7 +344,7 @@ class TreeDecoder:
         at = (self.lengths - 1).clamp(min=0).long()[:, None]
         nodes = self.draft_fn(self.tokens, self.lengths).to(torch.int32)
         nodes = torch.where(self.column == 0, self.tokens.gather(1, at), nodes)
-        logits, keys, values = self._target(nodes, self.parents, self.depth)
+        logits, keys, values, failed = self._target(nodes, self.parents, self.depth)
         if self.temperature is None:
             r = api.verify_tree_greedy(logits, nodes, self.parents)
         else:  # each node's token drawn from its row, then matched
@@ -345,6 +352,7 @@ class TreeDecoder:
             drawn = api.accept_from_logits(rows, rows[:0], self.temperature, nodes.reshape(-1)[:0], self._uniforms())
             r = api.verify_tree(drawn.next_token, nodes, self.parents)
         bad = torch.where(r.next_token < 0, r.status | api._lib.SEQ_BAD_VALUE, r.status & ~api._lib.SEQ_BAD_TOKEN)
+        bad = torch.where(failed != 0, failed, bad)  # (such logits say nothing)
         go = (self.status == 0) & (bad == 0) & (self.lengths + self.n <= self.max_len)
         counts = torch.where(go, r.n_accepted + 1, 0)
         full = api.cache_append(self.cache, keys, values, counts=counts, path=r.path).view(-1)
