@@ -254,9 +254,9 @@ class TreeDecoder:
       0's, the last committed token, is put in place here);
     * ``target_fn(nodes, positions, attend) -> [B, n, V]`` logits after each
       node: ``nodes [B, n]`` int32, ``positions [B, n]`` their places in the
-      sequence, ``attend(layer, q, k, v)`` the layer's attention, ``[B, n, Hq,
-      D]``, for its ``q [B, n, Hq, D]`` and ``k``, ``v [B, n, Hkv, D]``, called
-      once per layer of the cache.
+      sequence (below ``max_len``), ``attend(layer, q, k, v)`` the layer's
+      attention, ``[B, n, Hq, D]``, for its ``q [B, n, Hq, D]`` and ``k``, ``v
+      [B, n, Hkv, D]``, called once per layer of the cache.
 
     ``cache`` holds the committed tokens but the last one (``prefill`` brings it
     there).  A sequence that a whole tree could take past ``max_len`` stays as it
@@ -308,7 +308,8 @@ class TreeDecoder:
             statuses.append(r.status)
             return r.out.view(q.shape)
 
-        logits = self.target_fn(nodes, lengths[:, None] + depth, attend)
+        # (a node past the end is one that does not count: of a prompt's last chunk, or of a sequence that stays)
+        logits = self.target_fn(nodes, (lengths[:, None] + depth).clamp(max=self.max_len - 1), attend)
         if any(k is None for k in keys):
             raise ValueError("target_fn must call attend for every layer of the cache")
         # (a layout is bad in all layers or in none, so that the largest word has every layer's bits)

@@ -76,3 +76,18 @@ def test_a_wait_that_gave_up(monkeypatch):
         m.setattr(api, "tree_attention", functools.partial(api.tree_attention, flags=sv().FLAG_EXPIRE_EXCHANGE))
         d.prefill(chunk=50)
     assert (d.status == sv().SEQ_TIMEOUT).all() and not d.cache.lengths.any() and not d.cache.refs.any()
+
+
+@pytest.mark.parametrize("sampled", [False, True])
+def test_positions_are_below_max_len(sampled):
+    model, prompts, max_len = Model(9), (5, 60, 66), 70
+    d = decoder(model, 3, prompts, max_len=max_len, temperature=torch.full((3,), 0.5) if sampled else None)
+    seen, target = [], d.target_fn
+    d.target_fn = lambda nodes, positions, attend: seen.append((int(positions.min()), int(positions.max()))) or target(nodes, positions, attend)
+    d.prefill()
+    assert d.cache.lengths.tolist() == [p - 1 for p in prompts]
+    d.run(66, graph=False)
+    assert (d.lengths > max_len - d.n).all() and not d.status.any()
+    assert all(0 <= lo and hi < max_len for lo, hi in seen)
+    if not sampled:
+        check_greedy(model, d, prompts)

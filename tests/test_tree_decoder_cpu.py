@@ -111,3 +111,20 @@ def test_a_sampled_round_whose_attention_failed_commits_nothing(monkeypatch):
     d.round()
     assert d.status.tolist() == [0, 0, sv.SEQ_BAD_LAYOUT] and stand.appended[-1].tolist() == [2, 2, 0]
     assert d.lengths.tolist() == [7, 9, 3]
+
+
+@pytest.mark.parametrize("lengths", [(5, 30, 3), (1, 40, 39), (37, 36, 38)])
+def test_positions_are_within_the_sequences(monkeypatch, lengths):
+    """Through a prefill whose chunk is longer than what a sequence may hold, and
+    rounds of sequences that have stopped near their end."""
+    d, stand, seen = make(monkeypatch, lengths, max_len=40, cached=(0, 0, 0))
+    d.prefill()
+    assert d.cache.lengths.tolist() == [x - 1 for x in lengths]
+    for _ in range(25):
+        d.round()
+    assert (d.lengths > 40 - len(TREE)).all() and (d.lengths <= 40).all() and not d.status.any()
+    assert all(0 <= int(p.min()) and int(p.max()) < 40 for _, p in seen)
+    # nodes that count have their own place
+    nodes, positions = seen[0]
+    for b, n in enumerate(lengths):
+        assert torch.equal(positions[b, :n - 1], torch.arange(n - 1, dtype=torch.int32))
