@@ -259,16 +259,16 @@ class TreeDecoder:
       [B, n, Hkv, D]``, called once per layer of the cache.
 
     ``cache`` holds the committed tokens but the last one (``prefill`` brings it
-    there).  A sequence that a whole tree could take past ``max_len`` stays as it
-    is from then on, and so does one that cannot go on: ``status`` (int32
+    there).  A sequence without a token, or that a whole tree could take past
+    ``max_len``, stays as it is, and so does one that cannot go on: ``status`` (int32
     ``[B]``, SEQ_* bits) tells why, SEQ_NO_PAGES where the cache is full,
     SEQ_BAD_VALUE for a row that no token can be taken from, SEQ_BAD_LAYOUT or
     SEQ_TIMEOUT where a layer's attention gave no result."""
 
     def __init__(self, draft_fn: Callable, target_fn: Callable, cache: api.PagedCache, tokens: torch.Tensor,
                  lengths: torch.Tensor, parents, temperature: Optional[torch.Tensor] = None, seed: int = 0):
-        """``tokens`` [B, max_len] int32 (prompts in place, one token at least),
-        ``lengths`` [B] int32; ``parents``: the tree, the earlier node that each
+        """``tokens`` [B, max_len] int32 (prompts in place, one token at least in
+        a sequence that takes part), ``lengths`` [B] int32; ``parents``: the tree, the earlier node that each
         node continues, -1 for node 0 (a chain: -1, 0, 1, ...); greedy when
         ``temperature`` is None, else per-sequence temperatures [B] (0 =
         greedy for that sequence)."""
@@ -320,7 +320,7 @@ class TreeDecoder:
         the cache, from where it stands, up to ``chunk`` tokens at a time (the
         one call that reads lengths on the host)."""
         held = self.cache.lengths.view(-1)
-        want = self.lengths - 1
+        want = self.lengths.clamp(max=self.max_len) - 1
         room = torch.arange(chunk, device=self.device, dtype=torch.int32)
         for _ in range(-(-int((want - held).max()) // chunk)):
             left = (want - held).clamp(0, chunk)
@@ -342,7 +342,7 @@ class TreeDecoder:
     def round(self):
         """One round for every sequence (no host sync); returns the
         verification's result."""
-        at = (self.lengths - 1).clamp(min=0).long()[:, None]
+        at = (self.lengths - 1).clamp(0, self.max_len - 1).long()[:, None]
         nodes = self.draft_fn(self.tokens, self.lengths).to(torch.int32)
         nodes = torch.where(self.column == 0, self.tokens.gather(1, at), nodes)
         logits, keys, values, failed = self._target(nodes, self.parents, self.depth)
@@ -354,7 +354,7 @@ class TreeDecoder:
             r = api.verify_tree(drawn.next_token, nodes, self.parents)
         bad = torch.where(r.next_token < 0, r.status | api._lib.SEQ_BAD_VALUE, r.status & ~api._lib.SEQ_BAD_TOKEN)
         bad = torch.where(failed != 0, failed, bad)  # (such logits say nothing)
-        go = (self.status == 0) & (bad == 0) & (self.lengths + self.n <= self.max_len)
+        go = (self.status == 0) & (bad == 0) & (self.lengths > 0) & (self.lengths + self.n <= self.max_len)
         counts = torch.where(go, r.n_accepted + 1, 0)
         full = api.cache_append(self.cache, keys, values, counts=counts, path=r.path).view(-1)
         self.status |= torch.where(self.status == 0, bad | full, 0)

@@ -128,3 +128,27 @@ def test_positions_are_within_the_sequences(monkeypatch, lengths):
     nodes, positions = seen[0]
     for b, n in enumerate(lengths):
         assert torch.equal(positions[b, :n - 1], torch.arange(n - 1, dtype=torch.int32))
+
+
+def test_lengths_past_the_end_of_tokens(monkeypatch):
+    """No place of such a sequence is looked at beyond the row; it stays as it is."""
+    d, stand, seen = make(monkeypatch, (5, 41, 1000), max_len=40, cached=(4, 39, 39))
+    before = d.tokens.clone()
+    d.round()
+    assert d.lengths.tolist() == [7, 41, 1000] and torch.equal(d.tokens[1:], before[1:])
+    assert stand.appended[-1].tolist() == [2, 0, 0]
+
+
+def test_a_prefill_of_lengths_past_the_end_of_tokens(monkeypatch):
+    d, stand, _ = make(monkeypatch, (5, 41, 1000, 0), max_len=40, cached=(0, 0, 0, 0))
+    d.prefill(chunk=16)
+    assert d.cache.lengths.tolist() == [4, 39, 39, 0] and len(stand.appended) == 3
+
+
+def test_an_empty_sequence_stays_empty(monkeypatch):
+    """A slot without a token takes no part (padding of a batch)."""
+    d, stand, _ = make(monkeypatch, (5, 0, 3), cached=(4, 0, 2))
+    before = d.tokens.clone()
+    d.round()
+    assert stand.appended[-1].tolist() == [2, 0, 2] and d.lengths.tolist() == [7, 0, 5] and d.cache.lengths.tolist() == [6, 0, 4]
+    assert torch.equal(d.tokens[1], before[1]) and not d.status.any()
