@@ -36,6 +36,31 @@ import torch
 
 from . import api
 
+_MIX = ((0x5851F42D4C957F2D, 33), (0x2545F4914F6CDD1D, 29), (0x14057B7EF767814F, 31))  # (odd multiplier, shift)
+
+
+def _signed(x: int) -> int:
+    """The 64 bits of ``x`` as torch takes them."""
+    return (x & (1 << 64) - 1) - (1 << 64 if x >> 63 & 1 else 0)
+
+
+def _mixed(index: torch.Tensor, step: torch.Tensor, seed: int) -> torch.Tensor:
+    """Uniforms k * 2^-24 in [0, 1) from (seed, step, index): int64 ``index``
+    below 2^32, ``step`` an int64 scalar on the device, ``seed`` of 31 bits.
+    Their low bits are laid side by side (32, 16, 16), what a step and a seed have
+    above those is spread over the word, and the word is mixed."""
+    x = index + step * 0x100000000 + _signed((seed & 0xFFFF) << 48)
+    spread = seed >> 16  # (0 stays 0)
+    for mul, sh in _MIX:
+        spread = (spread ^ spread >> sh) * mul & (1 << 64) - 1
+    x = x ^ (step >> 16) * _MIX[0][0]
+    if spread:
+        x = x ^ _signed(spread)
+    for mul, sh in _MIX:
+        x = x ^ ((x >> sh) & ((1 << (64 - sh)) - 1))   # logical shift on int64
+        x = x * mul
+    return ((x >> 40) & 0xFFFFFF).to(torch.float32) * (1.0 / (1 << 24))
+
 
 class SpeculativeDecoder:
     def __init__(self, draft_fn: Callable, target_fn: Callable, tokens: torch.Tensor,
@@ -67,12 +92,7 @@ class SpeculativeDecoder:
         round, stream, sequence, position): reproducible and graph-safe."""
         K1 = self.k + 1
         idx = (self.rows[:, None] * K1 + torch.arange(K1, device=self.device)[None, :]).to(torch.int64)
-        x = idx + (self.counter * 4 + stream_id) * 0x100000000 + self.seed * 0x1000000000000
-        for mul, sh in ((0x5851F42D4C957F2D, 33), (0x2545F4914F6CDD1D, 29), (0x14057B7EF767814F, 31)):
-            x = x ^ ((x >> sh) & ((1 << (64 - sh)) - 1))   # logical shift on int64
-            x = x * (mul - (1 << 64) if mul >= (1 << 63) else mul)
-        bits = (x >> 40) & 0xFFFFFF
-        return bits.to(torch.float32) * (1.0 / (1 << 24))
+        return _mixed(idx, self.counter * 4 + stream_id, self.seed)
 
     def _draw(self, logits: torch.Tensor, u: torch.Tensor) -> torch.Tensor:
         """Greedy argmax (lowest index on ties) or an inverse-CDF draw from
@@ -334,10 +354,7 @@ class TreeDecoder:
     def _uniforms(self) -> torch.Tensor:
         """[B * n] uniforms k * 2^-24 from a counter-based mix of (seed, round,
         sequence, node): reproducible and graph-safe."""
-        x = torch.arange(self.B * self.n, device=self.device) + self.counter * 0x100000000 + self.seed * 0x1000000000000
-        for mul, sh in ((0x5851F42D4C957F2D, 33), (0x2545F4914F6CDD1D, 29), (0x14057B7EF767814F, 31)):
-            x = (x ^ ((x >> sh) & ((1 << (64 - sh)) - 1))) * mul
-        return ((x >> 40) & 0xFFFFFF).to(torch.float32) * (1.0 / (1 << 24))
+        return _mixed(torch.arange(self.B * self.n, device=self.device), self.counter, self.seed)
 
     def round(self):
         """One round for every sequence (no host sync); returns the
