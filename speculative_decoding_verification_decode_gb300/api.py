@@ -946,8 +946,9 @@ def tree_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_cache: t
     views.  ``parents``, ``cu_nodes``, ``n``
     as ``verify_tree_greedy`` takes them (without ``parents`` a chain, so one
     token per sequence is plain decoding); at most 256 nodes per sequence.
-    ``scale``: default ``D ** -0.5``.  ``out``: optional tensor for the result;
-    rows past the last sequence are left as they are.  ``flags``:
+    ``scale``: default ``D ** -0.5``.  ``out``: optional tensor for the result,
+    sharing no memory with an input; rows past the last sequence are left as they
+    are.  ``flags``:
     FLAG_EXPIRE_EXCHANGE is a testing aid."""
     dev = q.device
     if dev.type != "cuda":

@@ -1526,6 +1526,50 @@ bool encode(CUtensorMap* map, int64_t dtype, const void* data, int dims, const i
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Whether [total, heads, dim] elements of 2 bytes have places of their own: heads
+// within a row, or rows within a head's stretch.
+bool rows_apart(int64_t total, int64_t heads, int64_t dim, int64_t row, int64_t head) {
+  if (total <= 1) return heads <= 1 || head >= dim;
+  if (heads <= 1) return row >= dim;
+  return (head >= dim && row >= (heads - 1) * head + dim) || (row >= dim && head >= (total - 1) * row + dim);
+}
+
+// The array of the call that out shares memory with, NULL: none.  An array lies
+// between its first and its last element; two of rows of the same stride may lie in one
+// another's gaps (columns of one projection).
+const char* shares_with_out(const sv_tree_attn& a) {
+  using Big = __int128;  // (strides and sizes of 31 bits and more)
+  const auto at = [](const void* p) { return static_cast<Big>(reinterpret_cast<uintptr_t>(p)); };
+  const Big out = at(a.out), row_span = static_cast<Big>(a.q_heads - 1) * a.out_head + a.dim;  // (elements)
+  const Big out_end = out + 2 * (static_cast<Big>(a.total - 1) * a.out_row + row_span);
+  const auto meets = [&](const void* p, Big bytes) { return p && bytes > 0 && at(p) < out_end && out < at(p) + bytes; };
+  const struct {
+    const char* name;
+    const void* p;
+    int64_t row, head, heads;
+  } rows[] = {{"q", a.q, a.q_row, a.q_head, a.q_heads}, {"k", a.k, a.k_row, a.k_head, a.kv_heads}, {"v", a.v, a.v_row, a.v_head, a.kv_heads}};
+  for (const auto& x : rows) {
+    const Big span = static_cast<Big>(x.heads - 1) * x.head + a.dim;
+    if (!meets(x.p, 2 * (static_cast<Big>(a.total - 1) * x.row + span))) continue;
+    if (x.row == a.out_row && row_span <= x.row && span <= x.row) {
+      const Big d = ((at(x.p) - out) / 2 % x.row + x.row) % x.row;  // of its rows' places behind out's
+      if (d >= row_span && d + span <= x.row) continue;
+    }
+    return x.name;
+  }
+  const auto pool = [&](int64_t page, int64_t token, int64_t head) {
+    return 2 * (static_cast<Big>(a.pages - 1) * page + static_cast<Big>(a.page_size - 1) * token + static_cast<Big>(a.kv_heads - 1) * head + a.dim);
+  };
+  if (meets(a.k_cache, pool(a.kc_page, a.kc_token, a.kc_head))) return "k_cache";
+  if (meets(a.v_cache, pool(a.vc_page, a.vc_token, a.vc_head))) return "v_cache";
+  if (a.max_pages > 0 && meets(a.table, 4 * (static_cast<Big>(a.batch - 1) * a.table_stride + a.max_pages))) return "table";
+  if (meets(a.lengths, 4 * a.batch)) return "lengths";
+  if (meets(a.parents, 4 * a.total)) return "parents";
+  if (meets(a.cu_nodes, 4 * (a.batch + 1))) return "cu_nodes";
+  if (meets(a.lse, 4 * static_cast<Big>(a.total) * a.q_heads)) return "lse";
+  return meets(a.status, 4 * a.batch) ? "status" : nullptr;
+}
+
 size_t workspace_bytes_of(int dim) {
   const size_t rows = 2 * kMaxCtas * 256;
   return rows * (dim <= 64 ? 64 : 128) * 4 + rows * 8 + 2 * kMaxCtas * sizeof(Join);
@@ -1687,8 +1731,7 @@ sv_status sv_tree_attention_flagged(const sv_tree_attn* args, float scale, uint3
   for (const auto& x : steps)
     if (x.stride == 0 && x.size > 1 && a.total > 0)
       return svh::fail(SV_ERR_ARG, "%s: a stride of 0 along a dimension of %lld (a broadcast view)", x.name, (long long)x.size);
-  if ((a.out_row < a.dim && a.total > 1) || (a.out_head < a.dim && a.q_heads > 1))
-    return svh::fail(SV_ERR_ARG, "rows of out overlap");
+  if (!sva::rows_apart(a.total, a.q_heads, a.dim, a.out_row, a.out_head)) return svh::fail(SV_ERR_ARG, "rows of out overlap");
   for (const void* p : {a.q, a.k, a.v, a.k_cache, a.v_cache, static_cast<const void*>(a.out)})
     if (reinterpret_cast<uintptr_t>(p) & 15) return svh::fail(SV_ERR_ARG, "q, k, v, the caches and out must be 16-byte aligned");
   const size_t need = sva::workspace_bytes_of(static_cast<int>(a.dim));
@@ -1696,6 +1739,8 @@ sv_status sv_tree_attention_flagged(const sv_tree_attn* args, float scale, uint3
     return svh::fail(SV_ERR_ARG, "workspace_bytes (%zu) < the %zu bytes sv_tree_attention_workspace_size() asks for",
                      workspace_bytes, need);
   if (reinterpret_cast<uintptr_t>(workspace) & 15) return svh::fail(SV_ERR_ARG, "workspace must be 16-byte aligned");
+  if (a.total > 0)
+    if (const char* name = sva::shares_with_out(a)) return svh::fail(SV_ERR_ARG, "out shares memory with %s", name);
   unsigned char* ws = static_cast<unsigned char*>(workspace);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (a.dtype == SV_BF16)

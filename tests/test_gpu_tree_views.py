@@ -66,3 +66,23 @@ def test_broadcast_caches_are_refused():
     t = b["k_cache"]
     one = t.as_strided(t.shape, (t.stride(0), t.stride(1), 0, 1))
     assert torch.equal(sv().tree_attention(**b).out, sv().tree_attention(**{**b, "k_cache": one}).out)
+
+
+def test_an_out_in_the_projection_of_its_inputs():
+    """Beside q, k and v in one tensor: taken; over a part of one: refused."""
+    a = inputs(torch.bfloat16, 21, 8, 4, 64)
+    want = sv().tree_attention(**a)
+    fused = torch.full((21, 28, 64), 7.0, dtype=torch.bfloat16, device=DEV)
+    for name, lo, hi in (("q", 4, 12), ("k", 12, 16), ("v", 16, 20)):
+        fused[:, lo:hi] = a[name]
+        a[name] = fused[:, lo:hi]
+    got = sv().tree_attention(**a, out=fused[:, 20:])
+    assert torch.equal(got.out, want.out) and torch.equal(got.lse, want.lse)
+    assert (fused[:, :4] == 7).all() and torch.equal(fused[:, 20:], want.out)
+    kept = fused.clone()
+    flat = a["k_cache"].view(-1)
+    for out, name in ((fused[:, 3:11], "q"), (fused[:, 15:23], "k"), (fused[:, 17:25], "v"),
+                      (flat[4096:4096 + 21 * 8 * 64].view(21, 8, 64), "k_cache")):
+        with pytest.raises(sv().SVError, match=f"out shares memory with {name}"):
+            sv().tree_attention(**a, out=out)
+    assert torch.equal(fused, kept)
