@@ -55,6 +55,7 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "../../include/sv_tree.h"
@@ -1497,15 +1498,16 @@ __global__ void __launch_bounds__(kFinishThreads, kWide > 2 ? 2 : 4) finish_kern
 // ------------------------------------------------------------------ host
 
 PFN_cuTensorMapEncodeTiled_v12000 encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  if (!fn) {
+  static std::atomic<void*> fn{nullptr};  // (threads that ask at once find the same)
+  void* p = fn.load(std::memory_order_acquire);
+  if (!p) {
     cudaDriverEntryPointQueryResult q;
-    void* p = nullptr;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return nullptr;
+    fn.store(p, std::memory_order_release);
   }
-  return fn;
+  return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
 }
 
 // Dimensions innermost first; strides in elements of all but the first.  A
@@ -1632,20 +1634,19 @@ sv_status launch(const sv_tree_attn& a, float scale, uint32_t flags, unsigned ch
   }
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 0;
-  static bool attr_set[64] = {false};
-  static int sms[64] = {0};
-  if (!attr_set[dev]) {
+  // CTAs per device, 0: the kernels' attributes are not set yet.  One word, so that
+  // another thread's first call sees both or neither.
+  static std::atomic<int> ctas[64] = {};
+  int C = ctas[dev].load(std::memory_order_acquire);
+  if (!C) {
     const cudaError_t e = cudaFuncSetAttribute(attend_kernel<T, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<DP>());
     if (e != cudaSuccess) return svh::fail(SV_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
     // (the same split of the SM's memory as the first kernel's: no change between the two)
     cudaFuncSetAttribute(finish_kernel<T, DP, 2, DP / 8>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
     cudaFuncSetAttribute(finish_kernel<T, DP, 8, 8>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
-    int n = 0;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = kMaxCtas;
-    sms[dev] = n < kMaxCtas ? n : kMaxCtas;
-    attr_set[dev] = true;
+    if (cudaDeviceGetAttribute(&C, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || C <= 0 || C > kMaxCtas) C = kMaxCtas;
+    ctas[dev].store(C, std::memory_order_release);
   }
-  const int C = sms[dev];
   const long long pairs = (a.n + 2 * A.per_tile - 1) / (2 * A.per_tile);
   A.pairs = a.batch <= C && a.batch * a.kv_heads * pairs <= C ? static_cast<int>(pairs) : 0;
   if (a.total > 0) {
