@@ -808,12 +808,18 @@ class TreeAttention(NamedTuple):
 
 
 def _words(t: Optional[torch.Tensor], dev: torch.device, what: str) -> Optional[torch.Tensor]:
-    """``t`` as contiguous int32 on ``dev``."""
+    """``t`` as contiguous int32 on ``dev``; numbers that do not fit become the
+    type's ends, which are out of every range too."""
     if t is None:
         return None
     if t.dtype is not torch.int32:
-        if t.is_floating_point() or t.dtype == torch.bool:
+        if t.is_floating_point() or t.is_complex() or t.dtype == torch.bool:
             raise ValueError(f"{what} must be whole numbers")
+        if t.dtype.itemsize >= 4:
+            wide = t.to(torch.int64)
+            if t.dtype is torch.uint64:
+                wide = torch.where(wide < 0, 2**31 - 1, wide)  # (2^63 and above)
+            t = wide.clamp(-2**31, 2**31 - 1)
         t = t.to(torch.int32)
     if t.device != dev:
         t = t.to(dev)
