@@ -1424,26 +1424,28 @@ __global__ void __launch_bounds__(kFinishThreads, kWide > 2 ? 2 : 4) finish_kern
   const int col = (k % kColBlocks) * (8 * kCols) + (t >> 5) * kCols;
   bool bad = false;
   Sequence q;
-  if (A.pairs) {  // the item's sequence is known before its parts are there
-    const int b = which / (A.Hkv * A.pairs);
+  int b = 0, head = 0, pair = 0;
+  if (A.pairs) {  // the item is known before its parts are there (and from its place: the record may be what the workspace held)
+    const int item = which / A.pairs;
+    pair = which - item * A.pairs;
+    b = item / A.Hkv;
+    head = item - b * A.Hkv;
     q = sequence(A, b);
-    if (q.N <= 0 || which % A.pairs >= q.items) return;
+    if (q.N <= 0 || pair >= q.items) return;
     bad = __syncthreads_or(bad_layout(A, b, t, kFinishThreads));
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  Join j = A.join[A.pairs ? C + which : which];
-  if (A.pairs) {  // (the record may be what the workspace held before)
-    const int item = which / A.pairs;
-    j.b = item / A.Hkv;
-    j.head = item % A.Hkv;
-    j.pair = which % A.pairs;
-    j.nodes = q.N;
+  const Join j = A.join[A.pairs ? C + which : which];
+  if (j.parts <= 0 || j.cta < 0 || j.parts >= C - j.cta || j.slot < 0 || j.slot >= 2 * C) return;
+  int nodes = q.N;
+  if (!A.pairs) {
+    if (j.b < 0 || j.b >= A.batch) return;
+    b = j.b, head = j.head, pair = j.pair, nodes = j.nodes;
+    q = sequence(A, b);  // (needed at the end: its loads are in flight with the parts')
   }
-  if (j.parts <= 0 || j.cta < 0 || j.parts >= C - j.cta || j.slot < 0 || j.slot >= 2 * C || j.b < 0 || j.b >= A.batch) return;
-  if (!A.pairs) q = sequence(A, j.b);  // (needed at the end: its loads are in flight with the parts')
-  const int query = 2 * j.pair + (r >= kTile ? 1 : 0), rr = r % kTile;
+  const int query = 2 * pair + (r >= kTile ? 1 : 0), rr = r % kTile;
   const int node = query * A.per_tile + row_node(A, rr);
-  const bool mine = rr < A.per_tile * A.G && node < j.nodes && col < A.D;
+  const bool mine = rr < A.per_tile * A.G && node < nodes && col < A.D;
   float m = -INFINITY, sum = 0, o[kCols] = {};
   if (mine) {
     // the first part is the last segment of its CTA, the others are their CTAs' first
@@ -1483,10 +1485,10 @@ __global__ void __launch_bounds__(kFinishThreads, kWide > 2 ? 2 : 4) finish_kern
         }
     }
   }
-  if (!A.pairs) bad = __syncthreads_or(bad_layout(A, j.b, t, kFinishThreads));
+  if (!A.pairs) bad = __syncthreads_or(bad_layout(A, b, t, kFinishThreads));
   if (bad || !mine || node >= q.N) return;  // (a bad sequence's rows are written where its status is)
   const float inv = 1.0f / sum;
-  const int qh = j.head * A.G + row_head(A, rr);
+  const int qh = head * A.G + row_head(A, rr);
   const long long at = static_cast<long long>(q.first) + node;
   T* dst = static_cast<T*>(A.out) + at * A.out_row + static_cast<long long>(qh) * A.out_head;
 #pragma unroll
