@@ -6,7 +6,8 @@
  * committed token, every other node continues an earlier one (its parent).
  * The target scores all nodes in one pass, each seeing the cached tokens and
  * its own ancestors (sv_tree_attention); the accepted tokens are those of the
- * longest path from node 0 that follows the target's choices
+ * path from node 0 that follows the target's choices as far as the tree goes,
+ * to the lowest node where siblings carry the same token
  * (sv_verify_tree_greedy, sv_verify_tree).  The path's keys and values then go
  * into the cache (sv_cache.h); the others were never written there.
  * The conventions of sv.h apply: device pointers owned by the caller,
@@ -83,7 +84,8 @@ sv_status sv_verify_tree(const int32_t* choices, const int32_t* tokens, const in
  * Everything in `dtype` (SV_BF16 or SV_F16) except lse (f32).  Products and
  * sums in f32 (a row with a score past f32's range, or with values whose weighted
  * sum passes it before the division, weights being up to 2^8, has no defined
- * result); the weights are rounded to `dtype` before they multiply the values.
+ * result); the weights are rounded to `dtype` before they multiply the values, each
+ * off by at most half a step, 2^-8 (bf16) or 2^-11 (f16) of itself.
  * All strides in ELEMENTS; the head dimension has unit stride.  Addresses and
  * strides of q, k, v, out and the caches are multiples of 16 bytes, and no stride is
  * 0 along a dimension of more than one entry; out shares no memory with another

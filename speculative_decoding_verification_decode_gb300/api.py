@@ -1097,7 +1097,7 @@ def cache_append(cache: PagedCache, keys: Union[torch.Tensor, Sequence[torch.Ten
     [sequences, n]`` and ``n_accepted + 1`` of a verification) go behind the
     sequence; without ``path`` its first ``counts`` rows, without ``counts`` all.
     New pages are the lowest free ones, in sequence order; a shared last page is
-    copied first.  ``lengths`` grow by ``counts``.  Returns the per-sequence
+    copied first.  No new row may lie in a pool.  ``lengths`` grow by ``counts``.  Returns the per-sequence
     status: SEQ_NO_PAGES where pages or table entries do not suffice,
     SEQ_BAD_LAYOUT; such a sequence is left as it is."""
     if isinstance(keys, torch.Tensor):

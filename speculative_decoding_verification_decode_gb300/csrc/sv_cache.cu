@@ -9,12 +9,15 @@
 // threads.  The second moves the rows of all pools, shared last pages first
 // copied to their new ones.
 //
-// The second starts while the first still runs (a programmatic dependency).  64
+// The second starts while the first still runs (a programmatic dependency).  Calls in
+// a graph: 64
 // paths of 32 nodes into 16 layers, then back: 15.7 us with four pools to a CTA,
 // 18.7 with one, 16.6 with two, 16.0 with eight; the bytes alone are 3.  24 x 8 beams,
 // 12 layers: 31 us for sharing, appending and giving up, of which the one CTA that
 // deals out pages takes 9: a chain of dependent reads, which is what bounds these
-// calls on the device (on the host it is the launches and the layers' tensors).
+// calls on the device.  From Python they take 74 to 88 us, most of it the host's: a
+// launch each, and questions to every layer's tensors, which is what this interface (a
+// list of tensors per layer) costs and not what the work needs.
 //
 // Sharing (fork) reads the table entries that a group's slots hold, lets every
 // slot take its parent's, and corrects the pages' counts where an entry
