@@ -122,8 +122,9 @@ size_t sv_tree_attention_workspace_size(int32_t dim);
 sv_status sv_tree_attention(const sv_tree_attn* args, float scale, void* workspace, size_t workspace_bytes,
                             void* stream);
 /* The same with flags: 0, or SV_FLAG_EXPIRE_EXCHANGE (sv.h; a testing aid), with
- * which every wait for outputs of the tensor cores gives up at once: all sequences
- * end with SV_SEQ_TIMEOUT, their rows hold anything, and nothing else is written. */
+ * which every wait for outputs of the tensor cores gives up at once: where there is a
+ * row, all sequences end with SV_SEQ_TIMEOUT, their rows hold anything, and nothing
+ * else is written. */
 sv_status sv_tree_attention_flagged(const sv_tree_attn* args, float scale, uint32_t flags, void* workspace,
                                     size_t workspace_bytes, void* stream);
 

@@ -49,7 +49,7 @@ def _mixed(index: torch.Tensor, step: torch.Tensor, seed: int) -> torch.Tensor:
     below 2^32, ``step`` an int64 scalar on the device, ``seed`` of 31 bits.
     Their low bits are laid side by side (32, 16, 16), what a step and a seed have
     above those is spread over the word, and the word is mixed."""
-    x = index + step * 0x100000000 + _signed((seed & 0xFFFF) << 48)
+    x = torch.add(index, step, alpha=0x100000000) + _signed((seed & 0xFFFF) << 48)
     spread = seed >> 16  # (0 stays 0)
     for mul, sh in _MIX:
         spread = (spread ^ spread >> sh) * mul & (1 << 64) - 1
@@ -288,8 +288,8 @@ class TreeDecoder:
     def __init__(self, draft_fn: Callable, target_fn: Callable, cache: api.PagedCache, tokens: torch.Tensor,
                  lengths: torch.Tensor, parents, temperature: Optional[torch.Tensor] = None, seed: int = 0):
         """``tokens`` [B, max_len] int32 (prompts in place, one token at least in
-        a sequence that takes part), ``lengths`` [B] int32; ``parents``: the tree, the earlier node that each
-        node continues, -1 for node 0 (a chain: -1, 0, 1, ...); greedy when
+        a sequence that takes part), ``lengths`` [B] int32; ``parents``: the
+        tree, the earlier node that each node continues, -1 for node 0 (a chain: -1, 0, 1, ...); greedy when
         ``temperature`` is None, else per-sequence temperatures [B] (0 =
         greedy for that sequence)."""
         if tokens.dim() != 2 or tokens.dtype != torch.int32 or lengths.dtype != torch.int32:
