@@ -347,7 +347,7 @@ class TreeDecoder:
             at = (held[:, None] + room).clamp(max=self.max_len - 1).long()
             nodes = torch.where(room < left[:, None], self.tokens.gather(1, at), 0)  # (what lies past a prompt is no token)
             _, keys, values, failed = self._target(nodes, None, room)
-            self.status |= torch.where(left > 0, failed, 0)
+            self.status |= failed
             left = torch.where(self.status == 0, left, 0)  # (nothing behind what is not there)
             self.status |= api.cache_append(self.cache, keys, values, counts=left).view(-1)
 

@@ -152,20 +152,3 @@ def test_an_empty_sequence_stays_empty(monkeypatch):
     d.round()
     assert stand.appended[-1].tolist() == [2, 0, 2] and d.lengths.tolist() == [7, 0, 5] and d.cache.lengths.tolist() == [6, 0, 4]
     assert torch.equal(d.tokens[1], before[1]) and not d.status.any()
-
-
-def test_a_prefill_that_fails_where_a_sequence_has_nothing_left(monkeypatch):
-    """A chunk without a result stops the sequences that it was for."""
-    d, stand, _ = make(monkeypatch, (5, 30, 3), cached=(0, 0, 0))
-    attention = stand.attention
-
-    def late(*args, **kw):
-        r = attention(*args, **kw)
-        if stand.calls > LAYERS:  # from the second chunk on
-            r.status.fill_(sv.SEQ_TIMEOUT)
-        return r
-
-    monkeypatch.setattr(api, "tree_attention", late)
-    d.prefill(chunk=8)
-    assert d.status.tolist() == [0, sv.SEQ_TIMEOUT, 0]
-    assert d.cache.lengths.tolist() == [4, 8, 2]
